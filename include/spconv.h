@@ -1,6 +1,7 @@
 /*
  * spconv.h -- C ABI of the GB300 (sm_103a) submanifold sparse convolution
- * (3x3x3 and 5x5x5 kernels, stride 1).
+ * (3x3x3 and 5x5x5 kernels, stride 1) and of the row-wise operators between
+ * two convolutions (RMS norm, linear, gated feed-forward).
  *
  * The operation (FlyDSL PR #942, "Add submanifold sparse 3D convolution",
  * Summary: raw voxel coordinates in, output features out, the kernel map built
@@ -20,9 +21,10 @@
  * order.
  *
  * Memory: every pointer argument named *_dev is a device pointer that the
- * caller owns; host pointers are marked host.  The library allocates only map
+ * caller owns; host pointers are marked host.  The library allocates map
  * handles and packed-weight handles (stream-ordered, on the stream passed to
- * the creating call) and frees them in the matching destroy call.
+ * the creating call) and frees them in the matching destroy call; the row-wise
+ * operators below take scratch memory in stream order for the length of a call.
  *
  * Streams: all work is enqueued on the caller's stream; nothing synchronises
  * the device except where a function says it does.
@@ -56,7 +58,11 @@ typedef enum {
     SPCONV_ERR_INTERNAL = -9       /* a kernel's consistency guard fired (a library bug)     */
 } spconv_status_t;
 
-typedef enum { SPCONV_BF16 = 0, SPCONV_FP32 = 1 } spconv_dtype_t;
+typedef enum {
+    SPCONV_BF16 = 0,
+    SPCONV_FP32 = 1,
+    SPCONV_E4M3 = 2    /* 8-bit floats with separate scales: the row-wise operators only */
+} spconv_dtype_t;
 
 typedef enum {
     SPCONV_MAPPER_AUTO = 0,   /* dense grid iff padded cells <= dense_max_cells, else HASH when
@@ -363,6 +369,131 @@ void spconv_map_destroy(spconv_map_t map);
  */
 int spconv_kernel_map_static(const int32_t* coords_dev, int64_t n, const int32_t* spatial_shape,
                              int32_t batch_size, int32_t* nbr_dev, void* stream);
+
+/*
+ * Row-wise operators of a network over voxels: what stands between two
+ * convolutions on the same sites.  They need no map: each works on n rows of
+ * features, [n][c] as the convolution reads and writes them.  The pages' open
+ * question of "a layer stack with normalisation and residuals" (FlyDSL PR #942,
+ * "Open questions") for networks whose norm has row statistics and whose
+ * layers have a feed-forward part.
+ *
+ *   Rows       every [n][c] argument has a row stride ld_* in elements (>= c);
+ *              its rows are contiguous.  Outputs without a stride are dense.
+ *              Any element-aligned address and stride is taken.
+ *   Sizes      0 <= n < 2^30, 1 <= c <= 65536.  n = 0 writes only the
+ *              gradients of the parameters (zeros).
+ *   Rounding   sums, statistics and epilogues are fp32, with one rounding to
+ *              the output type.
+ *   Order      every sum has a fixed order: the same call gives the same bits.
+ *   Scratch    taken from the library's pool in stream order for the length
+ *              of the call.
+ *   Aliasing   an output must not overlap an input, unless said below
+ *              (SPCONV_ERR_ALIAS).
+ *   NaN, inf   pass through the formulas as in IEEE arithmetic.
+ */
+typedef enum {
+    SPCONV_ACT_NONE = 0,
+    SPCONV_ACT_RELU = 1,       /* max(z, 0)                                            */
+    SPCONV_ACT_SILU = 2,       /* z / (1 + exp(-z))                                    */
+    SPCONV_ACT_GELU = 3,       /* z (1 + erf(z / sqrt 2)) / 2                          */
+    SPCONV_ACT_GELU_TANH = 4   /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2    */
+} spconv_act_t;
+
+/*
+ * Root-mean-square norm of rows with the residual's addition:
+ *
+ *   h = x + residual;  y = h / sqrt(mean_c h^2 + eps) * weight;  sum = h
+ *
+ *   x_dev, residual_dev  [n] rows of c, dtype (SPCONV_BF16 or SPCONV_FP32);
+ *                        residual_dev NULL means 0.
+ *   weight_dev           fp32 [c].
+ *   sum_dev              [n][c] dtype, h rounded (the next residual), or NULL.
+ *                        May be x_dev or residual_dev themselves when dense.
+ *   out_dev              [n][c]: y in dtype, or with out_dtype SPCONV_E4M3 the
+ *                        e4m3 values q of y / scale, scale_dev fp32 [n] being
+ *                        max_c |y| / 448 of each row (0 for a row of zeros, with
+ *                        q 0).  scale_dev NULL exactly when y is in dtype.
+ */
+int spconv_rms_norm(const void* x_dev, int64_t ld_x, const void* residual_dev, int64_t ld_residual, const float* weight_dev,
+                    int64_t n, int32_t c, int32_t dtype, float eps, void* sum_dev, void* out_dev, int32_t out_dtype,
+                    float* scale_dev, void* stream);
+
+/*
+ * Its backward pass.  x is the normalised sum h, r = 1 / sqrt(mean_c x^2 + eps):
+ *
+ *   dx = r (dy w - x r^2 mean_c(dy w x)) + dres;   dweight_c = sum_rows dy x r
+ *
+ *   dres_dev   gradient that reaches the sum by another way (the residual
+ *              stream), or NULL; dx_dev may be dres_dev when dense.
+ *   dx_dev     [n][c] dtype: the gradient of x and of the residual alike.
+ *   dweight_dev fp32 [c], overwritten.
+ */
+int spconv_rms_norm_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, const float* weight_dev,
+                             const void* dres_dev, int64_t ld_dres, int64_t n, int32_t c, int32_t dtype, float eps,
+                             void* dx_dev, float* dweight_dev, void* stream);
+
+/*
+ * out = act(z) + residual,  z = x W + bias.
+ *
+ *   dtype SPCONV_BF16   x bf16 [n] rows of c_in, W bf16 [c_in][c_out] (one tap
+ *                       of a convolution's weights); the scales are NULL.
+ *   dtype SPCONV_E4M3   x e4m3 with fp32 x_scale [n], W e4m3 [c_out][c_in] with
+ *                       fp32 w_scale [c_out] (spconv_rms_norm and
+ *                       spconv_quantize_weight make them): the product of row i
+ *                       and channel o is multiplied by x_scale[i] w_scale[o].
+ *   bias_dev            fp32 [c_out] or NULL.
+ *   residual_dev        bf16 [n] rows of c_out or NULL; may be out_dev with the
+ *                       same stride.
+ *   out_dev             bf16 [n] rows of c_out.
+ * SPCONV_FP32 returns SPCONV_ERR_UNSUPPORTED.
+ */
+int spconv_linear(const void* x_dev, int64_t ld_x, const float* x_scale_dev, const void* w_dev, const float* w_scale_dev,
+                  int64_t n, int32_t c_in, int32_t c_out, int32_t dtype, const float* bias_dev, int32_t activation,
+                  const void* residual_dev, int64_t ld_residual, void* out_dev, int64_t ld_out, void* stream);
+
+/*
+ * Gradients of the bf16 form (the residual's is dy itself).  z is formed again:
+ *
+ *   dz = dy act'(z);  dx = dz W^T;  dw = x^T dz;  dbias = sum_rows dz
+ *
+ * dz is rounded to bf16 as an operand of the two products (dbias sums it
+ * unrounded).  dx_dev bf16 [n][c_in], dw_dev bf16 [c_in][c_out], dbias_dev
+ * fp32 [c_out]; each may be NULL, which leaves its work out.
+ */
+int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, const void* w_dev, int64_t n,
+                           int32_t c_in, int32_t c_out, int32_t dtype, const float* bias_dev, int32_t activation,
+                           void* dx_dev, void* dw_dev, float* dbias_dev, void* stream);
+
+/*
+ * Gated feed-forward: out = act(x W_gate) * (x W_up), both products, the
+ * activation and the product of the two in one kernel.  Operands as
+ * spconv_linear (gate_scale, up_scale fp32 [c_hidden] with e4m3);
+ * out_dev bf16 [n] rows of c_hidden.
+ */
+int spconv_gated_ffn(const void* x_dev, int64_t ld_x, const float* x_scale_dev, const void* w_gate_dev,
+                     const float* gate_scale_dev, const void* w_up_dev, const float* up_scale_dev, int64_t n, int32_t c_in,
+                     int32_t c_hidden, int32_t dtype, int32_t activation, void* out_dev, int64_t ld_out, void* stream);
+
+/*
+ * Gradients of the bf16 form, from dh, the gradient of out.  g = x W_gate and
+ * u = x W_up are formed again:
+ *
+ *   dg = dh u act'(g);  du = dh act(g)      (rounded to bf16 as operands)
+ *   dx = dg W_gate^T + du W_up^T;  dw_gate = x^T dg;  dw_up = x^T du
+ *
+ * dx_dev may be NULL, or dw_gate_dev and dw_up_dev both.
+ */
+int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_dev, int64_t ld_x, const void* w_gate_dev,
+                              const void* w_up_dev, int64_t n, int32_t c_in, int32_t c_hidden, int32_t dtype,
+                              int32_t activation, void* dx_dev, void* dw_gate_dev, void* dw_up_dev, void* stream);
+
+/*
+ * A weight for the e4m3 forms, made once: w bf16 [c_in][c_out] to q e4m3
+ * [c_out][c_in] with scale[o] = max_c |w[c][o]| / 448 (0, with q 0, for a
+ * channel of zeros).
+ */
+int spconv_quantize_weight(const void* w_dev, int32_t c_in, int32_t c_out, void* q_dev, float* scale_dev, void* stream);
 
 /* Number of kernel launches enqueued by the last call on this thread. */
 int32_t spconv_last_launch_count(void);

@@ -35,6 +35,8 @@ class Epilogue(ctypes.Structure):
                 ("residual_dev", ctypes.c_void_p), ("relu", ctypes.c_int32)]
 
 
+_P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "spconv_build_map": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, c_int32_p, ctypes.c_int32,
@@ -75,6 +77,15 @@ SIGNATURES = {
     "spconv_map_destroy": (None, [ctypes.c_void_p]),
     "spconv_kernel_map_static": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, c_int32_p, ctypes.c_int32,
                                                 ctypes.c_void_p, ctypes.c_void_p]),
+    "spconv_rms_norm": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I32, _I32, ctypes.c_float, _P, _P, _I32, _P, _P]),
+    "spconv_rms_norm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _I32, _I32, ctypes.c_float, _P,
+                                                _P, _P]),
+    "spconv_linear": (ctypes.c_int, [_P, _I64, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _I32, _P, _I64, _P, _I64, _P]),
+    "spconv_linear_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P]),
+    "spconv_gated_ffn": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _I64, _P]),
+    "spconv_gated_ffn_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P,
+                                                 _P]),
+    "spconv_quantize_weight": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P]),
     "spconv_last_launch_count": (ctypes.c_int32, []),
     "spconv_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
     "spconv_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -1,0 +1,182 @@
+// Shared by the row-wise operators (RMS norm, linear, gated feed-forward):
+// activations, vector loads and stores, stream-ordered scratch, and the
+// description of one matrix product with its epilogue.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace spconv {
+
+// ---- activations -----------------------------------------------------------
+// Evaluated on the fp32 sum.  __expf and __fdividef are a few fp32 ulps off,
+// far below the bf16 rounding of whatever is stored.
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// tanh form of GELU: 0.5 (1 + tanh(v / 2)) is the logistic function of v
+constexpr float kGeluA = 1.5957691216057308f;   // sqrt(8 / pi)
+constexpr float kGeluB = 0.044715f;
+
+template <int ACT>
+__device__ __forceinline__ float act_f(float z) {
+    if (ACT == SPCONV_ACT_RELU) return z < 0.0f ? 0.0f : z;   // keeps NaN
+    if (ACT == SPCONV_ACT_SILU) return z * sigmoid_f(z);
+    if (ACT == SPCONV_ACT_GELU) return 0.5f * z * erfcf(-0.70710678f * z);   // erfc: no cancellation for z << 0
+    if (ACT == SPCONV_ACT_GELU_TANH) return z * sigmoid_f(kGeluA * z * fmaf(kGeluB * z, z, 1.0f));
+    return z;
+}
+
+// *a = act(z), returns act'(z)
+template <int ACT>
+__device__ __forceinline__ float act_grad_f(float z, float* a) {
+    if (ACT == SPCONV_ACT_RELU) {
+        *a = z < 0.0f ? 0.0f : z;
+        return z > 0.0f ? 1.0f : 0.0f;
+    }
+    if (ACT == SPCONV_ACT_SILU) {
+        const float s = sigmoid_f(z);
+        *a = z * s;
+        return fmaf(z * s, 1.0f - s, s);
+    }
+    if (ACT == SPCONV_ACT_GELU) {
+        const float phi = 0.5f * erfcf(-0.70710678f * z);
+        *a = z * phi;
+        return fmaf(0.39894228f * z, __expf(-0.5f * z * z), phi);
+    }
+    if (ACT == SPCONV_ACT_GELU_TANH) {
+        const float s = sigmoid_f(kGeluA * z * fmaf(kGeluB * z, z, 1.0f));
+        *a = z * s;
+        return fmaf(z * s * (1.0f - s), kGeluA * fmaf(3.0f * kGeluB * z, z, 1.0f), s);
+    }
+    *a = z;
+    return 1.0f;
+}
+
+// Calls f with the activation as a compile-time constant.
+template <typename F>
+__device__ __forceinline__ void with_act(int32_t act, F&& f) {
+    switch (act) {
+        case SPCONV_ACT_RELU: f(std::integral_constant<int, SPCONV_ACT_RELU>()); break;
+        case SPCONV_ACT_SILU: f(std::integral_constant<int, SPCONV_ACT_SILU>()); break;
+        case SPCONV_ACT_GELU: f(std::integral_constant<int, SPCONV_ACT_GELU>()); break;
+        case SPCONV_ACT_GELU_TANH: f(std::integral_constant<int, SPCONV_ACT_GELU_TANH>()); break;
+        default: f(std::integral_constant<int, SPCONV_ACT_NONE>()); break;
+    }
+}
+
+// ---- scratch ---------------------------------------------------------------
+// Device memory for the length of one call: allocated and freed in stream
+// order from the library's pool, so it follows the call's stream by itself.
+class Scratch {
+public:
+    Scratch(size_t bytes, cudaStream_t s) : stream_(s) {
+        if (bytes == 0) return;
+        if (pool_alloc(&ptr_, bytes, s) != cudaSuccess) {
+            cudaGetLastError();
+            ptr_ = nullptr;
+            failed_ = true;
+        }
+    }
+    ~Scratch() {
+        if (ptr_) cudaFreeAsync(ptr_, stream_);
+    }
+    Scratch(const Scratch&) = delete;
+    Scratch& operator=(const Scratch&) = delete;
+    bool failed() const { return failed_; }
+    template <typename T>
+    T* as(size_t byte_offset = 0) const {
+        return reinterpret_cast<T*>(static_cast<uint8_t*>(ptr_) + byte_offset);
+    }
+
+private:
+    void* ptr_ = nullptr;
+    cudaStream_t stream_;
+    bool failed_ = false;
+};
+
+inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int launch_status() { return cuda_status(cudaGetLastError()); }
+
+// ---- RMS norm (norm.cu) ----------------------------------------------------
+struct NormArgs {
+    const void* x;          // [n] rows of c, ldx elements apart
+    int64_t ldx;
+    const void* residual;   // or null
+    int64_t ldr;
+    const float* weight;    // [c]
+    int64_t n;
+    int32_t c;
+    int32_t dtype;          // of x, residual, sum
+    float eps;
+    void* sum;              // [n][c] x + residual, or null
+    void* out;              // [n][c]
+    int32_t out_dtype;      // dtype, or SPCONV_E4M3
+    float* scale;           // [n], with SPCONV_E4M3
+};
+int norm_forward(const NormArgs& a, cudaStream_t s);
+
+struct NormGradArgs {
+    const void* dy;
+    int64_t ldy;
+    const void* x;
+    int64_t ldx;
+    const float* weight;
+    const void* dres;       // or null
+    int64_t ldr;
+    int64_t n;
+    int32_t c;
+    int32_t dtype;
+    float eps;
+    void* dx;               // [n][c]
+    float* dweight;         // [c]
+};
+int norm_backward(const NormGradArgs& a, cudaStream_t s);
+
+// ---- products with an epilogue (dense.cu) ----------------------------------
+// Element (i, k) of an operand is p[i ld + k] (k_major) or p[k ld + i].
+struct Operand {
+    const void* p[2] = {nullptr, nullptr};
+    int64_t ld = 0;
+    bool k_major = true;
+};
+
+enum : int32_t {
+    kEpiLinear = 0,      // out0 = act(acc * row_scale * col_scale + bias) + extra
+    kEpiGated = 1,       // out0 = act(acc0 ..) * (acc1 ..), acc1 from b.p[1]
+    kEpiActGrad = 2,     // out0 = extra * act'(acc + bias); col_sums += the unrounded values
+    kEpiGatedGrad = 3,   // out0 = extra * acc1 * act'(acc0), out1 = extra * act(acc0)
+};
+
+// out[m][n] = epilogue(sum_k A(m, k) B(n, k)), fp32 sums, bf16 out.
+struct DenseOp {
+    int32_t epi = kEpiLinear;
+    int64_t m = 0, n = 0, k = 0;
+    int32_t dtype = SPCONV_BF16;     // of A and B: SPCONV_BF16 or SPCONV_E4M3
+    Operand a, b;
+    int32_t k_sources = 1;           // 2: acc = A0 B0 + A1 B1
+    int32_t n_sources = 1;           // 2: out[1] = A B1 beside out[0] = A B0 (kEpiLinear, no epilogue terms)
+    int32_t act = SPCONV_ACT_NONE;
+    const float* row_scale = nullptr;            // [m]
+    const float* col_scale[2] = {nullptr, nullptr};   // [n] of b.p[0], b.p[1]
+    const float* bias = nullptr;                 // [n]
+    const void* extra = nullptr;                 // bf16 [m] rows, ld_extra apart
+    int64_t ld_extra = 0;
+    void* out[2] = {nullptr, nullptr};           // bf16 [m] rows, ld_out apart
+    int64_t ld_out = 0;
+    float* col_sums = nullptr;                   // fp32 [n] (kEpiActGrad), or null
+};
+int dense_run(const DenseOp& op, cudaStream_t s);
+
+// out[j] = sum_i v[i][j] (bf16 rows, ld apart), fp32
+int column_sums(const void* v, int64_t ld, int64_t m, int64_t n, float* out, cudaStream_t s);
+// out[j] = sum_i part[i][j] over p fp32 rows of n
+int sum_partials(const float* part, int64_t p, int64_t n, float* out, cudaStream_t s);
+// bf16 w [c_in][c_out] -> e4m3 q [c_out][c_in] with scale [c_out]
+int quantize_weight(const void* w, int32_t c_in, int32_t c_out, void* q, float* scale, cudaStream_t s);
+
+}  // namespace spconv
