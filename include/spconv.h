@@ -495,6 +495,14 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
  */
 int spconv_quantize_weight(const void* w_dev, int32_t c_in, int32_t c_out, void* q_dev, float* scale_dev, void* stream);
 
+/*
+ * Synchronise the stream and return the first error that the row-wise
+ * operators' kernels recorded on the current device since the last call of
+ * this function (SPCONV_ERR_TIMEOUT: a bounded wait ran out and the results
+ * of a call are incomplete), else SPCONV_OK.
+ */
+int spconv_rows_status(void* stream);
+
 /* Number of kernel launches enqueued by the last call on this thread. */
 int32_t spconv_last_launch_count(void);
 

@@ -50,7 +50,7 @@ from . import _native
 __all__ = ["SpconvError", "Map", "WPack", "build_map", "subm_forward", "wpack_create",
            "subm_forward_packed", "map_status", "map_info", "map_export", "map_destroy",
            "rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
-           "quantize_weight", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS", "BIT_ORDERS", "PIPELINES", "GEMMS", "library"]
+           "quantize_weight", "rows_status", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS", "BIT_ORDERS", "PIPELINES", "GEMMS", "library"]
 
 MAPPERS = {"auto": 0, "dense": 1, "sorted": 2, "hash": 3}
 PIPELINES = {"auto": 0, "fused": 1, "multi": 2, "wide": 3}
@@ -673,6 +673,12 @@ def quantize_weight(weight: torch.Tensor, *, stream: Optional[torch.cuda.Stream]
         rc = library().spconv_quantize_weight(weight.data_ptr(), c_in, c_out, q.data_ptr(), scale.data_ptr(), s)
     _check(rc, "spconv_quantize_weight")
     return q, scale
+
+
+def rows_status(stream: Optional[torch.cuda.Stream] = None) -> int:
+    """``spconv_rows_status``: 0, or the first error the row-wise operators recorded on the device since
+    the last call (synchronises)."""
+    return int(library().spconv_rows_status(_stream_ptr(stream)))
 
 
 def last_launch_count() -> int:

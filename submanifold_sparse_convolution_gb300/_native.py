@@ -86,6 +86,7 @@ SIGNATURES = {
     "spconv_gated_ffn_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P,
                                                  _P]),
     "spconv_quantize_weight": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P]),
+    "spconv_rows_status": (ctypes.c_int, [_P]),
     "spconv_last_launch_count": (ctypes.c_int32, []),
     "spconv_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
     "spconv_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -1,126 +1,41 @@
-// Products with an epilogue, the column sums of the bias gradients, and the
-// 8-bit weight layout.
+// Around the tensor-core products: rows brought into the alignment that the
+// tensor maps need, the column sums of the bias gradients, and the 8-bit weight
+// layout.
 #include "rows.cuh"
-
-#include <type_traits>
 
 namespace spconv {
 namespace {
 
-// ---- the product: 64 x 64 tiles in fp32 ---------------------------------------
-constexpr int kT = 64, kTK = 16;
+__device__ int32_t g_rows_status;   // kStatus* bits of the row-wise operators' bounded waits
 
-__device__ __forceinline__ float elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float elem(const __nv_fp8_e4m3* p) { return static_cast<float>(*p); }
-
-template <typename T, int EPI>
-__global__ void __launch_bounds__(256) k_dense_simt(const DenseOp op, int32_t n_tiles, float* part) {
-    __shared__ float sa[kTK][kT + 4], sb[2][kTK][kT + 4];
-    __shared__ float sh_cols[16][kT];
-    constexpr int kAcc = (EPI == kEpiGated || EPI == kEpiGatedGrad) ? 2 : 1;
-    const int src = static_cast<int>(blockIdx.y);   // n source
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x / n_tiles) * kT, n0 = static_cast<int64_t>(blockIdx.x % n_tiles) * kT;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[kAcc][4][4] = {};
-    for (int ks = 0; ks < op.k_sources; ++ks) {
-        const T* A = static_cast<const T*>(op.a.p[ks]);
-        for (int64_t k0 = 0; k0 < op.k; k0 += kTK) {
-            for (int i = threadIdx.x; i < kT * kTK; i += 256) {
-                const int r = op.a.k_major ? i / kTK : i % kT, k = op.a.k_major ? i % kTK : i / kT;
-                const int64_t gm = m0 + r, gk = k0 + k;
-                sa[k][r] = gm < op.m && gk < op.k ? elem(A + (op.a.k_major ? gm * op.a.ld + gk : gk * op.a.ld + gm)) : 0.0f;
-            }
-#pragma unroll
-            for (int q = 0; q < kAcc; ++q) {
-                const T* B = static_cast<const T*>(op.b.p[kAcc == 2 ? q : (op.k_sources == 2 ? ks : src)]);
-                for (int i = threadIdx.x; i < kT * kTK; i += 256) {
-                    const int r = op.b.k_major ? i / kTK : i % kT, k = op.b.k_major ? i % kTK : i / kT;
-                    const int64_t gn = n0 + r, gk = k0 + k;
-                    sb[q][k][r] =
-                        gn < op.n && gk < op.k ? elem(B + (op.b.k_major ? gn * op.b.ld + gk : gk * op.b.ld + gn)) : 0.0f;
-                }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kTK; ++k)
-#pragma unroll
-                for (int q = 0; q < kAcc; ++q)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[q][i][j] = fmaf(sa[k][ty + 16 * i], sb[q][k][tx + 16 * j], acc[q][i][j]);
-            __syncthreads();
-        }
-    }
-    const __nv_bfloat16* extra = static_cast<const __nv_bfloat16*>(op.extra);
-    __nv_bfloat16* out0 = static_cast<__nv_bfloat16*>(op.out[EPI == kEpiLinear ? src : 0]);
-    __nv_bfloat16* out1 = static_cast<__nv_bfloat16*>(op.out[1]);
-    float cols[4] = {};
-    with_act(op.act, [&](auto act) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-                if (m >= op.m || n >= op.n) continue;
-                float z = acc[0][i][j];
-                const float rs = op.row_scale ? op.row_scale[m] : 1.0f;
-                if (op.col_scale[0]) z *= rs * op.col_scale[0][n];
-                const int64_t o = m * op.ld_out + n;
-                const float ex = extra ? __bfloat162float(extra[m * op.ld_extra + n]) : 0.0f;
-                if (EPI == kEpiLinear) {
-                    if (op.bias) z += op.bias[n];
-                    out0[o] = __float2bfloat16_rn(act_f<act>(z) + ex);
-                } else if (EPI == kEpiActGrad) {
-                    if (op.bias) z += op.bias[n];
-                    float a;
-                    const float dz = ex * act_grad_f<act>(z, &a);
-                    cols[j] += dz;
-                    out0[o] = __float2bfloat16_rn(dz);
-                } else {
-                    float u = acc[kAcc - 1][i][j];
-                    if (op.col_scale[1]) u *= rs * op.col_scale[1][n];
-                    if (EPI == kEpiGated) {
-                        out0[o] = __float2bfloat16_rn(act_f<act>(z) * u);
-                    } else {
-                        float a;
-                        const float slope = act_grad_f<act>(z, &a);
-                        out0[o] = __float2bfloat16_rn(ex * u * slope);
-                        out1[o] = __float2bfloat16_rn(ex * a);
-                    }
-                }
-            }
-    });
-    if (EPI == kEpiActGrad && part) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sh_cols[ty][tx + 16 * j] = cols[j];
-        __syncthreads();
-        if (threadIdx.x < kT && n0 + threadIdx.x < op.n) {
-            float t = 0.0f;
-            for (int y = 0; y < 16; ++y) t += sh_cols[y][threadIdx.x];
-            part[(blockIdx.x / n_tiles) * op.n + n0 + threadIdx.x] = t;
-        }
-    }
-}
-
+// ---- copies between aligned and unaligned rows ------------------------------------
+// Eight elements per thread; the side whose rows are 16-byte aligned moves as one
+// vector.
 template <typename T>
-int run_simt(const DenseOp& op, cudaStream_t s) {
-    const int64_t tm = ceil_div(op.m, kT), tn = ceil_div(op.n, kT);
-    if (tm * tn > 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
-    Scratch part(op.col_sums ? static_cast<size_t>(tm) * op.n * 4 : 0, s);
-    if (part.failed()) return SPCONV_ERR_OOM;
-    const dim3 grid(static_cast<unsigned>(tm * tn), static_cast<unsigned>(op.n_sources));
-    const int32_t nt = static_cast<int32_t>(tn);
-    count_launch();
-    switch (op.epi) {
-        case kEpiGated: k_dense_simt<T, kEpiGated><<<grid, 256, 0, s>>>(op, nt, nullptr); break;
-        case kEpiActGrad: k_dense_simt<T, kEpiActGrad><<<grid, 256, 0, s>>>(op, nt, part.as<float>()); break;
-        case kEpiGatedGrad: k_dense_simt<T, kEpiGatedGrad><<<grid, 256, 0, s>>>(op, nt, nullptr); break;
-        default: k_dense_simt<T, kEpiLinear><<<grid, 256, 0, s>>>(op, nt, nullptr);
+__global__ void __launch_bounds__(256) k_copy_rows(const T* src, int64_t ld_src, T* dst, int64_t ld_dst, int64_t rows,
+                                                   int64_t cols, int64_t row_groups, bool vec_src, bool vec_dst) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t r = i / row_groups, c = (i - r * row_groups) * 8;
+    if (r >= rows) return;
+    struct alignas(8 * sizeof(T)) V {
+        T v[8];
+    } t;
+    const T* s = src + r * ld_src + c;
+    T* d = dst + r * ld_dst + c;
+    const bool whole = c + 8 <= cols;
+    if (vec_src && whole) {
+        t = *reinterpret_cast<const V*>(s);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t.v[j] = c + j < cols ? s[j] : T(0);
     }
-    SPCONV_CHECK(launch_status());
-    return op.col_sums ? sum_partials(part.as<float>(), tm, op.n, op.col_sums, s) : SPCONV_OK;
+    if (vec_dst && whole) {
+        *reinterpret_cast<V*>(d) = t;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < cols) d[j] = t.v[j];
+    }
 }
 
 // ---- column sums ----------------------------------------------------------------
@@ -219,11 +134,93 @@ __global__ void __launch_bounds__(256) k_quantize_weight(const __nv_bfloat16* w,
     }
 }
 
+int copy_rows(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t rows, int64_t cols, size_t es, cudaStream_t s) {
+    const int64_t groups = ceil_div(cols, 8), blocks = ceil_div(rows * groups, 256);
+    if (blocks > 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
+    auto vec = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % (8 * es) == 0 && ld % 8 == 0; };
+    const bool vs = vec(src, ld_src), vd = vec(dst, ld_dst);
+    count_launch();
+    if (es == 1)
+        k_copy_rows<uint8_t><<<static_cast<unsigned>(blocks), 256, 0, s>>>(static_cast<const uint8_t*>(src), ld_src,
+                                                                           static_cast<uint8_t*>(dst), ld_dst, rows, cols, groups, vs, vd);
+    else
+        k_copy_rows<uint16_t><<<static_cast<unsigned>(blocks), 256, 0, s>>>(static_cast<const uint16_t*>(src), ld_src,
+                                                                            static_cast<uint16_t*>(dst), ld_dst, rows, cols, groups, vs, vd);
+    return launch_status();
+}
+
 }  // namespace
+
+int rows_status_word(int32_t** word) {
+    static int32_t* words[kMaxDevices] = {};
+    int dev = 0;
+    SPCONV_CHECK_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= kMaxDevices) return SPCONV_ERR_UNSUPPORTED;
+    if (!words[dev]) {
+        void* p = nullptr;
+        SPCONV_CHECK_CUDA(cudaGetSymbolAddress(&p, g_rows_status));
+        words[dev] = static_cast<int32_t*>(p);
+    }
+    *word = words[dev];
+    return SPCONV_OK;
+}
 
 int dense_run(const DenseOp& op, cudaStream_t s) {
     if (op.m == 0 || op.n == 0) return SPCONV_OK;
-    return op.dtype == SPCONV_E4M3 ? run_simt<__nv_fp8_e4m3>(op, s) : run_simt<__nv_bfloat16>(op, s);
+    int32_t* status = nullptr;
+    SPCONV_CHECK(rows_status_word(&status));
+    // The tensor maps need 16-byte aligned rows.  Matrices without them (odd
+    // channel counts, strides or addresses) are copied to rows that have them,
+    // and such an output is copied back: one extra pass over that matrix.
+    const size_t es = op.dtype == SPCONV_E4M3 ? 1 : 2;
+    const bool dual = op.epi == kEpiGated || op.epi == kEpiGatedGrad;
+    const int na = op.k_sources, nb = dual || op.k_sources == 2 || op.n_sources == 2 ? 2 : 1;
+    const int nc = op.epi == kEpiGatedGrad || op.n_sources == 2 ? 2 : 1;
+    struct Matrix {   // up to two matrices of one shape
+        int64_t rows, cols;
+        size_t es;
+        bool move;
+        size_t off[2];
+        int64_t ld() const { return static_cast<int64_t>(round_up(static_cast<size_t>(cols), 16 / es)); }
+    };
+    size_t bytes = 0;
+    auto plan = [&](const void* const* ptr, int count, int64_t ld, int64_t rows, int64_t cols, size_t e) {
+        Matrix t{rows, cols, e, false, {0, 0}};
+        for (int i = 0; i < count; ++i) t.move = t.move || !tma_ok(ptr[i], ld, e);
+        for (int i = 0; t.move && i < count; ++i) {
+            t.off[i] = bytes;
+            bytes += round_up(static_cast<size_t>(rows) * t.ld() * e, 256);
+        }
+        return t;
+    };
+    const Matrix ma = op.a.k_major ? plan(op.a.p, na, op.a.ld, op.m, op.k, es) : plan(op.a.p, na, op.a.ld, op.k, op.m, es);
+    const Matrix mb = op.b.k_major ? plan(op.b.p, nb, op.b.ld, op.n, op.k, es) : plan(op.b.p, nb, op.b.ld, op.k, op.n, es);
+    const Matrix mx = plan(&op.extra, op.extra ? 1 : 0, op.ld_extra, op.m, op.n, 2);
+    const Matrix mc = plan(op.out, nc, op.ld_out, op.m, op.n, 2);
+    if (bytes == 0) return dense_tc_run(op, status, s);
+    Scratch buf(bytes, s);
+    if (buf.failed()) return SPCONV_ERR_OOM;
+    DenseOp o = op;
+    auto bring = [&](const Matrix& t, const void** ptr, int count, int64_t* ld) -> int {
+        if (!t.move) return SPCONV_OK;
+        for (int i = 0; i < count; ++i) {
+            SPCONV_CHECK(copy_rows(ptr[i], *ld, buf.as<void>(t.off[i]), t.ld(), t.rows, t.cols, t.es, s));
+            ptr[i] = buf.as<void>(t.off[i]);
+        }
+        *ld = t.ld();
+        return SPCONV_OK;
+    };
+    SPCONV_CHECK(bring(ma, o.a.p, na, &o.a.ld));
+    SPCONV_CHECK(bring(mb, o.b.p, nb, &o.b.ld));
+    SPCONV_CHECK(bring(mx, &o.extra, 1, &o.ld_extra));
+    if (mc.move) {
+        for (int i = 0; i < nc; ++i) o.out[i] = buf.as<void>(mc.off[i]);
+        o.ld_out = mc.ld();
+    }
+    SPCONV_CHECK(dense_tc_run(o, status, s));
+    for (int i = 0; mc.move && i < nc; ++i)
+        SPCONV_CHECK(copy_rows(o.out[i], o.ld_out, op.out[i], op.ld_out, op.m, op.n, 2, s));
+    return SPCONV_OK;
 }
 
 int sum_partials(const float* part, int64_t p, int64_t n, float* out, cudaStream_t s) {

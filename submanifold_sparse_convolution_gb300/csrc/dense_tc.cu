@@ -1,0 +1,649 @@
+// Products with an epilogue on the 5th-generation tensor cores.
+//
+//   out[m][n] = epilogue(sum_k A(m, k) B(n, k))
+//
+// A pair of CTAs works on one tile of 256 rows by 2 `hb` columns (hb = 64 or
+// 128): tcgen05.mma with cta_group::2, each CTA bringing its 128 rows of A and
+// hb rows of B, so an operand byte fetched from L2 feeds twice the products it
+// would in one CTA.  For a gated product CTA 0 brings hb rows of the gate's
+// weight and CTA 1 the same rows of the up weight: columns [0, hb) of the
+// accumulator are gate, [hb, 2 hb) up, side by side in each thread's row.
+//
+// Either operand may be K-major or have its rows contiguous (forward weights
+// [c_in][c_out], and x^T, dz^T of the weight gradients): the tensor maps and
+// the shared-memory descriptors take both as they lie in memory.
+//
+// Warps of each CTA (persistent over the tiles):
+//   warp 0     tensor-map loads into a ring of stages; both CTAs' loads
+//              complete on CTA 0's barrier
+//   warp 1     MMA issue (CTA 0), TMEM allocation
+//   warps 2-9  epilogue, two warps per 32 accumulator rows: 32 columns at a
+//              time from TMEM, fp32 epilogue, one rounding, staged in shared
+//              memory and stored by a tensor-map copy, which also clips the
+//              ragged edges; the residual or incoming gradient arrives in the
+//              same staging buffer by a tensor-map load before the accumulator
+//              is ready
+// The accumulator is double-buffered in TMEM (2 x 256 columns), so the
+// epilogue of one tile runs beside the main loop of the next.
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "ptx_sm100.cuh"
+#include "rows.cuh"
+
+namespace spconv {
+namespace {
+
+constexpr int kRowsA = 128;                   // rows of A per CTA
+constexpr int kStageA = kRowsA * 128;         // 128 bytes of K per stage
+constexpr int kStageB = 128 * 128;            // hb <= 128 rows
+constexpr int kStage = kStageA + kStageB;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kStaging = 32 * 128;            // 32 rows x 64 bf16, one epilogue warp
+constexpr int kTmemCols = 512;
+constexpr int kGroupM = 16;                   // row tiles that share the column tiles in L2
+constexpr int kPairs = 76;                    // CTA pairs of a full GPU
+
+constexpr int32_t kEpiPartial = 4;            // fp32 sums of one slice of K, to a workspace
+
+struct TcArgs {
+    CUtensorMap a[2], b[2], c[2], x;
+    int64_t m, n;
+    int32_t k_iters;       // stages of one source
+    int32_t k_total;       // stages of all sources
+    int32_t tiles_m, tiles_n, n_sources;
+    int32_t splits, split_iters;   // slices of K, stages of a slice
+    int32_t hb;
+    int32_t a_kmajor, b_kmajor;
+    int32_t k_sources;
+    int32_t act;
+    int32_t has_extra;
+    const float* row_scale;
+    const float* col_scale[2];
+    const float* bias;
+    float* part;           // kEpiActGrad: column sums of 32 rows each, [8 tiles_m][n], or null;
+                           // kEpiPartial: [splits][n_sources][m][n]
+    int32_t* status;
+};
+
+template <int EPI>
+struct TcConfig {
+    static constexpr int kBufs = EPI == kEpiGatedGrad ? 2 : 1;   // staging buffers of an epilogue warp
+    static constexpr int kStages = EPI == kEpiGatedGrad ? 5 : 6;
+    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kBufs * kStaging + 512;
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Eight fp32 values, as their bits, to bf16.
+__device__ __forceinline__ uint4 pack8(const uint32_t* v) {
+    auto two = [&](int j) { return bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])); };
+    return make_uint4(two(0), two(2), two(4), two(6));
+}
+
+// Sums of the fp32 values v[j] (as bits) over the 32 lanes: lane l returns that of column l.
+__device__ __forceinline__ float column_sum32(uint32_t (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+            const uint32_t send = up ? v[j] : v[j + o];
+            const float keep = __uint_as_float(up ? v[j + o] : v[j]);
+            v[j] = __float_as_uint(keep + __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, send, o)));
+        }
+    }
+    return __uint_as_float(v[0]);
+}
+
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) { ptx::tmem_ld_32x32b_x32(addr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { ptx::tmem_ld_32x32b_x16(addr, r); }
+
+template <int EPI, bool E4M3>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense_tc(const __grid_constant__ TcArgs p) {
+    using Cfg = TcConfig<EPI>;
+    constexpr int S = Cfg::kStages;
+    constexpr bool kDual = EPI == kEpiGated || EPI == kEpiGatedGrad;
+    constexpr int kBK = E4M3 ? 128 : 64;      // K elements of a stage
+    // accumulator columns a thread takes at once: 32, or 16 where 32 would spill
+    constexpr int CW = (EPI == kEpiGatedGrad || (EPI == kEpiLinear && E4M3)) ? 16 : 32;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+    uint8_t* staging = smem + S * kStage;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiWarps * Cfg::kBufs * kStaging);
+    uint64_t* full = bars;              // [S]  (CTA 0's are used)
+    uint64_t* empty = full + S;         // [S]
+    uint64_t* acc_full = empty + S;     // [2]
+    uint64_t* acc_empty = acc_full + 2; // [2]  (CTA 0's are used)
+    uint64_t* exit_bar = acc_empty + 2;
+    uint64_t* extra_full = exit_bar + 1;   // [kEpiWarps]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(extra_full + kEpiWarps);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&acc_full[b], 1);
+            ptx::mbar_init(&acc_empty[b], 2 * kEpiWarps);
+        }
+        ptx::mbar_init(exit_bar, 1);
+        for (int w = 0; w < kEpiWarps; ++w) ptx::mbar_init(&extra_full[w], 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_map(&p.a[0]);
+        ptx::prefetch_map(&p.b[0]);
+        ptx::prefetch_map(&p.c[0]);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(tmem_slot, kTmemCols);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t smem_base = ptx::smem_u32(smem);
+
+    auto fail = [&]() {
+        atomicOr(p.status, kStatusTimeout);
+        *abort_flag = 1;
+    };
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xFFFFFFFFu, ptx::mbar_wait(bar, parity, abort_flag));
+    };
+    const int32_t tiles_nn = p.tiles_n * p.n_sources;
+    const int32_t tiles = p.tiles_m * tiles_nn;
+    const int32_t units = tiles * p.splits;
+    const int32_t pair = static_cast<int32_t>(blockIdx.x >> 1), n_pairs = static_cast<int32_t>(gridDim.x >> 1);
+    struct Unit {
+        int32_t tm, tn, src, k0, k1, split;
+    };
+    auto decode = [&](int32_t u) {
+        Unit t;
+        t.split = u / tiles;
+        const int32_t i = u - t.split * tiles;
+        const int32_t grp = i / (kGroupM * tiles_nn);
+        const int32_t first = grp * kGroupM;
+        const int32_t gm = p.tiles_m - first < kGroupM ? p.tiles_m - first : kGroupM;
+        const int32_t r = i - grp * kGroupM * tiles_nn;
+        t.tm = first + r % gm;
+        const int32_t nn = r / gm;
+        t.src = nn / p.tiles_n;
+        t.tn = nn - t.src * p.tiles_n;
+        t.k0 = t.split * p.split_iters;
+        t.k1 = t.k0 + p.split_iters < p.k_total ? t.k0 + p.split_iters : p.k_total;
+        return t;
+    };
+
+    if (warp == 0) {
+        // ---------------- loads
+        if (lane == 0) {
+            const uint32_t bytes = 2u * (kStageA + static_cast<uint32_t>(p.hb) * 128u);
+            uint32_t f = 0;
+            bool ok = true;
+            for (int32_t u = pair; u < units && ok; u += n_pairs) {
+                const Unit t = decode(u);
+                const int32_t m0 = t.tm * 256 + static_cast<int32_t>(rank) * kRowsA;
+                const int32_t n0 = kDual ? t.tn * p.hb : t.tn * 2 * p.hb + static_cast<int32_t>(rank) * p.hb;
+                for (int32_t it = t.k0; it < t.k1; ++it, ++f) {
+                    const uint32_t s = f % S;
+                    if (f >= S && !ptx::mbar_wait(&empty[s], (f / S - 1) & 1, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    const int32_t ks = it >= p.k_iters ? 1 : 0;
+                    const int32_t k = (it - ks * p.k_iters) * kBK;
+                    const CUtensorMap* ma = &p.a[ks];
+                    const CUtensorMap* mb = &p.b[kDual ? rank : p.k_sources == 2 ? ks : t.src];
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], bytes);
+                    const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(&full[s]), 0);
+                    const uint32_t sa = smem_base + s * kStage, sb = sa + kStageA;
+                    if (p.a_kmajor) {
+                        ptx::tma_load_2d_pair(sa, ma, k, m0, bar);
+                    } else {
+                        ptx::tma_load_2d_pair(sa, ma, m0, k, bar);
+                        ptx::tma_load_2d_pair(sa + 8192, ma, m0 + 64, k, bar);
+                    }
+                    if (p.b_kmajor) {
+                        ptx::tma_load_2d_pair(sb, mb, k, n0, bar);
+                    } else {
+                        ptx::tma_load_2d_pair(sb, mb, n0, k, bar);
+                        if (p.hb > 64) ptx::tma_load_2d_pair(sb + 8192, mb, n0 + 64, k, bar);
+                    }
+                }
+            }
+            if (!ok && rank == 0)   // loads still in flight land before the CTAs exit
+                for (uint32_t s = 0; s < S && s < f; ++s) {
+                    const uint32_t last = (f - 1 - s) / S;   // fill number of stage s
+                    ptx::mbar_wait(&full[s], last & 1, nullptr);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issue (the warp runs the loop, lane 0 of CTA 0 issues)
+        if (rank == 0) {
+            const uint32_t leader = lane == 0;
+            const uint32_t idesc = ptx::idesc_dense(E4M3, p.a_kmajor, p.b_kmajor, 256, static_cast<uint32_t>(2 * p.hb));
+            const uint64_t a0 = p.a_kmajor ? ptx::sdesc_k128(smem_base) : ptx::sdesc_mn128(smem_base, 64);
+            const uint64_t b0 = p.b_kmajor ? ptx::sdesc_k128(smem_base + kStageA) : ptx::sdesc_mn128(smem_base + kStageA, 64);
+            // one MMA contracts 32 bytes of a K-major row, or 16 rows of 128 bytes
+            const uint64_t da = p.a_kmajor ? 2 : 128, db = p.b_kmajor ? 2 : 128;
+            uint32_t f = 0;
+            int32_t ai = 0;
+            bool ok = true;
+            for (int32_t u = pair; u < units && ok; u += n_pairs, ++ai) {
+                const Unit t = decode(u);
+                const int buf = ai & 1;
+                const uint32_t v = static_cast<uint32_t>(ai >> 1);
+                if (v > 0 && !warp_wait(&acc_empty[buf], (v - 1) & 1)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(buf * 256);
+                for (int32_t it = t.k0; it < t.k1; ++it, ++f) {
+                    const uint32_t s = f % S;
+                    if (!warp_wait(&full[s], (f / S) & 1)) {
+                        if (lane == 0) fail();
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint64_t off = static_cast<uint64_t>((s * kStage) >> 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ptx::mma_pair_if<E4M3>(leader, d, a0 + off + j * da, b0 + off + j * db, idesc,
+                                               (it > t.k0 || j > 0) ? 1u : 0u);
+                    ptx::mma_commit_pair_if(leader, &empty[s]);
+                }
+                if (ok) ptx::mma_commit_pair_if(leader, &acc_full[buf]);
+            }
+            // every MMA, and every arrival it sends to either CTA, is done once
+            // exit_bar flips; TMEM is freed after that
+            ptx::mma_commit_pair_if(leader, exit_bar);
+            const bool done = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(exit_bar, 0, nullptr));
+            if (!done && lane == 0) atomicOr(p.status, kStatusTimeout);
+        }
+    } else {
+        // ---------------- epilogue
+        const int e = warp - 2;
+        const int quarter = warp & 3;            // the TMEM lanes a warp may read
+        const int half = e >> 2;
+        uint8_t* stage0 = staging + e * Cfg::kBufs * kStaging;
+        const uint32_t st0 = ptx::smem_u32(stage0);
+        const uint32_t row_off = static_cast<uint32_t>(lane) * 128;
+        const uint32_t sw = lane & 7;
+        uint64_t* xbar = &extra_full[e];
+        uint32_t xphase = 0;
+        const uint32_t acc_bar = ptx::map_to_rank(ptx::smem_u32(&acc_empty[0]), 0);
+        const int chunks = (kDual ? p.hb : 2 * p.hb) / 64;
+        int32_t ai = 0;
+        for (int32_t u = pair; u < units; u += n_pairs, ++ai) {
+            const Unit t = decode(u);
+            const int buf = ai & 1;
+            const int32_t m0 = t.tm * 256 + static_cast<int32_t>(rank) * kRowsA + quarter * 32;
+            const int64_t row = m0 + lane;
+            const int32_t col0 = t.tn * (kDual ? p.hb : 2 * p.hb);
+            const bool rows_live = m0 < p.m;
+            const bool row_live = row < p.m;
+            const float rs = (p.row_scale && row_live) ? p.row_scale[row] : 1.0f;
+            bool waited = false;
+            bool ok = true;
+            for (int c = half; c < chunks; c += 2) {
+                const int32_t n0 = col0 + c * 64;
+                const bool live = rows_live && n0 < p.n;   // (warp-uniform)
+                if (EPI != kEpiPartial && live) {
+                    // the staging buffer is free once its last store has been read out
+                    if (lane == 0) {
+                        ptx::bulk_wait_read();
+                        if (EPI != kEpiGated && p.has_extra) {
+                            ptx::mbar_arrive_expect_tx(xbar, kStaging);
+                            ptx::tma_load_2d(st0, &p.x, n0, m0, ptx::smem_u32(xbar));
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!waited) {
+                    if (!warp_wait(&acc_full[buf], (static_cast<uint32_t>(ai) >> 1) & 1)) {
+                        if (lane == 0) fail();
+                        ok = false;
+                    }
+                    ptx::tc_fence_after();
+                    waited = true;
+                }
+                if (EPI != kEpiPartial && EPI != kEpiGated && live && p.has_extra) {
+                    // (also after a failed wait above: the copy must land before the CTA exits)
+                    if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(xbar, xphase, nullptr))) {
+                        if (lane == 0) fail();
+                        ok = false;
+                    }
+                    xphase ^= 1;
+                }
+                if (!ok) break;
+                if (!live) continue;
+                const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * 256 + c * 64);
+#pragma unroll 1
+                for (int h = 0; h < 64 / CW; ++h) {
+                    uint32_t z[CW], w[CW];
+                    tmem_ld(ta + h * CW, z);
+                    if (kDual) tmem_ld(ta + p.hb + h * CW, w);
+                    ptx::tmem_ld_wait();
+                    const int32_t nc = n0 + h * CW;
+                    if (EPI == kEpiPartial) {
+                        if (row_live) {
+                            float* dst = p.part + ((static_cast<int64_t>(t.split) * p.n_sources + t.src) * p.m + row) * p.n + nc;
+                            if (p.n % 4 == 0) {
+#pragma unroll
+                                for (int j = 0; j < CW; j += 4)
+                                    if (nc + j < p.n)
+                                        *reinterpret_cast<uint4*>(dst + j) = make_uint4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < CW; ++j)
+                                    if (nc + j < p.n) dst[j] = __uint_as_float(z[j]);
+                            }
+                        }
+                        continue;
+                    }
+                    // extra: this thread's CW columns, 16-byte pieces in the 128-byte swizzle
+                    uint32_t x[CW / 2];
+                    if (EPI != kEpiGated) {
+#pragma unroll
+                        for (int q = 0; q < CW / 8; ++q) {
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (p.has_extra)
+                                v = *reinterpret_cast<const uint4*>(stage0 + row_off + (((h * (CW / 8) + q) ^ sw) << 4));
+                            x[4 * q] = v.x;
+                            x[4 * q + 1] = v.y;
+                            x[4 * q + 2] = v.z;
+                            x[4 * q + 3] = v.w;
+                        }
+                    }
+                    if (E4M3) {
+#pragma unroll
+                        for (int j = 0; j < CW; ++j) {
+                            const int32_t n = nc + j;
+                            const float s0 = n < p.n ? __ldg(p.col_scale[0] + n) : 0.0f;
+                            z[j] = __float_as_uint(__uint_as_float(z[j]) * (rs * s0));
+                            if (kDual) {
+                                const float s1 = n < p.n ? __ldg(p.col_scale[1] + n) : 0.0f;
+                                w[j] = __float_as_uint(__uint_as_float(w[j]) * (rs * s1));
+                            }
+                        }
+                    }
+                    if (!kDual && p.bias) {
+#pragma unroll
+                        for (int j = 0; j < CW; ++j)
+                            z[j] = __float_as_uint(__uint_as_float(z[j]) + (nc + j < p.n ? __ldg(p.bias + nc + j) : 0.0f));
+                    }
+                    // the results take the places of what they are made of: y in z, the
+                    // second output in w
+                    with_act(p.act, [&](auto act) {
+#pragma unroll
+                        for (int j = 0; j < CW; ++j) {
+                            const float zz = __uint_as_float(z[j]);
+                            const float ww = kDual ? __uint_as_float(w[j]) : 0.0f;
+                            const float xx = EPI == kEpiGated
+                                                 ? 0.0f
+                                                 : __uint_as_float(j & 1 ? (x[j / 2] & 0xFFFF0000u) : (x[j / 2] << 16));
+                            float y;
+                            if (EPI == kEpiLinear) {
+                                y = act_f<act>(zz) + xx;
+                            } else if (EPI == kEpiGated) {
+                                y = act_f<act>(zz) * ww;
+                            } else {
+                                float a;
+                                const float slope = act_grad_f<act>(zz, &a);
+                                if (EPI == kEpiActGrad) {
+                                    y = row_live ? xx * slope : 0.0f;
+                                } else {
+                                    y = xx * ww * slope;
+                                    w[j] = __float_as_uint(xx * a);
+                                }
+                            }
+                            z[j] = __float_as_uint(y);
+                        }
+                    });
+#pragma unroll
+                    for (int q = 0; q < CW / 8; ++q) {
+                        const uint32_t at = row_off + (((h * (CW / 8) + q) ^ sw) << 4);
+                        *reinterpret_cast<uint4*>(stage0 + at) = pack8(z + 8 * q);
+                        if (EPI == kEpiGatedGrad) *reinterpret_cast<uint4*>(stage0 + kStaging + at) = pack8(w + 8 * q);
+                    }
+                    if constexpr (EPI == kEpiActGrad) {
+                        if (p.part) {
+                            const float s = column_sum32(z, lane);
+                            const int64_t pr = static_cast<int64_t>(t.tm) * 8 + rank * 4 + quarter;
+                            if (nc + lane < p.n) p.part[pr * p.n + nc + lane] = s;
+                        }
+                    }
+                }
+                if (EPI != kEpiPartial) {
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::tma_store_2d(&p.c[EPI == kEpiLinear ? t.src : 0], n0, m0, st0);
+                        if (EPI == kEpiGatedGrad) ptx::tma_store_2d(&p.c[1], n0, m0, st0 + kStaging);
+                        ptx::bulk_commit();
+                    }
+                }
+            }
+            // (a warp without a chunk of this tile still takes its turn)
+            if (!waited && !warp_wait(&acc_full[buf], (static_cast<uint32_t>(ai) >> 1) & 1)) {
+                if (lane == 0) fail();
+                ok = false;
+            }
+            if (!ok) break;
+            // rows past m of the column sums: whole 32-row groups without a row
+            if (EPI == kEpiActGrad && p.part && !rows_live) {
+                const int64_t pr = static_cast<int64_t>(t.tm) * 8 + rank * 4 + quarter;
+                for (int c = half; c < chunks; c += 2)
+                    for (int j = lane; j < 64; j += 32)
+                        if (col0 + c * 64 + j < p.n) p.part[pr * p.n + col0 + c * 64 + j] = 0.0f;
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(acc_bar + static_cast<uint32_t>(buf) * 8);
+        }
+        if (lane == 0) ptx::bulk_wait();
+        __syncwarp();
+    }
+    // neither CTA leaves, or frees TMEM, while the other may still signal it:
+    // once both have ended their roles, CTA 1 waits for the last arrival that
+    // CTA 0's MMAs send it
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    if (warp == 1 && rank == 1 && !ptx::mbar_wait(exit_bar, 0, nullptr)) atomicOr(p.status, kStatusTimeout);
+    __syncwarp();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// out = bf16(sum over the slices of K), a fixed order.
+__global__ void __launch_bounds__(256) k_sum_slices(const float* part, int32_t splits, int64_t slice, int64_t count, int64_t m,
+                                                    int64_t n, __nv_bfloat16* out0, __nv_bfloat16* out1, int64_t ld) {
+    pdl_wait();
+    pdl_trigger();
+    // four elements of one source and row per thread when n allows
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (i >= count) return;
+    float s[4] = {};
+    const int64_t left = count - i;
+    if (left >= 4 && slice % 4 == 0) {
+#pragma unroll 4
+        for (int32_t k = 0; k < splits; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(part + k * slice + i);
+            s[0] += v.x;
+            s[1] += v.y;
+            s[2] += v.z;
+            s[3] += v.w;
+        }
+    } else {
+        for (int32_t k = 0; k < splits; ++k)
+            for (int j = 0; j < 4; ++j)
+                if (j < left) s[j] += part[k * slice + i + j];
+    }
+    for (int j = 0; j < 4; ++j) {
+        if (j >= left) break;
+        const int64_t src = (i + j) / (m * n), r = (i + j) % (m * n);
+        (src ? out1 : out0)[r / n * ld + r % n] = __float2bfloat16_rn(s[j]);
+    }
+}
+
+// ---- host -------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// A [outer] x [inner] matrix of rows `ld` elements apart, copied in boxes of
+// box_inner (128 bytes) x box_outer, 128-byte swizzled in shared memory.
+int make_map(CUtensorMap* map, const void* base, size_t es, int64_t inner, int64_t outer, int64_t ld, int32_t box_outer) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return SPCONV_ERR_CUDA;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_outer)};
+    const cuuint32_t unit[2] = {1, 1};
+    const CUresult r = fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                          const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SPCONV_OK : SPCONV_ERR_CUDA;
+}
+
+template <int EPI, bool E4M3>
+int launch(const TcArgs& args, int32_t pairs, cudaStream_t s) {
+    static bool set[kMaxDevices] = {};
+    int dev = 0;
+    SPCONV_CHECK_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= kMaxDevices) return SPCONV_ERR_UNSUPPORTED;
+    if (!set[dev]) {
+        SPCONV_CHECK_CUDA(cudaFuncSetAttribute(k_dense_tc<EPI, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               TcConfig<EPI>::kSmem));
+        set[dev] = true;
+    }
+    cudaLaunchAttribute at[1] = {pdl_attr()};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = TcConfig<EPI>::kSmem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    count_launch();
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_dense_tc<EPI, E4M3>, args));
+}
+
+}  // namespace
+
+int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
+    const size_t es = op.dtype == SPCONV_E4M3 ? 1 : 2;
+    const int32_t bk = static_cast<int32_t>(128 / es);
+    const bool dual = op.epi == kEpiGated || op.epi == kEpiGatedGrad;
+    TcArgs p = {};
+    p.m = op.m;
+    p.n = op.n;
+    p.k_iters = static_cast<int32_t>(ceil_div(op.k, bk));
+    p.k_sources = op.k_sources;
+    p.k_total = p.k_iters * op.k_sources;
+    p.n_sources = op.n_sources;
+    p.a_kmajor = op.a.k_major;
+    p.b_kmajor = op.b.k_major;
+    p.act = op.act;
+    p.has_extra = op.extra != nullptr;
+    p.row_scale = op.row_scale;
+    p.col_scale[0] = op.col_scale[0];
+    p.col_scale[1] = op.col_scale[1];
+    p.bias = op.bias;
+    p.status = status;
+    p.tiles_m = static_cast<int32_t>(ceil_div(op.m, 256));
+    // 256-column tiles reuse an operand byte most; 128 columns when those would
+    // leave pairs without a tile, or be half empty
+    auto tiles_of = [&](int32_t hb) { return p.tiles_m * ceil_div(op.n, dual ? hb : 2 * hb) * op.n_sources; };
+    p.hb = (op.n <= (dual ? 64 : 128) || tiles_of(128) < kPairs) ? 64 : 128;
+    p.tiles_n = static_cast<int32_t>(ceil_div(op.n, dual ? p.hb : 2 * p.hb));
+    const int64_t tiles = tiles_of(p.hb);
+    if (tiles > 0x3FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
+    // Long contractions with few tiles (the weight gradients) are cut along K
+    p.splits = 1;
+    p.split_iters = p.k_total;
+    const bool plain = op.epi == kEpiLinear && op.act == SPCONV_ACT_NONE && !op.extra && !op.bias && !op.col_scale[0];
+    if (plain && tiles < kPairs && p.k_total >= 16) {
+        int64_t want = kPairs / tiles;
+        if (want > p.k_total / 8) want = p.k_total / 8;
+        p.split_iters = static_cast<int32_t>(ceil_div(p.k_total, want));
+        p.splits = static_cast<int32_t>(ceil_div(p.k_total, p.split_iters));
+    }
+    for (int i = 0; i < (op.k_sources == 2 ? 2 : 1); ++i)
+        SPCONV_CHECK(op.a.k_major ? make_map(&p.a[i], op.a.p[i], es, op.k, op.m, op.a.ld, kRowsA)
+                                  : make_map(&p.a[i], op.a.p[i], es, op.m, op.k, op.a.ld, 64));
+    for (int i = 0; i < ((dual || op.k_sources == 2 || op.n_sources == 2) ? 2 : 1); ++i)
+        SPCONV_CHECK(op.b.k_major ? make_map(&p.b[i], op.b.p[i], es, op.k, op.n, op.b.ld, p.hb)
+                                  : make_map(&p.b[i], op.b.p[i], es, op.n, op.k, op.b.ld, 64));
+    if (p.splits == 1)
+        for (int i = 0; i < ((op.epi == kEpiGatedGrad || op.n_sources == 2) ? 2 : 1); ++i)
+            SPCONV_CHECK(make_map(&p.c[i], op.out[i], 2, op.n, op.m, op.ld_out, 32));
+    if (op.extra) SPCONV_CHECK(make_map(&p.x, op.extra, 2, op.n, op.m, op.ld_extra, 32));
+    const int64_t units = tiles * p.splits;
+    const int32_t pairs = static_cast<int32_t>(units < kPairs ? units : kPairs);
+
+    const int64_t part_rows = op.col_sums ? 8 * static_cast<int64_t>(p.tiles_m) : 0;
+    const int64_t slice = op.m * op.n * op.n_sources;
+    Scratch part(static_cast<size_t>(p.splits > 1 ? slice * p.splits : part_rows * op.n) * 4, s);
+    if (part.failed()) return SPCONV_ERR_OOM;
+    p.part = part.as<float>();
+    if (p.splits > 1) {
+        SPCONV_CHECK((launch<kEpiPartial, false>(p, pairs, s)));
+        cudaLaunchAttribute at[1] = {pdl_attr()};
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(slice, 1024)));
+        cfg.blockDim = dim3(256);
+        cfg.stream = s;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        count_launch();
+        return cuda_status(cudaLaunchKernelEx(&cfg, k_sum_slices, static_cast<const float*>(p.part), p.splits, slice, slice,
+                                              op.m, op.n, static_cast<__nv_bfloat16*>(op.out[0]),
+                                              static_cast<__nv_bfloat16*>(op.out[1]), op.ld_out));
+    }
+    const bool eight = op.dtype == SPCONV_E4M3;
+    switch (op.epi) {
+        case kEpiGated:
+            SPCONV_CHECK((eight ? launch<kEpiGated, true>(p, pairs, s) : launch<kEpiGated, false>(p, pairs, s)));
+            break;
+        case kEpiActGrad: SPCONV_CHECK((launch<kEpiActGrad, false>(p, pairs, s))); break;
+        case kEpiGatedGrad: SPCONV_CHECK((launch<kEpiGatedGrad, false>(p, pairs, s))); break;
+        default:
+            SPCONV_CHECK((eight ? launch<kEpiLinear, true>(p, pairs, s) : launch<kEpiLinear, false>(p, pairs, s)));
+    }
+    return op.col_sums ? sum_partials(p.part, part_rows, op.n, op.col_sums, s) : SPCONV_OK;
+}
+
+}  // namespace spconv

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -137,7 +138,7 @@ struct NormGradArgs {
 };
 int norm_backward(const NormGradArgs& a, cudaStream_t s);
 
-// ---- products with an epilogue (dense.cu) ----------------------------------
+// ---- products with an epilogue (dense.cu, dense_tc.cu) ----------------------------------
 // Element (i, k) of an operand is p[i ld + k] (k_major) or p[k ld + i].
 struct Operand {
     const void* p[2] = {nullptr, nullptr};
@@ -171,6 +172,15 @@ struct DenseOp {
     float* col_sums = nullptr;                   // fp32 [n] (kEpiActGrad), or null
 };
 int dense_run(const DenseOp& op, cudaStream_t s);
+// the same on the tensor cores (dense_tc.cu); operands, extra and out satisfy tma_ok
+int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s);
+// The device status word of the row-wise operators on the current device.
+int rows_status_word(int32_t** word);
+
+// What a tensor map takes: 16-byte aligned rows.
+inline bool tma_ok(const void* p, int64_t ld, size_t es) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * static_cast<int64_t>(es)) % 16 == 0;
+}
 
 // out[j] = sum_i v[i][j] (bf16 rows, ld apart), fp32
 int column_sums(const void* v, int64_t ld, int64_t m, int64_t n, float* out, cudaStream_t s);

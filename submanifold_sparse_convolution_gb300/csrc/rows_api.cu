@@ -15,7 +15,7 @@ struct Rows {
     const void* p;
     int64_t n, c, ld;
     size_t es;
-    bool ok() const { return p && aligned(p, es) && ld >= c && ld < (int64_t(1) << 40); }
+    bool ok() const { return p && aligned(p, es) && ld >= c && ld < (int64_t(1) << 38); }
     size_t bytes() const { return n == 0 ? 0 : (static_cast<size_t>(n - 1) * ld + c) * es; }
     bool overlaps(const Rows& o) const {
         const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
@@ -312,6 +312,18 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
         SPCONV_CHECK(dense_run(o, s));
     }
     return SPCONV_OK;
+}
+
+int spconv_rows_status(void* stream) {
+    int32_t* word = nullptr;
+    SPCONV_CHECK(rows_status_word(&word));
+    int32_t st = 0;
+    SPCONV_CHECK_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
+    SPCONV_CHECK_CUDA(cudaMemcpy(&st, word, sizeof(st), cudaMemcpyDeviceToHost));
+    if (st == 0) return SPCONV_OK;
+    const int32_t zero_word = 0;
+    SPCONV_CHECK_CUDA(cudaMemcpy(word, &zero_word, sizeof(zero_word), cudaMemcpyHostToDevice));
+    return status_from_flags(st);
 }
 
 int spconv_quantize_weight(const void* w_dev, int32_t c_in, int32_t c_out, void* q_dev, float* scale_dev, void* stream) {
