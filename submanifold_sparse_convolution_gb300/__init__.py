@@ -430,74 +430,72 @@ def map_destroy(m: Map):
 
 
 # ---- row-wise operators --------------------------------------------------------
-def _rows(t: torch.Tensor, name: str, n: int, c: int, dtype) -> int:
-    """Row stride of ``t``, checked to be [n, c] rows of ``dtype`` on the GPU."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.dim() != 2 or t.size(0) != n or t.size(1) != c:
-        raise ValueError(f"{name} must be {dtype} [{n}, {c}]")
-    if c > 1 and t.stride(1) != 1:
+# A call on a few rows costs what the host does for it, so these functions look
+# at each tensor once and allocate only outputs.
+_BF16 = torch.bfloat16
+_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device, without making a Stream object
+_c = None
+
+
+def _lib():
+    global _c
+    if _c is None:
+        _c = library()
+    return _c
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
+    """Row stride of ``t``, checked to be ``shape`` rows of ``dtype`` on the GPU."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{name} must be a {dtype} {list(shape)} CUDA tensor")
+    ld, step = t.stride()
+    n, c = shape
+    if step != 1 and c > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    ld = t.stride(0)
-    if n <= 1:
-        return max(ld, c)
     if ld < c:
-        raise ValueError(f"{name} must not have overlapping rows")
+        if n > 1:
+            raise ValueError(f"{name} must not have overlapping rows")
+        return c
     return ld
 
 
-def _vector(t: Optional[torch.Tensor], name: str, c: int) -> Optional[int]:
-    """Address of an optional fp32 [c] vector."""
-    if t is None:
-        return None
-    if not t.is_cuda or t.dtype != torch.float32 or t.dim() != 1 or t.size(0) != c or not t.is_contiguous():
+def _vector(t: torch.Tensor, name: str, c: int) -> int:
+    """Address of an fp32 [c] vector."""
+    if t.dtype is not torch.float32 or t.shape != (c,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous fp32 [{c}] CUDA tensor")
     return t.data_ptr()
 
 
 def _weight(t: torch.Tensor, name: str, shape, dtype) -> int:
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    """Address of a dense weight."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} CUDA tensor")
     return t.data_ptr()
 
 
 def _activation(name: str) -> int:
-    if name not in ACTIVATIONS:
+    code = ACTIVATIONS.get(name)
+    if code is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
-    return ACTIVATIONS[name]
+    return code
 
 
-def _matrix(x: torch.Tensor, name: str = "x"):
-    """(n, c) of a 2-D CUDA tensor."""
-    if not x.is_cuda or x.dim() != 2:
+def _matrix(t: torch.Tensor, name: str):
+    """The shape of a 2-D CUDA tensor."""
+    if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    return x.size(0), x.size(1)
+    return t.shape
 
 
-class _On:
-    """The stream a call runs on.  What the call allocates belongs to that stream, and what it
-    reads is kept from reuse until the stream is past the call."""
-
-    def __init__(self, stream: Optional[torch.cuda.Stream], *tensors):
-        self._ctx = None
-        if stream is None:
-            self.ptr = torch.cuda.current_stream().cuda_stream
-            return
-        self.ptr = stream.cuda_stream
-        if self.ptr != torch.cuda.current_stream().cuda_stream:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-            self._ctx = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self.ptr
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+def _on_stream(stream: torch.cuda.Stream, tensors, call):
+    """``call()`` on ``stream``: what it allocates belongs to that stream, and what it reads is kept
+    from reuse until the stream is past it."""
+    if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return call()
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
@@ -509,32 +507,40 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     Returns y, or with ``quantize`` (q, scale): e4m3 values and one fp32 scale per row, y = q * scale.
     With a ``residual`` the sum h follows as the last value, in x's dtype: (y, h) or (q, scale, h).
     ``sum_out`` takes h ([N, C], contiguous; may be ``residual`` or ``x``)."""
-    n, c = _matrix(x)
-    if x.dtype not in _DTYPES:
+    if stream is not None:
+        return _on_stream(stream, (x, weight, residual, sum_out),
+                          lambda: rms_norm(x, weight, residual, eps=eps, quantize=quantize, sum_out=sum_out))
+    shape = _matrix(x, "x")
+    n, c = shape
+    dtype = x.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise ValueError("x must be bf16 or fp32")
-    ldx = _rows(x, "x", n, c, x.dtype)
-    ldr = 0 if residual is None else _rows(residual, "residual", n, c, x.dtype)
-    w = _vector(weight, "weight", c)
-    if w is None:
+    if weight is None:
         raise ValueError("weight is required")
-    dt = _DTYPES[x.dtype]
-    if sum_out is not None and (sum_out.dtype != x.dtype or tuple(sum_out.shape) != (n, c) or not sum_out.is_cuda
-                                or not sum_out.is_contiguous()):
-        raise ValueError(f"sum_out must be a contiguous {x.dtype} [{n}, {c}] CUDA tensor")
-    with _On(stream, x, weight, residual, sum_out) as s:
-        h = sum_out
-        if h is None and residual is not None:
-            h = torch.empty((n, c), dtype=x.dtype, device=x.device)
-        out = torch.empty((n, c), dtype=_E4M3 if quantize else x.dtype, device=x.device)
-        scale = torch.empty((n,), dtype=torch.float32, device=x.device) if quantize else None
-        rc = library().spconv_rms_norm(x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, w, n, c,
-                                       dt, eps, None if h is None else h.data_ptr(), out.data_ptr(), 2 if quantize else dt,
-                                       None if scale is None else scale.data_ptr(), s)
-    _check(rc, "spconv_rms_norm")
-    res = (out, scale) if quantize else (out,)
+    dev = x.device
+    ldx, r, ldr = _rows(x, "x", shape, dtype), None, 0
+    w = _vector(weight, "weight", c)
+    h = sum_out
+    if h is not None:
+        _weight(h, "sum_out", shape, dtype)
     if residual is not None:
-        res += (h,)
-    return res if len(res) > 1 else out
+        r, ldr = residual.data_ptr(), _rows(residual, "residual", shape, dtype)
+        if h is None:
+            h = torch.empty(shape, dtype=dtype, device=dev)
+    if quantize:
+        out = torch.empty(shape, dtype=_E4M3, device=dev)
+        scale = torch.empty((n,), dtype=torch.float32, device=dev)
+    else:
+        out, scale = torch.empty(shape, dtype=dtype, device=dev), None
+    rc = _lib().spconv_rms_norm(x.data_ptr(), ldx, r, ldr, w, n, c, dt, eps, None if h is None else h.data_ptr(),
+                                out.data_ptr(), 2 if quantize else dt, None if scale is None else scale.data_ptr(),
+                                _raw_stream(dev.index))
+    if rc:
+        raise SpconvError(rc, "spconv_rms_norm")
+    if residual is None:
+        return (out, scale) if quantize else out
+    return (out, scale, h) if quantize else (out, h)
 
 
 def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, dres: Optional[torch.Tensor] = None, *,
@@ -542,47 +548,55 @@ def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, d
     """``spconv_rms_norm_backward``: (dx, dweight) of the norm of ``x`` (the sum ``rms_norm`` returned,
     where there was a residual), for the gradient ``dy`` of y and ``dres`` of the sum.  dx is the gradient
     of x and of the residual alike; dweight fp32 [C]."""
-    n, c = _matrix(x)
-    if x.dtype not in _DTYPES:
+    if stream is not None:
+        return _on_stream(stream, (dy, x, weight, dres), lambda: rms_norm_backward(dy, x, weight, dres, eps=eps))
+    shape = _matrix(x, "x")
+    n, c = shape
+    dtype = x.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise ValueError("x must be bf16 or fp32")
-    ldx = _rows(x, "x", n, c, x.dtype)
-    ldy = _rows(dy, "dy", n, c, x.dtype)
-    ldr = 0 if dres is None else _rows(dres, "dres", n, c, x.dtype)
-    w = _vector(weight, "weight", c)
-    if w is None:
+    if weight is None:
         raise ValueError("weight is required")
-    with _On(stream, dy, x, weight, dres) as s:
-        dx = torch.empty((n, c), dtype=x.dtype, device=x.device)
-        dw = torch.empty((c,), dtype=torch.float32, device=x.device)
-        rc = library().spconv_rms_norm_backward(dy.data_ptr(), ldy, x.data_ptr(), ldx, w,
-                                                None if dres is None else dres.data_ptr(), ldr, n, c, _DTYPES[x.dtype],
-                                                eps, dx.data_ptr(), dw.data_ptr(), s)
-    _check(rc, "spconv_rms_norm_backward")
+    ldx, ldy, r, ldr = _rows(x, "x", shape, dtype), _rows(dy, "dy", shape, dtype), None, 0
+    if dres is not None:
+        r, ldr = dres.data_ptr(), _rows(dres, "dres", shape, dtype)
+    w = _vector(weight, "weight", c)
+    dev = x.device
+    dx = torch.empty(shape, dtype=dtype, device=dev)
+    dw = torch.empty((c,), dtype=torch.float32, device=dev)
+    rc = _lib().spconv_rms_norm_backward(dy.data_ptr(), ldy, x.data_ptr(), ldx, w, r, ldr, n, c, dt, eps, dx.data_ptr(),
+                                         dw.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        raise SpconvError(rc, "spconv_rms_norm_backward")
     return dx, dw
 
 
-def _operands(x: torch.Tensor, names, weights, x_scale, scales):
-    """Checks x [N, C_in] against its weights, bf16 [C_in, C_out] or e4m3 [C_out, C_in] with scales.
+def _operands(x: torch.Tensor, w: torch.Tensor, name: str):
+    """Checks x [N, C_in] against a weight, bf16 [C_in, C_out] or e4m3 [C_out, C_in].
 
-    Returns (n, c_in, c_out, dtype code, row stride of x)."""
-    n, c_in = _matrix(x)
-    w = weights[0]
+    Returns (n, c_in, c_out, whether e4m3, row stride of x, shape of the weight)."""
+    shape = _matrix(x, "x")
+    n, c_in = shape
+    dtype = x.dtype
     if w.dim() != 2:
-        raise ValueError(f"{names[0]} must be 2-D")
-    if x.dtype == torch.bfloat16:
-        code, c_out = 0, w.size(1)
-        shape = (c_in, c_out)
-    elif x.dtype == _E4M3:
-        code, c_out = 2, w.size(0)
-        shape = (c_out, c_in)
+        raise ValueError(f"{name} must be 2-D")
+    if dtype is _BF16:
+        eight, c_out = False, w.shape[1]
+        wshape = (c_in, c_out)
+    elif dtype is _E4M3:
+        eight, c_out = True, w.shape[0]
+        wshape = (c_out, c_in)
     else:
         raise ValueError("x must be bf16 or float8_e4m3fn")
-    for name, t in zip(names, weights):
-        _weight(t, name, shape, x.dtype)
-    for t in (x_scale, *scales):
-        if (t is not None) != (code == 2):
-            raise ValueError("e4m3 operands need their scales, bf16 ones have none")
-    return n, c_in, c_out, code, _rows(x, "x", n, c_in, x.dtype)
+    _weight(w, name, wshape, dtype)
+    return n, c_in, c_out, eight, _rows(x, "x", shape, dtype), wshape
+
+
+def _scale(t: Optional[torch.Tensor], name: str, c: int, eight: bool) -> Optional[int]:
+    if (t is not None) != eight:
+        raise ValueError(f"{name}: e4m3 operands need their scales, bf16 ones have none")
+    return _vector(t, name, c) if eight else None
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor] = None, activation: str = "none",
@@ -594,17 +608,26 @@ def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor
     bf16: ``x`` [N, C_in], ``weight`` [C_in, C_out].  8 bits: ``x`` float8_e4m3fn with ``x_scale`` fp32 [N],
     ``weight`` float8_e4m3fn [C_out, C_in] with ``w_scale`` fp32 [C_out] (``quantize_weight``).  ``bias`` fp32
     [C_out], ``residual`` bf16 [N, C_out] (may be ``out``); rows of x, residual and out may be strided."""
-    n, c_in, c_out, code, ldx = _operands(x, ("weight",), (weight,), x_scale, (w_scale,))
-    act = _activation(activation)
-    xs, ws, b = _vector(x_scale, "x_scale", n), _vector(w_scale, "w_scale", c_out), _vector(bias, "bias", c_out)
-    ldr = 0 if residual is None else _rows(residual, "residual", n, c_out, torch.bfloat16)
-    with _On(stream, x, weight, bias, residual, out, x_scale, w_scale) as s:
-        if out is None:
-            out = torch.empty((n, c_out), dtype=torch.bfloat16, device=x.device)
-        rc = library().spconv_linear(x.data_ptr(), ldx, xs, weight.data_ptr(), ws, n, c_in, c_out, code, b, act,
-                                     None if residual is None else residual.data_ptr(), ldr, out.data_ptr(),
-                                     _rows(out, "out", n, c_out, torch.bfloat16), s)
-    _check(rc, "spconv_linear")
+    if stream is not None:
+        return _on_stream(stream, (x, weight, bias, residual, out, x_scale, w_scale),
+                          lambda: linear(x, weight, bias=bias, activation=activation, residual=residual, out=out,
+                                         x_scale=x_scale, w_scale=w_scale))
+    n, c_in, c_out, eight, ldx, _ = _operands(x, weight, "weight")
+    xs, ws = _scale(x_scale, "x_scale", n, eight), _scale(w_scale, "w_scale", c_out, eight)
+    b, r, ldr = None, None, 0
+    if bias is not None:
+        b = _vector(bias, "bias", c_out)
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _rows(residual, "residual", (n, c_out), _BF16)
+    dev = x.device
+    if out is None:
+        out, ldo = torch.empty((n, c_out), dtype=_BF16, device=dev), c_out
+    else:
+        ldo = _rows(out, "out", (n, c_out), _BF16)
+    rc = _lib().spconv_linear(x.data_ptr(), ldx, xs, weight.data_ptr(), ws, n, c_in, c_out, 2 if eight else 0, b,
+                              _activation(activation), r, ldr, out.data_ptr(), ldo, _raw_stream(dev.index))
+    if rc:
+        raise SpconvError(rc, "spconv_linear")
     return out
 
 
@@ -612,18 +635,23 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *, 
                     activation: str = "none", stream: Optional[torch.cuda.Stream] = None):
     """``spconv_linear_backward``: (dx, dweight, dbias) of act(x W + bias) for the gradient ``dy``; bf16,
     dbias fp32 (None without a bias).  The residual's gradient is ``dy`` itself."""
-    n, c_in, c_out, code, ldx = _operands(x, ("weight",), (weight,), None, (None,))
-    act = _activation(activation)
-    b = _vector(bias, "bias", c_out)
-    ldy = _rows(dy, "dy", n, c_out, torch.bfloat16)
-    with _On(stream, dy, x, weight, bias) as s:
-        dx = torch.empty((n, c_in), dtype=torch.bfloat16, device=x.device)
-        dw = torch.empty((c_in, c_out), dtype=torch.bfloat16, device=x.device)
-        db = None if bias is None else torch.empty((c_out,), dtype=torch.float32, device=x.device)
-        rc = library().spconv_linear_backward(dy.data_ptr(), ldy, x.data_ptr(), ldx, weight.data_ptr(), n, c_in, c_out,
-                                              code, b, act, dx.data_ptr(), dw.data_ptr(),
-                                              None if db is None else db.data_ptr(), s)
-    _check(rc, "spconv_linear_backward")
+    if stream is not None:
+        return _on_stream(stream, (dy, x, weight, bias),
+                          lambda: linear_backward(dy, x, weight, bias=bias, activation=activation))
+    n, c_in, c_out, eight, ldx, wshape = _operands(x, weight, "weight")
+    if eight:
+        raise ValueError("gradients are of bf16 operands")
+    ldy = _rows(dy, "dy", (n, c_out), _BF16)
+    dev = x.device
+    dx = torch.empty((n, c_in), dtype=_BF16, device=dev)
+    dw = torch.empty(wshape, dtype=_BF16, device=dev)
+    db = None if bias is None else torch.empty((c_out,), dtype=torch.float32, device=dev)
+    rc = _lib().spconv_linear_backward(dy.data_ptr(), ldy, x.data_ptr(), ldx, weight.data_ptr(), n, c_in, c_out, 0,
+                                       None if bias is None else _vector(bias, "bias", c_out), _activation(activation),
+                                       dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(),
+                                       _raw_stream(dev.index))
+    if rc:
+        raise SpconvError(rc, "spconv_linear_backward")
     return dx, dw, db
 
 
@@ -634,44 +662,59 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, acti
     """``spconv_gated_ffn``: act(x W_gate) * (x W_up), bf16 [N, C_hidden], in one kernel.
 
     Operands as for ``linear``: bf16 [C_in, C_hidden] weights, or e4m3 [C_hidden, C_in] with scales."""
-    n, c_in, c_h, code, ldx = _operands(x, ("w_gate", "w_up"), (w_gate, w_up), x_scale, (gate_scale, up_scale))
-    act = _activation(activation)
-    xs = _vector(x_scale, "x_scale", n)
-    gs, us = _vector(gate_scale, "gate_scale", c_h), _vector(up_scale, "up_scale", c_h)
-    with _On(stream, x, w_gate, w_up, out, x_scale, gate_scale, up_scale) as s:
-        if out is None:
-            out = torch.empty((n, c_h), dtype=torch.bfloat16, device=x.device)
-        rc = library().spconv_gated_ffn(x.data_ptr(), ldx, xs, w_gate.data_ptr(), gs, w_up.data_ptr(), us, n, c_in, c_h,
-                                        code, act, out.data_ptr(), _rows(out, "out", n, c_h, torch.bfloat16), s)
-    _check(rc, "spconv_gated_ffn")
+    if stream is not None:
+        return _on_stream(stream, (x, w_gate, w_up, out, x_scale, gate_scale, up_scale),
+                          lambda: gated_ffn(x, w_gate, w_up, activation=activation, out=out, x_scale=x_scale,
+                                            gate_scale=gate_scale, up_scale=up_scale))
+    n, c_in, c_h, eight, ldx, wshape = _operands(x, w_gate, "w_gate")
+    up = _weight(w_up, "w_up", wshape, x.dtype)
+    xs = _scale(x_scale, "x_scale", n, eight)
+    gs, us = _scale(gate_scale, "gate_scale", c_h, eight), _scale(up_scale, "up_scale", c_h, eight)
+    dev = x.device
+    if out is None:
+        out, ldo = torch.empty((n, c_h), dtype=_BF16, device=dev), c_h
+    else:
+        ldo = _rows(out, "out", (n, c_h), _BF16)
+    rc = _lib().spconv_gated_ffn(x.data_ptr(), ldx, xs, w_gate.data_ptr(), gs, up, us, n, c_in, c_h, 2 if eight else 0,
+                                 _activation(activation), out.data_ptr(), ldo, _raw_stream(dev.index))
+    if rc:
+        raise SpconvError(rc, "spconv_gated_ffn")
     return out
 
 
 def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *,
                        activation: str = "silu", stream: Optional[torch.cuda.Stream] = None):
     """``spconv_gated_ffn_backward``: (dx, dw_gate, dw_up) for the gradient ``dh`` of ``gated_ffn``; bf16."""
-    n, c_in, c_h, code, ldx = _operands(x, ("w_gate", "w_up"), (w_gate, w_up), None, (None, None))
-    act = _activation(activation)
-    ldh = _rows(dh, "dh", n, c_h, torch.bfloat16)
-    with _On(stream, dh, x, w_gate, w_up) as s:
-        dx = torch.empty((n, c_in), dtype=torch.bfloat16, device=x.device)
-        dwg, dwu = (torch.empty((c_in, c_h), dtype=torch.bfloat16, device=x.device) for _ in range(2))
-        rc = library().spconv_gated_ffn_backward(dh.data_ptr(), ldh, x.data_ptr(), ldx, w_gate.data_ptr(),
-                                                 w_up.data_ptr(), n, c_in, c_h, code, act, dx.data_ptr(),
-                                                 dwg.data_ptr(), dwu.data_ptr(), s)
-    _check(rc, "spconv_gated_ffn_backward")
+    if stream is not None:
+        return _on_stream(stream, (dh, x, w_gate, w_up),
+                          lambda: gated_ffn_backward(dh, x, w_gate, w_up, activation=activation))
+    n, c_in, c_h, eight, ldx, wshape = _operands(x, w_gate, "w_gate")
+    if eight:
+        raise ValueError("gradients are of bf16 operands")
+    up = _weight(w_up, "w_up", wshape, x.dtype)
+    ldh = _rows(dh, "dh", (n, c_h), _BF16)
+    dev = x.device
+    dx = torch.empty((n, c_in), dtype=_BF16, device=dev)
+    dwg, dwu = torch.empty(wshape, dtype=_BF16, device=dev), torch.empty(wshape, dtype=_BF16, device=dev)
+    rc = _lib().spconv_gated_ffn_backward(dh.data_ptr(), ldh, x.data_ptr(), ldx, w_gate.data_ptr(), up, n, c_in, c_h, 0,
+                                          _activation(activation), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(),
+                                          _raw_stream(dev.index))
+    if rc:
+        raise SpconvError(rc, "spconv_gated_ffn_backward")
     return dx, dwg, dwu
 
 
 def quantize_weight(weight: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None):
     """``spconv_quantize_weight``: bf16 [C_in, C_out] to (e4m3 [C_out, C_in], fp32 scale [C_out]), once per weight."""
+    if stream is not None:
+        return _on_stream(stream, (weight,), lambda: quantize_weight(weight))
     c_in, c_out = _matrix(weight, "weight")
-    _weight(weight, "weight", (c_in, c_out), torch.bfloat16)
-    with _On(stream, weight) as s:
-        q = torch.empty((c_out, c_in), dtype=_E4M3, device=weight.device)
-        scale = torch.empty((c_out,), dtype=torch.float32, device=weight.device)
-        rc = library().spconv_quantize_weight(weight.data_ptr(), c_in, c_out, q.data_ptr(), scale.data_ptr(), s)
-    _check(rc, "spconv_quantize_weight")
+    w = _weight(weight, "weight", (c_in, c_out), _BF16)
+    q = torch.empty((c_out, c_in), dtype=_E4M3, device=weight.device)
+    scale = torch.empty((c_out,), dtype=torch.float32, device=weight.device)
+    rc = _lib().spconv_quantize_weight(w, c_in, c_out, q.data_ptr(), scale.data_ptr(), _raw_stream(weight.device.index))
+    if rc:
+        raise SpconvError(rc, "spconv_quantize_weight")
     return q, scale
 
 
