@@ -7,6 +7,7 @@
 // Everything between the loads and the stores is fp32, with one rounding per
 // output.  The kernels are bound by HBM: a row is read once into registers,
 // reduced, and written; the next row's loads are in flight meanwhile.
+#include "ptx_sm100.cuh"
 #include "rows.cuh"
 
 namespace spconv {
@@ -30,10 +31,47 @@ struct alignas(16) Pack<float, 8> {
     float v[8];
 };
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void from_f(float v, float& o) { o = v; }
-__device__ __forceinline__ void from_f(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
+// To fp32 and back (one rounding); pairs of bf16 take one instruction each.
+template <int W>
+__device__ __forceinline__ void unpack(const Pack<float, W>& p, float (&f)[W]) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) f[j] = p.v[j];
+}
+template <int W>
+__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, W>& p, float (&f)[W]) {
+    if constexpr (W == 8) {
+        const uint4 q = reinterpret_cast<const uint4&>(p);
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = __uint_as_float(u[j] << 16);
+            f[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[j] = __bfloat162float(p.v[j]);
+    }
+}
+template <int W>
+__device__ __forceinline__ void pack(const float (&f)[W], Pack<float, W>& p) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) p.v[j] = f[j];
+}
+template <int W>
+__device__ __forceinline__ void pack(const float (&f)[W], Pack<__nv_bfloat16, W>& p) {
+    if constexpr (W == 8) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+            u[j] = reinterpret_cast<const uint32_t&>(v);
+        }
+        reinterpret_cast<uint4&>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) p.v[j] = __float2bfloat16_rn(f[j]);
+    }
+}
 
 template <int W>
 __device__ __forceinline__ void store_e4m3(uint8_t* dst, const float* v) {
@@ -94,15 +132,6 @@ __device__ __forceinline__ V block_reduce(V v, V* sh, int turn) {
     return lanes_reduce<32>(r);
 }
 
-// The scale of a row whose largest |y| is amax, and the factors with
-// q = (y * pre) * inv.  448 / amax overflows for amax below 2^-119, so tiny
-// rows are first brought up by 2^100.  A row of zeros has scale 0, q 0.
-__device__ __forceinline__ float row_scale_of(float amax, float* pre, float* inv) {
-    *pre = amax < 0x1p-100f ? 0x1p100f : 1.0f;
-    *inv = amax == 0.0f ? 0.0f : kE4m3Max / (amax * *pre);
-    return amax / kE4m3Max;
-}
-
 // ---- forward ------------------------------------------------------------------
 // The VPT vectors of W elements of one row that one of its TPR threads handles:
 // elements (v TPR + t) W ..
@@ -127,19 +156,23 @@ struct RowPart {
 // h = x + residual, this thread's share of the row's statistics.
 template <typename T, int W, int VPT, bool EIGHT>
 __device__ __forceinline__ SumMax row_stats(const NormArgs& a, const RowPart<T, W, VPT>& p, const Pack<float, W> (&w)[VPT],
-                                            float (&h)[VPT * W], int t, int tpr) {
+                                            float (&h)[VPT][W], int t, int tpr) {
     SumMax st{0.0f, 0u};
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         if ((v * tpr + t) * W >= a.c) continue;
+        unpack<W>(p.x[v], h[v]);
+        if (a.residual) {
+            float r[W];
+            unpack<W>(p.r[v], r);
+#pragma unroll
+            for (int j = 0; j < W; ++j) h[v][j] += r[j];
+        }
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            float f = to_f(p.x[v].v[j]);
-            if (a.residual) f += to_f(p.r[v].v[j]);
-            h[v * W + j] = f;
-            st.s = fmaf(f, f, st.s);
+            st.s = fmaf(h[v][j], h[v][j], st.s);
             if (EIGHT) {
-                const uint32_t b = __float_as_uint(fabsf(f * w[v].v[j]));
+                const uint32_t b = __float_as_uint(fabsf(h[v][j] * w[v].v[j]));
                 st.m = b > st.m ? b : st.m;
             }
         }
@@ -147,17 +180,22 @@ __device__ __forceinline__ SumMax row_stats(const NormArgs& a, const RowPart<T, 
     return st;
 }
 
-// Writes the row.  y = (h w) r: r is one positive factor, so max |y| is
-// (max |h w|) r, rounding included, and the two reductions are one.
+// Writes the row.  y = (h w) r, and r is one positive factor: max |y| is
+// (max |h w|) r, so the two reductions are one, and y / scale is
+// (h w) 448 / max |h w| without r.  That factor overflows where the maximum is
+// below 2^-119: such rows are first brought up by 2^100.  A row of zeros has
+// scale 0 and q 0.
 template <typename T, int W, int VPT, bool EIGHT>
 __device__ __forceinline__ void row_write(const NormArgs& a, int64_t row, SumMax st, const Pack<float, W> (&w)[VPT],
-                                          const float (&h)[VPT * W], int t, int tpr) {
+                                          const float (&h)[VPT][W], int t, int tpr) {
     using P = Pack<T, W>;
     const float r = rsqrtf(st.s / static_cast<float>(a.c) + a.eps);
-    float pre = 1.0f, inv = 1.0f;
+    float factor = r, pre = 1.0f;
     if (EIGHT) {
-        const float scale = row_scale_of(__uint_as_float(st.m) * r, &pre, &inv);
-        if (t == 0) a.scale[row] = scale;
+        const float amax = __uint_as_float(st.m);
+        if (t == 0) a.scale[row] = amax * r / kE4m3Max;
+        pre = amax < 0x1p-100f ? 0x1p100f : 1.0f;
+        factor = amax == 0.0f ? 0.0f : kE4m3Max / (amax * pre);
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -165,21 +203,22 @@ __device__ __forceinline__ void row_write(const NormArgs& a, int64_t row, SumMax
         if (e >= a.c) continue;
         P o;
         if (a.sum) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) from_f(h[v * W + j], o.v[j]);
+            pack<W>(h[v], o);
             *reinterpret_cast<P*>(static_cast<T*>(a.sum) + row * a.c + e) = o;
         }
         float y[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            y[j] = h[v * W + j] * w[v].v[j] * r;
-            if (EIGHT) y[j] = y[j] * pre * inv;
+        for (int j = 0; j < W; ++j) y[j] = h[v][j] * w[v].v[j];
+        if (EIGHT && pre != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) y[j] *= pre;
         }
+#pragma unroll
+        for (int j = 0; j < W; ++j) y[j] *= factor;
         if (EIGHT) {
             store_e4m3<W>(static_cast<uint8_t*>(a.out) + row * a.c + e, y);
         } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) from_f(y[j], o.v[j]);
+            pack<W>(y, o);
             *reinterpret_cast<P*>(static_cast<T*>(a.out) + row * a.c + e) = o;
         }
     }
@@ -203,7 +242,7 @@ __global__ void __launch_bounds__(kBlock) k_rms_norm(const NormArgs a) {
     const bool live = row < a.n;   // (lanes of absent rows still take part in the shuffles)
     RowPart<T, W, VPT> p;
     Pack<float, W> w[VPT];
-    float h[VPT * W];
+    float h[VPT][W];
     SumMax st{0.0f, 0u};
     load_weight<W, VPT>(a.weight, a.c, w, t, TPR);
     pdl_wait();
@@ -224,7 +263,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_block(const NormArgs a) {
     const int t = threadIdx.x, tpr = blockDim.x;
     RowPart<T, W, VPT> p, next;
     Pack<float, W> w[VPT];
-    float h[VPT * W];
+    float h[VPT][W];
     load_weight<W, VPT>(a.weight, a.c, w, t, tpr);
     pdl_wait();
     pdl_trigger();
@@ -254,7 +293,7 @@ __global__ void __launch_bounds__(kLongThreads) k_rms_norm_long(const NormArgs a
         SumMax st{0.0f, 0u};
         RowPart<T, W, 1> p;
         Pack<float, W> w[1];
-        float h[W];
+        float h[1][W];
 #pragma unroll 4
         for (int t = threadIdx.x; t * W < a.c; t += step) {
             p.load(a, row, t, 0);
@@ -306,11 +345,13 @@ __device__ __forceinline__ Sum2 grad_stats(const NormGradArgs& a, const GradPart
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         if ((v * tpr + t) * W >= a.c) continue;
+        float h[W], d[W];
+        unpack<W>(p.x[v], h);
+        unpack<W>(p.d[v], d);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            const float h = to_f(p.x[v].v[j]);
-            st.s = fmaf(h, h, st.s);
-            st.t = fmaf(to_f(p.d[v].v[j]) * w[v].v[j], h, st.t);
+            st.s = fmaf(h[j], h[j], st.s);
+            st.t = fmaf(d[j] * w[v].v[j], h[j], st.t);
         }
     }
     return st;
@@ -325,20 +366,27 @@ __device__ __forceinline__ Sum2 grad_factors(Sum2 st, int32_t c, float eps) {
 
 template <typename T, int W, int VPT>
 __device__ __forceinline__ void grad_write(const NormGradArgs& a, int64_t row, Sum2 f, const GradPart<T, W, VPT>& p,
-                                           const Pack<float, W> (&w)[VPT], float (&dw)[VPT * W], int t, int tpr) {
+                                           const Pack<float, W> (&w)[VPT], float (&dw)[VPT][W], int t, int tpr) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         const int e = (v * tpr + t) * W;
         if (e >= a.c) continue;
-        Pack<T, W> o;
+        float h[W], d[W], dx[W];
+        unpack<W>(p.x[v], h);
+        unpack<W>(p.d[v], d);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            const float h = to_f(p.x[v].v[j]), d = to_f(p.d[v].v[j]);
-            float dx = fmaf(d * w[v].v[j], f.s, -h * f.t);
-            if (a.dres) dx += to_f(p.r[v].v[j]);
-            from_f(dx, o.v[j]);
-            dw[v * W + j] = fmaf(d, h * f.s, dw[v * W + j]);
+            dx[j] = fmaf(d[j] * w[v].v[j], f.s, -h[j] * f.t);
+            dw[v][j] = fmaf(d[j], h[j] * f.s, dw[v][j]);
         }
+        if (a.dres) {
+            float r[W];
+            unpack<W>(p.r[v], r);
+#pragma unroll
+            for (int j = 0; j < W; ++j) dx[j] += r[j];
+        }
+        Pack<T, W> o;
+        pack<W>(dx, o);
         *reinterpret_cast<Pack<T, W>*>(static_cast<T*>(a.dx) + row * a.c + e) = o;
     }
 }
@@ -351,7 +399,7 @@ __global__ void __launch_bounds__(kBlock) k_rms_norm_grad(const NormGradArgs a, 
     const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
     Pack<float, W> w[VPT];
-    float dw[VPT * W] = {};
+    float dw[VPT][W] = {};
     GradPart<T, W, VPT> p, next;
     load_weight<W, VPT>(a.weight, a.c, w, t, TPR);
     pdl_wait();
@@ -371,7 +419,7 @@ __global__ void __launch_bounds__(kBlock) k_rms_norm_grad(const NormGradArgs a, 
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
-        for (int j = 0; j < W; ++j) sh_dw[grp * kCols + (v * TPR + t) * W + j] = dw[v * W + j];
+        for (int j = 0; j < W; ++j) sh_dw[grp * kCols + (v * TPR + t) * W + j] = dw[v][j];
     __syncthreads();
     for (int e = threadIdx.x; e < a.c; e += kBlock) {
         float s = 0.0f;
@@ -387,7 +435,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_grad_block(const NormGradArgs 
     __shared__ Sum2 sh[64];
     const int t = threadIdx.x, tpr = blockDim.x;
     Pack<float, W> w[VPT];
-    float dw[VPT * W] = {};
+    float dw[VPT][W] = {};
     GradPart<T, W, VPT> p, next;
     load_weight<W, VPT>(a.weight, a.c, w, t, tpr);
     pdl_wait();
@@ -407,7 +455,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_grad_block(const NormGradArgs 
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             const int e = (v * tpr + t) * W + j;
-            if (e < a.c) part[static_cast<int64_t>(blockIdx.x) * a.c + e] = dw[v * W + j];
+            if (e < a.c) part[static_cast<int64_t>(blockIdx.x) * a.c + e] = dw[v][j];
         }
 }
 
@@ -441,7 +489,7 @@ __global__ void __launch_bounds__(kBlock) k_rms_norm_grad_columns(const NormGrad
     if (t * W >= a.c) return;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows, r1 = r0 + rows < a.n ? r0 + rows : a.n;
     Pack<float, W> w[1];
-    float dw[W] = {};
+    float dw[1][W] = {};
     load_weight<W, 1>(a.weight, a.c, w, t, 0);
 #pragma unroll 2
     for (int64_t row = r0; row < r1; ++row) {
@@ -450,7 +498,305 @@ __global__ void __launch_bounds__(kBlock) k_rms_norm_grad_columns(const NormGrad
         grad_write<T, W, 1>(a, row, factors[row], p, w, dw, t, 0);
     }
 #pragma unroll
-    for (int j = 0; j < W; ++j) part[static_cast<int64_t>(blockIdx.y) * a.c + t * W + j] = dw[j];
+    for (int j = 0; j < W; ++j) part[static_cast<int64_t>(blockIdx.y) * a.c + t * W + j] = dw[0][j];
+}
+
+// ---- rows through shared memory -------------------------------------------------
+// A load in flight costs a thread its destination registers: threads x 16 bytes
+// x inputs is what an SM keeps on its way, and HBM wants some 60 KB per SM at
+// its loaded latency.  Here bulk asynchronous copies bring stages of rows (one
+// copy per input where the rows are dense) into a ring and the threads compute
+// from it, so the bytes in flight are the ring's size.
+constexpr int kMaxStages = 8;
+
+struct Ring {
+    int32_t stages, rows;       // of the ring; of a stage
+    uint32_t bytes;             // of one input in a stage (a multiple of 16)
+    int32_t* status;
+};
+
+// Consumers and producer of a ring of IN inputs.
+template <typename T, int IN>
+struct RingState {
+    uint8_t* base;
+    uint64_t *full, *empty;
+    volatile int* abort_flag;
+
+    // all threads; ends with a barrier
+    __device__ __forceinline__ void init(uint8_t* smem, const Ring& g, int consumer_warps) {
+        base = smem;
+        full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(g.stages) * IN * g.bytes);
+        empty = full + kMaxStages;
+        abort_flag = reinterpret_cast<volatile int*>(empty + kMaxStages);
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < g.stages; ++s) {
+                ptx::mbar_init(&full[s], 1);
+                ptx::mbar_init(&empty[s], consumer_warps);
+            }
+            *abort_flag = 0;
+            ptx::fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ const T* rows(const Ring& g, int s, int in) const {
+        return reinterpret_cast<const T*>(base + (static_cast<size_t>(s) * IN + in) * g.bytes);
+    }
+    __device__ __forceinline__ void fail(const Ring& g) {
+        atomicOr(g.status, kStatusTimeout);
+        *abort_flag = 1;
+    }
+    // Starts fill number k, tile `tile`, by `lanes` lanes of one warp (1: the calling thread).
+    __device__ __forceinline__ void fill(const Ring& g, int64_t k, int64_t tile, int64_t n, int32_t c, const T* const (&src)[IN],
+                                         const int64_t (&ld)[IN], int lane, int lanes) const {
+        const int s = static_cast<int>(k % g.stages);
+        const uint32_t row_bytes = static_cast<uint32_t>(c) * sizeof(T);
+        const int64_t r0 = tile * g.rows;
+        const int32_t rows_here = static_cast<int32_t>(n - r0 < g.rows ? n - r0 : g.rows);
+        int inputs = 0;
+#pragma unroll
+        for (int i = 0; i < IN; ++i) inputs += src[i] != nullptr;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], inputs * rows_here * row_bytes);
+        if (lanes > 1) __syncwarp();
+#pragma unroll
+        for (int i = 0; i < IN; ++i) {
+            if (!src[i]) continue;
+            const uint32_t dst = ptx::smem_u32(rows(g, s, i));
+            if (ld[i] == c) {
+                if (lane == 0) ptx::bulk_copy_g2s(dst, src[i] + r0 * ld[i], rows_here * row_bytes, &full[s]);
+            } else {
+                for (int r = lane; r < rows_here; r += lanes)
+                    ptx::bulk_copy_g2s(dst + r * row_bytes, src[i] + (r0 + r) * ld[i], row_bytes, &full[s]);
+            }
+        }
+    }
+    // After an abort: the copies of the fills before number k land before the block exits.
+    __device__ __forceinline__ void drain(const Ring& g, int64_t k) const {
+        for (int64_t j = k > g.stages ? k - g.stages : 0; j < k; ++j)
+            ptx::mbar_wait(&full[j % g.stages], static_cast<uint32_t>(j / g.stages) & 1, nullptr);
+    }
+};
+
+// Keeps the shared-memory loads of one vector behind the work on the one
+// before: all of a row's loaded at once would cost the registers that hold dw.
+__device__ __forceinline__ void apart() { asm volatile("" ::: "memory"); }
+
+// Rows of 513 elements and more: a row per block and stage, so a block needs
+// 1/32 of the row's elements as threads and many blocks share an SM (the
+// barriers of one fall into the work of others).  There is no copying warp:
+// when the block meets to reduce row k, every thread is done with row k - 1,
+// and thread 0 refills that row's stage.
+template <typename T, bool EIGHT>
+__global__ void __launch_bounds__(512, 1) k_rms_norm_ring(const NormArgs a, const Ring g) {
+    constexpr int VPT = 4;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ SumMax sh[64];
+    RingState<T, 2> ring;
+    ring.init(smem, g, 1);
+    const int t = threadIdx.x, threads = blockDim.x;
+    Pack<float, 8> w[VPT];
+    load_weight<8, VPT>(a.weight, a.c, w, t, threads);
+    const T* const src[2] = {static_cast<const T*>(a.x), static_cast<const T*>(a.residual)};
+    const int64_t ld[2] = {a.ldx, a.ldr};
+    pdl_wait();
+    pdl_trigger();
+    int64_t filled = 0;   // (thread 0)
+    if (t == 0)
+        for (int64_t row = blockIdx.x; row < a.n && filled < g.stages; row += gridDim.x, ++filled)
+            ring.fill(g, filled, row, a.n, a.c, src, ld, 0, 1);
+    bool ok = true;
+    int k = 0;
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, ++k) {
+        const int s = k % g.stages;
+        // (a thread that gave up still meets the others at the barrier)
+        if (!ptx::mbar_wait(&ring.full[s], static_cast<uint32_t>(k / g.stages) & 1, ring.abort_flag)) {
+            ring.fail(g);
+            ok = false;
+        }
+        NormArgs b = a;   // the stage's row in place of the global one
+        b.x = ring.rows(g, s, 0);
+        b.residual = a.residual ? ring.rows(g, s, 1) : nullptr;
+        RowPart<T, 8, 1> p;
+        Pack<float, 8> wv[1];
+        float h[1][8];
+        SumMax st{0.0f, 0u};
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            p.load(b, 0, v * threads + t, 0);
+            wv[0] = w[v];
+            st = join(st, row_stats<T, 8, 1, EIGHT>(a, p, wv, h, v * threads + t, 0));
+        }
+        st = block_reduce(st, sh, k);
+        if (*ring.abort_flag) break;
+        const int64_t next = row + (g.stages - 1) * static_cast<int64_t>(gridDim.x);
+        if (t == 0 && k > 0 && next < a.n) ring.fill(g, filled++, next, a.n, a.c, src, ld, 0, 1);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            apart();
+            p.load(b, 0, v * threads + t, 0);
+            wv[0] = w[v];
+            row_stats<T, 8, 1, false>(a, p, wv, h, v * threads + t, 0);
+            row_write<T, 8, 1, EIGHT>(a, row, st, wv, h, v * threads + t, 0);
+        }
+    }
+    if (t == 0 && !ok) ring.drain(g, filled);
+}
+
+// The backward pass of such rows.  The row's vectors are taken from shared
+// memory again for the second pass, and the weight's from L1 or L2: the
+// registers hold the running dw.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(512, 1) k_rms_norm_grad_ring(const NormGradArgs a, const Ring g, float* part) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Sum2 sh[64];
+    RingState<T, 3> ring;
+    ring.init(smem, g, 1);
+    const int t = threadIdx.x, threads = blockDim.x;
+    float dw[VPT][1][8] = {};
+    const T* const src[3] = {static_cast<const T*>(a.x), static_cast<const T*>(a.dy), static_cast<const T*>(a.dres)};
+    const int64_t ld[3] = {a.ldx, a.ldy, a.ldr};
+    pdl_wait();
+    pdl_trigger();
+    int64_t filled = 0;
+    if (t == 0)
+        for (int64_t row = blockIdx.x; row < a.n && filled < g.stages; row += gridDim.x, ++filled)
+            ring.fill(g, filled, row, a.n, a.c, src, ld, 0, 1);
+    bool ok = true;
+    int k = 0;
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, ++k) {
+        const int s = k % g.stages;
+        if (!ptx::mbar_wait(&ring.full[s], static_cast<uint32_t>(k / g.stages) & 1, ring.abort_flag)) {
+            ring.fail(g);
+            ok = false;
+        }
+        NormGradArgs b = a;
+        b.x = ring.rows(g, s, 0);
+        b.dy = ring.rows(g, s, 1);
+        b.dres = nullptr;
+        GradPart<T, 8, 1> p;
+        Pack<float, 8> wv[1];
+        Sum2 st{0.0f, 0.0f};
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            apart();
+            p.load(b, 0, v * threads + t, 0);
+            load_weight<8, 1>(a.weight, a.c, wv, v * threads + t, 0);
+            st = join(st, grad_stats<T, 8, 1>(a, p, wv, v * threads + t, 0));
+        }
+        st = block_reduce(st, sh, k);
+        if (*ring.abort_flag) break;
+        const int64_t next = row + (g.stages - 1) * static_cast<int64_t>(gridDim.x);
+        if (t == 0 && k > 0 && next < a.n) ring.fill(g, filled++, next, a.n, a.c, src, ld, 0, 1);
+        const Sum2 f = grad_factors(st, a.c, a.eps);
+        b.dres = a.dres ? ring.rows(g, s, 2) : nullptr;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            apart();
+            p.load(b, 0, v * threads + t, 0);
+            load_weight<8, 1>(a.weight, a.c, wv, v * threads + t, 0);
+            grad_write<T, 8, 1>(a, row, f, p, wv, dw[v], v * threads + t, 0);
+        }
+    }
+    if (t == 0 && !ok) ring.drain(g, filled);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = (v * threads + t) * 8 + j;
+            if (e < a.c) part[static_cast<int64_t>(blockIdx.x) * a.c + e] = dw[v][0][j];
+        }
+}
+
+// Shorter rows, backward: a row per TPR lanes, one warp of the block copies
+// stages of many rows.
+template <typename T, int TPR, int VPT>
+__global__ void __launch_bounds__(kBlock + 32, VPT > 1 && sizeof(T) == 4 ? 1 : 2) k_rms_norm_grad_lanes(const NormGradArgs a, const Ring g, float* part) {
+    constexpr int kGroups = kBlock / TPR, kCols = TPR * VPT * 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    RingState<T, 3> ring;
+    ring.init(smem, g, kBlock / 32);
+    const bool consumer = threadIdx.x < kBlock;
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    Pack<float, 8> w[VPT];
+    float dw[VPT][1][8] = {};
+    if (consumer) load_weight<8, VPT>(a.weight, a.c, w, t, TPR);
+    const int64_t tiles = (a.n + g.rows - 1) / g.rows;
+    pdl_wait();
+    pdl_trigger();
+    int64_t k = 0;
+    if (!consumer) {
+        const T* const src[3] = {static_cast<const T*>(a.x), static_cast<const T*>(a.dy), static_cast<const T*>(a.dres)};
+        const int64_t ld[3] = {a.ldx, a.ldy, a.ldr};
+        const int lane = threadIdx.x & 31;
+        bool ok = true;
+        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++k) {
+            if (k >= g.stages) {
+                ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ring.empty[k % g.stages],
+                                                            static_cast<uint32_t>(k / g.stages - 1) & 1, ring.abort_flag));
+                if (!ok) {
+                    if (lane == 0) ring.fail(g);
+                    break;
+                }
+            }
+            ring.fill(g, k, tile, a.n, a.c, src, ld, lane, 32);
+        }
+        if (!ok) ring.drain(g, k);
+    } else {
+        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++k) {
+            const int s = static_cast<int>(k % g.stages);
+            if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ring.full[s], static_cast<uint32_t>(k / g.stages) & 1, ring.abort_flag))) {
+                if ((threadIdx.x & 31) == 0) ring.fail(g);
+                break;
+            }
+            NormGradArgs b = a;   // the stage's rows in place of global ones
+            b.x = ring.rows(g, s, 0);
+            b.dy = ring.rows(g, s, 1);
+            b.dres = a.dres ? ring.rows(g, s, 2) : nullptr;
+            b.ldx = b.ldy = b.ldr = a.c;
+            for (int r = grp; r < g.rows; r += kGroups) {
+                const int64_t row = tile * g.rows + r;
+                const bool live = row < a.n;
+                GradPart<T, 8, 1> p;
+                Pack<float, 8> wv[1];
+                Sum2 st{0.0f, 0.0f};
+                if (live) {
+#pragma unroll
+                    for (int v = 0; v < VPT; ++v) {
+                        p.load(b, r, v * TPR + t, 0);
+                        wv[0] = w[v];
+                        st = join(st, grad_stats<T, 8, 1>(a, p, wv, v * TPR + t, 0));
+                    }
+                }
+                st = lanes_reduce<TPR>(st);
+                if (live) {
+                    const Sum2 f = grad_factors(st, a.c, a.eps);
+#pragma unroll
+                    for (int v = 0; v < VPT; ++v) {
+                        apart();
+                        p.load(b, r, v * TPR + t, 0);
+                        wv[0] = w[v];
+                        grad_write<T, 8, 1>(a, row, f, p, wv, dw[v], v * TPR + t, 0);
+                    }
+                }
+            }
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&ring.empty[s]);
+        }
+    }
+    // the block's rows are added through the ring's memory, free by now
+    float* sh_dw = reinterpret_cast<float*>(smem);   // [kGroups][kCols]
+    __syncthreads();
+    if (consumer) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sh_dw[grp * kCols + (v * TPR + t) * 8 + j] = dw[v][0][j];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.c; e += blockDim.x) {
+        float sum = 0.0f;
+        for (int q = 0; q < kGroups; ++q) sum += sh_dw[q * kCols + e];
+        part[static_cast<int64_t>(blockIdx.x) * a.c + e] = sum;
+    }
 }
 
 bool vec_ok(const void* p, int64_t ld, size_t elem) {
@@ -475,6 +821,35 @@ int launch(void (*kernel)(K...), int64_t blocks, int threads, size_t smem, cudaS
 
 constexpr int64_t kSms = 152;
 
+// The ring of a kernel with `in` inputs and `rows` rows a stage.  *per_sm
+// blocks share an SM's shared memory: the most asked for, or fewer where that
+// leaves less than two stages.
+int make_ring(Ring* g, size_t* smem, int32_t c, size_t es, int in, int64_t rows, int* per_sm) {
+    g->rows = static_cast<int32_t>(rows);
+    g->bytes = static_cast<uint32_t>(round_up(static_cast<size_t>(rows) * c * es, 128));
+    for (;; --*per_sm) {
+        if (*per_sm < 1) return SPCONV_ERR_UNSUPPORTED;
+        g->stages = static_cast<int32_t>((static_cast<size_t>(220 * 1024) / *per_sm - 2048) / (in * g->bytes));
+        if (g->stages >= 2) break;
+    }
+    if (g->stages > kMaxStages) g->stages = kMaxStages;
+    *smem = static_cast<size_t>(g->stages) * in * g->bytes + 2 * kMaxStages * 8 + 16;
+    return rows_status_word(&g->status);
+}
+
+template <auto KERNEL, typename... A>
+int launch_ring(int64_t blocks, int threads, size_t smem, cudaStream_t s, A... args) {
+    static bool set[kMaxDevices] = {};
+    int dev = 0;
+    SPCONV_CHECK_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= kMaxDevices) return SPCONV_ERR_UNSUPPORTED;
+    if (!set[dev]) {
+        SPCONV_CHECK_CUDA(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024));
+        set[dev] = true;
+    }
+    return launch(KERNEL, blocks, threads, smem, s, args...);
+}
+
 // Threads of a block that holds a row of c elements, `per` of them each.
 int block_threads(int32_t c, int per) { return static_cast<int>(round_up(static_cast<size_t>(ceil_div(c, per)), 32)); }
 
@@ -498,25 +873,31 @@ int with_lanes(int32_t c, F&& f) {
     return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
 }
 
-// How long a row a thread's registers allow to hold: vectors of 8 take fewer
-// than single elements, the forward pass fewer than the backward one (which
-// also keeps dy, dres and the running dw), bf16 fewer than fp32.
 template <typename T, int W, bool EIGHT>
 int forward_t(const NormArgs& a, cudaStream_t s) {
     constexpr int S = 8 / W;   // W = 1 holds the same elements in eight times the loads
     constexpr bool kVec = W == 8;
+    if constexpr (kVec) {
+        if (a.c > 1024 && a.c <= (sizeof(T) == 2 ? 16384 : 8192)) {
+            Ring g;
+            size_t smem;
+            const int threads = block_threads(a.c, 32);
+            int per_sm = 512 / threads;
+            SPCONV_CHECK(make_ring(&g, &smem, a.c, sizeof(T), 2, 1, &per_sm));
+            const int64_t most = kSms * per_sm;
+            return launch_ring<k_rms_norm_ring<T, EIGHT>>(a.n < most ? a.n : most, threads, smem, s, a, g);
+        }
+    }
     if (a.c <= (kVec ? 1024 : 512))
         return with_lanes<kVec>(a.c, [&](auto tpr, auto vpt) {
             return launch(k_rms_norm<T, W, tpr, vpt * S, EIGHT>, ceil_div(a.n, kBlock / tpr), kBlock, 0, s, a);
         });
-    auto persistent = [&](auto kernel, int per) {
-        const int threads = block_threads(a.c, per);
-        const int64_t most = kSms * (1024 / threads);
-        return launch(kernel, a.n < most ? a.n : most, threads, 0, s, a);
-    };
-    if (a.c <= 4096) return persistent(k_rms_norm_block<T, W, S, EIGHT>, 8);
-    if constexpr (kVec) {
-        if (a.c <= 8192) return persistent(k_rms_norm_block<T, W, 2, EIGHT>, 16);
+    if constexpr (!kVec) {
+        if (a.c <= 4096) {
+            const int threads = block_threads(a.c, 8);
+            const int64_t most = kSms * (1024 / threads);
+            return launch(k_rms_norm_block<T, W, S, EIGHT>, a.n < most ? a.n : most, threads, 0, s, a);
+        }
     }
     const int64_t most = kSms * 4;
     return launch(k_rms_norm_long<T, W, EIGHT>, a.n < most ? a.n : most, kLongThreads, 0, s, a);
@@ -524,7 +905,6 @@ int forward_t(const NormArgs& a, cudaStream_t s) {
 
 template <typename T, int W>
 int backward_t(const NormGradArgs& a, cudaStream_t s) {
-    constexpr int S = 8 / W;
     constexpr bool kVec = W == 8;
     // blocks: partial sums of dw, one row each
     auto with_part = [&](int64_t blocks, auto&& run) -> int {
@@ -533,24 +913,47 @@ int backward_t(const NormGradArgs& a, cudaStream_t s) {
         SPCONV_CHECK(run(part.as<float>()));
         return sum_partials(part.as<float>(), blocks, a.c, a.dweight, s);
     };
-    if (a.c <= 512)
-        return with_lanes<false>(a.c, [&](auto tpr, auto vpt) {
-            const int64_t want = ceil_div(a.n, kBlock / tpr), most = kSms * 4;
-            const int64_t blocks = want < most ? want : most;
-            return with_part(blocks, [&](float* part) {
-                return launch(k_rms_norm_grad<T, W, tpr, vpt * S>, blocks, kBlock, size_t(kBlock) * vpt * 8 * 4, s, a, part);
+    if constexpr (kVec) {
+        Ring g;
+        size_t smem;
+        if (a.c <= 512)
+            return with_lanes<false>(a.c, [&](auto tpr, auto vpt) {
+                // stages of 8 KB per input at least, so that barriers are few
+                const int64_t unit = kBlock / tpr, row = static_cast<int64_t>(a.c) * sizeof(T);
+                int per_sm = 2;
+                SPCONV_CHECK(make_ring(&g, &smem, a.c, sizeof(T), 3, unit * ceil_div(8192, unit * row), &per_sm));
+                const int64_t tiles = ceil_div(a.n, g.rows), most = kSms * per_sm, blocks = tiles < most ? tiles : most;
+                return with_part(blocks, [&](float* part) {
+                    return launch_ring<k_rms_norm_grad_lanes<T, tpr, vpt>>(blocks, kBlock + 32, smem, s, a, g, part);
+                });
             });
-        });
-    auto persistent = [&](auto kernel, int per) {
-        const int threads = block_threads(a.c, per);
-        const int64_t most = kSms * (1024 / threads);
-        const int64_t blocks = a.n < most ? a.n : most;
-        return with_part(blocks, [&](float* part) { return launch(kernel, blocks, threads, 0, s, a, part); });
-    };
-    constexpr int kPer = kVec ? 8 : 4;
-    if (a.c <= 512 * kPer) return persistent(k_rms_norm_grad_block<T, W, kPer / W>, kPer);
-    if constexpr (kVec && sizeof(T) == 2) {
-        if (a.c <= 8192) return persistent(k_rms_norm_grad_block<T, W, 2>, 16);
+        if (a.c <= (sizeof(T) == 2 ? 8192 : 4096)) {
+            constexpr int kVpt = sizeof(T) == 2 ? 4 : 2;
+            const int threads = block_threads(a.c, 8 * kVpt);
+            int per_sm = 512 / threads;
+            SPCONV_CHECK(make_ring(&g, &smem, a.c, sizeof(T), 3, 1, &per_sm));
+            const int64_t most = kSms * per_sm, blocks = a.n < most ? a.n : most;
+            return with_part(blocks, [&](float* part) {
+                return launch_ring<k_rms_norm_grad_ring<T, kVpt>>(blocks, threads, smem, s, a, g, part);
+            });
+        }
+    } else {
+        if (a.c <= 512)
+            return with_lanes<false>(a.c, [&](auto tpr, auto vpt) {
+                const int64_t want = ceil_div(a.n, kBlock / tpr), most = kSms * 4;
+                const int64_t blocks = want < most ? want : most;
+                return with_part(blocks, [&](float* part) {
+                    return launch(k_rms_norm_grad<T, W, tpr, vpt * 8>, blocks, kBlock, size_t(kBlock) * vpt * 8 * 4, s, a, part);
+                });
+            });
+        if (a.c <= 2048) {
+            const int threads = block_threads(a.c, 4);
+            const int64_t most = kSms * (1024 / threads);
+            const int64_t blocks = a.n < most ? a.n : most;
+            return with_part(blocks, [&](float* part) {
+                return launch(k_rms_norm_grad_block<T, W, 4>, blocks, threads, 0, s, a, part);
+            });
+        }
     }
     Scratch factors(static_cast<size_t>(a.n) * sizeof(Sum2), s);
     if (factors.failed()) return SPCONV_ERR_OOM;
