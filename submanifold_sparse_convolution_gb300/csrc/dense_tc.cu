@@ -102,6 +102,25 @@ __device__ __forceinline__ float column_sum32(uint32_t (&v)[32], int lane) {
     return __uint_as_float(v[0]);
 }
 
+// v[n0 .. n0 + CW) of a column vector of n values (the same for all lanes), 0 past its end.
+template <int CW>
+__device__ __forceinline__ void load_columns(float (&f)[CW], const float* v, int64_t n0, int64_t n) {
+    const float* p = v + n0;
+    if (n0 + CW <= n && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+        for (int j = 0; j < CW; j += 4) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(p + j));
+            f[j] = q.x;
+            f[j + 1] = q.y;
+            f[j + 2] = q.z;
+            f[j + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < CW; ++j) f[j] = n0 + j < n ? __ldg(p + j) : 0.0f;
+    }
+}
+
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) { ptx::tmem_ld_32x32b_x32(addr, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { ptx::tmem_ld_32x32b_x16(addr, r); }
 
@@ -375,21 +394,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                         }
                     }
                     if (E4M3) {
+                        float f[CW];
+                        load_columns(f, p.col_scale[0], nc, p.n);
 #pragma unroll
-                        for (int j = 0; j < CW; ++j) {
-                            const int32_t n = nc + j;
-                            const float s0 = n < p.n ? __ldg(p.col_scale[0] + n) : 0.0f;
-                            z[j] = __float_as_uint(__uint_as_float(z[j]) * (rs * s0));
-                            if (kDual) {
-                                const float s1 = n < p.n ? __ldg(p.col_scale[1] + n) : 0.0f;
-                                w[j] = __float_as_uint(__uint_as_float(w[j]) * (rs * s1));
-                            }
+                        for (int j = 0; j < CW; ++j) z[j] = __float_as_uint(__uint_as_float(z[j]) * (rs * f[j]));
+                        if (kDual) {
+                            load_columns(f, p.col_scale[1], nc, p.n);
+#pragma unroll
+                            for (int j = 0; j < CW; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * (rs * f[j]));
                         }
                     }
                     if (!kDual && p.bias) {
+                        float f[CW];
+                        load_columns(f, p.bias, nc, p.n);
 #pragma unroll
-                        for (int j = 0; j < CW; ++j)
-                            z[j] = __float_as_uint(__uint_as_float(z[j]) + (nc + j < p.n ? __ldg(p.bias + nc + j) : 0.0f));
+                        for (int j = 0; j < CW; ++j) z[j] = __float_as_uint(__uint_as_float(z[j]) + f[j]);
                     }
                     // the results take the places of what they are made of: y in z, the
                     // second output in w

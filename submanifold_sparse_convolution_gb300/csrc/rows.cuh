@@ -14,20 +14,50 @@
 namespace spconv {
 
 // ---- activations -----------------------------------------------------------
-// Evaluated on the fp32 sum.  __expf and __fdividef are a few fp32 ulps off,
-// far below the bf16 rounding of whatever is stored.
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// Evaluated on the fp32 sum in every epilogue, so they are made of few
+// instructions: 2^x and 1/x of the special-function unit (relative error about
+// 2^-22, far below the bf16 rounding of whatever is stored) and FMAs.  2^x of a
+// large argument is infinity and 1/infinity is 0, which are the limits wanted.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float sigmoid_f(float z) { return rcp_approx(1.0f + exp2_approx(-1.44269504f * z)); }
 
 // tanh form of GELU: 0.5 (1 + tanh(v / 2)) is the logistic function of v
 constexpr float kGeluA = 1.5957691216057308f;   // sqrt(8 / pi)
 constexpr float kGeluB = 0.044715f;
 
+// The normal distribution function Phi(z) = erfc(-z / sqrt 2) / 2 and e =
+// exp(-z^2 / 2), with erfc of x = |z| / sqrt 2 from Abramowitz and Stegun,
+// Handbook of Mathematical Functions, 7.1.26: (a1 t + .. + a5 t^5) exp(-x^2),
+// t = 1 / (1 + p x), absolute error at most 1.5e-7.
+__device__ __forceinline__ float normal_cdf(float z, float* e) {
+    const float t = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
+    float q = fmaf(t, 1.061405429f, -1.453152027f);
+    q = fmaf(t, q, 1.421413741f);
+    q = fmaf(t, q, -0.284496736f);
+    q = fmaf(t, q, 0.254829592f);
+    *e = exp2_approx(-0.72134752f * z * z);   // log2(e) / 2
+    q = 0.5f * q * t * *e;
+    return z < 0.0f ? q : 1.0f - q;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
     if (ACT == SPCONV_ACT_RELU) return z < 0.0f ? 0.0f : z;   // keeps NaN
     if (ACT == SPCONV_ACT_SILU) return z * sigmoid_f(z);
-    if (ACT == SPCONV_ACT_GELU) return 0.5f * z * erfcf(-0.70710678f * z);   // erfc: no cancellation for z << 0
-    if (ACT == SPCONV_ACT_GELU_TANH) return z * sigmoid_f(kGeluA * z * fmaf(kGeluB * z, z, 1.0f));
+    if (ACT == SPCONV_ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, &e);
+    }
+    if (ACT == SPCONV_ACT_GELU_TANH) return z * sigmoid_f(z * fmaf(kGeluA * kGeluB * z, z, kGeluA));
     return z;
 }
 
@@ -41,17 +71,18 @@ __device__ __forceinline__ float act_grad_f(float z, float* a) {
     if (ACT == SPCONV_ACT_SILU) {
         const float s = sigmoid_f(z);
         *a = z * s;
-        return fmaf(z * s, 1.0f - s, s);
+        return fmaf(*a, 1.0f - s, s);
     }
     if (ACT == SPCONV_ACT_GELU) {
-        const float phi = 0.5f * erfcf(-0.70710678f * z);
+        float e;
+        const float phi = normal_cdf(z, &e);
         *a = z * phi;
-        return fmaf(0.39894228f * z, __expf(-0.5f * z * z), phi);
+        return fmaf(0.39894228f * z, e, phi);
     }
     if (ACT == SPCONV_ACT_GELU_TANH) {
-        const float s = sigmoid_f(kGeluA * z * fmaf(kGeluB * z, z, 1.0f));
+        const float s = sigmoid_f(z * fmaf(kGeluA * kGeluB * z, z, kGeluA));
         *a = z * s;
-        return fmaf(z * s * (1.0f - s), kGeluA * fmaf(3.0f * kGeluB * z, z, 1.0f), s);
+        return fmaf(fmaf(-*a, s, *a), fmaf(3.0f * kGeluA * kGeluB * z, z, kGeluA), s);
     }
     *a = z;
     return 1.0f;
