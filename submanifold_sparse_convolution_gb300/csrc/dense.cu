@@ -197,7 +197,8 @@ int dense_run(const DenseOp& op, cudaStream_t s) {
     const Matrix mb = op.b.k_major ? plan(op.b.p, nb, op.b.ld, op.n, op.k, es) : plan(op.b.p, nb, op.b.ld, op.k, op.n, es);
     const Matrix mx = plan(&op.extra, op.extra ? 1 : 0, op.ld_extra, op.m, op.n, 2);
     const Matrix mc = plan(op.out, nc, op.ld_out, op.m, op.n, 2);
-    if (bytes == 0) return dense_tc_run(op, status, s);
+    auto run = [&](const DenseOp& o) { return dense_few_takes(o) ? dense_few_run(o, status, s) : dense_tc_run(o, status, s); };
+    if (bytes == 0) return run(op);
     Scratch buf(bytes, s);
     if (buf.failed()) return SPCONV_ERR_OOM;
     DenseOp o = op;
@@ -217,7 +218,7 @@ int dense_run(const DenseOp& op, cudaStream_t s) {
         for (int i = 0; i < nc; ++i) o.out[i] = buf.as<void>(mc.off[i]);
         o.ld_out = mc.ld();
     }
-    SPCONV_CHECK(dense_tc_run(o, status, s));
+    SPCONV_CHECK(run(o));
     for (int i = 0; mc.move && i < nc; ++i)
         SPCONV_CHECK(copy_rows(o.out[i], o.ld_out, op.out[i], op.ld_out, op.m, op.n, 2, s));
     return SPCONV_OK;

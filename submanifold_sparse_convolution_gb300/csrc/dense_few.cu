@@ -1,0 +1,272 @@
+// Products with an epilogue for few rows (single tokens up to a small batch).
+//
+// The weight is the traffic: every byte of it is used for a handful of
+// products, so the kernel streams it at the memory's rate and the tensor cores
+// only have to keep up.  The roles of the operands are exchanged: 128 output
+// channels are the MMA's M (the weight's columns as they lie in memory, or the
+// e4m3 weight's rows) and the rows of x its N, padded to 16 instead of 256.
+//
+// 128 channels x all of K would leave most SMs without work, so a cluster of
+// `splits` CTAs cuts K between them.  Each keeps its fp32 sums in shared
+// memory and every CTA adds the partial sums of its share of the rows through
+// distributed shared memory, in the order of the ranks, applies the epilogue
+// and stores: one launch, no workspace, the same bits every run.  Two CTAs fit
+// an SM, which together keep about 200 KB of loads in flight.
+#include "ptx_sm100.cuh"
+#include "tensor_map.cuh"
+
+namespace spconv {
+namespace {
+
+constexpr int kThreads = 192;          // warp 0 loads, warp 1 issues MMAs, warps 2-5 read the accumulator
+constexpr int kChannels = 128;         // output channels per CTA (MMA M)
+constexpr int kTileA = kChannels * 128;
+constexpr int kMaxRows = 128;          // one accumulator
+constexpr int kMaxRowsDual = 64;       // gate and up
+constexpr int kMaxSplits = 8;          // portable cluster size
+constexpr int kMaxStages = 8;
+constexpr int kRing = 100 * 1024;      // stages, of one CTA
+
+struct FewArgs {
+    CUtensorMap w[2], x;
+    int64_t n;             // channels
+    int32_t rows, rows_pad;
+    int32_t k_iters;
+    int32_t stages, stage_bytes;
+    int32_t w_kmajor;
+    int32_t act;
+    const float* row_scale;
+    const float* col_scale[2];
+    const float* bias;
+    const __nv_bfloat16* extra;
+    int64_t ld_extra;
+    __nv_bfloat16* out;
+    int64_t ld_out;
+    int32_t* status;
+};
+
+template <bool DUAL, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 2) k_dense_few(const __grid_constant__ FewArgs p) {
+    constexpr int kAcc = DUAL ? 2 : 1;
+    constexpr int kBK = E4M3 ? 128 : 64;
+    constexpr uint32_t kCols = DUAL ? 2 * kMaxRowsDual : kMaxRows;   // TMEM columns (a power of two)
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    uint8_t* ring = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t splits = gridDim.y, rank = blockIdx.y;   // the cluster is one column of the grid
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        ptx::mbar_init(&done, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_map(&p.w[0]);
+        ptx::prefetch_map(&p.x);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&tmem_slot, kCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = tmem_slot;
+    const int32_t n0 = static_cast<int32_t>(blockIdx.x) * kChannels;
+    // (k_iters >= splits: no slice is empty)
+    const int32_t it0 = static_cast<int32_t>(rank * static_cast<uint32_t>(p.k_iters) / splits);
+    const int32_t it1 = static_cast<int32_t>((rank + 1) * static_cast<uint32_t>(p.k_iters) / splits);
+    auto fail = [&]() {
+        atomicOr(p.status, kStatusTimeout);
+        *abort_flag = 1;
+    };
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t bytes = kAcc * kTileA + static_cast<uint32_t>(p.rows_pad) * 128u;
+            int32_t f = 0;
+            bool ok = true;
+            for (int32_t it = it0; it < it1; ++it, ++f) {
+                const int32_t s = f % p.stages;
+                if (f >= p.stages && !ptx::mbar_wait(&empty[s], static_cast<uint32_t>(f / p.stages - 1) & 1, abort_flag)) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                const uint32_t base = ptx::smem_u32(ring) + static_cast<uint32_t>(s * p.stage_bytes);
+                const uint32_t bar = ptx::smem_u32(&full[s]);
+                ptx::mbar_arrive_expect_tx(&full[s], bytes);
+#pragma unroll
+                for (int a = 0; a < kAcc; ++a) {
+                    if (p.w_kmajor) {
+                        ptx::tma_load_2d(base + a * kTileA, &p.w[a], it * kBK, n0, bar);
+                    } else {
+                        ptx::tma_load_2d(base + a * kTileA, &p.w[a], n0, it * kBK, bar);
+                        ptx::tma_load_2d(base + a * kTileA + 8192, &p.w[a], n0 + 64, it * kBK, bar);
+                    }
+                }
+                ptx::tma_load_2d(base + kAcc * kTileA, &p.x, it * kBK, 0, bar);
+            }
+            if (!ok)   // loads still in flight land before the CTA exits
+                for (int32_t j = f > p.stages ? f - p.stages : 0; j < f; ++j)
+                    ptx::mbar_wait(&full[j % p.stages], static_cast<uint32_t>(j / p.stages) & 1, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint32_t leader = lane == 0;
+        const uint32_t idesc = ptx::idesc_dense(E4M3, p.w_kmajor, true, kChannels, static_cast<uint32_t>(p.rows_pad));
+        const uint32_t base = ptx::smem_u32(ring);
+        const uint64_t a0 = p.w_kmajor ? ptx::sdesc_k128(base) : ptx::sdesc_mn128(base, 64);
+        const uint64_t b0 = ptx::sdesc_k128(base + kAcc * kTileA);
+        const uint64_t da = p.w_kmajor ? 2 : 128;
+        int32_t f = 0;
+        for (int32_t it = it0; it < it1; ++it, ++f) {
+            const int32_t s = f % p.stages;
+            if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&full[s], static_cast<uint32_t>(f / p.stages) & 1, abort_flag))) {
+                if (lane == 0) fail();
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint64_t off = static_cast<uint64_t>(s * p.stage_bytes) >> 4;
+#pragma unroll
+            for (int a = 0; a < kAcc; ++a)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    ptx::mma_if<E4M3>(leader, tmem + a * kMaxRowsDual, a0 + off + a * (kTileA >> 4) + j * da, b0 + off + 2 * j,
+                                      idesc, (f > 0 || j > 0) ? 1u : 0u);
+            ptx::mma_commit_if(leader, &empty[s]);
+        }
+        ptx::mma_commit_if(leader, &done);
+    }
+    // every MMA of this CTA has completed: its sums are whole, its ring is free
+    const bool whole = ptx::mbar_wait(&done, 0, nullptr);
+    if (!whole && threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+    __syncthreads();
+    ptx::tc_fence_after();
+    float* sums = reinterpret_cast<float*>(ring);   // [kAcc][rows][kChannels]
+    if (warp >= 2) {
+        const int quarter = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+#pragma unroll
+        for (int a = 0; a < kAcc; ++a)
+            for (int32_t r0 = 0; r0 < p.rows; r0 += 16) {
+                uint32_t v[16];
+                ptx::tmem_ld_32x32b_x16(tmem + lanes + a * kMaxRowsDual + r0, v);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (r0 + j < p.rows) sums[(a * p.rows + r0 + j) * kChannels + quarter * 32 + lane] = __uint_as_float(v[j]);
+            }
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    // this CTA's share: rows rank, rank + splits, ..
+    const int32_t mine = (p.rows - static_cast<int32_t>(rank) + static_cast<int32_t>(splits) - 1) / static_cast<int32_t>(splits);
+    const uint32_t sums_addr = ptx::smem_u32(sums);
+    for (int32_t i = threadIdx.x; i < mine * kChannels; i += kThreads) {
+        const int32_t ch = i & (kChannels - 1);
+        const int32_t row = static_cast<int32_t>(rank) + (i >> 7) * static_cast<int32_t>(splits);
+        const int64_t n = n0 + ch;
+        if (n >= p.n) continue;
+        float z[kAcc];
+#pragma unroll
+        for (int a = 0; a < kAcc; ++a) {
+            const uint32_t at = sums_addr + static_cast<uint32_t>(((a * p.rows + row) * kChannels + ch) * 4);
+            float part[kMaxSplits];
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxSplits; ++r)
+                part[r] = r < splits ? ptx::ld_cluster_f32(ptx::map_to_rank(at, r)) : 0.0f;
+            z[a] = part[0];
+#pragma unroll
+            for (uint32_t r = 1; r < kMaxSplits; ++r) z[a] += part[r];
+            if (E4M3) z[a] *= p.row_scale[row] * p.col_scale[a][n];
+        }
+        if (!DUAL && p.bias) z[0] += p.bias[n];
+        const float x = (!DUAL && p.extra) ? __bfloat162float(p.extra[row * p.ld_extra + n]) : 0.0f;
+        float y = 0.0f;
+        with_act(p.act, [&](auto act) { y = DUAL ? act_f<act>(z[0]) * z[kAcc - 1] : act_f<act>(z[0]) + x; });
+        p.out[row * p.ld_out + n] = __float2bfloat16_rn(y);
+    }
+    // no CTA's sums go away while another may still read them
+    ptx::cluster_sync();
+    if (warp == 1) ptx::tmem_dealloc(tmem, kCols);
+}
+
+template <bool DUAL, bool E4M3>
+int launch(const FewArgs& p, int32_t tiles, int32_t splits, size_t smem, cudaStream_t s) {
+    static bool set[kMaxDevices] = {};
+    int dev = 0;
+    SPCONV_CHECK_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= kMaxDevices) return SPCONV_ERR_UNSUPPORTED;
+    if (!set[dev]) {
+        SPCONV_CHECK_CUDA(cudaFuncSetAttribute(k_dense_few<DUAL, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 2048));
+        set[dev] = true;
+    }
+    cudaLaunchAttribute at[2] = {pdl_attr(), {}};
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = static_cast<unsigned>(splits);
+    at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(splits));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    count_launch();
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_dense_few<DUAL, E4M3>, p));
+}
+
+}  // namespace
+
+bool dense_few_takes(const DenseOp& op) {
+    if (op.k_sources != 1 || op.n_sources != 1 || !op.a.k_major) return false;
+    if (op.epi == kEpiGated) return op.m <= kMaxRowsDual;
+    return op.epi == kEpiLinear && op.m <= kMaxRows;
+}
+
+int dense_few_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
+    const bool dual = op.epi == kEpiGated, eight = op.dtype == SPCONV_E4M3;
+    const size_t es = eight ? 1 : 2;
+    FewArgs p = {};
+    p.n = op.n;
+    p.rows = static_cast<int32_t>(op.m);
+    p.rows_pad = static_cast<int32_t>(round_up(static_cast<size_t>(op.m), 16));
+    p.k_iters = static_cast<int32_t>(ceil_div(op.k, static_cast<int64_t>(128 / es)));
+    p.w_kmajor = op.b.k_major;
+    p.act = op.act;
+    p.row_scale = op.row_scale;
+    p.col_scale[0] = op.col_scale[0];
+    p.col_scale[1] = op.col_scale[1];
+    p.bias = op.bias;
+    p.extra = static_cast<const __nv_bfloat16*>(op.extra);
+    p.ld_extra = op.ld_extra;
+    p.out = static_cast<__nv_bfloat16*>(op.out[0]);
+    p.ld_out = op.ld_out;
+    p.status = status;
+    const int32_t tiles = static_cast<int32_t>(ceil_div(op.n, kChannels));
+    // As many CTAs as two per SM, each with four steps of K at least
+    int32_t splits = 1;
+    while (splits < kMaxSplits && tiles * splits * 2 <= 2 * 152 && p.k_iters >= 8 * splits) splits *= 2;
+    const int acc = dual ? 2 : 1;
+    p.stage_bytes = static_cast<int32_t>(round_up(acc * kTileA + p.rows_pad * 128, 1024));
+    p.stages = kRing / p.stage_bytes < kMaxStages ? kRing / p.stage_bytes : kMaxStages;
+    for (int a = 0; a < acc; ++a)
+        SPCONV_CHECK(op.b.k_major ? make_tensor_map(&p.w[a], op.b.p[a], es, op.k, op.n, op.b.ld, kChannels)
+                                  : make_tensor_map(&p.w[a], op.b.p[a], es, op.n, op.k, op.b.ld, 64));
+    SPCONV_CHECK(make_tensor_map(&p.x, op.a.p[0], es, op.k, op.m, op.a.ld, p.rows_pad));
+    const size_t ring = static_cast<size_t>(p.stages) * p.stage_bytes, sums = static_cast<size_t>(acc) * op.m * kChannels * 4;
+    const size_t smem = (ring > sums ? ring : sums) + 1024;
+    if (dual) return eight ? launch<true, true>(p, tiles, splits, smem, s) : launch<true, false>(p, tiles, splits, smem, s);
+    return eight ? launch<false, true>(p, tiles, splits, smem, s) : launch<false, false>(p, tiles, splits, smem, s);
+}
+
+}  // namespace spconv

@@ -25,12 +25,8 @@
 //              is ready
 // The accumulator is double-buffered in TMEM (2 x 256 columns), so the
 // epilogue of one tile runs beside the main loop of the next.
-#include <cuda.h>
-
-#include <type_traits>
-
 #include "ptx_sm100.cuh"
-#include "rows.cuh"
+#include "tensor_map.cuh"
 
 namespace spconv {
 namespace {
@@ -526,37 +522,6 @@ __global__ void __launch_bounds__(256) k_sum_slices(const float* part, int32_t s
 }
 
 // ---- host -------------------------------------------------------------------
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static const EncodeFn fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult r = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<EncodeFn>(f);
-    }();
-    return fn;
-}
-
-// A [outer] x [inner] matrix of rows `ld` elements apart, copied in boxes of
-// box_inner (128 bytes) x box_outer, 128-byte swizzled in shared memory.
-int make_map(CUtensorMap* map, const void* base, size_t es, int64_t inner, int64_t outer, int64_t ld, int32_t box_outer) {
-    const EncodeFn fn = encode_fn();
-    if (!fn) return SPCONV_ERR_CUDA;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_outer)};
-    const cuuint32_t unit[2] = {1, 1};
-    const CUresult r = fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                          const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? SPCONV_OK : SPCONV_ERR_CUDA;
-}
-
 template <int EPI, bool E4M3>
 int launch(const TcArgs& args, int32_t pairs, cudaStream_t s) {
     static bool set[kMaxDevices] = {};
@@ -581,6 +546,40 @@ int launch(const TcArgs& args, int32_t pairs, cudaStream_t s) {
 }
 
 }  // namespace
+
+namespace {
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+}  // namespace
+
+// A [outer] x [inner] matrix of rows `ld` elements apart, copied in boxes of
+// box_inner (128 bytes) x box_outer, 128-byte swizzled in shared memory.
+int make_tensor_map(CUtensorMap* map, const void* base, size_t es, int64_t inner, int64_t outer, int64_t ld, int32_t box_outer) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return SPCONV_ERR_CUDA;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_outer)};
+    const cuuint32_t unit[2] = {1, 1};
+    const CUresult r = fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                          const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SPCONV_OK : SPCONV_ERR_CUDA;
+}
 
 int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     const size_t es = op.dtype == SPCONV_E4M3 ? 1 : 2;
@@ -621,15 +620,15 @@ int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
         p.splits = static_cast<int32_t>(ceil_div(p.k_total, p.split_iters));
     }
     for (int i = 0; i < (op.k_sources == 2 ? 2 : 1); ++i)
-        SPCONV_CHECK(op.a.k_major ? make_map(&p.a[i], op.a.p[i], es, op.k, op.m, op.a.ld, kRowsA)
-                                  : make_map(&p.a[i], op.a.p[i], es, op.m, op.k, op.a.ld, 64));
+        SPCONV_CHECK(op.a.k_major ? make_tensor_map(&p.a[i], op.a.p[i], es, op.k, op.m, op.a.ld, kRowsA)
+                                  : make_tensor_map(&p.a[i], op.a.p[i], es, op.m, op.k, op.a.ld, 64));
     for (int i = 0; i < ((dual || op.k_sources == 2 || op.n_sources == 2) ? 2 : 1); ++i)
-        SPCONV_CHECK(op.b.k_major ? make_map(&p.b[i], op.b.p[i], es, op.k, op.n, op.b.ld, p.hb)
-                                  : make_map(&p.b[i], op.b.p[i], es, op.n, op.k, op.b.ld, 64));
+        SPCONV_CHECK(op.b.k_major ? make_tensor_map(&p.b[i], op.b.p[i], es, op.k, op.n, op.b.ld, p.hb)
+                                  : make_tensor_map(&p.b[i], op.b.p[i], es, op.n, op.k, op.b.ld, 64));
     if (p.splits == 1)
         for (int i = 0; i < ((op.epi == kEpiGatedGrad || op.n_sources == 2) ? 2 : 1); ++i)
-            SPCONV_CHECK(make_map(&p.c[i], op.out[i], 2, op.n, op.m, op.ld_out, 32));
-    if (op.extra) SPCONV_CHECK(make_map(&p.x, op.extra, 2, op.n, op.m, op.ld_extra, 32));
+            SPCONV_CHECK(make_tensor_map(&p.c[i], op.out[i], 2, op.n, op.m, op.ld_out, 32));
+    if (op.extra) SPCONV_CHECK(make_tensor_map(&p.x, op.extra, 2, op.n, op.m, op.ld_extra, 32));
     const int64_t units = tiles * p.splits;
     const int32_t pairs = static_cast<int32_t>(units < kPairs ? units : kPairs);
 

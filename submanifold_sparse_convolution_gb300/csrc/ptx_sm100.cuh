@@ -292,8 +292,11 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 }
 
 // Arrive on an mbarrier anywhere in the cluster (address from map_to_rank).
+// The scope is the CTA: enough where only tensor memory is handed over (the
+// tcgen05 fences order that).  A release at cluster scope would wait for all of
+// the thread's stores first (measured: about 3,000 cycles behind an epilogue).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -389,6 +392,30 @@ __device__ __forceinline__ void mma_pair_if(uint32_t issue, uint32_t d_tmem, uin
             "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
             : "memory");
     }
+}
+
+// One CTA's MMA (cta_group::1) by the threads whose `issue` is nonzero.
+template <bool E4M3>
+__device__ __forceinline__ void mma_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    if (!E4M3) {
+        mma_bf16_if(issue, d_tmem, a_desc, b_desc, idesc, accumulate);
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+            : "memory");
+    }
+}
+
+// A float of another CTA's shared memory (address from map_to_rank).
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // Arrive on the mbarrier at this offset in both CTAs once the MMAs issued so far are done.

@@ -205,6 +205,9 @@ struct DenseOp {
 int dense_run(const DenseOp& op, cudaStream_t s);
 // the same on the tensor cores (dense_tc.cu); operands, extra and out satisfy tma_ok
 int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s);
+// the same for few rows (dense_few.cu): dense_few_takes says which
+bool dense_few_takes(const DenseOp& op);
+int dense_few_run(const DenseOp& op, int32_t* status, cudaStream_t s);
 // The device status word of the row-wise operators on the current device.
 int rows_status_word(int32_t** word);
 

@@ -1,0 +1,14 @@
+// Tensor maps of row matrices, for the kernels that load operands with them.
+#pragma once
+#include <cuda.h>
+
+#include "rows.cuh"
+
+namespace spconv {
+
+// Copies of [outer] rows of `inner` elements, `ld` elements apart, in boxes of
+// 128 bytes x box_outer rows, 128-byte swizzled in shared memory; what lies
+// outside reads zeros and is not written.  The rows satisfy tma_ok.
+int make_tensor_map(CUtensorMap* map, const void* base, size_t es, int64_t inner, int64_t outer, int64_t ld, int32_t box_outer);
+
+}  // namespace spconv
