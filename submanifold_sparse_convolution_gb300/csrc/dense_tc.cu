@@ -17,12 +17,15 @@
 //   warp 0     tensor-map loads into a ring of stages; both CTAs' loads
 //              complete on CTA 0's barrier
 //   warp 1     MMA issue (CTA 0), TMEM allocation
-//   warps 2-9  epilogue, two warps per 32 accumulator rows: 32 columns at a
-//              time from TMEM, fp32 epilogue, one rounding, staged in shared
-//              memory and stored by a tensor-map copy, which also clips the
-//              ragged edges; the residual or incoming gradient arrives in the
-//              same staging buffer by a tensor-map load before the accumulator
-//              is ready
+//   warps 2-17 epilogue, in eight pairs: two pairs per 32 accumulator rows take
+//              blocks of 64 columns in turn, 32 columns a warp.  Columns come
+//              from TMEM 16 at a time, fp32 epilogue, one rounding, staged in
+//              shared memory and stored by a tensor-map copy, which also clips
+//              the ragged edges; the residual or incoming gradient arrives in
+//              the same staging buffer by a tensor-map load before the
+//              accumulator is ready.  (With half as many warps the latencies of
+//              one tile's epilogue, not its instructions, set the pace of short
+//              contractions: 38912 x 128 x 512 gated took 19.0 us.)
 // The accumulator is double-buffered in TMEM (2 x 256 columns), so the
 // epilogue of one tile runs beside the main loop of the next.
 #include "ptx_sm100.cuh"
@@ -35,17 +38,33 @@ constexpr int kRowsA = 128;                   // rows of A per CTA
 constexpr int kStageA = kRowsA * 128;         // 128 bytes of K per stage
 constexpr int kStageB = 128 * 128;            // hb <= 128 rows
 constexpr int kStage = kStageA + kStageB;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
+constexpr int kEpiPairs = kEpiWarps / 2;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr int kStaging = 32 * 128;            // 32 rows x 64 bf16, one epilogue warp
+constexpr int kStaging = 32 * 128;            // 32 rows x 64 bf16, one pair of epilogue warps
 constexpr int kTmemCols = 512;
 constexpr int kGroupM = 16;                   // row tiles that share the column tiles in L2
 constexpr int kPairs = 76;                    // CTA pairs of a full GPU
 
 constexpr int32_t kEpiPartial = 4;            // fp32 sums of one slice of K, to a workspace
 
+// x / d for 0 <= x < 2^31, without a division: x m / 2^(31 + s) with
+// s = ceil(log2 d) and m = ceil(2^(31 + s) / d).
+struct FastDiv {
+    uint32_t d, m, s;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t v) : d(v), s(0) {
+        while ((1ull << s) < v) ++s;
+        m = static_cast<uint32_t>(((1ull << (31 + s)) + v - 1) / v);
+    }
+    __device__ __forceinline__ int32_t operator()(int32_t x) const {
+        return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(x)) * m) >> (31 + s));
+    }
+};
+
 struct TcArgs {
     CUtensorMap a[2], b[2], c[2], x;
+    FastDiv by_tiles, by_group, by_height, by_last_height, by_tiles_n;   // divisors of the unit numbers
     int64_t m, n;
     int32_t k_iters;       // stages of one source
     int32_t k_total;       // stages of all sources
@@ -66,9 +85,9 @@ struct TcArgs {
 
 template <int EPI>
 struct TcConfig {
-    static constexpr int kBufs = EPI == kEpiGatedGrad ? 2 : 1;   // staging buffers of an epilogue warp
+    static constexpr int kBufs = EPI == kEpiGatedGrad ? 2 : 1;   // staging buffers of a pair of epilogue warps
     static constexpr int kStages = EPI == kEpiGatedGrad ? 5 : 6;
-    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kBufs * kStaging + 512;
+    static constexpr int kSmem = 1024 + kStages * kStage + kEpiPairs * kBufs * kStaging + 512;
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -83,10 +102,11 @@ __device__ __forceinline__ uint4 pack8(const uint32_t* v) {
     return make_uint4(two(0), two(2), two(4), two(6));
 }
 
-// Sums of the fp32 values v[j] (as bits) over the 32 lanes: lane l returns that of column l.
-__device__ __forceinline__ float column_sum32(uint32_t (&v)[32], int lane) {
+// Sums of the fp32 values v[j] (as bits) over the 32 lanes: lanes l and l + 16
+// return that of column l < 16.
+__device__ __forceinline__ float column_sum16(uint32_t (&v)[16], int lane) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = 8; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int j = 0; j < o; ++j) {
@@ -95,7 +115,8 @@ __device__ __forceinline__ float column_sum32(uint32_t (&v)[32], int lane) {
             v[j] = __float_as_uint(keep + __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, send, o)));
         }
     }
-    return __uint_as_float(v[0]);
+    const float s = __uint_as_float(v[0]);
+    return s + __shfl_xor_sync(0xFFFFFFFFu, s, 16);
 }
 
 // v[n0 .. n0 + CW) of a column vector of n values (the same for all lanes), 0 past its end.
@@ -117,29 +138,25 @@ __device__ __forceinline__ void load_columns(float (&f)[CW], const float* v, int
     }
 }
 
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) { ptx::tmem_ld_32x32b_x32(addr, r); }
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { ptx::tmem_ld_32x32b_x16(addr, r); }
-
 template <int EPI, bool E4M3>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense_tc(const __grid_constant__ TcArgs p) {
     using Cfg = TcConfig<EPI>;
     constexpr int S = Cfg::kStages;
     constexpr bool kDual = EPI == kEpiGated || EPI == kEpiGatedGrad;
     constexpr int kBK = E4M3 ? 128 : 64;      // K elements of a stage
-    // accumulator columns a thread takes at once: 32, or 16 where 32 would spill
-    constexpr int CW = (EPI == kEpiGatedGrad || (EPI == kEpiLinear && E4M3)) ? 16 : 32;
+    constexpr int CW = 16;                    // accumulator columns a thread takes at once
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
     uint8_t* staging = smem + S * kStage;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiWarps * Cfg::kBufs * kStaging);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiPairs * Cfg::kBufs * kStaging);
     uint64_t* full = bars;              // [S]  (CTA 0's are used)
     uint64_t* empty = full + S;         // [S]
     uint64_t* acc_full = empty + S;     // [2]
     uint64_t* acc_empty = acc_full + 2; // [2]  (CTA 0's are used)
     uint64_t* exit_bar = acc_empty + 2;
-    uint64_t* extra_full = exit_bar + 1;   // [kEpiWarps]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(extra_full + kEpiWarps);
+    uint64_t* extra_full = exit_bar + 1;   // [kEpiPairs]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(extra_full + kEpiPairs);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -154,7 +171,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
             ptx::mbar_init(&acc_empty[b], 2 * kEpiWarps);
         }
         ptx::mbar_init(exit_bar, 1);
-        for (int w = 0; w < kEpiWarps; ++w) ptx::mbar_init(&extra_full[w], 1);
+        for (int w = 0; w < kEpiPairs; ++w) ptx::mbar_init(&extra_full[w], 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_map(&p.a[0]);
@@ -189,15 +206,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
     };
     auto decode = [&](int32_t u) {
         Unit t;
-        t.split = u / tiles;
+        t.split = p.by_tiles(u);
         const int32_t i = u - t.split * tiles;
-        const int32_t grp = i / (kGroupM * tiles_nn);
+        const int32_t grp = p.by_group(i);
         const int32_t first = grp * kGroupM;
-        const int32_t gm = p.tiles_m - first < kGroupM ? p.tiles_m - first : kGroupM;
         const int32_t r = i - grp * kGroupM * tiles_nn;
-        t.tm = first + r % gm;
-        const int32_t nn = r / gm;
-        t.src = nn / p.tiles_n;
+        const bool last = p.tiles_m - first < kGroupM;
+        const int32_t gm = last ? p.tiles_m - first : kGroupM;
+        const int32_t nn = last ? p.by_last_height(r) : p.by_height(r);
+        t.tm = first + r - nn * gm;
+        t.src = p.by_tiles_n(nn);
         t.tn = nn - t.src * p.tiles_n;
         t.k0 = t.split * p.split_iters;
         t.k1 = t.k0 + p.split_iters < p.k_total ? t.k0 + p.split_iters : p.k_total;
@@ -296,18 +314,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
         }
     } else {
         // ---------------- epilogue
+        // A pair of warps meets before and after each block of 64 columns, and
+        // once per tile to agree on going on: a warp whose wait ran out keeps
+        // meeting its partner until then.
         const int e = warp - 2;
         const int quarter = warp & 3;            // the TMEM lanes a warp may read
-        const int half = e >> 2;
-        uint8_t* stage0 = staging + e * Cfg::kBufs * kStaging;
+        const int sub = (e >> 2) & 1, half = e >> 3;   // which 32 columns of a block; which blocks
+        const int pair_of = quarter + 4 * half;
+        const uint32_t meet = 1 + pair_of;
+        uint8_t* stage0 = staging + pair_of * Cfg::kBufs * kStaging;
         const uint32_t st0 = ptx::smem_u32(stage0);
         const uint32_t row_off = static_cast<uint32_t>(lane) * 128;
         const uint32_t sw = lane & 7;
-        uint64_t* xbar = &extra_full[e];
+        uint64_t* xbar = &extra_full[pair_of];
         uint32_t xphase = 0;
         const uint32_t acc_bar = ptx::map_to_rank(ptx::smem_u32(&acc_empty[0]), 0);
         const int chunks = (kDual ? p.hb : 2 * p.hb) / 64;
+        const bool lead = sub == 0 && lane == 0;
         int32_t ai = 0;
+        bool ok = true;
         for (int32_t u = pair; u < units; u += n_pairs, ++ai) {
             const Unit t = decode(u);
             const int buf = ai & 1;
@@ -316,49 +341,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
             const int32_t col0 = t.tn * (kDual ? p.hb : 2 * p.hb);
             const bool rows_live = m0 < p.m;
             const bool row_live = row < p.m;
-            const float rs = (p.row_scale && row_live) ? p.row_scale[row] : 1.0f;
+            const float rs = (E4M3 && row_live) ? p.row_scale[row] : 1.0f;
             bool waited = false;
-            bool ok = true;
+            auto wait_acc = [&]() {
+                if (waited) return;
+                waited = true;
+                if (ok && !warp_wait(&acc_full[buf], (static_cast<uint32_t>(ai) >> 1) & 1)) {
+                    if (lane == 0) fail();
+                    ok = false;
+                }
+                ptx::tc_fence_after();
+            };
             for (int c = half; c < chunks; c += 2) {
                 const int32_t n0 = col0 + c * 64;
-                const bool live = rows_live && n0 < p.n;   // (warp-uniform)
-                if (EPI != kEpiPartial && live) {
+                if (!(rows_live && n0 < p.n)) continue;   // (the same for both warps of a pair)
+                if (EPI != kEpiPartial) {
                     // the staging buffer is free once its last store has been read out
-                    if (lane == 0) {
+                    if (lead) {
                         ptx::bulk_wait_read();
                         if (EPI != kEpiGated && p.has_extra) {
                             ptx::mbar_arrive_expect_tx(xbar, kStaging);
                             ptx::tma_load_2d(st0, &p.x, n0, m0, ptx::smem_u32(xbar));
                         }
                     }
-                    __syncwarp();
+                    ptx::named_barrier_sync(meet, 64);
                 }
-                if (!waited) {
-                    if (!warp_wait(&acc_full[buf], (static_cast<uint32_t>(ai) >> 1) & 1)) {
-                        if (lane == 0) fail();
-                        ok = false;
-                    }
-                    ptx::tc_fence_after();
-                    waited = true;
-                }
-                if (EPI != kEpiPartial && EPI != kEpiGated && live && p.has_extra) {
-                    // (also after a failed wait above: the copy must land before the CTA exits)
+                wait_acc();
+                if (EPI != kEpiPartial && EPI != kEpiGated && p.has_extra) {
+                    // (also after a failed wait: the copy must land before the CTA exits)
                     if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(xbar, xphase, nullptr))) {
                         if (lane == 0) fail();
                         ok = false;
                     }
                     xphase ^= 1;
                 }
-                if (!ok) break;
-                if (!live) continue;
-                const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * 256 + c * 64);
-#pragma unroll 1
-                for (int h = 0; h < 64 / CW; ++h) {
+                const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                    static_cast<uint32_t>(buf * 256 + c * 64 + sub * 32);
+#pragma unroll
+                for (int h = 0; h < 32 / CW; ++h) {
+                    if (!ok) break;
                     uint32_t z[CW], w[CW];
-                    tmem_ld(ta + h * CW, z);
-                    if (kDual) tmem_ld(ta + p.hb + h * CW, w);
+                    ptx::tmem_ld_32x32b_x16(ta + h * CW, z);
+                    if (kDual) ptx::tmem_ld_32x32b_x16(ta + p.hb + h * CW, w);
                     ptx::tmem_ld_wait();
-                    const int32_t nc = n0 + h * CW;
+                    const int32_t nc = n0 + sub * 32 + h * CW;
+                    const uint32_t piece = sub * 4 + h * (CW / 8);   // first 16-byte piece of these columns in a row
                     if (EPI == kEpiPartial) {
                         if (row_live) {
                             float* dst = p.part + ((static_cast<int64_t>(t.split) * p.n_sources + t.src) * p.m + row) * p.n + nc;
@@ -381,8 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
 #pragma unroll
                         for (int q = 0; q < CW / 8; ++q) {
                             uint4 v = make_uint4(0, 0, 0, 0);
-                            if (p.has_extra)
-                                v = *reinterpret_cast<const uint4*>(stage0 + row_off + (((h * (CW / 8) + q) ^ sw) << 4));
+                            if (p.has_extra) v = *reinterpret_cast<const uint4*>(stage0 + row_off + (((piece + q) ^ sw) << 4));
                             x[4 * q] = v.x;
                             x[4 * q + 1] = v.y;
                             x[4 * q + 2] = v.z;
@@ -436,46 +462,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                     });
 #pragma unroll
                     for (int q = 0; q < CW / 8; ++q) {
-                        const uint32_t at = row_off + (((h * (CW / 8) + q) ^ sw) << 4);
+                        const uint32_t at = row_off + (((piece + q) ^ sw) << 4);
                         *reinterpret_cast<uint4*>(stage0 + at) = pack8(z + 8 * q);
                         if (EPI == kEpiGatedGrad) *reinterpret_cast<uint4*>(stage0 + kStaging + at) = pack8(w + 8 * q);
                     }
                     if constexpr (EPI == kEpiActGrad) {
                         if (p.part) {
-                            const float s = column_sum32(z, lane);
+                            const float s = column_sum16(z, lane);
                             const int64_t pr = static_cast<int64_t>(t.tm) * 8 + rank * 4 + quarter;
-                            if (nc + lane < p.n) p.part[pr * p.n + nc + lane] = s;
+                            if (lane < CW && nc + lane < p.n) p.part[pr * p.n + nc + lane] = s;
                         }
                     }
                 }
                 if (EPI != kEpiPartial) {
                     ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
+                    ptx::named_barrier_sync(meet, 64);
+                    if (lead) {
                         ptx::tma_store_2d(&p.c[EPI == kEpiLinear ? t.src : 0], n0, m0, st0);
                         if (EPI == kEpiGatedGrad) ptx::tma_store_2d(&p.c[1], n0, m0, st0 + kStaging);
                         ptx::bulk_commit();
                     }
                 }
             }
-            // (a warp without a chunk of this tile still takes its turn)
-            if (!waited && !warp_wait(&acc_full[buf], (static_cast<uint32_t>(ai) >> 1) & 1)) {
-                if (lane == 0) fail();
-                ok = false;
-            }
-            if (!ok) break;
+            wait_acc();   // (a warp without a block of this tile still takes its turn)
             // rows past m of the column sums: whole 32-row groups without a row
             if (EPI == kEpiActGrad && p.part && !rows_live) {
                 const int64_t pr = static_cast<int64_t>(t.tm) * 8 + rank * 4 + quarter;
-                for (int c = half; c < chunks; c += 2)
-                    for (int j = lane; j < 64; j += 32)
-                        if (col0 + c * 64 + j < p.n) p.part[pr * p.n + col0 + c * 64 + j] = 0.0f;
+                for (int c = half; c < chunks; c += 2) {
+                    const int32_t n = col0 + c * 64 + sub * 32 + lane;
+                    if (n < p.n) p.part[pr * p.n + n] = 0.0f;
+                }
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(acc_bar + static_cast<uint32_t>(buf) * 8);
+            if (ok && lane == 0) ptx::mbar_arrive_cluster(acc_bar + static_cast<uint32_t>(buf) * 8);
+            if (ptx::named_barrier_or(meet, 64, !ok)) break;
         }
-        if (lane == 0) ptx::bulk_wait();
+        if (lead) ptx::bulk_wait();
         __syncwarp();
     }
     // neither CTA leaves, or frees TMEM, while the other may still signal it:
@@ -619,6 +642,11 @@ int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
         p.split_iters = static_cast<int32_t>(ceil_div(p.k_total, want));
         p.splits = static_cast<int32_t>(ceil_div(p.k_total, p.split_iters));
     }
+    p.by_tiles = FastDiv(static_cast<uint32_t>(tiles));
+    p.by_group = FastDiv(static_cast<uint32_t>(kGroupM * p.tiles_n * p.n_sources));
+    p.by_height = FastDiv(kGroupM);
+    p.by_last_height = FastDiv(p.tiles_m % kGroupM ? p.tiles_m % kGroupM : kGroupM);
+    p.by_tiles_n = FastDiv(static_cast<uint32_t>(p.tiles_n));
     for (int i = 0; i < (op.k_sources == 2 ? 2 : 1); ++i)
         SPCONV_CHECK(op.a.k_major ? make_tensor_map(&p.a[i], op.a.p[i], es, op.k, op.m, op.a.ld, kRowsA)
                                   : make_tensor_map(&p.a[i], op.a.p[i], es, op.m, op.k, op.a.ld, 64));
