@@ -14,8 +14,8 @@
 // the shared-memory descriptors take both as they lie in memory.
 //
 // Warps of each CTA (persistent over the tiles):
-//   warp 0     tensor-map loads into a ring of stages; both CTAs' loads
-//              complete on CTA 0's barrier
+//   warps 0, 18  tensor-map loads of one operand each into a ring of stages;
+//              both CTAs' loads complete on CTA 0's barrier
 //   warp 1     MMA issue (CTA 0), TMEM allocation
 //   warps 2-17 epilogue, in eight pairs: two pairs per 32 accumulator rows take
 //              blocks of 64 columns in turn, 32 columns a warp.  Columns come
@@ -40,7 +40,8 @@ constexpr int kStageB = 128 * 128;            // hb <= 128 rows
 constexpr int kStage = kStageA + kStageB;
 constexpr int kEpiWarps = 16;
 constexpr int kEpiPairs = kEpiWarps / 2;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kLoadA = 0, kLoadB = 2 + kEpiWarps;   // warps that load an operand each
+constexpr int kThreads = 32 * (3 + kEpiWarps);
 constexpr int kStaging = 32 * 128;            // 32 rows x 64 bf16, one pair of epilogue warps
 constexpr int kTmemCols = 512;
 constexpr int kGroupM = 16;                   // row tiles that share the column tiles in L2
@@ -62,6 +63,10 @@ struct FastDiv {
     }
 };
 
+// How an operand lies in memory: K contiguous; rows contiguous; rows contiguous
+// and a multiple of 64, which one copy takes whole.
+enum : int32_t { kLayoutK = 0, kLayoutRows = 1, kLayoutBlocks = 2 };
+
 struct TcArgs {
     CUtensorMap a[2], b[2], c[2], x;
     FastDiv by_tiles, by_group, by_height, by_last_height, by_tiles_n;   // divisors of the unit numbers
@@ -71,8 +76,7 @@ struct TcArgs {
     int32_t tiles_m, tiles_n, n_sources;
     int32_t splits, split_iters;   // slices of K, stages of a slice
     int32_t hb;
-    int32_t a_kmajor, b_kmajor;
-    int32_t k_sources;
+    int32_t a_layout, b_layout;    // kLayout*
     int32_t act;
     int32_t has_extra;
     const float* row_scale;
@@ -163,7 +167,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
     const uint32_t rank = ptx::cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&full[s], 2);   // one arrival per operand
             ptx::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -222,16 +226,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
         return t;
     };
 
-    if (warp == 0) {
-        // ---------------- loads
+    if (warp == kLoadA || warp == kLoadB) {
+        // ---------------- loads of one operand
         if (lane == 0) {
-            const uint32_t bytes = 2u * (kStageA + static_cast<uint32_t>(p.hb) * 128u);
+            const bool is_a = warp == kLoadA;
+            const int32_t rows = is_a ? kRowsA : p.hb;
+            const int32_t layout = is_a ? p.a_layout : p.b_layout;
+            const uint32_t bytes = 2u * static_cast<uint32_t>(rows) * 128u;   // of both CTAs
             uint32_t f = 0;
             bool ok = true;
             for (int32_t u = pair; u < units && ok; u += n_pairs) {
                 const Unit t = decode(u);
-                const int32_t m0 = t.tm * 256 + static_cast<int32_t>(rank) * kRowsA;
-                const int32_t n0 = kDual ? t.tn * p.hb : t.tn * 2 * p.hb + static_cast<int32_t>(rank) * p.hb;
+                const int32_t r0 = is_a    ? t.tm * 256 + static_cast<int32_t>(rank) * kRowsA
+                                   : kDual ? t.tn * p.hb
+                                           : t.tn * 2 * p.hb + static_cast<int32_t>(rank) * p.hb;
+                const CUtensorMap* map0 = is_a ? &p.a[0] : &p.b[kDual ? rank : t.src];
                 for (int32_t it = t.k0; it < t.k1; ++it, ++f) {
                     const uint32_t s = f % S;
                     if (f >= S && !ptx::mbar_wait(&empty[s], (f / S - 1) & 1, abort_flag)) {
@@ -239,24 +248,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                         ok = false;
                         break;
                     }
-                    const int32_t ks = it >= p.k_iters ? 1 : 0;
-                    const int32_t k = (it - ks * p.k_iters) * kBK;
-                    const CUtensorMap* ma = &p.a[ks];
-                    const CUtensorMap* mb = &p.b[kDual ? rank : p.k_sources == 2 ? ks : t.src];
+                    const bool second = it >= p.k_iters;   // the second source of a sum over two
+                    const int32_t k = (second ? it - p.k_iters : it) * kBK;
+                    const CUtensorMap* map = second ? map0 + 1 : map0;
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], bytes);
                     const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(&full[s]), 0);
-                    const uint32_t sa = smem_base + s * kStage, sb = sa + kStageA;
-                    if (p.a_kmajor) {
-                        ptx::tma_load_2d_pair(sa, ma, k, m0, bar);
+                    const uint32_t dst = smem_base + s * kStage + (is_a ? 0 : kStageA);
+                    if (layout == kLayoutK) {
+                        ptx::tma_load_2d_pair(dst, map, k, r0, bar);
+                    } else if (layout == kLayoutBlocks) {
+                        ptx::tma_load_3d_pair(dst, map, 0, k, r0 >> 6, bar);
                     } else {
-                        ptx::tma_load_2d_pair(sa, ma, m0, k, bar);
-                        ptx::tma_load_2d_pair(sa + 8192, ma, m0 + 64, k, bar);
-                    }
-                    if (p.b_kmajor) {
-                        ptx::tma_load_2d_pair(sb, mb, k, n0, bar);
-                    } else {
-                        ptx::tma_load_2d_pair(sb, mb, n0, k, bar);
-                        if (p.hb > 64) ptx::tma_load_2d_pair(sb + 8192, mb, n0 + 64, k, bar);
+                        ptx::tma_load_2d_pair(dst, map, r0, k, bar);
+                        if (rows > 64) ptx::tma_load_2d_pair(dst + 8192, map, r0 + 64, k, bar);
                     }
                 }
             }
@@ -271,11 +275,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
         // ---------------- MMA issue (the warp runs the loop, lane 0 of CTA 0 issues)
         if (rank == 0) {
             const uint32_t leader = lane == 0;
-            const uint32_t idesc = ptx::idesc_dense(E4M3, p.a_kmajor, p.b_kmajor, 256, static_cast<uint32_t>(2 * p.hb));
-            const uint64_t a0 = p.a_kmajor ? ptx::sdesc_k128(smem_base) : ptx::sdesc_mn128(smem_base, 64);
-            const uint64_t b0 = p.b_kmajor ? ptx::sdesc_k128(smem_base + kStageA) : ptx::sdesc_mn128(smem_base + kStageA, 64);
+            const bool a_k = p.a_layout == kLayoutK, b_k = p.b_layout == kLayoutK;
+            const uint32_t idesc = ptx::idesc_dense(E4M3, a_k, b_k, 256, static_cast<uint32_t>(2 * p.hb));
+            const uint64_t a0 = a_k ? ptx::sdesc_k128(smem_base) : ptx::sdesc_mn128(smem_base, 64);
+            const uint64_t b0 = b_k ? ptx::sdesc_k128(smem_base + kStageA) : ptx::sdesc_mn128(smem_base + kStageA, 64);
             // one MMA contracts 32 bytes of a K-major row, or 16 rows of 128 bytes
-            const uint64_t da = p.a_kmajor ? 2 : 128, db = p.b_kmajor ? 2 : 128;
+            const uint64_t da = a_k ? 2 : 128, db = b_k ? 2 : 128;
             uint32_t f = 0;
             int32_t ai = 0;
             bool ok = true;
@@ -604,6 +609,19 @@ int make_tensor_map(CUtensorMap* map, const void* base, size_t es, int64_t inner
     return r == CUDA_SUCCESS ? SPCONV_OK : SPCONV_ERR_CUDA;
 }
 
+int make_tensor_map_blocks(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld, int32_t blocks) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return SPCONV_ERR_CUDA;
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(outer), static_cast<cuuint64_t>(inner / 64)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, 128};
+    const cuuint32_t box[3] = {64, 64, static_cast<cuuint32_t>(blocks)};
+    const cuuint32_t unit[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, unit,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SPCONV_OK : SPCONV_ERR_CUDA;
+}
+
 int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     const size_t es = op.dtype == SPCONV_E4M3 ? 1 : 2;
     const int32_t bk = static_cast<int32_t>(128 / es);
@@ -612,11 +630,11 @@ int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     p.m = op.m;
     p.n = op.n;
     p.k_iters = static_cast<int32_t>(ceil_div(op.k, bk));
-    p.k_sources = op.k_sources;
     p.k_total = p.k_iters * op.k_sources;
     p.n_sources = op.n_sources;
-    p.a_kmajor = op.a.k_major;
-    p.b_kmajor = op.b.k_major;
+    auto layout = [](const Operand& t, int64_t rows) { return t.k_major ? kLayoutK : rows % 64 == 0 ? kLayoutBlocks : kLayoutRows; };
+    p.a_layout = layout(op.a, op.m);
+    p.b_layout = layout(op.b, op.n);
     p.act = op.act;
     p.has_extra = op.extra != nullptr;
     p.row_scale = op.row_scale;
@@ -647,12 +665,14 @@ int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     p.by_height = FastDiv(kGroupM);
     p.by_last_height = FastDiv(p.tiles_m % kGroupM ? p.tiles_m % kGroupM : kGroupM);
     p.by_tiles_n = FastDiv(static_cast<uint32_t>(p.tiles_n));
-    for (int i = 0; i < (op.k_sources == 2 ? 2 : 1); ++i)
-        SPCONV_CHECK(op.a.k_major ? make_tensor_map(&p.a[i], op.a.p[i], es, op.k, op.m, op.a.ld, kRowsA)
-                                  : make_tensor_map(&p.a[i], op.a.p[i], es, op.m, op.k, op.a.ld, 64));
+    auto operand = [&](CUtensorMap* map, const Operand& t, int i, int32_t lay, int64_t rows, int32_t box) {
+        return lay == kLayoutK      ? make_tensor_map(map, t.p[i], es, op.k, rows, t.ld, box)
+               : lay == kLayoutRows ? make_tensor_map(map, t.p[i], es, rows, op.k, t.ld, 64)
+                                    : make_tensor_map_blocks(map, t.p[i], rows, op.k, t.ld, box / 64);
+    };
+    for (int i = 0; i < op.k_sources; ++i) SPCONV_CHECK(operand(&p.a[i], op.a, i, p.a_layout, op.m, kRowsA));
     for (int i = 0; i < ((dual || op.k_sources == 2 || op.n_sources == 2) ? 2 : 1); ++i)
-        SPCONV_CHECK(op.b.k_major ? make_tensor_map(&p.b[i], op.b.p[i], es, op.k, op.n, op.b.ld, p.hb)
-                                  : make_tensor_map(&p.b[i], op.b.p[i], es, op.n, op.k, op.b.ld, 64));
+        SPCONV_CHECK(operand(&p.b[i], op.b, i, p.b_layout, op.n, p.hb));
     if (p.splits == 1)
         for (int i = 0; i < ((op.epi == kEpiGatedGrad || op.n_sources == 2) ? 2 : 1); ++i)
             SPCONV_CHECK(make_tensor_map(&p.c[i], op.out[i], 2, op.n, op.m, op.ld_out, 32));

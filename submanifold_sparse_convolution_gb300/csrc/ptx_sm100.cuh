@@ -321,6 +321,15 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst_smem, const void* 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst_smem, const void* map, int32_t x, int32_t y, int32_t z,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];" ::"r"(dst_smem),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_store_2d(const void* map, int32_t x, int32_t y, uint32_t src_smem) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
                  "r"(src_smem)
