@@ -14,6 +14,8 @@ __device__ int32_t g_rows_status;   // kStatus* bits of the row-wise operators' 
 template <typename T>
 __global__ void __launch_bounds__(256) k_copy_rows(const T* src, int64_t ld_src, T* dst, int64_t ld_dst, int64_t rows,
                                                    int64_t cols, int64_t row_groups, bool vec_src, bool vec_dst) {
+    pdl_wait();
+    pdl_trigger();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int64_t r = i / row_groups, c = (i - r * row_groups) * 8;
     if (r >= rows) return;
@@ -43,11 +45,13 @@ __global__ void __launch_bounds__(256) k_copy_rows(const T* src, int64_t ld_src,
 // in a fixed order.
 __global__ void __launch_bounds__(1024) k_sum_partials(const float* part, int64_t p, int64_t n, float* out) {
     __shared__ float sh[32][33];
+    pdl_wait();
+    pdl_trigger();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + x;
     float s = 0.0f;
     if (col < n) {
-#pragma unroll 8
+#pragma unroll 16
         for (int64_t i = y; i < p; i += 32) s += part[i * n + col];
     }
     sh[y][x] = s;
@@ -66,6 +70,8 @@ __global__ void __launch_bounds__(256) k_column_sums(const __nv_bfloat16* v, int
                                                      float* part) {
     constexpr int kX = 64 / W, kY = 256 / kX;
     __shared__ float sh[kY][64 + 1];
+    pdl_wait();
+    pdl_trigger();
     const int x = threadIdx.x % kX, y = threadIdx.x / kX;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + x * W;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows, r1 = r0 + rows < m ? r0 + rows : m;
@@ -139,14 +145,12 @@ int copy_rows(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_
     if (blocks > 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
     auto vec = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % (8 * es) == 0 && ld % 8 == 0; };
     const bool vs = vec(src, ld_src), vd = vec(dst, ld_dst);
-    count_launch();
+    const dim3 grid(static_cast<unsigned>(blocks));
     if (es == 1)
-        k_copy_rows<uint8_t><<<static_cast<unsigned>(blocks), 256, 0, s>>>(static_cast<const uint8_t*>(src), ld_src,
-                                                                           static_cast<uint8_t*>(dst), ld_dst, rows, cols, groups, vs, vd);
-    else
-        k_copy_rows<uint16_t><<<static_cast<unsigned>(blocks), 256, 0, s>>>(static_cast<const uint16_t*>(src), ld_src,
-                                                                            static_cast<uint16_t*>(dst), ld_dst, rows, cols, groups, vs, vd);
-    return launch_status();
+        return launch_pdl(k_copy_rows<uint8_t>, grid, 256, 0, s, static_cast<const uint8_t*>(src), ld_src,
+                          static_cast<uint8_t*>(dst), ld_dst, rows, cols, groups, vs, vd);
+    return launch_pdl(k_copy_rows<uint16_t>, grid, 256, 0, s, static_cast<const uint16_t*>(src), ld_src,
+                      static_cast<uint16_t*>(dst), ld_dst, rows, cols, groups, vs, vd);
 }
 
 }  // namespace
@@ -225,9 +229,7 @@ int dense_run(const DenseOp& op, cudaStream_t s) {
 }
 
 int sum_partials(const float* part, int64_t p, int64_t n, float* out, cudaStream_t s) {
-    count_launch();
-    k_sum_partials<<<static_cast<unsigned>(ceil_div(n, 32)), 1024, 0, s>>>(part, p, n, out);
-    return launch_status();
+    return launch_pdl(k_sum_partials, dim3(static_cast<unsigned>(ceil_div(n, 32))), 1024, 0, s, part, p, n, out);
 }
 
 int column_sums(const void* v, int64_t ld, int64_t m, int64_t n, float* out, cudaStream_t s) {
@@ -241,12 +243,8 @@ int column_sums(const void* v, int64_t ld, int64_t m, int64_t n, float* out, cud
     if (part.failed()) return SPCONV_ERR_OOM;
     const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(chunks));
     const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(v);
-    count_launch();
-    if (n % 8 == 0 && ld % 8 == 0 && (reinterpret_cast<uintptr_t>(v) & 15) == 0)
-        k_column_sums<8><<<grid, 256, 0, s>>>(p, ld, m, n, rows, part.as<float>());
-    else
-        k_column_sums<1><<<grid, 256, 0, s>>>(p, ld, m, n, rows, part.as<float>());
-    SPCONV_CHECK(launch_status());
+    const bool vec = n % 8 == 0 && ld % 8 == 0 && (reinterpret_cast<uintptr_t>(v) & 15) == 0;
+    SPCONV_CHECK(launch_pdl(vec ? k_column_sums<8> : k_column_sums<1>, grid, 256, 0, s, p, ld, m, n, rows, part.as<float>()));
     return sum_partials(part.as<float>(), chunks, n, out, s);
 }
 

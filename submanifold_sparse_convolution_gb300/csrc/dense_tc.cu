@@ -190,7 +190,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
     ptx::cluster_sync();
     ptx::tc_fence_after();
     pdl_wait();
-    pdl_trigger();
+    // The next product's blocks may be scheduled as this one's leave the SMs.
+    // The sums that follow partial results may not: their small blocks would
+    // crowd on the SMs that are free first (a weight gradient and its sum of
+    // slices, 15052 x 512 x 512: 22.7 us, against 19.7).
+    if (!p.part) pdl_trigger();
     const uint32_t tmem = *tmem_slot;
     const uint32_t smem_base = ptx::smem_u32(smem);
 
@@ -529,13 +533,20 @@ __global__ void __launch_bounds__(256) k_sum_slices(const float* part, int32_t s
     float s[4] = {};
     const int64_t left = count - i;
     if (left >= 4 && slice % 4 == 0) {
-#pragma unroll 4
-        for (int32_t k = 0; k < splits; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(part + k * slice + i);
-            s[0] += v.x;
-            s[1] += v.y;
-            s[2] += v.z;
-            s[3] += v.w;
+        const float* q = part + i;
+        // eight slices' loads in flight, added in order
+        for (int32_t k = 0; k < splits; k += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int32_t t = 0; t < 8; ++t)
+                v[t] = k + t < splits ? *reinterpret_cast<const float4*>(q + (k + t) * slice) : make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int32_t t = 0; t < 8; ++t) {
+                s[0] += v[t].x;
+                s[1] += v[t].y;
+                s[2] += v[t].z;
+                s[3] += v[t].w;
+            }
         }
     } else {
         for (int32_t k = 0; k < splits; ++k)
@@ -561,16 +572,7 @@ int launch(const TcArgs& args, int32_t pairs, cudaStream_t s) {
                                                TcConfig<EPI>::kSmem));
         set[dev] = true;
     }
-    cudaLaunchAttribute at[1] = {pdl_attr()};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = TcConfig<EPI>::kSmem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    count_launch();
-    return cuda_status(cudaLaunchKernelEx(&cfg, k_dense_tc<EPI, E4M3>, args));
+    return launch_pdl(k_dense_tc<EPI, E4M3>, dim3(static_cast<unsigned>(2 * pairs)), kThreads, TcConfig<EPI>::kSmem, s, args);
 }
 
 }  // namespace
@@ -687,17 +689,9 @@ int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     p.part = part.as<float>();
     if (p.splits > 1) {
         SPCONV_CHECK((launch<kEpiPartial, false>(p, pairs, s)));
-        cudaLaunchAttribute at[1] = {pdl_attr()};
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(slice, 1024)));
-        cfg.blockDim = dim3(256);
-        cfg.stream = s;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        count_launch();
-        return cuda_status(cudaLaunchKernelEx(&cfg, k_sum_slices, static_cast<const float*>(p.part), p.splits, slice, slice,
-                                              op.m, op.n, static_cast<__nv_bfloat16*>(op.out[0]),
-                                              static_cast<__nv_bfloat16*>(op.out[1]), op.ld_out));
+        return launch_pdl(k_sum_slices, dim3(static_cast<unsigned>(ceil_div(slice, 1024))), 256, 0, s,
+                          static_cast<const float*>(p.part), p.splits, slice, slice, op.m, op.n,
+                          static_cast<__nv_bfloat16*>(op.out[0]), static_cast<__nv_bfloat16*>(op.out[1]), op.ld_out);
     }
     const bool eight = op.dtype == SPCONV_E4M3;
     switch (op.epi) {

@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_grad_ring(const NormGradArg
 // Shorter rows, backward: a row per TPR lanes, one warp of the block copies
 // stages of many rows.
 template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(kBlock + 32, VPT > 1 && sizeof(T) == 4 ? 1 : 2) k_rms_norm_grad_lanes(const NormGradArgs a, const Ring g, float* part) {
+__global__ void __launch_bounds__(kBlock + 32, VPT > 2 || (VPT > 1 && sizeof(T) == 4) ? 1 : 2) k_rms_norm_grad_lanes(const NormGradArgs a, const Ring g, float* part) {
     constexpr int kGroups = kBlock / TPR, kCols = TPR * VPT * 8;
     extern __shared__ __align__(128) uint8_t smem[];
     RingState<T, 3> ring;
@@ -803,20 +803,9 @@ bool vec_ok(const void* p, int64_t ld, size_t elem) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * static_cast<int64_t>(elem)) % 16 == 0;
 }
 
-// Launches with programmatic dependent launch: each kernel waits (pdl_wait)
-// before its first read of what an earlier one wrote.
 template <typename... K, typename... A>
 int launch(void (*kernel)(K...), int64_t blocks, int threads, size_t smem, cudaStream_t s, A... args) {
-    cudaLaunchAttribute at[1] = {pdl_attr()};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    count_launch();
-    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), threads, smem, s, args...);
 }
 
 constexpr int64_t kSms = 152;
@@ -916,11 +905,11 @@ int backward_t(const NormGradArgs& a, cudaStream_t s) {
     if constexpr (kVec) {
         Ring g;
         size_t smem;
-        if (a.c <= 512)
-            return with_lanes<false>(a.c, [&](auto tpr, auto vpt) {
+        if (a.c <= (sizeof(T) == 2 ? 1024 : 512))
+            return with_lanes<sizeof(T) == 2>(a.c, [&](auto tpr, auto vpt) {
                 // stages of 8 KB per input at least, so that barriers are few
                 const int64_t unit = kBlock / tpr, row = static_cast<int64_t>(a.c) * sizeof(T);
-                int per_sm = 2;
+                int per_sm = vpt > 2 ? 1 : 2;
                 SPCONV_CHECK(make_ring(&g, &smem, a.c, sizeof(T), 3, unit * ceil_div(8192, unit * row), &per_sm));
                 const int64_t tiles = ceil_div(a.n, g.rows), most = kSms * per_sm, blocks = tiles < most ? tiles : most;
                 return with_part(blocks, [&](float* part) {

@@ -130,6 +130,22 @@ private:
     bool failed_ = false;
 };
 
+// Launches a kernel with programmatic dependent launch: it calls pdl_wait()
+// before its first access to what an earlier kernel wrote or reads.
+template <typename... K, typename... A>
+int launch_pdl(void (*kernel)(K...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute at[1] = {pdl_attr()};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    count_launch();
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int launch_status() { return cuda_status(cudaGetLastError()); }
