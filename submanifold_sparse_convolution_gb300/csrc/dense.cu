@@ -41,33 +41,91 @@ __global__ void __launch_bounds__(256) k_copy_rows(const T* src, int64_t ld_src,
 }
 
 // ---- column sums ----------------------------------------------------------------
-// 32 columns per block, 32 threads down each column, added through shared memory
-// in a fixed order.
-__global__ void __launch_bounds__(1024) k_sum_partials(const float* part, int64_t p, int64_t n, float* out) {
-    __shared__ float sh[32][33];
+// The sums that are left after partial results, by block: slices of the first
+// product, of the second, then columns.
+struct FinishArgs {
+    SliceSums slices[2];
+    ColumnSums cols;
+    int32_t blocks[2];   // of each product's slices
+};
+
+constexpr int kFinishCols = 8;   // columns of a block, 32 threads down each
+
+__device__ __forceinline__ void sum_slices(const SliceSums& a, int32_t block) {
+    const int64_t mn = a.m * a.n, slice = mn * a.outputs;
+    const int64_t i = (static_cast<int64_t>(block) * 256 + threadIdx.x) * 4;
+    if (i >= slice) return;
+    if (a.n % 4 == 0) {   // four elements of one row
+        float s[4] = {};
+        const float* q = a.part + i;
+        // eight slices' loads in flight, added in order
+        for (int32_t k = 0; k < a.splits; k += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int32_t t = 0; t < 8; ++t)
+                v[t] = k + t < a.splits ? *reinterpret_cast<const float4*>(q + (k + t) * slice) : make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int32_t t = 0; t < 8; ++t) {
+                s[0] += v[t].x;
+                s[1] += v[t].y;
+                s[2] += v[t].z;
+                s[3] += v[t].w;
+            }
+        }
+        const int src = i >= mn;
+        const int64_t r = i - (src ? mn : 0);
+        const int64_t row = slice < 0x7FFFFFFF ? static_cast<uint32_t>(r) / static_cast<uint32_t>(a.n) : r / a.n;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(s[0], s[1]), hi = __floats2bfloat162_rn(s[2], s[3]);
+        // (rows of the output are 16-byte aligned: tma_ok)
+        *reinterpret_cast<uint2*>(a.out[src] + row * a.ld + (r - row * a.n)) =
+            make_uint2(reinterpret_cast<const uint32_t&>(lo), reinterpret_cast<const uint32_t&>(hi));
+    } else {
+        for (int64_t e = i; e < i + 4 && e < slice; ++e) {
+            float s = 0.0f;
+            for (int32_t k = 0; k < a.splits; ++k) s += a.part[k * slice + e];
+            const int src = e >= mn;
+            const int64_t r = e - (src ? mn : 0), row = r / a.n;
+            a.out[src][row * a.ld + (r - row * a.n)] = __float2bfloat16_rn(s);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) k_finish(const FinishArgs a) {
+    __shared__ float sh[32][kFinishCols + 1];
     pdl_wait();
     pdl_trigger();
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + x;
+    int32_t b = static_cast<int32_t>(blockIdx.x);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        if (b < a.blocks[g]) {
+            sum_slices(a.slices[g], b);
+            return;
+        }
+        b -= a.blocks[g];
+    }
+    const int x = threadIdx.x % kFinishCols, y = threadIdx.x / kFinishCols;
+    const int64_t col = static_cast<int64_t>(b) * kFinishCols + x;
     float s = 0.0f;
-    if (col < n) {
+    if (col < a.cols.n) {
 #pragma unroll 16
-        for (int64_t i = y; i < p; i += 32) s += part[i * n + col];
+        for (int64_t i = y; i < a.cols.rows; i += 32) s += a.cols.part[i * a.cols.n + col];
     }
     sh[y][x] = s;
     __syncthreads();
-    float v = sh[x][y];   // thread (x, y) now holds part x of column y
+    // a warp per column adds its 32 parts
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float v = sh[lane][warp];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + y;
-    if (x == 0 && c < n) out[c] = v;
+    const int64_t c = static_cast<int64_t>(b) * kFinishCols + warp;
+    if (lane == 0 && c < a.cols.n) a.cols.out[c] = v;
 }
 
 // One row of partial sums per block of `rows` rows: 64 columns, 8 per thread
 // (W = 8: one 16-byte load) or one (W = 1).
 template <int W>
-__global__ void __launch_bounds__(256) k_column_sums(const __nv_bfloat16* v, int64_t ld, int64_t m, int64_t n, int64_t rows,
-                                                     float* part) {
+__global__ void __launch_bounds__(256) k_column_parts(const __nv_bfloat16* v, int64_t ld, int64_t m, int64_t n, int64_t rows,
+                                                      float* part) {
     constexpr int kX = 64 / W, kY = 256 / kX;
     __shared__ float sh[kY][64 + 1];
     pdl_wait();
@@ -169,17 +227,44 @@ int rows_status_word(int32_t** word) {
     return SPCONV_OK;
 }
 
-int dense_run(const DenseOp& op, cudaStream_t s) {
-    if (op.m == 0 || op.n == 0) return SPCONV_OK;
-    int32_t* status = nullptr;
-    SPCONV_CHECK(rows_status_word(&status));
-    // The tensor maps need 16-byte aligned rows.  Matrices without them (odd
-    // channel counts, strides or addresses) are copied to rows that have them,
-    // and such an output is copied back: one extra pass over that matrix.
-    const size_t es = op.dtype == SPCONV_E4M3 ? 1 : 2;
-    const bool dual = op.epi == kEpiGated || op.epi == kEpiGatedGrad;
-    const int na = op.k_sources, nb = dual || op.k_sources == 2 || op.n_sources == 2 ? 2 : 1;
-    const int nc = op.epi == kEpiGatedGrad || op.n_sources == 2 ? 2 : 1;
+namespace {
+
+// The tensor maps need 16-byte aligned rows.  Matrices without them (odd
+// channel counts, strides or addresses) are copied to rows that have them, and
+// such an output is copied back: one extra pass over that matrix.
+class AlignedOp {
+public:
+    DenseOp op;   // what to run between begin and end
+
+    int begin(const DenseOp& given, cudaStream_t s) {
+        given_ = op = given;
+        const size_t es = op.dtype == SPCONV_E4M3 ? 1 : 2;
+        const bool dual = op.epi == kEpiGated || op.epi == kEpiGatedGrad;
+        const int na = op.k_sources, nb = dual || op.k_sources == 2 || op.n_sources == 2 ? 2 : 1;
+        outs_ = op.epi == kEpiGatedGrad || op.n_sources == 2 ? 2 : 1;
+        const Matrix a = op.a.k_major ? plan(op.a.p, na, op.a.ld, op.m, op.k, es) : plan(op.a.p, na, op.a.ld, op.k, op.m, es);
+        const Matrix b = op.b.k_major ? plan(op.b.p, nb, op.b.ld, op.n, op.k, es) : plan(op.b.p, nb, op.b.ld, op.k, op.n, es);
+        const Matrix x = plan(&op.extra, op.extra ? 1 : 0, op.ld_extra, op.m, op.n, 2);
+        const Matrix c = plan(op.out, outs_, op.ld_out, op.m, op.n, 2);
+        copy_back_ = c.move;
+        if (bytes_ == 0) return SPCONV_OK;
+        if (!buf_.alloc(bytes_, s)) return SPCONV_ERR_OOM;
+        SPCONV_CHECK(bring(a, op.a.p, na, &op.a.ld, s));
+        SPCONV_CHECK(bring(b, op.b.p, nb, &op.b.ld, s));
+        SPCONV_CHECK(bring(x, &op.extra, 1, &op.ld_extra, s));
+        if (c.move) {
+            for (int i = 0; i < outs_; ++i) op.out[i] = buf_.as<void>(c.off[i]);
+            op.ld_out = c.ld();
+        }
+        return SPCONV_OK;
+    }
+    int end(cudaStream_t s) const {
+        for (int i = 0; copy_back_ && i < outs_; ++i)
+            SPCONV_CHECK(copy_rows(op.out[i], op.ld_out, given_.out[i], given_.ld_out, op.m, op.n, 2, s));
+        return SPCONV_OK;
+    }
+
+private:
     struct Matrix {   // up to two matrices of one shape
         int64_t rows, cols;
         size_t es;
@@ -187,65 +272,96 @@ int dense_run(const DenseOp& op, cudaStream_t s) {
         size_t off[2];
         int64_t ld() const { return static_cast<int64_t>(round_up(static_cast<size_t>(cols), 16 / es)); }
     };
-    size_t bytes = 0;
-    auto plan = [&](const void* const* ptr, int count, int64_t ld, int64_t rows, int64_t cols, size_t e) {
+    Matrix plan(const void* const* ptr, int count, int64_t ld, int64_t rows, int64_t cols, size_t e) {
         Matrix t{rows, cols, e, false, {0, 0}};
         for (int i = 0; i < count; ++i) t.move = t.move || !tma_ok(ptr[i], ld, e);
         for (int i = 0; t.move && i < count; ++i) {
-            t.off[i] = bytes;
-            bytes += round_up(static_cast<size_t>(rows) * t.ld() * e, 256);
+            t.off[i] = bytes_;
+            bytes_ += round_up(static_cast<size_t>(rows) * t.ld() * e, 256);
         }
         return t;
-    };
-    const Matrix ma = op.a.k_major ? plan(op.a.p, na, op.a.ld, op.m, op.k, es) : plan(op.a.p, na, op.a.ld, op.k, op.m, es);
-    const Matrix mb = op.b.k_major ? plan(op.b.p, nb, op.b.ld, op.n, op.k, es) : plan(op.b.p, nb, op.b.ld, op.k, op.n, es);
-    const Matrix mx = plan(&op.extra, op.extra ? 1 : 0, op.ld_extra, op.m, op.n, 2);
-    const Matrix mc = plan(op.out, nc, op.ld_out, op.m, op.n, 2);
-    auto run = [&](const DenseOp& o) { return dense_few_takes(o) ? dense_few_run(o, status, s) : dense_tc_run(o, status, s); };
-    if (bytes == 0) return run(op);
-    Scratch buf(bytes, s);
-    if (buf.failed()) return SPCONV_ERR_OOM;
-    DenseOp o = op;
-    auto bring = [&](const Matrix& t, const void** ptr, int count, int64_t* ld) -> int {
+    }
+    int bring(const Matrix& t, const void** ptr, int count, int64_t* ld, cudaStream_t s) {
         if (!t.move) return SPCONV_OK;
         for (int i = 0; i < count; ++i) {
-            SPCONV_CHECK(copy_rows(ptr[i], *ld, buf.as<void>(t.off[i]), t.ld(), t.rows, t.cols, t.es, s));
-            ptr[i] = buf.as<void>(t.off[i]);
+            SPCONV_CHECK(copy_rows(ptr[i], *ld, buf_.as<void>(t.off[i]), t.ld(), t.rows, t.cols, t.es, s));
+            ptr[i] = buf_.as<void>(t.off[i]);
         }
         *ld = t.ld();
         return SPCONV_OK;
-    };
-    SPCONV_CHECK(bring(ma, o.a.p, na, &o.a.ld));
-    SPCONV_CHECK(bring(mb, o.b.p, nb, &o.b.ld));
-    SPCONV_CHECK(bring(mx, &o.extra, 1, &o.ld_extra));
-    if (mc.move) {
-        for (int i = 0; i < nc; ++i) o.out[i] = buf.as<void>(mc.off[i]);
-        o.ld_out = mc.ld();
     }
-    SPCONV_CHECK(run(o));
-    for (int i = 0; mc.move && i < nc; ++i)
-        SPCONV_CHECK(copy_rows(o.out[i], o.ld_out, op.out[i], op.ld_out, op.m, op.n, 2, s));
+
+    DenseOp given_;
+    Scratch buf_;
+    size_t bytes_ = 0;
+    int outs_ = 1;
+    bool copy_back_ = false;
+};
+
+}  // namespace
+
+int dense_run(const DenseOp& op, cudaStream_t s) {
+    if (op.m == 0 || op.n == 0) return SPCONV_OK;
+    int32_t* status = nullptr;
+    SPCONV_CHECK(rows_status_word(&status));
+    AlignedOp a;
+    SPCONV_CHECK(a.begin(op, s));
+    SPCONV_CHECK(dense_few_takes(a.op) ? dense_few_run(a.op, status, s)
+                 : a.op.plain()        ? dense_tc_plain(&a.op, 1, {}, status, s)
+                                       : dense_tc_run(a.op, status, s));
+    return a.end(s);
+}
+
+int dense_run_plain(const DenseOp* ops, int count, const ColumnSums& cols, cudaStream_t s) {
+    if (count == 0) return cols.out ? finish_sums(nullptr, 0, cols, s) : SPCONV_OK;
+    int32_t* status = nullptr;
+    SPCONV_CHECK(rows_status_word(&status));
+    AlignedOp a[2];
+    DenseOp o[2];
+    for (int i = 0; i < count; ++i) {
+        SPCONV_CHECK(a[i].begin(ops[i], s));
+        o[i] = a[i].op;
+    }
+    SPCONV_CHECK(dense_tc_plain(o, count, cols, status, s));
+    for (int i = 0; i < count; ++i) SPCONV_CHECK(a[i].end(s));
     return SPCONV_OK;
 }
 
-int sum_partials(const float* part, int64_t p, int64_t n, float* out, cudaStream_t s) {
-    return launch_pdl(k_sum_partials, dim3(static_cast<unsigned>(ceil_div(n, 32))), 1024, 0, s, part, p, n, out);
+int finish_sums(const SliceSums* slices, int count, const ColumnSums& cols, cudaStream_t s) {
+    FinishArgs a = {};
+    int64_t blocks = 0;
+    for (int i = 0; i < count; ++i) {
+        a.slices[i] = slices[i];
+        const int64_t b = slices[i].splits ? ceil_div(slices[i].m * slices[i].n * slices[i].outputs, 1024) : 0;
+        if (b > 0x3FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
+        a.blocks[i] = static_cast<int32_t>(b);
+        blocks += b;
+    }
+    if (cols.out) {
+        a.cols = cols;
+        blocks += ceil_div(cols.n, kFinishCols);
+    }
+    if (blocks == 0) return SPCONV_OK;
+    return launch_pdl(k_finish, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a);
 }
 
-int column_sums(const void* v, int64_t ld, int64_t m, int64_t n, float* out, cudaStream_t s) {
-    const int64_t bx = ceil_div(n, 64);
-    // about eight blocks per SM, each of 64 rows at least
-    int64_t chunks = ceil_div(8 * 152, bx);
+namespace {
+// about eight blocks per SM, each of 64 rows at least
+int64_t column_chunk(int64_t m, int64_t n) {
+    int64_t chunks = ceil_div(8 * 152, ceil_div(n, 64));
     if (chunks > ceil_div(m, 64)) chunks = ceil_div(m, 64);
-    if (chunks < 1) chunks = 1;
-    const int64_t rows = ceil_div(m, chunks);
-    Scratch part(static_cast<size_t>(chunks) * n * 4, s);
-    if (part.failed()) return SPCONV_ERR_OOM;
-    const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(chunks));
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(v);
+    return ceil_div(m, chunks < 1 ? 1 : chunks);
+}
+}  // namespace
+
+int64_t column_part_rows(int64_t m, int64_t n) { return ceil_div(m, column_chunk(m, n)); }
+
+int column_parts(const void* v, int64_t ld, int64_t m, int64_t n, float* part, cudaStream_t s) {
+    const int64_t rows = column_chunk(m, n);
+    const dim3 grid(static_cast<unsigned>(ceil_div(n, 64)), static_cast<unsigned>(ceil_div(m, rows)));
     const bool vec = n % 8 == 0 && ld % 8 == 0 && (reinterpret_cast<uintptr_t>(v) & 15) == 0;
-    SPCONV_CHECK(launch_pdl(vec ? k_column_sums<8> : k_column_sums<1>, grid, 256, 0, s, p, ld, m, n, rows, part.as<float>()));
-    return sum_partials(part.as<float>(), chunks, n, out, s);
+    return launch_pdl(vec ? k_column_parts<8> : k_column_parts<1>, grid, 256, 0, s, static_cast<const __nv_bfloat16*>(v), ld, m, n,
+                      rows, part);
 }
 
 int quantize_weight(const void* w, int32_t c_in, int32_t c_out, void* q, float* scale, cudaStream_t s) {

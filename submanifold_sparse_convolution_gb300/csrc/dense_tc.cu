@@ -47,7 +47,7 @@ constexpr int kTmemCols = 512;
 constexpr int kGroupM = 16;                   // row tiles that share the column tiles in L2
 constexpr int kPairs = 76;                    // CTA pairs of a full GPU
 
-constexpr int32_t kEpiPartial = 4;            // fp32 sums of one slice of K, to a workspace
+constexpr int32_t kEpiPlain = 4;              // the sums, rounded; or, of one slice of K, fp32 to a workspace
 
 // x / d for 0 <= x < 2^31, without a division: x m / 2^(31 + s) with
 // s = ceil(log2 d) and m = ceil(2^(31 + s) / d).
@@ -83,7 +83,22 @@ struct TcArgs {
     const float* col_scale[2];
     const float* bias;
     float* part;           // kEpiActGrad: column sums of 32 rows each, [8 tiles_m][n], or null;
-                           // kEpiPartial: [splits][n_sources][m][n]
+                           // kEpiPlain: with splits > 1, [splits][n_sources][m][n]
+    int32_t tiles, units;  // of the product; tiles splits
+};
+
+// A launch: one product, or two plain ones.  The units (tile, slice of K) of
+// the first come before those of the second, and CTA pairs take them in turn.
+// Where the first product's last turn is short, the pairs without a unit in it
+// take `rounds` units of the second instead (about as long), and the others
+// follow.
+template <int EPI>
+struct TcLaunch {
+    static constexpr int kMax = EPI == kEpiPlain ? 2 : 1;
+    TcArgs g[kMax];
+    int32_t count;
+    int32_t late, rounds;  // first pair without a unit in the short turn (0: none is short)
+    int32_t trigger;       // whether the next kernel may be scheduled early
     int32_t* status;
 };
 
@@ -143,10 +158,11 @@ __device__ __forceinline__ void load_columns(float (&f)[CW], const float* v, int
 }
 
 template <int EPI, bool E4M3>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense_tc(const __grid_constant__ TcArgs p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense_tc(const __grid_constant__ TcLaunch<EPI> L) {
     using Cfg = TcConfig<EPI>;
     constexpr int S = Cfg::kStages;
     constexpr bool kDual = EPI == kEpiGated || EPI == kEpiGatedGrad;
+    constexpr bool kExtra = EPI != kEpiGated && EPI != kEpiPlain;
     constexpr int kBK = E4M3 ? 128 : 64;      // K elements of a stage
     constexpr int CW = 16;                    // accumulator columns a thread takes at once
     extern __shared__ uint8_t smem_raw[];
@@ -178,9 +194,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
         for (int w = 0; w < kEpiPairs; ++w) ptx::mbar_init(&extra_full[w], 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
-        ptx::prefetch_map(&p.a[0]);
-        ptx::prefetch_map(&p.b[0]);
-        ptx::prefetch_map(&p.c[0]);
+        ptx::prefetch_map(&L.g[0].a[0]);
+        ptx::prefetch_map(&L.g[0].b[0]);
     }
     if (warp == 1) {
         ptx::tmem_alloc_pair(tmem_slot, kTmemCols);
@@ -194,28 +209,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
     // The sums that follow partial results may not: their small blocks would
     // crowd on the SMs that are free first (a weight gradient and its sum of
     // slices, 15052 x 512 x 512: 22.7 us, against 19.7).
-    if (!p.part) pdl_trigger();
+    if (L.trigger) pdl_trigger();
     const uint32_t tmem = *tmem_slot;
     const uint32_t smem_base = ptx::smem_u32(smem);
 
     auto fail = [&]() {
-        atomicOr(p.status, kStatusTimeout);
+        atomicOr(L.status, kStatusTimeout);
         *abort_flag = 1;
     };
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xFFFFFFFFu, ptx::mbar_wait(bar, parity, abort_flag));
     };
-    const int32_t tiles_nn = p.tiles_n * p.n_sources;
-    const int32_t tiles = p.tiles_m * tiles_nn;
-    const int32_t units = tiles * p.splits;
     const int32_t pair = static_cast<int32_t>(blockIdx.x >> 1), n_pairs = static_cast<int32_t>(gridDim.x >> 1);
     struct Unit {
-        int32_t tm, tn, src, k0, k1, split;
+        int32_t g, tm, tn, src, k0, k1, split;
     };
-    auto decode = [&](int32_t u) {
-        Unit t;
+    // The k-th unit of this pair; false past its last one.
+    const int32_t mine0 = (L.g[0].units - pair + n_pairs - 1) / n_pairs;   // its units of the first product
+    auto unit_at = [&](int32_t k, Unit& t) -> bool {
+        int32_t u;
+        if (k < mine0) {
+            t.g = 0;
+            u = pair + k * n_pairs;
+        } else {
+            if (EPI != kEpiPlain || L.count == 1) return false;
+            t.g = 1;
+            k -= mine0;
+            const int32_t idle = n_pairs - L.late, ahead = L.rounds * idle;   // (late = 0: rounds = 0)
+            if (pair < L.late || L.rounds == 0) u = ahead + pair + k * n_pairs;
+            else u = k < L.rounds ? pair - L.late + k * idle : ahead + pair + (k - L.rounds) * n_pairs;
+            if (u >= L.g[TcLaunch<EPI>::kMax - 1].units) return false;
+        }
+        const TcArgs& p = L.g[EPI == kEpiPlain ? t.g : 0];
+        const int32_t tiles_nn = p.tiles_n * p.n_sources;
         t.split = p.by_tiles(u);
-        const int32_t i = u - t.split * tiles;
+        const int32_t i = u - t.split * p.tiles;
         const int32_t grp = p.by_group(i);
         const int32_t first = grp * kGroupM;
         const int32_t r = i - grp * kGroupM * tiles_nn;
@@ -227,20 +255,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
         t.tn = nn - t.src * p.tiles_n;
         t.k0 = t.split * p.split_iters;
         t.k1 = t.k0 + p.split_iters < p.k_total ? t.k0 + p.split_iters : p.k_total;
-        return t;
+        return true;
     };
+    auto args_of = [&](const Unit& t) -> const TcArgs& { return L.g[EPI == kEpiPlain ? t.g : 0]; };
 
     if (warp == kLoadA || warp == kLoadB) {
         // ---------------- loads of one operand
         if (lane == 0) {
             const bool is_a = warp == kLoadA;
-            const int32_t rows = is_a ? kRowsA : p.hb;
-            const int32_t layout = is_a ? p.a_layout : p.b_layout;
-            const uint32_t bytes = 2u * static_cast<uint32_t>(rows) * 128u;   // of both CTAs
             uint32_t f = 0;
             bool ok = true;
-            for (int32_t u = pair; u < units && ok; u += n_pairs) {
-                const Unit t = decode(u);
+            Unit t;
+            for (int32_t q = 0; ok && unit_at(q, t); ++q) {
+                const TcArgs& p = args_of(t);
+                const int32_t rows = is_a ? kRowsA : p.hb;
+                const int32_t layout = is_a ? p.a_layout : p.b_layout;
+                const uint32_t bytes = 2u * static_cast<uint32_t>(rows) * 128u;   // of both CTAs
                 const int32_t r0 = is_a    ? t.tm * 256 + static_cast<int32_t>(rank) * kRowsA
                                    : kDual ? t.tn * p.hb
                                            : t.tn * 2 * p.hb + static_cast<int32_t>(rank) * p.hb;
@@ -279,17 +309,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
         // ---------------- MMA issue (the warp runs the loop, lane 0 of CTA 0 issues)
         if (rank == 0) {
             const uint32_t leader = lane == 0;
-            const bool a_k = p.a_layout == kLayoutK, b_k = p.b_layout == kLayoutK;
-            const uint32_t idesc = ptx::idesc_dense(E4M3, a_k, b_k, 256, static_cast<uint32_t>(2 * p.hb));
-            const uint64_t a0 = a_k ? ptx::sdesc_k128(smem_base) : ptx::sdesc_mn128(smem_base, 64);
-            const uint64_t b0 = b_k ? ptx::sdesc_k128(smem_base + kStageA) : ptx::sdesc_mn128(smem_base + kStageA, 64);
-            // one MMA contracts 32 bytes of a K-major row, or 16 rows of 128 bytes
-            const uint64_t da = a_k ? 2 : 128, db = b_k ? 2 : 128;
             uint32_t f = 0;
-            int32_t ai = 0;
             bool ok = true;
-            for (int32_t u = pair; u < units && ok; u += n_pairs, ++ai) {
-                const Unit t = decode(u);
+            Unit t;
+            for (int32_t ai = 0; ok && unit_at(ai, t); ++ai) {
+                const TcArgs& p = args_of(t);
+                const bool a_k = p.a_layout == kLayoutK, b_k = p.b_layout == kLayoutK;
+                const uint32_t idesc = ptx::idesc_dense(E4M3, a_k, b_k, 256, static_cast<uint32_t>(2 * p.hb));
+                const uint64_t a0 = a_k ? ptx::sdesc_k128(smem_base) : ptx::sdesc_mn128(smem_base, 64);
+                const uint64_t b0 = b_k ? ptx::sdesc_k128(smem_base + kStageA) : ptx::sdesc_mn128(smem_base + kStageA, 64);
+                // one MMA contracts 32 bytes of a K-major row, or 16 rows of 128 bytes
+                const uint64_t da = a_k ? 2 : 128, db = b_k ? 2 : 128;
                 const int buf = ai & 1;
                 const uint32_t v = static_cast<uint32_t>(ai >> 1);
                 if (v > 0 && !warp_wait(&acc_empty[buf], (v - 1) & 1)) {
@@ -319,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
             // exit_bar flips; TMEM is freed after that
             ptx::mma_commit_pair_if(leader, exit_bar);
             const bool done = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(exit_bar, 0, nullptr));
-            if (!done && lane == 0) atomicOr(p.status, kStatusTimeout);
+            if (!done && lane == 0) atomicOr(L.status, kStatusTimeout);
         }
     } else {
         // ---------------- epilogue
@@ -338,12 +368,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
         uint64_t* xbar = &extra_full[pair_of];
         uint32_t xphase = 0;
         const uint32_t acc_bar = ptx::map_to_rank(ptx::smem_u32(&acc_empty[0]), 0);
-        const int chunks = (kDual ? p.hb : 2 * p.hb) / 64;
         const bool lead = sub == 0 && lane == 0;
-        int32_t ai = 0;
         bool ok = true;
-        for (int32_t u = pair; u < units; u += n_pairs, ++ai) {
-            const Unit t = decode(u);
+        Unit t;
+        for (int32_t ai = 0; unit_at(ai, t); ++ai) {
+            const TcArgs& p = args_of(t);
+            const int chunks = (kDual ? p.hb : 2 * p.hb) / 64;
+            const bool to_part = EPI == kEpiPlain && p.part;   // fp32 sums of a slice, not staged
             const int buf = ai & 1;
             const int32_t m0 = t.tm * 256 + static_cast<int32_t>(rank) * kRowsA + quarter * 32;
             const int64_t row = m0 + lane;
@@ -364,11 +395,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
             for (int c = half; c < chunks; c += 2) {
                 const int32_t n0 = col0 + c * 64;
                 if (!(rows_live && n0 < p.n)) continue;   // (the same for both warps of a pair)
-                if (EPI != kEpiPartial) {
+                if (!to_part) {
                     // the staging buffer is free once its last store has been read out
                     if (lead) {
                         ptx::bulk_wait_read();
-                        if (EPI != kEpiGated && p.has_extra) {
+                        if (kExtra && p.has_extra) {
                             ptx::mbar_arrive_expect_tx(xbar, kStaging);
                             ptx::tma_load_2d(st0, &p.x, n0, m0, ptx::smem_u32(xbar));
                         }
@@ -376,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                     ptx::named_barrier_sync(meet, 64);
                 }
                 wait_acc();
-                if (EPI != kEpiPartial && EPI != kEpiGated && p.has_extra) {
+                if (kExtra && p.has_extra) {
                     // (also after a failed wait: the copy must land before the CTA exits)
                     if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(xbar, xphase, nullptr))) {
                         if (lane == 0) fail();
@@ -395,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                     ptx::tmem_ld_wait();
                     const int32_t nc = n0 + sub * 32 + h * CW;
                     const uint32_t piece = sub * 4 + h * (CW / 8);   // first 16-byte piece of these columns in a row
-                    if (EPI == kEpiPartial) {
+                    if (to_part) {
                         if (row_live) {
                             float* dst = p.part + ((static_cast<int64_t>(t.split) * p.n_sources + t.src) * p.m + row) * p.n + nc;
                             if (p.n % 4 == 0) {
@@ -413,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                     }
                     // extra: this thread's CW columns, 16-byte pieces in the 128-byte swizzle
                     uint32_t x[CW / 2];
-                    if (EPI != kEpiGated) {
+                    if (kExtra) {
 #pragma unroll
                         for (int q = 0; q < CW / 8; ++q) {
                             uint4 v = make_uint4(0, 0, 0, 0);
@@ -435,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                             for (int j = 0; j < CW; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * (rs * f[j]));
                         }
                     }
-                    if (!kDual && p.bias) {
+                    if (EPI != kEpiPlain && !kDual && p.bias) {
                         float f[CW];
                         load_columns(f, p.bias, nc, p.n);
 #pragma unroll
@@ -443,14 +474,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                     }
                     // the results take the places of what they are made of: y in z, the
                     // second output in w
-                    with_act(p.act, [&](auto act) {
+                    if (EPI != kEpiPlain) with_act(p.act, [&](auto act) {
 #pragma unroll
                         for (int j = 0; j < CW; ++j) {
                             const float zz = __uint_as_float(z[j]);
                             const float ww = kDual ? __uint_as_float(w[j]) : 0.0f;
-                            const float xx = EPI == kEpiGated
-                                                 ? 0.0f
-                                                 : __uint_as_float(j & 1 ? (x[j / 2] & 0xFFFF0000u) : (x[j / 2] << 16));
+                            const float xx = kExtra ? __uint_as_float(j & 1 ? (x[j / 2] & 0xFFFF0000u) : (x[j / 2] << 16)) : 0.0f;
                             float y;
                             if (EPI == kEpiLinear) {
                                 y = act_f<act>(zz) + xx;
@@ -483,11 +512,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                         }
                     }
                 }
-                if (EPI != kEpiPartial) {
+                if (!to_part) {
                     ptx::fence_proxy_async_smem();
                     ptx::named_barrier_sync(meet, 64);
                     if (lead) {
-                        ptx::tma_store_2d(&p.c[EPI == kEpiLinear ? t.src : 0], n0, m0, st0);
+                        ptx::tma_store_2d(&p.c[EPI == kEpiPlain ? t.src : 0], n0, m0, st0);
                         if (EPI == kEpiGatedGrad) ptx::tma_store_2d(&p.c[1], n0, m0, st0 + kStaging);
                         ptx::bulk_commit();
                     }
@@ -515,54 +544,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
     // CTA 0's MMAs send it
     ptx::tc_fence_before();
     ptx::cluster_sync();
-    if (warp == 1 && rank == 1 && !ptx::mbar_wait(exit_bar, 0, nullptr)) atomicOr(p.status, kStatusTimeout);
+    if (warp == 1 && rank == 1 && !ptx::mbar_wait(exit_bar, 0, nullptr)) atomicOr(L.status, kStatusTimeout);
     __syncwarp();
     ptx::cluster_sync();
     ptx::tc_fence_after();
     if (warp == 1) ptx::tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-// out = bf16(sum over the slices of K), a fixed order.
-__global__ void __launch_bounds__(256) k_sum_slices(const float* part, int32_t splits, int64_t slice, int64_t count, int64_t m,
-                                                    int64_t n, __nv_bfloat16* out0, __nv_bfloat16* out1, int64_t ld) {
-    pdl_wait();
-    pdl_trigger();
-    // four elements of one source and row per thread when n allows
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-    if (i >= count) return;
-    float s[4] = {};
-    const int64_t left = count - i;
-    if (left >= 4 && slice % 4 == 0) {
-        const float* q = part + i;
-        // eight slices' loads in flight, added in order
-        for (int32_t k = 0; k < splits; k += 8) {
-            float4 v[8];
-#pragma unroll
-            for (int32_t t = 0; t < 8; ++t)
-                v[t] = k + t < splits ? *reinterpret_cast<const float4*>(q + (k + t) * slice) : make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int32_t t = 0; t < 8; ++t) {
-                s[0] += v[t].x;
-                s[1] += v[t].y;
-                s[2] += v[t].z;
-                s[3] += v[t].w;
-            }
-        }
-    } else {
-        for (int32_t k = 0; k < splits; ++k)
-            for (int j = 0; j < 4; ++j)
-                if (j < left) s[j] += part[k * slice + i + j];
-    }
-    for (int j = 0; j < 4; ++j) {
-        if (j >= left) break;
-        const int64_t src = (i + j) / (m * n), r = (i + j) % (m * n);
-        (src ? out1 : out0)[r / n * ld + r % n] = __float2bfloat16_rn(s[j]);
-    }
-}
-
 // ---- host -------------------------------------------------------------------
 template <int EPI, bool E4M3>
-int launch(const TcArgs& args, int32_t pairs, cudaStream_t s) {
+int launch(const TcLaunch<EPI>& args, int64_t units, cudaStream_t s) {
     static bool set[kMaxDevices] = {};
     int dev = 0;
     SPCONV_CHECK_CUDA(cudaGetDevice(&dev));
@@ -572,7 +563,8 @@ int launch(const TcArgs& args, int32_t pairs, cudaStream_t s) {
                                                TcConfig<EPI>::kSmem));
         set[dev] = true;
     }
-    return launch_pdl(k_dense_tc<EPI, E4M3>, dim3(static_cast<unsigned>(2 * pairs)), kThreads, TcConfig<EPI>::kSmem, s, args);
+    const unsigned pairs = static_cast<unsigned>(units < kPairs ? units : kPairs);
+    return launch_pdl(k_dense_tc<EPI, E4M3>, dim3(2 * pairs), kThreads, TcConfig<EPI>::kSmem, s, args);
 }
 
 }  // namespace
@@ -624,11 +616,15 @@ int make_tensor_map_blocks(CUtensorMap* map, const void* base, int64_t inner, in
     return r == CUDA_SUCCESS ? SPCONV_OK : SPCONV_ERR_CUDA;
 }
 
-int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
+namespace {
+
+// Everything of a product but its workspace.
+int set_args(const DenseOp& op, TcArgs* args) {
     const size_t es = op.dtype == SPCONV_E4M3 ? 1 : 2;
     const int32_t bk = static_cast<int32_t>(128 / es);
     const bool dual = op.epi == kEpiGated || op.epi == kEpiGatedGrad;
-    TcArgs p = {};
+    TcArgs& p = *args;
+    p = {};
     p.m = op.m;
     p.n = op.n;
     p.k_iters = static_cast<int32_t>(ceil_div(op.k, bk));
@@ -643,7 +639,6 @@ int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     p.col_scale[0] = op.col_scale[0];
     p.col_scale[1] = op.col_scale[1];
     p.bias = op.bias;
-    p.status = status;
     p.tiles_m = static_cast<int32_t>(ceil_div(op.m, 256));
     // 256-column tiles reuse an operand byte most; 128 columns when those would
     // leave pairs without a tile, or be half empty
@@ -651,17 +646,18 @@ int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     p.hb = (op.n <= (dual ? 64 : 128) || tiles_of(128) < kPairs) ? 64 : 128;
     p.tiles_n = static_cast<int32_t>(ceil_div(op.n, dual ? p.hb : 2 * p.hb));
     const int64_t tiles = tiles_of(p.hb);
-    if (tiles > 0x3FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
     // Long contractions with few tiles (the weight gradients) are cut along K
     p.splits = 1;
     p.split_iters = p.k_total;
-    const bool plain = op.epi == kEpiLinear && op.act == SPCONV_ACT_NONE && !op.extra && !op.bias && !op.col_scale[0];
-    if (plain && tiles < kPairs && p.k_total >= 16) {
+    if (op.plain() && tiles < kPairs && p.k_total >= 16) {
         int64_t want = kPairs / tiles;
         if (want > p.k_total / 8) want = p.k_total / 8;
         p.split_iters = static_cast<int32_t>(ceil_div(p.k_total, want));
         p.splits = static_cast<int32_t>(ceil_div(p.k_total, p.split_iters));
     }
+    if (tiles * p.splits > 0x3FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
+    p.tiles = static_cast<int32_t>(tiles);
+    p.units = p.tiles * p.splits;
     p.by_tiles = FastDiv(static_cast<uint32_t>(tiles));
     p.by_group = FastDiv(static_cast<uint32_t>(kGroupM * p.tiles_n * p.n_sources));
     p.by_height = FastDiv(kGroupM);
@@ -679,31 +675,84 @@ int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
         for (int i = 0; i < ((op.epi == kEpiGatedGrad || op.n_sources == 2) ? 2 : 1); ++i)
             SPCONV_CHECK(make_tensor_map(&p.c[i], op.out[i], 2, op.n, op.m, op.ld_out, 32));
     if (op.extra) SPCONV_CHECK(make_tensor_map(&p.x, op.extra, 2, op.n, op.m, op.ld_extra, 32));
-    const int64_t units = tiles * p.splits;
-    const int32_t pairs = static_cast<int32_t>(units < kPairs ? units : kPairs);
+    return SPCONV_OK;
+}
 
-    const int64_t part_rows = op.col_sums ? 8 * static_cast<int64_t>(p.tiles_m) : 0;
-    const int64_t slice = op.m * op.n * op.n_sources;
-    Scratch part(static_cast<size_t>(p.splits > 1 ? slice * p.splits : part_rows * op.n) * 4, s);
-    if (part.failed()) return SPCONV_ERR_OOM;
-    p.part = part.as<float>();
-    if (p.splits > 1) {
-        SPCONV_CHECK((launch<kEpiPartial, false>(p, pairs, s)));
-        return launch_pdl(k_sum_slices, dim3(static_cast<unsigned>(ceil_div(slice, 1024))), 256, 0, s,
-                          static_cast<const float*>(p.part), p.splits, slice, slice, op.m, op.n,
-                          static_cast<__nv_bfloat16*>(op.out[0]), static_cast<__nv_bfloat16*>(op.out[1]), op.ld_out);
-    }
+template <int EPI, bool E4M3>
+int run_one(const DenseOp& op, int32_t* status, cudaStream_t s) {
+    TcLaunch<EPI> l = {};
+    SPCONV_CHECK(set_args(op, &l.g[0]));
+    l.count = 1;
+    l.g[0].part = op.col_part;
+    l.trigger = op.col_part == nullptr;
+    l.status = status;
+    return launch<EPI, E4M3>(l, l.g[0].units, s);
+}
+
+}  // namespace
+
+int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     const bool eight = op.dtype == SPCONV_E4M3;
     switch (op.epi) {
-        case kEpiGated:
-            SPCONV_CHECK((eight ? launch<kEpiGated, true>(p, pairs, s) : launch<kEpiGated, false>(p, pairs, s)));
-            break;
-        case kEpiActGrad: SPCONV_CHECK((launch<kEpiActGrad, false>(p, pairs, s))); break;
-        case kEpiGatedGrad: SPCONV_CHECK((launch<kEpiGatedGrad, false>(p, pairs, s))); break;
-        default:
-            SPCONV_CHECK((eight ? launch<kEpiLinear, true>(p, pairs, s) : launch<kEpiLinear, false>(p, pairs, s)));
+        case kEpiGated: return eight ? run_one<kEpiGated, true>(op, status, s) : run_one<kEpiGated, false>(op, status, s);
+        case kEpiActGrad: return run_one<kEpiActGrad, false>(op, status, s);
+        case kEpiGatedGrad: return run_one<kEpiGatedGrad, false>(op, status, s);
+        default: return eight ? run_one<kEpiLinear, true>(op, status, s) : run_one<kEpiLinear, false>(op, status, s);
     }
-    return op.col_sums ? sum_partials(p.part, part_rows, op.n, op.col_sums, s) : SPCONV_OK;
+}
+
+int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_t* status, cudaStream_t s) {
+    TcLaunch<kEpiPlain> l = {};
+    l.count = count;
+    l.status = status;
+    // the product of the longer units first
+    int order[2] = {0, 1};
+    int64_t cost[2] = {0, 0};
+    for (int i = 0; i < count; ++i) {
+        SPCONV_CHECK(set_args(ops[i], &l.g[i]));
+        cost[i] = static_cast<int64_t>(l.g[i].split_iters) * l.g[i].hb;
+    }
+    if (count == 2 && cost[1] > cost[0]) {
+        const TcArgs t = l.g[0];
+        l.g[0] = l.g[1];
+        l.g[1] = t;
+        order[0] = 1;
+        order[1] = 0;
+    }
+    int64_t units = 0;
+    size_t bytes = 0, off[2] = {0, 0};
+    for (int i = 0; i < count; ++i) {
+        units += l.g[i].units;
+        off[i] = bytes;
+        if (l.g[i].splits > 1)
+            bytes += round_up(static_cast<size_t>(l.g[i].m) * l.g[i].n * l.g[i].n_sources * l.g[i].splits * 4, 256);
+    }
+    Scratch part(bytes, s);
+    if (part.failed()) return SPCONV_ERR_OOM;
+    SliceSums sums[2];
+    for (int i = 0; i < count; ++i) {
+        TcArgs& p = l.g[i];
+        if (p.splits == 1) continue;
+        const DenseOp& op = ops[order[i]];
+        p.part = part.as<float>(off[i]);
+        sums[i].part = p.part;
+        sums[i].splits = p.splits;
+        sums[i].m = p.m;
+        sums[i].n = p.n;
+        sums[i].outputs = p.n_sources;
+        sums[i].out[0] = static_cast<__nv_bfloat16*>(op.out[0]);
+        sums[i].out[1] = static_cast<__nv_bfloat16*>(op.out[1]);
+        sums[i].ld = op.ld_out;
+    }
+    const bool sums_follow = bytes > 0 || cols.out;
+    l.trigger = !sums_follow;
+    if (count == 2 && units > kPairs) {
+        l.late = l.g[0].units % kPairs;
+        const int64_t c0 = cost[order[0]], c1 = cost[order[1]];
+        if (l.late) l.rounds = static_cast<int32_t>((2 * c0 + c1) / (2 * c1));
+    }
+    SPCONV_CHECK((launch<kEpiPlain, false>(l, units, s)));
+    return sums_follow ? finish_sums(sums, count, cols, s) : SPCONV_OK;
 }
 
 }  // namespace spconv

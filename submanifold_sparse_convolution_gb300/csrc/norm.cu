@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kLongThreads) k_rms_norm_long(const NormArgs a
 //   dx = r g - h r^3 mean_c(g h) + dres,   dw_c = sum_rows dy h r
 // Each row's threads walk the rows first, first + step, ...; the weight and the
 // running dw of their columns stay in registers, a block's rows are added in a
-// fixed order and the block writes one row of partial sums (sum_partials adds
+// fixed order and the block writes one row of partial sums (finish_sums adds
 // those): no atomics, the same bits every run.
 template <typename T, int W, int VPT>
 struct GradPart {
@@ -403,7 +403,6 @@ __global__ void __launch_bounds__(kBlock) k_rms_norm_grad(const NormGradArgs a, 
     GradPart<T, W, VPT> p, next;
     load_weight<W, VPT>(a.weight, a.c, w, t, TPR);
     pdl_wait();
-    pdl_trigger();
     int64_t base = static_cast<int64_t>(blockIdx.x) * kRows;
     if (base + grp < a.n) p.load(a, base + grp, t, TPR);
     // (every lane of the block runs the same number of rounds: shuffles inside)
@@ -439,7 +438,6 @@ __global__ void __launch_bounds__(512) k_rms_norm_grad_block(const NormGradArgs 
     GradPart<T, W, VPT> p, next;
     load_weight<W, VPT>(a.weight, a.c, w, t, tpr);
     pdl_wait();
-    pdl_trigger();
     int64_t row = blockIdx.x;
     p.load(a, row, t, tpr);
     for (int turn = 0; row < a.n; ++turn) {
@@ -655,7 +653,6 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_grad_ring(const NormGradArg
     const T* const src[3] = {static_cast<const T*>(a.x), static_cast<const T*>(a.dy), static_cast<const T*>(a.dres)};
     const int64_t ld[3] = {a.ldx, a.ldy, a.ldr};
     pdl_wait();
-    pdl_trigger();
     int64_t filled = 0;
     if (t == 0)
         for (int64_t row = blockIdx.x; row < a.n && filled < g.stages; row += gridDim.x, ++filled)
@@ -721,7 +718,6 @@ __global__ void __launch_bounds__(kBlock + 32, VPT > 2 || (VPT > 1 && sizeof(T) 
     if (consumer) load_weight<8, VPT>(a.weight, a.c, w, t, TPR);
     const int64_t tiles = (a.n + g.rows - 1) / g.rows;
     pdl_wait();
-    pdl_trigger();
     int64_t k = 0;
     if (!consumer) {
         const T* const src[3] = {static_cast<const T*>(a.x), static_cast<const T*>(a.dy), static_cast<const T*>(a.dres)};
@@ -900,7 +896,7 @@ int backward_t(const NormGradArgs& a, cudaStream_t s) {
         Scratch part(static_cast<size_t>(blocks) * a.c * 4, s);
         if (part.failed()) return SPCONV_ERR_OOM;
         SPCONV_CHECK(run(part.as<float>()));
-        return sum_partials(part.as<float>(), blocks, a.c, a.dweight, s);
+        return finish_sums(nullptr, 0, {part.as<float>(), blocks, a.c, a.dweight}, s);
     };
     if constexpr (kVec) {
         Ring g;

@@ -105,19 +105,23 @@ __device__ __forceinline__ void with_act(int32_t act, F&& f) {
 // order from the library's pool, so it follows the call's stream by itself.
 class Scratch {
 public:
-    Scratch(size_t bytes, cudaStream_t s) : stream_(s) {
-        if (bytes == 0) return;
-        if (pool_alloc(&ptr_, bytes, s) != cudaSuccess) {
-            cudaGetLastError();
-            ptr_ = nullptr;
-            failed_ = true;
-        }
-    }
+    Scratch() = default;
+    Scratch(size_t bytes, cudaStream_t s) { alloc(bytes, s); }
     ~Scratch() {
         if (ptr_) cudaFreeAsync(ptr_, stream_);
     }
     Scratch(const Scratch&) = delete;
     Scratch& operator=(const Scratch&) = delete;
+    // (once per object)
+    bool alloc(size_t bytes, cudaStream_t s) {
+        stream_ = s;
+        if (bytes && pool_alloc(&ptr_, bytes, s) != cudaSuccess) {
+            cudaGetLastError();
+            ptr_ = nullptr;
+            failed_ = true;
+        }
+        return !failed_;
+    }
     bool failed() const { return failed_; }
     template <typename T>
     T* as(size_t byte_offset = 0) const {
@@ -126,7 +130,7 @@ public:
 
 private:
     void* ptr_ = nullptr;
-    cudaStream_t stream_;
+    cudaStream_t stream_ = nullptr;
     bool failed_ = false;
 };
 
@@ -196,7 +200,7 @@ struct Operand {
 enum : int32_t {
     kEpiLinear = 0,      // out0 = act(acc * row_scale * col_scale + bias) + extra
     kEpiGated = 1,       // out0 = act(acc0 ..) * (acc1 ..), acc1 from b.p[1]
-    kEpiActGrad = 2,     // out0 = extra * act'(acc + bias); col_sums += the unrounded values
+    kEpiActGrad = 2,     // out0 = extra * act'(acc + bias); col_part: sums of the unrounded values
     kEpiGatedGrad = 3,   // out0 = extra * acc1 * act'(acc0), out1 = extra * act(acc0)
 };
 
@@ -216,11 +220,29 @@ struct DenseOp {
     int64_t ld_extra = 0;
     void* out[2] = {nullptr, nullptr};           // bf16 [m] rows, ld_out apart
     int64_t ld_out = 0;
-    float* col_sums = nullptr;                   // fp32 [n] (kEpiActGrad), or null
+    float* col_part = nullptr;                   // fp32 [col_part_rows(m)][n] (kEpiActGrad), or null
+
+    // no epilogue: bf16 operands, the sums rounded and stored
+    bool plain() const {
+        return epi == kEpiLinear && act == SPCONV_ACT_NONE && !extra && !bias && !col_scale[0];
+    }
+};
+
+// Rows of a matrix of partial column sums: one per 32 rows of a 256-row tile.
+inline int64_t col_part_rows(int64_t m) { return 8 * ceil_div(m, 256); }
+
+// out[j] = sum_i part[i][j] over fp32 rows of n.
+struct ColumnSums {
+    const float* part = nullptr;
+    int64_t rows = 0, n = 0;
+    float* out = nullptr;
 };
 int dense_run(const DenseOp& op, cudaStream_t s);
-// the same on the tensor cores (dense_tc.cu); operands, extra and out satisfy tma_ok
+// Up to two plain products in one launch, and column sums, if any, with them.
+int dense_run_plain(const DenseOp* ops, int count, const ColumnSums& cols, cudaStream_t s);
+// On the tensor cores (dense_tc.cu); operands, extra and out satisfy tma_ok.
 int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s);
+int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_t* status, cudaStream_t s);
 // the same for few rows (dense_few.cu): dense_few_takes says which
 bool dense_few_takes(const DenseOp& op);
 int dense_few_run(const DenseOp& op, int32_t* status, cudaStream_t s);
@@ -232,10 +254,21 @@ inline bool tma_ok(const void* p, int64_t ld, size_t es) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * static_cast<int64_t>(es)) % 16 == 0;
 }
 
-// out[j] = sum_i v[i][j] (bf16 rows, ld apart), fp32
-int column_sums(const void* v, int64_t ld, int64_t m, int64_t n, float* out, cudaStream_t s);
-// out[j] = sum_i part[i][j] over p fp32 rows of n
-int sum_partials(const float* part, int64_t p, int64_t n, float* out, cudaStream_t s);
+// Partial column sums of bf16 rows: fills part (column_part_rows(m, n) fp32 rows of n).
+int64_t column_part_rows(int64_t m, int64_t n);
+int column_parts(const void* v, int64_t ld, int64_t m, int64_t n, float* part, cudaStream_t s);
+// What is left after partial results: for up to two products the sums of their
+// slices of K (fp32 [splits][outputs][m][n], outputs one or two), rounded, and
+// column sums.  One launch.
+struct SliceSums {
+    const float* part = nullptr;
+    int32_t splits = 0;
+    int64_t m = 0, n = 0;
+    int32_t outputs = 0;
+    __nv_bfloat16* out[2] = {nullptr, nullptr};
+    int64_t ld = 0;
+};
+int finish_sums(const SliceSums* slices, int count, const ColumnSums& cols, cudaStream_t s);
 // bf16 w [c_in][c_out] -> e4m3 q [c_out][c_in] with scale [c_out]
 int quantize_weight(const void* w, int32_t c_in, int32_t c_out, void* q, float* scale, cudaStream_t s);
 

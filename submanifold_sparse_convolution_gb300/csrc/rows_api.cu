@@ -194,7 +194,13 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
     const bool act = activation != SPCONV_ACT_NONE;
     const int64_t ld_dz = static_cast<int64_t>(round_up(c_out, 8));   // whole 16-byte rows
     Scratch dz_buf(act ? static_cast<size_t>(n) * ld_dz * 2 : 0, s);
-    if (dz_buf.failed()) return SPCONV_ERR_OOM;
+    ColumnSums cols;
+    cols.n = c_out;
+    cols.out = dbias_dev;
+    if (dbias_dev) cols.rows = act ? col_part_rows(n) : column_part_rows(n, c_out);
+    Scratch col_buf(static_cast<size_t>(cols.rows) * c_out * 4, s);
+    if (dz_buf.failed() || col_buf.failed()) return SPCONV_ERR_OOM;
+    cols.part = col_buf.as<float>();
     Rows dz = dy;
     if (act) {
         DenseOp op = product(x, w_dev, c_out, SPCONV_BF16);
@@ -205,24 +211,24 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
         op.ld_extra = ld_dy;
         op.out[0] = dz_buf.as<void>();
         op.ld_out = ld_dz;
-        op.col_sums = dbias_dev;
+        op.col_part = dbias_dev ? col_buf.as<float>() : nullptr;
         SPCONV_CHECK(dense_run(op, s));
         dz = Rows{dz_buf.as<void>(), n, c_out, ld_dz, 2};
     } else if (dbias_dev) {
-        SPCONV_CHECK(column_sums(dy_dev, ld_dy, n, c_out, dbias_dev, s));
+        SPCONV_CHECK(column_parts(dy_dev, ld_dy, n, c_out, col_buf.as<float>(), s));
+    }
+    DenseOp ops[2];
+    int count = 0;
+    if (dw_dev) {
+        ops[count] = outer(x, dz);
+        ops[count++].out[0] = dw_dev;
     }
     if (dx_dev) {
-        DenseOp op = product_t(dz, w_dev, c_in);
-        op.out[0] = dx_dev;
-        op.ld_out = c_in;
-        SPCONV_CHECK(dense_run(op, s));
+        ops[count] = product_t(dz, w_dev, c_in);
+        ops[count].ld_out = c_in;
+        ops[count++].out[0] = dx_dev;
     }
-    if (dw_dev) {
-        DenseOp op = outer(x, dz);
-        op.out[0] = dw_dev;
-        SPCONV_CHECK(dense_run(op, s));
-    }
-    return SPCONV_OK;
+    return dense_run_plain(ops, count, cols, s);
 }
 
 int spconv_gated_ffn(const void* x_dev, int64_t ld_x, const float* x_scale_dev, const void* w_gate_dev,
@@ -294,24 +300,26 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
     op.out[1] = d_buf.as<void>(one);
     op.ld_out = ld_d;
     SPCONV_CHECK(dense_run(op, s));
+    DenseOp ops[2];
+    int count = 0;
+    if (dw_gate_dev) {
+        DenseOp& o = ops[count++];
+        o = outer(x, dg);
+        o.n_sources = 2;
+        o.b.p[1] = du.p;
+        o.out[0] = dw_gate_dev;
+        o.out[1] = dw_up_dev;
+    }
     if (dx_dev) {
-        DenseOp o = product_t(dg, w_gate_dev, c_in);
+        DenseOp& o = ops[count++];
+        o = product_t(dg, w_gate_dev, c_in);
         o.k_sources = 2;
         o.a.p[1] = du.p;
         o.b.p[1] = w_up_dev;
         o.out[0] = dx_dev;
         o.ld_out = c_in;
-        SPCONV_CHECK(dense_run(o, s));
     }
-    if (dw_gate_dev) {
-        DenseOp o = outer(x, dg);
-        o.n_sources = 2;
-        o.b.p[1] = du.p;
-        o.out[0] = dw_gate_dev;
-        o.out[1] = dw_up_dev;
-        SPCONV_CHECK(dense_run(o, s));
-    }
-    return SPCONV_OK;
+    return dense_run_plain(ops, count, {}, s);
 }
 
 int spconv_rows_status(void* stream) {
