@@ -17,15 +17,15 @@
 //   warps 0, 18  tensor-map loads of one operand each into a ring of stages;
 //              both CTAs' loads complete on CTA 0's barrier
 //   warp 1     MMA issue (CTA 0), TMEM allocation
-//   warps 2-17 epilogue, in eight pairs: two pairs per 32 accumulator rows take
-//              blocks of 64 columns in turn, 32 columns a warp.  Columns come
-//              from TMEM 16 at a time, fp32 epilogue, one rounding, staged in
-//              shared memory and stored by a tensor-map copy, which also clips
-//              the ragged edges; the residual or incoming gradient arrives in
-//              the same staging buffer by a tensor-map load before the
-//              accumulator is ready.  (With half as many warps the latencies of
-//              one tile's epilogue, not its instructions, set the pace of short
-//              contractions: 38912 x 128 x 512 gated took 19.0 us.)
+//   warps 2-17 epilogue, in two sets of eight: each set takes every other
+//              tile, so that the chain of latencies of one tile's epilogue
+//              (accumulator wait, TMEM loads, staging, store) runs beside that
+//              of the next.  Two warps share 32 accumulator rows and take
+//              blocks of columns in turn: 16 columns at a time from TMEM, fp32
+//              epilogue, one rounding, staged in shared memory and stored by a
+//              tensor-map copy, which also clips the ragged edges; the residual
+//              or incoming gradient arrives in the same staging buffer by a
+//              tensor-map load before the accumulator is ready
 // The accumulator is double-buffered in TMEM (2 x 256 columns), so the
 // epilogue of one tile runs beside the main loop of the next.
 #include "ptx_sm100.cuh"
@@ -39,10 +39,9 @@ constexpr int kStageA = kRowsA * 128;         // 128 bytes of K per stage
 constexpr int kStageB = 128 * 128;            // hb <= 128 rows
 constexpr int kStage = kStageA + kStageB;
 constexpr int kEpiWarps = 16;
-constexpr int kEpiPairs = kEpiWarps / 2;
 constexpr int kLoadA = 0, kLoadB = 2 + kEpiWarps;   // warps that load an operand each
 constexpr int kThreads = 32 * (3 + kEpiWarps);
-constexpr int kStaging = 32 * 128;            // 32 rows x 64 bf16, one pair of epilogue warps
+constexpr int kStaging = 32 * 128;            // of an epilogue warp: 32 rows of 64 bf16, or twice 32 of 32
 constexpr int kTmemCols = 512;
 constexpr int kGroupM = 16;                   // row tiles that share the column tiles in L2
 constexpr int kPairs = 76;                    // CTA pairs of a full GPU
@@ -102,13 +101,13 @@ struct TcLaunch {
     int32_t* status;
 };
 
-template <int EPI>
-struct TcConfig {
-    static constexpr int kBufs = EPI == kEpiGatedGrad ? 2 : 1;   // staging buffers of a pair of epilogue warps
-    static constexpr int kStages = EPI == kEpiGatedGrad ? 5 : 6;
-    static constexpr int kSmem = 1024 + kStages * kStage + kEpiPairs * kBufs * kStaging + 512;
-    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-};
+constexpr int kStages = 5;
+constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStaging + 512;
+static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+
+// Columns of an epilogue warp's block: one staging buffer of 128-byte rows, or
+// two of 64-byte rows where there are two outputs.
+__host__ __device__ constexpr int block_columns(int epi) { return epi == kEpiGatedGrad ? 32 : 64; }
 
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -159,8 +158,8 @@ __device__ __forceinline__ void load_columns(float (&f)[CW], const float* v, int
 
 template <int EPI, bool E4M3>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense_tc(const __grid_constant__ TcLaunch<EPI> L) {
-    using Cfg = TcConfig<EPI>;
-    constexpr int S = Cfg::kStages;
+    constexpr int S = kStages;
+    constexpr int kBC = block_columns(EPI);
     constexpr bool kDual = EPI == kEpiGated || EPI == kEpiGatedGrad;
     constexpr bool kExtra = EPI != kEpiGated && EPI != kEpiPlain;
     constexpr int kBK = E4M3 ? 128 : 64;      // K elements of a stage
@@ -169,14 +168,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
     const uint32_t raw = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
     uint8_t* staging = smem + S * kStage;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiPairs * Cfg::kBufs * kStaging);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging);
     uint64_t* full = bars;              // [S]  (CTA 0's are used)
     uint64_t* empty = full + S;         // [S]
     uint64_t* acc_full = empty + S;     // [2]
     uint64_t* acc_empty = acc_full + 2; // [2]  (CTA 0's are used)
     uint64_t* exit_bar = acc_empty + 2;
-    uint64_t* extra_full = exit_bar + 1;   // [kEpiPairs]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(extra_full + kEpiPairs);
+    uint64_t* extra_full = exit_bar + 1;   // [kEpiWarps]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(extra_full + kEpiWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -188,10 +187,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&acc_full[b], 1);
-            ptx::mbar_init(&acc_empty[b], 2 * kEpiWarps);
+            ptx::mbar_init(&acc_empty[b], kEpiWarps);   // a set of either CTA
         }
         ptx::mbar_init(exit_bar, 1);
-        for (int w = 0; w < kEpiPairs; ++w) ptx::mbar_init(&extra_full[w], 1);
+        for (int w = 0; w < kEpiWarps; ++w) ptx::mbar_init(&extra_full[w], 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_map(&L.g[0].a[0]);
@@ -353,29 +352,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
         }
     } else {
         // ---------------- epilogue
-        // A pair of warps meets before and after each block of 64 columns, and
-        // once per tile to agree on going on: a warp whose wait ran out keeps
-        // meeting its partner until then.
         const int e = warp - 2;
         const int quarter = warp & 3;            // the TMEM lanes a warp may read
-        const int sub = (e >> 2) & 1, half = e >> 3;   // which 32 columns of a block; which blocks
-        const int pair_of = quarter + 4 * half;
-        const uint32_t meet = 1 + pair_of;
-        uint8_t* stage0 = staging + pair_of * Cfg::kBufs * kStaging;
+        const int half = (e >> 2) & 1, buf = e >> 3;   // which blocks of columns; the set, and its accumulator
+        uint8_t* stage0 = staging + e * kStaging;
         const uint32_t st0 = ptx::smem_u32(stage0);
-        const uint32_t row_off = static_cast<uint32_t>(lane) * 128;
-        const uint32_t sw = lane & 7;
-        uint64_t* xbar = &extra_full[pair_of];
+        const uint32_t row_off = static_cast<uint32_t>(lane) * (kBC * 2);
+        const uint32_t sw = kBC == 64 ? lane & 7 : (lane >> 1) & 3;   // the copies' 128- or 64-byte swizzle
+        uint64_t* xbar = &extra_full[e];
         uint32_t xphase = 0;
         const uint32_t acc_bar = ptx::map_to_rank(ptx::smem_u32(&acc_empty[0]), 0);
-        const bool lead = sub == 0 && lane == 0;
         bool ok = true;
         Unit t;
-        for (int32_t ai = 0; unit_at(ai, t); ++ai) {
+        for (int32_t ai = buf; ok && unit_at(ai, t); ai += 2) {
             const TcArgs& p = args_of(t);
-            const int chunks = (kDual ? p.hb : 2 * p.hb) / 64;
+            const int blocks = (kDual ? p.hb : 2 * p.hb) / kBC;
             const bool to_part = EPI == kEpiPlain && p.part;   // fp32 sums of a slice, not staged
-            const int buf = ai & 1;
             const int32_t m0 = t.tm * 256 + static_cast<int32_t>(rank) * kRowsA + quarter * 32;
             const int64_t row = m0 + lane;
             const int32_t col0 = t.tn * (kDual ? p.hb : 2 * p.hb);
@@ -386,25 +378,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
             auto wait_acc = [&]() {
                 if (waited) return;
                 waited = true;
-                if (ok && !warp_wait(&acc_full[buf], (static_cast<uint32_t>(ai) >> 1) & 1)) {
+                if (!warp_wait(&acc_full[buf], (static_cast<uint32_t>(ai) >> 1) & 1)) {
                     if (lane == 0) fail();
                     ok = false;
                 }
                 ptx::tc_fence_after();
             };
-            for (int c = half; c < chunks; c += 2) {
-                const int32_t n0 = col0 + c * 64;
-                if (!(rows_live && n0 < p.n)) continue;   // (the same for both warps of a pair)
+            for (int c = half; ok && c < blocks; c += 2) {
+                const int32_t n0 = col0 + c * kBC;
+                if (!(rows_live && n0 < p.n)) continue;
                 if (!to_part) {
                     // the staging buffer is free once its last store has been read out
-                    if (lead) {
+                    if (lane == 0) {
                         ptx::bulk_wait_read();
                         if (kExtra && p.has_extra) {
-                            ptx::mbar_arrive_expect_tx(xbar, kStaging);
+                            ptx::mbar_arrive_expect_tx(xbar, 32 * kBC * 2);
                             ptx::tma_load_2d(st0, &p.x, n0, m0, ptx::smem_u32(xbar));
                         }
                     }
-                    ptx::named_barrier_sync(meet, 64);
+                    __syncwarp();
                 }
                 wait_acc();
                 if (kExtra && p.has_extra) {
@@ -416,16 +408,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                     xphase ^= 1;
                 }
                 const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                    static_cast<uint32_t>(buf * 256 + c * 64 + sub * 32);
-#pragma unroll
-                for (int h = 0; h < 32 / CW; ++h) {
-                    if (!ok) break;
+                                    static_cast<uint32_t>(buf * 256 + c * kBC);
+                if (!ok) break;
+#pragma unroll 2
+                for (int h = 0; h < kBC / CW; ++h) {
                     uint32_t z[CW], w[CW];
                     ptx::tmem_ld_32x32b_x16(ta + h * CW, z);
                     if (kDual) ptx::tmem_ld_32x32b_x16(ta + p.hb + h * CW, w);
                     ptx::tmem_ld_wait();
-                    const int32_t nc = n0 + sub * 32 + h * CW;
-                    const uint32_t piece = sub * 4 + h * (CW / 8);   // first 16-byte piece of these columns in a row
+                    const int32_t nc = n0 + h * CW;
+                    const uint32_t piece = h * (CW / 8);   // first 16-byte piece of these columns in a row
                     if (to_part) {
                         if (row_live) {
                             float* dst = p.part + ((static_cast<int64_t>(t.split) * p.n_sources + t.src) * p.m + row) * p.n + nc;
@@ -502,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                     for (int q = 0; q < CW / 8; ++q) {
                         const uint32_t at = row_off + (((piece + q) ^ sw) << 4);
                         *reinterpret_cast<uint4*>(stage0 + at) = pack8(z + 8 * q);
-                        if (EPI == kEpiGatedGrad) *reinterpret_cast<uint4*>(stage0 + kStaging + at) = pack8(w + 8 * q);
+                        if (EPI == kEpiGatedGrad) *reinterpret_cast<uint4*>(stage0 + kStaging / 2 + at) = pack8(w + 8 * q);
                     }
                     if constexpr (EPI == kEpiActGrad) {
                         if (p.part) {
@@ -514,10 +506,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                 }
                 if (!to_part) {
                     ptx::fence_proxy_async_smem();
-                    ptx::named_barrier_sync(meet, 64);
-                    if (lead) {
+                    __syncwarp();
+                    if (lane == 0) {
                         ptx::tma_store_2d(&p.c[EPI == kEpiPlain ? t.src : 0], n0, m0, st0);
-                        if (EPI == kEpiGatedGrad) ptx::tma_store_2d(&p.c[1], n0, m0, st0 + kStaging);
+                        if (EPI == kEpiGatedGrad) ptx::tma_store_2d(&p.c[1], n0, m0, st0 + kStaging / 2);
                         ptx::bulk_commit();
                     }
                 }
@@ -526,17 +518,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
             // rows past m of the column sums: whole 32-row groups without a row
             if (EPI == kEpiActGrad && p.part && !rows_live) {
                 const int64_t pr = static_cast<int64_t>(t.tm) * 8 + rank * 4 + quarter;
-                for (int c = half; c < chunks; c += 2) {
-                    const int32_t n = col0 + c * 64 + sub * 32 + lane;
-                    if (n < p.n) p.part[pr * p.n + n] = 0.0f;
-                }
+                for (int c = half; c < blocks; c += 2)
+                    for (int32_t n = col0 + c * kBC + lane; n < col0 + (c + 1) * kBC && n < p.n; n += 32)
+                        p.part[pr * p.n + n] = 0.0f;
             }
             ptx::tc_fence_before();
             __syncwarp();
             if (ok && lane == 0) ptx::mbar_arrive_cluster(acc_bar + static_cast<uint32_t>(buf) * 8);
-            if (ptx::named_barrier_or(meet, 64, !ok)) break;
         }
-        if (lead) ptx::bulk_wait();
+        if (lane == 0) ptx::bulk_wait();
         __syncwarp();
     }
     // neither CTA leaves, or frees TMEM, while the other may still signal it:
@@ -560,11 +550,11 @@ int launch(const TcLaunch<EPI>& args, int64_t units, cudaStream_t s) {
     if (dev < 0 || dev >= kMaxDevices) return SPCONV_ERR_UNSUPPORTED;
     if (!set[dev]) {
         SPCONV_CHECK_CUDA(cudaFuncSetAttribute(k_dense_tc<EPI, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               TcConfig<EPI>::kSmem));
+                                               kSmem));
         set[dev] = true;
     }
     const unsigned pairs = static_cast<unsigned>(units < kPairs ? units : kPairs);
-    return launch_pdl(k_dense_tc<EPI, E4M3>, dim3(2 * pairs), kThreads, TcConfig<EPI>::kSmem, s, args);
+    return launch_pdl(k_dense_tc<EPI, E4M3>, dim3(2 * pairs), kThreads, kSmem, s, args);
 }
 
 }  // namespace
@@ -588,18 +578,17 @@ EncodeFn encode_fn() {
 
 }  // namespace
 
-// A [outer] x [inner] matrix of rows `ld` elements apart, copied in boxes of
-// box_inner (128 bytes) x box_outer, 128-byte swizzled in shared memory.
-int make_tensor_map(CUtensorMap* map, const void* base, size_t es, int64_t inner, int64_t outer, int64_t ld, int32_t box_outer) {
+int make_tensor_map(CUtensorMap* map, const void* base, size_t es, int64_t inner, int64_t outer, int64_t ld, int32_t box_outer,
+                    int32_t box_bytes) {
     const EncodeFn fn = encode_fn();
     if (!fn) return SPCONV_ERR_CUDA;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_outer)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes / es), static_cast<cuuint32_t>(box_outer)};
     const cuuint32_t unit[2] = {1, 1};
     const CUresult r = fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                           const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? SPCONV_OK : SPCONV_ERR_CUDA;
 }
 
@@ -673,8 +662,8 @@ int set_args(const DenseOp& op, TcArgs* args) {
         SPCONV_CHECK(operand(&p.b[i], op.b, i, p.b_layout, op.n, p.hb));
     if (p.splits == 1)
         for (int i = 0; i < ((op.epi == kEpiGatedGrad || op.n_sources == 2) ? 2 : 1); ++i)
-            SPCONV_CHECK(make_tensor_map(&p.c[i], op.out[i], 2, op.n, op.m, op.ld_out, 32));
-    if (op.extra) SPCONV_CHECK(make_tensor_map(&p.x, op.extra, 2, op.n, op.m, op.ld_extra, 32));
+            SPCONV_CHECK(make_tensor_map(&p.c[i], op.out[i], 2, op.n, op.m, op.ld_out, 32, 2 * block_columns(op.epi)));
+    if (op.extra) SPCONV_CHECK(make_tensor_map(&p.x, op.extra, 2, op.n, op.m, op.ld_extra, 32, 2 * block_columns(op.epi)));
     return SPCONV_OK;
 }
 

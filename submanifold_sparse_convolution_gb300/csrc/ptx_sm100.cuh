@@ -137,20 +137,6 @@ __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t count) 
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// The same barrier, returning to all of them whether any passed a nonzero `p`.
-__device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t count, int p) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred a, b;\n\t"
-        "setp.ne.s32 a, %3, 0;\n\t"
-        "bar.red.or.pred b, %1, %2, a;\n\t"
-        "selp.u32 %0, 1, 0, b;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(count), "r"(p)
-        : "memory");
-    return r != 0;
-}
-
 // ---------------------------------------------------------------------------
 // tcgen05: tensor memory and the 5th-generation MMA
 // ---------------------------------------------------------------------------
