@@ -51,43 +51,70 @@ struct FinishArgs {
 
 constexpr int kFinishCols = 8;   // columns of a block, 32 threads down each
 
+// W (4 or 1) neighbouring sums of the slices, eight loads in flight, added in order.
+template <int W>
+__device__ __forceinline__ void add_slices(const float* q, int32_t splits, int64_t slice, float (&s)[W]) {
+    struct alignas(4 * W) V {
+        float v[W];
+    };
+#pragma unroll
+    for (int j = 0; j < W; ++j) s[j] = 0.0f;
+    for (int32_t k = 0; k < splits; k += 8) {
+        V v[8];
+#pragma unroll
+        for (int32_t t = 0; t < 8; ++t)
+            if (k + t < splits) v[t] = *reinterpret_cast<const V*>(q + (k + t) * slice);
+#pragma unroll
+        for (int32_t t = 0; t < 8; ++t)
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (k + t < splits) s[j] += v[t].v[j];
+    }
+}
+
+// W elements of one row of one output (W = 4 where n % 4 == 0).
+template <int W>
 __device__ __forceinline__ void sum_slices(const SliceSums& a, int32_t block) {
     const int64_t mn = a.m * a.n, slice = mn * a.outputs;
-    const int64_t i = (static_cast<int64_t>(block) * 256 + threadIdx.x) * 4;
-    if (i >= slice) return;
-    if (a.n % 4 == 0) {   // four elements of one row
-        float s[4] = {};
-        const float* q = a.part + i;
-        // eight slices' loads in flight, added in order
-        for (int32_t k = 0; k < a.splits; k += 8) {
-            float4 v[8];
+    const bool gated = a.epi == kEpiGated;
+    const int64_t i = (static_cast<int64_t>(block) * 256 + threadIdx.x) * W;
+    if (i >= (gated ? mn : slice)) return;
+    const int src = !gated && i >= mn;
+    const int64_t r = i - (src ? mn : 0);
+    const int64_t row = mn < 0x7FFFFFFF ? static_cast<uint32_t>(r) / static_cast<uint32_t>(a.n) : r / a.n, col = r - row * a.n;
+    float z[W], u[W];
+    add_slices<W>(a.part + i, a.splits, slice, z);
+    if (gated) add_slices<W>(a.part + mn + i, a.splits, slice, u);
+    if (a.row_scale) {
+        const float rs = a.row_scale[row];
 #pragma unroll
-            for (int32_t t = 0; t < 8; ++t)
-                v[t] = k + t < a.splits ? *reinterpret_cast<const float4*>(q + (k + t) * slice) : make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int32_t t = 0; t < 8; ++t) {
-                s[0] += v[t].x;
-                s[1] += v[t].y;
-                s[2] += v[t].z;
-                s[3] += v[t].w;
-            }
-        }
-        const int src = i >= mn;
-        const int64_t r = i - (src ? mn : 0);
-        const int64_t row = slice < 0x7FFFFFFF ? static_cast<uint32_t>(r) / static_cast<uint32_t>(a.n) : r / a.n;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(s[0], s[1]), hi = __floats2bfloat162_rn(s[2], s[3]);
-        // (rows of the output are 16-byte aligned: tma_ok)
-        *reinterpret_cast<uint2*>(a.out[src] + row * a.ld + (r - row * a.n)) =
-            make_uint2(reinterpret_cast<const uint32_t&>(lo), reinterpret_cast<const uint32_t&>(hi));
-    } else {
-        for (int64_t e = i; e < i + 4 && e < slice; ++e) {
-            float s = 0.0f;
-            for (int32_t k = 0; k < a.splits; ++k) s += a.part[k * slice + e];
-            const int src = e >= mn;
-            const int64_t r = e - (src ? mn : 0), row = r / a.n;
-            a.out[src][row * a.ld + (r - row * a.n)] = __float2bfloat16_rn(s);
+        for (int j = 0; j < W; ++j) {
+            z[j] *= rs * a.col_scale[0][col + j];
+            if (gated) u[j] *= rs * a.col_scale[1][col + j];
         }
     }
+    if (a.bias) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) z[j] += a.bias[col + j];
+    }
+    with_act(a.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) z[j] = act_f<act>(z[j]);
+    });
+    struct alignas(2 * W) V {
+        __nv_bfloat16 v[W];
+    } o;
+    if (gated) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) z[j] *= u[j];
+    } else if (a.extra) {
+        const V x = *reinterpret_cast<const V*>(a.extra + row * a.ld_extra + col);
+#pragma unroll
+        for (int j = 0; j < W; ++j) z[j] += __bfloat162float(x.v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) o.v[j] = __float2bfloat16_rn(z[j]);
+    *reinterpret_cast<V*>(a.out[src] + row * a.ld + col) = o;
 }
 
 __global__ void __launch_bounds__(256) k_finish(const FinishArgs a) {
@@ -98,7 +125,9 @@ __global__ void __launch_bounds__(256) k_finish(const FinishArgs a) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
         if (b < a.blocks[g]) {
-            sum_slices(a.slices[g], b);
+            // (rows of the slices, of extra and of the output are aligned for four: n % 4 == 0 and tma_ok)
+            if (a.slices[g].n % 4 == 0) sum_slices<4>(a.slices[g], b);
+            else sum_slices<1>(a.slices[g], b);
             return;
         }
         b -= a.blocks[g];
@@ -307,7 +336,7 @@ int dense_run(const DenseOp& op, cudaStream_t s) {
     AlignedOp a;
     SPCONV_CHECK(a.begin(op, s));
     SPCONV_CHECK(dense_few_takes(a.op) ? dense_few_run(a.op, status, s)
-                 : a.op.plain()        ? dense_tc_plain(&a.op, 1, {}, status, s)
+                 : dense_tc_cuts(a.op) ? dense_tc_plain(&a.op, 1, {}, status, s)
                                        : dense_tc_run(a.op, status, s));
     return a.end(s);
 }
@@ -332,7 +361,9 @@ int finish_sums(const SliceSums* slices, int count, const ColumnSums& cols, cuda
     int64_t blocks = 0;
     for (int i = 0; i < count; ++i) {
         a.slices[i] = slices[i];
-        const int64_t b = slices[i].splits ? ceil_div(slices[i].m * slices[i].n * slices[i].outputs, 1024) : 0;
+        const SliceSums& t = slices[i];
+        const int64_t elems = t.m * t.n * (t.epi == kEpiGated ? 1 : t.outputs);
+        const int64_t b = t.splits ? ceil_div(elems, t.n % 4 == 0 ? 1024 : 256) : 0;
         if (b > 0x3FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
         a.blocks[i] = static_cast<int32_t>(b);
         blocks += b;

@@ -373,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
             const int32_t col0 = t.tn * (kDual ? p.hb : 2 * p.hb);
             const bool rows_live = m0 < p.m;
             const bool row_live = row < p.m;
-            const float rs = (E4M3 && row_live) ? p.row_scale[row] : 1.0f;
+            const float rs = (E4M3 && EPI != kEpiPlain && row_live) ? p.row_scale[row] : 1.0f;
             bool waited = false;
             auto wait_acc = [&]() {
                 if (waited) return;
@@ -447,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                             x[4 * q + 3] = v.w;
                         }
                     }
-                    if (E4M3) {
+                    if (E4M3 && EPI != kEpiPlain) {
                         float f[CW];
                         load_columns(f, p.col_scale[0], nc, p.n);
 #pragma unroll
@@ -607,8 +607,54 @@ int make_tensor_map_blocks(CUtensorMap* map, const void* base, int64_t inner, in
 
 namespace {
 
+// How a product is cut into units, and a model of its time in us.  A step of K
+// of a 256-column tile takes 0.33 us and one of a 128-column tile 0.26 (both
+// bound by the loads: 32 and 24 KB per SM and step; 2048 rows x 8192 x 1024);
+// a launch of sums takes 3 us and the fp32 partial results move at 6 TB/s.
+struct Cut {
+    int32_t hb = 128, splits = 1, split_iters = 1;
+    int64_t tiles = 0;
+    double us = 0.0;
+};
+
+Cut best_cut(const DenseOp& op, bool dual, int outputs, bool may_split) {
+    const int64_t k_total = ceil_div(op.k, op.dtype == SPCONV_E4M3 ? 128 : 64) * op.k_sources;
+    const int64_t tiles_m = ceil_div(op.m, 256);
+    Cut best;
+    best.us = 1e30;
+    for (int32_t hb : {128, 64}) {
+        const int64_t tiles = tiles_m * ceil_div(op.n, dual ? hb : 2 * hb) * outputs;
+        int64_t most = may_split && tiles < kPairs ? kPairs / tiles : 1;
+        if (most > k_total / 8) most = k_total / 8;
+        for (int64_t splits = 1; splits == 1 || splits <= most; ++splits) {
+            const int64_t iters = ceil_div(k_total, splits), used = ceil_div(k_total, iters);
+            if (used != splits) continue;   // the same cut as a smaller count
+            double us = static_cast<double>(ceil_div(tiles * splits, kPairs) * iters) * (hb == 128 ? 0.33 : 0.26);
+            if (splits > 1) us += 3.0 + 8.0e-6 / 6.0 * static_cast<double>(op.m * op.n * outputs) * static_cast<double>(splits);
+            if (us < best.us) {
+                best.hb = hb;
+                best.splits = static_cast<int32_t>(splits);
+                best.split_iters = static_cast<int32_t>(iters);
+                best.tiles = tiles;
+                best.us = us;
+            }
+        }
+    }
+    return best;
+}
+
+// kEpiGated with K cut: gate and up as two outputs of a plain product.
+DenseOp as_plain(const DenseOp& op) {
+    DenseOp o = op;
+    if (op.epi == kEpiGated) {
+        o.epi = kEpiLinear;
+        o.n_sources = 2;
+    }
+    return o;
+}
+
 // Everything of a product but its workspace.
-int set_args(const DenseOp& op, TcArgs* args) {
+int set_args(const DenseOp& op, bool may_split, TcArgs* args) {
     const size_t es = op.dtype == SPCONV_E4M3 ? 1 : 2;
     const int32_t bk = static_cast<int32_t>(128 / es);
     const bool dual = op.epi == kEpiGated || op.epi == kEpiGatedGrad;
@@ -628,26 +674,16 @@ int set_args(const DenseOp& op, TcArgs* args) {
     p.col_scale[0] = op.col_scale[0];
     p.col_scale[1] = op.col_scale[1];
     p.bias = op.bias;
+    const Cut cut = best_cut(op, dual, op.n_sources, may_split);
+    p.hb = cut.hb;
     p.tiles_m = static_cast<int32_t>(ceil_div(op.m, 256));
-    // 256-column tiles reuse an operand byte most; 128 columns when those would
-    // leave pairs without a tile, or be half empty
-    auto tiles_of = [&](int32_t hb) { return p.tiles_m * ceil_div(op.n, dual ? hb : 2 * hb) * op.n_sources; };
-    p.hb = (op.n <= (dual ? 64 : 128) || tiles_of(128) < kPairs) ? 64 : 128;
     p.tiles_n = static_cast<int32_t>(ceil_div(op.n, dual ? p.hb : 2 * p.hb));
-    const int64_t tiles = tiles_of(p.hb);
-    // Long contractions with few tiles (the weight gradients) are cut along K
-    p.splits = 1;
-    p.split_iters = p.k_total;
-    if (op.plain() && tiles < kPairs && p.k_total >= 16) {
-        int64_t want = kPairs / tiles;
-        if (want > p.k_total / 8) want = p.k_total / 8;
-        p.split_iters = static_cast<int32_t>(ceil_div(p.k_total, want));
-        p.splits = static_cast<int32_t>(ceil_div(p.k_total, p.split_iters));
-    }
-    if (tiles * p.splits > 0x3FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
-    p.tiles = static_cast<int32_t>(tiles);
+    p.splits = cut.splits;
+    p.split_iters = cut.split_iters;
+    if (cut.tiles * p.splits > 0x3FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
+    p.tiles = static_cast<int32_t>(cut.tiles);
     p.units = p.tiles * p.splits;
-    p.by_tiles = FastDiv(static_cast<uint32_t>(tiles));
+    p.by_tiles = FastDiv(static_cast<uint32_t>(p.tiles));
     p.by_group = FastDiv(static_cast<uint32_t>(kGroupM * p.tiles_n * p.n_sources));
     p.by_height = FastDiv(kGroupM);
     p.by_last_height = FastDiv(p.tiles_m % kGroupM ? p.tiles_m % kGroupM : kGroupM);
@@ -663,14 +699,14 @@ int set_args(const DenseOp& op, TcArgs* args) {
     if (p.splits == 1)
         for (int i = 0; i < ((op.epi == kEpiGatedGrad || op.n_sources == 2) ? 2 : 1); ++i)
             SPCONV_CHECK(make_tensor_map(&p.c[i], op.out[i], 2, op.n, op.m, op.ld_out, 32, 2 * block_columns(op.epi)));
-    if (op.extra) SPCONV_CHECK(make_tensor_map(&p.x, op.extra, 2, op.n, op.m, op.ld_extra, 32, 2 * block_columns(op.epi)));
+    if (op.extra && p.splits == 1) SPCONV_CHECK(make_tensor_map(&p.x, op.extra, 2, op.n, op.m, op.ld_extra, 32, 2 * block_columns(op.epi)));
     return SPCONV_OK;
 }
 
 template <int EPI, bool E4M3>
 int run_one(const DenseOp& op, int32_t* status, cudaStream_t s) {
     TcLaunch<EPI> l = {};
-    SPCONV_CHECK(set_args(op, &l.g[0]));
+    SPCONV_CHECK(set_args(op, false, &l.g[0]));
     l.count = 1;
     l.g[0].part = op.col_part;
     l.trigger = op.col_part == nullptr;
@@ -690,6 +726,14 @@ int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     }
 }
 
+bool dense_tc_cuts(const DenseOp& op) {
+    if (op.plain()) return true;
+    if (op.epi != kEpiLinear && op.epi != kEpiGated) return false;
+    const DenseOp o = as_plain(op);
+    const Cut cut = best_cut(o, false, o.n_sources, true);
+    return cut.splits > 1 && cut.us < best_cut(op, op.epi == kEpiGated, 1, false).us;
+}
+
 int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_t* status, cudaStream_t s) {
     TcLaunch<kEpiPlain> l = {};
     l.count = count;
@@ -698,7 +742,7 @@ int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_
     int order[2] = {0, 1};
     int64_t cost[2] = {0, 0};
     for (int i = 0; i < count; ++i) {
-        SPCONV_CHECK(set_args(ops[i], &l.g[i]));
+        SPCONV_CHECK(set_args(as_plain(ops[i]), true, &l.g[i]));
         cost[i] = static_cast<int64_t>(l.g[i].split_iters) * l.g[i].hb;
     }
     if (count == 2 && cost[1] > cost[0]) {
@@ -732,6 +776,14 @@ int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_
         sums[i].out[0] = static_cast<__nv_bfloat16*>(op.out[0]);
         sums[i].out[1] = static_cast<__nv_bfloat16*>(op.out[1]);
         sums[i].ld = op.ld_out;
+        sums[i].epi = op.epi;
+        sums[i].act = op.act;
+        sums[i].row_scale = op.row_scale;
+        sums[i].col_scale[0] = op.col_scale[0];
+        sums[i].col_scale[1] = op.col_scale[1];
+        sums[i].bias = op.bias;
+        sums[i].extra = static_cast<const __nv_bfloat16*>(op.extra);
+        sums[i].ld_extra = op.ld_extra;
     }
     const bool sums_follow = bytes > 0 || cols.out;
     l.trigger = !sums_follow;
@@ -740,7 +792,7 @@ int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_
         const int64_t c0 = cost[order[0]], c1 = cost[order[1]];
         if (l.late) l.rounds = static_cast<int32_t>((2 * c0 + c1) / (2 * c1));
     }
-    SPCONV_CHECK((launch<kEpiPlain, false>(l, units, s)));
+    SPCONV_CHECK(ops[0].dtype == SPCONV_E4M3 ? (launch<kEpiPlain, true>(l, units, s)) : (launch<kEpiPlain, false>(l, units, s)));
     return sums_follow ? finish_sums(sums, count, cols, s) : SPCONV_OK;
 }
 

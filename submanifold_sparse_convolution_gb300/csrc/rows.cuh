@@ -242,6 +242,9 @@ int dense_run(const DenseOp& op, cudaStream_t s);
 int dense_run_plain(const DenseOp* ops, int count, const ColumnSums& cols, cudaStream_t s);
 // On the tensor cores (dense_tc.cu); operands, extra and out satisfy tma_ok.
 int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s);
+// (one product may have the epilogue of kEpiLinear or kEpiGated: dense_tc_cuts
+// says whether cutting its K is worth the workspace; plain ones always go here)
+bool dense_tc_cuts(const DenseOp& op);
 int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_t* status, cudaStream_t s);
 // the same for few rows (dense_few.cu): dense_few_takes says which
 bool dense_few_takes(const DenseOp& op);
@@ -258,8 +261,8 @@ inline bool tma_ok(const void* p, int64_t ld, size_t es) {
 int64_t column_part_rows(int64_t m, int64_t n);
 int column_parts(const void* v, int64_t ld, int64_t m, int64_t n, float* part, cudaStream_t s);
 // What is left after partial results: for up to two products the sums of their
-// slices of K (fp32 [splits][outputs][m][n], outputs one or two), rounded, and
-// column sums.  One launch.
+// slices of K (fp32 [splits][outputs][m][n], outputs one or two), the epilogue
+// and the rounding; and column sums.  One launch.
 struct SliceSums {
     const float* part = nullptr;
     int32_t splits = 0;
@@ -267,6 +270,13 @@ struct SliceSums {
     int32_t outputs = 0;
     __nv_bfloat16* out[2] = {nullptr, nullptr};
     int64_t ld = 0;
+    // kEpiLinear's or kEpiGated's terms (DenseOp); kEpiGated makes one output of two
+    int32_t epi = kEpiLinear, act = SPCONV_ACT_NONE;
+    const float* row_scale = nullptr;
+    const float* col_scale[2] = {nullptr, nullptr};
+    const float* bias = nullptr;
+    const __nv_bfloat16* extra = nullptr;
+    int64_t ld_extra = 0;
 };
 int finish_sums(const SliceSums* slices, int count, const ColumnSums& cols, cudaStream_t s);
 // bf16 w [c_in][c_out] -> e4m3 q [c_out][c_in] with scale [c_out]

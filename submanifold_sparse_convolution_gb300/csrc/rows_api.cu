@@ -193,14 +193,16 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
     if (!dx_dev && !dw_dev && !dbias_dev) return SPCONV_OK;
     const bool act = activation != SPCONV_ACT_NONE;
     const int64_t ld_dz = static_cast<int64_t>(round_up(c_out, 8));   // whole 16-byte rows
-    Scratch dz_buf(act ? static_cast<size_t>(n) * ld_dz * 2 : 0, s);
     ColumnSums cols;
     cols.n = c_out;
     cols.out = dbias_dev;
     if (dbias_dev) cols.rows = act ? col_part_rows(n) : column_part_rows(n, c_out);
-    Scratch col_buf(static_cast<size_t>(cols.rows) * c_out * 4, s);
-    if (dz_buf.failed() || col_buf.failed()) return SPCONV_ERR_OOM;
-    cols.part = col_buf.as<float>();
+    // dz, then the partial column sums
+    const size_t dz_bytes = act ? round_up(static_cast<size_t>(n) * ld_dz * 2, 256) : 0;
+    Scratch buf(dz_bytes + static_cast<size_t>(cols.rows) * c_out * 4, s);
+    if (buf.failed()) return SPCONV_ERR_OOM;
+    float* col_part = buf.as<float>(dz_bytes);
+    cols.part = col_part;
     Rows dz = dy;
     if (act) {
         DenseOp op = product(x, w_dev, c_out, SPCONV_BF16);
@@ -209,13 +211,13 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
         op.bias = bias_dev;
         op.extra = dy_dev;
         op.ld_extra = ld_dy;
-        op.out[0] = dz_buf.as<void>();
+        op.out[0] = buf.as<void>();
         op.ld_out = ld_dz;
-        op.col_part = dbias_dev ? col_buf.as<float>() : nullptr;
+        op.col_part = dbias_dev ? col_part : nullptr;
         SPCONV_CHECK(dense_run(op, s));
-        dz = Rows{dz_buf.as<void>(), n, c_out, ld_dz, 2};
+        dz = Rows{buf.as<void>(), n, c_out, ld_dz, 2};
     } else if (dbias_dev) {
-        SPCONV_CHECK(column_parts(dy_dev, ld_dy, n, c_out, col_buf.as<float>(), s));
+        SPCONV_CHECK(column_parts(dy_dev, ld_dy, n, c_out, col_part, s));
     }
     DenseOp ops[2];
     int count = 0;
