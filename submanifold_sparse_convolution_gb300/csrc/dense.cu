@@ -136,8 +136,14 @@ __global__ void __launch_bounds__(256) k_finish(const FinishArgs a) {
     const int64_t col = static_cast<int64_t>(b) * kFinishCols + x;
     float s = 0.0f;
     if (col < a.cols.n) {
-#pragma unroll 16
-        for (int64_t i = y; i < a.cols.rows; i += 32) s += a.cols.part[i * a.cols.n + col];
+        // eight loads in flight, added in order
+        for (int64_t i = y; i < a.cols.rows; i += 8 * 32) {
+            float v[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) v[t] = i + 32 * t < a.cols.rows ? a.cols.part[(i + 32 * t) * a.cols.n + col] : 0.0f;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) s += v[t];
+        }
     }
     sh[y][x] = s;
     __syncthreads();
