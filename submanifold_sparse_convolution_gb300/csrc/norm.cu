@@ -19,16 +19,8 @@ constexpr float kE4m3Max = 448.0f;
 
 // W consecutive elements as they lie in memory (W = 8 is one or two 16-byte loads).
 template <typename T, int W>
-struct Pack {
+struct alignas(sizeof(T) * W < 16 ? sizeof(T) * W : 16) Pack {
     T v[W];
-};
-template <>
-struct alignas(16) Pack<__nv_bfloat16, 8> {
-    __nv_bfloat16 v[8];
-};
-template <>
-struct alignas(16) Pack<float, 8> {
-    float v[8];
 };
 
 // To fp32 and back (one rounding); pairs of bf16 take one instruction each.
@@ -84,6 +76,8 @@ __device__ __forceinline__ void store_e4m3(uint8_t* dst, const float* v) {
             q[j] = lo | (hi << 16);
         }
         *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+    } else if (W == 2) {
+        *reinterpret_cast<uint16_t*>(dst) = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1 % W]), __NV_SATFINITE, __NV_E4M3);
     } else {
 #pragma unroll
         for (int j = 0; j < W; ++j) dst[j] = __nv_cvt_float_to_fp8(v[j], __NV_SATFINITE, __NV_E4M3);
@@ -255,8 +249,9 @@ __global__ void __launch_bounds__(kBlock) k_rms_norm(const NormArgs a) {
     if (live) row_write<T, W, VPT, EIGHT>(a, row, st, w, h, t, TPR);
 }
 
-// Up to 8192 elements: one block per row, persistent, the next row's loads in
-// flight while this one is reduced and written; the weight stays in registers.
+// Rows of 513 to 4096 elements that no vector load takes: one block per row,
+// persistent, the next row's loads in flight while this one is reduced and
+// written; the weight stays in registers.
 template <typename T, int W, int VPT, bool EIGHT>
 __global__ void __launch_bounds__(512) k_rms_norm_block(const NormArgs a) {
     __shared__ SumMax sh[64];
@@ -391,44 +386,7 @@ __device__ __forceinline__ void grad_write(const NormGradArgs& a, int64_t row, S
     }
 }
 
-// Short rows: TPR lanes per row.
-template <typename T, int W, int TPR, int VPT>
-__global__ void __launch_bounds__(kBlock) k_rms_norm_grad(const NormGradArgs a, float* part) {
-    constexpr int kRows = kBlock / TPR, kCols = TPR * VPT * W;
-    extern __shared__ float sh_dw[];   // [kRows][kCols]
-    const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-    Pack<float, W> w[VPT];
-    float dw[VPT][W] = {};
-    GradPart<T, W, VPT> p, next;
-    load_weight<W, VPT>(a.weight, a.c, w, t, TPR);
-    pdl_wait();
-    int64_t base = static_cast<int64_t>(blockIdx.x) * kRows;
-    if (base + grp < a.n) p.load(a, base + grp, t, TPR);
-    // (every lane of the block runs the same number of rounds: shuffles inside)
-    for (; base < a.n; base += step) {
-        const int64_t row = base + grp;
-        if (row + step < a.n) next.load(a, row + step, t, TPR);
-        Sum2 st{0.0f, 0.0f};
-        if (row < a.n) st = grad_stats<T, W, VPT>(a, p, w, t, TPR);
-        st = lanes_reduce<TPR>(st);
-        if (row < a.n) grad_write<T, W, VPT>(a, row, grad_factors(st, a.c, a.eps), p, w, dw, t, TPR);
-        p = next;
-    }
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-#pragma unroll
-        for (int j = 0; j < W; ++j) sh_dw[grp * kCols + (v * TPR + t) * W + j] = dw[v][j];
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.c; e += kBlock) {
-        float s = 0.0f;
-#pragma unroll
-        for (int g = 0; g < kRows; ++g) s += sh_dw[g * kCols + e];
-        part[static_cast<int64_t>(blockIdx.x) * a.c + e] = s;
-    }
-}
-
-// Up to 8192 elements: one block per row.
+// Rows of 513 elements and more that no 16-byte load takes: one block per row.
 template <typename T, int W, int VPT>
 __global__ void __launch_bounds__(512) k_rms_norm_grad_block(const NormGradArgs a, float* part) {
     __shared__ Sum2 sh[64];
@@ -553,14 +511,25 @@ struct RingState {
         int inputs = 0;
 #pragma unroll
         for (int i = 0; i < IN; ++i) inputs += src[i] != nullptr;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], inputs * rows_here * row_bytes);
+        // bulk copies move 16 bytes at a time: what dense rows of another size
+        // leave over at the matrix's end is stored before the stage is published
+        const uint32_t all = rows_here * row_bytes, over = all & 15;
+        if (over) {
+            const int32_t first = static_cast<int32_t>((all - over) / sizeof(T)), count = static_cast<int32_t>(all / sizeof(T));
+#pragma unroll
+            for (int i = 0; i < IN; ++i)
+                for (int e = first + lane; src[i] && e < count; e += lanes)
+                    const_cast<T*>(rows(g, s, i))[e] = src[i][r0 * ld[i] + e];
+            if (lanes > 1) __syncwarp();
+        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], inputs * (all - over));
         if (lanes > 1) __syncwarp();
 #pragma unroll
         for (int i = 0; i < IN; ++i) {
             if (!src[i]) continue;
             const uint32_t dst = ptx::smem_u32(rows(g, s, i));
             if (ld[i] == c) {
-                if (lane == 0) ptx::bulk_copy_g2s(dst, src[i] + r0 * ld[i], rows_here * row_bytes, &full[s]);
+                if (lane == 0 && all > over) ptx::bulk_copy_g2s(dst, src[i] + r0 * ld[i], all - over, &full[s]);
             } else {
                 for (int r = lane; r < rows_here; r += lanes)
                     ptx::bulk_copy_g2s(dst + r * row_bytes, src[i] + (r0 + r) * ld[i], row_bytes, &full[s]);
@@ -704,18 +673,20 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_grad_ring(const NormGradArg
 }
 
 // Shorter rows, backward: a row per TPR lanes, one warp of the block copies
-// stages of many rows.
-template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(kBlock + 32, VPT > 2 || (VPT > 1 && sizeof(T) == 4) ? 1 : 2) k_rms_norm_grad_lanes(const NormGradArgs a, const Ring g, float* part) {
-    constexpr int kGroups = kBlock / TPR, kCols = TPR * VPT * 8;
+// stages of many rows.  A stage starts a multiple of eight rows in, which is 16
+// bytes aligned for any number of elements where the rows are dense (W < 8).
+template <typename T, int W, int TPR, int VPT>
+__global__ void __launch_bounds__(kBlock + 32, VPT * W > 16 || (VPT * W > 8 && (sizeof(T) == 4 || W < 8)) ? 1 : 2)
+    k_rms_norm_grad_lanes(const NormGradArgs a, const Ring g, float* part) {
+    constexpr int kGroups = kBlock / TPR, kCols = TPR * VPT * W;
     extern __shared__ __align__(128) uint8_t smem[];
     RingState<T, 3> ring;
     ring.init(smem, g, kBlock / 32);
     const bool consumer = threadIdx.x < kBlock;
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-    Pack<float, 8> w[VPT];
-    float dw[VPT][1][8] = {};
-    if (consumer) load_weight<8, VPT>(a.weight, a.c, w, t, TPR);
+    Pack<float, W> w[VPT];
+    float dw[VPT][1][W] = {};
+    if (consumer) load_weight<W, VPT>(a.weight, a.c, w, t, TPR);
     const int64_t tiles = (a.n + g.rows - 1) / g.rows;
     pdl_wait();
     int64_t k = 0;
@@ -751,15 +722,15 @@ __global__ void __launch_bounds__(kBlock + 32, VPT > 2 || (VPT > 1 && sizeof(T) 
             for (int r = grp; r < g.rows; r += kGroups) {
                 const int64_t row = tile * g.rows + r;
                 const bool live = row < a.n;
-                GradPart<T, 8, 1> p;
-                Pack<float, 8> wv[1];
+                GradPart<T, W, 1> p;
+                Pack<float, W> wv[1];
                 Sum2 st{0.0f, 0.0f};
                 if (live) {
 #pragma unroll
                     for (int v = 0; v < VPT; ++v) {
                         p.load(b, r, v * TPR + t, 0);
                         wv[0] = w[v];
-                        st = join(st, grad_stats<T, 8, 1>(a, p, wv, v * TPR + t, 0));
+                        st = join(st, grad_stats<T, W, 1>(a, p, wv, v * TPR + t, 0));
                     }
                 }
                 st = lanes_reduce<TPR>(st);
@@ -770,7 +741,7 @@ __global__ void __launch_bounds__(kBlock + 32, VPT > 2 || (VPT > 1 && sizeof(T) 
                         apart();
                         p.load(b, r, v * TPR + t, 0);
                         wv[0] = w[v];
-                        grad_write<T, 8, 1>(a, row, f, p, wv, dw[v], v * TPR + t, 0);
+                        grad_write<T, W, 1>(a, row, f, p, wv, dw[v], v * TPR + t, 0);
                     }
                 }
             }
@@ -785,7 +756,7 @@ __global__ void __launch_bounds__(kBlock + 32, VPT > 2 || (VPT > 1 && sizeof(T) 
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sh_dw[grp * kCols + (v * TPR + t) * 8 + j] = dw[v][0][j];
+            for (int j = 0; j < W; ++j) sh_dw[grp * kCols + (v * TPR + t) * W + j] = dw[v][0][j];
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.c; e += blockDim.x) {
@@ -797,6 +768,11 @@ __global__ void __launch_bounds__(kBlock + 32, VPT > 2 || (VPT > 1 && sizeof(T) 
 
 bool vec_ok(const void* p, int64_t ld, size_t elem) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * static_cast<int64_t>(elem)) % 16 == 0;
+}
+
+// bf16 rows that two-element loads may take
+bool pair_ok(const void* p, int64_t ld, uintptr_t align = 4) {
+    return (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0 && ld % 2 == 0;
 }
 
 template <typename... K, typename... A>
@@ -860,7 +836,7 @@ int with_lanes(int32_t c, F&& f) {
 
 template <typename T, int W, bool EIGHT>
 int forward_t(const NormArgs& a, cudaStream_t s) {
-    constexpr int S = 8 / W;   // W = 1 holds the same elements in eight times the loads
+    constexpr int S = 8 / W;   // fewer elements per load: as many times the loads
     constexpr bool kVec = W == 8;
     if constexpr (kVec) {
         if (a.c > 1024 && a.c <= (sizeof(T) == 2 ? 16384 : 8192)) {
@@ -877,7 +853,7 @@ int forward_t(const NormArgs& a, cudaStream_t s) {
         return with_lanes<kVec>(a.c, [&](auto tpr, auto vpt) {
             return launch(k_rms_norm<T, W, tpr, vpt * S, EIGHT>, ceil_div(a.n, kBlock / tpr), kBlock, 0, s, a);
         });
-    if constexpr (!kVec) {
+    if constexpr (W == 1) {
         if (a.c <= 4096) {
             const int threads = block_threads(a.c, 8);
             const int64_t most = kSms * (1024 / threads);
@@ -898,20 +874,22 @@ int backward_t(const NormGradArgs& a, cudaStream_t s) {
         SPCONV_CHECK(run(part.as<float>()));
         return finish_sums(nullptr, 0, {part.as<float>(), blocks, a.c, a.dweight}, s);
     };
-    if constexpr (kVec) {
-        Ring g;
-        size_t smem;
-        if (a.c <= (sizeof(T) == 2 ? 1024 : 512))
-            return with_lanes<sizeof(T) == 2>(a.c, [&](auto tpr, auto vpt) {
-                // stages of 8 KB per input at least, so that barriers are few
-                const int64_t unit = kBlock / tpr, row = static_cast<int64_t>(a.c) * sizeof(T);
-                int per_sm = vpt > 2 ? 1 : 2;
-                SPCONV_CHECK(make_ring(&g, &smem, a.c, sizeof(T), 3, unit * ceil_div(8192, unit * row), &per_sm));
-                const int64_t tiles = ceil_div(a.n, g.rows), most = kSms * per_sm, blocks = tiles < most ? tiles : most;
-                return with_part(blocks, [&](float* part) {
-                    return launch_ring<k_rms_norm_grad_lanes<T, tpr, vpt>>(blocks, kBlock + 32, smem, s, a, g, part);
-                });
+    Ring g;
+    size_t smem;
+    auto dense = [&](const void* p, int64_t ld) { return !p || (vec_ok(p, 0, 2) && ld == a.c); };
+    constexpr bool kWide = kVec && sizeof(T) == 2;   // (others would spill)
+    if (a.c <= (kWide ? 1024 : 512) && (kVec || (dense(a.x, a.ldx) && dense(a.dy, a.ldy) && dense(a.dres, a.ldr))))
+        return with_lanes<kWide>(a.c, [&](auto tpr, auto vpt) {
+            // stages of 8 KB per input at least, so that barriers are few
+            const int64_t unit = kBlock / tpr, row = static_cast<int64_t>(a.c) * sizeof(T);
+            int per_sm = vpt > 2 || (vpt > 1 && !kWide) ? 1 : 2;
+            SPCONV_CHECK(make_ring(&g, &smem, a.c, sizeof(T), 3, unit * ceil_div(8192, unit * row), &per_sm));
+            const int64_t tiles = ceil_div(a.n, g.rows), most = kSms * per_sm, blocks = tiles < most ? tiles : most;
+            return with_part(blocks, [&](float* part) {
+                return launch_ring<k_rms_norm_grad_lanes<T, W, tpr, vpt * (8 / W)>>(blocks, kBlock + 32, smem, s, a, g, part);
             });
+        });
+    if constexpr (kVec) {
         if (a.c <= (sizeof(T) == 2 ? 8192 : 4096)) {
             constexpr int kVpt = sizeof(T) == 2 ? 4 : 2;
             const int threads = block_threads(a.c, 8 * kVpt);
@@ -922,17 +900,11 @@ int backward_t(const NormGradArgs& a, cudaStream_t s) {
                 return launch_ring<k_rms_norm_grad_ring<T, kVpt>>(blocks, threads, smem, s, a, g, part);
             });
         }
-    } else {
-        if (a.c <= 512)
-            return with_lanes<false>(a.c, [&](auto tpr, auto vpt) {
-                const int64_t want = ceil_div(a.n, kBlock / tpr), most = kSms * 4;
-                const int64_t blocks = want < most ? want : most;
-                return with_part(blocks, [&](float* part) {
-                    return launch(k_rms_norm_grad<T, W, tpr, vpt * 8>, blocks, kBlock, size_t(kBlock) * vpt * 8 * 4, s, a, part);
-                });
-            });
-        if (a.c <= 2048) {
-            const int threads = block_threads(a.c, 4);
+    }
+    if constexpr (!kVec) {
+        constexpr int kPer = 4 * W;   // elements of a thread
+        if (a.c <= 512 * kPer) {
+            const int threads = block_threads(a.c, kPer);
             const int64_t most = kSms * (1024 / threads);
             const int64_t blocks = a.n < most ? a.n : most;
             return with_part(blocks, [&](float* part) {
@@ -965,11 +937,15 @@ int norm_forward(const NormArgs& a, cudaStream_t s) {
     const bool vec = a.c % 8 == 0 && vec_ok(a.x, a.ldx, es) && vec_ok(a.residual, a.ldr, es) &&
                      vec_ok(a.weight, 0, 4) && vec_ok(a.sum, 0, es) && vec_ok(a.out, 0, es);
     const bool eight = a.out_dtype == SPCONV_E4M3;
+    // (between, a block per row with single loads is faster: 2818 against 4424 GB/s at 1002 and 1001 elements)
+    const bool pairs = (a.c <= 512 || a.c > 4096) && a.c % 2 == 0 && pair_ok(a.x, a.ldx) && pair_ok(a.residual, a.ldr) && pair_ok(a.weight, 0, 8) &&
+                       pair_ok(a.sum, 0) && pair_ok(a.out, 0, eight ? 2 : 4);
     if (a.dtype == SPCONV_FP32)
         return vec ? (eight ? forward_t<float, 8, true>(a, s) : forward_t<float, 8, false>(a, s))
                    : (eight ? forward_t<float, 1, true>(a, s) : forward_t<float, 1, false>(a, s));
-    return vec ? (eight ? forward_t<__nv_bfloat16, 8, true>(a, s) : forward_t<__nv_bfloat16, 8, false>(a, s))
-               : (eight ? forward_t<__nv_bfloat16, 1, true>(a, s) : forward_t<__nv_bfloat16, 1, false>(a, s));
+    if (vec) return eight ? forward_t<__nv_bfloat16, 8, true>(a, s) : forward_t<__nv_bfloat16, 8, false>(a, s);
+    if (pairs) return eight ? forward_t<__nv_bfloat16, 2, true>(a, s) : forward_t<__nv_bfloat16, 2, false>(a, s);
+    return eight ? forward_t<__nv_bfloat16, 1, true>(a, s) : forward_t<__nv_bfloat16, 1, false>(a, s);
 }
 
 int norm_backward(const NormGradArgs& a, cudaStream_t s) {
@@ -977,7 +953,11 @@ int norm_backward(const NormGradArgs& a, cudaStream_t s) {
     const bool vec = a.c % 8 == 0 && vec_ok(a.dy, a.ldy, es) && vec_ok(a.x, a.ldx, es) && vec_ok(a.dres, a.ldr, es) &&
                      vec_ok(a.weight, 0, 4) && vec_ok(a.dx, 0, es);
     if (a.dtype == SPCONV_FP32) return vec ? backward_t<float, 8>(a, s) : backward_t<float, 1>(a, s);
-    return vec ? backward_t<__nv_bfloat16, 8>(a, s) : backward_t<__nv_bfloat16, 1>(a, s);
+    const bool pairs = a.c % 2 == 0 && pair_ok(a.dy, a.ldy) && pair_ok(a.x, a.ldx) && pair_ok(a.dres, a.ldr) &&
+                       pair_ok(a.weight, 0, 8) && pair_ok(a.dx, 0);
+    return vec     ? backward_t<__nv_bfloat16, 8>(a, s)
+           : pairs ? backward_t<__nv_bfloat16, 2>(a, s)
+                   : backward_t<__nv_bfloat16, 1>(a, s);
 }
 
 }  // namespace spconv
