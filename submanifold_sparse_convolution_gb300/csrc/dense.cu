@@ -266,7 +266,8 @@ namespace {
 
 // The tensor maps need 16-byte aligned rows.  Matrices without them (odd
 // channel counts, strides or addresses) are copied to rows that have them, and
-// such an output is copied back: one extra pass over that matrix.
+// an output whose rows are not whole 16 bytes is copied back: one extra pass
+// over that matrix.
 class AlignedOp {
 public:
     DenseOp op;   // what to run between begin and end
@@ -280,7 +281,8 @@ public:
         const Matrix a = op.a.k_major ? plan(op.a.p, na, op.a.ld, op.m, op.k, es) : plan(op.a.p, na, op.a.ld, op.k, op.m, es);
         const Matrix b = op.b.k_major ? plan(op.b.p, nb, op.b.ld, op.n, op.k, es) : plan(op.b.p, nb, op.b.ld, op.k, op.n, es);
         const Matrix x = plan(&op.extra, op.extra ? 1 : 0, op.ld_extra, op.m, op.n, 2);
-        const Matrix c = plan(op.out, outs_, op.ld_out, op.m, op.n, 2);
+        // a tensor-map store clips a row at 16 bytes, not at an element
+        const Matrix c = plan(op.out, outs_, op.ld_out, op.m, op.n, 2, op.n % 8 != 0 && !op.out_padded);
         copy_back_ = c.move;
         if (bytes_ == 0) return SPCONV_OK;
         if (!buf_.alloc(bytes_, s)) return SPCONV_ERR_OOM;
@@ -307,8 +309,8 @@ private:
         size_t off[2];
         int64_t ld() const { return static_cast<int64_t>(round_up(static_cast<size_t>(cols), 16 / es)); }
     };
-    Matrix plan(const void* const* ptr, int count, int64_t ld, int64_t rows, int64_t cols, size_t e) {
-        Matrix t{rows, cols, e, false, {0, 0}};
+    Matrix plan(const void* const* ptr, int count, int64_t ld, int64_t rows, int64_t cols, size_t e, bool move = false) {
+        Matrix t{rows, cols, e, move, {0, 0}};
         for (int i = 0; i < count; ++i) t.move = t.move || !tma_ok(ptr[i], ld, e);
         for (int i = 0; t.move && i < count; ++i) {
             t.off[i] = bytes_;

@@ -220,6 +220,7 @@ struct DenseOp {
     int64_t ld_extra = 0;
     void* out[2] = {nullptr, nullptr};           // bf16 [m] rows, ld_out apart
     int64_t ld_out = 0;
+    bool out_padded = false;                     // columns n .. up to whole 16 bytes are the library's to write
     float* col_part = nullptr;                   // fp32 [col_part_rows(m)][n] (kEpiActGrad), or null
 
     // no epilogue: bf16 operands, the sums rounded and stored

@@ -213,6 +213,7 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
         op.ld_extra = ld_dy;
         op.out[0] = buf.as<void>();
         op.ld_out = ld_dz;
+        op.out_padded = true;
         op.col_part = dbias_dev ? col_part : nullptr;
         SPCONV_CHECK(dense_run(op, s));
         dz = Rows{buf.as<void>(), n, c_out, ld_dz, 2};
@@ -301,6 +302,7 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
     op.out[0] = d_buf.as<void>();
     op.out[1] = d_buf.as<void>(one);
     op.ld_out = ld_d;
+    op.out_padded = true;
     SPCONV_CHECK(dense_run(op, s));
     DenseOp ops[2];
     int count = 0;

@@ -213,7 +213,7 @@ def test_norm_backward_differences():
 # rows x c_in x c_out: one token to long ones, odd channel counts, edges of 16, 64, 128 and 256
 SIZES = [(1, 64, 64), (1, 1, 1), (1, 4096, 4096), (2, 16, 16), (7, 2048, 600), (16, 128, 512), (33, 24, 40), (63, 200, 136),
          (64, 64, 256), (65, 72, 264), (100, 17, 33), (127, 129, 65), (128, 128, 128), (129, 512, 96), (200, 1000, 1001),
-         (256, 256, 256), (257, 320, 520), (500, 33, 8), (1000, 8, 700), (1025, 640, 384), (3000, 128, 512), (4111, 520, 72)]
+         (256, 256, 256), (257, 320, 520), (65, 3000, 24), (130, 4096, 256), (300, 2048, 100), (1000, 1536, 36), (500, 33, 8), (1000, 8, 700), (1025, 640, 384), (3000, 128, 512), (4111, 520, 72)]
 
 
 def make(g, n, c, h, eight, k=1):
@@ -367,14 +367,14 @@ def test_gradients_against_differences():
             assert abs(num - ana) <= 2.0 ** -8 * 4 * size
 
 
-@pytest.mark.parametrize("n,c,h", [(5, 64, 72), (300, 128, 264), (300, 40, 33)])
+@pytest.mark.parametrize("n,c,h", [(5, 64, 72), (300, 128, 264), (300, 40, 33), (300, 64, 36), (520, 1056, 60)])
 def test_strides_and_in_place(n, c, h):
     g = gen(4)
     x, (wg, wu), _, _, _, _ = make(g, n, c, h, False, 2)
     r, dy = normal(g, n, h).to(BF), normal(g, n, h).to(BF)
     y, f = sc.linear(x, wg, residual=r), sc.gated_ffn(x, wg, wu)
     d1, d2 = sc.linear_backward(dy, x, wg, activation="silu"), sc.gated_ffn_backward(dy, x, wg, wu)
-    for extra in (8, 24, 3):
+    for extra in (8, 24, 3, 4):
         xs, rs, ds = strided(x, extra), strided(r, extra), strided(dy, extra)
         ys = strided(torch.zeros_like(y), extra)
         fs = strided(torch.zeros_like(f), extra)
@@ -550,6 +550,11 @@ def test_refusals():
         sc.rms_norm(x, wn, eps=-1.0)
     with pytest.raises(sc.SpconvError):
         sc.rms_norm(x, wn, eps=float("nan"))
+
+
+def test_no_wait_ran_out():
+    """The status word of the operators' bounded waits after everything above."""
+    assert sc.rows_status() == 0
 
 
 def test_strided_outputs_past_32_bits():
