@@ -87,16 +87,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_dense_few(const __grid_constant
         atomicOr(p.status, kStatusTimeout);
         *abort_flag = 1;
     };
+    int32_t fills = 0;   // stages this thread has filled
     if (warp == 0) {
         if (lane == 0) {
             const uint32_t bytes = kAcc * kTileA + static_cast<uint32_t>(p.rows_pad) * 128u;
-            int32_t f = 0;
-            bool ok = true;
+            int32_t& f = fills;
             for (int32_t it = it0; it < it1; ++it, ++f) {
                 const int32_t s = f % p.stages;
                 if (f >= p.stages && !ptx::mbar_wait(&empty[s], static_cast<uint32_t>(f / p.stages - 1) & 1, abort_flag)) {
                     fail();
-                    ok = false;
                     break;
                 }
                 const uint32_t base = ptx::smem_u32(ring) + static_cast<uint32_t>(s * p.stage_bytes);
@@ -113,9 +112,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_dense_few(const __grid_constant
                 }
                 ptx::tma_load_2d(base + kAcc * kTileA, &p.x, it * kBK, 0, bar);
             }
-            if (!ok)   // loads still in flight land before the CTA exits
-                for (int32_t j = f > p.stages ? f - p.stages : 0; j < f; ++j)
-                    ptx::mbar_wait(&full[j % p.stages], static_cast<uint32_t>(j / p.stages) & 1, nullptr);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -144,6 +140,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_dense_few(const __grid_constant
         }
         ptx::mma_commit_if(leader, &done);
     }
+    __syncthreads();
+    if (*abort_flag)   // given up: loads still in flight land first
+        for (int32_t j = fills > p.stages ? fills - p.stages : 0; j < fills; ++j)
+            ptx::mbar_wait(&full[j % p.stages], static_cast<uint32_t>(j / p.stages) & 1, nullptr);
     // every MMA of this CTA has completed: its sums are whole, its ring is free
     const bool whole = ptx::mbar_wait(&done, 0, nullptr);
     if (!whole && threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);

@@ -253,11 +253,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
     };
     auto args_of = [&](const Unit& t) -> const TcArgs& { return L.g[EPI == kEpiPlain ? t.g : 0]; };
 
+    uint32_t fills = 0;   // stages this thread has filled
     if (warp == kLoadA || warp == kLoadB) {
         // ---------------- loads of one operand
         if (lane == 0) {
             const bool is_a = warp == kLoadA;
-            uint32_t f = 0;
+            uint32_t& f = fills;
             bool ok = true;
             Unit t;
             for (int32_t q = 0; ok && unit_at(q, t); ++q) {
@@ -292,11 +293,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                     }
                 }
             }
-            if (!ok && rank == 0)   // loads still in flight land before the CTAs exit
-                for (uint32_t s = 0; s < S && s < f; ++s) {
-                    const uint32_t last = (f - 1 - s) / S;   // fill number of stage s
-                    ptx::mbar_wait(&full[s], last & 1, nullptr);
-                }
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -527,6 +523,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
     // CTA 0's MMAs send it
     ptx::tc_fence_before();
     ptx::cluster_sync();
+    if (rank == 0 && fills && *abort_flag)   // given up: loads of either CTA still in flight land first
+        for (uint32_t q = fills > S ? fills - S : 0; q < fills; ++q) ptx::mbar_wait(&full[q % S], (q / S) & 1, nullptr);
+    __syncwarp();
     if (warp == 1 && rank == 1 && !ptx::mbar_wait(exit_bar, 0, nullptr)) atomicOr(L.status, kStatusTimeout);
     __syncwarp();
     ptx::cluster_sync();

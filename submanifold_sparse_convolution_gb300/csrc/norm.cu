@@ -570,15 +570,11 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_ring(const NormArgs a, cons
     if (t == 0)
         for (int64_t row = blockIdx.x; row < a.n && filled < g.stages; row += gridDim.x, ++filled)
             ring.fill(g, filled, row, a.n, a.c, src, ld, 0, 1);
-    bool ok = true;
     int k = 0;
     for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, ++k) {
         const int s = k % g.stages;
         // (a thread that gave up still meets the others at the barrier)
-        if (!ptx::mbar_wait(&ring.full[s], static_cast<uint32_t>(k / g.stages) & 1, ring.abort_flag)) {
-            ring.fail(g);
-            ok = false;
-        }
+        if (!ptx::mbar_wait(&ring.full[s], static_cast<uint32_t>(k / g.stages) & 1, ring.abort_flag)) ring.fail(g);
         NormArgs b = a;   // the stage's row in place of the global one
         b.x = ring.rows(g, s, 0);
         b.residual = a.residual ? ring.rows(g, s, 1) : nullptr;
@@ -605,7 +601,7 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_ring(const NormArgs a, cons
             row_write<T, 8, 1, EIGHT>(a, row, st, wv, h, v * threads + t, 0);
         }
     }
-    if (t == 0 && !ok) ring.drain(g, filled);
+    if (t == 0 && *ring.abort_flag) ring.drain(g, filled);   // (set before the last barrier, if at all)
 }
 
 // The backward pass of such rows.  The row's vectors are taken from shared
@@ -626,14 +622,10 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_grad_ring(const NormGradArg
     if (t == 0)
         for (int64_t row = blockIdx.x; row < a.n && filled < g.stages; row += gridDim.x, ++filled)
             ring.fill(g, filled, row, a.n, a.c, src, ld, 0, 1);
-    bool ok = true;
     int k = 0;
     for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, ++k) {
         const int s = k % g.stages;
-        if (!ptx::mbar_wait(&ring.full[s], static_cast<uint32_t>(k / g.stages) & 1, ring.abort_flag)) {
-            ring.fail(g);
-            ok = false;
-        }
+        if (!ptx::mbar_wait(&ring.full[s], static_cast<uint32_t>(k / g.stages) & 1, ring.abort_flag)) ring.fail(g);
         NormGradArgs b = a;
         b.x = ring.rows(g, s, 0);
         b.dy = ring.rows(g, s, 1);
@@ -662,7 +654,7 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_grad_ring(const NormGradArg
             grad_write<T, 8, 1>(a, row, f, p, wv, dw[v], v * threads + t, 0);
         }
     }
-    if (t == 0 && !ok) ring.drain(g, filled);
+    if (t == 0 && *ring.abort_flag) ring.drain(g, filled);   // (set before the last barrier, if at all)
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
@@ -694,19 +686,15 @@ __global__ void __launch_bounds__(kBlock + 32, VPT * W > 16 || (VPT * W > 8 && (
         const T* const src[3] = {static_cast<const T*>(a.x), static_cast<const T*>(a.dy), static_cast<const T*>(a.dres)};
         const int64_t ld[3] = {a.ldx, a.ldy, a.ldr};
         const int lane = threadIdx.x & 31;
-        bool ok = true;
         for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++k) {
-            if (k >= g.stages) {
-                ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ring.empty[k % g.stages],
-                                                            static_cast<uint32_t>(k / g.stages - 1) & 1, ring.abort_flag));
-                if (!ok) {
-                    if (lane == 0) ring.fail(g);
-                    break;
-                }
+            if (k >= g.stages &&
+                !__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ring.empty[k % g.stages], static_cast<uint32_t>(k / g.stages - 1) & 1,
+                                                        ring.abort_flag))) {
+                if (lane == 0) ring.fail(g);
+                break;
             }
             ring.fill(g, k, tile, a.n, a.c, src, ld, lane, 32);
         }
-        if (!ok) ring.drain(g, k);
     } else {
         for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++k) {
             const int s = static_cast<int>(k % g.stages);
@@ -752,6 +740,7 @@ __global__ void __launch_bounds__(kBlock + 32, VPT * W > 16 || (VPT * W > 8 && (
     // the block's rows are added through the ring's memory, free by now
     float* sh_dw = reinterpret_cast<float*>(smem);   // [kGroups][kCols]
     __syncthreads();
+    if (!consumer && *ring.abort_flag) ring.drain(g, k);
     if (consumer) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
