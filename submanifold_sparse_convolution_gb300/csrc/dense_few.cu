@@ -10,8 +10,9 @@
 // `splits` CTAs cuts K between them.  Each keeps its fp32 sums in shared
 // memory and every CTA adds the partial sums of its share of the rows through
 // distributed shared memory, in the order of the ranks, applies the epilogue
-// and stores: one launch, no workspace, the same bits every run.  Two CTAs fit
-// an SM, which together keep about 200 KB of loads in flight.
+// and stores: one launch, no workspace, the same bits every run.  An SM keeps
+// about 200 KB of loads in flight: two CTAs up to 128 rows (gated: 64), one up
+// to twice that, where the sums need the room.
 #include "ptx_sm100.cuh"
 #include "tensor_map.cuh"
 
@@ -21,11 +22,18 @@ namespace {
 constexpr int kThreads = 192;          // warp 0 loads, warp 1 issues MMAs, warps 2-5 read the accumulator
 constexpr int kChannels = 128;         // output channels per CTA (MMA M)
 constexpr int kTileA = kChannels * 128;
-constexpr int kMaxRows = 128;          // one accumulator
-constexpr int kMaxRowsDual = 64;       // gate and up
 constexpr int kMaxSplits = 8;          // portable cluster size
 constexpr int kMaxStages = 8;
-constexpr int kRing = 100 * 1024;      // stages, of one CTA
+
+// BIG: one CTA per SM.
+template <bool DUAL, bool BIG>
+struct FewConfig {
+    static constexpr int kRows = (BIG ? 256 : 128) / (DUAL ? 2 : 1);   // of an accumulator
+    static constexpr int kCols = (DUAL ? 2 : 1) * kRows;              // TMEM columns (a power of two)
+    static constexpr int kRing = (BIG ? 200 : 100) * 1024;            // stages, of one CTA
+    static constexpr int kPerSm = BIG ? 1 : 2;
+    static_assert(kCols * kChannels * 4 <= kRing, "the sums take the ring's place");
+};
 
 struct FewArgs {
     CUtensorMap w[2], x;
@@ -45,11 +53,12 @@ struct FewArgs {
     int32_t* status;
 };
 
-template <bool DUAL, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 2) k_dense_few(const __grid_constant__ FewArgs p) {
+template <bool DUAL, bool E4M3, bool BIG>
+__global__ void __launch_bounds__(kThreads, FewConfig<DUAL, BIG>::kPerSm) k_dense_few(const __grid_constant__ FewArgs p) {
     constexpr int kAcc = DUAL ? 2 : 1;
     constexpr int kBK = E4M3 ? 128 : 64;
-    constexpr uint32_t kCols = DUAL ? 2 * kMaxRowsDual : kMaxRows;   // TMEM columns (a power of two)
+    constexpr int kRows = FewConfig<DUAL, BIG>::kRows;
+    constexpr uint32_t kCols = FewConfig<DUAL, BIG>::kCols;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
     __shared__ uint32_t tmem_slot;
@@ -134,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_dense_few(const __grid_constant
             for (int a = 0; a < kAcc; ++a)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    ptx::mma_if<E4M3>(leader, tmem + a * kMaxRowsDual, a0 + off + a * (kTileA >> 4) + j * da, b0 + off + 2 * j,
+                    ptx::mma_if<E4M3>(leader, tmem + a * kRows, a0 + off + a * (kTileA >> 4) + j * da, b0 + off + 2 * j,
                                       idesc, (f > 0 || j > 0) ? 1u : 0u);
             ptx::mma_commit_if(leader, &empty[s]);
         }
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_dense_few(const __grid_constant
         for (int a = 0; a < kAcc; ++a)
             for (int32_t r0 = 0; r0 < p.rows; r0 += 16) {
                 uint32_t v[16];
-                ptx::tmem_ld_32x32b_x16(tmem + lanes + a * kMaxRowsDual + r0, v);
+                ptx::tmem_ld_32x32b_x16(tmem + lanes + a * kRows + r0, v);
                 ptx::tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -170,43 +179,77 @@ __global__ void __launch_bounds__(kThreads, 2) k_dense_few(const __grid_constant
     // this CTA's share: rows rank, rank + splits, ..
     const int32_t mine = (p.rows - static_cast<int32_t>(rank) + static_cast<int32_t>(splits) - 1) / static_cast<int32_t>(splits);
     const uint32_t sums_addr = ptx::smem_u32(sums);
-    for (int32_t i = threadIdx.x; i < mine * kChannels; i += kThreads) {
-        const int32_t ch = i & (kChannels - 1);
-        const int32_t row = static_cast<int32_t>(rank) + (i >> 7) * static_cast<int32_t>(splits);
-        const int64_t n = n0 + ch;
-        if (n >= p.n) continue;
-        float z[kAcc];
+    // a warp takes a row, a lane four of its channels
+    const int64_t n = n0 + 4 * lane;
+    for (int32_t i = warp; i < mine && n < p.n; i += kThreads / 32) {
+        const int32_t row = static_cast<int32_t>(rank) + i * static_cast<int32_t>(splits);
+        float z[kAcc][4];
 #pragma unroll
         for (int a = 0; a < kAcc; ++a) {
-            const uint32_t at = sums_addr + static_cast<uint32_t>(((a * p.rows + row) * kChannels + ch) * 4);
-            float part[kMaxSplits];
+            const uint32_t at = sums_addr + static_cast<uint32_t>(((a * p.rows + row) * kChannels + 4 * lane) * 4);
+            float4 part[kMaxSplits];
 #pragma unroll
             for (uint32_t r = 0; r < kMaxSplits; ++r)
-                part[r] = r < splits ? ptx::ld_cluster_f32(ptx::map_to_rank(at, r)) : 0.0f;
-            z[a] = part[0];
+                if (r < splits) part[r] = ptx::ld_cluster_f32x4(ptx::map_to_rank(at, r));
+            z[a][0] = part[0].x;
+            z[a][1] = part[0].y;
+            z[a][2] = part[0].z;
+            z[a][3] = part[0].w;
 #pragma unroll
-            for (uint32_t r = 1; r < kMaxSplits; ++r) z[a] += part[r];
-            if (E4M3) z[a] *= p.row_scale[row] * p.col_scale[a][n];
+            for (uint32_t r = 1; r < kMaxSplits; ++r)
+                if (r < splits) {
+                    z[a][0] += part[r].x;
+                    z[a][1] += part[r].y;
+                    z[a][2] += part[r].z;
+                    z[a][3] += part[r].w;
+                }
         }
-        if (!DUAL && p.bias) z[0] += p.bias[n];
-        const float x = (!DUAL && p.extra) ? __bfloat162float(p.extra[row * p.ld_extra + n]) : 0.0f;
-        float y = 0.0f;
-        with_act(p.act, [&](auto act) { y = DUAL ? act_f<act>(z[0]) * z[kAcc - 1] : act_f<act>(z[0]) + x; });
-        p.out[row * p.ld_out + n] = __float2bfloat16_rn(y);
+        alignas(8) __nv_bfloat16 y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (n + j >= p.n) continue;
+            if (E4M3) {
+#pragma unroll
+                for (int a = 0; a < kAcc; ++a) z[a][j] *= p.row_scale[row] * p.col_scale[a][n + j];
+            }
+            if (!DUAL && p.bias) z[0][j] += p.bias[n + j];
+        }
+        with_act(p.act, [&](auto act) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = (!DUAL && p.extra && n + j < p.n) ? __bfloat162float(p.extra[row * p.ld_extra + n + j]) : 0.0f;
+                y[j] = __float2bfloat16_rn(DUAL ? act_f<act>(z[0][j]) * z[kAcc - 1][j] : act_f<act>(z[0][j]) + x);
+            }
+        });
+        __nv_bfloat16* out = p.out + row * p.ld_out + n;   // (8-byte aligned: tma_ok)
+        if (n + 4 <= p.n) {
+            *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
+        } else {
+            for (int j = 0; n + j < p.n; ++j) out[j] = y[j];
+        }
     }
     // no CTA's sums go away while another may still read them
     ptx::cluster_sync();
     if (warp == 1) ptx::tmem_dealloc(tmem, kCols);
 }
 
-template <bool DUAL, bool E4M3>
-int launch(const FewArgs& p, int32_t tiles, int32_t splits, size_t smem, cudaStream_t s) {
+template <bool DUAL, bool E4M3, bool BIG>
+int launch(FewArgs& p, cudaStream_t s) {
+    using Cfg = FewConfig<DUAL, BIG>;
+    constexpr int kAcc = DUAL ? 2 : 1;
+    // As many CTAs as the SMs hold, each with four steps of K at least
+    const int32_t tiles = static_cast<int32_t>(ceil_div(p.n, kChannels));
+    int32_t splits = 1;
+    while (splits < kMaxSplits && tiles * splits * 2 <= Cfg::kPerSm * 152 && p.k_iters >= 8 * splits) splits *= 2;
+    p.stage_bytes = static_cast<int32_t>(round_up(kAcc * kTileA + p.rows_pad * 128, 1024));
+    p.stages = Cfg::kRing / p.stage_bytes < kMaxStages ? Cfg::kRing / p.stage_bytes : kMaxStages;
     static bool set[kMaxDevices] = {};
     int dev = 0;
     SPCONV_CHECK_CUDA(cudaGetDevice(&dev));
     if (dev < 0 || dev >= kMaxDevices) return SPCONV_ERR_UNSUPPORTED;
     if (!set[dev]) {
-        SPCONV_CHECK_CUDA(cudaFuncSetAttribute(k_dense_few<DUAL, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 2048));
+        SPCONV_CHECK_CUDA(cudaFuncSetAttribute(k_dense_few<DUAL, E4M3, BIG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Cfg::kRing + 1024));
         set[dev] = true;
     }
     cudaLaunchAttribute at[2] = {pdl_attr(), {}};
@@ -217,20 +260,32 @@ int launch(const FewArgs& p, int32_t tiles, int32_t splits, size_t smem, cudaStr
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(splits));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    // (at most the ring's room: the sums fit it too)
+    const size_t ring = static_cast<size_t>(p.stages) * p.stage_bytes, sums = static_cast<size_t>(kAcc) * p.rows * kChannels * 4;
+    cfg.dynamicSmemBytes = (ring > sums ? ring : sums) + 1024;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 2;
     count_launch();
-    return cuda_status(cudaLaunchKernelEx(&cfg, k_dense_few<DUAL, E4M3>, p));
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_dense_few<DUAL, E4M3, BIG>, static_cast<const FewArgs&>(p)));
+}
+
+template <bool DUAL, bool E4M3>
+int launch(FewArgs& p, cudaStream_t s) {
+    return p.rows <= FewConfig<DUAL, false>::kRows ? launch<DUAL, E4M3, false>(p, s) : launch<DUAL, E4M3, true>(p, s);
 }
 
 }  // namespace
 
 bool dense_few_takes(const DenseOp& op) {
     if (op.k_sources != 1 || op.n_sources != 1 || !op.a.k_major) return false;
-    if (op.epi == kEpiGated) return op.m <= kMaxRowsDual;
-    return op.epi == kEpiLinear && op.m <= kMaxRows;
+    if (op.epi != kEpiGated && op.epi != kEpiLinear) return false;
+    const bool dual = op.epi == kEpiGated;
+    if (op.m <= (dual ? FewConfig<true, false>::kRows : FewConfig<false, false>::kRows)) return true;
+    // Beyond, the pairs' tiles of 256 rows are no longer mostly empty and win where
+    // there are enough of them: 256 rows x 2048 x 8192 (64 tiles of channels) 15.4 us,
+    // against 20.3 here; x 4096 x 4096 (32 tiles) 21.9, against 16.3
+    return op.m <= (dual ? FewConfig<true, true>::kRows : FewConfig<false, true>::kRows) && ceil_div(op.n, kChannels) <= 38;
 }
 
 int dense_few_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
@@ -252,21 +307,12 @@ int dense_few_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     p.out = static_cast<__nv_bfloat16*>(op.out[0]);
     p.ld_out = op.ld_out;
     p.status = status;
-    const int32_t tiles = static_cast<int32_t>(ceil_div(op.n, kChannels));
-    // As many CTAs as two per SM, each with four steps of K at least
-    int32_t splits = 1;
-    while (splits < kMaxSplits && tiles * splits * 2 <= 2 * 152 && p.k_iters >= 8 * splits) splits *= 2;
-    const int acc = dual ? 2 : 1;
-    p.stage_bytes = static_cast<int32_t>(round_up(acc * kTileA + p.rows_pad * 128, 1024));
-    p.stages = kRing / p.stage_bytes < kMaxStages ? kRing / p.stage_bytes : kMaxStages;
-    for (int a = 0; a < acc; ++a)
+    for (int a = 0; a < (dual ? 2 : 1); ++a)
         SPCONV_CHECK(op.b.k_major ? make_tensor_map(&p.w[a], op.b.p[a], es, op.k, op.n, op.b.ld, kChannels)
                                   : make_tensor_map(&p.w[a], op.b.p[a], es, op.n, op.k, op.b.ld, 64));
     SPCONV_CHECK(make_tensor_map(&p.x, op.a.p[0], es, op.k, op.m, op.a.ld, p.rows_pad));
-    const size_t ring = static_cast<size_t>(p.stages) * p.stage_bytes, sums = static_cast<size_t>(acc) * op.m * kChannels * 4;
-    const size_t smem = (ring > sums ? ring : sums) + 1024;
-    if (dual) return eight ? launch<true, true>(p, tiles, splits, smem, s) : launch<true, false>(p, tiles, splits, smem, s);
-    return eight ? launch<false, true>(p, tiles, splits, smem, s) : launch<false, false>(p, tiles, splits, smem, s);
+    if (dual) return eight ? launch<true, true>(p, s) : launch<true, false>(p, s);
+    return eight ? launch<false, true>(p, s) : launch<false, false>(p, s);
 }
 
 }  // namespace spconv
