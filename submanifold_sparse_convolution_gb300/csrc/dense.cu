@@ -75,16 +75,17 @@ __device__ __forceinline__ void add_slices(const float* q, int32_t splits, int64
 // W elements of one row of one output (W = 4 where n % 4 == 0).
 template <int W>
 __device__ __forceinline__ void sum_slices(const SliceSums& a, int32_t block) {
-    const int64_t mn = a.m * a.n, slice = mn * a.outputs;
+    const int64_t mn = a.m * a.n, one = a.m * a.ld_part, slice = one * a.outputs;
     const bool gated = a.epi == kEpiGated;
     const int64_t i = (static_cast<int64_t>(block) * 256 + threadIdx.x) * W;
-    if (i >= (gated ? mn : slice)) return;
+    if (i >= (gated ? mn : mn * a.outputs)) return;
     const int src = !gated && i >= mn;
     const int64_t r = i - (src ? mn : 0);
     const int64_t row = mn < 0x7FFFFFFF ? static_cast<uint32_t>(r) / static_cast<uint32_t>(a.n) : r / a.n, col = r - row * a.n;
     float z[W], u[W];
-    add_slices<W>(a.part + i, a.splits, slice, z);
-    if (gated) add_slices<W>(a.part + mn + i, a.splits, slice, u);
+    const float* q = a.part + src * one + row * a.ld_part + col;
+    add_slices<W>(q, a.splits, slice, z);
+    if (gated) add_slices<W>(q + one, a.splits, slice, u);
     if (a.row_scale) {
         const float rs = a.row_scale[row];
 #pragma unroll

@@ -82,7 +82,7 @@ struct TcArgs {
     const float* col_scale[2];
     const float* bias;
     float* part;           // kEpiActGrad: column sums of 32 rows each, [8 tiles_m][n], or null;
-                           // kEpiPlain: with splits > 1, [splits][n_sources][m][n]
+                           // kEpiPlain: with splits > 1, [splits][n_sources][m][n] by c[0]
     int32_t tiles, units;  // of the product; tiles splits
 };
 
@@ -405,6 +405,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                 const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                     static_cast<uint32_t>(buf * 256 + c * kBC);
                 if (!ok) break;
+                if (to_part) {
+                    // 32 columns of fp32 fill the staging buffer
+#pragma unroll 1
+                    for (int q = 0; q < 2 && n0 + q * 32 < p.n; ++q) {
+                        if (lane == 0) ptx::bulk_wait_read();
+                        __syncwarp();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t z[CW];
+                            ptx::tmem_ld_32x32b_x16(ta + q * 32 + h * CW, z);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < CW; j += 4)
+                                *reinterpret_cast<uint4*>(stage0 + row_off + (((h * 4 + j / 4) ^ sw) << 4)) =
+                                    make_uint4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::tma_store_3d(&p.c[0], n0 + q * 32, m0, t.split * p.n_sources + t.src, st0);
+                            ptx::bulk_commit();
+                        }
+                    }
+                    continue;
+                }
 #pragma unroll 2
                 for (int h = 0; h < kBC / CW; ++h) {
                     uint32_t z[CW], w[CW];
@@ -413,22 +438,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                     ptx::tmem_ld_wait();
                     const int32_t nc = n0 + h * CW;
                     const uint32_t piece = h * (CW / 8);   // first 16-byte piece of these columns in a row
-                    if (to_part) {
-                        if (row_live) {
-                            float* dst = p.part + ((static_cast<int64_t>(t.split) * p.n_sources + t.src) * p.m + row) * p.n + nc;
-                            if (p.n % 4 == 0) {
-#pragma unroll
-                                for (int j = 0; j < CW; j += 4)
-                                    if (nc + j < p.n)
-                                        *reinterpret_cast<uint4*>(dst + j) = make_uint4(z[j], z[j + 1], z[j + 2], z[j + 3]);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < CW; ++j)
-                                    if (nc + j < p.n) dst[j] = __uint_as_float(z[j]);
-                            }
-                        }
-                        continue;
-                    }
                     // extra: this thread's CW columns, 16-byte pieces in the 128-byte swizzle
                     uint32_t x[CW / 2];
                     if (kExtra) {
@@ -493,14 +502,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                         }
                     }
                 }
-                if (!to_part) {
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        ptx::tma_store_2d(&p.c[EPI == kEpiPlain ? t.src : 0], n0, m0, st0);
-                        if (EPI == kEpiGatedGrad) ptx::tma_store_2d(&p.c[1], n0, m0, st0 + kStaging / 2);
-                        ptx::bulk_commit();
-                    }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::tma_store_2d(&p.c[EPI == kEpiPlain ? t.src : 0], n0, m0, st0);
+                    if (EPI == kEpiGatedGrad) ptx::tma_store_2d(&p.c[1], n0, m0, st0 + kStaging / 2);
+                    ptx::bulk_commit();
                 }
             }
             wait_acc();   // (a warp without a block of this tile still takes its turn)
@@ -635,6 +642,23 @@ Cut best_cut(const DenseOp& op, bool dual, int outputs, bool may_split) {
     return best;
 }
 
+// Rows of the fp32 partial results: whole 16 bytes.
+int64_t part_ld(int64_t n) { return static_cast<int64_t>(round_up(static_cast<size_t>(n), 4)); }
+
+// The slices [slices][m][part_ld(n)], stored in boxes of 32 columns x 32 rows,
+// clipped at each slice's last row.
+int make_part_map(CUtensorMap* map, float* base, int64_t n, int64_t m, int32_t slices) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return SPCONV_ERR_CUDA;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(m), static_cast<cuuint64_t>(slices)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(part_ld(n)) * 4, static_cast<cuuint64_t>(part_ld(n) * m) * 4};
+    const cuuint32_t box[3] = {32, 32, 1}, unit[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, unit,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SPCONV_OK : SPCONV_ERR_CUDA;
+}
+
 // kEpiGated with K cut: gate and up as two outputs of a plain product.
 DenseOp as_plain(const DenseOp& op) {
     DenseOp o = op;
@@ -750,7 +774,7 @@ int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_
         units += l.g[i].units;
         off[i] = bytes;
         if (l.g[i].splits > 1)
-            bytes += round_up(static_cast<size_t>(l.g[i].m) * l.g[i].n * l.g[i].n_sources * l.g[i].splits * 4, 256);
+            bytes += round_up(static_cast<size_t>(l.g[i].m) * part_ld(l.g[i].n) * l.g[i].n_sources * l.g[i].splits * 4, 256);
     }
     Scratch part(bytes, s);
     if (part.failed()) return SPCONV_ERR_OOM;
@@ -760,6 +784,8 @@ int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_
         if (p.splits == 1) continue;
         const DenseOp& op = ops[order[i]];
         p.part = part.as<float>(off[i]);
+        SPCONV_CHECK(make_part_map(&p.c[0], p.part, p.n, p.m, p.splits * p.n_sources));
+        sums[i].ld_part = part_ld(p.n);
         sums[i].part = p.part;
         sums[i].splits = p.splits;
         sums[i].m = p.m;

@@ -322,6 +322,12 @@ __device__ __forceinline__ void tma_store_2d(const void* map, int32_t x, int32_t
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d(const void* map, int32_t x, int32_t y, int32_t z, uint32_t src_smem) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(src_smem)
+                 : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // all of this thread's bulk stores have read their shared memory / are complete
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }

@@ -262,10 +262,11 @@ inline bool tma_ok(const void* p, int64_t ld, size_t es) {
 int64_t column_part_rows(int64_t m, int64_t n);
 int column_parts(const void* v, int64_t ld, int64_t m, int64_t n, float* part, cudaStream_t s);
 // What is left after partial results: for up to two products the sums of their
-// slices of K (fp32 [splits][outputs][m][n], outputs one or two), the epilogue
-// and the rounding; and column sums.  One launch.
+// slices of K (fp32 [splits][outputs][m][ld_part], outputs one or two), the
+// epilogue and the rounding; and column sums.  One launch.
 struct SliceSums {
     const float* part = nullptr;
+    int64_t ld_part = 0;
     int32_t splits = 0;
     int64_t m = 0, n = 0;
     int32_t outputs = 0;
