@@ -607,8 +607,9 @@ int make_tensor_map_blocks(CUtensorMap* map, const void* base, int64_t inner, in
 namespace {
 
 // How a product is cut into units, and a model of its time in us.  A step of K
-// of a 256-column tile takes 0.33 us and one of a 128-column tile 0.26 (both
-// bound by the loads: 32 and 24 KB per SM and step; 2048 rows x 8192 x 1024);
+// of a 256-column tile takes 0.37 us and one of a 128-column tile 0.34 (both
+// bound by the loads: 32 and 24 KB per SM and step; 1024 and 300 rows x 4096 x
+// 4096);
 // a launch of sums takes 3 us and the fp32 partial results move at 6 TB/s.
 struct Cut {
     int32_t hb = 128, splits = 1, split_iters = 1;
@@ -628,7 +629,7 @@ Cut best_cut(const DenseOp& op, bool dual, int outputs, bool may_split) {
         for (int64_t splits = 1; splits == 1 || splits <= most; ++splits) {
             const int64_t iters = ceil_div(k_total, splits), used = ceil_div(k_total, iters);
             if (used != splits) continue;   // the same cut as a smaller count
-            double us = static_cast<double>(ceil_div(tiles * splits, kPairs) * iters) * (hb == 128 ? 0.33 : 0.26);
+            double us = static_cast<double>(ceil_div(tiles * splits, kPairs) * iters) * (hb == 128 ? 0.37 : 0.34);
             if (splits > 1) us += 3.0 + 8.0e-6 / 6.0 * static_cast<double>(op.m * op.n * outputs) * static_cast<double>(splits);
             if (us < best.us) {
                 best.hb = hb;
