@@ -8,36 +8,25 @@ namespace {
 
 __device__ int32_t g_rows_status;   // kStatus* bits of the row-wise operators' bounded waits
 
-// ---- copies between aligned and unaligned rows ------------------------------------
-// Eight elements per thread; the side whose rows are 16-byte aligned moves as one
-// vector.
-template <typename T>
-__global__ void __launch_bounds__(256) k_copy_rows(const T* src, int64_t ld_src, T* dst, int64_t ld_dst, int64_t rows,
-                                                   int64_t cols, int64_t row_groups, bool vec_src, bool vec_dst) {
+// ---- copies to aligned rows ---------------------------------------------------------
+// A warp per 256 elements E of a row, neighbouring lanes on neighbouring
+// elements: rows of any alignment move in whole 32-byte sectors.
+template <typename E>
+__global__ void __launch_bounds__(256) k_copy_rows(const E* src, int64_t ld_src, E* dst, int64_t ld_dst, int64_t rows, int32_t cols,
+                                                   int32_t row_warps) {
     pdl_wait();
     pdl_trigger();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t r = i / row_groups, c = (i - r * row_groups) * 8;
+    const int64_t w = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+    const int64_t r = w / row_warps;
     if (r >= rows) return;
-    struct alignas(8 * sizeof(T)) V {
-        T v[8];
-    } t;
-    const T* s = src + r * ld_src + c;
-    T* d = dst + r * ld_dst + c;
-    const bool whole = c + 8 <= cols;
-    if (vec_src && whole) {
-        t = *reinterpret_cast<const V*>(s);
-    } else {
+    const int32_t c0 = static_cast<int32_t>(w - r * row_warps) * 256 + (threadIdx.x & 31);
+    E v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t.v[j] = c + j < cols ? s[j] : T(0);
-    }
-    if (vec_dst && whole) {
-        *reinterpret_cast<V*>(d) = t;
-    } else {
+    for (int k = 0; k < 8; ++k)
+        if (c0 + 32 * k < cols) v[k] = src[r * ld_src + c0 + 32 * k];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < cols) d[j] = t.v[j];
-    }
+    for (int k = 0; k < 8; ++k)
+        if (c0 + 32 * k < cols) dst[r * ld_dst + c0 + 32 * k] = v[k];
 }
 
 // ---- column sums ----------------------------------------------------------------
@@ -109,13 +98,19 @@ __device__ __forceinline__ void sum_slices(const SliceSums& a, int32_t block) {
 #pragma unroll
         for (int j = 0; j < W; ++j) z[j] *= u[j];
     } else if (a.extra) {
-        const V x = *reinterpret_cast<const V*>(a.extra + row * a.ld_extra + col);
+        const V x = *reinterpret_cast<const V*>(a.extra + row * a.ld_extra + col);   // (tma_ok)
 #pragma unroll
         for (int j = 0; j < W; ++j) z[j] += __bfloat162float(x.v[j]);
     }
 #pragma unroll
     for (int j = 0; j < W; ++j) o.v[j] = __float2bfloat16_rn(z[j]);
-    *reinterpret_cast<V*>(a.out[src] + row * a.ld + col) = o;
+    __nv_bfloat16* out = a.out[src] + row * a.ld + col;
+    if (a.vec_out) {
+        *reinterpret_cast<V*>(out) = o;
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) out[j] = o.v[j];
+    }
 }
 
 __global__ void __launch_bounds__(256) k_finish(const FinishArgs a) {
@@ -126,7 +121,6 @@ __global__ void __launch_bounds__(256) k_finish(const FinishArgs a) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
         if (b < a.blocks[g]) {
-            // (rows of the slices, of extra and of the output are aligned for four: n % 4 == 0 and tma_ok)
             if (a.slices[g].n % 4 == 0) sum_slices<4>(a.slices[g], b);
             else sum_slices<1>(a.slices[g], b);
             return;
@@ -234,17 +228,22 @@ __global__ void __launch_bounds__(256) k_quantize_weight(const __nv_bfloat16* w,
     }
 }
 
-int copy_rows(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t rows, int64_t cols, size_t es, cudaStream_t s) {
-    const int64_t groups = ceil_div(cols, 8), blocks = ceil_div(rows * groups, 256);
+template <typename E>
+int copy_rows_as(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t rows, int64_t bytes, size_t es, cudaStream_t s) {
+    const int64_t e = sizeof(E), cols = bytes / e, row_warps = ceil_div(cols, 256), blocks = ceil_div(rows * row_warps, 8);
     if (blocks > 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
-    auto vec = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % (8 * es) == 0 && ld % 8 == 0; };
-    const bool vs = vec(src, ld_src), vd = vec(dst, ld_dst);
-    const dim3 grid(static_cast<unsigned>(blocks));
-    if (es == 1)
-        return launch_pdl(k_copy_rows<uint8_t>, grid, 256, 0, s, static_cast<const uint8_t*>(src), ld_src,
-                          static_cast<uint8_t*>(dst), ld_dst, rows, cols, groups, vs, vd);
-    return launch_pdl(k_copy_rows<uint16_t>, grid, 256, 0, s, static_cast<const uint16_t*>(src), ld_src,
-                      static_cast<uint16_t*>(dst), ld_dst, rows, cols, groups, vs, vd);
+    return launch_pdl(k_copy_rows<E>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, static_cast<const E*>(src),
+                      ld_src * static_cast<int64_t>(es) / e, static_cast<E*>(dst), ld_dst * static_cast<int64_t>(es) / e, rows,
+                      static_cast<int32_t>(cols), static_cast<int32_t>(row_warps));
+}
+
+// dst has 16-byte aligned rows; the copy takes the largest elements that src's allow.
+int copy_rows(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t rows, int64_t cols, size_t es, cudaStream_t s) {
+    const uintptr_t all = reinterpret_cast<uintptr_t>(src) | static_cast<uintptr_t>(ld_src * es) | static_cast<uintptr_t>(cols * es);
+    const int64_t bytes = cols * static_cast<int64_t>(es);
+    if (all % 4 == 0) return copy_rows_as<uint32_t>(src, ld_src, dst, ld_dst, rows, bytes, es, s);
+    if (all % 2 == 0) return copy_rows_as<uint16_t>(src, ld_src, dst, ld_dst, rows, bytes, es, s);
+    return copy_rows_as<uint8_t>(src, ld_src, dst, ld_dst, rows, bytes, es, s);
 }
 
 }  // namespace
@@ -265,41 +264,26 @@ int rows_status_word(int32_t** word) {
 
 namespace {
 
-// The tensor maps need 16-byte aligned rows.  Matrices without them (odd
-// channel counts, strides or addresses) are copied to rows that have them, and
-// an output whose rows are not whole 16 bytes is copied back: one extra pass
-// over that matrix.
+// The tensor maps need 16-byte aligned rows.  Operands without them (odd
+// channel counts, strides or addresses) are copied to rows that have them: one
+// extra pass over that matrix.
 class AlignedOp {
 public:
-    DenseOp op;   // what to run between begin and end
+    DenseOp op;   // what to run
 
     int begin(const DenseOp& given, cudaStream_t s) {
-        given_ = op = given;
+        op = given;
         const size_t es = op.dtype == SPCONV_E4M3 ? 1 : 2;
         const bool dual = op.epi == kEpiGated || op.epi == kEpiGatedGrad;
         const int na = op.k_sources, nb = dual || op.k_sources == 2 || op.n_sources == 2 ? 2 : 1;
-        outs_ = op.epi == kEpiGatedGrad || op.n_sources == 2 ? 2 : 1;
         const Matrix a = op.a.k_major ? plan(op.a.p, na, op.a.ld, op.m, op.k, es) : plan(op.a.p, na, op.a.ld, op.k, op.m, es);
         const Matrix b = op.b.k_major ? plan(op.b.p, nb, op.b.ld, op.n, op.k, es) : plan(op.b.p, nb, op.b.ld, op.k, op.n, es);
         const Matrix x = plan(&op.extra, op.extra ? 1 : 0, op.ld_extra, op.m, op.n, 2);
-        // a tensor-map store clips a row at 16 bytes, not at an element
-        const Matrix c = plan(op.out, outs_, op.ld_out, op.m, op.n, 2, op.n % 8 != 0 && !op.out_padded);
-        copy_back_ = c.move;
         if (bytes_ == 0) return SPCONV_OK;
         if (!buf_.alloc(bytes_, s)) return SPCONV_ERR_OOM;
         SPCONV_CHECK(bring(a, op.a.p, na, &op.a.ld, s));
         SPCONV_CHECK(bring(b, op.b.p, nb, &op.b.ld, s));
-        SPCONV_CHECK(bring(x, &op.extra, 1, &op.ld_extra, s));
-        if (c.move) {
-            for (int i = 0; i < outs_; ++i) op.out[i] = buf_.as<void>(c.off[i]);
-            op.ld_out = c.ld();
-        }
-        return SPCONV_OK;
-    }
-    int end(cudaStream_t s) const {
-        for (int i = 0; copy_back_ && i < outs_; ++i)
-            SPCONV_CHECK(copy_rows(op.out[i], op.ld_out, given_.out[i], given_.ld_out, op.m, op.n, 2, s));
-        return SPCONV_OK;
+        return bring(x, &op.extra, 1, &op.ld_extra, s);
     }
 
 private:
@@ -310,8 +294,8 @@ private:
         size_t off[2];
         int64_t ld() const { return static_cast<int64_t>(round_up(static_cast<size_t>(cols), 16 / es)); }
     };
-    Matrix plan(const void* const* ptr, int count, int64_t ld, int64_t rows, int64_t cols, size_t e, bool move = false) {
-        Matrix t{rows, cols, e, move, {0, 0}};
+    Matrix plan(const void* const* ptr, int count, int64_t ld, int64_t rows, int64_t cols, size_t e) {
+        Matrix t{rows, cols, e, false, {0, 0}};
         for (int i = 0; i < count; ++i) t.move = t.move || !tma_ok(ptr[i], ld, e);
         for (int i = 0; t.move && i < count; ++i) {
             t.off[i] = bytes_;
@@ -329,11 +313,8 @@ private:
         return SPCONV_OK;
     }
 
-    DenseOp given_;
     Scratch buf_;
     size_t bytes_ = 0;
-    int outs_ = 1;
-    bool copy_back_ = false;
 };
 
 }  // namespace
@@ -344,10 +325,8 @@ int dense_run(const DenseOp& op, cudaStream_t s) {
     SPCONV_CHECK(rows_status_word(&status));
     AlignedOp a;
     SPCONV_CHECK(a.begin(op, s));
-    SPCONV_CHECK(dense_few_takes(a.op) ? dense_few_run(a.op, status, s)
-                 : dense_tc_cuts(a.op) ? dense_tc_plain(&a.op, 1, {}, status, s)
-                                       : dense_tc_run(a.op, status, s));
-    return a.end(s);
+    if (dense_few_takes(a.op)) return dense_few_run(a.op, status, s);
+    return dense_tc_cuts(a.op) ? dense_tc_plain(&a.op, 1, {}, status, s) : dense_tc_run(a.op, status, s);
 }
 
 int dense_run_plain(const DenseOp* ops, int count, const ColumnSums& cols, cudaStream_t s) {
@@ -360,9 +339,7 @@ int dense_run_plain(const DenseOp* ops, int count, const ColumnSums& cols, cudaS
         SPCONV_CHECK(a[i].begin(ops[i], s));
         o[i] = a[i].op;
     }
-    SPCONV_CHECK(dense_tc_plain(o, count, cols, status, s));
-    for (int i = 0; i < count; ++i) SPCONV_CHECK(a[i].end(s));
-    return SPCONV_OK;
+    return dense_tc_plain(o, count, cols, status, s);
 }
 
 int finish_sums(const SliceSums* slices, int count, const ColumnSums& cols, cudaStream_t s) {
@@ -371,6 +348,7 @@ int finish_sums(const SliceSums* slices, int count, const ColumnSums& cols, cuda
     for (int i = 0; i < count; ++i) {
         a.slices[i] = slices[i];
         const SliceSums& t = slices[i];
+        a.slices[i].vec_out = t.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(t.out[0]) | reinterpret_cast<uintptr_t>(t.out[1])) % 8 == 0;
         const int64_t elems = t.m * t.n * (t.epi == kEpiGated ? 1 : t.outputs);
         const int64_t b = t.splits ? ceil_div(elems, t.n % 4 == 0 ? 1024 : 256) : 0;
         if (b > 0x3FFFFFFF) return SPCONV_ERR_UNSUPPORTED;

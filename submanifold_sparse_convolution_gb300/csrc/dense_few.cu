@@ -50,6 +50,7 @@ struct FewArgs {
     int64_t ld_extra;
     __nv_bfloat16* out;
     int64_t ld_out;
+    int32_t vec_out;       // rows of out take 8-byte stores
     int32_t* status;
 };
 
@@ -221,11 +222,11 @@ __global__ void __launch_bounds__(kThreads, FewConfig<DUAL, BIG>::kPerSm) k_dens
                 y[j] = __float2bfloat16_rn(DUAL ? act_f<act>(z[0][j]) * z[kAcc - 1][j] : act_f<act>(z[0][j]) + x);
             }
         });
-        __nv_bfloat16* out = p.out + row * p.ld_out + n;   // (8-byte aligned: tma_ok)
-        if (n + 4 <= p.n) {
+        __nv_bfloat16* out = p.out + row * p.ld_out + n;
+        if (p.vec_out && n + 4 <= p.n) {
             *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
         } else {
-            for (int j = 0; n + j < p.n; ++j) out[j] = y[j];
+            for (int j = 0; j < 4 && n + j < p.n; ++j) out[j] = y[j];
         }
     }
     // no CTA's sums go away while another may still read them
@@ -306,6 +307,7 @@ int dense_few_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
     p.ld_extra = op.ld_extra;
     p.out = static_cast<__nv_bfloat16*>(op.out[0]);
     p.ld_out = op.ld_out;
+    p.vec_out = op.ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(op.out[0]) % 8 == 0;
     p.status = status;
     for (int a = 0; a < (dual ? 2 : 1); ++a)
         SPCONV_CHECK(op.b.k_major ? make_tensor_map(&p.w[a], op.b.p[a], es, op.k, op.n, op.b.ld, kChannels)

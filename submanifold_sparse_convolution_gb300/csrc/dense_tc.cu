@@ -84,6 +84,11 @@ struct TcArgs {
     float* part;           // kEpiActGrad: column sums of 32 rows each, [8 tiles_m][n], or null;
                            // kEpiPlain: with splits > 1, [splits][n_sources][m][n] by c[0]
     int32_t tiles, units;  // of the product; tiles splits
+    // outputs that a tensor-map store does not take (it wants 16-byte aligned rows
+    // and clips them at 16 bytes): stored a row at a time
+    int32_t direct;        // 0: by c[]; 1: pairs of columns; 2: single ones
+    __nv_bfloat16* out[2];
+    int64_t ld_out;
 };
 
 // A launch: one product, or two plain ones.  The units (tile, slice of K) of
@@ -155,6 +160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
     constexpr int kBC = block_columns(EPI);
     constexpr bool kDual = EPI == kEpiGated || EPI == kEpiGatedGrad;
     constexpr bool kExtra = EPI != kEpiGated && EPI != kEpiPlain;
+    constexpr bool kDirect = EPI == kEpiLinear || EPI == kEpiGated || EPI == kEpiPlain;   // (the others' outputs are the library's)
     constexpr bool kScaled = E4M3 && EPI != kEpiPlain;
     constexpr bool kBias = EPI == kEpiLinear || EPI == kEpiActGrad;
     constexpr int kBK = E4M3 ? 128 : 64;      // K elements of a stage
@@ -502,6 +508,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                         }
                     }
                 }
+                if (kDirect && p.direct) {
+                    __syncwarp();
+                    // lane l has columns 2 l and 2 l + 1 of a row: one 128-byte row a store
+                    __nv_bfloat16* out = p.out[EPI == kEpiPlain ? t.src : 0] + m0 * p.ld_out + n0 + 2 * lane;
+                    const int32_t left = static_cast<int32_t>(p.n - n0 - 2 * lane < 2 ? p.n - n0 - 2 * lane : 2);
+                    const int32_t rows = static_cast<int32_t>(p.m - m0 < 32 ? p.m - m0 : 32);
+#pragma unroll 4
+                    for (int32_t r = 0; r < rows; ++r, out += p.ld_out) {
+                        const uint32_t v = *reinterpret_cast<const uint32_t*>(stage0 + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
+                                                                              (lane & 3) * 4);
+                        if (left == 2 && p.direct == 1) {
+                            *reinterpret_cast<uint32_t*>(out) = v;
+                        } else {
+                            if (left > 0) out[0] = __ushort_as_bfloat16(static_cast<uint16_t>(v & 0xFFFFu));
+                            if (left > 1) out[1] = __ushort_as_bfloat16(static_cast<uint16_t>(v >> 16));
+                        }
+                    }
+                    __syncwarp();
+                    continue;
+                }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -713,9 +739,18 @@ int set_args(const DenseOp& op, bool may_split, TcArgs* args) {
     for (int i = 0; i < op.k_sources; ++i) SPCONV_CHECK(operand(&p.a[i], op.a, i, p.a_layout, op.m, kRowsA));
     for (int i = 0; i < ((dual || op.k_sources == 2 || op.n_sources == 2) ? 2 : 1); ++i)
         SPCONV_CHECK(operand(&p.b[i], op.b, i, p.b_layout, op.n, p.hb));
-    if (p.splits == 1)
-        for (int i = 0; i < ((op.epi == kEpiGatedGrad || op.n_sources == 2) ? 2 : 1); ++i)
-            SPCONV_CHECK(make_tensor_map(&p.c[i], op.out[i], 2, op.n, op.m, op.ld_out, 32, 2 * block_columns(op.epi)));
+    const int outs = op.epi == kEpiGatedGrad || op.n_sources == 2 ? 2 : 1;
+    uintptr_t at = static_cast<uintptr_t>(op.ld_out) * 2;
+    bool mapped = op.n % 8 == 0 || op.out_padded;
+    for (int i = 0; i < outs; ++i) {
+        mapped = mapped && tma_ok(op.out[i], op.ld_out, 2);
+        at |= reinterpret_cast<uintptr_t>(op.out[i]);
+        p.out[i] = static_cast<__nv_bfloat16*>(op.out[i]);
+    }
+    p.ld_out = op.ld_out;
+    p.direct = mapped ? 0 : at % 4 == 0 ? 1 : 2;
+    for (int i = 0; p.splits == 1 && mapped && i < outs; ++i)
+        SPCONV_CHECK(make_tensor_map(&p.c[i], op.out[i], 2, op.n, op.m, op.ld_out, 32, 2 * block_columns(op.epi)));
     if (op.extra && p.splits == 1) SPCONV_CHECK(make_tensor_map(&p.x, op.extra, 2, op.n, op.m, op.ld_extra, 32, 2 * block_columns(op.epi)));
     return SPCONV_OK;
 }

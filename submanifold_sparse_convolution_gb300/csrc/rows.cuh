@@ -241,7 +241,7 @@ struct ColumnSums {
 int dense_run(const DenseOp& op, cudaStream_t s);
 // Up to two plain products in one launch, and column sums, if any, with them.
 int dense_run_plain(const DenseOp* ops, int count, const ColumnSums& cols, cudaStream_t s);
-// On the tensor cores (dense_tc.cu); operands, extra and out satisfy tma_ok.
+// On the tensor cores (dense_tc.cu); operands and extra satisfy tma_ok.
 int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s);
 // (one product may have the epilogue of kEpiLinear or kEpiGated: dense_tc_cuts
 // says whether cutting its K is worth the workspace; plain ones always go here)
@@ -272,6 +272,7 @@ struct SliceSums {
     int32_t outputs = 0;
     __nv_bfloat16* out[2] = {nullptr, nullptr};
     int64_t ld = 0;
+    bool vec_out = false;   // (set by finish_sums: the rows take 8-byte stores)
     // kEpiLinear's or kEpiGated's terms (DenseOp); kEpiGated makes one output of two
     int32_t epi = kEpiLinear, act = SPCONV_ACT_NONE;
     const float* row_scale = nullptr;
