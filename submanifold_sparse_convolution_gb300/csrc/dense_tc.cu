@@ -525,6 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                             if (left > 1) out[1] = __ushort_as_bfloat16(static_cast<uint16_t>(v >> 16));
                         }
                     }
+                    ptx::fence_proxy_async_smem();   // (the next residual's copy comes into the same bytes)
                     __syncwarp();
                     continue;
                 }

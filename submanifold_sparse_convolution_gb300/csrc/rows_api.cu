@@ -32,6 +32,9 @@ struct Rows {
     bool same(const Rows& o) const { return p == o.p && (ld == o.ld || n <= 1); }
 };
 
+// fp32 values in a row (absent: null, which overlaps nothing)
+Rows vec(const float* p, int64_t c) { return {p, 1, c, c, 4}; }
+
 size_t size_of(int32_t dtype) { return dtype == SPCONV_FP32 ? 4 : dtype == SPCONV_E4M3 ? 1 : 2; }
 
 bool bad_sizes(int64_t n, int32_t c_in, int32_t c_out) {
@@ -111,11 +114,11 @@ int spconv_rms_norm(const void* x_dev, int64_t ld_x, const void* residual_dev, i
     if ((scale_dev != nullptr) != (out_dtype == SPCONV_E4M3) || bad_vec(scale_dev)) return SPCONV_ERR_INVALID_ARG;
     const size_t es = size_of(dtype);
     const Rows x{x_dev, n, c, ld_x, es}, res{residual_dev, n, c, ld_residual, es}, sum{sum_dev, n, c, c, es},
-        out{out_dev, n, c, c, size_of(out_dtype)}, scale{scale_dev, n, 1, 1, 4};
+        out{out_dev, n, c, c, size_of(out_dtype)}, scale = vec(scale_dev, n), w = vec(weight_dev, c);
     if (!x.ok() || !out.ok() || !weight_dev || bad_vec(weight_dev)) return SPCONV_ERR_INVALID_ARG;
     if ((residual_dev && !res.ok()) || (sum_dev && !sum.ok())) return SPCONV_ERR_INVALID_ARG;
     if (out.overlaps(x) || out.overlaps(res) || out.overlaps(sum) || scale.overlaps(out) || scale.overlaps(x) ||
-        scale.overlaps(res) || scale.overlaps(sum))
+        scale.overlaps(res) || scale.overlaps(sum) || w.overlaps(out) || w.overlaps(sum) || w.overlaps(scale))
         return SPCONV_ERR_ALIAS;
     if ((sum.overlaps(x) && !sum.same(x)) || (sum.overlaps(res) && !sum.same(res))) return SPCONV_ERR_ALIAS;
     return norm_forward({x_dev, ld_x, residual_dev, ld_residual, weight_dev, n, c, dtype, eps, sum_dev, out_dev, out_dtype,
@@ -134,11 +137,11 @@ int spconv_rms_norm_backward(const void* dy_dev, int64_t ld_dy, const void* x_de
     if (n == 0) return zero(dweight_dev, static_cast<size_t>(c) * 4, s);
     const size_t es = size_of(dtype);
     const Rows dy{dy_dev, n, c, ld_dy, es}, x{x_dev, n, c, ld_x, es}, dres{dres_dev, n, c, ld_dres, es},
-        dx{dx_dev, n, c, c, es}, dw{dweight_dev, 1, c, c, 4};
+        dx{dx_dev, n, c, c, es}, dw = vec(dweight_dev, c), w = vec(weight_dev, c);
     if (!dy.ok() || !x.ok() || !dx.ok() || !weight_dev || bad_vec(weight_dev) || (dres_dev && !dres.ok()))
         return SPCONV_ERR_INVALID_ARG;
     if (dx.overlaps(x) || dx.overlaps(dy) || (dx.overlaps(dres) && !dx.same(dres)) || dw.overlaps(dx) || dw.overlaps(x) ||
-        dw.overlaps(dy) || dw.overlaps(dres))
+        dw.overlaps(dy) || dw.overlaps(dres) || w.overlaps(dx) || w.overlaps(dw))
         return SPCONV_ERR_ALIAS;
     return norm_backward({dy_dev, ld_dy, x_dev, ld_x, weight_dev, dres_dev, ld_dres, n, c, dtype, eps, dx_dev, dweight_dev}, s);
 }
@@ -154,7 +157,9 @@ int spconv_linear(const void* x_dev, int64_t ld_x, const float* x_scale_dev, con
     const Rows x{x_dev, n, c_in, ld_x, es}, w{w_dev, 1, int64_t(c_in) * c_out, int64_t(c_in) * c_out, es},
         res{residual_dev, n, c_out, ld_residual, 2}, out{out_dev, n, c_out, ld_out, 2};
     if (!x.ok() || !w.ok() || !out.ok() || (residual_dev && !res.ok())) return SPCONV_ERR_INVALID_ARG;
-    if (out.overlaps(x) || out.overlaps(w) || (out.overlaps(res) && !out.same(res))) return SPCONV_ERR_ALIAS;
+    if (out.overlaps(x) || out.overlaps(w) || (out.overlaps(res) && !out.same(res)) || out.overlaps(vec(bias_dev, c_out)) ||
+        out.overlaps(vec(x_scale_dev, n)) || out.overlaps(vec(w_scale_dev, c_out)))
+        return SPCONV_ERR_ALIAS;
     DenseOp op = product(x, w_dev, c_out, dtype);
     op.row_scale = x_scale_dev;
     op.col_scale[0] = w_scale_dev;
@@ -181,12 +186,13 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
         return zero(dbias_dev, static_cast<size_t>(c_out) * 4, s);
     }
     const Rows dy{dy_dev, n, c_out, ld_dy, 2}, x{x_dev, n, c_in, ld_x, 2}, w{w_dev, 1, wn, wn, 2};
-    const Rows outs[3] = {{dx_dev, n, c_in, c_in, 2}, {dw_dev, 1, wn, wn, 2}, {dbias_dev, 1, c_out, c_out, 4}};
+    const Rows outs[3] = {{dx_dev, n, c_in, c_in, 2}, {dw_dev, 1, wn, wn, 2}, vec(dbias_dev, c_out)};
     if (!dy.ok() || !x.ok() || !w.ok()) return SPCONV_ERR_INVALID_ARG;
     for (int i = 0; i < 3; ++i) {
         if (!outs[i].p) continue;
         if (!outs[i].ok()) return SPCONV_ERR_INVALID_ARG;
-        if (outs[i].overlaps(dy) || outs[i].overlaps(x) || outs[i].overlaps(w)) return SPCONV_ERR_ALIAS;
+        if (outs[i].overlaps(dy) || outs[i].overlaps(x) || outs[i].overlaps(w) || outs[i].overlaps(vec(bias_dev, c_out)))
+            return SPCONV_ERR_ALIAS;
         for (int j = 0; j < i; ++j)
             if (outs[i].overlaps(outs[j])) return SPCONV_ERR_ALIAS;
     }
@@ -247,7 +253,9 @@ int spconv_gated_ffn(const void* x_dev, int64_t ld_x, const float* x_scale_dev, 
     const Rows x{x_dev, n, c_in, ld_x, es}, wg{w_gate_dev, 1, wn, wn, es}, wu{w_up_dev, 1, wn, wn, es},
         out{out_dev, n, c_hidden, ld_out, 2};
     if (!x.ok() || !wg.ok() || !wu.ok() || !out.ok()) return SPCONV_ERR_INVALID_ARG;
-    if (out.overlaps(x) || out.overlaps(wg) || out.overlaps(wu)) return SPCONV_ERR_ALIAS;
+    if (out.overlaps(x) || out.overlaps(wg) || out.overlaps(wu) || out.overlaps(vec(x_scale_dev, n)) ||
+        out.overlaps(vec(gate_scale_dev, c_hidden)) || out.overlaps(vec(up_scale_dev, c_hidden)))
+        return SPCONV_ERR_ALIAS;
     DenseOp op = product(x, w_gate_dev, c_hidden, dtype);
     op.epi = kEpiGated;
     op.b.p[1] = w_up_dev;

@@ -86,3 +86,17 @@ def test_quantize_weight(lib):
     for kw, rc in [(dict(w=None), INVALID), (dict(ci=0), INVALID), (dict(out=None), INVALID), (dict(s=None), INVALID),
                    (dict(out=A), ALIAS), (dict(s=B), ALIAS)]:
         assert q(**kw) == rc, kw
+
+
+def test_outputs_on_vectors(lib):
+    """An output may not lie on a bias, a scale or a norm's weight either."""
+    cases = [linear(lib, bias=C + 8), linear(lib, dt=E4M3, xs=C + 64, ws=D), linear(lib, dt=E4M3, xs=D, ws=C),
+             gated(lib, dt=E4M3, xs=D + 16, gs=E, us=F), gated(lib, dt=E4M3, xs=E, gs=D, us=F),
+             gated(lib, dt=E4M3, xs=E, gs=F, us=D + 128)]
+    for dx, dw, db in ((D, E, F), (E, D, F), (E, F, D)):
+        cases.append(lib.spconv_linear_backward(A, 32, B, 64, C, 4, 64, 32, BF16, D, 2, dx, dw, db, None))
+    for s, out, odt, scale in ((C, E, BF16, None), (D, C + 64, BF16, None), (D, E, E4M3, C)):
+        cases.append(lib.spconv_rms_norm(A, 32, B, 32, C, 4, 32, BF16, 1e-6, s, out, odt, scale, None))
+    for dx, dw in ((C, E), (D, C)):
+        cases.append(lib.spconv_rms_norm_backward(A, 32, B, 32, C, None, 32, 4, 32, BF16, 1e-6, dx, dw, None))
+    assert cases == [ALIAS] * len(cases)
