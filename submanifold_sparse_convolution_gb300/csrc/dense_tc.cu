@@ -457,41 +457,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                             x[4 * q + 3] = v.w;
                         }
                     }
+                    // two columns at a time; the results take the places of what they are
+                    // made of: y in z, the second output in w
+                    auto pair_of = [](const uint32_t* v) { return F2(__uint_as_float(v[0]), __uint_as_float(v[1])); };
+                    auto keep = [](uint32_t* v, F2 y) {
+                        float lo, hi;
+                        y.get(lo, hi);
+                        v[0] = __float_as_uint(lo);
+                        v[1] = __float_as_uint(hi);
+                    };
+                    auto columns = [&](const Columns& v, int j) { return F2(v.at(h * CW + j), v.at(h * CW + j + 1)); };
                     if (kScaled) {
 #pragma unroll
-                        for (int j = 0; j < CW; ++j) {
-                            z[j] = __float_as_uint(__uint_as_float(z[j]) * (rs * scale0.at(h * CW + j)));
-                            if (kDual) w[j] = __float_as_uint(__uint_as_float(w[j]) * (rs * scale1.at(h * CW + j)));
+                        for (int j = 0; j < CW; j += 2) {
+                            keep(z + j, pair_of(z + j) * (F2(rs) * columns(scale0, j)));
+                            if (kDual) keep(w + j, pair_of(w + j) * (F2(rs) * columns(scale1, j)));
                         }
                     }
                     if (kBias && p.bias) {
 #pragma unroll
-                        for (int j = 0; j < CW; ++j) z[j] = __float_as_uint(__uint_as_float(z[j]) + bias.at(h * CW + j));
+                        for (int j = 0; j < CW; j += 2) keep(z + j, pair_of(z + j) + columns(bias, j));
                     }
-                    // the results take the places of what they are made of: y in z, the
-                    // second output in w
                     if (EPI != kEpiPlain) with_act(p.act, [&](auto act) {
 #pragma unroll
-                        for (int j = 0; j < CW; ++j) {
-                            const float zz = __uint_as_float(z[j]);
-                            const float ww = kDual ? __uint_as_float(w[j]) : 0.0f;
-                            const float xx = kExtra ? __uint_as_float(j & 1 ? (x[j / 2] & 0xFFFF0000u) : (x[j / 2] << 16)) : 0.0f;
-                            float y;
+                        for (int j = 0; j < CW; j += 2) {
+                            const F2 zz = pair_of(z + j), ww = kDual ? pair_of(w + j) : F2(0.0f);
+                            const F2 xx = kExtra ? F2(__uint_as_float(x[j / 2] << 16), __uint_as_float(x[j / 2] & 0xFFFF0000u)) : F2(0.0f);
+                            F2 y;
                             if (EPI == kEpiLinear) {
                                 y = act_f<act>(zz) + xx;
                             } else if (EPI == kEpiGated) {
                                 y = act_f<act>(zz) * ww;
                             } else {
-                                float a;
-                                const float slope = act_grad_f<act>(zz, &a);
+                                F2 a;
+                                const F2 slope = act_grad_f<act>(zz, &a);
                                 if (EPI == kEpiActGrad) {
-                                    y = row_live ? xx * slope : 0.0f;
+                                    y = row_live ? xx * slope : F2(0.0f);
                                 } else {
                                     y = xx * ww * slope;
-                                    w[j] = __float_as_uint(xx * a);
+                                    keep(w + j, xx * a);
                                 }
                             }
-                            z[j] = __float_as_uint(y);
+                            keep(z + j, y);
                         }
                     });
 #pragma unroll

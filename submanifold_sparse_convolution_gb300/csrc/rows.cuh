@@ -18,19 +18,76 @@ namespace spconv {
 // instructions: 2^x and 1/x of the special-function unit (relative error about
 // 2^-22, far below the bf16 rounding of whatever is stored) and FMAs.  2^x of a
 // large argument is infinity and 1/infinity is 0, which are the limits wanted.
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+//
+// The functions take one value (V = float) or two (V = F2): the tensor-core
+// epilogues issue the packed multiplies and adds, one instruction for both
+// values with the same roundings.
+struct F2 {
+    uint64_t v;
+    F2() = default;
+    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
+    // f of each value
+    template <typename F>
+    __device__ __forceinline__ F2 each(F&& f) const {
+        float a, b;
+        get(a, b);
+        return F2(f(a), f(b));
+    }
+    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
 }
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
 }
-__device__ __forceinline__ float sigmoid_f(float z) { return rcp_approx(1.0f + exp2_approx(-1.44269504f * z)); }
+__device__ __forceinline__ F2 fma_v(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float fma_v(float a, float b, float c) { return fmaf(a, b, c); }
 
-// tanh form of GELU: 0.5 (1 + tanh(v / 2)) is the logistic function of v
+template <typename F>
+__device__ __forceinline__ float each(float x, F&& f) { return f(x); }
+template <typename F>
+__device__ __forceinline__ F2 each(F2 x, F&& f) { return x.each(f); }
+template <typename F>
+__device__ __forceinline__ float each(float x, float y, F&& f) { return f(x, y); }
+template <typename F>
+__device__ __forceinline__ F2 each(F2 x, F2 y, F&& f) {
+    float a, b, c, d;
+    x.get(a, b);
+    y.get(c, d);
+    return F2(f(a, c), f(b, d));
+}
+
+template <typename V>
+__device__ __forceinline__ V exp2_approx(V x) {
+    return each(x, [](float t) {
+        float y;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
+        return y;
+    });
+}
+template <typename V>
+__device__ __forceinline__ V rcp_approx(V x) {
+    return each(x, [](float t) {
+        float y;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
+        return y;
+    });
+}
+template <typename V>
+__device__ __forceinline__ V sigmoid_f(V z) { return rcp_approx(V(1.0f) + exp2_approx(V(-1.44269504f) * z)); }
+
+// tanh form of GELU: 0.5 (1 + tanh(v / 2)) is the logistic function of
+// v = z (A + A B z^2)
 constexpr float kGeluA = 1.5957691216057308f;   // sqrt(8 / pi)
 constexpr float kGeluB = 0.044715f;
 
@@ -38,54 +95,55 @@ constexpr float kGeluB = 0.044715f;
 // exp(-z^2 / 2), with erfc of x = |z| / sqrt 2 from Abramowitz and Stegun,
 // Handbook of Mathematical Functions, 7.1.26: (a1 t + .. + a5 t^5) exp(-x^2),
 // t = 1 / (1 + p x), absolute error at most 1.5e-7.
-__device__ __forceinline__ float normal_cdf(float z, float* e) {
-    const float t = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
-    float q = fmaf(t, 1.061405429f, -1.453152027f);
-    q = fmaf(t, q, 1.421413741f);
-    q = fmaf(t, q, -0.284496736f);
-    q = fmaf(t, q, 0.254829592f);
-    *e = exp2_approx(-0.72134752f * z * z);   // log2(e) / 2
-    q = 0.5f * q * t * *e;
-    return z < 0.0f ? q : 1.0f - q;
+template <typename V>
+__device__ __forceinline__ V normal_cdf(V z, V* e) {
+    const V t = rcp_approx(each(z, [](float x) { return fmaf(0.3275911f * 0.70710678f, fabsf(x), 1.0f); }));
+    V q = fma_v(t, V(0.5f * 1.061405429f), V(0.5f * -1.453152027f));
+    q = fma_v(t, q, V(0.5f * 1.421413741f));
+    q = fma_v(t, q, V(0.5f * -0.284496736f));
+    q = fma_v(t, q, V(0.5f * 0.254829592f));
+    *e = exp2_approx(V(-0.72134752f) * z * z);   // log2(e) / 2
+    q = q * t * *e;
+    return each(z, q, [](float x, float y) { return x < 0.0f ? y : 1.0f - y; });
 }
 
-template <int ACT>
-__device__ __forceinline__ float act_f(float z) {
-    if (ACT == SPCONV_ACT_RELU) return z < 0.0f ? 0.0f : z;   // keeps NaN
+template <int ACT, typename V>
+__device__ __forceinline__ V act_f(V z) {
+    if (ACT == SPCONV_ACT_RELU) return each(z, [](float x) { return x < 0.0f ? 0.0f : x; });   // keeps NaN
     if (ACT == SPCONV_ACT_SILU) return z * sigmoid_f(z);
     if (ACT == SPCONV_ACT_GELU) {
-        float e;
+        V e;
         return z * normal_cdf(z, &e);
     }
-    if (ACT == SPCONV_ACT_GELU_TANH) return z * sigmoid_f(z * fmaf(kGeluA * kGeluB * z, z, kGeluA));
+    if (ACT == SPCONV_ACT_GELU_TANH) return z * sigmoid_f(z * fma_v(V(kGeluA * kGeluB) * z, z, V(kGeluA)));
     return z;
 }
 
 // *a = act(z), returns act'(z)
-template <int ACT>
-__device__ __forceinline__ float act_grad_f(float z, float* a) {
+template <int ACT, typename V>
+__device__ __forceinline__ V act_grad_f(V z, V* a) {
     if (ACT == SPCONV_ACT_RELU) {
-        *a = z < 0.0f ? 0.0f : z;
-        return z > 0.0f ? 1.0f : 0.0f;
+        *a = act_f<ACT>(z);
+        return each(z, [](float x) { return x > 0.0f ? 1.0f : 0.0f; });
     }
     if (ACT == SPCONV_ACT_SILU) {
-        const float s = sigmoid_f(z);
+        const V s = sigmoid_f(z);
         *a = z * s;
-        return fmaf(*a, 1.0f - s, s);
+        return fma_v(*a, fma_v(s, V(-1.0f), V(1.0f)), s);
     }
     if (ACT == SPCONV_ACT_GELU) {
-        float e;
-        const float phi = normal_cdf(z, &e);
+        V e;
+        const V phi = normal_cdf(z, &e);
         *a = z * phi;
-        return fmaf(0.39894228f * z, e, phi);
+        return fma_v(V(0.39894228f) * z, e, phi);
     }
     if (ACT == SPCONV_ACT_GELU_TANH) {
-        const float s = sigmoid_f(z * fmaf(kGeluA * kGeluB * z, z, kGeluA));
+        const V s = sigmoid_f(z * fma_v(V(kGeluA * kGeluB) * z, z, V(kGeluA)));
         *a = z * s;
-        return fmaf(fmaf(-*a, s, *a), fmaf(3.0f * kGeluA * kGeluB * z, z, kGeluA), s);
+        return fma_v(fma_v(*a * V(-1.0f), s, *a), fma_v(V(3.0f * kGeluA * kGeluB) * z, z, V(kGeluA)), s);
     }
     *a = z;
-    return 1.0f;
+    return V(1.0f);
 }
 
 // Calls f with the activation as a compile-time constant.
