@@ -643,8 +643,11 @@ namespace {
 // How a product is cut into units, and a model of its time in us.  A step of K
 // of a 256-column tile takes 0.37 us and one of a 128-column tile 0.34 (both
 // bound by the loads: 32 and 24 KB per SM and step; 1024 and 300 rows x 4096 x
-// 4096);
-// a launch of sums takes 3 us and the fp32 partial results move at 6 TB/s.
+// 4096).  Where there are few steps the epilogue bounds a tile: 1.6 and 1.1 us,
+// or 2.6 and 1.7 with an activation per column or with a residual (32371 x 96 x
+// 384 with SiLU in narrow tiles 12.6 us, in wide ones 14.2; x 128 x 512: 14.9 and
+// 14.7), and that of the last tile runs alone.  A launch of sums takes 3 us and the fp32
+// partial results move at 6 TB/s.
 struct Cut {
     int32_t hb = 128, splits = 1, split_iters = 1;
     int64_t tiles = 0;
@@ -654,16 +657,20 @@ struct Cut {
 Cut best_cut(const DenseOp& op, bool dual, int outputs, bool may_split) {
     const int64_t k_total = ceil_div(op.k, op.dtype == SPCONV_E4M3 ? 128 : 64) * op.k_sources;
     const int64_t tiles_m = ceil_div(op.m, 256);
+    const bool more = !may_split && (op.epi == kEpiActGrad || op.epi == kEpiGatedGrad ||
+                                     (op.epi == kEpiLinear && (op.act != SPCONV_ACT_NONE || op.extra)));
     Cut best;
     best.us = 1e30;
     for (int32_t hb : {128, 64}) {
+        const double step = hb == 128 ? 0.37 : 0.34, epi = hb == 128 ? (more ? 2.6 : 1.6) : (more ? 1.7 : 1.1);
         const int64_t tiles = tiles_m * ceil_div(op.n, dual ? hb : 2 * hb) * outputs;
         int64_t most = may_split && tiles < kPairs ? kPairs / tiles : 1;
         if (most > k_total / 8) most = k_total / 8;
         for (int64_t splits = 1; splits == 1 || splits <= most; ++splits) {
             const int64_t iters = ceil_div(k_total, splits), used = ceil_div(k_total, iters);
             if (used != splits) continue;   // the same cut as a smaller count
-            double us = static_cast<double>(ceil_div(tiles * splits, kPairs) * iters) * (hb == 128 ? 0.37 : 0.34);
+            const double unit = static_cast<double>(iters) * step > epi ? static_cast<double>(iters) * step : epi;
+            double us = static_cast<double>(ceil_div(tiles * splits, kPairs)) * unit + epi;
             if (splits > 1) us += 3.0 + 8.0e-6 / 6.0 * static_cast<double>(op.m * op.n * outputs) * static_cast<double>(splits);
             if (us < best.us) {
                 best.hb = hb;
