@@ -319,6 +319,16 @@ private:
 
 }  // namespace
 
+int align_rows(const void** p, int64_t* ld, int64_t rows, int64_t cols, Scratch* buf, cudaStream_t s) {
+    if (tma_ok(*p, *ld, 2)) return SPCONV_OK;
+    const int64_t pitch = static_cast<int64_t>(round_up(static_cast<size_t>(cols), 8));
+    if (!buf->alloc(static_cast<size_t>(rows) * pitch * 2, s)) return SPCONV_ERR_OOM;
+    SPCONV_CHECK(copy_rows(*p, *ld, buf->as<void>(), pitch, rows, cols, 2, s));
+    *p = buf->as<void>();
+    *ld = pitch;
+    return SPCONV_OK;
+}
+
 int dense_run(const DenseOp& op, cudaStream_t s) {
     if (op.m == 0 || op.n == 0) return SPCONV_OK;
     int32_t* status = nullptr;

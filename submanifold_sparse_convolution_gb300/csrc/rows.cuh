@@ -297,6 +297,10 @@ struct ColumnSums {
     float* out = nullptr;
 };
 int dense_run(const DenseOp& op, cudaStream_t s);
+// Where bf16 rows at *p, *ld apart, do not satisfy tma_ok: a copy of them that
+// does, in buf, for operands of two products (a product copies what it alone
+// reads).  Backward pass of 35309 x 459 x 228 with SiLU: 93.6 us, a copy each 105.4.
+int align_rows(const void** p, int64_t* ld, int64_t rows, int64_t cols, Scratch* buf, cudaStream_t s);
 // Up to two plain products in one launch, and column sums, if any, with them.
 int dense_run_plain(const DenseOp* ops, int count, const ColumnSums& cols, cudaStream_t s);
 // On the tensor cores (dense_tc.cu); operands and extra satisfy tma_ok.

@@ -52,8 +52,9 @@ int check_scales(int32_t dtype, const float* a, const float* b) {
     return SPCONV_OK;
 }
 
-// x [n][c_in] times a weight: bf16 [c_in][c_out], e4m3 [c_out][c_in].
-DenseOp product(const Rows& x, const void* w, int32_t c_out, int32_t dtype) {
+// x [n][c_in] times a weight: bf16 [c_in][c_out], e4m3 [c_out][c_in], its rows
+// ld_w apart.
+DenseOp product(const Rows& x, const void* w, int64_t ld_w, int32_t c_out, int32_t dtype) {
     DenseOp op;
     op.m = x.n;
     op.n = c_out;
@@ -64,12 +65,12 @@ DenseOp product(const Rows& x, const void* w, int32_t c_out, int32_t dtype) {
     op.a.k_major = true;
     op.b.p[0] = w;
     op.b.k_major = dtype == SPCONV_E4M3;
-    op.b.ld = op.b.k_major ? x.c : c_out;
+    op.b.ld = ld_w;
     return op;
 }
 
 // dz [n][c_out] times the transposed bf16 weight [c_in][c_out].
-DenseOp product_t(const Rows& dz, const void* w, int32_t c_in) {
+DenseOp product_t(const Rows& dz, const void* w, int64_t ld_w, int32_t c_in) {
     DenseOp op;
     op.m = dz.n;
     op.n = c_in;
@@ -77,7 +78,7 @@ DenseOp product_t(const Rows& dz, const void* w, int32_t c_in) {
     op.a.p[0] = dz.p;
     op.a.ld = dz.ld;
     op.b.p[0] = w;
-    op.b.ld = dz.c;
+    op.b.ld = ld_w;
     return op;
 }
 
@@ -160,7 +161,7 @@ int spconv_linear(const void* x_dev, int64_t ld_x, const float* x_scale_dev, con
     if (out.overlaps(x) || out.overlaps(w) || (out.overlaps(res) && !out.same(res)) || out.overlaps(vec(bias_dev, c_out)) ||
         out.overlaps(vec(x_scale_dev, n)) || out.overlaps(vec(w_scale_dev, c_out)))
         return SPCONV_ERR_ALIAS;
-    DenseOp op = product(x, w_dev, c_out, dtype);
+    DenseOp op = product(x, w_dev, dtype == SPCONV_E4M3 ? c_in : c_out, c_out, dtype);
     op.row_scale = x_scale_dev;
     op.col_scale[0] = w_scale_dev;
     op.bias = bias_dev;
@@ -185,7 +186,8 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
         SPCONV_CHECK(zero(dw_dev, wn * 2, s));
         return zero(dbias_dev, static_cast<size_t>(c_out) * 4, s);
     }
-    const Rows dy{dy_dev, n, c_out, ld_dy, 2}, x{x_dev, n, c_in, ld_x, 2}, w{w_dev, 1, wn, wn, 2};
+    Rows dy{dy_dev, n, c_out, ld_dy, 2}, x{x_dev, n, c_in, ld_x, 2};
+    const Rows w{w_dev, 1, wn, wn, 2};
     const Rows outs[3] = {{dx_dev, n, c_in, c_in, 2}, {dw_dev, 1, wn, wn, 2}, vec(dbias_dev, c_out)};
     if (!dy.ok() || !x.ok() || !w.ok()) return SPCONV_ERR_INVALID_ARG;
     for (int i = 0; i < 3; ++i) {
@@ -198,6 +200,12 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
     }
     if (!dx_dev && !dw_dev && !dbias_dev) return SPCONV_OK;
     const bool act = activation != SPCONV_ACT_NONE;
+    // what two products read is brought into alignment once
+    Scratch x_buf, w_buf, dy_buf;
+    int64_t ld_w = c_out;
+    if (act || dw_dev) SPCONV_CHECK(align_rows(&x.p, &x.ld, n, c_in, &x_buf, s));
+    if (act || dx_dev) SPCONV_CHECK(align_rows(&w_dev, &ld_w, c_in, c_out, &w_buf, s));
+    if (act || dw_dev || dx_dev) SPCONV_CHECK(align_rows(&dy.p, &dy.ld, n, c_out, &dy_buf, s));
     const int64_t ld_dz = static_cast<int64_t>(round_up(c_out, 8));   // whole 16-byte rows
     ColumnSums cols;
     cols.n = c_out;
@@ -211,12 +219,12 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
     cols.part = col_part;
     Rows dz = dy;
     if (act) {
-        DenseOp op = product(x, w_dev, c_out, SPCONV_BF16);
+        DenseOp op = product(x, w_dev, ld_w, c_out, SPCONV_BF16);
         op.epi = kEpiActGrad;
         op.act = activation;
         op.bias = bias_dev;
-        op.extra = dy_dev;
-        op.ld_extra = ld_dy;
+        op.extra = dy.p;
+        op.ld_extra = dy.ld;
         op.out[0] = buf.as<void>();
         op.ld_out = ld_dz;
         op.out_padded = true;
@@ -224,7 +232,7 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
         SPCONV_CHECK(dense_run(op, s));
         dz = Rows{buf.as<void>(), n, c_out, ld_dz, 2};
     } else if (dbias_dev) {
-        SPCONV_CHECK(column_parts(dy_dev, ld_dy, n, c_out, col_part, s));
+        SPCONV_CHECK(column_parts(dy.p, dy.ld, n, c_out, col_part, s));
     }
     DenseOp ops[2];
     int count = 0;
@@ -233,7 +241,7 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
         ops[count++].out[0] = dw_dev;
     }
     if (dx_dev) {
-        ops[count] = product_t(dz, w_dev, c_in);
+        ops[count] = product_t(dz, w_dev, ld_w, c_in);
         ops[count].ld_out = c_in;
         ops[count++].out[0] = dx_dev;
     }
@@ -256,7 +264,7 @@ int spconv_gated_ffn(const void* x_dev, int64_t ld_x, const float* x_scale_dev, 
     if (out.overlaps(x) || out.overlaps(wg) || out.overlaps(wu) || out.overlaps(vec(x_scale_dev, n)) ||
         out.overlaps(vec(gate_scale_dev, c_hidden)) || out.overlaps(vec(up_scale_dev, c_hidden)))
         return SPCONV_ERR_ALIAS;
-    DenseOp op = product(x, w_gate_dev, c_hidden, dtype);
+    DenseOp op = product(x, w_gate_dev, dtype == SPCONV_E4M3 ? c_in : c_hidden, c_hidden, dtype);
     op.epi = kEpiGated;
     op.b.p[1] = w_up_dev;
     op.row_scale = x_scale_dev;
@@ -281,7 +289,7 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
         SPCONV_CHECK(zero(dw_gate_dev, wn * 2, s));
         return zero(dw_up_dev, wn * 2, s);
     }
-    const Rows dh{dh_dev, n, c_hidden, ld_dh, 2}, x{x_dev, n, c_in, ld_x, 2};
+    Rows dh{dh_dev, n, c_hidden, ld_dh, 2}, x{x_dev, n, c_in, ld_x, 2};
     const Rows ins[4] = {dh, x, {w_gate_dev, 1, wn, wn, 2}, {w_up_dev, 1, wn, wn, 2}};
     const Rows outs[3] = {{dx_dev, n, c_in, c_in, 2}, {dw_gate_dev, 1, wn, wn, 2}, {dw_up_dev, 1, wn, wn, 2}};
     for (const Rows& r : ins)
@@ -295,13 +303,20 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
             if (outs[i].overlaps(outs[j])) return SPCONV_ERR_ALIAS;
     }
     if (!dx_dev && !dw_gate_dev) return SPCONV_OK;
+    // what two products read is brought into alignment once (c_hidden whole
+    // 16-byte rows or not: the weights keep one row stride)
+    Scratch x_buf, g_buf, u_buf;
+    int64_t ld_w = c_hidden, ld_u = c_hidden;
+    SPCONV_CHECK(align_rows(&x.p, &x.ld, n, c_in, &x_buf, s));
+    SPCONV_CHECK(align_rows(&w_gate_dev, &ld_w, c_in, c_hidden, &g_buf, s));
+    SPCONV_CHECK(align_rows(&w_up_dev, &ld_u, c_in, c_hidden, &u_buf, s));
     // gate and up are formed again in the product's epilogue, which writes their gradients
     const int64_t ld_d = static_cast<int64_t>(round_up(c_hidden, 8));
     const size_t one = static_cast<size_t>(n) * ld_d * 2;
     Scratch d_buf(2 * one, s);
     if (d_buf.failed()) return SPCONV_ERR_OOM;
     const Rows dg{d_buf.as<void>(), n, c_hidden, ld_d, 2}, du{d_buf.as<void>(one), n, c_hidden, ld_d, 2};
-    DenseOp op = product(x, w_gate_dev, c_hidden, SPCONV_BF16);
+    DenseOp op = product(x, w_gate_dev, ld_w, c_hidden, SPCONV_BF16);
     op.epi = kEpiGatedGrad;
     op.b.p[1] = w_up_dev;
     op.act = activation;
@@ -324,7 +339,7 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
     }
     if (dx_dev) {
         DenseOp& o = ops[count++];
-        o = product_t(dg, w_gate_dev, c_in);
+        o = product_t(dg, w_gate_dev, ld_w, c_in);
         o.k_sources = 2;
         o.a.p[1] = du.p;
         o.b.p[1] = w_up_dev;
