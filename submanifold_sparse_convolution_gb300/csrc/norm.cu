@@ -238,9 +238,9 @@ __global__ void __launch_bounds__(kBlock) k_rms_norm(const NormArgs a) {
     Pack<float, W> w[VPT];
     float h[VPT][W];
     SumMax st{0.0f, 0u};
-    load_weight<W, VPT>(a.weight, a.c, w, t, TPR);
-    pdl_wait();
+    pdl_wait();   // (also before the weight: the kernel before this one may write it)
     pdl_trigger();
+    load_weight<W, VPT>(a.weight, a.c, w, t, TPR);
     if (live) {
         p.load(a, row, t, TPR);
         st = row_stats<T, W, VPT, EIGHT>(a, p, w, h, t, TPR);
@@ -259,9 +259,9 @@ __global__ void __launch_bounds__(512) k_rms_norm_block(const NormArgs a) {
     RowPart<T, W, VPT> p, next;
     Pack<float, W> w[VPT];
     float h[VPT][W];
-    load_weight<W, VPT>(a.weight, a.c, w, t, tpr);
     pdl_wait();
     pdl_trigger();
+    load_weight<W, VPT>(a.weight, a.c, w, t, tpr);
     int64_t row = blockIdx.x;
     p.load(a, row, t, tpr);   // (the grid has at most n blocks)
     for (int turn = 0; row < a.n; ++turn) {
@@ -394,8 +394,8 @@ __global__ void __launch_bounds__(512) k_rms_norm_grad_block(const NormGradArgs 
     Pack<float, W> w[VPT];
     float dw[VPT][W] = {};
     GradPart<T, W, VPT> p, next;
-    load_weight<W, VPT>(a.weight, a.c, w, t, tpr);
     pdl_wait();
+    load_weight<W, VPT>(a.weight, a.c, w, t, tpr);
     int64_t row = blockIdx.x;
     p.load(a, row, t, tpr);
     for (int turn = 0; row < a.n; ++turn) {
@@ -561,7 +561,6 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_ring(const NormArgs a, cons
     ring.init(smem, g, 1);
     const int t = threadIdx.x, threads = blockDim.x;
     Pack<float, 8> w[VPT];
-    load_weight<8, VPT>(a.weight, a.c, w, t, threads);
     const T* const src[2] = {static_cast<const T*>(a.x), static_cast<const T*>(a.residual)};
     const int64_t ld[2] = {a.ldx, a.ldr};
     pdl_wait();
@@ -570,6 +569,7 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_ring(const NormArgs a, cons
     if (t == 0)
         for (int64_t row = blockIdx.x; row < a.n && filled < g.stages; row += gridDim.x, ++filled)
             ring.fill(g, filled, row, a.n, a.c, src, ld, 0, 1);
+    load_weight<8, VPT>(a.weight, a.c, w, t, threads);
     int k = 0;
     for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, ++k) {
         const int s = k % g.stages;
@@ -678,9 +678,9 @@ __global__ void __launch_bounds__(kBlock + 32, VPT * W > 16 || (VPT * W > 8 && (
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     Pack<float, W> w[VPT];
     float dw[VPT][1][W] = {};
-    if (consumer) load_weight<W, VPT>(a.weight, a.c, w, t, TPR);
     const int64_t tiles = (a.n + g.rows - 1) / g.rows;
     pdl_wait();
+    if (consumer) load_weight<W, VPT>(a.weight, a.c, w, t, TPR);
     int64_t k = 0;
     if (!consumer) {
         const T* const src[3] = {static_cast<const T*>(a.x), static_cast<const T*>(a.dy), static_cast<const T*>(a.dres)};

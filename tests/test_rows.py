@@ -552,6 +552,25 @@ def test_refusals():
         sc.rms_norm(x, wn, eps=float("nan"))
 
 
+@pytest.mark.parametrize("n,c,dtype", [(3, 24, BF), (900, 1000, BF), (900, 1001, BF), (900, 2048, BF), (40, 17000, BF),
+                                       (900, 512, torch.float32)])
+def test_weight_written_by_the_call_before(n, c, dtype):
+    """A norm whose weight the preceding kernel writes reads what that kernel wrote."""
+    g = gen(77)
+    x, w = normal(g, n, c).to(dtype), normal(g, c)
+    grads = [(normal(gen(78), n, c, std=1e-2) * 2.0 ** i).to(dtype) for i in range(12)]   # (powers of two: scaled exactly)
+    out = []
+    for dy in grads:
+        dw = sc.rms_norm_backward(dy, x, w)[1]   # (its memory is the last pass's again)
+        y = sc.rms_norm(x, dw)
+        dw = sc.rms_norm_backward(dy, x, w)[1]
+        out.append((y, sc.rms_norm_backward(grads[0], x, dw)[0]))
+    torch.cuda.synchronize()
+    for i, (y, dx) in enumerate(out):
+        assert torch.equal(y, out[0][0] * 2.0 ** i) and torch.equal(dx, out[0][1] * 2.0 ** i)
+    assert out[0][0].abs().max() > 0 and out[0][1].abs().max() > 0
+
+
 def test_no_wait_ran_out():
     """The status word of the operators' bounded waits after everything above."""
     assert sc.rows_status() == 0
