@@ -12,7 +12,9 @@
 // distributed shared memory, in the order of the ranks, applies the epilogue
 // and stores: one launch, no workspace, the same bits every run.  An SM keeps
 // about 200 KB of loads in flight: two CTAs up to 128 rows (gated: 64), one up
-// to twice that, where the sums need the room.
+// to twice that, where the sums need the room.  1 x 8192 x 16384 takes 47.5 us,
+// 5.7 TB/s of weight; 1 x 4096 x 4096 7.1, of which about 3 are the launch, the
+// first loads' latency and the sums.
 #include "ptx_sm100.cuh"
 #include "tensor_map.cuh"
 
@@ -24,6 +26,40 @@ constexpr int kChannels = 128;         // output channels per CTA (MMA M)
 constexpr int kTileA = kChannels * 128;
 constexpr int kMaxSplits = 8;          // portable cluster size
 constexpr int kMaxStages = 8;
+constexpr int kWarps = kThreads / 32;
+
+// Four channels of `rows` (<= kBatch) rows summed over the cluster's ranks (S of
+// them at most), in their order; at: their addresses in this CTA.
+template <int S, int kBatch>
+__device__ __forceinline__ void add_ranks(const uint32_t (&at)[kBatch], int rows, uint32_t splits, float (&z)[kBatch][4]) {
+    constexpr int kAtOnce = S == 8 ? 1 : kBatch;   // (the loads in flight are registers)
+#pragma unroll
+    for (int b0 = 0; b0 < kBatch; b0 += kAtOnce) {
+        float4 part[kAtOnce][S];
+#pragma unroll
+        for (int b = 0; b < kAtOnce; ++b)
+#pragma unroll
+            for (uint32_t r = 0; r < S; ++r)
+                part[b][r] = b0 + b < rows && (S < kMaxSplits || r < splits)
+                                 ? ptx::ld_cluster_f32x4(ptx::map_to_rank(at[b0 + b], r))
+                                 : make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < kAtOnce; ++b) {
+            float4 t = part[b][0];
+#pragma unroll
+            for (int r = 1; r < S; ++r) {
+                t.x += part[b][r].x;
+                t.y += part[b][r].y;
+                t.z += part[b][r].z;
+                t.w += part[b][r].w;
+            }
+            z[b0 + b][0] = t.x;
+            z[b0 + b][1] = t.y;
+            z[b0 + b][2] = t.z;
+            z[b0 + b][3] = t.w;
+        }
+    }
+}
 
 // BIG: one CTA per SM.
 template <bool DUAL, bool BIG>
@@ -58,6 +94,10 @@ template <bool DUAL, bool E4M3, bool BIG>
 __global__ void __launch_bounds__(kThreads, FewConfig<DUAL, BIG>::kPerSm) k_dense_few(const __grid_constant__ FewArgs p) {
     constexpr int kAcc = DUAL ? 2 : 1;
     constexpr int kBK = E4M3 ? 128 : 64;
+    // Rows of a warp's step of the epilogue: more loads together (128 x 512 x 2048 7.4 us,
+    // one row at a time 11.9), but more code to fetch (1 row, gated, 1024 x 2048 with two
+    // 6.1 us, with one 5.7)
+    constexpr int kBatch = DUAL ? 1 : 2;
     constexpr int kRows = FewConfig<DUAL, BIG>::kRows;
     constexpr uint32_t kCols = FewConfig<DUAL, BIG>::kCols;
     extern __shared__ uint8_t smem_raw[];
@@ -150,6 +190,18 @@ __global__ void __launch_bounds__(kThreads, FewConfig<DUAL, BIG>::kPerSm) k_dens
         }
         ptx::mma_commit_if(leader, &done);
     }
+    // the terms of this lane's channels, while the last products run
+    const int64_t n = n0 + 4 * lane;
+    float bias[4] = {}, scale[kAcc][4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (n + j >= p.n) continue;
+        if (!DUAL && p.bias) bias[j] = p.bias[n + j];
+        if (E4M3) {
+#pragma unroll
+            for (int a = 0; a < kAcc; ++a) scale[a][j] = p.col_scale[a][n + j];
+        }
+    }
     __syncthreads();
     if (*abort_flag)   // given up: loads still in flight land first
         for (int32_t j = fills > p.stages ? fills - p.stages : 0; j < fills; ++j)
@@ -177,57 +229,73 @@ __global__ void __launch_bounds__(kThreads, FewConfig<DUAL, BIG>::kPerSm) k_dens
     ptx::tc_fence_before();
     ptx::cluster_sync();
     ptx::tc_fence_after();
-    // this CTA's share: rows rank, rank + splits, ..
+    // this CTA's share: rows rank, rank + splits, ..; a warp takes kBatch of them at
+    // once (their loads travel together), a lane four channels
     const int32_t mine = (p.rows - static_cast<int32_t>(rank) + static_cast<int32_t>(splits) - 1) / static_cast<int32_t>(splits);
     const uint32_t sums_addr = ptx::smem_u32(sums);
-    // a warp takes a row, a lane four of its channels
-    const int64_t n = n0 + 4 * lane;
-    for (int32_t i = warp; i < mine && n < p.n; i += kThreads / 32) {
-        const int32_t row = static_cast<int32_t>(rank) + i * static_cast<int32_t>(splits);
-        float z[kAcc][4];
+    for (int32_t i0 = warp; i0 < mine && n < p.n; i0 += kBatch * kWarps) {
+        const int32_t left = (mine - i0 + kWarps - 1) / kWarps, rows = left < kBatch ? left : kBatch;
+        int32_t row[kBatch];
+        uint2 x[kBatch];
+        float z[kAcc][kBatch][4];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            row[b] = static_cast<int32_t>(rank) + (i0 + b * kWarps) * static_cast<int32_t>(splits);
+            x[b] = make_uint2(0, 0);
+            if (!DUAL && p.extra && b < rows) {
+                const __nv_bfloat16* e = p.extra + row[b] * p.ld_extra + n;   // (tma_ok: 8-byte loads, where the row has four)
+                if (n + 4 <= p.n) {
+                    x[b] = *reinterpret_cast<const uint2*>(e);
+                } else {
+                    uint32_t v[3] = {};
+                    for (int j = 0; j < 3 && n + j < p.n; ++j) v[j] = __bfloat16_as_ushort(e[j]);
+                    x[b] = make_uint2(v[0] | v[1] << 16, v[2]);
+                }
+            }
+        }
 #pragma unroll
         for (int a = 0; a < kAcc; ++a) {
-            const uint32_t at = sums_addr + static_cast<uint32_t>(((a * p.rows + row) * kChannels + 4 * lane) * 4);
-            float4 part[kMaxSplits];
+            uint32_t at[kBatch];
 #pragma unroll
-            for (uint32_t r = 0; r < kMaxSplits; ++r)
-                if (r < splits) part[r] = ptx::ld_cluster_f32x4(ptx::map_to_rank(at, r));
-            z[a][0] = part[0].x;
-            z[a][1] = part[0].y;
-            z[a][2] = part[0].z;
-            z[a][3] = part[0].w;
-#pragma unroll
-            for (uint32_t r = 1; r < kMaxSplits; ++r)
-                if (r < splits) {
-                    z[a][0] += part[r].x;
-                    z[a][1] += part[r].y;
-                    z[a][2] += part[r].z;
-                    z[a][3] += part[r].w;
-                }
+            for (int b = 0; b < kBatch; ++b) at[b] = sums_addr + static_cast<uint32_t>(((a * p.rows + row[b]) * kChannels + 4 * lane) * 4);
+            if (DUAL || splits == 8) add_ranks<8>(at, rows, splits, z[a]);
+            else if (splits == 4) add_ranks<4>(at, rows, splits, z[a]);
+            else if (splits == 2) add_ranks<2>(at, rows, splits, z[a]);
+            else add_ranks<1>(at, rows, splits, z[a]);
         }
-        alignas(8) __nv_bfloat16 y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (n + j >= p.n) continue;
+        for (int b = 0; b < kBatch; ++b) {
             if (E4M3) {
+                const float rs = b < rows ? p.row_scale[row[b]] : 0.0f;
 #pragma unroll
-                for (int a = 0; a < kAcc; ++a) z[a][j] *= p.row_scale[row] * p.col_scale[a][n + j];
+                for (int a = 0; a < kAcc; ++a)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) z[a][b][j] *= rs * scale[a][j];
             }
-            if (!DUAL && p.bias) z[0][j] += p.bias[n + j];
+            if (!DUAL) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[0][b][j] += bias[j];
+            }
         }
         with_act(p.act, [&](auto act) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float x = (!DUAL && p.extra && n + j < p.n) ? __bfloat162float(p.extra[row * p.ld_extra + n + j]) : 0.0f;
-                y[j] = __float2bfloat16_rn(DUAL ? act_f<act>(z[0][j]) * z[kAcc - 1][j] : act_f<act>(z[0][j]) + x);
+            for (int b = 0; b < kBatch; ++b) {
+                if (b >= rows) break;
+                alignas(8) __nv_bfloat16 y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t h = j < 2 ? x[b].x : x[b].y;
+                    const float v = __uint_as_float(j & 1 ? h & 0xFFFF0000u : h << 16);
+                    y[j] = __float2bfloat16_rn(DUAL ? act_f<act>(z[0][b][j]) * z[kAcc - 1][b][j] : act_f<act>(z[0][b][j]) + v);
+                }
+                __nv_bfloat16* out = p.out + row[b] * p.ld_out + n;
+                if (p.vec_out && n + 4 <= p.n) {
+                    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
+                } else {
+                    for (int j = 0; j < 4 && n + j < p.n; ++j) out[j] = y[j];
+                }
             }
         });
-        __nv_bfloat16* out = p.out + row * p.ld_out + n;
-        if (p.vec_out && n + 4 <= p.n) {
-            *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
-        } else {
-            for (int j = 0; j < 4 && n + j < p.n; ++j) out[j] = y[j];
-        }
     }
     // no CTA's sums go away while another may still read them
     ptx::cluster_sync();
@@ -238,10 +306,13 @@ template <bool DUAL, bool E4M3, bool BIG>
 int launch(FewArgs& p, cudaStream_t s) {
     using Cfg = FewConfig<DUAL, BIG>;
     constexpr int kAcc = DUAL ? 2 : 1;
-    // As many CTAs as the SMs hold, each with four steps of K at least
+    // As many CTAs as the SMs hold, each with four steps of K at least.  Clusters of
+    // eight lie within a GPC, so fewer fit: with one CTA per SM 12 of them run at once
+    // and 16 do not (160 x 2048 x 2048: 16.6 us, with clusters of four 9.6), with two 36
+    // and not 37 (1 x 4096 x 4736: 13.0 us, with clusters of four 9.4)
     const int32_t tiles = static_cast<int32_t>(ceil_div(p.n, kChannels));
     int32_t splits = 1;
-    while (splits < kMaxSplits && tiles * splits * 2 <= Cfg::kPerSm * 152 && p.k_iters >= 8 * splits) splits *= 2;
+    while (splits < kMaxSplits && tiles * splits * 2 <= (splits == 4 ? (BIG ? 96 : 288) : Cfg::kPerSm * 152) && p.k_iters >= 8 * splits) splits *= 2;
     p.stage_bytes = static_cast<int32_t>(round_up(kAcc * kTileA + p.rows_pad * 128, 1024));
     p.stages = Cfg::kRing / p.stage_bytes < kMaxStages ? Cfg::kRing / p.stage_bytes : kMaxStages;
     static bool set[kMaxDevices] = {};
@@ -284,9 +355,13 @@ bool dense_few_takes(const DenseOp& op) {
     const bool dual = op.epi == kEpiGated;
     if (op.m <= (dual ? FewConfig<true, false>::kRows : FewConfig<false, false>::kRows)) return true;
     // Beyond, the pairs' tiles of 256 rows are no longer mostly empty and win where
-    // there are enough of them: 256 rows x 2048 x 8192 (64 tiles of channels) 15.4 us,
-    // against 20.3 here; x 4096 x 4096 (32 tiles) 21.9, against 16.3
-    return op.m <= (dual ? FewConfig<true, true>::kRows : FewConfig<false, true>::kRows) && ceil_div(op.n, kChannels) <= 38;
+    // there are enough of them (256 rows x 2048 x 8192, 64 tiles of channels: 15.4 us,
+    // 20.3 here), where the weight's rows are short (200 x 512 x 2048: 7.3, 8.8) and where
+    // each CTA here would stream too many (256 x 8192 x 1024: 13.7, 15.7).  Between: 256
+    // x 4096 x 4096 16.3, 15.2 here; 160 x 2048 x 1024 10.7, 8.9 here
+    const int64_t k_bytes = op.k * (op.dtype == SPCONV_E4M3 ? 1 : 2);
+    return op.m <= (dual ? FewConfig<true, true>::kRows : FewConfig<false, true>::kRows) && ceil_div(op.n, kChannels) <= 38 &&
+           k_bytes >= 2048 && k_bytes <= 8192;
 }
 
 int dense_few_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
