@@ -386,7 +386,11 @@ __device__ __forceinline__ void grad_write(const NormGradArgs& a, int64_t row, S
     }
 }
 
-// Rows of 513 elements and more that no 16-byte load takes: one block per row.
+// Rows of 513 elements and more that no 16-byte load takes: one block per row, while
+// the weight and the running dw fit the registers (with single elements up to 3584,
+// fp32 4096: 25000 x 3001 bf16 199 us, the two passes below 479; with pairs up to
+// 4096: of 6002 elements the passes take 170 us for 9000 rows, this 198).  75000 x
+// 1001 takes 234 us, 2.6 TB/s: loads of two bytes keep too few on their way.
 template <typename T, int W, int VPT>
 __global__ void __launch_bounds__(512) k_rms_norm_grad_block(const NormGradArgs a, float* part) {
     __shared__ Sum2 sh[64];
@@ -891,14 +895,17 @@ int backward_t(const NormGradArgs& a, cudaStream_t s) {
         }
     }
     if constexpr (!kVec) {
-        constexpr int kPer = 4 * W;   // elements of a thread
-        if (a.c <= 512 * kPer) {
-            const int threads = block_threads(a.c, kPer);
-            const int64_t most = kSms * (1024 / threads);
-            const int64_t blocks = a.n < most ? a.n : most;
+        auto block = [&](auto vpt) {
+            const int threads = block_threads(a.c, vpt * W);
+            const int64_t most = kSms * (1024 / threads), blocks = a.n < most ? a.n : most;
             return with_part(blocks, [&](float* part) {
-                return launch(k_rms_norm_grad_block<T, W, 4>, blocks, threads, 0, s, a, part);
+                return launch(k_rms_norm_grad_block<T, W, vpt>, blocks, threads, 0, s, a, part);
             });
+        };
+        if (a.c <= 512 * 4 * W) return block(std::integral_constant<int, 4>());
+        if constexpr (W == 1) {
+            constexpr int kMost = sizeof(T) == 2 ? 7 : 8;   // (bf16 rows would spill)
+            if (a.c <= 512 * kMost) return block(std::integral_constant<int, kMost>());
         }
     }
     Scratch factors(static_cast<size_t>(a.n) * sizeof(Sum2), s);
