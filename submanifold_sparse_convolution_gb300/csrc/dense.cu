@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(256) k_weight_amax(const __nv_bfloat16* w, int
     const int32_t o = blockIdx.x * 64 + threadIdx.x % 64;
     uint32_t m = 0;
     if (o < c_out)
+#pragma unroll 8
         for (int64_t c = blockIdx.y * 4 + threadIdx.x / 64; c < c_in; c += gridDim.y * 4) {
             const uint32_t b = __float_as_uint(fabsf(__bfloat162float(w[c * c_out + o])));
             m = b > m ? b : m;
@@ -206,25 +207,45 @@ __global__ void __launch_bounds__(256) k_weight_amax(const __nv_bfloat16* w, int
     if (m) atomicMax(amax + o, m);
 }
 
-// 64 x 64 tiles, transposed through shared memory.
+// 64 x 64 tiles, transposed through shared memory; four values a store where the
+// rows of q are whole words.
 __global__ void __launch_bounds__(256) k_quantize_weight(const __nv_bfloat16* w, int32_t c_in, int32_t c_out,
-                                                         const uint32_t* amax, uint8_t* q, float* scale) {
+                                                         const uint32_t* amax, uint8_t* q, float* scale, bool words) {
     __shared__ float sh[64][65];
+    __shared__ float first[64], then[64];   // factors of a channel
     const int32_t c0 = blockIdx.x * 64, o0 = blockIdx.y * 64;
-    for (int i = threadIdx.x; i < 64 * 64; i += 256) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int i = k * 256 + threadIdx.x;
         const int32_t c = c0 + i / 64, o = o0 + i % 64;
         sh[i / 64][i % 64] = c < c_in && o < c_out ? __bfloat162float(w[static_cast<int64_t>(c) * c_out + o]) : 0.0f;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-        const int32_t o = o0 + i / 64, c = c0 + i % 64;
-        if (o >= c_out || c >= c_in) continue;
-        const float m = __uint_as_float(amax[o]);
+    const int32_t ch = o0 + static_cast<int32_t>(threadIdx.x);
+    if (threadIdx.x < 64 && ch < c_out) {
+        const float m = __uint_as_float(amax[ch]);
         // (448 / m overflows below 2^-119: bring such channels up first)
         const float pre = m < 0x1p-100f ? 0x1p100f : 1.0f;
-        const float inv = m == 0.0f ? 0.0f : 448.0f / (m * pre);
-        q[static_cast<int64_t>(o) * c_in + c] = __nv_cvt_float_to_fp8(sh[i % 64][i / 64] * pre * inv, __NV_SATFINITE, __NV_E4M3);
-        if (c == 0) scale[o] = m / 448.0f;
+        first[threadIdx.x] = pre;
+        then[threadIdx.x] = m == 0.0f ? 0.0f : 448.0f / (m * pre);
+        if (c0 == 0) scale[ch] = m / 448.0f;
+    }
+    __syncthreads();
+    const int c4 = threadIdx.x % 16 * 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int j = k * 16 + threadIdx.x / 16;
+        const int32_t o = o0 + j, c = c0 + c4;
+        if (o >= c_out || c >= c_in) continue;
+        uint32_t v = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            v |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(sh[c4 + t][j] * first[j] * then[j], __NV_SATFINITE, __NV_E4M3)) << (8 * t);
+        uint8_t* out = q + static_cast<int64_t>(o) * c_in + c;
+        if (words) {
+            *reinterpret_cast<uint32_t*>(out) = v;
+        } else {
+            for (int t = 0; t < 4 && c + t < c_in; ++t) out[t] = static_cast<uint8_t>(v >> (8 * t));
+        }
     }
 }
 
@@ -400,7 +421,8 @@ int quantize_weight(const void* w, int32_t c_in, int32_t c_out, void* q, float* 
     const unsigned bo = static_cast<unsigned>(ceil_div(c_out, 64)), bc = static_cast<unsigned>(ceil_div(c_in, 64));
     count_launch(2);
     k_weight_amax<<<dim3(bo, bc < 64 ? bc : 64), 256, 0, s>>>(p, c_in, c_out, amax.as<uint32_t>());
-    k_quantize_weight<<<dim3(bc, bo), 256, 0, s>>>(p, c_in, c_out, amax.as<uint32_t>(), static_cast<uint8_t*>(q), scale);
+    k_quantize_weight<<<dim3(bc, bo), 256, 0, s>>>(p, c_in, c_out, amax.as<uint32_t>(), static_cast<uint8_t*>(q), scale,
+                                                  c_in % 4 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0);
     return launch_status();
 }
 
