@@ -227,8 +227,10 @@ __device__ __forceinline__ void load_weight(const float* weight, int32_t c, Pack
     }
 }
 
-// Short rows: TPR lanes per row, many rows per block; enough
-// independent warps that the loads of some cover the arithmetic of others.
+// Rows of up to 1024 elements (512 where no 16-byte load takes them): TPR lanes per
+// row, many rows per block; enough independent warps that the loads of some cover the
+// arithmetic of others.  With a residual, bf16: 600000 x 128 89 us, 6.9 TB/s; 75000 x
+// 1024 89 us, where the ring below takes 102.
 template <typename T, int W, int TPR, int VPT, bool EIGHT>
 __global__ void __launch_bounds__(kBlock) k_rms_norm(const NormArgs a) {
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (kBlock / TPR) + threadIdx.x / TPR;
@@ -251,7 +253,8 @@ __global__ void __launch_bounds__(kBlock) k_rms_norm(const NormArgs a) {
 
 // Rows of 513 to 4096 elements that no vector load takes: one block per row,
 // persistent, the next row's loads in flight while this one is reduced and
-// written; the weight stays in registers.
+// written; the weight stays in registers.  75000 x 1001 bf16 133 us, 4.5 TB/s: the
+// loads of two bytes bound it (in two passes as below 306; 25000 x 3001 167, 189).
 template <typename T, int W, int VPT, bool EIGHT>
 __global__ void __launch_bounds__(512) k_rms_norm_block(const NormArgs a) {
     __shared__ SumMax sh[64];
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_block(const NormArgs a) {
 }
 
 // Longer rows: one block per row, the row read once per pass (the second
-// mostly from L2).  Every element is read by the thread that writes it, after
+// mostly from L2; 3000 x 24000 bf16 113 us, 5.1 TB/s).  Every element is read by the thread that writes it, after
 // the first pass, so sum may be the residual.
 template <typename T, int W, bool EIGHT>
 __global__ void __launch_bounds__(kLongThreads) k_rms_norm_long(const NormArgs a) {
@@ -420,7 +423,8 @@ __global__ void __launch_bounds__(512) k_rms_norm_grad_block(const NormGradArgs 
 }
 
 // Longer rows in two passes: the factors of each row, then dx and the partial
-// dw of a block of columns over a run of rows.
+// dw of a block of columns over a run of rows.  The second pass finds part of the
+// rows in L2: 4600 x 16384 bf16 158 us, 3.8 TB/s of the bytes that one pass has.
 template <typename T, int W>
 __global__ void __launch_bounds__(kLongThreads) k_rms_norm_grad_factors(const NormGradArgs a, Sum2* factors) {
     __shared__ Sum2 sh[64];
@@ -555,7 +559,10 @@ __device__ __forceinline__ void apart() { asm volatile("" ::: "memory"); }
 // 1/32 of the row's elements as threads and many blocks share an SM (the
 // barriers of one fall into the work of others).  There is no copying warp:
 // when the block meets to reduce row k, every thread is done with row k - 1,
-// and thread 0 refills that row's stage.
+// and thread 0 refills that row's stage.  Rows of 1025 to 16384 elements (fp32
+// 8192), as many as two stages of an SM's shared memory hold: to e4m3, 37000 x 2048
+// 85 us, 6.2 TB/s (the two passes above 198), 16381 x 8192 154 us; 4600 x 16384 to
+// bf16 104 us (110).
 template <typename T, bool EIGHT>
 __global__ void __launch_bounds__(512, 1) k_rms_norm_ring(const NormArgs a, const Ring g) {
     constexpr int VPT = 4;
@@ -608,9 +615,11 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_ring(const NormArgs a, cons
     if (t == 0 && *ring.abort_flag) ring.drain(g, filled);   // (set before the last barrier, if at all)
 }
 
-// The backward pass of such rows.  The row's vectors are taken from shared
-// memory again for the second pass, and the weight's from L1 or L2: the
-// registers hold the running dw.
+// The backward pass of such rows, up to 8192 elements (fp32 4096).  The row's
+// vectors are taken from shared memory again for the second pass, and the weight's
+// from L1 or L2: the registers hold the running dw.  Bound by issue and the row's
+// barriers rather than HBM: 9000 x 8192 bf16 117 us, 5.1 TB/s (in two passes 160),
+// 37000 x 2048 118 (231).
 template <typename T, int VPT>
 __global__ void __launch_bounds__(512, 1) k_rms_norm_grad_ring(const NormGradArgs a, const Ring g, float* part) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -668,8 +677,10 @@ __global__ void __launch_bounds__(512, 1) k_rms_norm_grad_ring(const NormGradArg
         }
 }
 
-// Shorter rows, backward: a row per TPR lanes, one warp of the block copies
-// stages of many rows.  A stage starts a multiple of eight rows in, which is 16
+// Shorter rows, backward (up to 1024 elements; fp32, and where no 16-byte load takes
+// them, 512): a row per TPR lanes, one warp of the block copies stages of many rows;
+// no barrier of the block.  75000 x 1000 bf16 92 us, 6.5 TB/s (the ring above 129);
+// 300000 x 255 133 (a block per row 241).  A stage starts a multiple of eight rows in, which is 16
 // bytes aligned for any number of elements where the rows are dense (W < 8).
 template <typename T, int W, int TPR, int VPT>
 __global__ void __launch_bounds__(kBlock + 32, VPT * W > 16 || (VPT * W > 8 && (sizeof(T) == 4 || W < 8)) ? 1 : 2)
@@ -933,7 +944,7 @@ int norm_forward(const NormArgs& a, cudaStream_t s) {
     const bool vec = a.c % 8 == 0 && vec_ok(a.x, a.ldx, es) && vec_ok(a.residual, a.ldr, es) &&
                      vec_ok(a.weight, 0, 4) && vec_ok(a.sum, 0, es) && vec_ok(a.out, 0, es);
     const bool eight = a.out_dtype == SPCONV_E4M3;
-    // (between, a block per row with single loads is faster: 2818 against 4424 GB/s at 1002 and 1001 elements)
+    // (between, a block per row with single loads is faster: 75000 x 1002 133 us, by pairs 268)
     const bool pairs = (a.c <= 512 || a.c > 4096) && a.c % 2 == 0 && pair_ok(a.x, a.ldx) && pair_ok(a.residual, a.ldr) && pair_ok(a.weight, 0, 8) &&
                        pair_ok(a.sum, 0) && pair_ok(a.out, 0, eight ? 2 : 4);
     if (a.dtype == SPCONV_FP32)
