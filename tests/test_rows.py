@@ -171,7 +171,7 @@ def test_norm_special_rows():
     assert (q.float() == 448).all()
 
 
-@pytest.mark.parametrize("n,c", NORM_SIZES + [(2000, 72), (3001, 1000), (1100, 2049), (700, 3001), (300, 4095)])
+@pytest.mark.parametrize("n,c", NORM_SIZES + [(2000, 72), (3001, 1000), (1100, 2049), (700, 3001), (300, 4095), (400, 2502), (300, 4094)])
 @pytest.mark.parametrize("dtype", [BF, torch.float32])
 @pytest.mark.parametrize("with_dres", [False, True])
 def test_norm_backward(n, c, dtype, with_dres):
