@@ -726,13 +726,11 @@ int make_part_map(CUtensorMap* map, float* base, int64_t n, int64_t m, int32_t s
     return r == CUDA_SUCCESS ? SPCONV_OK : SPCONV_ERR_CUDA;
 }
 
-// kEpiGated with K cut: gate and up as two outputs of a plain product.
+// An epilogue's product with K cut: gate and up are two outputs of a plain one.
 DenseOp as_plain(const DenseOp& op) {
     DenseOp o = op;
-    if (op.epi == kEpiGated) {
-        o.epi = kEpiLinear;
-        o.n_sources = 2;
-    }
+    if (op.epi == kEpiGated || op.epi == kEpiGatedGrad) o.n_sources = 2;
+    o.epi = kEpiLinear;
     return o;
 }
 
@@ -820,10 +818,9 @@ int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s) {
 
 bool dense_tc_cuts(const DenseOp& op) {
     if (op.plain()) return true;
-    if (op.epi != kEpiLinear && op.epi != kEpiGated) return false;
     const DenseOp o = as_plain(op);
     const Cut cut = best_cut(o, false, o.n_sources, true);
-    return cut.splits > 1 && cut.us < best_cut(op, op.epi == kEpiGated, 1, false).us;
+    return cut.splits > 1 && cut.us < best_cut(op, op.epi == kEpiGated || op.epi == kEpiGatedGrad, 1, false).us;
 }
 
 int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_t* status, cudaStream_t s) {
@@ -878,6 +875,7 @@ int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_
         sums[i].bias = op.bias;
         sums[i].extra = static_cast<const __nv_bfloat16*>(op.extra);
         sums[i].ld_extra = op.ld_extra;
+        sums[i].col_part = op.col_part;
     }
     const bool sums_follow = bytes > 0 || cols.out;
     l.trigger = !sums_follow;
@@ -887,6 +885,7 @@ int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_
         if (l.late) l.rounds = static_cast<int32_t>((2 * c0 + c1) / (2 * c1));
     }
     SPCONV_CHECK(ops[0].dtype == SPCONV_E4M3 ? (launch<kEpiPlain, true>(l, units, s)) : (launch<kEpiPlain, false>(l, units, s)));
+    if (ops[0].epi == kEpiActGrad || ops[0].epi == kEpiGatedGrad) return finish_grad(sums[0], s);   // (K is cut: dense_tc_cuts)
     return sums_follow ? finish_sums(sums, count, cols, s) : SPCONV_OK;
 }
 

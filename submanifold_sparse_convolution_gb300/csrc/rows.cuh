@@ -305,7 +305,7 @@ int align_rows(const void** p, int64_t* ld, int64_t rows, int64_t cols, Scratch*
 int dense_run_plain(const DenseOp* ops, int count, const ColumnSums& cols, cudaStream_t s);
 // On the tensor cores (dense_tc.cu); operands and extra satisfy tma_ok.
 int dense_tc_run(const DenseOp& op, int32_t* status, cudaStream_t s);
-// (one product may have the epilogue of kEpiLinear or kEpiGated: dense_tc_cuts
+// (one product may have an epilogue: dense_tc_cuts
 // says whether cutting its K is worth the workspace; plain ones always go here)
 bool dense_tc_cuts(const DenseOp& op);
 int dense_tc_plain(const DenseOp* ops, int count, const ColumnSums& cols, int32_t* status, cudaStream_t s);
@@ -342,7 +342,10 @@ struct SliceSums {
     const float* bias = nullptr;
     const __nv_bfloat16* extra = nullptr;
     int64_t ld_extra = 0;
+    float* col_part = nullptr;   // (finish_grad; DenseOp's)
 };
+// The same for one product with kEpiActGrad or kEpiGatedGrad.
+int finish_grad(const SliceSums& a, cudaStream_t s);
 int finish_sums(const SliceSums* slices, int count, const ColumnSums& cols, cudaStream_t s);
 // bf16 w [c_in][c_out] -> e4m3 q [c_out][c_in] with scale [c_out]
 int quantize_weight(const void* w, int32_t c_in, int32_t c_out, void* q, float* scale, cudaStream_t s);

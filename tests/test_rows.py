@@ -274,7 +274,8 @@ def test_gated(n, c, h, eight):
 
 
 GRAD_SIZES = [(1, 16, 16), (1, 1, 1), (3, 40, 24), (64, 128, 64), (100, 17, 33), (129, 72, 264), (257, 320, 136), (1000, 8, 700),
-              (1500, 513, 130), (4111, 128, 512), (9001, 64, 64), (20000, 40, 16)]
+              (1500, 513, 130), (4111, 128, 512), (9001, 64, 64), (20000, 40, 16), (200, 2048, 136), (300, 1500, 91),
+              (40, 4096, 260)]
 
 
 def grad_check(got, ref, terms, what):
