@@ -388,8 +388,12 @@ int spconv_kernel_map_static(const int32_t* coords_dev, int64_t n, const int32_t
  *   Order      every sum has a fixed order: the same call gives the same bits.
  *   Scratch    taken from the library's pool in stream order for the length
  *              of the call.
- *   Aliasing   an output must not overlap an input, unless said below
- *              (SPCONV_ERR_ALIAS).
+ *   Capture    calls can be captured into a CUDA graph; the first call of an
+ *              operator on a device loads its kernels, so make it before.
+ *   Aliasing   an output must not overlap an input (biases, scales and weights
+ *              included) or another output, unless said below
+ *              (SPCONV_ERR_ALIAS).  Column ranges of one wider matrix do not
+ *              overlap.
  *   NaN, inf   pass through the formulas as in IEEE arithmetic.
  */
 typedef enum {
@@ -467,7 +471,8 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
 
 /*
  * Gated feed-forward: out = act(x W_gate) * (x W_up), both products, the
- * activation and the product of the two in one kernel.  Operands as
+ * activation and the product of the two in one kernel (for a few hundred rows
+ * and a long c_in, where that is cut, in two).  Operands as
  * spconv_linear (gate_scale, up_scale fp32 [c_hidden] with e4m3);
  * out_dev bf16 [n] rows of c_hidden.
  */

@@ -659,7 +659,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, acti
               out: Optional[torch.Tensor] = None, x_scale: Optional[torch.Tensor] = None,
               gate_scale: Optional[torch.Tensor] = None, up_scale: Optional[torch.Tensor] = None,
               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-    """``spconv_gated_ffn``: act(x W_gate) * (x W_up), bf16 [N, C_hidden], in one kernel.
+    """``spconv_gated_ffn``: act(x W_gate) * (x W_up), bf16 [N, C_hidden].
 
     Operands as for ``linear``: bf16 [C_in, C_hidden] weights, or e4m3 [C_hidden, C_in] with scales."""
     if stream is not None:
