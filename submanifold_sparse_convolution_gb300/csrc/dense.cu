@@ -11,23 +11,40 @@ __device__ int32_t g_rows_status;   // kStatus* bits of the row-wise operators' 
 // ---- copies to aligned rows ---------------------------------------------------------
 // A warp per 256 elements E of a row, neighbouring lanes on neighbouring
 // elements: rows of any alignment move in whole 32-byte sectors.  Bound by HBM
-// and the loads in flight: 120000 x 459 bf16 41.7 us, 5.3 TB/s.
+// and the loads in flight: 120000 x 459 bf16 41.7 us, 5.3 TB/s.  All matrices of a
+// call in one launch (gated, 1 x 930 x 62: 9.3 us, a launch each 11.1).
 template <typename E>
-__global__ void __launch_bounds__(256) k_copy_rows(const E* src, int64_t ld_src, E* dst, int64_t ld_dst, int64_t rows, int32_t cols,
-                                                   int32_t row_warps) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-    const int64_t r = w / row_warps;
-    if (r >= rows) return;
-    const int32_t c0 = static_cast<int32_t>(w - r * row_warps) * 256 + (threadIdx.x & 31);
+__device__ __forceinline__ void copy_rows(const RowCopy& c, int32_t block) {
+    const int64_t w = (static_cast<int64_t>(block) * 256 + threadIdx.x) >> 5;
+    const int64_t r = w / c.row_warps;
+    if (r >= c.rows) return;
+    const int32_t c0 = static_cast<int32_t>(w - r * c.row_warps) * 256 + (threadIdx.x & 31);
+    const E* src = reinterpret_cast<const E*>(static_cast<const uint8_t*>(c.src) + r * c.pitch_src);
+    E* dst = reinterpret_cast<E*>(static_cast<uint8_t*>(c.dst) + r * c.pitch_dst);
     E v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        if (c0 + 32 * k < cols) v[k] = src[r * ld_src + c0 + 32 * k];
+        if (c0 + 32 * k < c.cols) v[k] = src[c0 + 32 * k];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        if (c0 + 32 * k < cols) dst[r * ld_dst + c0 + 32 * k] = v[k];
+        if (c0 + 32 * k < c.cols) dst[c0 + 32 * k] = v[k];
+}
+
+__global__ void __launch_bounds__(256) k_copy_rows(const RowCopies a) {
+    pdl_wait();
+    pdl_trigger();
+    int32_t b = static_cast<int32_t>(blockIdx.x);
+#pragma unroll
+    for (int i = 0; i < kMaxCopies; ++i) {
+        const RowCopy& c = a.copy[i];
+        if (b < c.blocks) {
+            if (c.e == 4) copy_rows<uint32_t>(c, b);
+            else if (c.e == 2) copy_rows<uint16_t>(c, b);
+            else copy_rows<uint8_t>(c, b);
+            return;
+        }
+        b -= c.blocks;
+    }
 }
 
 // ---- column sums ----------------------------------------------------------------
@@ -303,24 +320,6 @@ __global__ void __launch_bounds__(256) k_quantize_weight(const __nv_bfloat16* w,
     }
 }
 
-template <typename E>
-int copy_rows_as(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t rows, int64_t bytes, size_t es, cudaStream_t s) {
-    const int64_t e = sizeof(E), cols = bytes / e, row_warps = ceil_div(cols, 256), blocks = ceil_div(rows * row_warps, 8);
-    if (blocks > 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
-    return launch_pdl(k_copy_rows<E>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, static_cast<const E*>(src),
-                      ld_src * static_cast<int64_t>(es) / e, static_cast<E*>(dst), ld_dst * static_cast<int64_t>(es) / e, rows,
-                      static_cast<int32_t>(cols), static_cast<int32_t>(row_warps));
-}
-
-// dst has 16-byte aligned rows; the copy takes the largest elements that src's allow.
-int copy_rows(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t rows, int64_t cols, size_t es, cudaStream_t s) {
-    const uintptr_t all = reinterpret_cast<uintptr_t>(src) | static_cast<uintptr_t>(ld_src * es) | static_cast<uintptr_t>(cols * es);
-    const int64_t bytes = cols * static_cast<int64_t>(es);
-    if (all % 4 == 0) return copy_rows_as<uint32_t>(src, ld_src, dst, ld_dst, rows, bytes, es, s);
-    if (all % 2 == 0) return copy_rows_as<uint16_t>(src, ld_src, dst, ld_dst, rows, bytes, es, s);
-    return copy_rows_as<uint8_t>(src, ld_src, dst, ld_dst, rows, bytes, es, s);
-}
-
 }  // namespace
 
 int rows_status_word(int32_t** word) {
@@ -337,92 +336,78 @@ int rows_status_word(int32_t** word) {
     return SPCONV_OK;
 }
 
+void AlignedRows::add(const void** p, int count, int64_t* ld, int64_t rows, int64_t cols, size_t es) {
+    bool move = false;
+    for (int i = 0; i < count; ++i) move = move || !tma_ok(p[i], *ld, es);
+    if (!move) return;
+    const int64_t pitch = static_cast<int64_t>(round_up(static_cast<size_t>(cols), 16 / es));
+    for (int i = 0; i < count; ++i) {
+        // the largest elements that the rows allow
+        const uintptr_t all = reinterpret_cast<uintptr_t>(p[i]) | static_cast<uintptr_t>(*ld * es) | static_cast<uintptr_t>(cols * es);
+        RowCopy& c = args_.copy[count_];
+        c.e = all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
+        c.src = p[i];
+        c.pitch_src = *ld * static_cast<int64_t>(es);
+        c.pitch_dst = pitch * static_cast<int64_t>(es);
+        c.rows = rows;
+        c.cols = static_cast<int32_t>(cols * static_cast<int64_t>(es) / c.e);
+        c.row_warps = static_cast<int32_t>(ceil_div(c.cols, 256));
+        const int64_t b = ceil_div(rows * c.row_warps, 8);
+        blocks_ += b;
+        c.blocks = static_cast<int32_t>(b);
+        off_[count_] = bytes_;
+        bytes_ += round_up(static_cast<size_t>(rows) * c.pitch_dst, 256);
+        out_[count_++] = &p[i];
+    }
+    *ld = pitch;
+}
+
+int AlignedRows::run(cudaStream_t s) {
+    if (count_ == 0) return SPCONV_OK;
+    if (blocks_ > 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
+    if (!buf_.alloc(bytes_, s)) return SPCONV_ERR_OOM;
+    for (int i = 0; i < count_; ++i) *out_[i] = args_.copy[i].dst = buf_.as<void>(off_[i]);
+    return launch_pdl(k_copy_rows, dim3(static_cast<unsigned>(blocks_)), 256, 0, s, args_);
+}
+
 namespace {
 
-// The tensor maps need 16-byte aligned rows.  Operands without them (odd
-// channel counts, strides or addresses) are copied to rows that have them: one
-// extra pass over that matrix.
-class AlignedOp {
-public:
-    DenseOp op;   // what to run
-
-    int begin(const DenseOp& given, cudaStream_t s) {
-        op = given;
-        const size_t es = op.dtype == SPCONV_E4M3 ? 1 : 2;
-        const bool dual = op.epi == kEpiGated || op.epi == kEpiGatedGrad;
-        const int na = op.k_sources, nb = dual || op.k_sources == 2 || op.n_sources == 2 ? 2 : 1;
-        const Matrix a = op.a.k_major ? plan(op.a.p, na, op.a.ld, op.m, op.k, es) : plan(op.a.p, na, op.a.ld, op.k, op.m, es);
-        const Matrix b = op.b.k_major ? plan(op.b.p, nb, op.b.ld, op.n, op.k, es) : plan(op.b.p, nb, op.b.ld, op.k, op.n, es);
-        const Matrix x = plan(&op.extra, op.extra ? 1 : 0, op.ld_extra, op.m, op.n, 2);
-        if (bytes_ == 0) return SPCONV_OK;
-        if (!buf_.alloc(bytes_, s)) return SPCONV_ERR_OOM;
-        SPCONV_CHECK(bring(a, op.a.p, na, &op.a.ld, s));
-        SPCONV_CHECK(bring(b, op.b.p, nb, &op.b.ld, s));
-        return bring(x, &op.extra, 1, &op.ld_extra, s);
-    }
-
-private:
-    struct Matrix {   // up to two matrices of one shape
-        int64_t rows, cols;
-        size_t es;
-        bool move;
-        size_t off[2];
-        int64_t ld() const { return static_cast<int64_t>(round_up(static_cast<size_t>(cols), 16 / es)); }
+// Brings the operands of a product, and what its epilogue reads, into alignment.
+int align(DenseOp* op, AlignedRows* rows, cudaStream_t s) {
+    const size_t es = op->dtype == SPCONV_E4M3 ? 1 : 2;
+    const bool dual = op->epi == kEpiGated || op->epi == kEpiGatedGrad;
+    const int nb = dual || op->k_sources == 2 || op->n_sources == 2 ? 2 : 1;
+    auto add = [&](Operand& t, int count, int64_t r) {
+        rows->add(t.p, count, &t.ld, t.k_major ? r : op->k, t.k_major ? op->k : r, es);
     };
-    Matrix plan(const void* const* ptr, int count, int64_t ld, int64_t rows, int64_t cols, size_t e) {
-        Matrix t{rows, cols, e, false, {0, 0}};
-        for (int i = 0; i < count; ++i) t.move = t.move || !tma_ok(ptr[i], ld, e);
-        for (int i = 0; t.move && i < count; ++i) {
-            t.off[i] = bytes_;
-            bytes_ += round_up(static_cast<size_t>(rows) * t.ld() * e, 256);
-        }
-        return t;
-    }
-    int bring(const Matrix& t, const void** ptr, int count, int64_t* ld, cudaStream_t s) {
-        if (!t.move) return SPCONV_OK;
-        for (int i = 0; i < count; ++i) {
-            SPCONV_CHECK(copy_rows(ptr[i], *ld, buf_.as<void>(t.off[i]), t.ld(), t.rows, t.cols, t.es, s));
-            ptr[i] = buf_.as<void>(t.off[i]);
-        }
-        *ld = t.ld();
-        return SPCONV_OK;
-    }
-
-    Scratch buf_;
-    size_t bytes_ = 0;
-};
+    add(op->a, op->k_sources, op->m);
+    add(op->b, nb, op->n);
+    if (op->extra) rows->add(&op->extra, 1, &op->ld_extra, op->m, op->n, 2);
+    return rows->run(s);
+}
 
 }  // namespace
-
-int align_rows(const void** p, int64_t* ld, int64_t rows, int64_t cols, Scratch* buf, cudaStream_t s) {
-    if (tma_ok(*p, *ld, 2)) return SPCONV_OK;
-    const int64_t pitch = static_cast<int64_t>(round_up(static_cast<size_t>(cols), 8));
-    if (!buf->alloc(static_cast<size_t>(rows) * pitch * 2, s)) return SPCONV_ERR_OOM;
-    SPCONV_CHECK(copy_rows(*p, *ld, buf->as<void>(), pitch, rows, cols, 2, s));
-    *p = buf->as<void>();
-    *ld = pitch;
-    return SPCONV_OK;
-}
 
 int dense_run(const DenseOp& op, cudaStream_t s) {
     if (op.m == 0 || op.n == 0) return SPCONV_OK;
     int32_t* status = nullptr;
     SPCONV_CHECK(rows_status_word(&status));
-    AlignedOp a;
-    SPCONV_CHECK(a.begin(op, s));
-    if (dense_few_takes(a.op)) return dense_few_run(a.op, status, s);
-    return dense_tc_cuts(a.op) ? dense_tc_plain(&a.op, 1, {}, status, s) : dense_tc_run(a.op, status, s);
+    AlignedRows rows;
+    DenseOp o = op;
+    SPCONV_CHECK(align(&o, &rows, s));
+    if (dense_few_takes(o)) return dense_few_run(o, status, s);
+    return dense_tc_cuts(o) ? dense_tc_plain(&o, 1, {}, status, s) : dense_tc_run(o, status, s);
 }
 
 int dense_run_plain(const DenseOp* ops, int count, const ColumnSums& cols, cudaStream_t s) {
     if (count == 0) return cols.out ? finish_sums(nullptr, 0, cols, s) : SPCONV_OK;
     int32_t* status = nullptr;
     SPCONV_CHECK(rows_status_word(&status));
-    AlignedOp a[2];
+    AlignedRows rows[2];
     DenseOp o[2];
     for (int i = 0; i < count; ++i) {
-        SPCONV_CHECK(a[i].begin(ops[i], s));
-        o[i] = a[i].op;
+        o[i] = ops[i];
+        SPCONV_CHECK(align(&o[i], &rows[i], s));
     }
     return dense_tc_plain(o, count, cols, status, s);
 }

@@ -297,10 +297,37 @@ struct ColumnSums {
     float* out = nullptr;
 };
 int dense_run(const DenseOp& op, cudaStream_t s);
-// Where bf16 rows at *p, *ld apart, do not satisfy tma_ok: a copy of them that
-// does, in buf, for operands of two products (a product copies what it alone
-// reads).  Backward pass of 35309 x 459 x 228 with SiLU: 93.6 us, a copy each 105.4.
-int align_rows(const void** p, int64_t* ld, int64_t rows, int64_t cols, Scratch* buf, cudaStream_t s);
+
+// Matrices brought into the alignment that the tensor maps need (tma_ok): those
+// whose rows (odd channel counts, strides or addresses) do not have it are copied
+// to workspace rows that do, all in one launch.  A product does so with what it
+// reads; what two products of a gradient read is brought over before both (35309
+// x 459 x 228 with SiLU: 93.6 us, by each product 105.4).
+constexpr int kMaxCopies = 5;
+struct RowCopy {
+    const void* src;
+    void* dst;
+    int64_t pitch_src, pitch_dst, rows;   // bytes, bytes, rows
+    int32_t cols, row_warps, blocks, e;   // elements of a row, warps for them, their blocks, bytes of an element
+};
+struct RowCopies {
+    RowCopy copy[kMaxCopies];
+};
+class AlignedRows {
+public:
+    // `count` matrices of one shape and row stride (kMaxCopies of all calls)
+    void add(const void** p, int count, int64_t* ld, int64_t rows, int64_t cols, size_t es);
+    // after the last add: allocates and copies, and sets their addresses
+    int run(cudaStream_t s);
+
+private:
+    RowCopies args_ = {};
+    const void** out_[kMaxCopies];
+    size_t off_[kMaxCopies], bytes_ = 0;
+    int64_t blocks_ = 0;
+    int count_ = 0;
+    Scratch buf_;
+};
 // Up to two plain products in one launch, and column sums, if any, with them.
 int dense_run_plain(const DenseOp* ops, int count, const ColumnSums& cols, cudaStream_t s);
 // On the tensor cores (dense_tc.cu); operands and extra satisfy tma_ok.

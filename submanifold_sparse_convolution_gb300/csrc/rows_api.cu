@@ -201,11 +201,12 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
     if (!dx_dev && !dw_dev && !dbias_dev) return SPCONV_OK;
     const bool act = activation != SPCONV_ACT_NONE;
     // what two products read is brought into alignment once
-    Scratch x_buf, w_buf, dy_buf;
+    AlignedRows rows;
     int64_t ld_w = c_out;
-    if (act || dw_dev) SPCONV_CHECK(align_rows(&x.p, &x.ld, n, c_in, &x_buf, s));
-    if (act || dx_dev) SPCONV_CHECK(align_rows(&w_dev, &ld_w, c_in, c_out, &w_buf, s));
-    if (act || dw_dev || dx_dev) SPCONV_CHECK(align_rows(&dy.p, &dy.ld, n, c_out, &dy_buf, s));
+    if (act || dw_dev) rows.add(&x.p, 1, &x.ld, n, c_in, 2);
+    if (act || dx_dev) rows.add(&w_dev, 1, &ld_w, c_in, c_out, 2);
+    if (act || dw_dev || dx_dev) rows.add(&dy.p, 1, &dy.ld, n, c_out, 2);
+    SPCONV_CHECK(rows.run(s));
     const int64_t ld_dz = static_cast<int64_t>(round_up(c_out, 8));   // whole 16-byte rows
     ColumnSums cols;
     cols.n = c_out;
@@ -303,25 +304,26 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
             if (outs[i].overlaps(outs[j])) return SPCONV_ERR_ALIAS;
     }
     if (!dx_dev && !dw_gate_dev) return SPCONV_OK;
-    // what two products read is brought into alignment once (c_hidden whole
-    // 16-byte rows or not: the weights keep one row stride)
-    Scratch x_buf, g_buf, u_buf;
-    int64_t ld_w = c_hidden, ld_u = c_hidden;
-    SPCONV_CHECK(align_rows(&x.p, &x.ld, n, c_in, &x_buf, s));
-    SPCONV_CHECK(align_rows(&w_gate_dev, &ld_w, c_in, c_hidden, &g_buf, s));
-    SPCONV_CHECK(align_rows(&w_up_dev, &ld_u, c_in, c_hidden, &u_buf, s));
+    // what two products read is brought into alignment once, and dh with it
+    AlignedRows rows;
+    const void* w[2] = {w_gate_dev, w_up_dev};
+    int64_t ld_w = c_hidden;
+    rows.add(&x.p, 1, &x.ld, n, c_in, 2);
+    rows.add(w, 2, &ld_w, c_in, c_hidden, 2);
+    rows.add(&dh.p, 1, &dh.ld, n, c_hidden, 2);
+    SPCONV_CHECK(rows.run(s));
     // gate and up are formed again in the product's epilogue, which writes their gradients
     const int64_t ld_d = static_cast<int64_t>(round_up(c_hidden, 8));
     const size_t one = static_cast<size_t>(n) * ld_d * 2;
     Scratch d_buf(2 * one, s);
     if (d_buf.failed()) return SPCONV_ERR_OOM;
     const Rows dg{d_buf.as<void>(), n, c_hidden, ld_d, 2}, du{d_buf.as<void>(one), n, c_hidden, ld_d, 2};
-    DenseOp op = product(x, w_gate_dev, ld_w, c_hidden, SPCONV_BF16);
+    DenseOp op = product(x, w[0], ld_w, c_hidden, SPCONV_BF16);
     op.epi = kEpiGatedGrad;
-    op.b.p[1] = w_up_dev;
+    op.b.p[1] = w[1];
     op.act = activation;
-    op.extra = dh_dev;
-    op.ld_extra = ld_dh;
+    op.extra = dh.p;
+    op.ld_extra = dh.ld;
     op.out[0] = d_buf.as<void>();
     op.out[1] = d_buf.as<void>(one);
     op.ld_out = ld_d;
@@ -339,10 +341,10 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
     }
     if (dx_dev) {
         DenseOp& o = ops[count++];
-        o = product_t(dg, w_gate_dev, ld_w, c_in);
+        o = product_t(dg, w[0], ld_w, c_in);
         o.k_sources = 2;
         o.a.p[1] = du.p;
-        o.b.p[1] = w_up_dev;
+        o.b.p[1] = w[1];
         o.out[0] = dx_dev;
         o.ld_out = c_in;
     }
