@@ -311,7 +311,10 @@ __global__ void __launch_bounds__(kLongThreads) k_rms_norm_long(const NormArgs a
 
 // ---- backward -----------------------------------------------------------------
 // With g = dy w and r as above:
-//   dx = r g - h r^3 mean_c(g h) + dres,   dw_c = sum_rows dy h r
+//   dx = r (g - (h r) m) + dres,  m = r mean_c(g h),   dw_c = sum_rows dy h r
+// h r has unit size and m the size of g whatever the size of the row; the cube
+// of r, which the same formula has when multiplied out, leaves the range of fp32
+// for rows below 1e-13 (eps = 0) and above 1e13.
 // Each row's threads walk the rows first, first + step, ...; the weight and the
 // running dw of their columns stay in registers, a block's rows are added in a
 // fixed order and the block writes one row of partial sums (finish_sums adds
@@ -355,11 +358,11 @@ __device__ __forceinline__ Sum2 grad_stats(const NormGradArgs& a, const GradPart
     return st;
 }
 
-// r = 1 / rms and k = r^3 mean(g h) of a row
+// r = 1 / rms and m = r mean(g h) of a row
 __device__ __forceinline__ Sum2 grad_factors(Sum2 st, int32_t c, float eps) {
     const float inv_c = 1.0f / static_cast<float>(c);
     const float r = rsqrtf(st.s * inv_c + eps);
-    return {r, r * r * r * st.t * inv_c};
+    return {r, r * st.t * inv_c};
 }
 
 template <typename T, int W, int VPT>
@@ -374,8 +377,9 @@ __device__ __forceinline__ void grad_write(const NormGradArgs& a, int64_t row, S
         unpack<W>(p.d[v], d);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            dx[j] = fmaf(d[j] * w[v].v[j], f.s, -h[j] * f.t);
-            dw[v][j] = fmaf(d[j], h[j] * f.s, dw[v][j]);
+            const float unit = h[j] * f.s;
+            dx[j] = f.s * fmaf(-unit, f.t, d[j] * w[v].v[j]);
+            dw[v][j] = fmaf(d[j], unit, dw[v][j]);
         }
         if (a.dres) {
             float r[W];

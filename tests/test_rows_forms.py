@@ -1,0 +1,45 @@
+"""Forms and ranges of the row-wise operators beside those of test_rows.py, against 64-bit formulas.
+
+Tolerances are those derived there: one rounding per output (bf16 2^-8, fp32
+2^-24), and (terms / 32 + 64) 2^-23 of the sum of magnitudes for fp32 sums.
+"""
+import pytest
+import torch
+
+import submanifold_sparse_convolution_gb300 as sc
+from submanifold_sparse_convolution_gb300 import build as build_mod
+from test_rows import BF, close, gen, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build_mod.build()
+
+
+# widths of every kernel of the norm's gradient: lanes (whole vectors, pairs, odd), ring, block, two passes
+GRAD_WIDTHS = [(300, 64), (300, 1000), (90, 502), (90, 255), (200, 2048), (60, 1001), (40, 3001), (9, 9000), (5, 20001)]
+
+
+@pytest.mark.parametrize("n,c", GRAD_WIDTHS)
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("size,eps", [(1e-14, 0.0), (1e13, 1e-6), (1e15, 1e-6)])
+def test_norm_backward_of_rows_far_from_unit_size(n, c, dtype, size, eps):
+    """r = 1 / rms is in range for such rows, its cube is not (from 1e38 on, and below 1e-38)."""
+    g = gen(n + c)
+    u = normal(g, n, c)
+    x = (size * u).to(dtype)
+    dy = (normal(g, n, c) + 0.5 * u).to(dtype)   # (along x in part, so that the projection counts)
+    w = 1 + normal(g, c, std=0.3)
+    dx, dw = sc.rms_norm_backward(dy, x, w, eps=eps)
+    X, D = x.double(), dy.double()
+    r = 1 / torch.sqrt((X * X).mean(1, keepdim=True) + eps)
+    G, unit = D * w.double(), X * r
+    along = unit * (G * unit).mean(1, keepdim=True)
+    acc = (c / 32 + 64) * 2.0 ** -23
+    ref = r * (G - along)
+    slack = acc * (r * (G.abs() + unit.abs() * (G * unit).abs().mean(1, keepdim=True)) + ref.abs())
+    close(dx, ref, slack, "dx", 2.0 ** -8 if dtype == BF else 2.0 ** -24)
+    terms = D * unit
+    assert ((dw.double() - terms.sum(0)).abs() <= (acc + (n / 152 + 40) * 2.0 ** -23) * terms.abs().sum(0)).all()
