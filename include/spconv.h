@@ -29,6 +29,9 @@
  * Streams: all work is enqueued on the caller's stream; nothing synchronises
  * the device except where a function says it does.
  *
+ * Devices: every call works on the calling thread's current device: its device
+ * pointers, its stream and the handles that it is given belong to that one.
+ *
  * Errors: functions return SPCONV_OK (0) or a negative spconv_status_t.
  * Argument errors are detected on the host before any work is enqueued.
  * Data errors found on the device (duplicate or out-of-range coordinates) are

@@ -34,6 +34,9 @@ Between two convolutions on the same sites, on rows of features alone:
 with 8-bit forms (``rms_norm(..., quantize=True)``, ``quantize_weight``) and
 gradients (``rms_norm_backward``, ``linear_backward``, ``gated_ffn_backward``).
 
+The tensors of a row-wise call lie on the current GPU (``ValueError``
+otherwise); a ``stream`` argument makes its own GPU current for the call.
+
 Errors raise ``SpconvError`` with the library's status code; errors found on
 the device (duplicate or out-of-range coordinates) surface through
 ``map_status`` or the next call on the map.
@@ -434,6 +437,7 @@ def map_destroy(m: Map):
 # at each tensor once and allocate only outputs.
 _BF16 = torch.bfloat16
 _raw_stream = torch._C._cuda_getCurrentRawStream   # of a device, without making a Stream object
+_current_device = torch._C._cuda_getDevice
 _c = None
 
 
@@ -444,10 +448,10 @@ def _lib():
     return _c
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
-    """Row stride of ``t``, checked to be ``shape`` rows of ``dtype`` on the GPU."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name} must be a {dtype} {list(shape)} CUDA tensor")
+def _rows(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
+    """Row stride of ``t``, checked to be ``shape`` rows of ``dtype`` on GPU ``dev``."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor on cuda:{dev}")
     ld, step = t.stride()
     n, c = shape
     if step != 1 and c > 1:
@@ -459,17 +463,17 @@ def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
     return ld
 
 
-def _vector(t: torch.Tensor, name: str, c: int) -> int:
-    """Address of an fp32 [c] vector."""
-    if t.dtype is not torch.float32 or t.shape != (c,) or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous fp32 [{c}] CUDA tensor")
+def _vector(t: torch.Tensor, name: str, c: int, dev: int) -> int:
+    """Address of an fp32 [c] vector on GPU ``dev``."""
+    if t.dtype is not torch.float32 or t.shape != (c,) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 [{c}] tensor on cuda:{dev}")
     return t.data_ptr()
 
 
-def _weight(t: torch.Tensor, name: str, shape, dtype) -> int:
-    """Address of a dense weight."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} CUDA tensor")
+def _weight(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
+    """Address of a dense weight on GPU ``dev``."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -481,16 +485,20 @@ def _activation(name: str) -> int:
 
 
 def _matrix(t: torch.Tensor, name: str):
-    """The shape of a 2-D CUDA tensor."""
+    """The shape of a 2-D CUDA tensor and its GPU, which has to be the current one: the library takes
+    its stream, its memory and its kernels there."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    return t.shape
+    dev = t.get_device()
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return t.shape, dev
 
 
 def _on_stream(stream: torch.cuda.Stream, tensors, call):
     """``call()`` on ``stream``: what it allocates belongs to that stream, and what it reads is kept
     from reuse until the stream is past it."""
-    if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+    if stream.cuda_stream != torch.cuda.current_stream(stream.device).cuda_stream:
         for t in tensors:
             if t is not None and t.is_cuda:
                 t.record_stream(stream)
@@ -510,7 +518,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     if stream is not None:
         return _on_stream(stream, (x, weight, residual, sum_out),
                           lambda: rms_norm(x, weight, residual, eps=eps, quantize=quantize, sum_out=sum_out))
-    shape = _matrix(x, "x")
+    shape, dev = _matrix(x, "x")
     n, c = shape
     dtype = x.dtype
     dt = _DTYPES.get(dtype)
@@ -518,24 +526,24 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
         raise ValueError("x must be bf16 or fp32")
     if weight is None:
         raise ValueError("weight is required")
-    dev = x.device
-    ldx, r, ldr = _rows(x, "x", shape, dtype), None, 0
-    w = _vector(weight, "weight", c)
+    ldx, r, ldr = _rows(x, "x", shape, dtype, dev), None, 0
+    w = _vector(weight, "weight", c, dev)
     h = sum_out
     if h is not None:
-        _weight(h, "sum_out", shape, dtype)
+        _weight(h, "sum_out", shape, dtype, dev)
+    device = x.device
     if residual is not None:
-        r, ldr = residual.data_ptr(), _rows(residual, "residual", shape, dtype)
+        r, ldr = residual.data_ptr(), _rows(residual, "residual", shape, dtype, dev)
         if h is None:
-            h = torch.empty(shape, dtype=dtype, device=dev)
+            h = torch.empty(shape, dtype=dtype, device=device)
     if quantize:
-        out = torch.empty(shape, dtype=_E4M3, device=dev)
-        scale = torch.empty((n,), dtype=torch.float32, device=dev)
+        out = torch.empty(shape, dtype=_E4M3, device=device)
+        scale = torch.empty((n,), dtype=torch.float32, device=device)
     else:
-        out, scale = torch.empty(shape, dtype=dtype, device=dev), None
+        out, scale = torch.empty(shape, dtype=dtype, device=device), None
     rc = _lib().spconv_rms_norm(x.data_ptr(), ldx, r, ldr, w, n, c, dt, eps, None if h is None else h.data_ptr(),
                                 out.data_ptr(), 2 if quantize else dt, None if scale is None else scale.data_ptr(),
-                                _raw_stream(dev.index))
+                                _raw_stream(dev))
     if rc:
         raise SpconvError(rc, "spconv_rms_norm")
     if residual is None:
@@ -550,7 +558,7 @@ def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, d
     of x and of the residual alike; dweight fp32 [C]."""
     if stream is not None:
         return _on_stream(stream, (dy, x, weight, dres), lambda: rms_norm_backward(dy, x, weight, dres, eps=eps))
-    shape = _matrix(x, "x")
+    shape, dev = _matrix(x, "x")
     n, c = shape
     dtype = x.dtype
     dt = _DTYPES.get(dtype)
@@ -558,15 +566,15 @@ def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, d
         raise ValueError("x must be bf16 or fp32")
     if weight is None:
         raise ValueError("weight is required")
-    ldx, ldy, r, ldr = _rows(x, "x", shape, dtype), _rows(dy, "dy", shape, dtype), None, 0
+    ldx, ldy, r, ldr = _rows(x, "x", shape, dtype, dev), _rows(dy, "dy", shape, dtype, dev), None, 0
     if dres is not None:
-        r, ldr = dres.data_ptr(), _rows(dres, "dres", shape, dtype)
-    w = _vector(weight, "weight", c)
-    dev = x.device
-    dx = torch.empty(shape, dtype=dtype, device=dev)
-    dw = torch.empty((c,), dtype=torch.float32, device=dev)
+        r, ldr = dres.data_ptr(), _rows(dres, "dres", shape, dtype, dev)
+    w = _vector(weight, "weight", c, dev)
+    device = x.device
+    dx = torch.empty(shape, dtype=dtype, device=device)
+    dw = torch.empty((c,), dtype=torch.float32, device=device)
     rc = _lib().spconv_rms_norm_backward(dy.data_ptr(), ldy, x.data_ptr(), ldx, w, r, ldr, n, c, dt, eps, dx.data_ptr(),
-                                         dw.data_ptr(), _raw_stream(dev.index))
+                                         dw.data_ptr(), _raw_stream(dev))
     if rc:
         raise SpconvError(rc, "spconv_rms_norm_backward")
     return dx, dw
@@ -575,8 +583,8 @@ def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, d
 def _operands(x: torch.Tensor, w: torch.Tensor, name: str):
     """Checks x [N, C_in] against a weight, bf16 [C_in, C_out] or e4m3 [C_out, C_in].
 
-    Returns (n, c_in, c_out, whether e4m3, row stride of x, shape of the weight)."""
-    shape = _matrix(x, "x")
+    Returns (n, c_in, c_out, whether e4m3, row stride of x, shape of the weight, the GPU)."""
+    shape, dev = _matrix(x, "x")
     n, c_in = shape
     dtype = x.dtype
     if w.dim() != 2:
@@ -589,14 +597,14 @@ def _operands(x: torch.Tensor, w: torch.Tensor, name: str):
         wshape = (c_out, c_in)
     else:
         raise ValueError("x must be bf16 or float8_e4m3fn")
-    _weight(w, name, wshape, dtype)
-    return n, c_in, c_out, eight, _rows(x, "x", shape, dtype), wshape
+    _weight(w, name, wshape, dtype, dev)
+    return n, c_in, c_out, eight, _rows(x, "x", shape, dtype, dev), wshape, dev
 
 
-def _scale(t: Optional[torch.Tensor], name: str, c: int, eight: bool) -> Optional[int]:
+def _scale(t: Optional[torch.Tensor], name: str, c: int, eight: bool, dev: int) -> Optional[int]:
     if (t is not None) != eight:
         raise ValueError(f"{name}: e4m3 operands need their scales, bf16 ones have none")
-    return _vector(t, name, c) if eight else None
+    return _vector(t, name, c, dev) if eight else None
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor] = None, activation: str = "none",
@@ -612,20 +620,20 @@ def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor
         return _on_stream(stream, (x, weight, bias, residual, out, x_scale, w_scale),
                           lambda: linear(x, weight, bias=bias, activation=activation, residual=residual, out=out,
                                          x_scale=x_scale, w_scale=w_scale))
-    n, c_in, c_out, eight, ldx, _ = _operands(x, weight, "weight")
-    xs, ws = _scale(x_scale, "x_scale", n, eight), _scale(w_scale, "w_scale", c_out, eight)
+    n, c_in, c_out, eight, ldx, _, dev = _operands(x, weight, "weight")
+    xs, ws = _scale(x_scale, "x_scale", n, eight, dev), _scale(w_scale, "w_scale", c_out, eight, dev)
     b, r, ldr = None, None, 0
     if bias is not None:
-        b = _vector(bias, "bias", c_out)
+        b = _vector(bias, "bias", c_out, dev)
     if residual is not None:
-        r, ldr = residual.data_ptr(), _rows(residual, "residual", (n, c_out), _BF16)
-    dev = x.device
+        r, ldr = residual.data_ptr(), _rows(residual, "residual", (n, c_out), _BF16, dev)
+    device = x.device
     if out is None:
-        out, ldo = torch.empty((n, c_out), dtype=_BF16, device=dev), c_out
+        out, ldo = torch.empty((n, c_out), dtype=_BF16, device=device), c_out
     else:
-        ldo = _rows(out, "out", (n, c_out), _BF16)
+        ldo = _rows(out, "out", (n, c_out), _BF16, dev)
     rc = _lib().spconv_linear(x.data_ptr(), ldx, xs, weight.data_ptr(), ws, n, c_in, c_out, 2 if eight else 0, b,
-                              _activation(activation), r, ldr, out.data_ptr(), ldo, _raw_stream(dev.index))
+                              _activation(activation), r, ldr, out.data_ptr(), ldo, _raw_stream(dev))
     if rc:
         raise SpconvError(rc, "spconv_linear")
     return out
@@ -638,18 +646,17 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *, 
     if stream is not None:
         return _on_stream(stream, (dy, x, weight, bias),
                           lambda: linear_backward(dy, x, weight, bias=bias, activation=activation))
-    n, c_in, c_out, eight, ldx, wshape = _operands(x, weight, "weight")
+    n, c_in, c_out, eight, ldx, wshape, dev = _operands(x, weight, "weight")
     if eight:
         raise ValueError("gradients are of bf16 operands")
-    ldy = _rows(dy, "dy", (n, c_out), _BF16)
-    dev = x.device
-    dx = torch.empty((n, c_in), dtype=_BF16, device=dev)
-    dw = torch.empty(wshape, dtype=_BF16, device=dev)
-    db = None if bias is None else torch.empty((c_out,), dtype=torch.float32, device=dev)
+    ldy, b = _rows(dy, "dy", (n, c_out), _BF16, dev), None if bias is None else _vector(bias, "bias", c_out, dev)
+    device = x.device
+    dx = torch.empty((n, c_in), dtype=_BF16, device=device)
+    dw = torch.empty(wshape, dtype=_BF16, device=device)
+    db = None if bias is None else torch.empty((c_out,), dtype=torch.float32, device=device)
     rc = _lib().spconv_linear_backward(dy.data_ptr(), ldy, x.data_ptr(), ldx, weight.data_ptr(), n, c_in, c_out, 0,
-                                       None if bias is None else _vector(bias, "bias", c_out), _activation(activation),
-                                       dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(),
-                                       _raw_stream(dev.index))
+                                       b, _activation(activation), dx.data_ptr(), dw.data_ptr(),
+                                       None if db is None else db.data_ptr(), _raw_stream(dev))
     if rc:
         raise SpconvError(rc, "spconv_linear_backward")
     return dx, dw, db
@@ -666,17 +673,17 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, acti
         return _on_stream(stream, (x, w_gate, w_up, out, x_scale, gate_scale, up_scale),
                           lambda: gated_ffn(x, w_gate, w_up, activation=activation, out=out, x_scale=x_scale,
                                             gate_scale=gate_scale, up_scale=up_scale))
-    n, c_in, c_h, eight, ldx, wshape = _operands(x, w_gate, "w_gate")
-    up = _weight(w_up, "w_up", wshape, x.dtype)
-    xs = _scale(x_scale, "x_scale", n, eight)
-    gs, us = _scale(gate_scale, "gate_scale", c_h, eight), _scale(up_scale, "up_scale", c_h, eight)
-    dev = x.device
+    n, c_in, c_h, eight, ldx, wshape, dev = _operands(x, w_gate, "w_gate")
+    up = _weight(w_up, "w_up", wshape, x.dtype, dev)
+    xs = _scale(x_scale, "x_scale", n, eight, dev)
+    gs, us = _scale(gate_scale, "gate_scale", c_h, eight, dev), _scale(up_scale, "up_scale", c_h, eight, dev)
+    device = x.device
     if out is None:
-        out, ldo = torch.empty((n, c_h), dtype=_BF16, device=dev), c_h
+        out, ldo = torch.empty((n, c_h), dtype=_BF16, device=device), c_h
     else:
-        ldo = _rows(out, "out", (n, c_h), _BF16)
+        ldo = _rows(out, "out", (n, c_h), _BF16, dev)
     rc = _lib().spconv_gated_ffn(x.data_ptr(), ldx, xs, w_gate.data_ptr(), gs, up, us, n, c_in, c_h, 2 if eight else 0,
-                                 _activation(activation), out.data_ptr(), ldo, _raw_stream(dev.index))
+                                 _activation(activation), out.data_ptr(), ldo, _raw_stream(dev))
     if rc:
         raise SpconvError(rc, "spconv_gated_ffn")
     return out
@@ -688,17 +695,17 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     if stream is not None:
         return _on_stream(stream, (dh, x, w_gate, w_up),
                           lambda: gated_ffn_backward(dh, x, w_gate, w_up, activation=activation))
-    n, c_in, c_h, eight, ldx, wshape = _operands(x, w_gate, "w_gate")
+    n, c_in, c_h, eight, ldx, wshape, dev = _operands(x, w_gate, "w_gate")
     if eight:
         raise ValueError("gradients are of bf16 operands")
-    up = _weight(w_up, "w_up", wshape, x.dtype)
-    ldh = _rows(dh, "dh", (n, c_h), _BF16)
-    dev = x.device
-    dx = torch.empty((n, c_in), dtype=_BF16, device=dev)
-    dwg, dwu = torch.empty(wshape, dtype=_BF16, device=dev), torch.empty(wshape, dtype=_BF16, device=dev)
+    up = _weight(w_up, "w_up", wshape, x.dtype, dev)
+    ldh = _rows(dh, "dh", (n, c_h), _BF16, dev)
+    device = x.device
+    dx = torch.empty((n, c_in), dtype=_BF16, device=device)
+    dwg, dwu = torch.empty(wshape, dtype=_BF16, device=device), torch.empty(wshape, dtype=_BF16, device=device)
     rc = _lib().spconv_gated_ffn_backward(dh.data_ptr(), ldh, x.data_ptr(), ldx, w_gate.data_ptr(), up, n, c_in, c_h, 0,
                                           _activation(activation), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(),
-                                          _raw_stream(dev.index))
+                                          _raw_stream(dev))
     if rc:
         raise SpconvError(rc, "spconv_gated_ffn_backward")
     return dx, dwg, dwu
@@ -708,11 +715,12 @@ def quantize_weight(weight: torch.Tensor, *, stream: Optional[torch.cuda.Stream]
     """``spconv_quantize_weight``: bf16 [C_in, C_out] to (e4m3 [C_out, C_in], fp32 scale [C_out]), once per weight."""
     if stream is not None:
         return _on_stream(stream, (weight,), lambda: quantize_weight(weight))
-    c_in, c_out = _matrix(weight, "weight")
-    w = _weight(weight, "weight", (c_in, c_out), _BF16)
-    q = torch.empty((c_out, c_in), dtype=_E4M3, device=weight.device)
-    scale = torch.empty((c_out,), dtype=torch.float32, device=weight.device)
-    rc = _lib().spconv_quantize_weight(w, c_in, c_out, q.data_ptr(), scale.data_ptr(), _raw_stream(weight.device.index))
+    (c_in, c_out), dev = _matrix(weight, "weight")
+    w = _weight(weight, "weight", (c_in, c_out), _BF16, dev)
+    device = weight.device
+    q = torch.empty((c_out, c_in), dtype=_E4M3, device=device)
+    scale = torch.empty((c_out,), dtype=torch.float32, device=device)
+    rc = _lib().spconv_quantize_weight(w, c_in, c_out, q.data_ptr(), scale.data_ptr(), _raw_stream(dev))
     if rc:
         raise SpconvError(rc, "spconv_quantize_weight")
     return q, scale
@@ -720,8 +728,10 @@ def quantize_weight(weight: torch.Tensor, *, stream: Optional[torch.cuda.Stream]
 
 def rows_status(stream: Optional[torch.cuda.Stream] = None) -> int:
     """``spconv_rows_status``: 0, or the first error the row-wise operators recorded on the device since
-    the last call (synchronises)."""
-    return int(library().spconv_rows_status(_stream_ptr(stream)))
+    the last call (synchronises): on the current GPU, or on the stream's."""
+    if stream is not None:
+        return _on_stream(stream, (), rows_status)
+    return int(library().spconv_rows_status(_stream_ptr(None)))
 
 
 def last_launch_count() -> int:
