@@ -34,8 +34,9 @@ Between two convolutions on the same sites, on rows of features alone:
 with 8-bit forms (``rms_norm(..., quantize=True)``, ``quantize_weight``) and
 gradients (``rms_norm_backward``, ``linear_backward``, ``gated_ffn_backward``).
 
-The tensors of a row-wise call lie on the current GPU (``ValueError``
-otherwise); a ``stream`` argument makes its own GPU current for the call.
+The tensors, maps and packs of a call lie on the current GPU (``ValueError``
+otherwise).  A ``stream`` argument belongs to it too; for a row-wise operator it
+makes its own GPU current during the call.
 
 Errors raise ``SpconvError`` with the library's status code; errors found on
 the device (duplicate or out-of-range coordinates) surface through
@@ -62,6 +63,7 @@ BIT_ORDERS = {"calibrated": 0, "plain": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _E4M3 = torch.float8_e4m3fn
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_current_device = torch._C._cuda_getDevice   # (without a Device object)
 
 
 def library():
@@ -87,9 +89,17 @@ def _check(code: int, where: str):
         raise SpconvError(code, where)
 
 
+def _require_current(dev: int, name: str):
+    """The library launches and allocates on the current device, so everything of a call belongs to it."""
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+
+
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    _require_current(stream.device.index, "stream")
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
@@ -101,6 +111,7 @@ def _require_cuda(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    _require_current(t.get_device(), name)
 
 
 class Map:
@@ -121,6 +132,10 @@ class Map:
         if self._h is None:
             raise ValueError("map has been destroyed")
         return self._h
+
+    def require_current(self):
+        """Raises ``ValueError`` where the map is not on the current GPU."""
+        _require_current(self._coords.get_device(), "map")
 
     def destroy(self):
         if getattr(self, "_h", None) is not None:
@@ -148,6 +163,10 @@ class WPack:
             raise ValueError("weight pack has been destroyed")
         return self._h
 
+    def require_current(self):
+        """Raises ``ValueError`` where the pack is not on the current GPU."""
+        _require_current(self._src.get_device(), "weight pack")
+
     def destroy(self):
         if getattr(self, "_h", None) is not None:
             library().spconv_wpack_destroy(self._h)
@@ -171,6 +190,7 @@ def build_map(coords: torch.Tensor, spatial_shape: Optional[Sequence[int]] = Non
     decomposition on this map (``GEMMS``).  ``kernel_size`` 3 or 5;
     ``groups`` the offset groups (0: 1 for K = 3, 5 for K = 5; or K).
     """
+    st = _stream_ptr(stream)
     lib = library()
     _require_cuda(coords, "coords")
     if coords.dtype != torch.int32 or coords.dim() != 2 or coords.shape[1] != 4:
@@ -183,7 +203,7 @@ def build_map(coords: torch.Tensor, spatial_shape: Optional[Sequence[int]] = Non
     h = ctypes.c_void_p()
     rc = lib.spconv_build_map(_ptr(coords), int(coords.shape[0]),
                               ctypes.cast(shape_arr, _native.c_int32_p) if shape_arr is not None else None,
-                              int(batch_size), int(kernel_size), ctypes.byref(opt), _stream_ptr(stream),
+                              int(batch_size), int(kernel_size), ctypes.byref(opt), st,
                               ctypes.byref(h))
     _check(rc, "spconv_build_map")
     return Map(h, int(coords.shape[0]), coords, int(kernel_size))
@@ -225,6 +245,7 @@ def build_map_strided(coords: torch.Tensor, spatial_shape: Optional[Sequence[int
     """``spconv_build_map_strided``: the map of a strided convolution (kernel 3, stride 2,
     padding 1) from the input sites ``coords``; its rows are the output sites
     (``map_out_coords``).  Synchronises the stream once."""
+    st = _stream_ptr(stream)
     lib = library()
     _require_cuda(coords, "coords")
     if coords.dtype != torch.int32 or coords.dim() != 2 or coords.shape[1] != 4:
@@ -237,7 +258,7 @@ def build_map_strided(coords: torch.Tensor, spatial_shape: Optional[Sequence[int
     rc = lib.spconv_build_map_strided(_ptr(coords), int(coords.shape[0]),
                                       ctypes.cast(shape_arr, _native.c_int32_p) if shape_arr is not None else None,
                                       int(batch_size), int(kernel_size), int(stride), ctypes.byref(opt),
-                                      _stream_ptr(stream), ctypes.byref(h))
+                                      st, ctypes.byref(h))
     _check(rc, "spconv_build_map_strided")
     rows = ctypes.c_int64(0)
     _check(lib.spconv_map_rows(h, ctypes.byref(rows), None), "spconv_map_rows")   # (no second synchronisation)
@@ -247,6 +268,7 @@ def build_map_strided(coords: torch.Tensor, spatial_shape: Optional[Sequence[int
 def build_map_inverse(m: Map, bit_order: str = "calibrated") -> Map:
     """``spconv_build_map_inverse``: the map of the transposed convolution of strided map
     ``m``, from its output sites back onto its input sites."""
+    m.require_current()
     opt = _native.Options(0, BIT_ORDERS[bit_order], 0, 0, 0, 0)
     h = ctypes.c_void_p()
     _check(library().spconv_build_map_inverse(m.handle, ctypes.byref(opt), ctypes.byref(h)),
@@ -256,8 +278,10 @@ def build_map_inverse(m: Map, bit_order: str = "calibrated") -> Map:
 
 def map_out_coords(m: Map, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """``spconv_map_out_coords``: a strided map's output sites, int32 [n, 4]."""
+    m.require_current()
+    st = _stream_ptr(stream)
     out = torch.empty((m.n, 4), dtype=torch.int32, device=torch.device("cuda", torch.cuda.current_device()))
-    _check(library().spconv_map_out_coords(m.handle, _ptr(out), _stream_ptr(stream)), "spconv_map_out_coords")
+    _check(library().spconv_map_out_coords(m.handle, _ptr(out), st), "spconv_map_out_coords")
     return out
 
 
@@ -274,6 +298,8 @@ def subm_forward(m: Map, feats: torch.Tensor, weights: torch.Tensor,
     are applied to each fp32 sum before that rounding
     (``spconv_subm_forward_ex``): y = sum*scale + bias + residual, then max(y, 0).
     """
+    m.require_current()
+    st = _stream_ptr(stream)
     lib = library()
     _require_cuda(feats, "feats")
     _require_cuda(weights, "weights")
@@ -293,11 +319,11 @@ def subm_forward(m: Map, feats: torch.Tensor, weights: torch.Tensor,
     epi, _keep = _epilogue(m.n, c_out, feats.dtype, feats.device, scale, bias, residual, relu)
     if epi is None:
         rc = lib.spconv_subm_forward(m.handle, _ptr(feats), _ptr(weights), _ptr(out), c_in, c_out,
-                                     _DTYPES[feats.dtype], _stream_ptr(stream))
+                                     _DTYPES[feats.dtype], st)
         _check(rc, "spconv_subm_forward")
     else:
         rc = lib.spconv_subm_forward_ex(m.handle, _ptr(feats), _ptr(weights), _ptr(out), c_in, c_out,
-                                        _DTYPES[feats.dtype], ctypes.byref(epi), _stream_ptr(stream))
+                                        _DTYPES[feats.dtype], ctypes.byref(epi), st)
         _check(rc, "spconv_subm_forward_ex")
     return out
 
@@ -305,6 +331,7 @@ def subm_forward(m: Map, feats: torch.Tensor, weights: torch.Tensor,
 def wpack_create(weights: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> WPack:
     """``spconv_wpack_create_ex``: pack [K^3, C_in, C_out] weights (K = 3 or 5,
     from the first dimension) once for many forwards."""
+    st = _stream_ptr(stream)
     lib = library()
     _require_cuda(weights, "weights")
     sizes = {27: 3, 125: 5}
@@ -313,7 +340,7 @@ def wpack_create(weights: torch.Tensor, stream: Optional[torch.cuda.Stream] = No
     c_in, c_out = int(weights.shape[1]), int(weights.shape[2])
     h = ctypes.c_void_p()
     rc = lib.spconv_wpack_create_ex(_ptr(weights), sizes[int(weights.shape[0])], c_in, c_out,
-                                    _DTYPES[weights.dtype], _stream_ptr(stream), ctypes.byref(h))
+                                    _DTYPES[weights.dtype], st, ctypes.byref(h))
     _check(rc, "spconv_wpack_create_ex")
     return WPack(h, c_in, c_out, weights.dtype, weights, int(weights.shape[0]))
 
@@ -324,6 +351,9 @@ def subm_forward_packed(m: Map, feats: torch.Tensor, wp: WPack, out: Optional[to
                         residual: Optional[torch.Tensor] = None, relu: bool = False) -> torch.Tensor:
     """``spconv_subm_forward_packed``: forward with weights from ``wpack_create``;
     the epilogue arguments are those of ``subm_forward``."""
+    m.require_current()
+    wp.require_current()
+    st = _stream_ptr(stream)
     lib = library()
     _require_cuda(feats, "feats")
     if feats.dtype != wp.dtype or feats.dim() != 2 or feats.shape != (m.n_in, wp.c_in):
@@ -338,11 +368,10 @@ def subm_forward_packed(m: Map, feats: torch.Tensor, wp: WPack, out: Optional[to
             raise ValueError(f"out must be {feats.dtype} [{m.n}, {wp.c_out}]")
     epi, _keep = _epilogue(m.n, wp.c_out, feats.dtype, feats.device, scale, bias, residual, relu)
     if epi is None:
-        rc = lib.spconv_subm_forward_packed(m.handle, _ptr(feats), wp.handle, _ptr(out), _stream_ptr(stream))
+        rc = lib.spconv_subm_forward_packed(m.handle, _ptr(feats), wp.handle, _ptr(out), st)
         _check(rc, "spconv_subm_forward_packed")
     else:
-        rc = lib.spconv_subm_forward_packed_ex(m.handle, _ptr(feats), wp.handle, _ptr(out), ctypes.byref(epi),
-                                               _stream_ptr(stream))
+        rc = lib.spconv_subm_forward_packed_ex(m.handle, _ptr(feats), wp.handle, _ptr(out), ctypes.byref(epi), st)
         _check(rc, "spconv_subm_forward_packed_ex")
     return out
 
@@ -355,6 +384,10 @@ def subm_forward_layers(m: Map, feats: torch.Tensor, wps: Sequence[WPack], relu:
     when ``relu[l]``.  ``outs`` gives one output per layer (consecutive ones may
     not overlap; two buffers may alternate); by default two buffers alternate.
     Returns the list of per-layer outputs (views of ``outs``)."""
+    m.require_current()
+    for w in wps:
+        w.require_current()
+    st = _stream_ptr(stream)
     lib = library()
     _require_cuda(feats, "feats")
     L = len(wps)
@@ -381,8 +414,7 @@ def subm_forward_layers(m: Map, feats: torch.Tensor, wps: Sequence[WPack], relu:
     for l in range(L):
         epis[l].relu = 1 if relu[l] else 0
     rc = lib.spconv_subm_forward_layers(m.handle, _ptr(feats), ctypes.cast(wh, ctypes.POINTER(ctypes.c_void_p)),
-                                        ctypes.cast(oh, ctypes.POINTER(ctypes.c_void_p)), L, epis,
-                                        _stream_ptr(stream))
+                                        ctypes.cast(oh, ctypes.POINTER(ctypes.c_void_p)), L, epis, st)
     _check(rc, "spconv_subm_forward_layers")
     return outs
 
@@ -409,6 +441,8 @@ def map_info(m: Map) -> dict:
 def map_export(m: Map, stream: Optional[torch.cuda.Stream] = None) -> dict:
     """``spconv_map_export``: nbr [N, V], tap_off [V+1], in_rows/out_rows [P];
     mask and perm [N] with one offset group, [G, N] with G > 1."""
+    m.require_current()
+    st = _stream_ptr(stream)
     info = map_info(m)
     n, p = info["n"], info["pairs"]
     V, G = info["kernel_size"] ** 3, info["groups"]
@@ -421,7 +455,7 @@ def map_export(m: Map, stream: Optional[torch.cuda.Stream] = None) -> dict:
     ins = torch.empty((max(p, 1),), dtype=torch.int32, device=dev)
     outs = torch.empty((max(p, 1),), dtype=torch.int32, device=dev)
     rc = library().spconv_map_export(m.handle, _ptr(nbr), _ptr(mask), _ptr(perm), _ptr(tap_off),
-                                     _ptr(ins), _ptr(outs), _stream_ptr(stream))
+                                     _ptr(ins), _ptr(outs), st)
     _check(rc, "spconv_map_export")
     return dict(nbr=nbr, mask=mask, perm=perm, tap_off=tap_off, in_rows=ins[:p], out_rows=outs[:p],
                 info=info)
@@ -437,7 +471,6 @@ def map_destroy(m: Map):
 # at each tensor once and allocate only outputs.
 _BF16 = torch.bfloat16
 _raw_stream = torch._C._cuda_getCurrentRawStream   # of a device, without making a Stream object
-_current_device = torch._C._cuda_getDevice
 _c = None
 
 
@@ -490,8 +523,7 @@ def _matrix(t: torch.Tensor, name: str):
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     dev = t.get_device()
-    if dev != _current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    _require_current(dev, name)
     return t.shape, dev
 
 

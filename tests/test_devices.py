@@ -72,3 +72,56 @@ def test_row_operators_refuse_another_gpu(entry, operands):
     for name in operands:                                          # one of them on another
         with pytest.raises(ValueError):
             entry(**make(operands, [name]))
+
+
+# ---- the convolution's entries ---------------------------------------------------
+class Stream:
+    cuda_stream = 0
+
+    def __init__(self, gpu):
+        self.device = torch.device("cuda", gpu)
+
+
+def conv_map(gpu):
+    return sc.Map(None, N, On(gpu, (N, 4), torch.int32))
+
+
+def pack(gpu):
+    return sc.WPack(None, C, H, BF, On(gpu, (27, C, H)))
+
+
+def square(gpu):
+    return sc.WPack(None, C, C, BF, On(gpu, (27, C, C)))
+
+
+FEATS, OUT, WEIGHTS = ((N, C), BF), ((N, H), BF), ((27, C, H), BF)
+CONV = [
+    ("build_map", dict(coords=((N, 4), torch.int32)), {}),
+    ("build_map_strided", dict(coords=((N, 4), torch.int32)), {}),
+    ("wpack_create", dict(weights=WEIGHTS), {}),
+    ("subm_forward", dict(feats=FEATS, weights=WEIGHTS, out=OUT, scale=((H,), F32), bias=((H,), F32), residual=OUT),
+     dict(m=conv_map)),
+    ("subm_forward_packed", dict(feats=FEATS, out=OUT, scale=((H,), F32), bias=((H,), F32), residual=OUT),
+     dict(m=conv_map, wp=pack)),
+    ("subm_forward_layers", dict(feats=FEATS), dict(m=conv_map, wps=lambda gpu: [square(gpu)])),
+    ("map_export", {}, dict(m=conv_map)),
+    ("map_out_coords", {}, dict(m=conv_map)),
+]
+
+
+@pytest.mark.parametrize("name,tensors,handles", CONV)
+def test_convolution_entries_refuse_another_gpu(monkeypatch, name, tensors, handles):
+    class Lib:   # stands for the library; no function of it may be called
+        def __getattr__(self, fn):
+            raise AssertionError("the call went past the checks")
+    monkeypatch.setattr(sc, "library", Lib)
+    entry = getattr(sc, name)
+
+    def call(there=(), stream=0):
+        kw = {k: h(1 if k in there else 0) for k, h in handles.items()}
+        return entry(**kw, **make(tensors, there), stream=Stream(stream))
+    for there in [[k] for k in (*tensors, *handles)]:
+        with pytest.raises(ValueError, match="current"):
+            call(there)
+    with pytest.raises(ValueError, match="current"):
+        call(stream=1)
