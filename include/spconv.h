@@ -537,6 +537,15 @@ int32_t spconv_last_launch_count(void);
  */
 int spconv_selftest_wait_timeout(int32_t which, int64_t limit_ns, void* stream);
 
+/*
+ * Diagnostics: the same for the row-wise operators.  Enqueues a kernel that
+ * waits, as theirs do, on a barrier that nothing arrives on and gives up after
+ * limit_ns (1 ms .. 100 ms).  spconv_rows_status then returns
+ * SPCONV_ERR_TIMEOUT once.  Returns SPCONV_OK, SPCONV_ERR_INVALID_ARG for a
+ * limit out of range, or SPCONV_ERR_CUDA.
+ */
+int spconv_selftest_rows_wait(int64_t limit_ns, void* stream);
+
 const char* spconv_status_string(int status);
 
 #ifdef __cplusplus

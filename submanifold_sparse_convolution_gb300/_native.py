@@ -89,6 +89,7 @@ SIGNATURES = {
     "spconv_rows_status": (ctypes.c_int, [_P]),
     "spconv_last_launch_count": (ctypes.c_int32, []),
     "spconv_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
+    "spconv_selftest_rows_wait": (ctypes.c_int, [_I64, _P]),
     "spconv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

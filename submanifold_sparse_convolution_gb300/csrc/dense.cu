@@ -1,12 +1,25 @@
 // Around the tensor-core products: rows brought into the alignment that the
 // tensor maps need, the column sums of the bias gradients, and the 8-bit weight
 // layout.
+#include "ptx_sm100.cuh"
 #include "rows.cuh"
 
 namespace spconv {
 namespace {
 
 __device__ int32_t g_rows_status;   // kStatus* bits of the row-wise operators' bounded waits
+
+// A warp's wait as the operators make it, on a barrier without copies or
+// arrivals: it gives up after limit_ns and records that.
+__global__ void __launch_bounds__(32) k_rows_wait_probe(int32_t* status, uint64_t limit_ns) {
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&bar, 1);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&bar, 0, nullptr, limit_ns)) && threadIdx.x == 0) atomicOr(status, kStatusTimeout);
+}
 
 // ---- copies to aligned rows ---------------------------------------------------------
 // A warp per 256 elements E of a row, neighbouring lanes on neighbouring
@@ -334,6 +347,14 @@ int rows_status_word(int32_t** word) {
     }
     *word = words[dev];
     return SPCONV_OK;
+}
+
+int rows_wait_probe(uint64_t limit_ns, cudaStream_t s) {
+    int32_t* status = nullptr;
+    SPCONV_CHECK(rows_status_word(&status));
+    count_launch();
+    k_rows_wait_probe<<<1, 32, 0, s>>>(status, limit_ns);
+    return launch_status();
 }
 
 void AlignedRows::add(const void** p, int count, int64_t* ld, int64_t rows, int64_t cols, size_t es) {

@@ -341,6 +341,8 @@ bool dense_few_takes(const DenseOp& op);
 int dense_few_run(const DenseOp& op, int32_t* status, cudaStream_t s);
 // The device status word of the row-wise operators on the current device.
 int rows_status_word(int32_t** word);
+// Runs their wait against a barrier that nothing arrives on (spconv_selftest_rows_wait).
+int rows_wait_probe(uint64_t limit_ns, cudaStream_t s);
 
 // What a tensor map takes: 16-byte aligned rows.
 inline bool tma_ok(const void* p, int64_t ld, size_t es) {

@@ -363,6 +363,12 @@ int spconv_rows_status(void* stream) {
     return status_from_flags(st);
 }
 
+int spconv_selftest_rows_wait(int64_t limit_ns, void* stream) {
+    reset_launch_count();
+    if (limit_ns < 1000000 || limit_ns > 100000000) return SPCONV_ERR_INVALID_ARG;
+    return rows_wait_probe(static_cast<uint64_t>(limit_ns), static_cast<cudaStream_t>(stream));
+}
+
 int spconv_quantize_weight(const void* w_dev, int32_t c_in, int32_t c_out, void* q_dev, float* scale_dev, void* stream) {
     reset_launch_count();
     if (bad_sizes(0, c_in, c_out) || !w_dev || !aligned(w_dev, 2) || !q_dev || !scale_dev || bad_vec(scale_dev))

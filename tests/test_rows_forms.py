@@ -43,3 +43,22 @@ def test_norm_backward_of_rows_far_from_unit_size(n, c, dtype, size, eps):
     close(dx, ref, slack, "dx", 2.0 ** -8 if dtype == BF else 2.0 ** -24)
     terms = D * unit
     assert ((dw.double() - terms.sum(0)).abs() <= (acc + (n / 152 + 40) * 2.0 ** -23) * terms.abs().sum(0)).all()
+
+
+def test_a_wait_that_runs_out_reaches_the_status():
+    """The operators' bounded wait on a barrier that nothing arrives on, with a 50 ms limit: it gives up, the
+    status says so once, and the operators go on working."""
+    lib, stream = sc.library(), torch.cuda.current_stream().cuda_stream
+    assert sc.rows_status() == 0
+    for limit in (0, 999_999, 100_000_001, -5):
+        assert lib.spconv_selftest_rows_wait(limit, stream) == -1
+    assert sc.rows_status() == 0
+    assert lib.spconv_selftest_rows_wait(50_000_000, stream) == 0
+    assert sc.rows_status() == -8
+    assert sc.rows_status() == 0
+    side = torch.cuda.Stream()
+    assert lib.spconv_selftest_rows_wait(50_000_000, side.cuda_stream) == 0
+    assert sc.rows_status(stream=side) == -8 and sc.rows_status(stream=side) == 0
+    x = torch.ones(3, 64, device="cuda")
+    assert torch.allclose(sc.rms_norm(x, x[0], eps=0.0), x)
+    assert sc.rows_status() == 0
