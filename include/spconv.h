@@ -391,8 +391,10 @@ int spconv_kernel_map_static(const int32_t* coords_dev, int64_t n, const int32_t
  *   Order      every sum has a fixed order: the same call gives the same bits.
  *   Scratch    taken from the library's pool in stream order for the length
  *              of the call.
- *   Capture    calls can be captured into a CUDA graph; the first call of an
- *              operator on a device loads its kernels, so make it before.
+ *   Capture    calls can be captured into a CUDA graph.  Which kernels a call
+ *              takes depends on its sizes, types, strides, alignment and
+ *              options, and each is loaded at its first launch on a device: make
+ *              the call that is to be captured once before.
  *   Aliasing   an output must not overlap an input (biases, scales and weights
  *              included) or another output, unless said below
  *              (SPCONV_ERR_ALIAS).  Column ranges of one wider matrix do not

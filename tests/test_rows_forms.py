@@ -62,3 +62,32 @@ def test_a_wait_that_runs_out_reaches_the_status():
     x = torch.ones(3, 64, device="cuda")
     assert torch.allclose(sc.rms_norm(x, x[0], eps=0.0), x)
     assert sc.rows_status() == 0
+
+
+@pytest.mark.parametrize("n,c,h", [(1, 2048, 2048), (3000, 512, 256), (300, 501, 77), (200, 2048, 136), (20, 5001, 64)])
+def test_captured_after_the_same_call(n, c, h):
+    """Every operator at sizes that reach few-row, wide, cut and copying kernels: made once, then captured."""
+    g = gen(n + c + h)
+    x, dy = normal(g, n, c).to(BF), normal(g, n, h).to(BF)
+    w, u = normal(g, c, h, std=c ** -0.5).to(BF), normal(g, c, h, std=c ** -0.5).to(BF)
+    wn, b = 1 + normal(g, c, std=0.1), normal(g, h)
+
+    def calls():
+        q, scale = sc.quantize_weight(w)
+        x8, xs = sc.rms_norm(x, wn, quantize=True)
+        return [sc.rms_norm(x, wn), scale, xs, sc.linear(x, w, bias=b, activation="gelu"),
+                sc.linear(x8, q, x_scale=xs, w_scale=scale), sc.gated_ffn(x, w, u),
+                sc.gated_ffn(x8, q, q, x_scale=xs, gate_scale=scale, up_scale=scale),
+                *sc.linear_backward(dy, x, w, bias=b, activation="silu"), *sc.gated_ffn_backward(dy, x, w, u),
+                *sc.rms_norm_backward(x, x, wn)]
+    first = [t.clone() for t in calls()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = calls()
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, first))
