@@ -8,7 +8,7 @@ import torch
 
 import submanifold_sparse_convolution_gb300 as sc
 from submanifold_sparse_convolution_gb300 import build as build_mod
-from test_rows import BF, close, gen, normal
+from test_rows import BF, act64, close, gen, grad_check, make, normal, sum_error
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +91,80 @@ def test_captured_after_the_same_call(n, c, h):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, first))
+
+
+# ---- the C entries' forms that the Python ones do not take -----------------------------
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def address(t):
+    return None if t is None else t.data_ptr()
+
+
+PARTS = [(5, 64, 72), (300, 64, 72), (129, 33, 50), (2000, 512, 520), (200, 2048, 136)]
+
+
+@pytest.mark.parametrize("n,c,h", PARTS)
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("wants", ["x", "w", "b", "xw", "xb", "wb", "xwb"])
+def test_linear_backward_of_some_outputs(n, c, h, act, wants):
+    g = gen(n + c + h)
+    x, (w,), _, _, X, (W,) = make(g, n, c, h, False)
+    dy, b = normal(g, n, h).to(BF), normal(g, h)
+    nan = float("nan")
+    dx = torch.full((n, c), nan, device="cuda", dtype=BF) if "x" in wants else None
+    dw = torch.full((c, h), nan, device="cuda", dtype=BF) if "w" in wants else None
+    db = torch.full((h,), nan, device="cuda") if "b" in wants else None
+    assert sc.library().spconv_linear_backward(dy.data_ptr(), h, x.data_ptr(), c, w.data_ptr(), n, c, h, 0, b.data_ptr(),
+                                               sc.ACTIVATIONS[act], address(dx), address(dw), address(db), stream()) == 0
+    z = X @ W + b.double()
+    dz = dy.double() * act64(act, z)[1]
+    err = dy.double().abs() * (1.1 * sum_error(X, W) + 2.0 ** -20)   # (of z, second derivatives below 1.1)
+    dz_abs = dz.abs() + 2.0 ** 8 * err
+    if dx is not None:
+        grad_check(dx, dz @ W.t(), dz_abs @ W.abs().t(), "dx")
+    if dw is not None:
+        grad_check(dw, X.t() @ dz, X.abs().t() @ dz_abs, "dw")
+    if db is not None:
+        bound = err + dz.abs() * (n / 128 + 64) * 2.0 ** -23
+        assert ((db.double() - dz.sum(0)).abs() <= bound.sum(0) + 1e-30).all()
+
+
+@pytest.mark.parametrize("n,c,h", PARTS)
+@pytest.mark.parametrize("wants", ["x", "w"])
+def test_gated_backward_of_some_outputs(n, c, h, wants):
+    g = gen(n + 5 * c + h)
+    x, (wg, wu), _, _, X, (G, U) = make(g, n, c, h, False, 2)
+    dh = normal(g, n, h).to(BF)
+    nan = float("nan")
+    dx = torch.full((n, c), nan, device="cuda", dtype=BF) if wants == "x" else None
+    dwg, dwu = (torch.full((c, h), nan, device="cuda", dtype=BF) if wants == "w" else None for _ in range(2))
+    assert sc.library().spconv_gated_ffn_backward(dh.data_ptr(), h, x.data_ptr(), c, wg.data_ptr(), wu.data_ptr(), n, c, h, 0,
+                                                  sc.ACTIVATIONS["silu"], address(dx), address(dwg), address(dwu),
+                                                  stream()) == 0
+    zg, zu, D = X @ G, X @ U, dh.double()
+    a, slope = act64("silu", zg)
+    dg, du = D * zu * slope, D * a
+    eg, eu = 1.2 * sum_error(X, G) + 2.0 ** -20, sum_error(X, U) + 2.0 ** -20
+    dg_abs = dg.abs() + 2.0 ** 8 * D.abs() * (eg * (zu.abs() + eu) + 1.2 * eu)
+    du_abs = du.abs() + 2.0 ** 8 * D.abs() * eg
+    if dx is not None:
+        grad_check(dx, dg @ G.t() + du @ U.t(), dg_abs @ G.abs().t() + du_abs @ U.abs().t(), "dx")
+    else:
+        grad_check(dwg, X.t() @ dg, X.abs().t() @ dg_abs, "dw_gate")
+        grad_check(dwu, X.t() @ du, X.abs().t() @ du_abs, "dw_up")
+
+
+@pytest.mark.parametrize("n,c", [*GRAD_WIDTHS, (1, 64), (1700, 128)])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_norm_backward_onto_the_incoming_gradient(n, c, dtype):
+    """dx may be dres: the same bits as into memory of its own."""
+    g = gen(n + 7 * c)
+    x, dy, dres = (normal(g, n, c).to(dtype) for _ in range(3))
+    w = 1 + normal(g, c, std=0.3)
+    dx, dw = sc.rms_norm_backward(dy, x, w, dres)
+    own = torch.full((c,), float("nan"), device="cuda")
+    assert sc.library().spconv_rms_norm_backward(dy.data_ptr(), c, x.data_ptr(), c, w.data_ptr(), dres.data_ptr(), c, n, c,
+                                                 0 if dtype == BF else 1, 1e-6, dres.data_ptr(), own.data_ptr(), stream()) == 0
+    assert torch.equal(dres, dx) and torch.equal(own, dw)
