@@ -25,6 +25,9 @@
  * handles and packed-weight handles (stream-ordered, on the stream passed to
  * the creating call) and frees them in the matching destroy call; the row-wise
  * operators below take scratch memory in stream order for the length of a call.
+ * All of it comes from a pool of the library's own on each device, which keeps
+ * what is freed for later calls (a gated gradient of n rows and c_hidden
+ * channels leaves 4 n c_hidden bytes there); spconv_trim_pool gives it back.
  *
  * Streams: all work is enqueued on the caller's stream; nothing synchronises
  * the device except where a function says it does.
@@ -512,6 +515,13 @@ int spconv_quantize_weight(const void* w_dev, int32_t c_in, int32_t c_out, void*
  * of a call are incomplete), else SPCONV_OK.
  */
 int spconv_rows_status(void* stream);
+
+/*
+ * Synchronise the current device and give the memory that the library's pool
+ * holds there without using it back to the device, down to keep_bytes in all.
+ * Maps and weight packs stay.
+ */
+int spconv_trim_pool(int64_t keep_bytes);
 
 /* Number of kernel launches enqueued by the last call on this thread. */
 int32_t spconv_last_launch_count(void);

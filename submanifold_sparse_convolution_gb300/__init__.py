@@ -54,7 +54,8 @@ from . import _native
 __all__ = ["SpconvError", "Map", "WPack", "build_map", "subm_forward", "wpack_create",
            "subm_forward_packed", "map_status", "map_info", "map_export", "map_destroy",
            "rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
-           "quantize_weight", "rows_status", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS", "BIT_ORDERS", "PIPELINES", "GEMMS", "library"]
+           "quantize_weight", "rows_status", "trim_pool", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS",
+           "BIT_ORDERS", "PIPELINES", "GEMMS", "library"]
 
 MAPPERS = {"auto": 0, "dense": 1, "sorted": 2, "hash": 3}
 PIPELINES = {"auto": 0, "fused": 1, "multi": 2, "wide": 3}
@@ -764,6 +765,12 @@ def rows_status(stream: Optional[torch.cuda.Stream] = None) -> int:
     if stream is not None:
         return _on_stream(stream, (), rows_status)
     return int(library().spconv_rows_status(_stream_ptr(None)))
+
+
+def trim_pool(keep_bytes: int = 0):
+    """``spconv_trim_pool``: gives the memory that the library's pool holds on the current GPU without using it
+    (scratch of the row-wise operators, destroyed maps and packs) back to the device (synchronises)."""
+    _check(library().spconv_trim_pool(int(keep_bytes)), "spconv_trim_pool")
 
 
 def last_launch_count() -> int:

@@ -87,6 +87,7 @@ SIGNATURES = {
                                                  _P]),
     "spconv_quantize_weight": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P]),
     "spconv_rows_status": (ctypes.c_int, [_P]),
+    "spconv_trim_pool": (ctypes.c_int, [_I64]),
     "spconv_last_launch_count": (ctypes.c_int32, []),
     "spconv_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
     "spconv_selftest_rows_wait": (ctypes.c_int, [_I64, _P]),

@@ -67,13 +67,17 @@ bool use_tensor_path(int32_t c_in, int32_t c_out, int32_t dtype, const void* fea
 
 }  // namespace
 
+static cudaMemPool_t pools[kMaxDevices] = {};   // of the library, by device
+
 cudaError_t pool_alloc(void** p, size_t bytes, cudaStream_t s) {
-    static cudaMemPool_t pools[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaMallocAsync(p, bytes, s);
     if (pools[dev] == nullptr) {
+        // it keeps what is freed for the next call: given back at every
+        // synchronisation, a call after it would wait for new memory (spconv_trim_pool
+        // gives it back when asked)
         cudaMemPoolProps props = {};
         props.allocType = cudaMemAllocationTypePinned;
         props.location.type = cudaMemLocationTypeDevice;
@@ -472,6 +476,16 @@ int spconv_selftest_wait_timeout(int32_t which, int64_t limit_ns, void* stream) 
     reset_launch_count();
     if (which < 0 || which > 2 || limit_ns < 1000000 || limit_ns > 100000000) return SPCONV_ERR_INVALID_ARG;
     return wait_probe(which, static_cast<uint64_t>(limit_ns), static_cast<cudaStream_t>(stream));
+}
+
+int spconv_trim_pool(int64_t keep_bytes) {
+    if (keep_bytes < 0) return SPCONV_ERR_INVALID_ARG;
+    int dev = 0;
+    SPCONV_CHECK_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= kMaxDevices || pools[dev] == nullptr) return SPCONV_OK;
+    SPCONV_CHECK_CUDA(cudaDeviceSynchronize());   // (memory of work in flight is not free yet)
+    SPCONV_CHECK_CUDA(cudaMemPoolTrimTo(pools[dev], static_cast<size_t>(keep_bytes)));
+    return SPCONV_OK;
 }
 
 const char* spconv_status_string(int status) {

@@ -8,6 +8,7 @@ import torch
 
 import submanifold_sparse_convolution_gb300 as sc
 from submanifold_sparse_convolution_gb300 import build as build_mod
+from submanifold_sparse_convolution_gb300 import synthetic
 from test_rows import BF, act64, close, gen, grad_check, make, normal, sum_error
 
 pytestmark = pytest.mark.gpu
@@ -168,3 +169,26 @@ def test_norm_backward_onto_the_incoming_gradient(n, c, dtype):
     assert sc.library().spconv_rms_norm_backward(dy.data_ptr(), c, x.data_ptr(), c, w.data_ptr(), dres.data_ptr(), c, n, c,
                                                  0 if dtype == BF else 1, 1e-6, dres.data_ptr(), own.data_ptr(), stream()) == 0
     assert torch.equal(dres, dx) and torch.equal(own, dw)
+
+
+def test_scratch_is_given_back():
+    """The pool keeps a gated gradient's scratch (4 n c_hidden bytes) until it is trimmed; a map in it stays."""
+    wl = synthetic.random_cloud(31, 3000, shape=(16, 16, 16), c_in=64, c_out=64)
+    m = sc.build_map(wl.coords.cuda(), wl.spatial_shape, wl.batch_size)
+    feats, weights = wl.feats.cuda(), wl.weights[0].cuda()
+    ref = sc.subm_forward(m, feats, weights)
+    g = gen(32)
+    n, c, h = 16384, 64, 4096
+    x, dh = normal(g, n, c).to(BF), normal(g, n, h).to(BF)
+    wg, wu = normal(g, c, h).to(BF), normal(g, c, h).to(BF)
+    first = sc.gated_ffn_backward(dh, x, wg, wu)
+    torch.cuda.synchronize()
+    held = torch.cuda.mem_get_info()[0]
+    sc.trim_pool()
+    assert torch.cuda.mem_get_info()[0] - held >= 4 * n * h
+    assert all(torch.equal(a, b) for a, b in zip(sc.gated_ffn_backward(dh, x, wg, wu), first))
+    assert torch.equal(sc.subm_forward(m, feats, weights), ref) and sc.map_status(m) == 0
+    m.destroy()
+    sc.trim_pool(1 << 40)                     # keeps all
+    with pytest.raises(sc.SpconvError):
+        sc.trim_pool(-1)
