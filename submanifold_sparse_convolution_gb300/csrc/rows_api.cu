@@ -212,7 +212,10 @@ int spconv_linear_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev,
     cols.n = c_out;
     cols.out = dbias_dev;
     if (dbias_dev) cols.rows = act ? col_part_rows(n) : column_part_rows(n, c_out);
-    // dz, then the partial column sums
+    // dz, then the partial column sums.  dz is an operand of two products on the
+    // bf16 tensor pipe, so it is rounded once like any other: dx and dw are off by
+    // 2.3e-3 of their size, by their own rounding alone 1.7e-3.  Kept in 32 bits it
+    // would need products at half the rate (tf32) or twice as many (two halves).
     const size_t dz_bytes = act ? round_up(static_cast<size_t>(n) * ld_dz * 2, 256) : 0;
     Scratch buf(dz_bytes + static_cast<size_t>(cols.rows) * c_out * 4, s);
     if (buf.failed()) return SPCONV_ERR_OOM;
@@ -312,7 +315,8 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
     rows.add(w, 2, &ld_w, c_in, c_hidden, 2);
     rows.add(&dh.p, 1, &dh.ld, n, c_hidden, 2);
     SPCONV_CHECK(rows.run(s));
-    // gate and up are formed again in the product's epilogue, which writes their gradients
+    // gate and up are formed again in the product's epilogue, which writes their
+    // gradients, rounded as operands of the products that follow (as dz above)
     const int64_t ld_d = static_cast<int64_t>(round_up(c_hidden, 8));
     const size_t one = static_cast<size_t>(n) * ld_d * 2;
     Scratch d_buf(2 * one, s);
