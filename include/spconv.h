@@ -509,6 +509,48 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
 int spconv_quantize_weight(const void* w_dev, int32_t c_in, int32_t c_out, void* q_dev, float* scale_dev, void* stream);
 
 /*
+ * Group norm of ragged scans with an activation.  Rows offsets[s] ..
+ * offsets[s + 1] - 1 are scan s, a group is c / groups neighbouring channels,
+ * and the rows of a scan share each group's statistics:
+ *
+ *   out = act((x - mean) / sqrt(var + eps) * weight + bias)
+ *
+ * with the variance of the whole population (divided by the count).
+ *
+ *   x_dev        [n] rows of c, dtype (SPCONV_BF16 or SPCONV_FP32).
+ *   weight_dev   fp32 [c];  bias_dev fp32 [c] or NULL (0).
+ *   offsets_dev  int32 [scans + 1], ascending, in [0, n]; or NULL: one scan of
+ *                all rows (scans = 1).  A scan may be empty.  Rows of no scan
+ *                (before the first border, behind the last) are written as
+ *                zeros.  Borders out of order or range are an error that
+ *                spconv_rows_status returns (SPCONV_ERR_COORD_RANGE); no memory
+ *                outside the arguments is touched, and out is undefined.
+ *   out_dev      [n][c] dtype.
+ *   stats_dev    fp32 [scans][groups][2], mean and 1 / sqrt(var + eps), for the
+ *                backward pass (8-byte aligned); or NULL.  An empty scan has
+ *                mean 0 and variance 0.
+ * groups divides c; scans <= 2^20.  c > 8192 returns SPCONV_ERR_UNSUPPORTED.
+ */
+int spconv_group_norm(const void* x_dev, int64_t ld_x, const float* weight_dev, const float* bias_dev,
+                      const int32_t* offsets_dev, int64_t scans, int64_t n, int32_t c, int32_t groups, int32_t dtype,
+                      int32_t activation, float eps, void* out_dev, float* stats_dev, void* stream);
+
+/*
+ * Its backward pass, from the statistics that the forward pass wrote: with
+ * u = (x - mean) r, dz = dy act'(u weight + bias), p = dz weight, and means over
+ * a scan's group,
+ *
+ *   dx = r (p - mean(p) - u mean(p u));  dweight = sum dz u;  dbias = sum dz
+ *
+ *   dx_dev       [n][c] dtype, zeros in rows of no scan.
+ *   dweight_dev  fp32 [c]; dbias_dev fp32 [c] or NULL: over the rows of scans.
+ */
+int spconv_group_norm_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, const float* weight_dev,
+                               const float* bias_dev, const float* stats_dev, const int32_t* offsets_dev, int64_t scans,
+                               int64_t n, int32_t c, int32_t groups, int32_t dtype, int32_t activation, void* dx_dev,
+                               float* dweight_dev, float* dbias_dev, void* stream);
+
+/*
  * Synchronise the stream and return the first error that the row-wise
  * operators' kernels recorded on the current device since the last call of
  * this function (SPCONV_ERR_TIMEOUT: a bounded wait ran out and the results

@@ -54,7 +54,7 @@ from . import _native
 __all__ = ["SpconvError", "Map", "WPack", "build_map", "subm_forward", "wpack_create",
            "subm_forward_packed", "map_status", "map_info", "map_export", "map_destroy",
            "rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
-           "quantize_weight", "rows_status", "trim_pool", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS",
+           "quantize_weight", "group_norm", "group_norm_backward", "rows_status", "trim_pool", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS",
            "BIT_ORDERS", "PIPELINES", "GEMMS", "library"]
 
 MAPPERS = {"auto": 0, "dense": 1, "sorted": 2, "hash": 3}
@@ -611,6 +611,79 @@ def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, d
     if rc:
         raise SpconvError(rc, "spconv_rms_norm_backward")
     return dx, dw
+
+
+def _offsets(t: Optional[torch.Tensor], dev: int):
+    """(address, number of runs) of int32 borders [runs + 1] on GPU ``dev``; none: one run of all rows."""
+    if t is None:
+        return None, 1
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != dev or not t.is_contiguous() or t.shape[0] < 2:
+        raise ValueError(f"offsets must be a contiguous int32 [runs + 1] tensor on cuda:{dev}")
+    return t.data_ptr(), t.shape[0] - 1
+
+
+def _group_args(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], groups: int):
+    """(shape, GPU, dtype code, weight, bias) of a group norm's input and parameters."""
+    shape, dev = _matrix(x, "x")
+    c = shape[1]
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
+        raise ValueError("x must be bf16 or fp32")
+    if weight is None:
+        raise ValueError("weight is required")
+    if groups < 1 or c % groups:
+        raise ValueError(f"{groups} groups do not divide {c} channels")
+    return shape, dev, dt, _vector(weight, "weight", c, dev), None if bias is None else _vector(bias, "bias", c, dev)
+
+
+def group_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], groups: int, *,
+               offsets: Optional[torch.Tensor] = None, activation: str = "none", eps: float = 1e-5, stats: bool = False,
+               stream: Optional[torch.cuda.Stream] = None):
+    """``spconv_group_norm``: act((x - mean) / sqrt(var + eps) * weight + bias), the statistics of each scan and group.
+
+    ``x`` bf16 or fp32 [N, C] (rows may be strided), C at most 8192; ``weight`` fp32 [C], ``bias`` fp32 [C] or
+    None.  Rows ``offsets[s]`` to ``offsets[s + 1] - 1`` are scan s (int32 [scans + 1] on the GPU, ascending;
+    None: all rows are one scan); rows of no scan give zeros.  Returns y, or with ``stats`` (y, fp32 [scans,
+    groups, 2]): mean and 1 / sqrt(var + eps), which ``group_norm_backward`` takes."""
+    if stream is not None:
+        return _on_stream(stream, (x, weight, bias, offsets),
+                          lambda: group_norm(x, weight, bias, groups, offsets=offsets, activation=activation, eps=eps,
+                                             stats=stats))
+    shape, dev, dt, w, b = _group_args(x, weight, bias, groups)
+    ldx = _rows(x, "x", shape, x.dtype, dev)
+    off, scans = _offsets(offsets, dev)
+    y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    st = torch.empty((scans, groups, 2), dtype=torch.float32, device=x.device) if stats else None
+    rc = _lib().spconv_group_norm(x.data_ptr(), ldx, w, b, off, scans, shape[0], shape[1], groups, dt, _activation(activation),
+                                  eps, y.data_ptr(), None if st is None else st.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise SpconvError(rc, "spconv_group_norm")
+    return y if st is None else (y, st)
+
+
+def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], groups: int,
+                        stats: torch.Tensor, *, offsets: Optional[torch.Tensor] = None, activation: str = "none",
+                        stream: Optional[torch.cuda.Stream] = None):
+    """``spconv_group_norm_backward``: (dx, dweight, dbias) for the gradient ``dy`` of ``group_norm``'s y, from the
+    ``stats`` that it returned; dbias None without a bias."""
+    if stream is not None:
+        return _on_stream(stream, (dy, x, weight, bias, stats, offsets),
+                          lambda: group_norm_backward(dy, x, weight, bias, groups, stats, offsets=offsets,
+                                                      activation=activation))
+    shape, dev, dt, w, b = _group_args(x, weight, bias, groups)
+    ldx, ldy = _rows(x, "x", shape, x.dtype, dev), _rows(dy, "dy", shape, x.dtype, dev)
+    off, scans = _offsets(offsets, dev)
+    st = _weight(stats, "stats", (scans, groups, 2), torch.float32, dev)
+    device = x.device
+    dx = torch.empty(shape, dtype=x.dtype, device=device)
+    dw = torch.empty((shape[1],), dtype=torch.float32, device=device)
+    db = None if bias is None else torch.empty((shape[1],), dtype=torch.float32, device=device)
+    rc = _lib().spconv_group_norm_backward(dy.data_ptr(), ldy, x.data_ptr(), ldx, w, b, st, off, scans, shape[0], shape[1],
+                                           groups, dt, _activation(activation), dx.data_ptr(), dw.data_ptr(),
+                                           None if db is None else db.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise SpconvError(rc, "spconv_group_norm_backward")
+    return dx, dw, db
 
 
 def _operands(x: torch.Tensor, w: torch.Tensor, name: str):

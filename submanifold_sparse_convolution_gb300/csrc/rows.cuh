@@ -247,6 +247,44 @@ struct NormGradArgs {
 };
 int norm_backward(const NormGradArgs& a, cudaStream_t s);
 
+// ---- group norm (norm_groups.cu) -------------------------------------------
+constexpr int32_t kMaxGroupNormChannels = 8192;
+
+struct GroupNormArgs {
+    const void* x;          // [n] rows of c, ldx elements apart
+    int64_t ldx;
+    const float* weight;    // [c]
+    const float* bias;      // [c] or null
+    const int32_t* offsets; // [scans + 1] or null: one scan of all rows
+    int64_t scans, n;
+    int32_t c, groups;
+    int32_t dtype;          // of x, out
+    int32_t act;
+    float eps;
+    void* out;              // [n][c]
+    float2* stats;          // [scans][groups] mean, 1 / sqrt(var + eps); or null
+};
+int group_norm_forward(const GroupNormArgs& a, cudaStream_t s);
+
+struct GroupNormGradArgs {
+    const void* dy;
+    int64_t ldy;
+    const void* x;
+    int64_t ldx;
+    const float* weight;
+    const float* bias;      // or null
+    const float2* stats;
+    const int32_t* offsets;
+    int64_t scans, n;
+    int32_t c, groups;
+    int32_t dtype;
+    int32_t act;
+    void* dx;               // [n][c]
+    float* dweight;         // [c]
+    float* dbias;           // [c] or null
+};
+int group_norm_backward(const GroupNormGradArgs& a, cudaStream_t s);
+
 // ---- products with an epilogue (dense.cu, dense_tc.cu) ----------------------------------
 // Element (i, k) of an operand is p[i ld + k] (k_major) or p[k ld + i].
 struct Operand {

@@ -1,47 +1,10 @@
 // C ABI of the row-wise operators (declared in include/spconv.h): argument
 // checks, and the products that each operator is made of.
-#include "rows.cuh"
+#include "rows_args.cuh"
 
 using namespace spconv;
 
 namespace {
-
-constexpr int32_t kMaxChannels = 65536;
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// A row matrix as the caller gave it: n rows of c elements, ld elements apart.
-struct Rows {
-    const void* p;
-    int64_t n, c, ld;
-    size_t es;
-    bool ok() const { return p && aligned(p, es) && ld >= c && ld < (int64_t(1) << 38); }
-    size_t bytes() const { return n == 0 ? 0 : (static_cast<size_t>(n - 1) * ld + c) * es; }
-    bool overlaps(const Rows& o) const {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
-        if (!p || !o.p || a >= b + o.bytes() || b >= a + bytes()) return false;
-        // column ranges of one wider matrix: the rows interleave without touching
-        const uintptr_t pitch = static_cast<uintptr_t>(ld) * es;
-        if (n > 1 && o.n > 1 && pitch == static_cast<uintptr_t>(o.ld) * o.es) {
-            const uintptr_t d = b >= a ? (b - a) % pitch : (pitch - (a - b) % pitch) % pitch;   // o's row after this one's
-            return d < static_cast<uintptr_t>(c) * es || d + static_cast<uintptr_t>(o.c) * o.es > pitch;
-        }
-        return true;
-    }
-    // the same rows at the same places: an in-place update
-    bool same(const Rows& o) const { return p == o.p && (ld == o.ld || n <= 1); }
-};
-
-// fp32 values in a row (absent: null, which overlaps nothing)
-Rows vec(const float* p, int64_t c) { return {p, 1, c, c, 4}; }
-
-size_t size_of(int32_t dtype) { return dtype == SPCONV_FP32 ? 4 : dtype == SPCONV_E4M3 ? 1 : 2; }
-
-bool bad_sizes(int64_t n, int32_t c_in, int32_t c_out) {
-    return n < 0 || n >= (int64_t(1) << 30) || c_in < 1 || c_out < 1 || c_in > kMaxChannels || c_out > kMaxChannels;
-}
-bool bad_act(int32_t a) { return a < SPCONV_ACT_NONE || a > SPCONV_ACT_GELU_TANH; }
-bool bad_vec(const float* v) { return !aligned(v, 4); }
 
 // e4m3 operands need their scales, bf16 ones have none.
 int check_scales(int32_t dtype, const float* a, const float* b) {
@@ -98,7 +61,15 @@ DenseOp outer(const Rows& x, const Rows& dz) {
     return op;
 }
 
-int zero(void* p, size_t bytes, cudaStream_t s) { return p ? cuda_status(cudaMemsetAsync(p, 0, bytes, s)) : SPCONV_OK; }
+// Scans without offsets are one; the sums of a group norm's pieces take shared
+// memory in proportion to c.
+int check_groups(int64_t n, int32_t c, int32_t groups, int64_t scans, const int32_t* offsets, int32_t dtype, int32_t act) {
+    if (bad_sizes(n, c, 1) || bad_act(act) || groups < 1 || c % groups != 0 || scans < 1 || scans > (int64_t(1) << 20) ||
+        (!offsets && scans != 1) || !aligned(offsets, 4))
+        return SPCONV_ERR_INVALID_ARG;
+    if (dtype != SPCONV_BF16 && dtype != SPCONV_FP32) return SPCONV_ERR_INVALID_ARG;
+    return c > kMaxGroupNormChannels ? SPCONV_ERR_UNSUPPORTED : SPCONV_OK;
+}
 
 }  // namespace
 
@@ -353,6 +324,56 @@ int spconv_gated_ffn_backward(const void* dh_dev, int64_t ld_dh, const void* x_d
         o.ld_out = c_in;
     }
     return dense_run_plain(ops, count, {}, s);
+}
+
+int spconv_group_norm(const void* x_dev, int64_t ld_x, const float* weight_dev, const float* bias_dev,
+                      const int32_t* offsets_dev, int64_t scans, int64_t n, int32_t c, int32_t groups, int32_t dtype,
+                      int32_t activation, float eps, void* out_dev, float* stats_dev, void* stream) {
+    reset_launch_count();
+    const GroupNormArgs a{x_dev, ld_x, weight_dev, bias_dev, offsets_dev, scans, n, c, groups, dtype, activation, eps, out_dev,
+                          reinterpret_cast<float2*>(stats_dev)};
+    SPCONV_CHECK(check_groups(n, c, groups, scans, offsets_dev, dtype, activation));
+    if (!(eps >= 0.0f) || !weight_dev || bad_vec(weight_dev) || bad_vec(bias_dev) || !aligned(stats_dev, 8)) return SPCONV_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n == 0) return stats_dev ? group_norm_forward(a, s) : SPCONV_OK;
+    const size_t es = size_of(dtype);
+    const Rows x{x_dev, n, c, ld_x, es}, out{out_dev, n, c, c, es}, w = vec(weight_dev, c), b = vec(bias_dev, c),
+        off{offsets_dev, 1, scans + 1, scans + 1, 4}, st = vec(stats_dev, scans * groups * 2);
+    if (!x.ok() || !out.ok()) return SPCONV_ERR_INVALID_ARG;
+    for (const Rows& in : {x, w, b, off})
+        if (out.overlaps(in) || st.overlaps(in)) return SPCONV_ERR_ALIAS;
+    if (st.overlaps(out)) return SPCONV_ERR_ALIAS;
+    return group_norm_forward(a, s);
+}
+
+int spconv_group_norm_backward(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, const float* weight_dev,
+                               const float* bias_dev, const float* stats_dev, const int32_t* offsets_dev, int64_t scans,
+                               int64_t n, int32_t c, int32_t groups, int32_t dtype, int32_t activation, void* dx_dev,
+                               float* dweight_dev, float* dbias_dev, void* stream) {
+    reset_launch_count();
+    SPCONV_CHECK(check_groups(n, c, groups, scans, offsets_dev, dtype, activation));
+    if (!weight_dev || bad_vec(weight_dev) || bad_vec(bias_dev) || !stats_dev || !aligned(stats_dev, 8) || !dweight_dev ||
+        bad_vec(dweight_dev) || bad_vec(dbias_dev))
+        return SPCONV_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n == 0) {
+        SPCONV_CHECK(zero(dweight_dev, static_cast<size_t>(c) * 4, s));
+        return zero(dbias_dev, static_cast<size_t>(c) * 4, s);
+    }
+    const size_t es = size_of(dtype);
+    const Rows dy{dy_dev, n, c, ld_dy, es}, x{x_dev, n, c, ld_x, es}, off{offsets_dev, 1, scans + 1, scans + 1, 4};
+    const Rows ins[6] = {dy, x, off, vec(weight_dev, c), vec(bias_dev, c), vec(stats_dev, scans * groups * 2)};
+    const Rows outs[3] = {{dx_dev, n, c, c, es}, vec(dweight_dev, c), vec(dbias_dev, c)};
+    if (!dy.ok() || !x.ok() || !outs[0].ok()) return SPCONV_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i) {
+        for (const Rows& r : ins)
+            if (outs[i].overlaps(r)) return SPCONV_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (outs[i].overlaps(outs[j])) return SPCONV_ERR_ALIAS;
+    }
+    return group_norm_backward({dy_dev, ld_dy, x_dev, ld_x, weight_dev, bias_dev, reinterpret_cast<const float2*>(stats_dev),
+                                offsets_dev, scans, n, c, groups, dtype, activation, dx_dev, dweight_dev, dbias_dev},
+                               s);
 }
 
 int spconv_rows_status(void* stream) {
