@@ -76,6 +76,7 @@ struct Shape {
     int32_t c, groups, width;      // width: channels of a group
     int32_t vectors, tx, ty;       // vectors of a row; threads across and down
     int32_t rows;                  // of a block (R)
+    int32_t joined;                // channels of a group that a thread of k_group_stats joins: a power of two
     int64_t slots;                 // blocks + scans
 };
 
@@ -115,15 +116,17 @@ struct NormPass {
 };
 
 // Statistics of the block's pieces.  A thread's sums are about its first value
-// of the channel, so a mean far from zero costs no digits; they are joined about
-// the group's mean, in two passes over shared memory.
+// of the channel, so a mean far from zero costs no digits; it joins its channels
+// of a group, and a warp the threads' about the group's mean, in two passes over
+// shared memory.
 template <typename T, int W>
 __global__ void __launch_bounds__(kStatThreads, 1) k_group_stats(const __grid_constant__ NormPass p) {
     using P = Pack<T, W>;
     extern __shared__ float sh[];
     const Shape& h = p.h;
-    float* sh_mean = sh;                                            // [ty][c]
-    float* sh_m2 = sh + static_cast<size_t>(h.ty) * h.c;
+    const int32_t entries = h.c / h.joined;
+    float* sh_mean = sh;                                            // [ty][entries]
+    float* sh_m2 = sh + static_cast<size_t>(h.ty) * entries;
     const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx, lane = threadIdx.x & 31;
     const int32_t row0 = static_cast<int32_t>(blockIdx.x) * h.rows;
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
@@ -131,6 +134,7 @@ __global__ void __launch_bounds__(kStatThreads, 1) k_group_stats(const __grid_co
     pdl_trigger();
     p.scans.pieces(row0, row1, [&](int32_t s, int32_t lo, int32_t hi) {
         if (s < 0 || s >= p.scans.scans) return;
+        const int32_t each = (hi - lo) / h.ty, extra = (hi - lo) % h.ty;   // rows of a thread; threads with one more
         for (int32_t v = tx; v < h.vectors && ty < h.ty; v += h.tx) {
             const T* x = static_cast<const T*>(p.a.x) + v * W;
             float first[W], sum[W], sq[W];
@@ -159,35 +163,57 @@ __global__ void __launch_bounds__(kStatThreads, 1) k_group_stats(const __grid_co
                     for (int u = 0; u < U; ++u) add(q[u]);
                 }
                 for (; r < hi; r += h.ty) add(*reinterpret_cast<const P*>(x + r * p.a.ldx));
-                const float n = static_cast<float>((hi - lo - ty + h.ty - 1) / h.ty), by_n = 1.0f / n;
+                const float n = static_cast<float>(each + (ty < extra)), by_n = 1.0f / n;
+                float mean[W], m2[W];
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     const float m = sum[j] * by_n;   // of x - first
-                    sh_mean[ty * h.c + v * W + j] = first[j] + m;
-                    const float m2 = fmaf(-m, sum[j], sq[j]);
-                    sh_m2[ty * h.c + v * W + j] = m2 < 0.0f ? 0.0f : m2;   // (keeps NaN)
+                    mean[j] = first[j] + m;
+                    const float q = fmaf(-m, sum[j], sq[j]);
+                    m2[j] = q < 0.0f ? 0.0f : q;     // (keeps NaN)
                 }
+                // neighbouring channels of a group, as many as lie in one vector
+#pragma unroll
+                for (int w = 1; w < W; w *= 2)
+                    if (h.joined > w) {
+#pragma unroll
+                        for (int j = 0; j < W; j += 2 * w) {
+                            const float d = mean[j + w] - mean[j];
+                            mean[j] = fmaf(0.5f, d, mean[j]);
+                            m2[j] += fmaf(0.5f * n * static_cast<float>(w) * d, d, m2[j + w]);
+                        }
+                    }
+                const int32_t at = ty * entries + v * W / h.joined;
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    if (j % h.joined == 0) {
+                        sh_mean[at + j / h.joined] = mean[j];
+                        sh_m2[at + j / h.joined] = m2[j];
+                    }
             }
         }
         __syncthreads();
         const int32_t deep = hi - lo < h.ty ? hi - lo : h.ty;   // thread rows that have any
         const float by_count = 1.0f / (static_cast<float>(hi - lo) * static_cast<float>(h.width));
+        // lanes across a group's entries, and down the thread rows where those are few
+        const int32_t wide = h.width / h.joined, down = wide < 32 ? 32 / wide : 1;
+        const int32_t k0 = wide < 32 ? lane % wide : lane, t0 = wide < 32 ? lane / wide : 0;
         for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
-            const float base = sh_mean[g * h.width];
+            const float base = sh_mean[g * wide];
             float sum = 0.0f, m2 = 0.0f;
-            for (int32_t t = 0; t < deep; ++t) {
-                const float n = static_cast<float>((hi - lo - t + h.ty - 1) / h.ty);
-                for (int32_t k = lane; k < h.width; k += 32) sum = fmaf(n, sh_mean[t * h.c + g * h.width + k] - base, sum);
-            }
-            const float mean = base + warp_sum(sum) * by_count;
-            for (int32_t t = 0; t < deep; ++t) {
-                const float n = static_cast<float>((hi - lo - t + h.ty - 1) / h.ty);
-                for (int32_t k = lane; k < h.width; k += 32) {
-                    const int32_t i = t * h.c + g * h.width + k;
-                    const float d = sh_mean[i] - mean;
-                    m2 += fmaf(n * d, d, sh_m2[i]);
+            auto entries_of = [&](auto&& f) {
+                if (t0 >= down) return;
+                for (int32_t t = t0; t < deep; t += down) {
+                    const float n = static_cast<float>((each + (t < extra)) * h.joined);
+                    for (int32_t k = k0; k < wide; k += 32) f(t * entries + g * wide + k, n);
                 }
-            }
+            };
+            entries_of([&](int32_t i, float n) { sum = fmaf(n, sh_mean[i] - base, sum); });
+            const float mean = base + warp_sum(sum) * by_count;
+            entries_of([&](int32_t i, float n) {
+                const float d = sh_mean[i] - mean;
+                m2 += fmaf(n * d, d, sh_m2[i]);
+            });
             m2 = warp_sum(m2);
             if (lane == 0) p.part[slot_of(h, g, s)] = make_float2(mean, m2);
         }
@@ -383,10 +409,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_group_grad_sums(const __grid
             }
         });
         __syncthreads();
+        // down the thread rows: by several threads where a row has fewer channels than the block threads
         const int32_t deep = hi - lo < h.ty ? hi - lo : h.ty;
-        for (int32_t c = threadIdx.x; c < h.c; c += blockDim.x) {
+        const int32_t threads = static_cast<int32_t>(blockDim.x);
+        int32_t rows = h.c < threads ? threads / h.c : 1;
+        if (rows > deep) rows = deep;
+        for (int32_t i = threadIdx.x; i < rows * h.c; i += threads) {
+            const int32_t c = i % h.c;
             float u = 0.0f, z = 0.0f;
-            for (int32_t t = 0; t < deep; ++t) {
+            for (int32_t t = i / h.c; t < deep; t += rows) {
+                u += sh_u[t * h.c + c];
+                z += sh_z[t * h.c + c];
+            }
+            sh_u[i] = u;   // (row i / c, which no other thread reads)
+            sh_z[i] = z;
+        }
+        __syncthreads();
+        for (int32_t c = threadIdx.x; c < h.c; c += threads) {
+            float u = 0.0f, z = 0.0f;
+            for (int32_t t = 0; t < rows; ++t) {
                 u += sh_u[t * h.c + c];
                 z += sh_z[t * h.c + c];
             }
@@ -543,6 +584,8 @@ Shape make_shape(int64_t n, int32_t c, int32_t groups, int64_t scans, int w, int
     h.groups = groups;
     h.width = c / groups;
     h.vectors = c / w;
+    h.joined = 1;
+    while (h.joined < w && h.width % (2 * h.joined) == 0) h.joined *= 2;
     *threads = set_threads(&h, most);
     int64_t b = ceil_div(n, static_cast<int64_t>(4) * h.ty);
     if (b > kSms) b = kSms;
@@ -576,7 +619,7 @@ int forward_w(const GroupNormArgs& a, cudaStream_t s) {
     Scratch part(static_cast<size_t>(p.h.slots) * a.groups * sizeof(float2), s);
     if (part.failed()) return SPCONV_ERR_OOM;
     p.part = part.as<float2>();
-    SPCONV_CHECK((launch_wide<k_group_stats<T, W>>(blocks, threads, static_cast<size_t>(2) * p.h.ty * a.c * 4, s, p)));
+    SPCONV_CHECK((launch_wide<k_group_stats<T, W>>(blocks, threads, static_cast<size_t>(2) * p.h.ty * (a.c / p.h.joined) * 4, s, p)));
     threads = set_threads(&p.h, kApplyThreads);
     return launch_wide<k_group_apply<T, W>>(blocks, threads, static_cast<size_t>(2) * a.groups * 4, s, p);
 }
