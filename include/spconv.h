@@ -551,6 +551,88 @@ int spconv_group_norm_backward(const void* dy_dev, int64_t ld_dy, const void* x_
                                float* dweight_dev, float* dbias_dev, void* stream);
 
 /*
+ * Rows sorted by expert.  Row t chooses k experts: pair (t, j) has the number
+ * t k + j.  The pairs are sorted by expert, those of one expert in their own
+ * order; a pair's place among them is its slot.
+ *
+ *   experts_dev  int32 (index_bytes 4) or int64 (8) [tokens][k], each in
+ *                [0, n_experts), or negative: no expert, and no slot.  One that
+ *                is too large counts as none and is an error that
+ *                spconv_rows_status returns (SPCONV_ERR_COORD_RANGE).  A row may
+ *                name an expert twice.
+ *   offsets_dev  int32 [n_experts + 1]: expert e's rows are the slots
+ *                offsets[e] .. offsets[e + 1] - 1.
+ *   pairs_dev    int32 [tokens k]: the pair of each slot, -1 behind the last.
+ *   slots_dev    int32 [tokens][k]: the slot of each pair, -1 for no expert.
+ * 1 <= k, n_experts <= 1024; tokens k < 2^30.  tokens = 0 writes the offsets.
+ */
+int spconv_expert_plan(const void* experts_dev, int32_t index_bytes, int64_t tokens, int32_t k, int32_t n_experts,
+                       int32_t* offsets_dev, int32_t* pairs_dev, int32_t* slots_dev, void* stream);
+
+/*
+ * Each row to the slots of its pairs: out[slots[t][j]] = x[t], for slots and
+ * offsets from spconv_expert_plan.  Rows of out at and behind
+ * offsets[n_experts] are zeros.
+ *
+ *   x_dev      [tokens] rows of c, dtype (SPCONV_BF16 or SPCONV_FP32).
+ *   out_dev    [tokens k][c] in dtype; or, with out_dtype SPCONV_E4M3, e4m3
+ *              values q with scale_dev fp32 [ceil(c / 128)][tokens k], one for
+ *              each 128 values of a row, as spconv_quantize_blocks makes them.
+ *              scale_dev NULL exactly when out is in dtype.
+ * The gradient of x is spconv_expert_combine of out's without weights.
+ */
+int spconv_expert_gather(const void* x_dev, int64_t ld_x, const int32_t* slots_dev, const int32_t* offsets_dev, int64_t tokens,
+                         int32_t k, int32_t n_experts, int32_t c, int32_t dtype, void* out_dev, int32_t out_dtype,
+                         float* scale_dev, void* stream);
+
+/*
+ * And back: out[t] = residual[t] + sum_j weights[t][j] y[slots[t][j]], in the
+ * order of j, over the pairs that have a slot (whatever the weights of the
+ * others are).
+ *
+ *   y_dev         [tokens k] rows of c, dtype.
+ *   weights_dev   fp32 [tokens][k], or NULL (1).
+ *   residual_dev  [tokens] rows of c, dtype, or NULL; may be out_dev when dense.
+ *   out_dev       [tokens][c] dtype.
+ */
+int spconv_expert_combine(const void* y_dev, int64_t ld_y, const int32_t* slots_dev, const float* weights_dev,
+                          const void* residual_dev, int64_t ld_residual, int64_t tokens, int32_t k, int32_t c, int32_t dtype,
+                          void* out_dev, void* stream);
+
+/*
+ * Its gradients: dy[slots[t][j]] = weights[t][j] dout[t], zeros at and behind
+ * offsets[n_experts], and dweights[t][j] = dout[t] . y[slots[t][j]], 0 for a
+ * pair without a slot.  The residual's gradient is dout itself.
+ *
+ *   dy_dev        [tokens k][c] dtype;  dweights_dev fp32 [tokens][k].
+ */
+int spconv_expert_combine_backward(const void* dout_dev, int64_t ld_dout, const void* y_dev, int64_t ld_y,
+                                   const int32_t* slots_dev, const int32_t* offsets_dev, const float* weights_dev, int64_t tokens,
+                                   int32_t k, int32_t n_experts, int32_t c, int32_t dtype, void* dy_dev, float* dweights_dev,
+                                   void* stream);
+
+/*
+ * Rows in e4m3 with a scale for each 128 values (the last of a row: what is
+ * left): scale[b][i] = max |x| / 448 over block b of row i, q = e4m3(x / scale),
+ * both divisions rounded to nearest; 0, with q 0, for a block of zeros.  A block
+ * with an infinity or a NaN stands for NaN.
+ *
+ *   x_dev      [n] rows of c, dtype (SPCONV_BF16 or SPCONV_FP32).
+ *   q_dev      e4m3 [n][c];  scale_dev fp32 [ceil(c / 128)][n].
+ */
+int spconv_quantize_blocks(const void* x_dev, int64_t ld_x, int64_t n, int32_t c, int32_t dtype, void* q_dev, float* scale_dev,
+                           void* stream);
+
+/*
+ * Weights for the block-scaled products, made once: w bf16
+ * [count][c_in][c_out] to q e4m3 [count][c_out][c_in] with a scale for each 128
+ * x 128 values, scale_dev fp32 [count][ceil(c_out / 128)][ceil(c_in / 128)].
+ * count <= 1024.
+ */
+int spconv_quantize_weight_blocks(const void* w_dev, int32_t count, int32_t c_in, int32_t c_out, void* q_dev, float* scale_dev,
+                                  void* stream);
+
+/*
  * Synchronise the stream and return the first error that the row-wise
  * operators' kernels recorded on the current device since the last call of
  * this function (SPCONV_ERR_TIMEOUT: a bounded wait ran out and the results

@@ -54,7 +54,9 @@ from . import _native
 __all__ = ["SpconvError", "Map", "WPack", "build_map", "subm_forward", "wpack_create",
            "subm_forward_packed", "map_status", "map_info", "map_export", "map_destroy",
            "rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
-           "quantize_weight", "group_norm", "group_norm_backward", "rows_status", "trim_pool", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS",
+           "quantize_weight", "group_norm", "group_norm_backward", "ExpertPlan", "expert_plan", "expert_gather",
+           "expert_gather_backward", "expert_combine", "expert_combine_backward", "quantize_blocks",
+           "quantize_weight_blocks", "rows_status", "trim_pool", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS",
            "BIT_ORDERS", "PIPELINES", "GEMMS", "library"]
 
 MAPPERS = {"auto": 0, "dense": 1, "sorted": 2, "hash": 3}
@@ -829,6 +831,183 @@ def quantize_weight(weight: torch.Tensor, *, stream: Optional[torch.cuda.Stream]
     rc = _lib().spconv_quantize_weight(w, c_in, c_out, q.data_ptr(), scale.data_ptr(), _raw_stream(dev))
     if rc:
         raise SpconvError(rc, "spconv_quantize_weight")
+    return q, scale
+
+
+class ExpertPlan:
+    """Where the rows of each expert lie (``expert_plan``).
+
+    ``offsets`` int32 [experts + 1]: expert e's rows are the slots offsets[e] to offsets[e + 1] - 1.  ``pairs`` int32
+    [tokens * k]: the pair token * k + j of each slot, -1 behind the last.  ``slots`` int32 [tokens, k]: the slot of
+    each pair, -1 for no expert."""
+
+    __slots__ = ("offsets", "pairs", "slots")
+
+    def __init__(self, offsets: torch.Tensor, pairs: torch.Tensor, slots: torch.Tensor):
+        self.offsets, self.pairs, self.slots = offsets, pairs, slots
+
+    def _args(self, dev: int):
+        """(slots, offsets, tokens, k, experts), checked to be on GPU ``dev``."""
+        s, o = self.slots, self.offsets
+        if s.dtype is not torch.int32 or s.dim() != 2 or s.get_device() != dev or not s.is_contiguous():
+            raise ValueError(f"the plan's slots must be a contiguous int32 [tokens, k] tensor on cuda:{dev}")
+        if o.dtype is not torch.int32 or o.dim() != 1 or o.get_device() != dev or not o.is_contiguous() or o.shape[0] < 2:
+            raise ValueError(f"the plan's offsets must be a contiguous int32 [experts + 1] tensor on cuda:{dev}")
+        t, k = s.shape
+        return s.data_ptr(), o.data_ptr(), t, k, o.shape[0] - 1
+
+
+def expert_plan(experts: torch.Tensor, n_experts: int, *, stream: Optional[torch.cuda.Stream] = None) -> ExpertPlan:
+    """``spconv_expert_plan``: the places of all rows sorted by expert, those of one expert in their tokens' order.
+
+    ``experts`` int32 or int64 [tokens, k] on the GPU: the experts that each token's row goes to, -1 for none."""
+    if stream is not None:
+        return _on_stream(stream, (experts,), lambda: expert_plan(experts, n_experts))
+    (t, k), dev = _matrix(experts, "experts")
+    size = {torch.int32: 4, torch.int64: 8}.get(experts.dtype)
+    if size is None or not experts.is_contiguous():
+        raise ValueError("experts must be a contiguous int32 or int64 [tokens, k] tensor")
+    if n_experts < 1:
+        raise ValueError("at least one expert")
+    device = experts.device
+    offsets = torch.empty((n_experts + 1,), dtype=torch.int32, device=device)
+    pairs = torch.empty((t * k,), dtype=torch.int32, device=device)
+    slots = torch.empty((t, k), dtype=torch.int32, device=device)
+    rc = _lib().spconv_expert_plan(experts.data_ptr(), size, t, k, n_experts, offsets.data_ptr(), pairs.data_ptr(),
+                                   slots.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise SpconvError(rc, "spconv_expert_plan")
+    return ExpertPlan(offsets, pairs, slots)
+
+
+def _plan_tensors(plan: ExpertPlan):
+    return plan.offsets, plan.slots
+
+
+def expert_gather(x: torch.Tensor, plan: ExpertPlan, *, quantize: bool = False, stream: Optional[torch.cuda.Stream] = None):
+    """``spconv_expert_gather``: each token's row to the slots of its pairs, [tokens * k, C]; rows of no pair, at the
+    end, are zeros.  ``x`` bf16 or fp32 [tokens, C] (rows may be strided).  With ``quantize`` (q, scale): e4m3 and
+    fp32 [ceil(C / 128), tokens * k], as ``quantize_blocks``."""
+    if stream is not None:
+        return _on_stream(stream, (x, *_plan_tensors(plan)), lambda: expert_gather(x, plan, quantize=quantize))
+    shape, dev = _matrix(x, "x")
+    slots, off, t, k, e = plan._args(dev)
+    c = shape[1]
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
+        raise ValueError("x must be bf16 or fp32")
+    ldx = _rows(x, "x", (t, c), x.dtype, dev)
+    device = x.device
+    out = torch.empty((t * k, c), dtype=_E4M3 if quantize else x.dtype, device=device)
+    scale = torch.empty((-(-c // 128), t * k), dtype=torch.float32, device=device) if quantize else None
+    rc = _lib().spconv_expert_gather(x.data_ptr(), ldx, slots, off, t, k, e, c, dt, out.data_ptr(), 2 if quantize else dt,
+                                     None if scale is None else scale.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise SpconvError(rc, "spconv_expert_gather")
+    return (out, scale) if quantize else out
+
+
+def _combine(y: torch.Tensor, plan: ExpertPlan, weights: Optional[torch.Tensor], residual: Optional[torch.Tensor], name: str):
+    shape, dev = _matrix(y, name)
+    slots, _, t, k, _ = plan._args(dev)
+    c, dtype = shape[1], y.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be bf16 or fp32")
+    ldy = _rows(y, name, (t * k, c), dtype, dev)
+    w = None if weights is None else _weight(weights, "weights", (t, k), torch.float32, dev)
+    r, ldr = None, 0
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _rows(residual, "residual", (t, c), dtype, dev)
+    out = torch.empty((t, c), dtype=dtype, device=y.device)
+    rc = _lib().spconv_expert_combine(y.data_ptr(), ldy, slots, w, r, ldr, t, k, c, dt, out.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise SpconvError(rc, "spconv_expert_combine")
+    return out
+
+
+def expert_gather_backward(dy: torch.Tensor, plan: ExpertPlan, *, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``spconv_expert_combine``: dx [tokens, C] for the gradient ``dy`` [tokens * k, C] of ``expert_gather``'s rows."""
+    if stream is not None:
+        return _on_stream(stream, (dy, *_plan_tensors(plan)), lambda: expert_gather_backward(dy, plan))
+    return _combine(dy, plan, None, None, "dy")
+
+
+def expert_combine(y: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor, *, residual: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``spconv_expert_combine``: residual + the sum of each token's rows of ``y`` [tokens * k, C] (bf16 or fp32) times
+    its ``weights`` (fp32 [tokens, k]); pairs of no expert add nothing."""
+    if stream is not None:
+        return _on_stream(stream, (y, weights, residual, *_plan_tensors(plan)),
+                          lambda: expert_combine(y, plan, weights, residual=residual))
+    if weights is None:
+        raise ValueError("weights are required")
+    return _combine(y, plan, weights, residual, "y")
+
+
+def expert_combine_backward(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor, *,
+                            stream: Optional[torch.cuda.Stream] = None):
+    """``spconv_expert_combine_backward``: (dy, dweights) for the gradient ``dout`` of ``expert_combine``; the
+    residual's gradient is ``dout`` itself.  dy is zeros in rows of no pair, dweights 0 for pairs of no expert."""
+    if stream is not None:
+        return _on_stream(stream, (dout, y, weights, *_plan_tensors(plan)),
+                          lambda: expert_combine_backward(dout, y, plan, weights))
+    shape, dev = _matrix(y, "y")
+    slots, off, t, k, e = plan._args(dev)
+    c, dtype = shape[1], y.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError("y must be bf16 or fp32")
+    ldy, ldd = _rows(y, "y", (t * k, c), dtype, dev), _rows(dout, "dout", (t, c), dtype, dev)
+    w = _weight(weights, "weights", (t, k), torch.float32, dev)
+    device = y.device
+    dy = torch.empty((t * k, c), dtype=dtype, device=device)
+    dw = torch.empty((t, k), dtype=torch.float32, device=device)
+    rc = _lib().spconv_expert_combine_backward(dout.data_ptr(), ldd, y.data_ptr(), ldy, slots, off, w, t, k, e, c, dt,
+                                               dy.data_ptr(), dw.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise SpconvError(rc, "spconv_expert_combine_backward")
+    return dy, dw
+
+
+def quantize_blocks(x: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None):
+    """``spconv_quantize_blocks``: bf16 or fp32 [N, C] (rows may be strided) to (e4m3 [N, C], fp32 scale
+    [ceil(C / 128), N]), a scale for each 128 values of a row."""
+    if stream is not None:
+        return _on_stream(stream, (x,), lambda: quantize_blocks(x))
+    shape, dev = _matrix(x, "x")
+    n, c = shape
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
+        raise ValueError("x must be bf16 or fp32")
+    ldx = _rows(x, "x", shape, x.dtype, dev)
+    device = x.device
+    q = torch.empty((n, c), dtype=_E4M3, device=device)
+    scale = torch.empty((-(-c // 128), n), dtype=torch.float32, device=device)
+    rc = _lib().spconv_quantize_blocks(x.data_ptr(), ldx, n, c, dt, q.data_ptr(), scale.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise SpconvError(rc, "spconv_quantize_blocks")
+    return q, scale
+
+
+def quantize_weight_blocks(weight: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None):
+    """``spconv_quantize_weight_blocks``: bf16 [C_in, C_out] or [experts, C_in, C_out] to (e4m3 [.., C_out, C_in], fp32
+    scale [.., ceil(C_out / 128), ceil(C_in / 128)]), a scale for each 128 x 128 values; once per weight."""
+    if stream is not None:
+        return _on_stream(stream, (weight,), lambda: quantize_weight_blocks(weight))
+    if weight.dim() not in (2, 3) or not weight.is_cuda:
+        raise ValueError("weight must be a 2-D or 3-D CUDA tensor")
+    dev = weight.get_device()
+    _require_current(dev, "weight")
+    w = _weight(weight, "weight", weight.shape, _BF16, dev)
+    *count, c_in, c_out = weight.shape
+    device = weight.device
+    q = torch.empty((*count, c_out, c_in), dtype=_E4M3, device=device)
+    scale = torch.empty((*count, -(-c_out // 128), -(-c_in // 128)), dtype=torch.float32, device=device)
+    rc = _lib().spconv_quantize_weight_blocks(w, count[0] if count else 1, c_in, c_out, q.data_ptr(), scale.data_ptr(),
+                                              _raw_stream(dev))
+    if rc:
+        raise SpconvError(rc, "spconv_quantize_weight_blocks")
     return q, scale
 
 

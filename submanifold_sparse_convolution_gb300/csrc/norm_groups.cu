@@ -643,18 +643,6 @@ int backward_w(const GroupNormGradArgs& a, cudaStream_t s) {
     return launch_wide<k_group_grad_apply<T, W>>(p.blocks + static_cast<int>(ceil_div(2 * a.c, 32)), kBwdThreads, smem, s, p);
 }
 
-// The widest vectors that every row of all matrices starts on.
-template <typename T, typename F>
-int with_width(uintptr_t all, int32_t c, F&& f) {
-    auto fits = [&](int w) { return c % w == 0 && all % (w * sizeof(T)) == 0; };
-    if constexpr (sizeof(T) == 2) {
-        if (fits(8)) return f(std::integral_constant<int, 8>());
-    }
-    if (fits(4)) return f(std::integral_constant<int, 4>());
-    if (fits(2)) return f(std::integral_constant<int, 2>());
-    return f(std::integral_constant<int, 1>());
-}
-
 }  // namespace
 
 int group_norm_forward(const GroupNormArgs& a, cudaStream_t s) {

@@ -72,4 +72,17 @@ __device__ __forceinline__ void store_e4m3(uint8_t* dst, const float* v) {
     }
 }
 
+// Calls f with the widest vectors (as a constant) that every row starts on: all
+// is the addresses' and row strides' bits in bytes, or-ed together.
+template <typename T, typename F>
+int with_width(uintptr_t all, int32_t c, F&& f) {
+    auto fits = [&](int w) { return c % w == 0 && all % (w * sizeof(T)) == 0; };
+    if constexpr (sizeof(T) == 2) {
+        if (fits(8)) return f(std::integral_constant<int, 8>());
+    }
+    if (fits(4)) return f(std::integral_constant<int, 4>());
+    if (fits(2)) return f(std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, 1>());
+}
+
 }  // namespace spconv

@@ -285,6 +285,66 @@ struct GroupNormGradArgs {
 };
 int group_norm_backward(const GroupNormGradArgs& a, cudaStream_t s);
 
+// ---- rows sorted by expert, blocks of 128 in e4m3 (experts.cu) ---------------
+constexpr int32_t kMaxExperts = 1024;
+
+// experts [pairs] (4- or 8-byte whole numbers) -> offsets [n_experts + 1], the
+// pair of each slot (-1 behind the last) and the slot of each pair (-1: none).
+int expert_plan(const void* experts, int32_t index_bytes, int64_t pairs, int32_t n_experts, int32_t* offsets, int32_t* sorted,
+                int32_t* slots, cudaStream_t s);
+
+// out[slots[t k + j]] = x[t], rows of no pair zeros; slots null (k = 1): every
+// row in its place.  With `scale` e4m3 with a scale per 128 values of a row.
+struct ExpertRows {
+    const void* x;          // [tokens] rows of c, ldx apart
+    int64_t ldx;
+    const int32_t* slots;   // [tokens][k]
+    const int32_t* offsets; // [n_experts + 1]
+    int32_t n_experts;
+    int64_t tokens;
+    int32_t k, c;
+    int32_t dtype;          // of x
+    void* out;              // [tokens k][c]
+    float* scale;           // [ceil(c / 128)][tokens k], or null: out in dtype
+    bool wide;              // (set by expert_gather: e4m3 rows take 8-byte stores)
+};
+int expert_gather(const ExpertRows& a, cudaStream_t s);
+
+// out[t] = residual[t] + sum_j weights[t k + j] y[slots[t k + j]]
+struct ExpertSums {
+    const void* y;          // [tokens k] rows of c, ldy apart
+    int64_t ldy;
+    const int32_t* slots;
+    const float* weights;   // or null: 1
+    const void* residual;   // or null
+    int64_t ldr;
+    int64_t tokens;
+    int32_t k, c;
+    int32_t dtype;
+    void* out;              // [tokens][c]
+};
+int expert_combine(const ExpertSums& a, cudaStream_t s);
+
+struct ExpertGrad {
+    const void* dout;       // [tokens] rows of c
+    int64_t ldd;
+    const void* y;
+    int64_t ldy;
+    const int32_t* slots;
+    const int32_t* offsets;
+    int32_t n_experts;
+    const float* weights;
+    int64_t tokens;
+    int32_t k, c;
+    int32_t dtype;
+    void* dy;               // [tokens k][c]
+    float* dweights;        // [tokens][k]
+};
+int expert_combine_backward(const ExpertGrad& a, cudaStream_t s);
+
+// w bf16 [count][c_in][c_out] -> q e4m3 [count][c_out][c_in], scale per 128 x 128
+int quantize_weight_blocks(const void* w, int64_t count, int32_t c_in, int32_t c_out, void* q, float* scale, cudaStream_t s);
+
 // ---- products with an epilogue (dense.cu, dense_tc.cu) ----------------------------------
 // Element (i, k) of an operand is p[i ld + k] (k_major) or p[k ld + i].
 struct Operand {
