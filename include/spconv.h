@@ -633,6 +633,47 @@ int spconv_quantize_weight_blocks(const void* w_dev, int32_t count, int32_t c_in
                                   void* stream);
 
 /*
+ * spconv_linear for e4m3 operands with a scale for each block of 128, and for
+ * sorted rows and the weights of their experts:
+ *
+ *   out = act(z + bias) + residual
+ *   z[i][o] = sum_b x_scale[b][i] w_scale[o / 128][b] sum_{c in block b} x[i][c] W[o][c]
+ *
+ *   x_dev          e4m3 [n] rows of c_in, x_scale_dev fp32 [ceil(c_in / 128)][n]
+ *                  (spconv_quantize_blocks, spconv_expert_gather).
+ *   w_dev          e4m3 [n_experts][c_out][c_in], 16-byte aligned, w_scale_dev
+ *                  fp32 [n_experts][ceil(c_out / 128)][ceil(c_in / 128)]
+ *                  (spconv_quantize_weight_blocks).
+ *   offsets_dev    int32 [n_experts + 1], ascending, in [0, n]: rows offsets[e]
+ *                  .. offsets[e + 1] - 1 are expert e's, any number of them.
+ *                  Rows of no expert are written as zeros.  Borders out of order
+ *                  or range are an error that spconv_rows_status returns
+ *                  (SPCONV_ERR_COORD_RANGE); out is undefined then.  NULL with
+ *                  n_experts 1: one weight for all rows.
+ *   bias_dev       fp32 [n_experts][c_out] or NULL.
+ *   residual_dev   bf16 [n] rows of c_out or NULL; may be out_dev with the same
+ *                  stride.
+ *   out_dev        bf16 [n] rows of c_out; or, with out_scale_dev fp32
+ *                  [ceil(c_out / 128)][n], e4m3 with a scale for each 128 values
+ *                  of a row, as spconv_quantize_blocks forms them (from the fp32
+ *                  values, and without a residual).
+ * The sums are fp32 throughout.  c_in is a multiple of 16
+ * (SPCONV_ERR_UNSUPPORTED otherwise); n_experts <= 1024.
+ */
+int spconv_linear_blocks(const void* x_dev, int64_t ld_x, const float* x_scale_dev, const void* w_dev, const float* w_scale_dev,
+                         const int32_t* offsets_dev, int32_t n_experts, int64_t n, int32_t c_in, int32_t c_out,
+                         const float* bias_dev, int32_t activation, const void* residual_dev, int64_t ld_residual, void* out_dev,
+                         int64_t ld_out, float* out_scale_dev, void* stream);
+
+/*
+ * spconv_gated_ffn of the same operands: out = act(z_gate) * z_up.
+ */
+int spconv_gated_ffn_blocks(const void* x_dev, int64_t ld_x, const float* x_scale_dev, const void* w_gate_dev,
+                            const float* gate_scale_dev, const void* w_up_dev, const float* up_scale_dev,
+                            const int32_t* offsets_dev, int32_t n_experts, int64_t n, int32_t c_in, int32_t c_hidden,
+                            int32_t activation, void* out_dev, int64_t ld_out, float* out_scale_dev, void* stream);
+
+/*
  * Synchronise the stream and return the first error that the row-wise
  * operators' kernels recorded on the current device since the last call of
  * this function (SPCONV_ERR_TIMEOUT: a bounded wait ran out and the results

@@ -56,7 +56,7 @@ __all__ = ["SpconvError", "Map", "WPack", "build_map", "subm_forward", "wpack_cr
            "rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
            "quantize_weight", "group_norm", "group_norm_backward", "ExpertPlan", "expert_plan", "expert_gather",
            "expert_gather_backward", "expert_combine", "expert_combine_backward", "quantize_blocks",
-           "quantize_weight_blocks", "rows_status", "trim_pool", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS",
+           "quantize_weight_blocks", "linear_blocks", "gated_ffn_blocks", "rows_status", "trim_pool", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS",
            "BIT_ORDERS", "PIPELINES", "GEMMS", "library"]
 
 MAPPERS = {"auto": 0, "dense": 1, "sorted": 2, "hash": 3}
@@ -1009,6 +1009,94 @@ def quantize_weight_blocks(weight: torch.Tensor, *, stream: Optional[torch.cuda.
     if rc:
         raise SpconvError(rc, "spconv_quantize_weight_blocks")
     return q, scale
+
+
+def _block_operands(x: torch.Tensor, x_scale: torch.Tensor, weights, offsets: Optional[torch.Tensor]):
+    """Checks e4m3 x [N, C_in] with block scales against ``weights``, (tensor, scale, name) each.
+
+    Returns (n, c_in, c_out, experts, row stride of x, address of x's scales, [address, of its scales] per weight,
+    address of the offsets, the GPU)."""
+    (n, c_in), dev = _matrix(x, "x")
+    if x.dtype is not _E4M3:
+        raise ValueError("x must be float8_e4m3fn")
+    ldx = _rows(x, "x", (n, c_in), _E4M3, dev)
+    kb = -(-c_in // 128)
+    xs = _weight(x_scale, "x_scale", (kb, n), torch.float32, dev)
+    shape = weights[0][0].shape
+    if len(shape) not in (2, 3) or shape[-1] != c_in:
+        raise ValueError(f"{weights[0][2]} must be [C_out, {c_in}] or [experts, C_out, {c_in}]")
+    c_out = shape[-2]
+    sshape = (*shape[:-2], -(-c_out // 128), kb)
+    at = []
+    for w, scale, name in weights:
+        at.append(_weight(w, name, shape, _E4M3, dev))
+        at.append(_weight(scale, name + " scale", sshape, torch.float32, dev))
+    off, experts = _offsets(offsets, dev)
+    if experts != (shape[0] if len(shape) == 3 else 1):
+        raise ValueError(f"{experts} runs of rows for weights of shape {list(shape)}")
+    return n, c_in, c_out, experts, ldx, xs, at, off, dev
+
+
+def _block_output(n: int, c: int, quantize: bool, out: Optional[torch.Tensor], device, dev: int):
+    """(out, row stride, scales or None)"""
+    if quantize:
+        if out is not None:
+            raise ValueError("out is for bf16 results")
+        return (torch.empty((n, c), dtype=_E4M3, device=device), c,
+                torch.empty((-(-c // 128), n), dtype=torch.float32, device=device))
+    if out is None:
+        return torch.empty((n, c), dtype=_BF16, device=device), c, None
+    return out, _rows(out, "out", (n, c), _BF16, dev), None
+
+
+def linear_blocks(x: torch.Tensor, weight: torch.Tensor, x_scale: torch.Tensor, w_scale: torch.Tensor, *,
+                  offsets: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, activation: str = "none",
+                  residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, quantize: bool = False,
+                  stream: Optional[torch.cuda.Stream] = None):
+    """``spconv_linear_blocks``: act(x W + bias) + residual of e4m3 operands with a scale for each block of 128.
+
+    ``x`` [N, C_in] with ``x_scale`` [ceil(C_in / 128), N] (``quantize_blocks``, ``expert_gather``), C_in a multiple of
+    16; ``weight`` [C_out, C_in] with ``w_scale`` (``quantize_weight_blocks``).  With ``offsets`` (int32 [experts +
+    1], ascending) rows offsets[e] to offsets[e + 1] - 1 take the weight of expert e, [experts, C_out, C_in], and row
+    e of ``bias`` [experts, C_out]; rows of no expert give zeros.  ``residual`` bf16 [N, C_out] (may be ``out``).
+    Returns bf16 [N, C_out], or with ``quantize`` (q, scale) as ``quantize_blocks`` makes them."""
+    if stream is not None:
+        return _on_stream(stream, (x, weight, x_scale, w_scale, offsets, bias, residual, out),
+                          lambda: linear_blocks(x, weight, x_scale, w_scale, offsets=offsets, bias=bias, activation=activation,
+                                                residual=residual, out=out, quantize=quantize))
+    n, c_in, c_out, e, ldx, xs, (w, ws), off, dev = _block_operands(x, x_scale, ((weight, w_scale, "weight"),), offsets)
+    b, r, ldr = None, None, 0
+    if bias is not None:
+        b = _weight(bias, "bias", (e, c_out) if weight.dim() == 3 else (c_out,), torch.float32, dev)
+    if residual is not None:
+        if quantize:
+            raise ValueError("a residual is for bf16 results")
+        r, ldr = residual.data_ptr(), _rows(residual, "residual", (n, c_out), _BF16, dev)
+    out, ldo, scale = _block_output(n, c_out, quantize, out, x.device, dev)
+    rc = _lib().spconv_linear_blocks(x.data_ptr(), ldx, xs, w, ws, off, e, n, c_in, c_out, b, _activation(activation), r, ldr,
+                                     out.data_ptr(), ldo, None if scale is None else scale.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise SpconvError(rc, "spconv_linear_blocks")
+    return out if scale is None else (out, scale)
+
+
+def gated_ffn_blocks(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, x_scale: torch.Tensor,
+                     gate_scale: torch.Tensor, up_scale: torch.Tensor, *, offsets: Optional[torch.Tensor] = None,
+                     activation: str = "silu", out: Optional[torch.Tensor] = None, quantize: bool = False,
+                     stream: Optional[torch.cuda.Stream] = None):
+    """``spconv_gated_ffn_blocks``: act(x W_gate) * (x W_up), operands, ``offsets`` and result as for ``linear_blocks``."""
+    if stream is not None:
+        return _on_stream(stream, (x, w_gate, w_up, x_scale, gate_scale, up_scale, offsets, out),
+                          lambda: gated_ffn_blocks(x, w_gate, w_up, x_scale, gate_scale, up_scale, offsets=offsets,
+                                                   activation=activation, out=out, quantize=quantize))
+    n, c_in, c_h, e, ldx, xs, (g, gs, u, us), off, dev = _block_operands(
+        x, x_scale, ((w_gate, gate_scale, "w_gate"), (w_up, up_scale, "w_up")), offsets)
+    out, ldo, scale = _block_output(n, c_h, quantize, out, x.device, dev)
+    rc = _lib().spconv_gated_ffn_blocks(x.data_ptr(), ldx, xs, g, gs, u, us, off, e, n, c_in, c_h, _activation(activation),
+                                        out.data_ptr(), ldo, None if scale is None else scale.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise SpconvError(rc, "spconv_gated_ffn_blocks")
+    return out if scale is None else (out, scale)
 
 
 def rows_status(stream: Optional[torch.cuda.Stream] = None) -> int:

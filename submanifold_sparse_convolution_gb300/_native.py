@@ -97,6 +97,10 @@ SIGNATURES = {
                                                       _P]),
     "spconv_quantize_blocks": (ctypes.c_int, [_P, _I64, _I64, _I32, _I32, _P, _P, _P]),
     "spconv_quantize_weight_blocks": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _P]),
+    "spconv_linear_blocks": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _P, _I32, _P, _I64, _P, _I64, _P,
+                                            _P]),
+    "spconv_gated_ffn_blocks": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _I32, _P, _I64, _P,
+                                               _P]),
     "spconv_rows_status": (ctypes.c_int, [_P]),
     "spconv_trim_pool": (ctypes.c_int, [_I64]),
     "spconv_last_launch_count": (ctypes.c_int32, []),

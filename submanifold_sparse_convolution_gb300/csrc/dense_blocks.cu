@@ -1,0 +1,892 @@
+// Products of e4m3 operands with a scale for each block of 128, and of sorted
+// rows with the weights of their experts.
+//
+//   z[i][o] = sum_b xs[b][i] ws[o / 128][b] sum_{k in block b} x[i][k] W[o][k]
+//
+// The tensor cores sum one block of 128 at a time into TMEM (fp32); the scales
+// differ from block to block, so the block's sums are read back, scaled and added
+// up in registers: one fp32 multiply-add a sum and block.
+//
+// A pair of CTAs works on a tile of 256 rows by 256 columns (gated: 128 of the
+// gate's weight and the same 128 of the up weight), CTA rank r bringing 128 rows of
+// x and 128 of W.  Two accumulators of 256 columns take turns: while the tensor
+// pipe fills one with a block of K (4 MMAs, 512 clocks at the e4m3 rate), eight
+// warps add the other to their registers (128 sums a thread; 256 clocks of TMEM
+// loads and as many of multiply-adds over an SM).
+//
+// Sorted rows: expert e's rows are offsets[e] .. offsets[e + 1] - 1, and its
+// weight rows e H .. (e + 1) H - 1 of the stacked weights.  The offsets stay on
+// the device: each CTA sums up the experts' row tiles and looks its tiles up.  A
+// tile reads past its expert's rows and columns (whatever is there, or zeros
+// behind the last) and stores only its own.
+#include "ptx_sm100.cuh"
+#include "row_vectors.cuh"
+#include "tensor_map.cuh"
+
+namespace spconv {
+namespace {
+
+constexpr int kPairs = 76;
+constexpr int kGroupM = 16;              // row tiles that share the column tiles in L2
+constexpr int kStageA = 128 * 128, kStage = 2 * kStageA;
+constexpr int kStages = 5;
+constexpr int kEpiWarps = 8;
+constexpr int kFirstEpi = 4;             // warp 0 loads, warp 1 issues MMAs, warps 4 .. 11 add up
+constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+constexpr int kStaging = 32 * 256;       // of an epilogue warp: 32 rows of 128 bf16
+// Registers a thread: 168 at the launch (three warps on each quarter of an SM), then
+// 56 for the first four warps and 224 for the others.
+constexpr int kRegsFirst = 56, kRegsEpi = 224;
+static_assert(128 * kRegsFirst + 32 * kEpiWarps * kRegsEpi <= kThreads * 168, "register split");
+constexpr int kTableSize = 256;
+constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStaging + 256 + 4 * (kTableSize + 1);
+static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+
+// Experts' runs of rows, in order and range whatever the offsets hold.
+struct Runs {
+    const int32_t* offsets;   // [count + 1] or null: one run of all rows
+    int32_t count;
+    int32_t n;
+    __device__ __forceinline__ void get(int32_t e, int32_t& lo, int32_t& hi) const {
+        lo = 0;
+        hi = n;
+        if (!offsets) return;
+        lo = __ldg(offsets + e);
+        hi = __ldg(offsets + e + 1);
+        lo = lo < 0 ? 0 : lo > n ? n : lo;
+        hi = hi < lo ? lo : hi > n ? n : hi;
+    }
+    // Borders out of order or range; by any number of threads.
+    __device__ __forceinline__ void check(int32_t first, int32_t step, int32_t* status) const {
+        if (!offsets) return;
+        for (int32_t e = first; e < count; e += step) {
+            const int32_t lo = __ldg(offsets + e), hi = __ldg(offsets + e + 1);
+            if (lo > hi || lo < 0 || hi > n) atomicOr(status, kStatusRange);
+        }
+    }
+};
+
+struct BlockArgs {
+    CUtensorMap x, w[2];
+    Runs runs;
+    int32_t h;                // columns of an expert's weight
+    int32_t kb;               // blocks of K
+    int32_t hb;               // blocks of columns
+    int32_t act;
+    const float* x_scale;     // [kb][n]
+    const float* w_scale[2];  // [experts][hb][kb]
+    const float* bias;        // [experts][h] or null
+    const __nv_bfloat16* extra;   // [n] rows of h, or null
+    int64_t ld_extra;
+    void* out;                // bf16 [n] rows of h; or e4m3 [n][h] with scale
+    int64_t ld_out;
+    float* scale;             // [hb][n]
+    int32_t vec_out, vec_extra;   // rows take 16-byte (e4m3: 8-byte) stores, loads
+    int32_t* status;
+};
+
+// Rows of no expert are zeros: before the first run, behind the last.
+template <bool EIGHT>
+__device__ __forceinline__ void zero_rest(const BlockArgs& p, int64_t first, int64_t step) {
+    if (!p.runs.offsets) return;
+    int32_t from = __ldg(p.runs.offsets), to = __ldg(p.runs.offsets + p.runs.count);
+    from = from < 0 ? 0 : from > p.runs.n ? p.runs.n : from;
+    to = to < from ? from : to > p.runs.n ? p.runs.n : to;
+    const int64_t rows = from + (p.runs.n - to);
+#pragma unroll 1
+    for (int64_t i = first; i < rows * p.h; i += step) {
+        const int64_t r = i / p.h, row = r < from ? r : to + (r - from);
+        if (EIGHT) static_cast<uint8_t*>(p.out)[row * p.ld_out + i % p.h] = 0;
+        else static_cast<__nv_bfloat16*>(p.out)[row * p.ld_out + i % p.h] = __float2bfloat16_rn(0.0f);
+    }
+    if (EIGHT)
+#pragma unroll 1
+        for (int64_t i = first; i < rows * p.hb; i += step) {
+            const int64_t r = i / p.hb, row = r < from ? r : to + (r - from);
+            p.scale[i % p.hb * p.runs.n + row] = 0.0f;
+        }
+}
+
+// The scale of a block whose largest magnitude is m, and the factor to its e4m3
+// values.  The values come from fp32 sums, so a product with the inverse serves;
+// below 2^-119 that would overflow, and they are brought up first.
+struct ToE4m3 {
+    float scale, pre, factor;
+    __device__ __forceinline__ explicit ToE4m3(float m) {
+        scale = __fdiv_rn(m, 448.0f);
+        pre = m < 0x1p-100f ? 0x1p100f : 1.0f;
+        factor = m == 0.0f ? 0.0f : __fdiv_rn(448.0f, m * pre);
+        if (!(m < __int_as_float(0x7F800000))) factor = __int_as_float(0x7FFFFFFF);   // infinity or NaN: all NaN
+    }
+    __device__ __forceinline__ float operator()(float v) const { return v * pre * factor; }
+};
+
+// A tile: its expert, first row, the run's end and its column tile.
+struct Tile {
+    int32_t e, row, end, tn;
+};
+
+// The k-th tile of this pair of CTAs, of `width` columns; false past its last one.
+template <int WIDTH>
+__device__ __forceinline__ bool find_tile(const BlockArgs& p, const int32_t* table, int32_t k, Tile& t) {
+    const int32_t stride = (p.runs.count + kTableSize - 1) / kTableSize, slots = (p.runs.count + stride - 1) / stride;
+    const int32_t tiles_n = (p.h + WIDTH - 1) / WIDTH;
+    const int64_t all = static_cast<int64_t>(table[slots]) * tiles_n;   // (below 2^31 where the borders are in order)
+    const int64_t next = (blockIdx.x >> 1) + static_cast<int64_t>(k) * (gridDim.x >> 1);
+    if (next >= (all < 0x7FFFFFFF ? all : 0x7FFFFFFF)) return false;
+    const int32_t u = static_cast<int32_t>(next);
+    const int32_t mt = u / tiles_n;   // (only which expert: its tiles are in an order of their own)
+    int32_t a = 0, b = slots;         // table[a] <= mt < table[b]
+#pragma unroll 1
+    while (b - a > 1) {
+        const int32_t mid = (a + b) >> 1;
+        if (table[mid] <= mt) a = mid;
+        else b = mid;
+    }
+    int32_t first = table[a], lo = 0, hi = 0, tiles = 0;
+    bool found = false;
+#pragma unroll 1
+    for (int32_t e = a * stride; e < p.runs.count && !found; ++e) {
+        p.runs.get(e, lo, hi);
+        tiles = (hi - lo + 255) / 256;
+        t.e = e;
+        found = mt < first + tiles;
+        if (!found) first += tiles;
+    }
+    if (!found) return false;
+    int32_t i = u - first * tiles_n;
+    const int32_t group = i / (kGroupM * tiles_n) * kGroupM;
+    i -= group * tiles_n;
+    const int32_t height = tiles - group < kGroupM ? tiles - group : kGroupM;
+    t.tn = i / height;
+    t.row = lo + (group + i - t.tn * height) * 256;
+    t.end = hi;
+    return true;
+}
+
+template <bool DUAL, bool EIGHT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_blocks_tc(const __grid_constant__ BlockArgs p) {
+    constexpr int S = kStages;
+    constexpr int kOut = DUAL ? 64 : 128;   // output columns of a warp
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+    uint8_t* staging = smem + S * kStage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging);   // [S]  (CTA 0's are used)
+    uint64_t* empty = full + S;             // [S]
+    uint64_t* acc_full = empty + S;         // [2]
+    uint64_t* acc_empty = acc_full + 2;     // [2]  (CTA 0's are used)
+    uint64_t* exit_bar = acc_empty + 2;
+    uint64_t* shared_max = exit_bar + 1;    // [4]  the two warps that share a block of a gated e4m3 output's columns
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shared_max + 4);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int32_t* table = reinterpret_cast<int32_t*>(staging + kEpiWarps * kStaging + 256);   // row tiles before every `stride`-th expert
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&acc_full[b], 1);
+            ptx::mbar_init(&acc_empty[b], 2 * kEpiWarps);
+        }
+        ptx::mbar_init(exit_bar, 1);
+        for (int g = 0; g < 4; ++g) ptx::mbar_init(&shared_max[g], 2);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_map(&p.x);
+        ptx::prefetch_map(&p.w[0]);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(tmem_slot, 512);
+        ptx::tmem_relinquish_pair();
+    }
+    pdl_wait();
+    const int32_t stride = (p.runs.count + kTableSize - 1) / kTableSize;
+    if (warp == 2) {
+        int32_t sum = 0;
+        for (int32_t i0 = 0; i0 * stride < p.runs.count; i0 += 32) {
+            const int32_t e0 = (i0 + lane) * stride;
+            int32_t tiles = 0;
+            for (int32_t e = e0; e < e0 + stride && e < p.runs.count; ++e) {
+                int32_t lo, hi;
+                p.runs.get(e, lo, hi);
+                tiles += (hi - lo + 255) / 256;
+            }
+            int32_t inc = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc += u;
+            }
+            // (at most 2^30, whatever the borders)
+            if (e0 < p.runs.count) table[i0 + lane] = min(sum + inc - tiles, 1 << 30);
+            sum = min(sum + __shfl_sync(0xFFFFFFFFu, inc, 31), 1 << 30);
+        }
+        if (lane == 0) table[(p.runs.count + stride - 1) / stride] = sum;
+    }
+    if (warp == 3 && blockIdx.x == 0) p.runs.check(lane, 32, p.status);
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    pdl_trigger();   // (once TMEM is allocated: the next kernel's blocks may want theirs on this SM)
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t smem_base = ptx::smem_u32(smem);
+    constexpr int kTileN = DUAL ? 128 : 256;
+
+    auto fail = [&]() {
+        atomicOr(p.status, kStatusTimeout);
+        *abort_flag = 1;
+    };
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xFFFFFFFFu, ptx::mbar_wait(bar, parity, abort_flag));
+    };
+    auto tile_at = [&](int32_t k, Tile& t) { return find_tile<DUAL ? 128 : 256>(p, table, k, t); };
+    uint32_t fills = 0;   // stages this thread has filled
+    if (warp < kFirstEpi) ptx::regs_dec<kRegsFirst>();
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t& f = fills;
+            bool ok = true;
+            Tile t;
+            for (int32_t q = 0; ok && tile_at(q, t); ++q) {
+                const int32_t r0 = t.row + static_cast<int32_t>(rank) * 128;
+                const int32_t o0 = t.e * p.h + (DUAL ? t.tn * 128 : t.tn * 256 + static_cast<int32_t>(rank) * 128);
+                const CUtensorMap* w = &p.w[DUAL ? rank : 0];
+#pragma unroll 1
+                for (int32_t it = 0; it < p.kb; ++it, ++f) {
+                    const uint32_t s = f % S;
+                    if (f >= S && !ptx::mbar_wait(&empty[s], (f / S - 1) & 1, abort_flag)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStage);   // of both CTAs
+                    const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(&full[s]), 0);
+                    ptx::tma_load_2d_pair(smem_base + s * kStage, &p.x, it * 128, r0, bar);
+                    ptx::tma_load_2d_pair(smem_base + s * kStage + kStageA, w, it * 128, o0, bar);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint32_t leader = lane == 0;
+            const uint32_t idesc = ptx::idesc_dense(true, true, true, 256, 256);
+            const uint64_t a0 = ptx::sdesc_k128(smem_base), b0 = ptx::sdesc_k128(smem_base + kStageA);
+            uint32_t f = 0;
+            bool ok = true;
+            Tile t;
+            for (int32_t q = 0; ok && tile_at(q, t); ++q) {
+#pragma unroll 1
+                for (int32_t it = 0; it < p.kb; ++it, ++f) {
+                    const uint32_t s = f % S, buf = f & 1;
+                    if ((f >= 2 && !warp_wait(&acc_empty[buf], ((f >> 1) - 1) & 1)) || !warp_wait(&full[s], (f / S) & 1)) {
+                        if (lane == 0) fail();
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint64_t off = static_cast<uint64_t>((s * kStage) >> 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ptx::mma_pair_if<true>(leader, tmem + buf * 256, a0 + off + 2 * j, b0 + off + 2 * j, idesc, j > 0 ? 1u : 0u);
+                    ptx::mma_commit_pair_if(leader, &empty[s]);
+                    ptx::mma_commit_pair_if(leader, &acc_full[buf]);
+                }
+            }
+            ptx::mma_commit_pair_if(leader, exit_bar);
+            const bool done = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(exit_bar, 0, nullptr));
+            if (!done && lane == 0) atomicOr(p.status, kStatusTimeout);
+        }
+    } else if (warp >= kFirstEpi) {
+        ptx::regs_inc<kRegsEpi>();
+        const int e = warp - kFirstEpi;
+        const int quarter = warp & 3, part = e >> 2;   // TMEM lanes; half of the columns
+        uint8_t* stage0 = staging + e * kStaging;
+        const uint32_t acc_bar = ptx::map_to_rank(ptx::smem_u32(&acc_empty[0]), 0);
+        // accumulator columns of each 16: 128 next to each other, or 64 of gate and 64 of up
+        const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        auto column = [&](int c) { return DUAL ? (c < 4 ? part * 64 + c * 16 : 128 + part * 64 + (c - 4) * 16) : part * 128 + c * 16; };
+        uint32_t f = 0;
+        bool ok = true;
+        Tile t;
+        for (int32_t q = 0; ok && tile_at(q, t); ++q) {
+            const int32_t m0 = t.row + static_cast<int32_t>(rank) * 128 + quarter * 32, row = m0 + lane;
+            const int32_t n0 = t.tn * kTileN + part * kOut;   // first output column
+            const bool live = row < t.end;
+            const float* xs = p.x_scale + (live ? row : 0);   // (other rows' sums are not used)
+            // (columns past the last block are not stored: any scale serves)
+            const int32_t block = DUAL ? t.tn : min(t.tn * 2 + part, p.hb - 1);
+            int32_t wi = (t.e * p.hb + block) * p.kb;
+            F2 acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = F2(0.0f);
+            float x_next = __ldg(xs);
+#pragma unroll 1
+            for (int32_t it = 0; it < p.kb; ++it, ++f, ++wi) {
+                const uint32_t buf = f & 1;
+                const F2 s0(x_next * __ldg(p.w_scale[0] + wi)), s1(DUAL ? x_next * __ldg(p.w_scale[1] + wi) : 0.0f);
+                if (it + 1 < p.kb) xs += p.runs.n, x_next = __ldg(xs);
+                if (!warp_wait(&acc_full[buf], (f >> 1) & 1)) {
+                    if (lane == 0) fail();
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                // the next 16 columns are on their way while these are added
+                uint32_t z[2][16];
+                ptx::tmem_ld_32x32b_x16(ta + buf * 256 + column(0), z[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    ptx::tmem_ld_wait_for(z[c & 1]);
+                    if (c < 7) {
+                        ptx::tmem_ld_32x32b_x16(ta + buf * 256 + column(c + 1), z[(c + 1) & 1]);
+                    } else {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_cluster(acc_bar + buf * 8);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2)
+                        acc[(c * 16 + j) / 2] = fma_v(F2(__uint_as_float(z[c & 1][j]), __uint_as_float(z[c & 1][j + 1])),
+                                                      DUAL && c >= 4 ? s1 : s0, acc[(c * 16 + j) / 2]);
+                }
+            }
+            if (!ok) break;
+            const int32_t rows = t.end - m0 < 32 ? t.end - m0 : 32, left = p.h - n0;   // (either may be negative)
+            // two columns at a time; the results take the places of the sums
+            if (!DUAL && p.bias && left > 0) {
+                const float* bias = p.bias + static_cast<int64_t>(t.e) * p.h + n0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float b = c * 32 + lane < left ? __ldg(bias + c * 32 + lane) : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[c * 16 + j] = acc[c * 16 + j] + F2(__shfl_sync(0xFFFFFFFFu, b, 2 * j), __shfl_sync(0xFFFFFFFFu, b, 2 * j + 1));
+                }
+            }
+            // (32 columns at a time, moved to where one copy of the code finds them: unrolled over all
+            // of them it needs more registers than there are)
+            if (DUAL || p.act != SPCONV_ACT_NONE) {
+#pragma unroll 1
+                for (int c = 0; c < kOut / 32; ++c) {
+                    F2 v[16], u[16];
+#pragma unroll
+                    for (int k = 0; k < kOut / 32; ++k)
+                        if (c == k) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                v[j] = acc[k * 16 + j];
+                                if (DUAL) u[j] = acc[(k * 16 + j + 32) % 64];
+                            }
+                        }
+                    with_act(p.act, [&](auto act) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = DUAL ? act_f<act>(v[j]) * u[j] : act_f<act>(v[j]);
+                    });
+#pragma unroll
+                    for (int k = 0; k < kOut / 32; ++k)
+                        if (c == k) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[k * 16 + j] = v[j];
+                        }
+                }
+            }
+            if (!EIGHT) {
+                // rows of kOut bf16 through shared memory, in 16-byte pieces whose places are
+                // turned by the row, so that neither side meets in a bank
+                constexpr int kPieces = kOut / 8, kRows = 32 / kPieces;
+                auto place = [](int r, int piece) { return r * (kOut * 2) + ((piece ^ (r & 7)) << 4); };
+                if (!DUAL && p.extra) {
+#pragma unroll 4
+                    for (int r = 0; r < 32; r += kRows) {
+                        const int i = r + lane / kPieces, c8 = lane % kPieces;   // row; eight columns
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (i < rows && c8 * 8 < left) {
+                            const __nv_bfloat16* x = p.extra + (m0 + i) * p.ld_extra + n0 + c8 * 8;
+                            if (p.vec_extra && c8 * 8 + 8 <= left) {
+                                v = *reinterpret_cast<const uint4*>(x);
+                            } else {
+                                uint32_t u[4] = {};
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    if (c8 * 8 + j < left) u[j / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x[j])) << (16 * (j & 1));
+                                v = make_uint4(u[0], u[1], u[2], u[3]);
+                            }
+                        }
+                        *reinterpret_cast<uint4*>(stage0 + place(i, c8)) = v;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int c8 = 0; c8 < kPieces; ++c8) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage0 + place(lane, c8));
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc[c8 * 4 + j] = acc[c8 * 4 + j] + F2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xFFFF0000u));
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int c8 = 0; c8 < kPieces; ++c8) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float a, b;
+                        acc[c8 * 4 + j].get(a, b);
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+                        u[j] = reinterpret_cast<const uint32_t&>(v);
+                    }
+                    *reinterpret_cast<uint4*>(stage0 + place(lane, c8)) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                __syncwarp();
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+#pragma unroll 4
+                for (int r = 0; r < 32; r += kRows) {
+                    const int i = r + lane / kPieces, c8 = lane % kPieces;
+                    if (i >= rows || c8 * 8 >= left) continue;
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage0 + place(i, c8));
+                    __nv_bfloat16* o = out + (m0 + i) * p.ld_out + n0 + c8 * 8;
+                    if (p.vec_out && c8 * 8 + 8 <= left) {
+                        *reinterpret_cast<uint4*>(o) = v;
+                    } else {
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (c8 * 8 + j < left) o[j] = __ushort_as_bfloat16(static_cast<uint16_t>(u[j / 2] >> (16 * (j & 1))));
+                    }
+                }
+            } else {
+                // the largest of the row's 128 columns: this warp's, or its half and another warp's
+                uint32_t most = 0;
+#pragma unroll
+                for (int j = 0; j < kOut / 2; ++j) {
+                    float a, b;
+                    acc[j].get(a, b);
+                    if (2 * j < left) most = max(most, __float_as_uint(fabsf(a)));
+                    if (2 * j + 1 < left) most = max(most, __float_as_uint(fabsf(b)));
+                }
+                if (DUAL) {
+                    // (behind the staged output, by the tiles' parity: a slot is written again two tiles
+                    // later, when both have passed the barrier of the tile between)
+                    uint64_t* bar = &shared_max[quarter];
+                    const uint32_t slot = 4096 + (q & 1) * 128 + lane * 4;
+                    *reinterpret_cast<volatile uint32_t*>(stage0 + slot) = most;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar);
+                    if (!warp_wait(bar, q & 1)) {
+                        if (lane == 0) fail();
+                        ok = false;
+                        break;
+                    }
+                    most = max(most, *reinterpret_cast<volatile uint32_t*>(staging + (e ^ 4) * kStaging + slot));
+                }
+                const ToE4m3 to(__uint_as_float(most));
+                if ((!DUAL || part == 0) && live && left > 0) p.scale[static_cast<int64_t>(n0 / 128) * p.runs.n + row] = to.scale;
+                constexpr int kPieces = kOut / 16, kRows = 32 / kPieces;   // 16-byte pieces of a row
+                auto place = [](int r, int piece) { return r * kOut + ((piece ^ (kPieces == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
+#pragma unroll
+                for (int c = 0; c < kPieces; ++c) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float a, b, d, g;
+                        acc[c * 8 + j * 2].get(a, b);
+                        acc[c * 8 + j * 2 + 1].get(d, g);
+                        u[j] = __nv_cvt_float2_to_fp8x2(make_float2(to(a), to(b)), __NV_SATFINITE, __NV_E4M3) |
+                               static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(to(d), to(g)), __NV_SATFINITE, __NV_E4M3)) << 16;
+                    }
+                    *reinterpret_cast<uint4*>(stage0 + place(lane, c)) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                __syncwarp();
+                uint8_t* out = static_cast<uint8_t*>(p.out);
+#pragma unroll 4
+                for (int r = 0; r < 32; r += kRows) {
+                    const int i = r + lane / kPieces, c = lane % kPieces;
+                    if (i >= rows || c * 16 >= left) continue;
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage0 + place(i, c));
+                    uint8_t* o = out + (m0 + i) * p.ld_out + n0 + c * 16;
+                    if (p.vec_out && c * 16 + 16 <= left) {
+                        *reinterpret_cast<uint4*>(o) = v;
+                    } else {
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (c * 16 + j < left) o[j] = static_cast<uint8_t>(u[j / 4] >> (8 * (j % 4)));
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        zero_rest<EIGHT>(p, static_cast<int64_t>(blockIdx.x) * (32 * kEpiWarps) + threadIdx.x - 32 * kFirstEpi, static_cast<int64_t>(gridDim.x) * (32 * kEpiWarps));
+    }
+    // (as in dense_tc.cu: neither CTA leaves, or frees TMEM, while the other may still signal it)
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    const uint32_t side = ptx::cluster_rank();   // (read again: no register is kept for it)
+    if (side == 0 && fills && *abort_flag)
+        for (uint32_t q = fills > S ? fills - S : 0; q < fills; ++q) ptx::mbar_wait(&full[q % S], (q / S) & 1, nullptr);
+    __syncwarp();
+    if (warp == 1 && side == 1 && !ptx::mbar_wait(exit_bar, 0, nullptr)) atomicOr(p.status, kStatusTimeout);
+    __syncwarp();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc_pair(*tmem_slot, 512);
+}
+
+// ---- few rows -------------------------------------------------------------------
+// The weights are the traffic, so they are streamed once and the operands change
+// places: 128 output channels (one block of the weight's scales) are the MMA's M,
+// R rows of x its N.  A cluster of `splits` CTAs cuts K between them; each adds
+// its blocks up in registers (a thread a channel), and the cluster's partial sums
+// are added through distributed shared memory in the order of the ranks.
+// Accumulators of one block of K take turns in a ring in TMEM.
+constexpr int kFewThreads = 192;       // warp 0 loads, warp 1 issues MMAs, warps 2-5 add up
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kTileW = 128 * 128;
+constexpr int kMaxStages = 8;
+constexpr int kMaxAcc = 4;
+constexpr int kFewRing = 100 * 1024;   // of one of two CTAs on an SM
+constexpr int kMaxSplits = 8;
+
+struct FewBlockArgs {
+    BlockArgs b;
+    int32_t stages, stage_bytes;
+};
+
+template <bool DUAL, bool EIGHT, int R>
+__global__ void __launch_bounds__(kFewThreads, 2) k_blocks_few(const __grid_constant__ FewBlockArgs a) {
+    constexpr int kAcc = DUAL ? 2 : 1;
+    constexpr int kCols = kAcc * R;                               // TMEM columns of an accumulator
+    constexpr int kBufs = 256 / kCols < kMaxAcc ? 256 / kCols : kMaxAcc;
+    constexpr uint32_t kTmem = kBufs * kCols;
+    static_assert(kTmem >= 32 && (kTmem & (kTmem - 1)) == 0, "TMEM columns");
+    static_assert(kAcc * R * 128 * 4 <= kFewRing, "the sums take the ring's place");
+    const BlockArgs& p = a.b;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kBufs], acc_empty[kBufs];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    uint8_t* ring = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t splits = gridDim.y, rank = blockIdx.y;   // the cluster is one column of the grid
+    const int32_t e = static_cast<int32_t>(blockIdx.z), tn = static_cast<int32_t>(blockIdx.x);
+    pdl_wait();
+    if (tn == 0 && rank == 0 && e == 0) p.runs.check(threadIdx.x, kFewThreads, p.status);
+    if (rank == 0) {
+        const int64_t block = static_cast<int64_t>(e) * gridDim.x + tn, step = static_cast<int64_t>(gridDim.z) * gridDim.x * kFewThreads;
+        zero_rest<EIGHT>(p, block * kFewThreads + threadIdx.x, step);
+    }
+    int32_t lo, hi;
+    p.runs.get(e, lo, hi);
+    if (lo == hi) return;   // (the whole cluster)
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < kBufs; ++s) {
+            ptx::mbar_init(&acc_full[s], 1);
+            ptx::mbar_init(&acc_empty[s], 4);
+        }
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&tmem_slot, kTmem);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    pdl_trigger();   // (once TMEM is allocated, as above)
+    const uint32_t tmem = tmem_slot;
+    const int32_t n0 = tn * 128;
+    const int32_t it0 = static_cast<int32_t>(rank * static_cast<uint32_t>(p.kb) / splits);
+    const int32_t it1 = static_cast<int32_t>((rank + 1) * static_cast<uint32_t>(p.kb) / splits);
+    auto fail = [&]() {
+        atomicOr(p.status, kStatusTimeout);
+        *abort_flag = 1;
+    };
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xFFFFFFFFu, ptx::mbar_wait(bar, parity, abort_flag));
+    };
+    const uint32_t base = ptx::smem_u32(ring);
+    float* sums = reinterpret_cast<float*>(ring);   // [kAcc][R][128]
+    uint32_t f = 0;                                 // blocks that this role has handled
+    uint32_t fills = 0;                             // of the loading thread
+    for (int32_t r0 = lo; r0 < hi; r0 += R) {
+        const int32_t rows = hi - r0 < R ? hi - r0 : R;
+        if (warp == 0) {
+            if (lane == 0) {
+                for (int32_t it = it0; it < it1; ++it, ++fills) {
+                    const uint32_t s = fills % a.stages;
+                    if (fills >= static_cast<uint32_t>(a.stages) && !ptx::mbar_wait(&empty[s], (fills / a.stages - 1) & 1, abort_flag)) {
+                        fail();
+                        break;
+                    }
+                    const uint32_t at = base + s * a.stage_bytes, bar = ptx::smem_u32(&full[s]);
+                    ptx::mbar_arrive_expect_tx(&full[s], kAcc * kTileW + R * 128);
+#pragma unroll
+                    for (int w = 0; w < kAcc; ++w) ptx::tma_load_2d(at + w * kTileW, &p.w[w], it * 128, e * p.h + n0, bar);
+                    ptx::tma_load_2d(at + kAcc * kTileW, &p.x, it * 128, r0, bar);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            const uint32_t leader = lane == 0;
+            const uint32_t idesc = ptx::idesc_dense(true, true, true, 128, R);
+            for (int32_t it = it0; it < it1; ++it, ++f) {
+                const uint32_t s = f % a.stages, buf = f % kBufs;
+                if ((f >= kBufs && !warp_wait(&acc_empty[buf], (f / kBufs - 1) & 1)) || !warp_wait(&full[s], (f / a.stages) & 1)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t at = base + s * a.stage_bytes;
+#pragma unroll
+                for (int w = 0; w < kAcc; ++w)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ptx::mma_if<true>(leader, tmem + buf * kCols + w * R, ptx::sdesc_k128(at + w * kTileW) + 2 * j,
+                                          ptx::sdesc_k128(at + kAcc * kTileW) + 2 * j, idesc, j > 0 ? 1u : 0u);
+                ptx::mma_commit_if(leader, &empty[s]);
+                ptx::mma_commit_if(leader, &acc_full[buf]);
+            }
+        } else {
+            const int quarter = warp & 3;
+            const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+            float acc[kAcc][R];
+#pragma unroll
+            for (int w = 0; w < kAcc; ++w)
+#pragma unroll
+                for (int j = 0; j < R; ++j) acc[w][j] = 0.0f;
+            for (int32_t it = it0; it < it1; ++it, ++f) {
+                const uint32_t buf = f % kBufs;
+                // lane j has the scale of row j (and j + 32), passed round below
+                const float* xs = p.x_scale + static_cast<int64_t>(it) * p.runs.n + r0;
+                const float x0 = lane < rows ? __ldg(xs + lane) : 0.0f, x1 = R > 32 && lane + 32 < rows ? __ldg(xs + lane + 32) : 0.0f;
+                float ws[kAcc];
+#pragma unroll
+                for (int w = 0; w < kAcc; ++w) ws[w] = __ldg(p.w_scale[w] + (static_cast<int64_t>(e) * p.hb + tn) * p.kb + it);
+                if (!warp_wait(&acc_full[buf], (f / kBufs) & 1)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int w = 0; w < kAcc; ++w)
+#pragma unroll
+                    for (int c = 0; c < R; c += 16) {
+                        uint32_t z[16];
+                        ptx::tmem_ld_32x32b_x16(tmem + lanes + buf * kCols + w * R + c, z);
+                        ptx::tmem_ld_wait();
+                        if (w == kAcc - 1 && c == R - 16) {
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float s = ws[w] * __shfl_sync(0xFFFFFFFFu, c + j < 32 ? x0 : x1, (c + j) & 31);
+                            // (a row past the run's end is some other row: its sums are not used)
+                            acc[w][c + j] = fmaf(__uint_as_float(z[j]), s, acc[w][c + j]);
+                        }
+                    }
+            }
+            // every block has been added up: the ring is free once all four warps are here
+            ptx::named_barrier_sync(1, 128);
+#pragma unroll
+            for (int w = 0; w < kAcc; ++w)
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    if (j < rows) sums[(w * R + j) * 128 + quarter * 32 + lane] = acc[w][j];
+        }
+        ptx::cluster_sync();
+        // this CTA's share: rows rank, rank + splits, ..; a warp a row, a lane four channels
+        const int32_t left = p.h - n0 - 4 * lane;
+        const uint32_t sums_addr = ptx::smem_u32(sums);
+        for (int32_t i = static_cast<int32_t>(rank) + warp * static_cast<int32_t>(splits); i < rows; i += kFewWarps * static_cast<int32_t>(splits)) {
+            const int64_t row = r0 + i;
+            float z[kAcc][4] = {};
+#pragma unroll
+            for (int w = 0; w < kAcc; ++w) {
+                const uint32_t at = sums_addr + static_cast<uint32_t>(((w * R + i) * 128 + 4 * lane) * 4);
+                float4 part[kMaxSplits];
+#pragma unroll
+                for (uint32_t r = 0; r < kMaxSplits; ++r)
+                    part[r] = r < splits ? ptx::ld_cluster_f32x4(ptx::map_to_rank(at, r)) : make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (uint32_t r = 0; r < kMaxSplits; ++r) {
+                    z[w][0] += part[r].x;
+                    z[w][1] += part[r].y;
+                    z[w][2] += part[r].z;
+                    z[w][3] += part[r].w;
+                }
+            }
+            if (!DUAL && p.bias)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < left) z[0][j] += __ldg(p.bias + static_cast<int64_t>(e) * p.h + n0 + 4 * lane + j);
+            with_act(p.act, [&](auto act) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[0][j] = DUAL ? act_f<act>(z[0][j]) * z[kAcc - 1][j] : act_f<act>(z[0][j]);
+            });
+            if (!DUAL && p.extra)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < left) z[0][j] += __bfloat162float(p.extra[row * p.ld_extra + n0 + 4 * lane + j]);
+            if (EIGHT) {
+                uint32_t most = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < left) most = max(most, __float_as_uint(fabsf(z[0][j])));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+                const ToE4m3 to(__uint_as_float(most));
+                if (lane == 0) p.scale[static_cast<int64_t>(tn) * p.runs.n + row] = to.scale;
+                const uint32_t v = __nv_cvt_float2_to_fp8x2(make_float2(to(z[0][0]), to(z[0][1])), __NV_SATFINITE, __NV_E4M3) |
+                                   static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(to(z[0][2]), to(z[0][3])), __NV_SATFINITE, __NV_E4M3)) << 16;
+                uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.ld_out + n0 + 4 * lane;
+                if (p.vec_out && left >= 4) {
+                    *reinterpret_cast<uint32_t*>(out) = v;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < left) out[j] = static_cast<uint8_t>(v >> (8 * j));
+                }
+            } else {
+                alignas(8) __nv_bfloat16 y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = __float2bfloat16_rn(z[0][j]);
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + n0 + 4 * lane;
+                if (p.vec_out && left >= 4) {
+                    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < left) out[j] = y[j];
+                }
+            }
+        }
+        // no CTA's sums go away while another may still read them; loads come into the same bytes
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        ptx::cluster_sync();
+        ptx::tc_fence_after();
+    }
+    if (warp == 0 && lane == 0 && *abort_flag)   // given up: loads still in flight land first
+        for (uint32_t j = fills > static_cast<uint32_t>(a.stages) ? fills - a.stages : 0; j < fills; ++j)
+            ptx::mbar_wait(&full[j % a.stages], (j / a.stages) & 1, nullptr);
+    __syncthreads();
+    if (warp == 1) ptx::tmem_dealloc(tmem, kTmem);
+}
+
+// ---- host -----------------------------------------------------------------------
+template <auto KERNEL>
+int allow_smem(int bytes) {
+    static bool set[kMaxDevices] = {};
+    int dev = 0;
+    SPCONV_CHECK_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= kMaxDevices) return SPCONV_ERR_UNSUPPORTED;
+    if (!set[dev]) {
+        SPCONV_CHECK_CUDA(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+        set[dev] = true;
+    }
+    return SPCONV_OK;
+}
+
+int make_maps(const BlockOp& op, const void* x, int64_t ldx, int32_t rows, BlockArgs* p) {
+    SPCONV_CHECK(make_tensor_map(&p->x, x, 1, op.k, op.n, ldx, rows));
+    for (int i = 0; i < (op.w[1] ? 2 : 1); ++i)
+        SPCONV_CHECK(make_tensor_map(&p->w[i], op.w[i], 1, op.k, static_cast<int64_t>(op.experts) * op.h, op.k, 128));
+    return SPCONV_OK;
+}
+
+template <bool DUAL, bool EIGHT>
+int run_tc(const BlockOp& op, const BlockArgs& p, cudaStream_t s) {
+    const int64_t tiles = (op.n / 256 + op.experts) * ceil_div(op.h, DUAL ? 128 : 256);
+    if (tiles >= 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
+    const unsigned pairs = static_cast<unsigned>(tiles < kPairs ? tiles : kPairs);
+    SPCONV_CHECK((allow_smem<k_blocks_tc<DUAL, EIGHT>>(kSmem)));
+    return launch_pdl(k_blocks_tc<DUAL, EIGHT>, dim3(2 * pairs), kThreads, kSmem, s, p);
+}
+
+template <bool DUAL, bool EIGHT, int R>
+int run_few(const BlockOp& op, const BlockArgs& p, int64_t active, cudaStream_t s) {
+    FewBlockArgs a = {};
+    a.b = p;
+    const int64_t tiles = ceil_div(op.h, 128);
+    int32_t splits = 1;
+    while (splits < kMaxSplits && tiles * active * splits * 2 <= 304 && p.kb >= 4 * splits) splits *= 2;
+    a.stage_bytes = (DUAL ? 2 : 1) * kTileW + R * 128;
+    a.stages = kFewRing / a.stage_bytes < kMaxStages ? kFewRing / a.stage_bytes : kMaxStages;
+    SPCONV_CHECK((allow_smem<k_blocks_few<DUAL, EIGHT, R>>(kFewRing + 1024)));
+    cudaLaunchAttribute at[2] = {pdl_attr(), {}};
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = static_cast<unsigned>(splits);
+    at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(splits), static_cast<unsigned>(op.experts));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = kFewRing + 1024;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    count_launch();
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_blocks_few<DUAL, EIGHT, R>, static_cast<const FewBlockArgs&>(a)));
+}
+
+template <bool DUAL, bool EIGHT>
+int run(const BlockOp& op, cudaStream_t s) {
+    BlockArgs p = {};
+    p.runs = Runs{op.offsets, op.experts, static_cast<int32_t>(op.n)};
+    p.h = op.h;
+    p.kb = static_cast<int32_t>(ceil_div(op.k, 128));
+    p.hb = static_cast<int32_t>(ceil_div(op.h, 128));
+    p.act = op.act;
+    p.x_scale = op.x_scale;
+    p.w_scale[0] = op.w_scale[0];
+    p.w_scale[1] = op.w_scale[1];
+    p.bias = op.bias;
+    p.extra = static_cast<const __nv_bfloat16*>(op.extra);
+    p.ld_extra = op.ld_extra;
+    p.out = op.out;
+    p.ld_out = op.ld_out;
+    p.scale = op.out_scale;
+    p.vec_extra = op.extra && tma_ok(op.extra, op.ld_extra, 2);
+    p.vec_out = tma_ok(op.out, op.ld_out, EIGHT ? 1 : 2);
+    SPCONV_CHECK(rows_status_word(&p.status));
+    // x in the alignment that its tensor map needs
+    AlignedRows rows;
+    const void* x = op.x;
+    int64_t ldx = op.ldx;
+    rows.add(&x, 1, &ldx, op.n, op.k, 1);
+    SPCONV_CHECK(rows.run(s));
+    // few rows a run: an expert has n / experts of them where all are chosen alike
+    const int64_t active = op.experts < op.n ? op.experts : op.n;
+    const int64_t each = ceil_div(op.n, active);
+    if (each <= 64) {
+        const int32_t r = each <= 16 ? 16 : each <= 32 ? 32 : 64;
+        SPCONV_CHECK(make_maps(op, x, ldx, r, &p));
+        return r == 16 ? run_few<DUAL, EIGHT, 16>(op, p, active, s) : r == 32 ? run_few<DUAL, EIGHT, 32>(op, p, active, s)
+                                                                             : run_few<DUAL, EIGHT, 64>(op, p, active, s);
+    }
+    SPCONV_CHECK(make_maps(op, x, ldx, 128, &p));
+    return run_tc<DUAL, EIGHT>(op, p, s);
+}
+
+}  // namespace
+
+int blocks_run(const BlockOp& op, cudaStream_t s) {
+    if (op.w[1]) return op.out_scale ? run<true, true>(op, s) : run<true, false>(op, s);
+    return op.out_scale ? run<false, true>(op, s) : run<false, false>(op, s);
+}
+
+}  // namespace spconv

@@ -17,6 +17,31 @@ bool overlaps_any(const Rows& out, const Rows* ins, int count) {
     return false;
 }
 
+// The arguments that both products have; out and what it may not lie on.
+int check_blocks(const BlockOp& op, int32_t c_in, int32_t c_out) {
+    if (bad_sizes(op.n, c_in, c_out) || bad_act(op.act) || op.experts < 1 || op.experts > kMaxExperts ||
+        (!op.offsets && op.experts != 1) || !aligned(op.offsets, 4))
+        return SPCONV_ERR_INVALID_ARG;
+    return c_in % 16 ? SPCONV_ERR_UNSUPPORTED : SPCONV_OK;
+}
+int run_blocks(const BlockOp& op, cudaStream_t s) {
+    const int64_t wn = int64_t(op.experts) * op.h * op.k, kb = ceil_div(op.k, 128), hb = ceil_div(op.h, 128);
+    const bool dual = op.w[1] != nullptr, eight = op.out_scale != nullptr;
+    const Rows x{op.x, op.n, op.k, op.ldx, 1}, out{op.out, op.n, op.h, op.ld_out, eight ? size_t(1) : size_t(2)},
+        scale = vec(op.out_scale, op.n * hb), res{op.extra, op.n, op.h, op.ld_extra, 2};
+    const Rows ins[8] = {x, vec(op.x_scale, kb * op.n), {op.w[0], 1, wn, wn, 1}, {op.w[1], 1, wn, wn, 1},
+                         vec(op.w_scale[0], op.experts * hb * kb), vec(op.w_scale[1], op.experts * hb * kb),
+                         ints(op.offsets, op.experts + 1), vec(op.bias, int64_t(op.experts) * op.h)};
+    if (!x.ok() || !out.ok() || !op.w[0] || !aligned(op.w[0], 16) || !aligned(op.w[1], 16) || (op.extra && !res.ok()))
+        return SPCONV_ERR_INVALID_ARG;
+    if (!op.x_scale || !op.w_scale[0] || (dual && !op.w_scale[1])) return SPCONV_ERR_INVALID_ARG;
+    for (const float* v : {op.x_scale, op.w_scale[0], op.w_scale[1], op.bias, static_cast<const float*>(op.out_scale)})
+        if (bad_vec(v)) return SPCONV_ERR_INVALID_ARG;
+    if (overlaps_any(out, ins, 8) || overlaps_any(scale, ins, 8) || scale.overlaps(out) || (out.overlaps(res) && !out.same(res)))
+        return SPCONV_ERR_ALIAS;
+    return blocks_run(op, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -115,6 +140,32 @@ int spconv_quantize_weight_blocks(const void* w_dev, int32_t count, int32_t c_in
     if (!w.ok() || !q.ok() || !scale.ok()) return SPCONV_ERR_INVALID_ARG;
     if (q.overlaps(w) || scale.overlaps(w) || q.overlaps(scale)) return SPCONV_ERR_ALIAS;
     return quantize_weight_blocks(w_dev, count, c_in, c_out, q_dev, scale_dev, static_cast<cudaStream_t>(stream));
+}
+
+int spconv_linear_blocks(const void* x_dev, int64_t ld_x, const float* x_scale_dev, const void* w_dev, const float* w_scale_dev,
+                         const int32_t* offsets_dev, int32_t n_experts, int64_t n, int32_t c_in, int32_t c_out,
+                         const float* bias_dev, int32_t activation, const void* residual_dev, int64_t ld_residual, void* out_dev,
+                         int64_t ld_out, float* out_scale_dev, void* stream) {
+    reset_launch_count();
+    const BlockOp op{x_dev, ld_x, x_scale_dev, {w_dev, nullptr}, {w_scale_dev, nullptr}, offsets_dev, n_experts, n, c_in, c_out,
+                     bias_dev, activation, residual_dev, ld_residual, out_dev, ld_out, out_scale_dev};
+    SPCONV_CHECK(check_blocks(op, c_in, c_out));
+    if (residual_dev && out_scale_dev) return SPCONV_ERR_UNSUPPORTED;
+    if (n == 0) return SPCONV_OK;
+    return run_blocks(op, static_cast<cudaStream_t>(stream));
+}
+
+int spconv_gated_ffn_blocks(const void* x_dev, int64_t ld_x, const float* x_scale_dev, const void* w_gate_dev,
+                            const float* gate_scale_dev, const void* w_up_dev, const float* up_scale_dev,
+                            const int32_t* offsets_dev, int32_t n_experts, int64_t n, int32_t c_in, int32_t c_hidden,
+                            int32_t activation, void* out_dev, int64_t ld_out, float* out_scale_dev, void* stream) {
+    reset_launch_count();
+    const BlockOp op{x_dev, ld_x, x_scale_dev, {w_gate_dev, w_up_dev}, {gate_scale_dev, up_scale_dev}, offsets_dev, n_experts, n,
+                     c_in, c_hidden, nullptr, activation, nullptr, 0, out_dev, ld_out, out_scale_dev};
+    SPCONV_CHECK(check_blocks(op, c_in, c_hidden));
+    if (n == 0) return SPCONV_OK;
+    if (!w_up_dev) return SPCONV_ERR_INVALID_ARG;
+    return run_blocks(op, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -345,6 +345,29 @@ int expert_combine_backward(const ExpertGrad& a, cudaStream_t s);
 // w bf16 [count][c_in][c_out] -> q e4m3 [count][c_out][c_in], scale per 128 x 128
 int quantize_weight_blocks(const void* w, int64_t count, int32_t c_in, int32_t c_out, void* q, float* scale, cudaStream_t s);
 
+// ---- products with block scales (dense_blocks.cu) ----------------------------
+// out = act(z + bias) + extra, or with w[1] act(z0) z1; z the product of e4m3 x
+// and the e4m3 weight of a row's expert, each block of 128 x 128 scaled.
+struct BlockOp {
+    const void* x;            // [n] rows of k, ldx apart
+    int64_t ldx;
+    const float* x_scale;     // [ceil(k / 128)][n]
+    const void* w[2];         // [experts][h][k], 16-byte aligned, k a multiple of 16
+    const float* w_scale[2];  // [experts][ceil(h / 128)][ceil(k / 128)]
+    const int32_t* offsets;   // [experts + 1], or null: one weight for all rows
+    int32_t experts;
+    int64_t n;
+    int32_t k, h;
+    const float* bias;        // [experts][h] or null
+    int32_t act;
+    const void* extra;        // bf16 [n] rows of h, or null (with w[1] or out_scale)
+    int64_t ld_extra;
+    void* out;                // bf16 [n] rows of h, ld_out apart; or e4m3 with
+    int64_t ld_out;
+    float* out_scale;         // [ceil(h / 128)][n], or null
+};
+int blocks_run(const BlockOp& op, cudaStream_t s);
+
 // ---- products with an epilogue (dense.cu, dense_tc.cu) ----------------------------------
 // Element (i, k) of an operand is p[i ld + k] (k_major) or p[k ld + i].
 struct Operand {
