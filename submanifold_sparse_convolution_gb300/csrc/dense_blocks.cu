@@ -12,7 +12,9 @@
 // x and 128 of W.  Two accumulators of 256 columns take turns: while the tensor
 // pipe fills one with a block of K (4 MMAs, 512 clocks at the e4m3 rate), eight
 // warps add the other to their registers (128 sums a thread; 256 clocks of TMEM
-// loads and as many of multiply-adds over an SM).
+// loads and as many of multiply-adds over an SM).  (Halves of 128 columns, which
+// would leave more time between a half's last MMA and its next, are slower: shared
+// memory then has to feed the pipe 1.5 times as much.)
 //
 // Sorted rows: expert e's rows are offsets[e] .. offsets[e + 1] - 1, and its
 // weight rows e H .. (e + 1) H - 1 of the stacked weights.  The offsets stay on
@@ -31,15 +33,17 @@ constexpr int kGroupM = 16;              // row tiles that share the column tile
 constexpr int kStageA = 128 * 128, kStage = 2 * kStageA;
 constexpr int kStages = 5;
 constexpr int kEpiWarps = 8;
-constexpr int kFirstEpi = 4;             // warp 0 loads, warp 1 issues MMAs, warps 4 .. 11 add up
+constexpr int kFirstEpi = 4;             // warp 0 loads, warp 1 issues MMAs, warp 3 brings scales, warps 4 .. 11 add up
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
-constexpr int kStaging = 32 * 256;       // of an epilogue warp: 32 rows of 128 bf16
+constexpr int kStaging = 32 * 128;       // of an epilogue warp: twice 32 rows of 32 bf16, or 32 of 128 e4m3
+constexpr int kScaleSlots = 4;           // blocks of K whose scales lie in shared memory: [2 blocks of columns][128 rows] each
+constexpr int kScaleBytes = kScaleSlots * 2 * 128 * 4 + kEpiWarps * 16;   // (and the epilogue warps' tiles)
 // Registers a thread: 168 at the launch (three warps on each quarter of an SM), then
 // 56 for the first four warps and 224 for the others.
 constexpr int kRegsFirst = 56, kRegsEpi = 224;
 static_assert(128 * kRegsFirst + 32 * kEpiWarps * kRegsEpi <= kThreads * 168, "register split");
 constexpr int kTableSize = 256;
-constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStaging + 256 + 4 * (kTableSize + 1);
+constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStaging + kScaleBytes + 256 + 4 * (kTableSize + 1);
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
 // Experts' runs of rows, in order and range whatever the offsets hold.
@@ -67,7 +71,7 @@ struct Runs {
 };
 
 struct BlockArgs {
-    CUtensorMap x, w[2];
+    CUtensorMap x, w[2], c;   // c: of out, where map_out
     Runs runs;
     int32_t h;                // columns of an expert's weight
     int32_t kb;               // blocks of K
@@ -81,7 +85,8 @@ struct BlockArgs {
     void* out;                // bf16 [n] rows of h; or e4m3 [n][h] with scale
     int64_t ld_out;
     float* scale;             // [hb][n]
-    int32_t vec_out, vec_extra;   // rows take 16-byte (e4m3: 8-byte) stores, loads
+    int32_t vec_out, vec_extra;   // rows take 16-byte stores, loads
+    int32_t map_out;
     int32_t* status;
 };
 
@@ -126,14 +131,51 @@ struct Tile {
     int32_t e, row, end, tn;
 };
 
-// The k-th tile of this pair of CTAs, of `width` columns; false past its last one.
+// Tiles of all experts, WIDTH columns wide (below 2^31 where the borders are in order).
+template <int WIDTH>
+__device__ __forceinline__ int64_t tiles_of(const BlockArgs& p, const int32_t* table) {
+    const int32_t stride = (p.runs.count + kTableSize - 1) / kTableSize, slots = (p.runs.count + stride - 1) / stride;
+    const int64_t all = static_cast<int64_t>(table[slots]) * ((p.h + WIDTH - 1) / WIDTH);
+    return all < 0x7FFFFFFF ? all : 0x7FFFFFFF;
+}
+
+// Issues the MMAs of `blocks` blocks of K, the accumulators in turn.  What the tensor
+// pipe waits for between a block and the next but one is this loop too, so its values
+// are kept the same for the warp to the compiler's knowledge (the descriptors lie in
+// uniform registers then) and the next stage is looked at before it is needed.
+__device__ __forceinline__ bool issue_blocks(uint32_t blocks, uint32_t tmem, uint32_t smem_base, uint64_t* full, uint64_t* empty,
+                                             uint64_t* acc_full, uint64_t* acc_empty, const volatile int* abort_flag) {
+    const uint32_t idesc = ptx::idesc_dense(true, true, true, 256, 256), leader = ptx::elect_one();
+    const uint64_t a0 = ptx::sdesc_k128(smem_base), b0 = ptx::sdesc_k128(smem_base + kStageA);
+    uint32_t s = 0, filled = 0;   // stage, and the parity of its fill
+    bool ready = false;
+#pragma unroll 1
+    for (uint32_t f = 0; f < blocks; ++f) {
+        const uint32_t turn = f & 1;
+        bool ok = ready || ptx::mbar_wait(&full[s], filled, abort_flag);
+        if (f >= 2) ok = ok && ptx::mbar_wait(&acc_empty[turn], ((f >> 1) - 1) & 1, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+        ptx::tc_fence_after();
+        const uint32_t off = s * (kStage >> 4);
+        ptx::mma_pair_k128_e4m3_if(leader, tmem + turn * 256, a0 + off, b0 + off, idesc);
+        ptx::mma_commit_pair_if(leader, &acc_full[turn]);
+        ptx::mma_commit_pair_if(leader, &empty[s]);
+        if (++s == kStages) {
+            s = 0;
+            filled ^= 1;
+        }
+        ready = ptx::mbar_test_wait(&full[s], filled);
+    }
+    return true;
+}
+
+// The k-th tile of this pair of CTAs, WIDTH columns wide; false past its last one.
 template <int WIDTH>
 __device__ __forceinline__ bool find_tile(const BlockArgs& p, const int32_t* table, int32_t k, Tile& t) {
     const int32_t stride = (p.runs.count + kTableSize - 1) / kTableSize, slots = (p.runs.count + stride - 1) / stride;
     const int32_t tiles_n = (p.h + WIDTH - 1) / WIDTH;
-    const int64_t all = static_cast<int64_t>(table[slots]) * tiles_n;   // (below 2^31 where the borders are in order)
     const int64_t next = (blockIdx.x >> 1) + static_cast<int64_t>(k) * (gridDim.x >> 1);
-    if (next >= (all < 0x7FFFFFFF ? all : 0x7FFFFFFF)) return false;
+    if (next >= tiles_of<WIDTH>(p, table)) return false;
     const int32_t u = static_cast<int32_t>(next);
     const int32_t mt = u / tiles_n;   // (only which expert: its tiles are in an order of their own)
     int32_t a = 0, b = slots;         // table[a] <= mt < table[b]
@@ -172,7 +214,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
     const uint32_t raw = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
     uint8_t* staging = smem + S * kStage;
-    uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging);   // [S]  (CTA 0's are used)
+    float* scales = reinterpret_cast<float*>(staging + kEpiWarps * kStaging);
+    int4* tiles = reinterpret_cast<int4*>(scales + kScaleSlots * 256);   // [kEpiWarps]
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging + kScaleBytes);   // [S]  (CTA 0's are used)
     uint64_t* empty = full + S;             // [S]
     uint64_t* acc_full = empty + S;         // [2]
     uint64_t* acc_empty = acc_full + 2;     // [2]  (CTA 0's are used)
@@ -180,9 +224,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
     uint64_t* shared_max = exit_bar + 1;    // [4]  the two warps that share a block of a gated e4m3 output's columns
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shared_max + 4);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int32_t* table = reinterpret_cast<int32_t*>(staging + kEpiWarps * kStaging + 256);   // row tiles before every `stride`-th expert
+    int32_t* table = reinterpret_cast<int32_t*>(staging + kEpiWarps * kStaging + kScaleBytes + 256);   // row tiles before every `stride`-th expert
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -190,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
             ptx::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            ptx::mbar_init(&acc_full[b], 1);
+            ptx::mbar_init(&acc_full[b], 2);    // the MMAs and the scales
             ptx::mbar_init(&acc_empty[b], 2 * kEpiWarps);
         }
         ptx::mbar_init(exit_bar, 1);
@@ -233,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
     ptx::cluster_sync();
     ptx::tc_fence_after();
     pdl_trigger();   // (once TMEM is allocated: the next kernel's blocks may want theirs on this SM)
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, *tmem_slot);   // (uniform)
     const uint32_t smem_base = ptx::smem_u32(smem);
     constexpr int kTileN = DUAL ? 128 : 256;
 
@@ -274,191 +318,264 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
-            const uint32_t leader = lane == 0;
-            const uint32_t idesc = ptx::idesc_dense(true, true, true, 256, 256);
-            const uint64_t a0 = ptx::sdesc_k128(smem_base), b0 = ptx::sdesc_k128(smem_base + kStageA);
-            uint32_t f = 0;
-            bool ok = true;
-            Tile t;
-            for (int32_t q = 0; ok && tile_at(q, t); ++q) {
-#pragma unroll 1
-                for (int32_t it = 0; it < p.kb; ++it, ++f) {
-                    const uint32_t s = f % S, buf = f & 1;
-                    if ((f >= 2 && !warp_wait(&acc_empty[buf], ((f >> 1) - 1) & 1)) || !warp_wait(&full[s], (f / S) & 1)) {
-                        if (lane == 0) fail();
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                    const uint64_t off = static_cast<uint64_t>((s * kStage) >> 4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        ptx::mma_pair_if<true>(leader, tmem + buf * 256, a0 + off + 2 * j, b0 + off + 2 * j, idesc, j > 0 ? 1u : 0u);
-                    ptx::mma_commit_pair_if(leader, &empty[s]);
-                    ptx::mma_commit_pair_if(leader, &acc_full[buf]);
-                }
-            }
-            ptx::mma_commit_pair_if(leader, exit_bar);
+            const int64_t all = tiles_of<kTileN>(p, table), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+            const uint32_t blocks = static_cast<uint32_t>(all > pair ? (all - pair + pairs - 1) / pairs : 0) * static_cast<uint32_t>(p.kb);
+            const bool ok = issue_blocks(__reduce_max_sync(0xFFFFFFFFu, blocks), tmem, smem_base, full, empty, acc_full, acc_empty, abort_flag);
+            if (!ok && lane == 0) fail();
+            ptx::mma_commit_pair_if(ptx::elect_one(), exit_bar);   // (the lane that issued)
             const bool done = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(exit_bar, 0, nullptr));
             if (!done && lane == 0) atomicOr(p.status, kStatusTimeout);
+        }
+    } else if (warp == 3) {
+        // The products of the two scales, four rows a lane: read two to four blocks
+        // before they are used, written once the accumulator's last turn is over
+        // (which means that the turn before it, whose slot this is, has been added up).
+        uint32_t f = 0;
+        bool ok = true;
+        Tile t;
+        for (int32_t q = 0; ok && tile_at(q, t); ++q) {
+            const int32_t row = t.row + static_cast<int32_t>(rank) * 128 + lane;
+            const float* xs = p.x_scale + row;
+            // (columns past the last block are not stored: any scale serves)
+            const int32_t wi0 = (t.e * p.hb + (DUAL ? t.tn : t.tn * 2)) * p.kb;
+            const int32_t wi1 = DUAL ? wi0 : (t.e * p.hb + min(t.tn * 2 + 1, p.hb - 1)) * p.kb;
+            const float* ws1 = DUAL ? p.w_scale[1] : p.w_scale[0];
+            constexpr int G = 2;
+            float x[2][G][4], w0 = 0.0f, w1 = 0.0f;   // [group of blocks][block][quarter]
+            auto load = [&](float (&v)[G][4], int32_t it0) {
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[j][r] = it0 + j < p.kb && row + 32 * r < t.end ? __ldg(xs + static_cast<int64_t>(it0 + j) * p.runs.n + 32 * r) : 0.0f;
+            };
+            load(x[0], 0);
+#pragma unroll 1
+            for (int32_t it0 = 0; ok && it0 < p.kb; it0 += 2 * G) {
+                if ((it0 & 31) == 0) {   // one block's in each lane
+                    w0 = it0 + lane < p.kb ? __ldg(p.w_scale[0] + wi0 + it0 + lane) : 0.0f;
+                    w1 = it0 + lane < p.kb ? __ldg(ws1 + wi1 + it0 + lane) : 0.0f;
+                }
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    load(x[g ^ 1], it0 + G * g + G);
+#pragma unroll
+                    for (int j = 0; j < G; ++j) {
+                        const int32_t it = it0 + G * g + j;
+                        if (!ok || it >= p.kb) continue;
+                        const float a = __shfl_sync(0xFFFFFFFFu, w0, it & 31), b = __shfl_sync(0xFFFFFFFFu, w1, it & 31);
+                        if (f >= 2 && !warp_wait(&acc_full[f & 1], ((f >> 1) - 1) & 1)) {
+                            if (lane == 0) fail();
+                            ok = false;
+                            continue;
+                        }
+                        float* slot = scales + (f % kScaleSlots) * 256 + lane;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            slot[32 * r] = x[g][j][r] * a;
+                            slot[128 + 32 * r] = x[g][j][r] * b;
+                        }
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&acc_full[f & 1]);
+                        ++f;
+                    }
+                }
+            }
         }
     } else if (warp >= kFirstEpi) {
         ptx::regs_inc<kRegsEpi>();
         const int e = warp - kFirstEpi;
         const int quarter = warp & 3, part = e >> 2;   // TMEM lanes; half of the columns
         uint8_t* stage0 = staging + e * kStaging;
+        volatile int4* tile = reinterpret_cast<volatile int4*>(tiles) + e;
         const uint32_t acc_bar = ptx::map_to_rank(ptx::smem_u32(&acc_empty[0]), 0);
-        // accumulator columns of each 16: 128 next to each other, or 64 of gate and 64 of up
+        // accumulator columns of each 32: 128 next to each other, or 64 of gate and 64 of up
         const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        auto column = [&](int c) { return DUAL ? (c < 4 ? part * 64 + c * 16 : 128 + part * 64 + (c - 4) * 16) : part * 128 + c * 16; };
+        auto column = [&](int c) { return DUAL ? (c < 2 ? part * 64 + c * 32 : 128 + part * 64 + (c - 2) * 32) : part * 128 + c * 32; };
         uint32_t f = 0;
         bool ok = true;
         Tile t;
         for (int32_t q = 0; ok && tile_at(q, t); ++q) {
-            const int32_t m0 = t.row + static_cast<int32_t>(rank) * 128 + quarter * 32, row = m0 + lane;
-            const int32_t n0 = t.tn * kTileN + part * kOut;   // first output column
-            const bool live = row < t.end;
-            const float* xs = p.x_scale + (live ? row : 0);   // (other rows' sums are not used)
-            // (columns past the last block are not stored: any scale serves)
-            const int32_t block = DUAL ? t.tn : min(t.tn * 2 + part, p.hb - 1);
-            int32_t wi = (t.e * p.hb + block) * p.kb;
+            // (the tile waits in shared memory: the loop has no registers for it)
+            __syncwarp();
+            if (lane == 0) tile->x = t.e, tile->y = t.row, tile->z = t.end, tile->w = t.tn;
+            __syncwarp();
             F2 acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = F2(0.0f);
-            float x_next = __ldg(xs);
+            bool ready = false;
+            // What can is done while TMEM's loads or the multiply-adds run: a warp has about 600
+            // clocks a block for all of it, and only one other warp to share them with.
 #pragma unroll 1
-            for (int32_t it = 0; it < p.kb; ++it, ++f, ++wi) {
+            for (int32_t it = 0; it < p.kb; ++it, ++f) {
                 const uint32_t buf = f & 1;
-                const F2 s0(x_next * __ldg(p.w_scale[0] + wi)), s1(DUAL ? x_next * __ldg(p.w_scale[1] + wi) : 0.0f);
-                if (it + 1 < p.kb) xs += p.runs.n, x_next = __ldg(xs);
-                if (!warp_wait(&acc_full[buf], (f >> 1) & 1)) {
+                if (!ready && !ptx::mbar_wait(&acc_full[buf], (f >> 1) & 1, abort_flag)) {
                     if (lane == 0) fail();
+                    ok = false;
+                }
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                // the next 16 columns are on their way while these are added
-                uint32_t z[2][16];
-                ptx::tmem_ld_32x32b_x16(ta + buf * 256 + column(0), z[0]);
+                uint32_t z[2][32];
+                ptx::tmem_ld_32x32b_x32(ta + buf * 256 + column(0), z[0]);
+                ptx::tmem_ld_32x32b_x32(ta + buf * 256 + column(1), z[1]);
+                const volatile float* scale = scales + (f % kScaleSlots) * 256 + quarter * 32 + lane;
+                const F2 now0(scale[DUAL ? 0 : part * 128]), now1(DUAL ? scale[128] : 0.0f);
+                auto add = [&](int c) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    ptx::tmem_ld_wait_for(z[c & 1]);
-                    if (c < 7) {
-                        ptx::tmem_ld_32x32b_x16(ta + buf * 256 + column(c + 1), z[(c + 1) & 1]);
-                    } else {
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_cluster(acc_bar + buf * 8);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2)
-                        acc[(c * 16 + j) / 2] = fma_v(F2(__uint_as_float(z[c & 1][j]), __uint_as_float(z[c & 1][j + 1])),
-                                                      DUAL && c >= 4 ? s1 : s0, acc[(c * 16 + j) / 2]);
-                }
+                    for (int j = 0; j < 32; j += 2)
+                        acc[(c * 32 + j) / 2] = fma_v(F2(__uint_as_float(z[c & 1][j]), __uint_as_float(z[c & 1][j + 1])),
+                                                      DUAL && c >= 2 ? now1 : now0, acc[(c * 32 + j) / 2]);
+                };
+                ptx::tmem_ld_wait_for(z[0]);
+                ptx::tmem_ld_wait_for(z[1]);
+                add(0);
+                ptx::tmem_ld_32x32b_x32(ta + buf * 256 + column(2), z[0]);
+                add(1);
+                ptx::tmem_ld_32x32b_x32(ta + buf * 256 + column(3), z[1]);
+                ptx::tmem_ld_wait_for(z[0]);
+                ptx::tmem_ld_wait_for(z[1]);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(acc_bar + buf * 8);
+                ready = ptx::mbar_test_wait(&acc_full[buf ^ 1], ((f + 1) >> 1) & 1);
+                add(2);
+                add(3);
             }
             if (!ok) break;
-            const int32_t rows = t.end - m0 < 32 ? t.end - m0 : 32, left = p.h - n0;   // (either may be negative)
-            // two columns at a time; the results take the places of the sums
-            if (!DUAL && p.bias && left > 0) {
-                const float* bias = p.bias + static_cast<int64_t>(t.e) * p.h + n0;
+            const int32_t expert = tile->x, end = tile->z;
+            const int32_t m0 = tile->y + static_cast<int32_t>(ptx::cluster_rank()) * 128 + quarter * 32, row = m0 + lane;
+            const int32_t n0 = tile->w * kTileN + part * kOut;   // first output column
+            const int32_t rows = end - m0 < 32 ? end - m0 : 32, left = p.h - n0;   // (either may be negative)
+            const bool live = row < end;
+            // Bias and activation, 16 columns at a time, moved to where one copy of the code finds
+            // them: unrolled over all of them it needs more registers than there are.  The bias
+            // lies in the staging buffer meanwhile.
+            if (DUAL || p.act != SPCONV_ACT_NONE || p.bias) {
+                if (!DUAL) {
+                    if (lane == 0) ptx::bulk_wait_read();
+                    __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float b = c * 32 + lane < left ? __ldg(bias + c * 32 + lane) : 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        acc[c * 16 + j] = acc[c * 16 + j] + F2(__shfl_sync(0xFFFFFFFFu, b, 2 * j), __shfl_sync(0xFFFFFFFFu, b, 2 * j + 1));
+                    for (int c = 0; c < 4; ++c)
+                        reinterpret_cast<float*>(stage0)[c * 32 + lane] =
+                            p.bias && c * 32 + lane < left ? __ldg(p.bias + static_cast<int64_t>(expert) * p.h + n0 + c * 32 + lane) : 0.0f;
+                    __syncwarp();
                 }
-            }
-            // (32 columns at a time, moved to where one copy of the code finds them: unrolled over all
-            // of them it needs more registers than there are)
-            if (DUAL || p.act != SPCONV_ACT_NONE) {
 #pragma unroll 1
-                for (int c = 0; c < kOut / 32; ++c) {
-                    F2 v[16], u[16];
+                for (int c = 0; c < kOut / 16; ++c) {
+                    F2 v[8], u[8];
 #pragma unroll
-                    for (int k = 0; k < kOut / 32; ++k)
+                    for (int k = 0; k < kOut / 16; ++k)
                         if (c == k) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                v[j] = acc[k * 16 + j];
-                                if (DUAL) u[j] = acc[(k * 16 + j + 32) % 64];
+                            for (int j = 0; j < 8; ++j) {
+                                v[j] = acc[k * 8 + j];
+                                if (DUAL) u[j] = acc[(k * 8 + j + 32) % 64];
                             }
                         }
+                    if (!DUAL) {
+                        const float4* bias = reinterpret_cast<const float4*>(stage0 + c * 64);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 b = bias[j];
+                            v[2 * j] = v[2 * j] + F2(b.x, b.y);
+                            v[2 * j + 1] = v[2 * j + 1] + F2(b.z, b.w);
+                        }
+                    }
                     with_act(p.act, [&](auto act) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = DUAL ? act_f<act>(v[j]) * u[j] : act_f<act>(v[j]);
+                        for (int j = 0; j < 8; ++j) v[j] = DUAL ? act_f<act>(v[j]) * u[j] : act_f<act>(v[j]);
                     });
 #pragma unroll
-                    for (int k = 0; k < kOut / 32; ++k)
+                    for (int k = 0; k < kOut / 16; ++k)
                         if (c == k) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) acc[k * 16 + j] = v[j];
+                            for (int j = 0; j < 8; ++j) acc[k * 8 + j] = v[j];
                         }
-                }
-            }
-            if (!EIGHT) {
-                // rows of kOut bf16 through shared memory, in 16-byte pieces whose places are
-                // turned by the row, so that neither side meets in a bank
-                constexpr int kPieces = kOut / 8, kRows = 32 / kPieces;
-                auto place = [](int r, int piece) { return r * (kOut * 2) + ((piece ^ (r & 7)) << 4); };
-                if (!DUAL && p.extra) {
-#pragma unroll 4
-                    for (int r = 0; r < 32; r += kRows) {
-                        const int i = r + lane / kPieces, c8 = lane % kPieces;   // row; eight columns
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (i < rows && c8 * 8 < left) {
-                            const __nv_bfloat16* x = p.extra + (m0 + i) * p.ld_extra + n0 + c8 * 8;
-                            if (p.vec_extra && c8 * 8 + 8 <= left) {
-                                v = *reinterpret_cast<const uint4*>(x);
-                            } else {
-                                uint32_t u[4] = {};
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    if (c8 * 8 + j < left) u[j / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x[j])) << (16 * (j & 1));
-                                v = make_uint4(u[0], u[1], u[2], u[3]);
-                            }
-                        }
-                        *reinterpret_cast<uint4*>(stage0 + place(i, c8)) = v;
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int c8 = 0; c8 < kPieces; ++c8) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(stage0 + place(lane, c8));
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[c8 * 4 + j] = acc[c8 * 4 + j] + F2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xFFFF0000u));
-                    }
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int c8 = 0; c8 < kPieces; ++c8) {
-                    uint32_t u[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float a, b;
-                        acc[c8 * 4 + j].get(a, b);
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-                        u[j] = reinterpret_cast<const uint32_t&>(v);
-                    }
-                    *reinterpret_cast<uint4*>(stage0 + place(lane, c8)) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
                 __syncwarp();
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-#pragma unroll 4
-                for (int r = 0; r < 32; r += kRows) {
-                    const int i = r + lane / kPieces, c8 = lane % kPieces;
-                    if (i >= rows || c8 * 8 >= left) continue;
-                    const uint4 v = *reinterpret_cast<const uint4*>(stage0 + place(i, c8));
-                    __nv_bfloat16* o = out + (m0 + i) * p.ld_out + n0 + c8 * 8;
-                    if (p.vec_out && c8 * 8 + 8 <= left) {
-                        *reinterpret_cast<uint4*>(o) = v;
-                    } else {
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            }
+            // Whole groups of 32 rows leave by tensor-map copies, which nobody waits for; a run's
+            // last ones, which a copy would not clip, and unaligned outputs by plain stores.
+            const bool mapped = p.map_out && rows == 32;
+            if (!EIGHT) {
+                // 32 columns at a time, two staging buffers in turn: rows of 64 bytes in 16-byte
+                // pieces whose places are turned by the row (the copies' 64-byte swizzle)
+                auto place = [](int r, int piece) { return r * 64 + ((piece ^ ((r >> 1) & 3)) << 4); };
+                const int i0 = lane >> 2, c8 = lane & 3;   // of eight rows at a time: row; eight columns
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (c8 * 8 + j < left) o[j] = __ushort_as_bfloat16(static_cast<uint16_t>(u[j / 2] >> (16 * (j & 1))));
+                for (int c = 0; c < kOut / 32; ++c) {
+                    const int32_t cols = left - 32 * c;    // (may be negative)
+                    uint8_t* stage = stage0 + (c & 1) * 2048;
+                    if (lane == 0) ptx::bulk_wait_read_but<1>();   // (the other buffer's copy may still run)
+                    __syncwarp();
+                    if (!DUAL && p.extra) {
+#pragma unroll
+                        for (int r = 0; r < 32; r += 8) {
+                            const int i = r + i0;
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (i < rows && c8 * 8 < cols) {
+                                const __nv_bfloat16* x = p.extra + (m0 + i) * p.ld_extra + n0 + c * 32 + c8 * 8;
+                                if (p.vec_extra && c8 * 8 + 8 <= cols) {
+                                    v = *reinterpret_cast<const uint4*>(x);
+                                } else {
+                                    uint32_t u[4] = {};
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j)
+                                        if (c8 * 8 + j < cols) u[j / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x[j])) << (16 * (j & 1));
+                                    v = make_uint4(u[0], u[1], u[2], u[3]);
+                                }
+                            }
+                            *reinterpret_cast<uint4*>(stage + place(i, c8)) = v;
+                        }
+                        __syncwarp();
                     }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint4* at = reinterpret_cast<uint4*>(stage + place(lane, k));
+                        if (!DUAL && p.extra) {
+                            const uint4 v = *at;
+                            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                acc[c * 16 + k * 4 + j] = acc[c * 16 + k * 4 + j] + F2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xFFFF0000u));
+                        }
+                        uint32_t u[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float a, b;
+                            acc[c * 16 + k * 4 + j].get(a, b);
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+                            u[j] = reinterpret_cast<const uint32_t&>(v);
+                        }
+                        *at = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                    if (mapped) ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (mapped) {
+                        if (lane == 0 && cols > 0) ptx::tma_store_2d(&p.c, n0 + c * 32, m0, ptx::smem_u32(stage));
+                    } else {
+                        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + n0 + c * 32 + c8 * 8;
+#pragma unroll
+                        for (int r = 0; r < 32; r += 8) {
+                            const int i = r + i0;
+                            if (i >= rows || c8 * 8 >= cols) continue;
+                            const uint4 v = *reinterpret_cast<const uint4*>(stage + place(i, c8));
+                            __nv_bfloat16* o = out + (m0 + i) * p.ld_out;
+                            if (p.vec_out && c8 * 8 + 8 <= cols) {
+                                *reinterpret_cast<uint4*>(o) = v;
+                            } else {
+                                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    if (c8 * 8 + j < cols) o[j] = __ushort_as_bfloat16(static_cast<uint16_t>(u[j / 2] >> (16 * (j & 1))));
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) ptx::bulk_commit();
                 }
             } else {
                 // the largest of the row's 128 columns: this warp's, or its half and another warp's
@@ -474,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                     // (behind the staged output, by the tiles' parity: a slot is written again two tiles
                     // later, when both have passed the barrier of the tile between)
                     uint64_t* bar = &shared_max[quarter];
-                    const uint32_t slot = 4096 + (q & 1) * 128 + lane * 4;
+                    const uint32_t slot = 2048 + (q & 1) * 128 + lane * 4;
                     *reinterpret_cast<volatile uint32_t*>(stage0 + slot) = most;
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(bar);
@@ -487,6 +604,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                 }
                 const ToE4m3 to(__uint_as_float(most));
                 if ((!DUAL || part == 0) && live && left > 0) p.scale[static_cast<int64_t>(n0 / 128) * p.runs.n + row] = to.scale;
+                if (lane == 0) ptx::bulk_wait_read();
+                __syncwarp();
                 constexpr int kPieces = kOut / 16, kRows = 32 / kPieces;   // 16-byte pieces of a row
                 auto place = [](int r, int piece) { return r * kOut + ((piece ^ (kPieces == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
 #pragma unroll
@@ -502,26 +621,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                     }
                     *reinterpret_cast<uint4*>(stage0 + place(lane, c)) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
+                if (mapped) ptx::fence_proxy_async_smem();
                 __syncwarp();
-                uint8_t* out = static_cast<uint8_t*>(p.out);
+                if (mapped) {
+                    if (lane == 0 && left > 0) ptx::tma_store_2d(&p.c, n0, m0, ptx::smem_u32(stage0));
+                    if (lane == 0) ptx::bulk_commit();
+                } else {
+                    uint8_t* out = static_cast<uint8_t*>(p.out);
 #pragma unroll 4
-                for (int r = 0; r < 32; r += kRows) {
-                    const int i = r + lane / kPieces, c = lane % kPieces;
-                    if (i >= rows || c * 16 >= left) continue;
-                    const uint4 v = *reinterpret_cast<const uint4*>(stage0 + place(i, c));
-                    uint8_t* o = out + (m0 + i) * p.ld_out + n0 + c * 16;
-                    if (p.vec_out && c * 16 + 16 <= left) {
-                        *reinterpret_cast<uint4*>(o) = v;
-                    } else {
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                    for (int r = 0; r < 32; r += kRows) {
+                        const int i = r + lane / kPieces, c = lane % kPieces;
+                        if (i >= rows || c * 16 >= left) continue;
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage0 + place(i, c));
+                        uint8_t* o = out + (m0 + i) * p.ld_out + n0 + c * 16;
+                        if (p.vec_out && c * 16 + 16 <= left) {
+                            *reinterpret_cast<uint4*>(o) = v;
+                        } else {
+                            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c * 16 + j < left) o[j] = static_cast<uint8_t>(u[j / 4] >> (8 * (j % 4)));
+                            for (int j = 0; j < 16; ++j)
+                                if (c * 16 + j < left) o[j] = static_cast<uint8_t>(u[j / 4] >> (8 * (j % 4)));
+                        }
                     }
                 }
             }
             __syncwarp();
         }
+        if (lane == 0) ptx::bulk_wait();
+        __syncwarp();
         zero_rest<EIGHT>(p, static_cast<int64_t>(blockIdx.x) * (32 * kEpiWarps) + threadIdx.x - 32 * kFirstEpi, static_cast<int64_t>(gridDim.x) * (32 * kEpiWarps));
     }
     // (as in dense_tc.cu: neither CTA leaves, or frees TMEM, while the other may still signal it)
@@ -879,6 +1006,9 @@ int run(const BlockOp& op, cudaStream_t s) {
                                                                              : run_few<DUAL, EIGHT, 64>(op, p, active, s);
     }
     SPCONV_CHECK(make_maps(op, x, ldx, 128, &p));
+    p.map_out = p.vec_out && op.h % (EIGHT ? 16 : 8) == 0;
+    if (p.map_out)
+        SPCONV_CHECK(make_tensor_map(&p.c, op.out, EIGHT ? 1 : 2, op.h, op.n, op.ld_out, 32, EIGHT && !DUAL ? 128 : 64));
     return run_tc<DUAL, EIGHT>(op, p, s);
 }
 

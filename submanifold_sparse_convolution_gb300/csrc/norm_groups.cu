@@ -13,20 +13,74 @@
 // are cut without looking at them, and a block walks the pieces of the scans
 // that it meets.  The piece of scan s in block b has the number b + s, which no
 // other piece has (along the rows both only grow, one of them strictly), and a
-// scan's pieces have consecutive ones.  The second kernel's blocks add up the
-// pieces of their scans in that order: no atomics, the same bits every run.
+// scan's pieces have consecutive ones.  They are added up in that order: no
+// atomics, the same bits every run.
 //
-// Bound by HBM, and for small inputs by the chain of latencies (two launches,
-// the loads, the pieces).
+// Up to kSmallBytes there is one block per SM at most, the second kernel's blocks
+// add up the pieces of their scans themselves, and they load their first rows
+// while the first kernel ends.  Beyond, blocks have kBlockBytes each, a small
+// kernel between the two adds the pieces up, and the second takes the blocks
+// from the last to the first: L2 still has the rows that were read last.
+//
+// Scans of at most kScanBytes on the average are taken whole by a cluster of up
+// to eight CTAs, which keep the rows in registers and exchange their sums through
+// distributed shared memory: one launch, the rows read once.
+//
+#include "ptx_sm100.cuh"
 #include "row_vectors.cuh"
 
 namespace spconv {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kMaxPieces = 160;          // blocks that a warp adds up: five pieces a lane
-constexpr int kPerLane = kMaxPieces / 32;
-constexpr int kStatThreads = 1024, kApplyThreads = 640, kBwdThreads = 512;   // (registers)
+constexpr int kPerLane = 5;              // pieces that a lane adds up where a block does so for itself
+static_assert(kSms <= 32 * kPerLane, "blocks of a small input");
+constexpr int kThreads = 512;            // blocks of a small input; half of it for those of a large one
+constexpr int kApplyThreads = 384;       // (80 registers a thread, and room on an SM beside a block of k_group_stats)
+constexpr int64_t kSmallBytes = 16 << 20, kBlockBytes = 256 << 10;
+constexpr int64_t kScanBytes = 512 << 10;
+constexpr int kMaxCluster = 8;           // portable cluster size
+
+// W values in fp32, two in a register pair where there are two: the packed
+// instructions do both in one issue.
+template <int W>
+struct Values {
+    using V = std::conditional_t<W == 1, float, F2>;
+    static constexpr int n = W == 1 ? 1 : W / 2;
+    V v[n];
+    __device__ __forceinline__ void set(float x) {
+#pragma unroll
+        for (int j = 0; j < n; ++j) v[j] = V(x);
+    }
+    __device__ __forceinline__ void put(const float (&f)[W]) {
+        if constexpr (W == 1) {
+            v[0] = f[0];
+        } else {
+#pragma unroll
+            for (int j = 0; j < n; ++j) v[j] = F2(f[2 * j], f[2 * j + 1]);
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[W]) const {
+        if constexpr (W == 1) {
+            f[0] = v[0];
+        } else {
+#pragma unroll
+            for (int j = 0; j < n; ++j) v[j].get(f[2 * j], f[2 * j + 1]);
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void unpack(const Pack<T, W>& p) {
+        float f[W];
+        spconv::unpack<W>(p, f);
+        put(f);
+    }
+    template <typename T>
+    __device__ __forceinline__ void pack(Pack<T, W>& p) const {
+        float f[W];
+        get(f);
+        spconv::pack<W>(f, p);
+    }
+};
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -76,13 +130,22 @@ struct Shape {
     int32_t c, groups, width;      // width: channels of a group
     int32_t vectors, tx, ty;       // vectors of a row; threads across and down
     int32_t rows;                  // of a block (R)
-    int32_t joined;                // channels of a group that a thread of k_group_stats joins: a power of two
+    int32_t blocks;
+    int32_t shift;                 // 2^shift channels of a group lie in a vector and are joined by a thread
     int64_t slots;                 // blocks + scans
 };
 
 // Where piece sums lie: [groups][slots], so that a warp reads a group's run.
 __device__ __forceinline__ int64_t slot_of(const Shape& h, int32_t group, int32_t scan) {
     return group * h.slots + static_cast<int32_t>(blockIdx.x) + scan;
+}
+
+// U vectors, `step` rows apart from row r on, those before `end`.
+template <typename P, typename T, int U>
+__device__ __forceinline__ void load_rows(P (&q)[U], const T* at, int64_t ld, int32_t r, int32_t step, int32_t end) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (r + u * step < end) q[u] = *reinterpret_cast<const P*>(at + (r + u * step) * ld);
 }
 
 // This lane's share of a scan's pieces of one group, in order, and how many
@@ -106,213 +169,475 @@ struct PieceSet {
     }
 };
 
+// Rows of no scan, by the block.
+template <typename P>
+__device__ __forceinline__ void zero_rows(const Shape& h, void* out, int32_t lo, int32_t hi) {
+    const P zero = {};
+    for (int64_t i = static_cast<int64_t>(lo) * h.vectors + threadIdx.x; i < static_cast<int64_t>(hi) * h.vectors; i += blockDim.x)
+        static_cast<P*>(out)[i] = zero;
+}
+
+// The group of channel v W + j, given that of the channel before it.
+template <int W>
+__device__ __forceinline__ int32_t group_of(const Shape& h, int32_t v, int j, int32_t before) {
+    if (j & ((1 << h.shift) - 1)) return before;
+    const int32_t e = (v * W + j) >> h.shift, wide = h.width >> h.shift;
+    return wide == 1 ? e : e / wide;
+}
+
 // ---- forward ------------------------------------------------------------------
 struct NormPass {
     GroupNormArgs a;
     Shape h;
     Scans scans;
     float2* part;        // of each piece: mean, sum of squares about it
+    const float2* stats; // [scans][groups], or null: the second kernel adds up the pieces
     int32_t* status;
 };
 
-// Statistics of the block's pieces.  A thread's sums are about its first value
-// of the channel, so a mean far from zero costs no digits; it joins its channels
-// of a group, and a warp the threads' about the group's mean, in two passes over
-// shared memory.
+// A thread's sums of its channels, about its first value of each, so that a mean
+// far from zero costs no digits.
+template <int W>
+struct Moments {
+    Values<W> first, sum, sq;
+    template <typename P>
+    __device__ __forceinline__ void begin(const P& q) {
+        float f[W];
+        first.unpack(q);
+        first.get(f);
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[j] = -f[j];
+        first.put(f);   // (negated: it is added)
+        sum.set(0.0f);
+        sq.set(0.0f);
+    }
+    template <typename P>
+    __device__ __forceinline__ void add(const P& q) {
+        Values<W> x;
+        x.unpack(q);
+#pragma unroll
+        for (int j = 0; j < Values<W>::n; ++j) {
+            const auto d = x.v[j] + first.v[j];
+            sum.v[j] = sum.v[j] + d;
+            sq.v[j] = fma_v(d, d, sq.v[j]);
+        }
+    }
+    // n rows: joins the channels of a group that lie in the vector, and writes mean and
+    // sum of squares about it of each, from entry `at` on
+    __device__ __forceinline__ void write(float n, int shift, float* sh_mean, float* sh_m2, int32_t at) const {
+        float mean[W], m2[W], s[W], q[W];
+        const float by_n = 1.0f / n;
+        first.get(mean);
+        sum.get(s);
+        sq.get(q);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const float m = s[j] * by_n;   // of x - first
+            mean[j] = m - mean[j];
+            const float v = fmaf(-m, s[j], q[j]);
+            m2[j] = v < 0.0f ? 0.0f : v;   // (keeps NaN)
+        }
+#pragma unroll
+        for (int l = 0; (1 << l) < W; ++l)
+            if (shift > l) {
+#pragma unroll
+                for (int j = 0; j < W; j += 2 << l) {
+                    const float d = mean[j + (1 << l)] - mean[j];
+                    mean[j] = fmaf(0.5f, d, mean[j]);
+                    m2[j] += fmaf(0.5f * n * static_cast<float>(1 << l) * d, d, m2[j + (1 << l)]);
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if ((j & ((1 << shift) - 1)) == 0) {
+                sh_mean[at + (j >> shift)] = mean[j];
+                sh_m2[at + (j >> shift)] = m2[j];
+            }
+    }
+};
+
+// Rows of the block's threads: each of the first `extra` of `ty` has one more.
+struct Deal {
+    int32_t rows, each, extra, deep;
+    __device__ __forceinline__ Deal(int32_t rows_, int32_t ty) : rows(rows_), each(rows_ / ty), extra(rows_ - each * ty), deep(rows_ < ty ? rows_ : ty) {}
+    __device__ __forceinline__ int32_t of(int32_t t) const { return each + (t < extra); }
+};
+
+// What the threads wrote, joined about each group's mean in two passes over shared
+// memory, a warp a group: f(group, mean, sum of squares) by all its lanes.
+template <typename F>
+__device__ __forceinline__ void join_threads(const Shape& h, const Deal& deal, const float* sh_mean, const float* sh_m2, F&& f) {
+    const int lane = threadIdx.x & 31;
+    const int32_t entries = h.c >> h.shift, wide = h.width >> h.shift;
+    const float by_count = 1.0f / (static_cast<float>(deal.rows) * static_cast<float>(h.width)), joined = static_cast<float>(1 << h.shift);
+    // lanes across a group's entries, and down the thread rows where those are few
+    const int32_t down = wide < 32 ? 32 / wide : 1;
+    const int32_t t0 = wide < 32 ? lane / wide : 0, k0 = wide < 32 ? lane - t0 * wide : lane;
+    for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
+        const float base = sh_mean[g * wide];
+        float sum = 0.0f, m2 = 0.0f;
+        auto entries_of = [&](auto&& each) {
+            if (t0 >= down) return;
+            for (int32_t t = t0; t < deal.deep; t += down) {
+                const float n = static_cast<float>(deal.of(t)) * joined;
+                for (int32_t k = k0; k < wide; k += 32) each(t * entries + g * wide + k, n);
+            }
+        };
+        entries_of([&](int32_t i, float n) { sum = fmaf(n, sh_mean[i] - base, sum); });
+        const float mean = base + warp_sum(sum) * by_count;
+        entries_of([&](int32_t i, float n) {
+            const float d = sh_mean[i] - mean;
+            m2 += fmaf(n * d, d, sh_m2[i]);
+        });
+        f(g, mean, warp_sum(m2));
+    }
+}
+
+// act(norm) of one vector
+template <int W>
+struct Affine {
+    Values<W> mean, scale, bias;   // (mean negated)
+    __device__ __forceinline__ void load(const NormPass& p, const float2* stats, int32_t v) {
+        float m[W], s[W], b[W];
+        int32_t g = 0;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            g = group_of<W>(p.h, v, j, g);
+            const float2 st = stats[g];
+            m[j] = -st.x;
+            s[j] = st.y * __ldg(p.a.weight + v * W + j);
+            b[j] = p.a.bias ? __ldg(p.a.bias + v * W + j) : 0.0f;
+        }
+        mean.put(m);
+        scale.put(s);
+        bias.put(b);
+    }
+    template <int ACT, typename P>
+    __device__ __forceinline__ P apply(const P& q) const {
+        Values<W> x;
+        x.unpack(q);
+#pragma unroll
+        for (int j = 0; j < Values<W>::n; ++j) x.v[j] = act_f<ACT>(fma_v(x.v[j] + mean.v[j], scale.v[j], bias.v[j]));
+        P o;
+        x.pack(o);
+        return o;
+    }
+};
+
+// Statistics of the block's pieces.
 template <typename T, int W>
-__global__ void __launch_bounds__(kStatThreads, 1) k_group_stats(const __grid_constant__ NormPass p) {
+__global__ void __launch_bounds__(kThreads, 2) k_group_stats(const __grid_constant__ NormPass p) {
     using P = Pack<T, W>;
+    constexpr int U = 4;
     extern __shared__ float sh[];
     const Shape& h = p.h;
-    const int32_t entries = h.c / h.joined;
+    const int32_t entries = h.c >> h.shift;
     float* sh_mean = sh;                                            // [ty][entries]
     float* sh_m2 = sh + static_cast<size_t>(h.ty) * entries;
-    const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx, lane = threadIdx.x & 31;
+    const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx;
     const int32_t row0 = static_cast<int32_t>(blockIdx.x) * h.rows;
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
+    const T* x0 = static_cast<const T*>(p.a.x);
     pdl_wait();
     pdl_trigger();
+    // the first rows are on their way while the offsets are read
+    P q[U];
+    if (ty < h.ty) load_rows(q, x0 + tx * W, p.a.ldx, row0 + ty, h.ty, row1);
     p.scans.pieces(row0, row1, [&](int32_t s, int32_t lo, int32_t hi) {
         if (s < 0 || s >= p.scans.scans) return;
-        const int32_t each = (hi - lo) / h.ty, extra = (hi - lo) % h.ty;   // rows of a thread; threads with one more
-        for (int32_t v = tx; v < h.vectors && ty < h.ty; v += h.tx) {
-            const T* x = static_cast<const T*>(p.a.x) + v * W;
-            float first[W], sum[W], sq[W];
-            int32_t r = lo + ty;
-            if (r < hi) {
-                unpack<W>(*reinterpret_cast<const P*>(x + r * p.a.ldx), first);
+        const Deal deal(hi - lo, h.ty);
+        for (int32_t v = tx; v < h.vectors && ty < deal.deep; v += h.tx) {
+            const T* x = x0 + v * W;
+            if (lo != row0 || v != tx) load_rows(q, x, p.a.ldx, lo + ty, h.ty, hi);
+            Moments<W> m;
+            m.begin(q[0]);
+            for (int32_t r = lo + ty; r < hi;) {
 #pragma unroll
-                for (int j = 0; j < W; ++j) sum[j] = sq[j] = 0.0f;
-                r += h.ty;
-                auto add = [&](const P& q) {
-                    float f[W];
-                    unpack<W>(q, f);
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        const float d = f[j] - first[j];
-                        sum[j] += d;
-                        sq[j] = fmaf(d, d, sq[j]);
-                    }
-                };
-                constexpr int U = 4;
-                for (; r + (U - 1) * h.ty < hi; r += U * h.ty) {
-                    P q[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) q[u] = *reinterpret_cast<const P*>(x + (r + u * h.ty) * p.a.ldx);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) add(q[u]);
-                }
-                for (; r < hi; r += h.ty) add(*reinterpret_cast<const P*>(x + r * p.a.ldx));
-                const float n = static_cast<float>(each + (ty < extra)), by_n = 1.0f / n;
-                float mean[W], m2[W];
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const float m = sum[j] * by_n;   // of x - first
-                    mean[j] = first[j] + m;
-                    const float q = fmaf(-m, sum[j], sq[j]);
-                    m2[j] = q < 0.0f ? 0.0f : q;     // (keeps NaN)
-                }
-                // neighbouring channels of a group, as many as lie in one vector
-#pragma unroll
-                for (int w = 1; w < W; w *= 2)
-                    if (h.joined > w) {
-#pragma unroll
-                        for (int j = 0; j < W; j += 2 * w) {
-                            const float d = mean[j + w] - mean[j];
-                            mean[j] = fmaf(0.5f, d, mean[j]);
-                            m2[j] += fmaf(0.5f * n * static_cast<float>(w) * d, d, m2[j + w]);
-                        }
-                    }
-                const int32_t at = ty * entries + v * W / h.joined;
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    if (j % h.joined == 0) {
-                        sh_mean[at + j / h.joined] = mean[j];
-                        sh_m2[at + j / h.joined] = m2[j];
-                    }
+                for (int u = 0; u < U; ++u)
+                    if (r + u * h.ty < hi) m.add(q[u]);
+                r += U * h.ty;
+                load_rows(q, x, p.a.ldx, r, h.ty, hi);
             }
+            m.write(static_cast<float>(deal.of(ty)), h.shift, sh_mean, sh_m2, ty * entries + ((v * W) >> h.shift));
         }
         __syncthreads();
-        const int32_t deep = hi - lo < h.ty ? hi - lo : h.ty;   // thread rows that have any
-        const float by_count = 1.0f / (static_cast<float>(hi - lo) * static_cast<float>(h.width));
-        // lanes across a group's entries, and down the thread rows where those are few
-        const int32_t wide = h.width / h.joined, down = wide < 32 ? 32 / wide : 1;
-        const int32_t k0 = wide < 32 ? lane % wide : lane, t0 = wide < 32 ? lane / wide : 0;
-        for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
-            const float base = sh_mean[g * wide];
-            float sum = 0.0f, m2 = 0.0f;
-            auto entries_of = [&](auto&& f) {
-                if (t0 >= down) return;
-                for (int32_t t = t0; t < deep; t += down) {
-                    const float n = static_cast<float>((each + (t < extra)) * h.joined);
-                    for (int32_t k = k0; k < wide; k += 32) f(t * entries + g * wide + k, n);
-                }
-            };
-            entries_of([&](int32_t i, float n) { sum = fmaf(n, sh_mean[i] - base, sum); });
-            const float mean = base + warp_sum(sum) * by_count;
-            entries_of([&](int32_t i, float n) {
-                const float d = sh_mean[i] - mean;
-                m2 += fmaf(n * d, d, sh_m2[i]);
-            });
-            m2 = warp_sum(m2);
-            if (lane == 0) p.part[slot_of(h, g, s)] = make_float2(mean, m2);
-        }
+        join_threads(h, deal, sh_mean, sh_m2, [&](int32_t g, float mean, float m2) {
+            if ((threadIdx.x & 31) == 0) p.part[slot_of(h, g, s)] = make_float2(mean, m2);
+        });
         __syncthreads();
     });
 }
 
-// The rows again, last ones first: those are the ones that L2 still has where
-// the input is larger.
+// The pieces of a scan's group: mean and 1 / sqrt(var + eps) for all of the warp.
+__device__ __forceinline__ float2 join_pieces(const NormPass& p, int32_t g, int32_t s, int32_t lo, int32_t hi) {
+    const float width = static_cast<float>(p.h.width), by_count = 1.0f / (static_cast<float>(hi - lo) * width);
+    PieceSet set;
+    set.load(p.h, p.part, g, s, lo, hi);
+    const float base = __shfl_sync(0xFFFFFFFFu, set.v[0].x, 0);
+    float sum = 0.0f, m2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) sum = fmaf(set.rows[k] * width, set.rows[k] > 0.0f ? set.v[k].x - base : 0.0f, sum);
+    const float mean = base + warp_sum(sum) * by_count;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+        const float d = set.rows[k] > 0.0f ? set.v[k].x - mean : 0.0f;
+        m2 += fmaf(set.rows[k] * width * d, d, set.v[k].y);
+    }
+    return make_float2(mean, rsqrtf(warp_sum(m2) * by_count + p.a.eps));
+}
+
+// The rows again.
 template <typename T, int W>
-__global__ void __launch_bounds__(kApplyThreads, 1) k_group_apply(const __grid_constant__ NormPass p) {
+__global__ void __launch_bounds__(kApplyThreads, 2) k_group_apply(const __grid_constant__ NormPass p) {
     using P = Pack<T, W>;
-    extern __shared__ float sh[];
+    constexpr int U = 4;
+    extern __shared__ float2 sh_stats[];   // [groups]
     const Shape& h = p.h;
     const GroupNormArgs& a = p.a;
-    float* sh_mean = sh;              // [groups]
-    float* sh_r = sh + h.groups;
     const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx, lane = threadIdx.x & 31;
-    const int32_t row0 = static_cast<int32_t>(blockIdx.x) * h.rows;
+    const int32_t block = p.stats ? h.blocks - 1 - static_cast<int32_t>(blockIdx.x) : static_cast<int32_t>(blockIdx.x);
+    const int32_t row0 = block * h.rows;
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
-    pdl_wait();
-    pdl_trigger();
-    // what the scans without a row have for statistics; borders out of order or range
-    if (p.scans.offsets)
-        for (int32_t s = blockIdx.x * blockDim.x + threadIdx.x; s < p.scans.scans; s += gridDim.x * blockDim.x) {
-            const int32_t lo = p.scans.raw(s), hi = p.scans.raw(s + 1);
-            if (lo > hi || lo < 0 || hi > p.scans.n) atomicOr(p.status, kStatusRange);
-            if (a.stats && p.scans.at(s) >= p.scans.at(s + 1))
-                for (int32_t g = 0; g < h.groups; ++g)
-                    a.stats[static_cast<int64_t>(s) * h.groups + g] = make_float2(0.0f, rsqrtf(a.eps));
+    const T* x0 = static_cast<const T*>(a.x);
+    T* out = static_cast<T*>(a.out);
+    // The kernel before this one began once all before it had ended, so what the caller
+    // gave may be read already; only the pieces' sums and what is written here wait.
+    P q[U];
+    if (ty < h.ty) load_rows(q, x0 + tx * W, a.ldx, row0 + ty, h.ty, row1);
+    bool waited = false;
+    auto wait = [&]() {
+        if (!waited) {
+            pdl_wait();
+            pdl_trigger();
         }
+        waited = true;
+    };
     p.scans.pieces(row0, row1, [&](int32_t s, int32_t lo, int32_t hi) {
-        T* out = static_cast<T*>(a.out);
         if (s < 0 || s >= p.scans.scans) {
-            P zero;
-            float f[W] = {};
-            pack<W>(f, zero);
-            for (int32_t v = tx; v < h.vectors && ty < h.ty; v += h.tx)
-                for (int32_t r = lo + ty; r < hi; r += h.ty) *reinterpret_cast<P*>(out + static_cast<int64_t>(r) * h.c + v * W) = zero;
+            wait();
+            zero_rows<P>(h, out, lo, hi);
             return;
         }
         const int32_t s_lo = p.scans.at(s), s_hi = p.scans.at(s + 1);
-        const float by_count = 1.0f / (static_cast<float>(s_hi - s_lo) * static_cast<float>(h.width));
+        wait();
         __syncthreads();   // (the last piece's statistics have been read)
-        for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
-            PieceSet set;
-            set.load(h, p.part, g, s, s_lo, s_hi);
-            const float base = __shfl_sync(0xFFFFFFFFu, set.v[0].x, 0), width = static_cast<float>(h.width);
-            float sum = 0.0f, m2 = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kPerLane; ++k) sum = fmaf(set.rows[k] * width, set.rows[k] > 0.0f ? set.v[k].x - base : 0.0f, sum);
-            const float mean = base + warp_sum(sum) * by_count;
-#pragma unroll
-            for (int k = 0; k < kPerLane; ++k) {
-                const float d = set.rows[k] > 0.0f ? set.v[k].x - mean : 0.0f;
-                m2 += fmaf(set.rows[k] * width * d, d, set.v[k].y);
-            }
-            const float r = rsqrtf(warp_sum(m2) * by_count + a.eps);
-            if (lane == 0) {
-                sh_mean[g] = mean;
-                sh_r[g] = r;
-                if (a.stats && lo == s_lo) a.stats[static_cast<int64_t>(s) * h.groups + g] = make_float2(mean, r);
+        if (p.stats) {
+            for (int32_t g = threadIdx.x; g < h.groups; g += blockDim.x) sh_stats[g] = __ldcg(p.stats + static_cast<int64_t>(s) * h.groups + g);
+        } else {
+            for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
+                const float2 st = join_pieces(p, g, s, s_lo, s_hi);
+                if (lane == 0) {
+                    sh_stats[g] = st;
+                    if (a.stats && lo == s_lo) a.stats[static_cast<int64_t>(s) * h.groups + g] = st;
+                }
             }
         }
         __syncthreads();
         with_act(a.act, [&](auto act) {
             for (int32_t v = tx; v < h.vectors && ty < h.ty; v += h.tx) {
-                const T* x = static_cast<const T*>(a.x) + v * W;
-                T* y = out + v * W;
-                float mean[W], scale[W], bias[W];
+                const T* x = x0 + v * W;
+                if (lo != row0 || v != tx) load_rows(q, x, a.ldx, lo + ty, h.ty, hi);
+                Affine<W> f;
+                f.load(p, sh_stats, v);
+                for (int32_t r = lo + ty; r < hi;) {
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const int32_t ch = v * W + j, g = ch / h.width;
-                    mean[j] = sh_mean[g];
-                    scale[j] = sh_r[g] * __ldg(a.weight + ch);
-                    bias[j] = a.bias ? __ldg(a.bias + ch) : 0.0f;
+                    for (int u = 0; u < U; ++u)
+                        if (r + u * h.ty < hi) *reinterpret_cast<P*>(out + static_cast<int64_t>(r + u * h.ty) * h.c + v * W) = f.template apply<act>(q[u]);
+                    r += U * h.ty;
+                    load_rows(q, x, a.ldx, r, h.ty, hi);
                 }
-                auto one = [&](const P& q, int32_t r) {
-                    float f[W];
-                    unpack<W>(q, f);
-#pragma unroll
-                    for (int j = 0; j < W; ++j) f[j] = act_f<act>(fmaf(f[j] - mean[j], scale[j], bias[j]));
-                    P o;
-                    pack<W>(f, o);
-                    *reinterpret_cast<P*>(y + static_cast<int64_t>(r) * h.c) = o;
-                };
-                constexpr int U = 4;
-                int32_t r = hi - 1 - ty;
-                for (; r - (U - 1) * h.ty >= lo; r -= U * h.ty) {
-                    P q[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) q[u] = *reinterpret_cast<const P*>(x + (r - u * h.ty) * a.ldx);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) one(q[u], r - u * h.ty);
-                }
-                for (; r >= lo; r -= h.ty) one(*reinterpret_cast<const P*>(x + r * a.ldx), r);
             }
         });
     });
+    wait();
+    if (p.scans.offsets) {
+        // borders out of order or range; what the scans without a row have for statistics
+        for (int32_t s = blockIdx.x * blockDim.x + threadIdx.x; s < p.scans.scans; s += gridDim.x * blockDim.x) {
+            const int32_t lo = p.scans.raw(s), hi = p.scans.raw(s + 1);
+            if (lo > hi || lo < 0 || hi > p.scans.n) atomicOr(p.status, kStatusRange);
+            if (a.stats && !p.stats && p.scans.at(s) >= p.scans.at(s + 1))
+                for (int32_t g = 0; g < h.groups; ++g)
+                    a.stats[static_cast<int64_t>(s) * h.groups + g] = make_float2(0.0f, rsqrtf(a.eps));
+        }
+    }
+}
+
+// Between the two for large inputs: THREADS (32 or 256) a scan and group.
+__device__ __forceinline__ float2 sum_of(float2 v, float2* sh, int threads) {
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if (threads == 32) return v;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float2 r = sh[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        r.x += sh[i].x;
+        r.y += sh[i].y;
+    }
+    return r;
+}
+template <int THREADS>
+__global__ void __launch_bounds__(256) k_group_join(const __grid_constant__ NormPass p, float2* stats) {
+    __shared__ float2 sh[8];
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * (256 / THREADS) + threadIdx.x / THREADS;
+    pdl_wait();
+    pdl_trigger();
+    if (i >= static_cast<int64_t>(p.scans.scans) * p.h.groups) return;   // (all threads of a scan and group)
+    const int32_t s = static_cast<int32_t>(i / p.h.groups), g = static_cast<int32_t>(i - static_cast<int64_t>(s) * p.h.groups);
+    const int32_t lo = p.scans.at(s), hi = p.scans.at(s + 1), t = threadIdx.x % THREADS, rows = p.h.rows;
+    if (lo >= hi) {
+        if (t == 0) stats[i] = make_float2(0.0f, rsqrtf(p.a.eps));
+        return;
+    }
+    const int32_t b0 = lo / rows, b1 = (hi - 1) / rows;
+    const float2* part = p.part + g * p.h.slots + s;
+    const float base = __ldcg(part + b0).x, width = static_cast<float>(p.h.width);
+    const float by_count = 1.0f / (static_cast<float>(hi - lo) * width);
+    auto values = [&](int32_t b) {   // of piece b: as many, over all channels of the group
+        const int32_t first = b * rows > lo ? b * rows : lo, last = (b + 1) * rows < hi ? (b + 1) * rows : hi;
+        return static_cast<float>(last - first) * width;
+    };
+    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int32_t b = b0 + t; b <= b1; b += THREADS) sum.x = fmaf(values(b), __ldcg(part + b).x - base, sum.x);
+    const float mean = base + sum_of(sum, sh, THREADS).x * by_count;
+    sum = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int32_t b = b0 + t; b <= b1; b += THREADS) {
+        const float2 v = __ldcg(part + b);
+        const float d = v.x - mean;
+        sum.y += fmaf(values(b) * d, d, v.y);
+    }
+    const float m2 = sum_of(sum, sh, THREADS).y;
+    if (t == 0) stats[i] = make_float2(mean, rsqrtf(m2 * by_count + p.a.eps));
+}
+
+// A scan's rows by a cluster: the statistics of each CTA's share, joined through
+// distributed shared memory, then the rows again from the registers that keep the
+// first ones (a longer share is read again).
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads, 1) k_group_scan(const __grid_constant__ NormPass p) {
+    using P = Pack<T, W>;
+    constexpr int KEEP = W == 8 ? 6 : 8, U = 4;   // (registers)
+    extern __shared__ float sh[];
+    const Shape& h = p.h;
+    const GroupNormArgs& a = p.a;
+    const int32_t entries = h.c >> h.shift;
+    float2* own = reinterpret_cast<float2*>(sh);                    // [groups] of this CTA's rows: mean, sum of squares
+    float2* stats = own + h.groups;                                 // [groups]
+    float* sh_mean = reinterpret_cast<float*>(stats + h.groups);    // [ty][entries]
+    float* sh_m2 = sh_mean + static_cast<size_t>(h.ty) * entries;
+    const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx;
+    const uint32_t rank = ptx::cluster_rank();
+    const int32_t size = h.blocks, s = static_cast<int32_t>(blockIdx.x) / size;
+    const T* x0 = static_cast<const T*>(a.x);
+    T* out = static_cast<T*>(a.out);
+    pdl_wait();
+    pdl_trigger();
+    const int32_t lo = p.scans.at(s), hi = p.scans.at(s + 1);
+    if (p.scans.offsets) {
+        if (rank == 0 && threadIdx.x == 0) {
+            const int32_t l = p.scans.raw(s), u = p.scans.raw(s + 1);
+            if (l > u || l < 0 || u > p.scans.n) atomicOr(p.status, kStatusRange);
+        }
+        // rows of no scan, a share each
+        const int32_t before = p.scans.at(0), after = p.scans.at(p.scans.scans);
+        const int32_t rest = before + (after > before ? p.scans.n - after : p.scans.n - before), blocks = static_cast<int32_t>(gridDim.x);
+        const int32_t share = (rest + blocks - 1) / blocks, z0 = static_cast<int64_t>(blockIdx.x) * share < rest ? static_cast<int32_t>(blockIdx.x) * share : rest;
+        const int32_t z1 = z0 + share < rest ? z0 + share : rest, skip = after > before ? after - before : 0;
+        if (z0 < before) zero_rows<P>(h, out, z0, z1 < before ? z1 : before);
+        if (z1 > before) zero_rows<P>(h, out, (z0 > before ? z0 : before) + skip, z1 + skip);
+    }
+    if (lo >= hi) {   // (the whole cluster)
+        if (a.stats && rank == 0)
+            for (int32_t g = threadIdx.x; g < h.groups; g += blockDim.x)
+                a.stats[static_cast<int64_t>(s) * h.groups + g] = make_float2(0.0f, rsqrtf(a.eps));
+        return;
+    }
+    const int32_t share = (hi - lo + size - 1) / size;
+    const int32_t r0 = lo + static_cast<int32_t>(rank) * share < hi ? lo + static_cast<int32_t>(rank) * share : hi;
+    const int32_t r1 = r0 + share < hi ? r0 + share : hi;
+    const Deal deal(r1 - r0, h.ty);
+    P keep[KEEP];
+    if (ty < deal.deep) load_rows(keep, x0 + tx * W, a.ldx, r0 + ty, h.ty, r1);
+    for (int32_t v = tx; v < h.vectors && ty < deal.deep; v += h.tx) {
+        const T* x = x0 + v * W;
+        Moments<W> m;
+        int32_t r = r0 + ty;
+        if (v == tx) {
+            m.begin(keep[0]);
+#pragma unroll
+            for (int u = 0; u < KEEP; ++u)
+                if (r + u * h.ty < r1) m.add(keep[u]);
+            r += KEEP * h.ty;
+        } else {
+            m.begin(*reinterpret_cast<const P*>(x + r * a.ldx));
+        }
+        for (; r < r1; r += U * h.ty) {
+            P q[U];
+            load_rows(q, x, a.ldx, r, h.ty, r1);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r + u * h.ty < r1) m.add(q[u]);
+        }
+        m.write(static_cast<float>(deal.of(ty)), h.shift, sh_mean, sh_m2, ty * entries + ((v * W) >> h.shift));
+    }
+    __syncthreads();
+    if (r0 < r1)
+        join_threads(h, deal, sh_mean, sh_m2, [&](int32_t g, float mean, float m2) {
+            if ((threadIdx.x & 31) == 0) own[g] = make_float2(mean, m2);
+        });
+    ptx::cluster_sync();
+    for (int32_t g = threadIdx.x; g < h.groups; g += blockDim.x) {
+        const float width = static_cast<float>(h.width), by_count = 1.0f / (static_cast<float>(hi - lo) * width);
+        float2 v[kMaxCluster];
+        float n[kMaxCluster];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            const int32_t left = hi - lo - c * share;
+            n[c] = c < size && left > 0 ? static_cast<float>(left < share ? left : share) * width : 0.0f;
+            v[c] = n[c] > 0.0f ? ptx::ld_cluster_f32x2(ptx::map_to_rank(ptx::smem_u32(own + g), c)) : make_float2(0.0f, 0.0f);
+        }
+        float sum = 0.0f, m2 = 0.0f;
+#pragma unroll
+        for (int c = 1; c < kMaxCluster; ++c) sum = fmaf(n[c], n[c] > 0.0f ? v[c].x - v[0].x : 0.0f, sum);
+        const float mean = v[0].x + sum * by_count;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            const float d = n[c] > 0.0f ? v[c].x - mean : 0.0f;
+            m2 += fmaf(n[c] * d, d, v[c].y);
+        }
+        const float2 st = make_float2(mean, rsqrtf(m2 * by_count + a.eps));
+        stats[g] = st;
+        if (a.stats && rank == 0) a.stats[static_cast<int64_t>(s) * h.groups + g] = st;
+    }
+    ptx::cluster_arrive();   // (its sums are read until all have come here)
+    __syncthreads();
+    with_act(a.act, [&](auto act) {
+        for (int32_t v = tx; v < h.vectors && ty < deal.deep; v += h.tx) {
+            const T* x = x0 + v * W;
+            Affine<W> f;
+            f.load(p, stats, v);
+            int32_t r = r0 + ty;
+            auto write = [&](int32_t row, const P& q) { *reinterpret_cast<P*>(out + static_cast<int64_t>(row) * h.c + v * W) = f.template apply<act>(q); };
+            if (v == tx) {
+#pragma unroll
+                for (int u = 0; u < KEEP; ++u)
+                    if (r + u * h.ty < r1) write(r + u * h.ty, keep[u]);
+                r += KEEP * h.ty;
+            }
+            for (; r < r1; r += U * h.ty) {
+                P q[U];
+                load_rows(q, x, a.ldx, r, h.ty, r1);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (r + u * h.ty < r1) write(r + u * h.ty, q[u]);
+            }
+        }
+    });
+    ptx::cluster_wait();
 }
 
 // Statistics where there is no row at all.
@@ -329,269 +654,378 @@ struct GradPass {
     Shape h;
     Scans scans;
     float2* part;        // of each piece: sums of p and of p u
+    const float2* sums;  // [scans][groups] of all pieces, or null: the second kernel adds them up
     float* cols;         // [blocks][2][c]: sums of dz u, of dz
-    int32_t blocks;      // of rows; the blocks after them add up cols
+    int32_t col_blocks;  // the second kernel's first blocks add up cols
     int32_t* status;
 };
 
 // What a thread needs of its W channels in a scan.
 template <int W>
 struct Channels {
-    float mean[W], r[W], w[W], b[W];
+    Values<W> mean, r, w, b;   // (mean negated)
     __device__ __forceinline__ void load(const GradPass& p, int32_t s, int32_t v) {
+        float fm[W], fr[W], fw[W], fb[W];
+        int32_t g = 0;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            const int32_t ch = v * W + j;
-            const float2 st = __ldg(p.a.stats + static_cast<int64_t>(s) * p.h.groups + ch / p.h.width);
-            mean[j] = st.x;
-            r[j] = st.y;
-            w[j] = __ldg(p.a.weight + ch);
-            b[j] = p.a.bias ? __ldg(p.a.bias + ch) : 0.0f;
+            g = group_of<W>(p.h, v, j, g);
+            const float2 st = __ldg(p.a.stats + static_cast<int64_t>(s) * p.h.groups + g);
+            fm[j] = -st.x;
+            fr[j] = st.y;
+            fw[j] = __ldg(p.a.weight + v * W + j);
+            fb[j] = p.a.bias ? __ldg(p.a.bias + v * W + j) : 0.0f;
         }
+        mean.put(fm);
+        r.put(fr);
+        w.put(fw);
+        b.put(fb);
+    }
+    // u of the j-th values (pairs) of x; *dz their gradient
+    template <int ACT, typename V>
+    __device__ __forceinline__ V unit(int j, V x, V dy, V* dz) const {
+        const V u = (x + mean.v[j]) * r.v[j];
+        V unused;
+        *dz = dy * act_grad_f<ACT>(fma_v(u, w.v[j], b.v[j]), &unused);
+        return u;
+    }
+};
+
+// Sums over a thread's rows of dz u and dz.
+template <int W>
+struct GradSums {
+    Values<W> u, z;
+    __device__ __forceinline__ void begin() {
+        u.set(0.0f);
+        z.set(0.0f);
+    }
+    template <int ACT, typename P>
+    __device__ __forceinline__ void add(const Channels<W>& ch, const P& qx, const P& qd) {
+        Values<W> x, d;
+        x.unpack(qx);
+        d.unpack(qd);
+#pragma unroll
+        for (int j = 0; j < Values<W>::n; ++j) {
+            typename Values<W>::V dz;
+            const auto un = ch.template unit<ACT>(j, x.v[j], d.v[j], &dz);
+            u.v[j] = fma_v(dz, un, u.v[j]);
+            z.v[j] = z.v[j] + dz;
+        }
+    }
+    __device__ __forceinline__ void write(float* sh_u, float* sh_z) const {
+        float f[W];
+        u.get(f);
+#pragma unroll
+        for (int j = 0; j < W; ++j) sh_u[j] = f[j];
+        z.get(f);
+#pragma unroll
+        for (int j = 0; j < W; ++j) sh_z[j] = f[j];
+    }
+};
+
+// The threads' sums: added to the block's totals [2][c], then, times the weight,
+// to each group's (group, sum of p, sum of p u) by a warp.  Ends at a barrier.
+template <typename F>
+__device__ __forceinline__ void join_grad_threads(const GradPass& p, int32_t deep, float* total, float* sh_u, float* sh_z, F&& f) {
+    const Shape& h = p.h;
+    const int lane = threadIdx.x & 31;
+    __syncthreads();
+    // down the thread rows: by several threads where a row has fewer channels than the block threads
+    const int32_t threads = static_cast<int32_t>(blockDim.x);
+    int32_t rows = h.c < threads ? threads / h.c : 1;
+    if (rows > deep) rows = deep;
+    for (int32_t i = threadIdx.x; i < rows * h.c; i += threads) {
+        const int32_t r = i / h.c, c = i - r * h.c;
+        float u = 0.0f, z = 0.0f;
+        for (int32_t t = r; t < deep; t += rows) {
+            u += sh_u[t * h.c + c];
+            z += sh_z[t * h.c + c];
+        }
+        sh_u[i] = u;   // (row r, which no other thread reads)
+        sh_z[i] = z;
+    }
+    __syncthreads();
+    for (int32_t c = threadIdx.x; c < h.c; c += threads) {
+        float u = 0.0f, z = 0.0f;
+        for (int32_t t = 0; t < rows; ++t) {
+            u += sh_u[t * h.c + c];
+            z += sh_z[t * h.c + c];
+        }
+        total[c] += u;
+        total[h.c + c] += z;
+        const float w = __ldg(p.a.weight + c);
+        sh_u[c] = u * w;
+        sh_z[c] = z * w;
+    }
+    __syncthreads();
+    // (as many lanes a group as it has channels, up to a warp)
+    const int32_t lanes = h.width >= 32 ? 32 : h.width > 8 ? 16 : h.width > 4 ? 8 : h.width > 1 ? 4 : 1;
+    const int32_t k0 = lane & (lanes - 1), per = 32 / lanes;
+    for (int32_t g0 = (threadIdx.x >> 5) * per; g0 < h.groups; g0 += (threads >> 5) * per) {
+        const int32_t g = g0 + lane / lanes;
+        float u = 0.0f, z = 0.0f;
+        if (g < h.groups)
+            for (int32_t k = k0; k < h.width; k += lanes) {
+                u += sh_u[g * h.width + k];
+                z += sh_z[g * h.width + k];
+            }
+        for (int32_t o = lanes >> 1; o > 0; o >>= 1) {
+            u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+            z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+        }
+        if (g < h.groups && k0 == 0) f(g, z, u);
+    }
+    __syncthreads();
+}
+
+// dx of one vector
+template <int W>
+struct GradAffine {
+    Channels<W> ch;
+    Values<W> mz, mu;   // means of p and p u (negated)
+    __device__ __forceinline__ void load(const GradPass& p, const float2* means, int32_t s, int32_t v) {
+        ch.load(p, s, v);
+        float a[W], b[W];
+        int32_t g = 0;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            g = group_of<W>(p.h, v, j, g);
+            const float2 m = means[g];
+            a[j] = -m.x;
+            b[j] = -m.y;
+        }
+        mz.put(a);
+        mu.put(b);
+    }
+    template <int ACT, typename P>
+    __device__ __forceinline__ P apply(const P& qx, const P& qd) const {
+        Values<W> x, d;
+        x.unpack(qx);
+        d.unpack(qd);
+#pragma unroll
+        for (int j = 0; j < Values<W>::n; ++j) {
+            typename Values<W>::V dz;
+            const auto u = ch.template unit<ACT>(j, x.v[j], d.v[j], &dz);
+            x.v[j] = ch.r.v[j] * fma_v(u, mu.v[j], fma_v(dz, ch.w.v[j], mz.v[j]));
+        }
+        P o;
+        x.pack(o);
+        return o;
     }
 };
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kBwdThreads, 1) k_group_grad_sums(const __grid_constant__ GradPass p) {
+__global__ void __launch_bounds__(kThreads, 1) k_group_grad_sums(const __grid_constant__ GradPass p) {
     using P = Pack<T, W>;
     extern __shared__ float sh[];
     const Shape& h = p.h;
     float* total = sh;                                              // [2][c]: of all pieces
     float* sh_u = sh + 2 * h.c;                                     // [ty][c]: sums of dz u
     float* sh_z = sh_u + static_cast<size_t>(h.ty) * h.c;           // sums of dz
-    const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx, lane = threadIdx.x & 31;
+    const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx;
     const int32_t row0 = static_cast<int32_t>(blockIdx.x) * h.rows;
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
+    const T* x0 = static_cast<const T*>(p.a.x);
+    const T* dy0 = static_cast<const T*>(p.a.dy);
+    constexpr int U = 2;
+    P qx[U], qd[U];
     pdl_wait();
     pdl_trigger();
+    if (ty < h.ty) {
+        load_rows(qx, x0 + tx * W, p.a.ldx, row0 + ty, h.ty, row1);
+        load_rows(qd, dy0 + tx * W, p.a.ldy, row0 + ty, h.ty, row1);
+    }
     for (int32_t i = threadIdx.x; i < 2 * h.c; i += blockDim.x) total[i] = 0.0f;
     p.scans.pieces(row0, row1, [&](int32_t s, int32_t lo, int32_t hi) {
         if (s < 0 || s >= p.scans.scans) return;
         with_act(p.a.act, [&](auto act) {
             for (int32_t v = tx; v < h.vectors && ty < h.ty; v += h.tx) {
-                const T* x = static_cast<const T*>(p.a.x) + v * W;
-                const T* dy = static_cast<const T*>(p.a.dy) + v * W;
+                const T* x = x0 + v * W;
+                const T* dy = dy0 + v * W;
+                if (lo != row0 || v != tx) {
+                    load_rows(qx, x, p.a.ldx, lo + ty, h.ty, hi);
+                    load_rows(qd, dy, p.a.ldy, lo + ty, h.ty, hi);
+                }
                 Channels<W> ch;
                 ch.load(p, s, v);
-                float su[W] = {}, sz[W] = {};
-                auto add = [&](const P& qx, const P& qd) {
-                    float f[W], d[W];
-                    unpack<W>(qx, f);
-                    unpack<W>(qd, d);
+                GradSums<W> sums;
+                sums.begin();
+                for (int32_t r = lo + ty; r < hi;) {
 #pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        const float u = (f[j] - ch.mean[j]) * ch.r[j];
-                        float unused;
-                        const float dz = d[j] * act_grad_f<act>(fmaf(u, ch.w[j], ch.b[j]), &unused);
-                        su[j] = fmaf(dz, u, su[j]);
-                        sz[j] += dz;
-                    }
-                };
-                constexpr int U = 2;
-                int32_t r = lo + ty;
-                for (; r + (U - 1) * h.ty < hi; r += U * h.ty) {
-                    P qx[U], qd[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        qx[u] = *reinterpret_cast<const P*>(x + (r + u * h.ty) * p.a.ldx);
-                        qd[u] = *reinterpret_cast<const P*>(dy + (r + u * h.ty) * p.a.ldy);
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) add(qx[u], qd[u]);
+                    for (int k = 0; k < U; ++k)
+                        if (r + k * h.ty < hi) sums.template add<act>(ch, qx[k], qd[k]);
+                    r += U * h.ty;
+                    load_rows(qx, x, p.a.ldx, r, h.ty, hi);
+                    load_rows(qd, dy, p.a.ldy, r, h.ty, hi);
                 }
-                for (; r < hi; r += h.ty)
-                    add(*reinterpret_cast<const P*>(x + r * p.a.ldx), *reinterpret_cast<const P*>(dy + r * p.a.ldy));
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    sh_u[ty * h.c + v * W + j] = su[j];
-                    sh_z[ty * h.c + v * W + j] = sz[j];
-                }
+                sums.write(sh_u + ty * h.c + v * W, sh_z + ty * h.c + v * W);
             }
         });
-        __syncthreads();
-        // down the thread rows: by several threads where a row has fewer channels than the block threads
-        const int32_t deep = hi - lo < h.ty ? hi - lo : h.ty;
-        const int32_t threads = static_cast<int32_t>(blockDim.x);
-        int32_t rows = h.c < threads ? threads / h.c : 1;
-        if (rows > deep) rows = deep;
-        for (int32_t i = threadIdx.x; i < rows * h.c; i += threads) {
-            const int32_t c = i % h.c;
-            float u = 0.0f, z = 0.0f;
-            for (int32_t t = i / h.c; t < deep; t += rows) {
-                u += sh_u[t * h.c + c];
-                z += sh_z[t * h.c + c];
-            }
-            sh_u[i] = u;   // (row i / c, which no other thread reads)
-            sh_z[i] = z;
-        }
-        __syncthreads();
-        for (int32_t c = threadIdx.x; c < h.c; c += threads) {
-            float u = 0.0f, z = 0.0f;
-            for (int32_t t = 0; t < rows; ++t) {
-                u += sh_u[t * h.c + c];
-                z += sh_z[t * h.c + c];
-            }
-            total[c] += u;
-            total[h.c + c] += z;
-            const float w = __ldg(p.a.weight + c);
-            sh_u[c] = u * w;
-            sh_z[c] = z * w;
-        }
-        __syncthreads();
-        for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
-            float u = 0.0f, z = 0.0f;
-            for (int32_t k = lane; k < h.width; k += 32) {
-                u += sh_u[g * h.width + k];
-                z += sh_z[g * h.width + k];
-            }
-            u = warp_sum(u);
-            z = warp_sum(z);
-            if (lane == 0) p.part[slot_of(h, g, s)] = make_float2(z, u);
-        }
-        __syncthreads();
+        join_grad_threads(p, hi - lo < h.ty ? hi - lo : h.ty, total, sh_u, sh_z,
+                          [&](int32_t g, float z, float u) { p.part[slot_of(h, g, s)] = make_float2(z, u); });
     });
     __syncthreads();
     for (int32_t i = threadIdx.x; i < 2 * h.c; i += blockDim.x) p.cols[static_cast<int64_t>(blockIdx.x) * 2 * h.c + i] = total[i];
 }
 
-// Columns of the blocks' sums: 32 of them a block, 16 threads down each.
-__device__ __forceinline__ void add_columns(const GradPass& p, float* sh) {
-    const int32_t col = (static_cast<int32_t>(blockIdx.x) - p.blocks) * 32 + (threadIdx.x & 31), deep = threadIdx.x >> 5;
+// Columns of the blocks' sums: 32 of them a block of kThreads, 16 threads down each.
+__device__ __forceinline__ void add_columns(const GradPass& p, int32_t blocks, float* sh) {
+    const int32_t col = static_cast<int32_t>(blockIdx.x) * 32 + (threadIdx.x & 31), deep = threadIdx.x >> 5;
+    const int32_t down = static_cast<int32_t>(blockDim.x) / 32;
     float sum = 0.0f;
     if (col < 2 * p.h.c)
-        for (int32_t b = deep; b < p.blocks; b += kBwdThreads / 32) sum += __ldcg(p.cols + static_cast<int64_t>(b) * 2 * p.h.c + col);
+#pragma unroll 4
+        for (int32_t b = deep; b < blocks; b += down) sum += __ldcg(p.cols + static_cast<int64_t>(b) * 2 * p.h.c + col);
     sh[threadIdx.x] = sum;
     __syncthreads();
     if (deep != 0 || col >= 2 * p.h.c) return;
-    for (int32_t t = 1; t < kBwdThreads / 32; ++t) sum += sh[t * 32 + threadIdx.x];
+    for (int32_t t = 1; t < down; ++t) sum += sh[t * 32 + threadIdx.x];
     if (col < p.h.c) p.a.dweight[col] = sum;
     else if (p.a.dbias) p.a.dbias[col - p.h.c] = sum;
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kBwdThreads, 1) k_group_grad_apply(const __grid_constant__ GradPass p) {
+__global__ void __launch_bounds__(kThreads, 1) k_group_grad_apply(const __grid_constant__ GradPass p) {
     using P = Pack<T, W>;
     extern __shared__ float sh[];
     const Shape& h = p.h;
     const GroupNormGradArgs& a = p.a;
-    float* sh_z = sh;                 // [groups]: means of p, of p u
-    float* sh_u = sh + h.groups;
-    pdl_wait();
-    pdl_trigger();
-    if (static_cast<int32_t>(blockIdx.x) >= p.blocks) {
-        add_columns(p, sh);
+    float2* sh_means = reinterpret_cast<float2*>(sh);   // [groups]: of p, of p u
+    if (static_cast<int32_t>(blockIdx.x) < p.col_blocks) {
+        pdl_wait();
+        pdl_trigger();
+        add_columns(p, h.blocks, sh);
         return;
     }
     const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx, lane = threadIdx.x & 31;
-    const int32_t row0 = static_cast<int32_t>(blockIdx.x) * h.rows;
+    const int32_t index = static_cast<int32_t>(blockIdx.x) - p.col_blocks, block = p.sums ? h.blocks - 1 - index : index;
+    const int32_t row0 = block * h.rows;
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
-    if (p.scans.offsets)
-        for (int32_t s = blockIdx.x * blockDim.x + threadIdx.x; s < p.scans.scans; s += p.blocks * blockDim.x) {
-            const int32_t lo = p.scans.raw(s), hi = p.scans.raw(s + 1);
-            if (lo > hi || lo < 0 || hi > p.scans.n) atomicOr(p.status, kStatusRange);
+    const T* x0 = static_cast<const T*>(a.x);
+    const T* dy0 = static_cast<const T*>(a.dy);
+    T* out = static_cast<T*>(a.dx);
+    // (as in the forward pass, what the caller gave may be read before the wait)
+    constexpr int U = 2;
+    P qx[U], qd[U];
+    if (ty < h.ty) {
+        load_rows(qx, x0 + tx * W, a.ldx, row0 + ty, h.ty, row1);
+        load_rows(qd, dy0 + tx * W, a.ldy, row0 + ty, h.ty, row1);
+    }
+    bool waited = false;
+    auto wait = [&]() {
+        if (!waited) {
+            pdl_wait();
+            pdl_trigger();
         }
+        waited = true;
+    };
     p.scans.pieces(row0, row1, [&](int32_t s, int32_t lo, int32_t hi) {
-        T* out = static_cast<T*>(a.dx);
         if (s < 0 || s >= p.scans.scans) {
-            P zero;
-            float f[W] = {};
-            pack<W>(f, zero);
-            for (int32_t v = tx; v < h.vectors && ty < h.ty; v += h.tx)
-                for (int32_t r = lo + ty; r < hi; r += h.ty) *reinterpret_cast<P*>(out + static_cast<int64_t>(r) * h.c + v * W) = zero;
+            wait();
+            zero_rows<P>(h, out, lo, hi);
             return;
         }
         const int32_t s_lo = p.scans.at(s), s_hi = p.scans.at(s + 1);
         const float by_count = 1.0f / (static_cast<float>(s_hi - s_lo) * static_cast<float>(h.width));
+        wait();
         __syncthreads();
-        for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
-            PieceSet set;
-            set.load(h, p.part, g, s, s_lo, s_hi);
-            float z = 0.0f, u = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kPerLane; ++k) {
-                z += set.v[k].x;
-                u += set.v[k].y;
+        if (p.sums) {
+            for (int32_t g = threadIdx.x; g < h.groups; g += blockDim.x) {
+                const float2 v = __ldcg(p.sums + static_cast<int64_t>(s) * h.groups + g);
+                sh_means[g] = make_float2(v.x * by_count, v.y * by_count);
             }
-            z = warp_sum(z);
-            u = warp_sum(u);
-            if (lane == 0) {
-                sh_z[g] = z * by_count;
-                sh_u[g] = u * by_count;
+        } else {
+            for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
+                PieceSet set;
+                set.load(h, p.part, g, s, s_lo, s_hi);
+                float z = 0.0f, u = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kPerLane; ++k) {
+                    z += set.v[k].x;
+                    u += set.v[k].y;
+                }
+                z = warp_sum(z);
+                u = warp_sum(u);
+                if (lane == 0) sh_means[g] = make_float2(z * by_count, u * by_count);
             }
         }
         __syncthreads();
         with_act(a.act, [&](auto act) {
             for (int32_t v = tx; v < h.vectors && ty < h.ty; v += h.tx) {
-                const T* x = static_cast<const T*>(a.x) + v * W;
-                const T* dy = static_cast<const T*>(a.dy) + v * W;
-                T* dx = out + v * W;
-                Channels<W> ch;
-                ch.load(p, s, v);
-                float mz[W], mu[W];
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const int32_t g = (v * W + j) / h.width;
-                    mz[j] = sh_z[g];
-                    mu[j] = sh_u[g];
+                const T* x = x0 + v * W;
+                const T* dy = dy0 + v * W;
+                if (lo != row0 || v != tx) {
+                    load_rows(qx, x, a.ldx, lo + ty, h.ty, hi);
+                    load_rows(qd, dy, a.ldy, lo + ty, h.ty, hi);
                 }
-                auto one = [&](const P& qx, const P& qd, int32_t r) {
-                    float f[W], d[W];
-                    unpack<W>(qx, f);
-                    unpack<W>(qd, d);
+                GradAffine<W> f;
+                f.load(p, sh_means, s, v);
+                for (int32_t r = lo + ty; r < hi;) {
 #pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        const float u = (f[j] - ch.mean[j]) * ch.r[j];
-                        float unused;
-                        const float dz = d[j] * act_grad_f<act>(fmaf(u, ch.w[j], ch.b[j]), &unused);
-                        f[j] = ch.r[j] * (fmaf(dz, ch.w[j], -mz[j]) - u * mu[j]);
-                    }
-                    P o;
-                    pack<W>(f, o);
-                    *reinterpret_cast<P*>(dx + static_cast<int64_t>(r) * h.c) = o;
-                };
-                constexpr int U = 2;
-                int32_t r = hi - 1 - ty;
-                for (; r - (U - 1) * h.ty >= lo; r -= U * h.ty) {
-                    P qx[U], qd[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        qx[u] = *reinterpret_cast<const P*>(x + (r - u * h.ty) * a.ldx);
-                        qd[u] = *reinterpret_cast<const P*>(dy + (r - u * h.ty) * a.ldy);
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) one(qx[u], qd[u], r - u * h.ty);
+                    for (int k = 0; k < U; ++k)
+                        if (r + k * h.ty < hi)
+                            *reinterpret_cast<P*>(out + static_cast<int64_t>(r + k * h.ty) * h.c + v * W) = f.template apply<act>(qx[k], qd[k]);
+                    r += U * h.ty;
+                    load_rows(qx, x, a.ldx, r, h.ty, hi);
+                    load_rows(qd, dy, a.ldy, r, h.ty, hi);
                 }
-                for (; r >= lo; r -= h.ty)
-                    one(*reinterpret_cast<const P*>(x + r * a.ldx), *reinterpret_cast<const P*>(dy + r * a.ldy), r);
             }
         });
     });
+    wait();
+    if (p.scans.offsets)
+        for (int32_t s = index * blockDim.x + threadIdx.x; s < p.scans.scans; s += h.blocks * blockDim.x) {
+            const int32_t lo = p.scans.raw(s), hi = p.scans.raw(s + 1);
+            if (lo > hi || lo < 0 || hi > p.scans.n) atomicOr(p.status, kStatusRange);
+        }
+}
+
+template <int THREADS>
+__global__ void __launch_bounds__(256) k_group_grad_join(const __grid_constant__ GradPass p, float2* sums) {
+    __shared__ float2 sh[8];
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * (256 / THREADS) + threadIdx.x / THREADS;
+    pdl_wait();
+    pdl_trigger();
+    if (i >= static_cast<int64_t>(p.scans.scans) * p.h.groups) return;
+    const int32_t s = static_cast<int32_t>(i / p.h.groups), g = static_cast<int32_t>(i - static_cast<int64_t>(s) * p.h.groups);
+    const int32_t lo = p.scans.at(s), hi = p.scans.at(s + 1), t = threadIdx.x % THREADS;
+    if (lo >= hi) return;
+    const float2* part = p.part + g * p.h.slots + s;
+    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int32_t b = lo / p.h.rows + t; b <= (hi - 1) / p.h.rows; b += THREADS) {
+        const float2 v = __ldcg(part + b);
+        sum.x += v.x;
+        sum.y += v.y;
+    }
+    sum = sum_of(sum, sh, THREADS);
+    if (t == 0) sums[i] = sum;
 }
 
 // ---- host -----------------------------------------------------------------------
-// A block of at most `most` threads over vectors of a row; how many it uses.
+// Vectors of W elements and the rows of a block; large: enough blocks to be taken
+// in turn, their pieces added up between.
 int set_threads(Shape* h, int most) {
     h->tx = h->vectors < most ? h->vectors : most;
     h->ty = most / h->tx;
     return static_cast<int>(round_up(static_cast<size_t>(h->tx) * h->ty, 32));
 }
-
-// Vectors of W elements, and the rows of a block: one block per SM, fewer where
-// each would have less than one step of loads.
-Shape make_shape(int64_t n, int32_t c, int32_t groups, int64_t scans, int w, int most, int* blocks, int* threads) {
+Shape make_shape(int64_t n, int32_t c, int32_t groups, int64_t scans, int w, size_t es, int64_t bytes, bool* large, int* threads) {
     Shape h = {};
     h.c = c;
     h.groups = groups;
     h.width = c / groups;
     h.vectors = c / w;
-    h.joined = 1;
-    while (h.joined < w && h.width % (2 * h.joined) == 0) h.joined *= 2;
-    *threads = set_threads(&h, most);
-    int64_t b = ceil_div(n, static_cast<int64_t>(4) * h.ty);
-    if (b > kSms) b = kSms;
-    h.rows = static_cast<int32_t>(ceil_div(n, b));
-    *blocks = static_cast<int>(ceil_div(n, h.rows));
-    h.slots = *blocks + scans;
+    while ((2 << h.shift) <= w && h.width % (2 << h.shift) == 0) ++h.shift;
+    *large = bytes > kSmallBytes;
+    *threads = set_threads(&h, *large ? kThreads / 2 : kThreads);
+    int64_t blocks = ceil_div(n, static_cast<int64_t>(4) * h.ty);   // (one step of loads each, at least)
+    int64_t limit = *large ? ceil_div(n * c * static_cast<int64_t>(es), kBlockBytes) : kSms;
+    if (*large && limit < 2 * kSms) limit = 2 * kSms;
+    if (blocks > limit) blocks = limit;
+    h.rows = static_cast<int32_t>(ceil_div(n, blocks));
+    h.blocks = static_cast<int32_t>(ceil_div(n, h.rows));
+    h.slots = h.blocks + scans;
     return h;
 }
 
@@ -608,39 +1042,114 @@ int launch_wide(int blocks, int threads, size_t smem, cudaStream_t s, const A& a
     return launch_pdl(KERNEL, dim3(static_cast<unsigned>(blocks)), threads, smem, s, args);
 }
 
+// The kernel between the two: a warp a scan and group, or a block where a scan
+// has many pieces.
+template <typename A>
+int launch_join(void (*warp)(A, float2*), void (*block)(A, float2*), const A& p, float2* to, cudaStream_t s) {
+    const int64_t count = static_cast<int64_t>(p.scans.scans) * p.h.groups;
+    const bool many = p.h.blocks / p.scans.scans > 64;
+    const int64_t blocks = many ? count : ceil_div(count, 8);
+    if (blocks > 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
+    return launch_pdl(many ? block : warp, dim3(static_cast<unsigned>(blocks)), 256, 0, s, p, to);
+}
+
+template <auto KERNEL, typename A>
+int launch_clusters(int64_t blocks, int cluster, int threads, size_t smem, cudaStream_t s, const A& args) {
+    if (blocks > 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
+    static bool set[kMaxDevices] = {};
+    int dev = 0;
+    SPCONV_CHECK_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= kMaxDevices) return SPCONV_ERR_UNSUPPORTED;
+    if (!set[dev]) {
+        SPCONV_CHECK_CUDA(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024));
+        set[dev] = true;
+    }
+    cudaLaunchAttribute at[2] = {pdl_attr(), {}};
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    count_launch();
+    return cuda_status(cudaLaunchKernelEx(&cfg, KERNEL, args));
+}
+
+// CTAs of a cluster that takes a scan of average size whole, with at most `keep`
+// bytes each; 0: too large.  Scans differ in size, so few large ones are left to
+// the other kernels, which deal rows and not scans.
+int scan_cluster(int64_t bytes, int64_t scans, int64_t keep) {
+    const int64_t each = ceil_div(bytes, scans);
+    if (each > kScanBytes) return 0;
+    int size = 1;
+    while (size < kMaxCluster && each > size * keep) size *= 2;
+    return scans * size >= kSms || bytes <= (int64_t(4) << 20) ? size : 0;
+}
+
 template <typename T, int W>
 int forward_w(const GroupNormArgs& a, cudaStream_t s) {
     NormPass p = {};
     p.a = a;
-    int blocks = 0, threads = 0;
-    p.h = make_shape(a.n, a.c, a.groups, a.scans, W, kStatThreads, &blocks, &threads);
+    bool large = false;
+    int threads = 0;
+    const int64_t bytes = a.n * a.c * static_cast<int64_t>(sizeof(T));
+    if (const int size = scan_cluster(bytes, a.scans, 32 << 10)) {
+        p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), bytes, &large, &threads);
+        threads = set_threads(&p.h, ceil_div(bytes, a.scans * size) > (16 << 10) ? kThreads : kThreads / 2);
+        p.h.blocks = size;
+        p.scans = Scans{a.offsets, static_cast<int32_t>(a.scans), static_cast<int32_t>(a.n)};
+        SPCONV_CHECK(rows_status_word(&p.status));
+        const size_t smem = static_cast<size_t>(4) * a.groups * 4 + static_cast<size_t>(2) * p.h.ty * (a.c >> p.h.shift) * 4;
+        return launch_clusters<k_group_scan<T, W>>(a.scans * size, size, threads, smem, s, p);
+    }
+    p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), a.n * a.c * static_cast<int64_t>(sizeof(T)), &large, &threads);
     p.scans = Scans{a.offsets, static_cast<int32_t>(a.scans), static_cast<int32_t>(a.n)};
     SPCONV_CHECK(rows_status_word(&p.status));
-    Scratch part(static_cast<size_t>(p.h.slots) * a.groups * sizeof(float2), s);
+    const size_t part_bytes = round_up(static_cast<size_t>(p.h.slots) * a.groups * sizeof(float2), 256);
+    const size_t stats_bytes = large && !a.stats ? static_cast<size_t>(a.scans) * a.groups * sizeof(float2) : 0;
+    Scratch part(part_bytes + stats_bytes, s);
     if (part.failed()) return SPCONV_ERR_OOM;
     p.part = part.as<float2>();
-    SPCONV_CHECK((launch_wide<k_group_stats<T, W>>(blocks, threads, static_cast<size_t>(2) * p.h.ty * (a.c / p.h.joined) * 4, s, p)));
-    threads = set_threads(&p.h, kApplyThreads);
-    return launch_wide<k_group_apply<T, W>>(blocks, threads, static_cast<size_t>(2) * a.groups * 4, s, p);
+    SPCONV_CHECK((launch_wide<k_group_stats<T, W>>(p.h.blocks, threads, static_cast<size_t>(2) * p.h.ty * (a.c >> p.h.shift) * 4, s, p)));
+    if (large) {
+        float2* stats = a.stats ? a.stats : part.as<float2>(part_bytes);
+        SPCONV_CHECK(launch_join(k_group_join<32>, k_group_join<256>, p, stats, s));
+        p.stats = stats;
+    }
+    threads = set_threads(&p.h, large ? kApplyThreads / 2 : kApplyThreads);
+    return launch_wide<k_group_apply<T, W>>(p.h.blocks, threads, static_cast<size_t>(2) * a.groups * 4, s, p);
 }
 
 template <typename T, int W>
 int backward_w(const GroupNormGradArgs& a, cudaStream_t s) {
     GradPass p = {};
     p.a = a;
+    bool large = false;
     int threads = 0;
-    p.h = make_shape(a.n, a.c, a.groups, a.scans, W, kBwdThreads, &p.blocks, &threads);
+    p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), 2 * a.n * a.c * static_cast<int64_t>(sizeof(T)), &large,
+                     &threads);
     p.scans = Scans{a.offsets, static_cast<int32_t>(a.scans), static_cast<int32_t>(a.n)};
     SPCONV_CHECK(rows_status_word(&p.status));
     const size_t part_bytes = round_up(static_cast<size_t>(p.h.slots) * a.groups * sizeof(float2), 256);
-    Scratch buf(part_bytes + static_cast<size_t>(p.blocks) * 2 * a.c * 4, s);
+    const size_t sums_bytes = large ? round_up(static_cast<size_t>(a.scans) * a.groups * sizeof(float2), 256) : 0;
+    Scratch buf(part_bytes + sums_bytes + static_cast<size_t>(p.h.blocks) * 2 * a.c * 4, s);
     if (buf.failed()) return SPCONV_ERR_OOM;
     p.part = buf.as<float2>();
-    p.cols = buf.as<float>(part_bytes);
-    SPCONV_CHECK((launch_wide<k_group_grad_sums<T, W>>(p.blocks, threads, static_cast<size_t>(2) * (p.h.ty + 1) * a.c * 4, s, p)));
+    p.cols = buf.as<float>(part_bytes + sums_bytes);
+    SPCONV_CHECK((launch_wide<k_group_grad_sums<T, W>>(p.h.blocks, threads, static_cast<size_t>(2) * (p.h.ty + 1) * a.c * 4, s, p)));
+    if (large) {
+        float2* sums = buf.as<float2>(part_bytes);
+        SPCONV_CHECK(launch_join(k_group_grad_join<32>, k_group_grad_join<256>, p, sums, s));
+        p.sums = sums;
+    }
+    p.col_blocks = static_cast<int32_t>(ceil_div(2 * a.c, 32));
     size_t smem = static_cast<size_t>(2) * a.groups * 4;
-    if (smem < kBwdThreads * 4) smem = kBwdThreads * 4;
-    return launch_wide<k_group_grad_apply<T, W>>(p.blocks + static_cast<int>(ceil_div(2 * a.c, 32)), kBwdThreads, smem, s, p);
+    if (smem < kThreads * 4) smem = kThreads * 4;
+    return launch_wide<k_group_grad_apply<T, W>>(p.h.blocks + p.col_blocks, threads, smem, s, p);
 }
 
 }  // namespace
