@@ -39,9 +39,13 @@ constexpr int kStaging = 32 * 128;       // of an epilogue warp: twice 32 rows o
 constexpr int kScaleSlots = 4;           // blocks of K whose scales lie in shared memory: [2 blocks of columns][128 rows] each
 constexpr int kScaleBytes = kScaleSlots * 2 * 128 * 4 + kEpiWarps * 16;   // (and the epilogue warps' tiles)
 // Registers a thread: 168 at the launch (three warps on each quarter of an SM), then
-// 56 for the first four warps and 224 for the others.
-constexpr int kRegsFirst = 56, kRegsEpi = 224;
-static_assert(128 * kRegsFirst + 32 * kEpiWarps * kRegsEpi <= kThreads * 168, "register split");
+// 56 for the first four warps and 224 for the others (gated: 88 and 208, which is
+// where neither side spills).
+template <bool DUAL>
+struct Regs {
+    static constexpr int first = DUAL ? 88 : 56, epi = DUAL ? 208 : 224;
+    static_assert(128 * first + 32 * kEpiWarps * epi <= kThreads * 168, "register split");
+};
 constexpr int kTableSize = 256;
 constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStaging + kScaleBytes + 256 + 4 * (kTableSize + 1);
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
@@ -290,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
     };
     auto tile_at = [&](int32_t k, Tile& t) { return find_tile<DUAL ? 128 : 256>(p, table, k, t); };
     uint32_t fills = 0;   // stages this thread has filled
-    if (warp < kFirstEpi) ptx::regs_dec<kRegsFirst>();
+    if (warp < kFirstEpi) ptx::regs_dec<Regs<DUAL>::first>();
     if (warp == 0) {
         if (lane == 0) {
             uint32_t& f = fills;
@@ -383,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
             }
         }
     } else if (warp >= kFirstEpi) {
-        ptx::regs_inc<kRegsEpi>();
+        ptx::regs_inc<Regs<DUAL>::epi>();
         const int e = warp - kFirstEpi;
         const int quarter = warp & 3, part = e >> 2;   // TMEM lanes; half of the columns
         uint8_t* stage0 = staging + e * kStaging;
@@ -450,10 +454,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
             const int32_t n0 = tile->w * kTileN + part * kOut;   // first output column
             const int32_t rows = end - m0 < 32 ? end - m0 : 32, left = p.h - n0;   // (either may be negative)
             const bool live = row < end;
-            // Bias and activation, 16 columns at a time, moved to where one copy of the code finds
-            // them: unrolled over all of them it needs more registers than there are.  The bias
-            // lies in the staging buffer meanwhile.
-            if (DUAL || p.act != SPCONV_ACT_NONE || p.bias) {
+            // Whole groups of 32 rows leave by tensor-map copies, which nobody waits for; a run's
+            // last ones, which a copy would not clip, and unaligned outputs by plain stores.
+            const bool mapped = p.map_out && rows == 32;
+            // For bias and activation sums are moved, kCols columns at a time, to where one copy of
+            // the code finds them: unrolled over all of them it needs more registers than there are.
+            constexpr int kCols = DUAL && !EIGHT ? 32 : 16;
+            auto pick = [&](int c, F2 (&v)[kCols / 2]) {   // the c-th columns, activated
+                F2 u[kCols / 2];
+#pragma unroll
+                for (int k = 0; k < kOut / kCols; ++k)
+                    if (c == k) {
+#pragma unroll
+                        for (int j = 0; j < kCols / 2; ++j) {
+                            v[j] = acc[k * (kCols / 2) + j];
+                            if (DUAL) u[j] = acc[(k * (kCols / 2) + j + 32) % 64];
+                        }
+                    }
+                if (!DUAL) {
+                    const float4* bias = reinterpret_cast<const float4*>(stage0 + c * kCols * 4);
+#pragma unroll
+                    for (int j = 0; j < kCols / 4; ++j) {
+                        const float4 b = bias[j];
+                        v[2 * j] = v[2 * j] + F2(b.x, b.y);
+                        v[2 * j + 1] = v[2 * j + 1] + F2(b.z, b.w);
+                    }
+                }
+                with_act(p.act, [&](auto act) {
+#pragma unroll
+                    for (int j = 0; j < kCols / 2; ++j) v[j] = DUAL ? act_f<act>(v[j]) * u[j] : act_f<act>(v[j]);
+                });
+            };
+            auto activate = [&]() {   // in place; the bias lies in the staging buffer meanwhile
                 if (!DUAL) {
                     if (lane == 0) ptx::bulk_wait_read();
                     __syncwarp();
@@ -464,49 +496,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (int c = 0; c < kOut / 16; ++c) {
-                    F2 v[8], u[8];
+                for (int c = 0; c < kOut / kCols; ++c) {
+                    F2 v[kCols / 2];
+                    pick(c, v);
 #pragma unroll
-                    for (int k = 0; k < kOut / 16; ++k)
+                    for (int k = 0; k < kOut / kCols; ++k)
                         if (c == k) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                v[j] = acc[k * 8 + j];
-                                if (DUAL) u[j] = acc[(k * 8 + j + 32) % 64];
-                            }
-                        }
-                    if (!DUAL) {
-                        const float4* bias = reinterpret_cast<const float4*>(stage0 + c * 64);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 b = bias[j];
-                            v[2 * j] = v[2 * j] + F2(b.x, b.y);
-                            v[2 * j + 1] = v[2 * j + 1] + F2(b.z, b.w);
-                        }
-                    }
-                    with_act(p.act, [&](auto act) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = DUAL ? act_f<act>(v[j]) * u[j] : act_f<act>(v[j]);
-                    });
-#pragma unroll
-                    for (int k = 0; k < kOut / 16; ++k)
-                        if (c == k) {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) acc[k * 8 + j] = v[j];
+                            for (int j = 0; j < kCols / 2; ++j) acc[k * (kCols / 2) + j] = v[j];
                         }
                 }
                 __syncwarp();
-            }
-            // Whole groups of 32 rows leave by tensor-map copies, which nobody waits for; a run's
-            // last ones, which a copy would not clip, and unaligned outputs by plain stores.
-            const bool mapped = p.map_out && rows == 32;
+            };
             if (!EIGHT) {
-                // 32 columns at a time, two staging buffers in turn: rows of 64 bytes in 16-byte
-                // pieces whose places are turned by the row (the copies' 64-byte swizzle)
+                // two staging buffers in turn: rows of 64 bytes in 16-byte pieces whose places are
+                // turned by the row (the copies' 64-byte swizzle)
                 auto place = [](int r, int piece) { return r * 64 + ((piece ^ ((r >> 1) & 3)) << 4); };
                 const int i0 = lane >> 2, c8 = lane & 3;   // of eight rows at a time: row; eight columns
-#pragma unroll
-                for (int c = 0; c < kOut / 32; ++c) {
+                auto store = [&](int c, F2 (&v)[16]) {     // 32 columns
                     const int32_t cols = left - 32 * c;    // (may be negative)
                     uint8_t* stage = stage0 + (c & 1) * 2048;
                     if (lane == 0) ptx::bulk_wait_read_but<1>();   // (the other buffer's copy may still run)
@@ -515,20 +522,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
 #pragma unroll
                         for (int r = 0; r < 32; r += 8) {
                             const int i = r + i0;
-                            uint4 v = make_uint4(0, 0, 0, 0);
+                            uint4 x4 = make_uint4(0, 0, 0, 0);
                             if (i < rows && c8 * 8 < cols) {
                                 const __nv_bfloat16* x = p.extra + (m0 + i) * p.ld_extra + n0 + c * 32 + c8 * 8;
                                 if (p.vec_extra && c8 * 8 + 8 <= cols) {
-                                    v = *reinterpret_cast<const uint4*>(x);
+                                    x4 = *reinterpret_cast<const uint4*>(x);
                                 } else {
                                     uint32_t u[4] = {};
 #pragma unroll
                                     for (int j = 0; j < 8; ++j)
                                         if (c8 * 8 + j < cols) u[j / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x[j])) << (16 * (j & 1));
-                                    v = make_uint4(u[0], u[1], u[2], u[3]);
+                                    x4 = make_uint4(u[0], u[1], u[2], u[3]);
                                 }
                             }
-                            *reinterpret_cast<uint4*>(stage + place(i, c8)) = v;
+                            *reinterpret_cast<uint4*>(stage + place(i, c8)) = x4;
                         }
                         __syncwarp();
                     }
@@ -536,19 +543,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                     for (int k = 0; k < 4; ++k) {
                         uint4* at = reinterpret_cast<uint4*>(stage + place(lane, k));
                         if (!DUAL && p.extra) {
-                            const uint4 v = *at;
-                            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                            const uint4 x4 = *at;
+                            const uint32_t u[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                acc[c * 16 + k * 4 + j] = acc[c * 16 + k * 4 + j] + F2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xFFFF0000u));
+                                v[k * 4 + j] = v[k * 4 + j] + F2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xFFFF0000u));
                         }
                         uint32_t u[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             float a, b;
-                            acc[c * 16 + k * 4 + j].get(a, b);
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-                            u[j] = reinterpret_cast<const uint32_t&>(v);
+                            v[k * 4 + j].get(a, b);
+                            const __nv_bfloat162 y = __floats2bfloat162_rn(a, b);
+                            u[j] = reinterpret_cast<const uint32_t&>(y);
                         }
                         *at = make_uint4(u[0], u[1], u[2], u[3]);
                     }
@@ -562,12 +569,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                         for (int r = 0; r < 32; r += 8) {
                             const int i = r + i0;
                             if (i >= rows || c8 * 8 >= cols) continue;
-                            const uint4 v = *reinterpret_cast<const uint4*>(stage + place(i, c8));
+                            const uint4 y4 = *reinterpret_cast<const uint4*>(stage + place(i, c8));
                             __nv_bfloat16* o = out + (m0 + i) * p.ld_out;
                             if (p.vec_out && c8 * 8 + 8 <= cols) {
-                                *reinterpret_cast<uint4*>(o) = v;
+                                *reinterpret_cast<uint4*>(o) = y4;
                             } else {
-                                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                                const uint32_t u[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
                                 for (int j = 0; j < 8; ++j)
                                     if (c8 * 8 + j < cols) o[j] = __ushort_as_bfloat16(static_cast<uint16_t>(u[j / 2] >> (16 * (j & 1))));
@@ -576,8 +583,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                         __syncwarp();
                     }
                     if (lane == 0) ptx::bulk_commit();
+                };
+                if constexpr (DUAL) {
+#pragma unroll 1
+                    for (int c = 0; c < kOut / 32; ++c) {
+                        F2 v[kCols / 2];
+                        pick(c, v);
+                        store(c, reinterpret_cast<F2(&)[16]>(v));
+                    }
+                } else {
+                    if (p.act != SPCONV_ACT_NONE || p.bias) activate();
+#pragma unroll
+                    for (int c = 0; c < kOut / 32; ++c) store(c, reinterpret_cast<F2(&)[16]>(acc[c * 16]));
                 }
             } else {
+                if (DUAL || p.act != SPCONV_ACT_NONE || p.bias) activate();
                 // the largest of the row's 128 columns: this warp's, or its half and another warp's
                 uint32_t most = 0;
 #pragma unroll

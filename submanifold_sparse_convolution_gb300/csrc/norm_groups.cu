@@ -36,7 +36,7 @@ constexpr int kSms = 152;
 constexpr int kPerLane = 5;              // pieces that a lane adds up where a block does so for itself
 static_assert(kSms <= 32 * kPerLane, "blocks of a small input");
 constexpr int kThreads = 512;            // blocks of a small input; half of it for those of a large one
-constexpr int kApplyThreads = 384;       // (80 registers a thread, and room on an SM beside a block of k_group_stats)
+constexpr int kApplyThreads = 320;       // (96 registers a thread, and room on an SM beside a block of k_group_stats)
 constexpr int64_t kSmallBytes = 16 << 20, kBlockBytes = 256 << 10;
 constexpr int64_t kScanBytes = 512 << 10;
 constexpr int kMaxCluster = 8;           // portable cluster size
