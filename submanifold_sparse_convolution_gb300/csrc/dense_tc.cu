@@ -57,20 +57,6 @@ constexpr int kPairs = 76;                    // CTA pairs of a full GPU
 
 constexpr int32_t kEpiPlain = 4;              // the sums, rounded; or, of one slice of K, fp32 to a workspace
 
-// x / d for 0 <= x < 2^31, without a division: x m / 2^(31 + s) with
-// s = ceil(log2 d) and m = ceil(2^(31 + s) / d).
-struct FastDiv {
-    uint32_t d, m, s;
-    FastDiv() = default;
-    explicit FastDiv(uint32_t v) : d(v), s(0) {
-        while ((1ull << s) < v) ++s;
-        m = static_cast<uint32_t>(((1ull << (31 + s)) + v - 1) / v);
-    }
-    __device__ __forceinline__ int32_t operator()(int32_t x) const {
-        return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(x)) * m) >> (31 + s));
-    }
-};
-
 // How an operand lies in memory: K contiguous; rows contiguous; rows contiguous
 // and a multiple of 64, which one copy takes whole.
 enum : int32_t { kLayoutK = 0, kLayoutRows = 1, kLayoutBlocks = 2 };

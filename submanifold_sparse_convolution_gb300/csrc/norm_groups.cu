@@ -35,7 +35,7 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kPerLane = 5;              // pieces that a lane adds up where a block does so for itself
 static_assert(kSms <= 32 * kPerLane, "blocks of a small input");
-constexpr int kThreads = 512;            // blocks of a small input; half of it for those of a large one
+constexpr int kThreads = 448;            // blocks of a small input (72 registers a thread, two on an SM); half of it for those of a large one
 constexpr int kApplyThreads = 320;       // (96 registers a thread, and room on an SM beside a block of k_group_stats)
 constexpr int64_t kSmallBytes = 16 << 20, kBlockBytes = 256 << 10;
 constexpr int64_t kScanBytes = 512 << 10;
@@ -132,6 +132,8 @@ struct Shape {
     int32_t rows;                  // of a block (R)
     int32_t blocks;
     int32_t shift;                 // 2^shift channels of a group lie in a vector and are joined by a thread
+    int32_t lanes;                 // of a warp that join one group's entries: a power of two
+    FastDiv by_tx, by_ty, by_wide, by_blocks;   // wide: entries of a group in a row
     int64_t slots;                 // blocks + scans
 };
 
@@ -181,8 +183,7 @@ __device__ __forceinline__ void zero_rows(const Shape& h, void* out, int32_t lo,
 template <int W>
 __device__ __forceinline__ int32_t group_of(const Shape& h, int32_t v, int j, int32_t before) {
     if (j & ((1 << h.shift) - 1)) return before;
-    const int32_t e = (v * W + j) >> h.shift, wide = h.width >> h.shift;
-    return wide == 1 ? e : e / wide;
+    return h.by_wide((v * W + j) >> h.shift);
 }
 
 // ---- forward ------------------------------------------------------------------
@@ -259,37 +260,44 @@ struct Moments {
 // Rows of the block's threads: each of the first `extra` of `ty` has one more.
 struct Deal {
     int32_t rows, each, extra, deep;
-    __device__ __forceinline__ Deal(int32_t rows_, int32_t ty) : rows(rows_), each(rows_ / ty), extra(rows_ - each * ty), deep(rows_ < ty ? rows_ : ty) {}
+    __device__ __forceinline__ Deal(int32_t rows_, const Shape& h)
+        : rows(rows_), each(h.by_ty(rows_)), extra(rows_ - each * h.ty), deep(rows_ < h.ty ? rows_ : h.ty) {}
     __device__ __forceinline__ int32_t of(int32_t t) const { return each + (t < extra); }
 };
 
 // What the threads wrote, joined about each group's mean in two passes over shared
-// memory, a warp a group: f(group, mean, sum of squares) by all its lanes.
+// memory, by as many lanes a group as it has entries for: f(group, mean, sum of
+// squares) by one of them.
 template <typename F>
 __device__ __forceinline__ void join_threads(const Shape& h, const Deal& deal, const float* sh_mean, const float* sh_m2, F&& f) {
     const int lane = threadIdx.x & 31;
-    const int32_t entries = h.c >> h.shift, wide = h.width >> h.shift;
+    const int32_t entries = h.c >> h.shift, wide = h.width >> h.shift, count = deal.deep * wide, lanes = h.lanes;
     const float by_count = 1.0f / (static_cast<float>(deal.rows) * static_cast<float>(h.width)), joined = static_cast<float>(1 << h.shift);
-    // lanes across a group's entries, and down the thread rows where those are few
-    const int32_t down = wide < 32 ? 32 / wide : 1;
-    const int32_t t0 = wide < 32 ? lane / wide : 0, k0 = wide < 32 ? lane - t0 * wide : lane;
-    for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
-        const float base = sh_mean[g * wide];
+    const int32_t log = 31 - __clz(lanes), per = 32 >> log, i0 = lane & (lanes - 1);
+    auto sum_lanes = [&](float v) {
+        for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        return v;
+    };
+    for (int32_t g0 = (threadIdx.x >> 5) * per; g0 < h.groups; g0 += (blockDim.x >> 5) * per) {
+        const int32_t g = g0 + (lane >> log);
+        const bool live = g < h.groups;
+        const float base = live ? sh_mean[g * wide] : 0.0f;
         float sum = 0.0f, m2 = 0.0f;
         auto entries_of = [&](auto&& each) {
-            if (t0 >= down) return;
-            for (int32_t t = t0; t < deal.deep; t += down) {
-                const float n = static_cast<float>(deal.of(t)) * joined;
-                for (int32_t k = k0; k < wide; k += 32) each(t * entries + g * wide + k, n);
-            }
+            if (live)
+                for (int32_t i = i0; i < count; i += lanes) {
+                    const int32_t t = h.by_wide(i);
+                    each(t * entries + g * wide + (i - t * wide), static_cast<float>(deal.of(t)) * joined);
+                }
         };
         entries_of([&](int32_t i, float n) { sum = fmaf(n, sh_mean[i] - base, sum); });
-        const float mean = base + warp_sum(sum) * by_count;
+        const float mean = base + sum_lanes(sum) * by_count;
         entries_of([&](int32_t i, float n) {
             const float d = sh_mean[i] - mean;
             m2 += fmaf(n * d, d, sh_m2[i]);
         });
-        f(g, mean, warp_sum(m2));
+        m2 = sum_lanes(m2);
+        if (live && i0 == 0) f(g, mean, m2);
     }
 }
 
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_group_stats(const __grid_consta
     const int32_t entries = h.c >> h.shift;
     float* sh_mean = sh;                                            // [ty][entries]
     float* sh_m2 = sh + static_cast<size_t>(h.ty) * entries;
-    const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx;
+    const int ty = h.by_tx(threadIdx.x), tx = threadIdx.x - ty * h.tx;
     const int32_t row0 = static_cast<int32_t>(blockIdx.x) * h.rows;
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
     const T* x0 = static_cast<const T*>(p.a.x);
@@ -345,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_group_stats(const __grid_consta
     if (ty < h.ty) load_rows(q, x0 + tx * W, p.a.ldx, row0 + ty, h.ty, row1);
     p.scans.pieces(row0, row1, [&](int32_t s, int32_t lo, int32_t hi) {
         if (s < 0 || s >= p.scans.scans) return;
-        const Deal deal(hi - lo, h.ty);
+        const Deal deal(hi - lo, h);
         for (int32_t v = tx; v < h.vectors && ty < deal.deep; v += h.tx) {
             const T* x = x0 + v * W;
             if (lo != row0 || v != tx) load_rows(q, x, p.a.ldx, lo + ty, h.ty, hi);
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_group_stats(const __grid_consta
         }
         __syncthreads();
         join_threads(h, deal, sh_mean, sh_m2, [&](int32_t g, float mean, float m2) {
-            if ((threadIdx.x & 31) == 0) p.part[slot_of(h, g, s)] = make_float2(mean, m2);
+            p.part[slot_of(h, g, s)] = make_float2(mean, m2);
         });
         __syncthreads();
     });
@@ -394,7 +402,7 @@ __global__ void __launch_bounds__(kApplyThreads, 2) k_group_apply(const __grid_c
     extern __shared__ float2 sh_stats[];   // [groups]
     const Shape& h = p.h;
     const GroupNormArgs& a = p.a;
-    const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx, lane = threadIdx.x & 31;
+    const int ty = h.by_tx(threadIdx.x), tx = threadIdx.x - ty * h.tx, lane = threadIdx.x & 31;
     const int32_t block = p.stats ? h.blocks - 1 - static_cast<int32_t>(blockIdx.x) : static_cast<int32_t>(blockIdx.x);
     const int32_t row0 = block * h.rows;
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
@@ -529,9 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_scan(const __grid_constan
     float2* stats = own + h.groups;                                 // [groups]
     float* sh_mean = reinterpret_cast<float*>(stats + h.groups);    // [ty][entries]
     float* sh_m2 = sh_mean + static_cast<size_t>(h.ty) * entries;
-    const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx;
+    const int ty = h.by_tx(threadIdx.x), tx = threadIdx.x - ty * h.tx;
     const uint32_t rank = ptx::cluster_rank();
-    const int32_t size = h.blocks, s = static_cast<int32_t>(blockIdx.x) / size;
+    const int32_t size = h.blocks, s = h.by_blocks(static_cast<int32_t>(blockIdx.x));
     const T* x0 = static_cast<const T*>(a.x);
     T* out = static_cast<T*>(a.out);
     pdl_wait();
@@ -543,12 +551,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_scan(const __grid_constan
             if (l > u || l < 0 || u > p.scans.n) atomicOr(p.status, kStatusRange);
         }
         // rows of no scan, a share each
-        const int32_t before = p.scans.at(0), after = p.scans.at(p.scans.scans);
-        const int32_t rest = before + (after > before ? p.scans.n - after : p.scans.n - before), blocks = static_cast<int32_t>(gridDim.x);
-        const int32_t share = (rest + blocks - 1) / blocks, z0 = static_cast<int64_t>(blockIdx.x) * share < rest ? static_cast<int32_t>(blockIdx.x) * share : rest;
-        const int32_t z1 = z0 + share < rest ? z0 + share : rest, skip = after > before ? after - before : 0;
-        if (z0 < before) zero_rows<P>(h, out, z0, z1 < before ? z1 : before);
-        if (z1 > before) zero_rows<P>(h, out, (z0 > before ? z0 : before) + skip, z1 + skip);
+        const int32_t before = p.scans.at(0), after = p.scans.at(p.scans.scans), skip = after > before ? after - before : 0;
+        if (const int32_t rest = p.scans.n - skip; rest > 0) {
+            const int32_t blocks = static_cast<int32_t>(gridDim.x), share = (rest + blocks - 1) / blocks;
+            const int32_t z0 = static_cast<int64_t>(blockIdx.x) * share < rest ? static_cast<int32_t>(blockIdx.x) * share : rest;
+            const int32_t z1 = z0 + share < rest ? z0 + share : rest;
+            if (z0 < before) zero_rows<P>(h, out, z0, z1 < before ? z1 : before);
+            if (z1 > before) zero_rows<P>(h, out, (z0 > before ? z0 : before) + skip, z1 + skip);
+        }
     }
     if (lo >= hi) {   // (the whole cluster)
         if (a.stats && rank == 0)
@@ -556,10 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_scan(const __grid_constan
                 a.stats[static_cast<int64_t>(s) * h.groups + g] = make_float2(0.0f, rsqrtf(a.eps));
         return;
     }
-    const int32_t share = (hi - lo + size - 1) / size;
+    const int32_t share = h.by_blocks(hi - lo + size - 1);
     const int32_t r0 = lo + static_cast<int32_t>(rank) * share < hi ? lo + static_cast<int32_t>(rank) * share : hi;
     const int32_t r1 = r0 + share < hi ? r0 + share : hi;
-    const Deal deal(r1 - r0, h.ty);
+    const Deal deal(r1 - r0, h);
     P keep[KEEP];
     if (ty < deal.deep) load_rows(keep, x0 + tx * W, a.ldx, r0 + ty, h.ty, r1);
     for (int32_t v = tx; v < h.vectors && ty < deal.deep; v += h.tx) {
@@ -587,33 +597,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_scan(const __grid_constan
     __syncthreads();
     if (r0 < r1)
         join_threads(h, deal, sh_mean, sh_m2, [&](int32_t g, float mean, float m2) {
-            if ((threadIdx.x & 31) == 0) own[g] = make_float2(mean, m2);
+            own[g] = make_float2(mean, m2);
         });
-    ptx::cluster_sync();
+    if (size > 1) ptx::cluster_sync();
+    else __syncthreads();
     for (int32_t g = threadIdx.x; g < h.groups; g += blockDim.x) {
         const float width = static_cast<float>(h.width), by_count = 1.0f / (static_cast<float>(hi - lo) * width);
-        float2 v[kMaxCluster];
-        float n[kMaxCluster];
+        float mean = own[g].x, m2 = own[g].y;
+        if (size > 1) {
+            float2 v[kMaxCluster];
+            float n[kMaxCluster];
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            const int32_t left = hi - lo - c * share;
-            n[c] = c < size && left > 0 ? static_cast<float>(left < share ? left : share) * width : 0.0f;
-            v[c] = n[c] > 0.0f ? ptx::ld_cluster_f32x2(ptx::map_to_rank(ptx::smem_u32(own + g), c)) : make_float2(0.0f, 0.0f);
-        }
-        float sum = 0.0f, m2 = 0.0f;
+            for (int c = 0; c < kMaxCluster; ++c) {
+                const int32_t left = hi - lo - c * share;
+                n[c] = c < size && left > 0 ? static_cast<float>(left < share ? left : share) * width : 0.0f;
+                v[c] = n[c] > 0.0f ? ptx::ld_cluster_f32x2(ptx::map_to_rank(ptx::smem_u32(own + g), c)) : make_float2(0.0f, 0.0f);
+            }
+            float sum = 0.0f;
 #pragma unroll
-        for (int c = 1; c < kMaxCluster; ++c) sum = fmaf(n[c], n[c] > 0.0f ? v[c].x - v[0].x : 0.0f, sum);
-        const float mean = v[0].x + sum * by_count;
+            for (int c = 1; c < kMaxCluster; ++c) sum = fmaf(n[c], n[c] > 0.0f ? v[c].x - v[0].x : 0.0f, sum);
+            mean = v[0].x + sum * by_count;
+            m2 = 0.0f;
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            const float d = n[c] > 0.0f ? v[c].x - mean : 0.0f;
-            m2 += fmaf(n[c] * d, d, v[c].y);
+            for (int c = 0; c < kMaxCluster; ++c) {
+                const float d = n[c] > 0.0f ? v[c].x - mean : 0.0f;
+                m2 += fmaf(n[c] * d, d, v[c].y);
+            }
         }
         const float2 st = make_float2(mean, rsqrtf(m2 * by_count + a.eps));
         stats[g] = st;
         if (a.stats && rank == 0) a.stats[static_cast<int64_t>(s) * h.groups + g] = st;
     }
-    ptx::cluster_arrive();   // (its sums are read until all have come here)
+    if (size > 1) ptx::cluster_arrive();   // (its sums are read until all have come here)
     __syncthreads();
     with_act(a.act, [&](auto act) {
         for (int32_t v = tx; v < h.vectors && ty < deal.deep; v += h.tx) {
@@ -637,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_scan(const __grid_constan
             }
         }
     });
-    ptx::cluster_wait();
+    if (size > 1) ptx::cluster_wait();
 }
 
 // Statistics where there is no row at all.
@@ -735,7 +750,7 @@ __device__ __forceinline__ void join_grad_threads(const GradPass& p, int32_t dee
     int32_t rows = h.c < threads ? threads / h.c : 1;
     if (rows > deep) rows = deep;
     for (int32_t i = threadIdx.x; i < rows * h.c; i += threads) {
-        const int32_t r = i / h.c, c = i - r * h.c;
+        const int32_t r = i >= h.c ? i / h.c : 0, c = i - r * h.c;
         float u = 0.0f, z = 0.0f;
         for (int32_t t = r; t < deep; t += rows) {
             u += sh_u[t * h.c + c];
@@ -822,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_grad_sums(const __grid_co
     float* total = sh;                                              // [2][c]: of all pieces
     float* sh_u = sh + 2 * h.c;                                     // [ty][c]: sums of dz u
     float* sh_z = sh_u + static_cast<size_t>(h.ty) * h.c;           // sums of dz
-    const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx;
+    const int ty = h.by_tx(threadIdx.x), tx = threadIdx.x - ty * h.tx;
     const int32_t row0 = static_cast<int32_t>(blockIdx.x) * h.rows;
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
     const T* x0 = static_cast<const T*>(p.a.x);
@@ -897,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_grad_apply(const __grid_c
         add_columns(p, h.blocks, sh);
         return;
     }
-    const int tx = threadIdx.x % h.tx, ty = threadIdx.x / h.tx, lane = threadIdx.x & 31;
+    const int ty = h.by_tx(threadIdx.x), tx = threadIdx.x - ty * h.tx, lane = threadIdx.x & 31;
     const int32_t index = static_cast<int32_t>(blockIdx.x) - p.col_blocks, block = p.sums ? h.blocks - 1 - index : index;
     const int32_t row0 = block * h.rows;
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
@@ -1008,6 +1023,12 @@ __global__ void __launch_bounds__(256) k_group_grad_join(const __grid_constant__
 int set_threads(Shape* h, int most) {
     h->tx = h->vectors < most ? h->vectors : most;
     h->ty = most / h->tx;
+    h->by_tx = FastDiv(static_cast<uint32_t>(h->tx));
+    h->by_ty = FastDiv(static_cast<uint32_t>(h->ty));
+    const int32_t wide = h->width >> h->shift;
+    h->by_wide = FastDiv(static_cast<uint32_t>(wide));
+    h->lanes = 1;
+    while (h->lanes < 32 && h->lanes < h->ty * wide) h->lanes *= 2;
     return static_cast<int>(round_up(static_cast<size_t>(h->tx) * h->ty, 32));
 }
 Shape make_shape(int64_t n, int32_t c, int32_t groups, int64_t scans, int w, size_t es, int64_t bytes, bool* large, int* threads) {
@@ -1101,6 +1122,7 @@ int forward_w(const GroupNormArgs& a, cudaStream_t s) {
         p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), bytes, &large, &threads);
         threads = set_threads(&p.h, ceil_div(bytes, a.scans * size) > (16 << 10) ? kThreads : kThreads / 2);
         p.h.blocks = size;
+        p.h.by_blocks = FastDiv(static_cast<uint32_t>(size));
         p.scans = Scans{a.offsets, static_cast<int32_t>(a.scans), static_cast<int32_t>(a.n)};
         SPCONV_CHECK(rows_status_word(&p.status));
         const size_t smem = static_cast<size_t>(4) * a.groups * 4 + static_cast<size_t>(2) * p.h.ty * (a.c >> p.h.shift) * 4;

@@ -208,6 +208,20 @@ int launch_pdl(void (*kernel)(K...), dim3 grid, int threads, size_t smem, cudaSt
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
+// x / d for 0 <= x < 2^31, without a division: x m / 2^(31 + s) with
+// s = ceil(log2 d) and m = ceil(2^(31 + s) / d).
+struct FastDiv {
+    uint32_t d, m, s;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t v) : d(v), s(0) {
+        while ((1ull << s) < v) ++s;
+        m = static_cast<uint32_t>(((1ull << (31 + s)) + v - 1) / v);
+    }
+    __device__ __forceinline__ int32_t operator()(int32_t x) const {
+        return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(x)) * m) >> (31 + s));
+    }
+};
+
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int launch_status() { return cuda_status(cudaGetLastError()); }
