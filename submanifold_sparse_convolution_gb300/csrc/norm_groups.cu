@@ -171,6 +171,53 @@ struct PieceSet {
     }
 };
 
+// A thread's vectors of N matrices on their way through its own slots of shared
+// memory: D rows ahead, without registers for them.
+template <typename P, int N, int D>
+struct Stream {
+    P* slots;        // this thread's: slot (s, a) at (s N + a) threads
+    int32_t threads;
+    __device__ __forceinline__ Stream(void* shared) : slots(static_cast<P*>(shared) + threadIdx.x), threads(blockDim.x) {}
+    static __host__ __device__ constexpr size_t bytes(int threads) { return static_cast<size_t>(D) * N * threads * sizeof(P); }
+    __device__ __forceinline__ void put(int32_t s, int a, const P* from) {
+        P* to = slots + (s * N + a) * threads;
+        if constexpr (sizeof(P) >= 4) ptx::cp_async_n<sizeof(P)>(ptx::smem_u32(to), from);
+        else *to = *from;
+    }
+    // The first rows of `count`: from(a, i) is row i of matrix a.
+    template <typename From>
+    __device__ __forceinline__ void begin(int32_t count, From&& from) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) {
+            if (i < count)
+#pragma unroll
+                for (int a = 0; a < N; ++a) put(i, a, from(a, i));
+            ptx::cp_async_commit();
+        }
+    }
+    // use(i, vectors) for each row in turn, after begin with at least as many.
+    template <typename From, typename Use>
+    __device__ __forceinline__ void run(int32_t count, From&& from, Use&& use) {
+        int32_t s = 0;
+#pragma unroll 2
+        for (int32_t i = 0; i < count; ++i) {
+            ptx::cp_async_wait_group<D - 1>();
+            P q[N];
+#pragma unroll
+            for (int a = 0; a < N; ++a) q[a] = *(slots + (s * N + a) * threads);
+            use(i, q);
+            if (i + D < count)
+#pragma unroll
+                for (int a = 0; a < N; ++a) put(s, a, from(a, i + D));
+            ptx::cp_async_commit();
+            s = s + 1 == D ? 0 : s + 1;
+        }
+        ptx::cp_async_wait_all();   // (what was begun past `count`)
+    }
+};
+constexpr int kDeep = 6;         // rows of one matrix ahead
+constexpr int kDeepGrad = 4;     // of two
+
 // Rows of no scan, by the block.
 template <typename P>
 __device__ __forceinline__ void zero_rows(const Shape& h, void* out, int32_t lo, int32_t hi) {
@@ -336,8 +383,9 @@ struct Affine {
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads, 2) k_group_stats(const __grid_constant__ NormPass p) {
     using P = Pack<T, W>;
-    constexpr int U = 4;
-    extern __shared__ float sh[];
+    extern __shared__ __align__(16) uint8_t sh_raw[];
+    Stream<P, 1, kDeep> stream(sh_raw);
+    float* sh = reinterpret_cast<float*>(sh_raw + stream.bytes(blockDim.x));
     const Shape& h = p.h;
     const int32_t entries = h.c >> h.shift;
     float* sh_mean = sh;                                            // [ty][entries]
@@ -349,23 +397,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_group_stats(const __grid_consta
     pdl_wait();
     pdl_trigger();
     // the first rows are on their way while the offsets are read
-    P q[U];
-    if (ty < h.ty) load_rows(q, x0 + tx * W, p.a.ldx, row0 + ty, h.ty, row1);
+    auto rows_from = [&](int32_t first, int32_t v) {
+        return [=, &p, &h](int, int32_t i) { return reinterpret_cast<const P*>(x0 + v * W + (first + ty + i * h.ty) * p.a.ldx); };
+    };
+    if (ty < h.ty) stream.begin(Deal(row1 - row0, h).of(ty), rows_from(row0, tx));
     p.scans.pieces(row0, row1, [&](int32_t s, int32_t lo, int32_t hi) {
         if (s < 0 || s >= p.scans.scans) return;
         const Deal deal(hi - lo, h);
         for (int32_t v = tx; v < h.vectors && ty < deal.deep; v += h.tx) {
-            const T* x = x0 + v * W;
-            if (lo != row0 || v != tx) load_rows(q, x, p.a.ldx, lo + ty, h.ty, hi);
-            Moments<W> m;
-            m.begin(q[0]);
-            for (int32_t r = lo + ty; r < hi;) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (r + u * h.ty < hi) m.add(q[u]);
-                r += U * h.ty;
-                load_rows(q, x, p.a.ldx, r, h.ty, hi);
+            const auto from = rows_from(lo, v);
+            if (lo != row0 || v != tx) {
+                ptx::cp_async_wait_all();
+                stream.begin(deal.of(ty), from);
             }
+            Moments<W> m;
+            stream.run(deal.of(ty), from, [&](int32_t i, const P (&q)[1]) {
+                if (i == 0) m.begin(q[0]);
+                m.add(q[0]);
+            });
             m.write(static_cast<float>(deal.of(ty)), h.shift, sh_mean, sh_m2, ty * entries + ((v * W) >> h.shift));
         }
         __syncthreads();
@@ -374,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_group_stats(const __grid_consta
         });
         __syncthreads();
     });
+    ptx::cp_async_wait_all();
 }
 
 // The pieces of a scan's group: mean and 1 / sqrt(var + eps) for all of the warp.
@@ -398,8 +448,9 @@ __device__ __forceinline__ float2 join_pieces(const NormPass& p, int32_t g, int3
 template <typename T, int W>
 __global__ void __launch_bounds__(kApplyThreads, 2) k_group_apply(const __grid_constant__ NormPass p) {
     using P = Pack<T, W>;
-    constexpr int U = 4;
-    extern __shared__ float2 sh_stats[];   // [groups]
+    extern __shared__ __align__(16) uint8_t sh_raw[];
+    Stream<P, 1, kDeep> stream(sh_raw);
+    float2* sh_stats = reinterpret_cast<float2*>(sh_raw + stream.bytes(blockDim.x));   // [groups]
     const Shape& h = p.h;
     const GroupNormArgs& a = p.a;
     const int ty = h.by_tx(threadIdx.x), tx = threadIdx.x - ty * h.tx, lane = threadIdx.x & 31;
@@ -410,8 +461,10 @@ __global__ void __launch_bounds__(kApplyThreads, 2) k_group_apply(const __grid_c
     T* out = static_cast<T*>(a.out);
     // The kernel before this one began once all before it had ended, so what the caller
     // gave may be read already; only the pieces' sums and what is written here wait.
-    P q[U];
-    if (ty < h.ty) load_rows(q, x0 + tx * W, a.ldx, row0 + ty, h.ty, row1);
+    auto rows_from = [&](int32_t first, int32_t v) {
+        return [=, &a, &h](int, int32_t i) { return reinterpret_cast<const P*>(x0 + v * W + (first + ty + i * h.ty) * a.ldx); };
+    };
+    if (ty < h.ty) stream.begin(Deal(row1 - row0, h).of(ty), rows_from(row0, tx));
     bool waited = false;
     auto wait = [&]() {
         if (!waited) {
@@ -441,22 +494,26 @@ __global__ void __launch_bounds__(kApplyThreads, 2) k_group_apply(const __grid_c
             }
         }
         __syncthreads();
+        const Deal deal(hi - lo, h);
         with_act(a.act, [&](auto act) {
-            for (int32_t v = tx; v < h.vectors && ty < h.ty; v += h.tx) {
-                const T* x = x0 + v * W;
-                if (lo != row0 || v != tx) load_rows(q, x, a.ldx, lo + ty, h.ty, hi);
+            for (int32_t v = tx; v < h.vectors && ty < deal.deep; v += h.tx) {
+                const auto from = rows_from(lo, v);
+                if (lo != row0 || v != tx) {
+                    ptx::cp_async_wait_all();
+                    stream.begin(deal.of(ty), from);
+                }
                 Affine<W> f;
                 f.load(p, sh_stats, v);
-                for (int32_t r = lo + ty; r < hi;) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (r + u * h.ty < hi) *reinterpret_cast<P*>(out + static_cast<int64_t>(r + u * h.ty) * h.c + v * W) = f.template apply<act>(q[u]);
-                    r += U * h.ty;
-                    load_rows(q, x, a.ldx, r, h.ty, hi);
-                }
+                P* y = reinterpret_cast<P*>(out + static_cast<int64_t>(lo + ty) * h.c + v * W);
+                const int64_t step = static_cast<int64_t>(h.ty) * h.vectors;
+                stream.run(deal.of(ty), from, [&](int32_t, const P (&q)[1]) {
+                    *y = f.template apply<act>(q[0]);
+                    y += step;
+                });
             }
         });
     });
+    ptx::cp_async_wait_all();
     wait();
     if (p.scans.offsets) {
         // borders out of order or range; what the scans without a row have for statistics
@@ -832,7 +889,9 @@ struct GradAffine {
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads, 1) k_group_grad_sums(const __grid_constant__ GradPass p) {
     using P = Pack<T, W>;
-    extern __shared__ float sh[];
+    extern __shared__ __align__(16) uint8_t sh_raw[];
+    Stream<P, 2, kDeepGrad> stream(sh_raw);
+    float* sh = reinterpret_cast<float*>(sh_raw + stream.bytes(blockDim.x));
     const Shape& h = p.h;
     float* total = sh;                                              // [2][c]: of all pieces
     float* sh_u = sh + 2 * h.c;                                     // [ty][c]: sums of dz u
@@ -842,59 +901,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_grad_sums(const __grid_co
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
     const T* x0 = static_cast<const T*>(p.a.x);
     const T* dy0 = static_cast<const T*>(p.a.dy);
-    constexpr int U = 2;
-    P qx[U], qd[U];
     pdl_wait();
     pdl_trigger();
-    if (ty < h.ty) {
-        load_rows(qx, x0 + tx * W, p.a.ldx, row0 + ty, h.ty, row1);
-        load_rows(qd, dy0 + tx * W, p.a.ldy, row0 + ty, h.ty, row1);
-    }
+    auto rows_from = [&](int32_t first, int32_t v) {
+        return [=, &p, &h](int m, int32_t i) {
+            const int32_t row = first + ty + i * h.ty;
+            return reinterpret_cast<const P*>(m ? dy0 + v * W + row * p.a.ldy : x0 + v * W + row * p.a.ldx);
+        };
+    };
+    if (ty < h.ty) stream.begin(Deal(row1 - row0, h).of(ty), rows_from(row0, tx));
     for (int32_t i = threadIdx.x; i < 2 * h.c; i += blockDim.x) total[i] = 0.0f;
     p.scans.pieces(row0, row1, [&](int32_t s, int32_t lo, int32_t hi) {
         if (s < 0 || s >= p.scans.scans) return;
+        const Deal deal(hi - lo, h);
         with_act(p.a.act, [&](auto act) {
-            for (int32_t v = tx; v < h.vectors && ty < h.ty; v += h.tx) {
-                const T* x = x0 + v * W;
-                const T* dy = dy0 + v * W;
+            for (int32_t v = tx; v < h.vectors && ty < deal.deep; v += h.tx) {
+                const auto from = rows_from(lo, v);
                 if (lo != row0 || v != tx) {
-                    load_rows(qx, x, p.a.ldx, lo + ty, h.ty, hi);
-                    load_rows(qd, dy, p.a.ldy, lo + ty, h.ty, hi);
+                    ptx::cp_async_wait_all();
+                    stream.begin(deal.of(ty), from);
                 }
                 Channels<W> ch;
                 ch.load(p, s, v);
                 GradSums<W> sums;
                 sums.begin();
-                for (int32_t r = lo + ty; r < hi;) {
-#pragma unroll
-                    for (int k = 0; k < U; ++k)
-                        if (r + k * h.ty < hi) sums.template add<act>(ch, qx[k], qd[k]);
-                    r += U * h.ty;
-                    load_rows(qx, x, p.a.ldx, r, h.ty, hi);
-                    load_rows(qd, dy, p.a.ldy, r, h.ty, hi);
-                }
+                stream.run(deal.of(ty), from, [&](int32_t, const P (&q)[2]) { sums.template add<act>(ch, q[0], q[1]); });
                 sums.write(sh_u + ty * h.c + v * W, sh_z + ty * h.c + v * W);
             }
         });
-        join_grad_threads(p, hi - lo < h.ty ? hi - lo : h.ty, total, sh_u, sh_z,
+        join_grad_threads(p, deal.deep, total, sh_u, sh_z,
                           [&](int32_t g, float z, float u) { p.part[slot_of(h, g, s)] = make_float2(z, u); });
     });
+    ptx::cp_async_wait_all();
     __syncthreads();
     for (int32_t i = threadIdx.x; i < 2 * h.c; i += blockDim.x) p.cols[static_cast<int64_t>(blockIdx.x) * 2 * h.c + i] = total[i];
 }
 
-// Columns of the blocks' sums: 32 of them a block of kThreads, 16 threads down each.
+// Columns of the blocks' sums: kColumns of them a block, the other threads down each.
+constexpr int kColumns = 8;
 __device__ __forceinline__ void add_columns(const GradPass& p, int32_t blocks, float* sh) {
-    const int32_t col = static_cast<int32_t>(blockIdx.x) * 32 + (threadIdx.x & 31), deep = threadIdx.x >> 5;
-    const int32_t down = static_cast<int32_t>(blockDim.x) / 32;
+    const int32_t col = static_cast<int32_t>(blockIdx.x) * kColumns + (threadIdx.x & (kColumns - 1));
+    const int32_t down = static_cast<int32_t>(blockDim.x) / kColumns;
     float sum = 0.0f;
     if (col < 2 * p.h.c)
-#pragma unroll 4
-        for (int32_t b = deep; b < blocks; b += down) sum += __ldcg(p.cols + static_cast<int64_t>(b) * 2 * p.h.c + col);
-    sh[threadIdx.x] = sum;
+#pragma unroll 8
+        for (int32_t b = threadIdx.x / kColumns; b < blocks; b += down) sum += __ldcg(p.cols + static_cast<int64_t>(b) * 2 * p.h.c + col);
+#pragma unroll
+    for (int32_t o = kColumns; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if ((threadIdx.x & 31) < kColumns) sh[(threadIdx.x >> 5) * kColumns + (threadIdx.x & 31)] = sum;
     __syncthreads();
-    if (deep != 0 || col >= 2 * p.h.c) return;
-    for (int32_t t = 1; t < down; ++t) sum += sh[t * 32 + threadIdx.x];
+    if (threadIdx.x >= kColumns || col >= 2 * p.h.c) return;
+    sum = sh[threadIdx.x];
+    for (int32_t w = 1; w < static_cast<int32_t>(blockDim.x >> 5); ++w) sum += sh[w * kColumns + threadIdx.x];
     if (col < p.h.c) p.a.dweight[col] = sum;
     else if (p.a.dbias) p.a.dbias[col - p.h.c] = sum;
 }
@@ -902,7 +960,9 @@ __device__ __forceinline__ void add_columns(const GradPass& p, int32_t blocks, f
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads, 1) k_group_grad_apply(const __grid_constant__ GradPass p) {
     using P = Pack<T, W>;
-    extern __shared__ float sh[];
+    extern __shared__ __align__(16) uint8_t sh_raw[];
+    Stream<P, 2, kDeepGrad> stream(sh_raw);
+    float* sh = reinterpret_cast<float*>(sh_raw + stream.bytes(blockDim.x));
     const Shape& h = p.h;
     const GroupNormGradArgs& a = p.a;
     float2* sh_means = reinterpret_cast<float2*>(sh);   // [groups]: of p, of p u
@@ -920,12 +980,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_grad_apply(const __grid_c
     const T* dy0 = static_cast<const T*>(a.dy);
     T* out = static_cast<T*>(a.dx);
     // (as in the forward pass, what the caller gave may be read before the wait)
-    constexpr int U = 2;
-    P qx[U], qd[U];
-    if (ty < h.ty) {
-        load_rows(qx, x0 + tx * W, a.ldx, row0 + ty, h.ty, row1);
-        load_rows(qd, dy0 + tx * W, a.ldy, row0 + ty, h.ty, row1);
-    }
+    auto rows_from = [&](int32_t first, int32_t v) {
+        return [=, &p, &h](int m, int32_t i) {
+            const int32_t row = first + ty + i * h.ty;
+            return reinterpret_cast<const P*>(m ? dy0 + v * W + row * p.a.ldy : x0 + v * W + row * p.a.ldx);
+        };
+    };
+    if (ty < h.ty) stream.begin(Deal(row1 - row0, h).of(ty), rows_from(row0, tx));
     bool waited = false;
     auto wait = [&]() {
         if (!waited) {
@@ -965,28 +1026,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_grad_apply(const __grid_c
             }
         }
         __syncthreads();
+        const Deal deal(hi - lo, h);
         with_act(a.act, [&](auto act) {
-            for (int32_t v = tx; v < h.vectors && ty < h.ty; v += h.tx) {
-                const T* x = x0 + v * W;
-                const T* dy = dy0 + v * W;
+            for (int32_t v = tx; v < h.vectors && ty < deal.deep; v += h.tx) {
+                const auto from = rows_from(lo, v);
                 if (lo != row0 || v != tx) {
-                    load_rows(qx, x, a.ldx, lo + ty, h.ty, hi);
-                    load_rows(qd, dy, a.ldy, lo + ty, h.ty, hi);
+                    ptx::cp_async_wait_all();
+                    stream.begin(deal.of(ty), from);
                 }
                 GradAffine<W> f;
                 f.load(p, sh_means, s, v);
-                for (int32_t r = lo + ty; r < hi;) {
-#pragma unroll
-                    for (int k = 0; k < U; ++k)
-                        if (r + k * h.ty < hi)
-                            *reinterpret_cast<P*>(out + static_cast<int64_t>(r + k * h.ty) * h.c + v * W) = f.template apply<act>(qx[k], qd[k]);
-                    r += U * h.ty;
-                    load_rows(qx, x, a.ldx, r, h.ty, hi);
-                    load_rows(qd, dy, a.ldy, r, h.ty, hi);
-                }
+                P* dx = reinterpret_cast<P*>(out + static_cast<int64_t>(lo + ty) * h.c + v * W);
+                const int64_t step = static_cast<int64_t>(h.ty) * h.vectors;
+                stream.run(deal.of(ty), from, [&](int32_t, const P (&q)[2]) {
+                    *dx = f.template apply<act>(q[0], q[1]);
+                    dx += step;
+                });
             }
         });
     });
+    ptx::cp_async_wait_all();
     wait();
     if (p.scans.offsets)
         for (int32_t s = index * blockDim.x + threadIdx.x; s < p.scans.scans; s += h.blocks * blockDim.x) {
@@ -1042,7 +1101,7 @@ Shape make_shape(int64_t n, int32_t c, int32_t groups, int64_t scans, int w, siz
     *threads = set_threads(&h, *large ? kThreads / 2 : kThreads);
     int64_t blocks = ceil_div(n, static_cast<int64_t>(4) * h.ty);   // (one step of loads each, at least)
     int64_t limit = *large ? ceil_div(n * c * static_cast<int64_t>(es), kBlockBytes) : kSms;
-    if (*large && limit < 2 * kSms) limit = 2 * kSms;
+    if (*large && limit < 4 * kSms) limit = 4 * kSms;
     if (blocks > limit) blocks = limit;
     h.rows = static_cast<int32_t>(ceil_div(n, blocks));
     h.blocks = static_cast<int32_t>(ceil_div(n, h.rows));
@@ -1136,14 +1195,15 @@ int forward_w(const GroupNormArgs& a, cudaStream_t s) {
     Scratch part(part_bytes + stats_bytes, s);
     if (part.failed()) return SPCONV_ERR_OOM;
     p.part = part.as<float2>();
-    SPCONV_CHECK((launch_wide<k_group_stats<T, W>>(p.h.blocks, threads, static_cast<size_t>(2) * p.h.ty * (a.c >> p.h.shift) * 4, s, p)));
+    using Rows1 = Stream<Pack<T, W>, 1, kDeep>;
+    SPCONV_CHECK((launch_wide<k_group_stats<T, W>>(p.h.blocks, threads, Rows1::bytes(threads) + static_cast<size_t>(2) * p.h.ty * (a.c >> p.h.shift) * 4, s, p)));
     if (large) {
         float2* stats = a.stats ? a.stats : part.as<float2>(part_bytes);
         SPCONV_CHECK(launch_join(k_group_join<32>, k_group_join<256>, p, stats, s));
         p.stats = stats;
     }
     threads = set_threads(&p.h, large ? kApplyThreads / 2 : kApplyThreads);
-    return launch_wide<k_group_apply<T, W>>(p.h.blocks, threads, static_cast<size_t>(2) * a.groups * 4, s, p);
+    return launch_wide<k_group_apply<T, W>>(p.h.blocks, threads, Rows1::bytes(threads) + static_cast<size_t>(2) * a.groups * 4, s, p);
 }
 
 template <typename T, int W>
@@ -1162,16 +1222,17 @@ int backward_w(const GroupNormGradArgs& a, cudaStream_t s) {
     if (buf.failed()) return SPCONV_ERR_OOM;
     p.part = buf.as<float2>();
     p.cols = buf.as<float>(part_bytes + sums_bytes);
-    SPCONV_CHECK((launch_wide<k_group_grad_sums<T, W>>(p.h.blocks, threads, static_cast<size_t>(2) * (p.h.ty + 1) * a.c * 4, s, p)));
+    using Rows2 = Stream<Pack<T, W>, 2, kDeepGrad>;
+    SPCONV_CHECK((launch_wide<k_group_grad_sums<T, W>>(p.h.blocks, threads, Rows2::bytes(threads) + static_cast<size_t>(2) * (p.h.ty + 1) * a.c * 4, s, p)));
     if (large) {
         float2* sums = buf.as<float2>(part_bytes);
         SPCONV_CHECK(launch_join(k_group_grad_join<32>, k_group_grad_join<256>, p, sums, s));
         p.sums = sums;
     }
-    p.col_blocks = static_cast<int32_t>(ceil_div(2 * a.c, 32));
+    p.col_blocks = static_cast<int32_t>(ceil_div(2 * a.c, kColumns));
     size_t smem = static_cast<size_t>(2) * a.groups * 4;
     if (smem < kThreads * 4) smem = kThreads * 4;
-    return launch_wide<k_group_grad_apply<T, W>>(p.h.blocks + p.col_blocks, threads, smem, s, p);
+    return launch_wide<k_group_grad_apply<T, W>>(p.h.blocks + p.col_blocks, threads, Rows2::bytes(threads) + smem, s, p);
 }
 
 }  // namespace

@@ -109,9 +109,11 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src, 
                  : "memory");
 }
 
-// Copies 4 bytes (through L1).
-__device__ __forceinline__ void cp_async_4(uint32_t dst_smem, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_smem), "l"(src) : "memory");
+// Copies 4, 8 (through L1) or 16 bytes.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_n(uint32_t dst_smem, const void* src) {
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst_smem), "l"(src), "n"(BYTES) : "memory");
 }
 
 __device__ __forceinline__ void st_shared_zero16(uint32_t dst_smem) {
