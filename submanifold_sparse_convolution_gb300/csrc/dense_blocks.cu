@@ -972,7 +972,10 @@ int run_few(const BlockOp& op, const BlockArgs& p, int64_t active, cudaStream_t 
     int32_t splits = 1;
     while (splits < kMaxSplits && tiles * active * splits * 2 <= 304 && p.kb >= 4 * splits) splits *= 2;
     a.stage_bytes = (DUAL ? 2 : 1) * kTileW + R * 128;
-    a.stages = kFewRing / a.stage_bytes < kMaxStages ? kFewRing / a.stage_bytes : kMaxStages;
+    // a smaller ring where all CTAs then run at once and do not otherwise
+    const int64_t ctas = tiles * active * splits;
+    const int32_t ring = R == 16 && !DUAL && ctas > 304 && ctas <= 608 ? kFewRing / 2 : kFewRing;
+    a.stages = ring / a.stage_bytes < kMaxStages ? ring / a.stage_bytes : kMaxStages;
     SPCONV_CHECK((allow_smem<k_blocks_few<DUAL, EIGHT, R>>(kFewRing + 1024)));
     cudaLaunchAttribute at[2] = {pdl_attr(), {}};
     at[1].id = cudaLaunchAttributeClusterDimension;
@@ -982,7 +985,7 @@ int run_few(const BlockOp& op, const BlockArgs& p, int64_t active, cudaStream_t 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(splits), static_cast<unsigned>(op.experts));
     cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = kFewRing + 1024;
+    cfg.dynamicSmemBytes = static_cast<size_t>(ring) + 1024;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 2;

@@ -211,45 +211,51 @@ __global__ void __launch_bounds__(256) k_expert_gather(const ExpertRows a) {
 // lie halfway between two e4m3 ones, where the scale's last bit decides.
 //
 // Without slots a row keeps its place (spconv_quantize_blocks).
-template <typename T, int W>
+template <typename T, int W, int ROWS>
 __global__ void __launch_bounds__(256) k_rows_to_blocks(const ExpertRows a) {
     using P = Pack<T, W>;
     pdl_wait();
     pdl_trigger();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int32_t blocks = (a.c + 127) / 128;
-    const int64_t t = i / (blocks * 16);
-    const int64_t rows = a.tokens * a.k;
-    const int32_t v = static_cast<int32_t>(i - t * (blocks * 16)), e = v * 8;
-    float f[8];
+    const int64_t t0 = i / (blocks * 16), rows = a.tokens * a.k, apart = (a.tokens + ROWS - 1) / ROWS;
+    const int32_t v = static_cast<int32_t>(i - t0 * (blocks * 16)), e = v * 8;
+    uint8_t* out = static_cast<uint8_t*>(a.out);
+    // the vectors of ROWS rows are on their way together
+    P x[ROWS][8 / W];
+    bool live[ROWS];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-    const bool live = t < a.tokens && e < a.c;
-    if (live) {
-        const T* x = static_cast<const T*>(a.x) + t * a.ldx + e;
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t t = t0 + r * apart;
+        live[r] = t0 < apart && t < a.tokens && e < a.c;
 #pragma unroll
         for (int j = 0; j < 8; j += W)
-            if (e + j < a.c) {
-                float g[W];
-                unpack<W>(*reinterpret_cast<const P*>(x + j), g);
-#pragma unroll
-                for (int u = 0; u < W; ++u) f[j + u] = g[u];
-            }
-    }
-    uint32_t most = 0;   // the bits of |x| order as whole numbers, NaN on top
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __float_as_uint(fabsf(f[j]));
-        most = b > most ? b : most;
+            if (live[r] && e + j < a.c) x[r][j / W] = *reinterpret_cast<const P*>(static_cast<const T*>(a.x) + t * a.ldx + e + j);
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-        const uint32_t u = __shfl_xor_sync(0xFFFFFFFFu, most, o);
-        most = u > most ? u : most;
-    }
-    const float scale = __fdiv_rn(__uint_as_float(most), 448.0f);
-    uint8_t* out = static_cast<uint8_t*>(a.out);
-    if (live) {
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t t = t0 + r * apart;
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += W) {
+            float g[W] = {};
+            if (live[r] && e + j < a.c) unpack<W>(x[r][j / W], g);
+#pragma unroll
+            for (int u = 0; u < W; ++u) f[j + u] = g[u];
+        }
+        uint32_t most = 0;   // the bits of |x| order as whole numbers, NaN on top
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = __float_as_uint(fabsf(f[j]));
+            most = b > most ? b : most;
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            const uint32_t u = __shfl_xor_sync(0xFFFFFFFFu, most, o);
+            most = u > most ? u : most;
+        }
+        const float scale = __fdiv_rn(__uint_as_float(most), 448.0f);
+        if (!live[r]) continue;
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = scale == 0.0f ? 0.0f : __fdiv_rn(f[j], scale);
         for (int32_t j = 0; j < a.k; ++j) {
@@ -492,9 +498,14 @@ int expert_gather(const ExpertRows& args, cudaStream_t s) {
     ExpertRows a = args;
     if (a.scale) {
         a.wide = a.c % 8 == 0 && bits(a.out) % 8 == 0;
+        // two rows a thread where one each would fill the GPU twice over
         const int64_t threads = a.tokens * ceil_div(a.c, 128) * 16;
-        return with_type(a.dtype, bits(a.x), a.ldx, a.c,
-                         [&](auto t, auto w) { return launch_flat(k_rows_to_blocks<decltype(t), w>, threads, s, a); });
+        const bool two = threads > 2 * 152 * 2048;
+        return with_type(a.dtype, bits(a.x), a.ldx, a.c, [&](auto t, auto w) {
+            using T = decltype(t);
+            return two ? launch_flat(k_rows_to_blocks<T, w, 2>, ceil_div(a.tokens, 2) * ceil_div(a.c, 128) * 16, s, a)
+                       : launch_flat(k_rows_to_blocks<T, w, 1>, threads, s, a);
+        });
     }
     return with_type(a.dtype, bits(a.x) | bits(a.out), a.ldx, a.c,
                      [&](auto t, auto w) { return launch_flat(k_expert_gather<decltype(t), w>, a.tokens * (a.c / w), s, a); });

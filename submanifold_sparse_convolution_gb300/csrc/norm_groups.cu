@@ -37,7 +37,7 @@ constexpr int kPerLane = 5;              // pieces that a lane adds up where a b
 static_assert(kSms <= 32 * kPerLane, "blocks of a small input");
 constexpr int kThreads = 448;            // blocks of a small input (72 registers a thread, two on an SM); half of it for those of a large one
 constexpr int kApplyThreads = 320;       // (96 registers a thread, and room on an SM beside a block of k_group_stats)
-constexpr int64_t kSmallBytes = 16 << 20, kBlockBytes = 256 << 10;
+constexpr int64_t kSmallBytes = 40 << 20, kBlockBytes = 256 << 10;
 constexpr int64_t kScanBytes = 512 << 10;
 constexpr int kMaxCluster = 8;           // portable cluster size
 
