@@ -168,6 +168,16 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_place(const SortArgs a)
     }
 }
 
+// Which row and which of its vectors a flat index is: by a product where the index
+// has 31 bits (a division of 64 bits takes longer than the rest).
+struct RowVector {
+    FastDiv by;
+    int32_t vectors, small;
+    RowVector(int64_t threads, int64_t vectors_)
+        : by(static_cast<uint32_t>(vectors_)), vectors(static_cast<int32_t>(vectors_)), small(threads + 256 < 0x7FFFFFFF) {}
+    __device__ __forceinline__ int64_t row(int64_t i) const { return small ? by(static_cast<int32_t>(i)) : i / vectors; }
+};
+
 // ---- rows to their slots ----------------------------------------------------------
 // Rows at and behind offsets[n_experts] have no pair: the blocks' threads write
 // zeros there.
@@ -181,12 +191,12 @@ __device__ __forceinline__ void zero_tail(V* out, int64_t row_vectors, const int
         out[i] = zero;
 }
 
-__device__ __forceinline__ bool in_range(int32_t slot, int64_t rows) {
-    return slot >= 0 && slot < rows;   // (whatever a caller's plan holds)
+__device__ __forceinline__ bool in_range(int64_t slot, int64_t rows) {
+    return static_cast<uint64_t>(slot) < static_cast<uint64_t>(rows);   // (whatever a caller's plan holds)
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(256) k_expert_gather(const ExpertRows a) {
+__global__ void __launch_bounds__(256) k_expert_gather(const ExpertRows a, const RowVector at) {
     using P = Pack<T, W>;
     pdl_wait();
     pdl_trigger();
@@ -195,7 +205,7 @@ __global__ void __launch_bounds__(256) k_expert_gather(const ExpertRows a) {
     const int64_t rows = a.tokens * a.k;
     P* out = static_cast<P*>(a.out);
     if (i < a.tokens * vectors) {
-        const int64_t t = i / vectors;
+        const int64_t t = at.row(i);
         const int32_t v = static_cast<int32_t>(i - t * vectors);
         const P x = *reinterpret_cast<const P*>(static_cast<const T*>(a.x) + t * a.ldx + v * W);
         for (int32_t j = 0; j < a.k; ++j) {
@@ -208,17 +218,21 @@ __global__ void __launch_bounds__(256) k_expert_gather(const ExpertRows a) {
 
 // A block of 128 values is half a warp's: eight values a lane.  scale = max |x| /
 // 448, q = e4m3(x / scale), both divisions rounded to nearest: bf16 values often
-// lie halfway between two e4m3 ones, where the scale's last bit decides.
+// lie halfway between two e4m3 ones, where the scale's last bit decides.  A division
+// is 25 instructions, so the product with the inverse, which is within 2.5 units in
+// the last place of it, is taken first, and the division only where that is within 4
+// of halfway between two e4m3 values (three mantissa bits: the other twenty are near
+// 0x80000) or below 2^-6, where those lie elsewhere.
 //
 // Without slots a row keeps its place (spconv_quantize_blocks).
 template <typename T, int W, int ROWS>
-__global__ void __launch_bounds__(256) k_rows_to_blocks(const ExpertRows a) {
+__global__ void __launch_bounds__(256) k_rows_to_blocks(const ExpertRows a, const RowVector at) {
     using P = Pack<T, W>;
     pdl_wait();
     pdl_trigger();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int32_t blocks = (a.c + 127) / 128;
-    const int64_t t0 = i / (blocks * 16), rows = a.tokens * a.k, apart = (a.tokens + ROWS - 1) / ROWS;
+    const int64_t t0 = at.row(i), rows = a.tokens * a.k, apart = (a.tokens + ROWS - 1) / ROWS;
     const int32_t v = static_cast<int32_t>(i - t0 * (blocks * 16)), e = v * 8;
     uint8_t* out = static_cast<uint8_t*>(a.out);
     // the vectors of ROWS rows are on their way together
@@ -256,20 +270,32 @@ __global__ void __launch_bounds__(256) k_rows_to_blocks(const ExpertRows a) {
         }
         const float scale = __fdiv_rn(__uint_as_float(most), 448.0f);
         if (!live[r]) continue;
+        const bool tiny = scale < 0x1p-100f;   // (its inverse may be infinite)
+        const float inverse = tiny ? 0.0f : __fdiv_rn(1.0f, scale);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = scale == 0.0f ? 0.0f : __fdiv_rn(f[j], scale);
+        for (int j = 0; j < 8; ++j) {
+            const float q = f[j] * inverse;
+            const uint32_t b = __float_as_uint(fabsf(q));
+            const bool near = ((b & 0xFFFFFu) - 0x7FFFCu) <= 8u || (b != 0 && b < 0x3C800000u);
+            if (tiny || near) f[j] = scale == 0.0f ? 0.0f : __fdiv_rn(f[j], scale);
+            else f[j] = q;
+        }
+        uint32_t q[2];   // eight e4m3 values
+        store_e4m3<8>(reinterpret_cast<uint8_t*>(q), f);
+        float* to_scale = v % 16 == 0 ? a.scale + static_cast<int64_t>(v / 16) * rows : nullptr;
+        const int32_t* slots = a.slots + t * a.k;
         for (int32_t j = 0; j < a.k; ++j) {
-            const int64_t slot = a.slots ? __ldg(a.slots + t * a.k + j) : t;
-            if (slot < 0 || slot >= rows) continue;
-            uint8_t* q = out + slot * a.c + e;
+            const int64_t slot = a.slots ? __ldg(slots + j) : t;
+            if (!in_range(slot, rows)) continue;
+            uint8_t* to = out + slot * a.c + e;
             if (a.wide) {
-                store_e4m3<8>(q, f);
+                *reinterpret_cast<uint2*>(to) = make_uint2(q[0], q[1]);
             } else {
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    if (e + u < a.c) store_e4m3<1>(q + u, f + u);
+                    if (e + u < a.c) to[u] = static_cast<uint8_t>(q[u / 4] >> (8 * (u % 4)));
             }
-            if (v % 16 == 0) a.scale[static_cast<int64_t>(v / 16) * rows + slot] = scale;
+            if (to_scale) to_scale[slot] = scale;
         }
     }
     if (a.slots) {
@@ -284,14 +310,14 @@ __global__ void __launch_bounds__(256) k_rows_to_blocks(const ExpertRows a) {
 // ---- slots to their rows ----------------------------------------------------------
 // Up to four choices' rows are in flight at once.
 template <typename T, int W>
-__global__ void __launch_bounds__(256) k_expert_combine(const ExpertSums a) {
+__global__ void __launch_bounds__(256) k_expert_combine(const ExpertSums a, const RowVector at) {
     using P = Pack<T, W>;
     pdl_wait();
     pdl_trigger();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int32_t vectors = a.c / W;
     if (i >= a.tokens * vectors) return;
-    const int64_t t = i / vectors, rows = a.tokens * a.k;
+    const int64_t t = at.row(i), rows = a.tokens * a.k;
     const int32_t v = static_cast<int32_t>(i - t * vectors);
     float sum[W] = {};
     if (a.residual) unpack<W>(*reinterpret_cast<const P*>(static_cast<const T*>(a.residual) + t * a.ldr + v * W), sum);
@@ -450,11 +476,12 @@ int with_type(int32_t dtype, uintptr_t all, int64_t ld, int32_t c, F&& f) {
 
 uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
+// A thread a vector of `rows` rows.
 template <typename... K, typename A>
-int launch_flat(void (*kernel)(K...), int64_t threads, cudaStream_t s, const A& a) {
-    const int64_t blocks = ceil_div(threads, 256);
+int launch_flat(void (*kernel)(K...), int64_t rows, int64_t vectors, cudaStream_t s, const A& a) {
+    const int64_t blocks = ceil_div(rows * vectors, 256);
     if (blocks > 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a, RowVector(rows * vectors, vectors));
 }
 
 template <typename I>
@@ -503,17 +530,17 @@ int expert_gather(const ExpertRows& args, cudaStream_t s) {
         const bool two = threads > 2 * 152 * 2048;
         return with_type(a.dtype, bits(a.x), a.ldx, a.c, [&](auto t, auto w) {
             using T = decltype(t);
-            return two ? launch_flat(k_rows_to_blocks<T, w, 2>, ceil_div(a.tokens, 2) * ceil_div(a.c, 128) * 16, s, a)
-                       : launch_flat(k_rows_to_blocks<T, w, 1>, threads, s, a);
+            return two ? launch_flat(k_rows_to_blocks<T, w, 2>, ceil_div(a.tokens, 2), ceil_div(a.c, 128) * 16, s, a)
+                       : launch_flat(k_rows_to_blocks<T, w, 1>, a.tokens, ceil_div(a.c, 128) * 16, s, a);
         });
     }
     return with_type(a.dtype, bits(a.x) | bits(a.out), a.ldx, a.c,
-                     [&](auto t, auto w) { return launch_flat(k_expert_gather<decltype(t), w>, a.tokens * (a.c / w), s, a); });
+                     [&](auto t, auto w) { return launch_flat(k_expert_gather<decltype(t), w>, a.tokens, a.c / w, s, a); });
 }
 
 int expert_combine(const ExpertSums& a, cudaStream_t s) {
     return with_type(a.dtype, bits(a.y) | bits(a.residual) | bits(a.out), a.residual ? a.ldy | a.ldr : a.ldy, a.c,
-                     [&](auto t, auto w) { return launch_flat(k_expert_combine<decltype(t), w>, a.tokens * (a.c / w), s, a); });
+                     [&](auto t, auto w) { return launch_flat(k_expert_combine<decltype(t), w>, a.tokens, a.c / w, s, a); });
 }
 
 int expert_combine_backward(const ExpertGrad& a, cudaStream_t s) {
