@@ -37,13 +37,14 @@ constexpr int kFirstEpi = 4;             // warp 0 loads, warp 1 issues MMAs, wa
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kStaging = 32 * 128;       // of an epilogue warp: twice 32 rows of 32 bf16, or 32 of 128 e4m3
 constexpr int kScaleSlots = 4;           // blocks of K whose scales lie in shared memory: [2 blocks of columns][128 rows] each
-constexpr int kScaleBytes = kScaleSlots * 2 * 128 * 4 + kEpiWarps * 16;   // (and the epilogue warps' tiles)
+constexpr int kBiasSlots = 4;            // tiles whose bias lies in shared memory: [256 columns] each
+constexpr int kScaleBytes = kScaleSlots * 2 * 128 * 4 + kBiasSlots * 256 * 4 + kEpiWarps * 16;   // (and the epilogue warps' tiles)
 // Registers a thread: 168 at the launch (three warps on each quarter of an SM), then
-// 56 for the first four warps and 224 for the others (gated: 88 and 208, which is
-// where neither side spills).
-template <bool DUAL>
+// 80 for the first four warps and 208 for the others (bf16 results of one product,
+// which have a residual on its way: 56 and 224): where neither side spills.
+template <bool DUAL, bool EIGHT>
 struct Regs {
-    static constexpr int first = DUAL ? 88 : 56, epi = DUAL ? 208 : 224;
+    static constexpr int first = DUAL || EIGHT ? 80 : 56, epi = DUAL || EIGHT ? 208 : 224;
     static_assert(128 * first + 32 * kEpiWarps * epi <= kThreads * 168, "register split");
 };
 constexpr int kTableSize = 256;
@@ -75,7 +76,7 @@ struct Runs {
 };
 
 struct BlockArgs {
-    CUtensorMap x, w[2], c;   // c: of out, where map_out
+    CUtensorMap x, w[2], c, map_extra;   // c: of out, where map_out; map_extra: where vec_extra
     Runs runs;
     int32_t h;                // columns of an expert's weight
     int32_t kb;               // blocks of K
@@ -219,7 +220,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
     uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
     uint8_t* staging = smem + S * kStage;
     float* scales = reinterpret_cast<float*>(staging + kEpiWarps * kStaging);
-    int4* tiles = reinterpret_cast<int4*>(scales + kScaleSlots * 256);   // [kEpiWarps]
+    float* biases = scales + kScaleSlots * 256;
+    int4* tiles = reinterpret_cast<int4*>(biases + kBiasSlots * 256);   // [kEpiWarps]
     uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging + kScaleBytes);   // [S]  (CTA 0's are used)
     uint64_t* empty = full + S;             // [S]
     uint64_t* acc_full = empty + S;         // [2]
@@ -294,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
     };
     auto tile_at = [&](int32_t k, Tile& t) { return find_tile<DUAL ? 128 : 256>(p, table, k, t); };
     uint32_t fills = 0;   // stages this thread has filled
-    if (warp < kFirstEpi) ptx::regs_dec<Regs<DUAL>::first>();
+    if (warp < kFirstEpi) ptx::regs_dec<Regs<DUAL, EIGHT>::first>();
     if (warp == 0) {
         if (lane == 0) {
             uint32_t& f = fills;
@@ -304,6 +306,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                 const int32_t r0 = t.row + static_cast<int32_t>(rank) * 128;
                 const int32_t o0 = t.e * p.h + (DUAL ? t.tn * 128 : t.tn * 256 + static_cast<int32_t>(rank) * 128);
                 const CUtensorMap* w = &p.w[DUAL ? rank : 0];
+                if (!DUAL && p.vec_extra)   // the residual to L2
+                    for (int32_t o = t.tn * 256; o < p.h && o < t.tn * 256 + 256; o += 64) ptx::tma_prefetch_2d(&p.map_extra, o, r0);
 #pragma unroll 1
                 for (int32_t it = 0; it < p.kb; ++it, ++f) {
                     const uint32_t s = f % S;
@@ -354,6 +358,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                         v[j][r] = it0 + j < p.kb && row + 32 * r < t.end ? __ldg(xs + static_cast<int64_t>(it0 + j) * p.runs.n + 32 * r) : 0.0f;
             };
             load(x[0], 0);
+            if (!DUAL && p.bias) {   // (once the slot's tile before has been added up: as for the first block's scales)
+                if (f >= 2 && !warp_wait(&acc_full[f & 1], ((f >> 1) - 1) & 1)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+#pragma unroll
+                for (int k = 0; k < 256; k += 32) {
+                    const int32_t o = t.tn * 256 + k + lane;
+                    biases[(q & (kBiasSlots - 1)) * 256 + k + lane] = o < p.h ? __ldg(p.bias + static_cast<int64_t>(t.e) * p.h + o) : 0.0f;
+                }
+            }
 #pragma unroll 1
             for (int32_t it0 = 0; ok && it0 < p.kb; it0 += 2 * G) {
                 if ((it0 & 31) == 0) {   // one block's in each lane
@@ -387,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
             }
         }
     } else if (warp >= kFirstEpi) {
-        ptx::regs_inc<Regs<DUAL>::epi>();
+        ptx::regs_inc<Regs<DUAL, EIGHT>::epi>();
         const int e = warp - kFirstEpi;
         const int quarter = warp & 3, part = e >> 2;   // TMEM lanes; half of the columns
         uint8_t* stage0 = staging + e * kStaging;
@@ -408,6 +423,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = F2(0.0f);
             bool ready = false;
+            if (!DUAL && p.bias) {   // the sums begin with it: it comes with the first block's scales
+                ready = ptx::mbar_wait(&acc_full[f & 1], (f >> 1) & 1, abort_flag);
+                __syncwarp();
+                const volatile float4* bias = reinterpret_cast<const volatile float4*>(biases + (q & (kBiasSlots - 1)) * 256 + part * 128);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    acc[2 * j] = F2(bias[j].x, bias[j].y);
+                    acc[2 * j + 1] = F2(bias[j].z, bias[j].w);
+                }
+            }
             // What can is done while TMEM's loads or the multiply-adds run: a warp has about 600
             // clocks a block for all of it, and only one other warp to share them with.
 #pragma unroll 1
@@ -449,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                 add(3);
             }
             if (!ok) break;
-            const int32_t expert = tile->x, end = tile->z;
+            const int32_t end = tile->z;
             const int32_t m0 = tile->y + static_cast<int32_t>(ptx::cluster_rank()) * 128 + quarter * 32, row = m0 + lane;
             const int32_t n0 = tile->w * kTileN + part * kOut;   // first output column
             const int32_t rows = end - m0 < 32 ? end - m0 : 32, left = p.h - n0;   // (either may be negative)
@@ -457,62 +482,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
             // Whole groups of 32 rows leave by tensor-map copies, which nobody waits for; a run's
             // last ones, which a copy would not clip, and unaligned outputs by plain stores.
             const bool mapped = p.map_out && rows == 32;
-            // For bias and activation sums are moved, kCols columns at a time, to where one copy of
-            // the code finds them: unrolled over all of them it needs more registers than there are.
-            constexpr int kCols = DUAL && !EIGHT ? 32 : 16;
-            auto pick = [&](int c, F2 (&v)[kCols / 2]) {   // the c-th columns, activated
-                F2 u[kCols / 2];
+            // Activations in place, 16 columns at a time: the empty statement keeps the compiler
+            // from joining them, which would take more registers than there are.
+            auto activate = [&]() {
 #pragma unroll
-                for (int k = 0; k < kOut / kCols; ++k)
-                    if (c == k) {
+                for (int c = 0; c < kOut / 2; c += 8) {
+                    int32_t a = p.act;
+                    asm volatile("" : "+r"(a));
+                    with_act(a, [&](auto act) {
 #pragma unroll
-                        for (int j = 0; j < kCols / 2; ++j) {
-                            v[j] = acc[k * (kCols / 2) + j];
-                            if (DUAL) u[j] = acc[(k * (kCols / 2) + j + 32) % 64];
-                        }
-                    }
-                if (!DUAL) {
-                    const float4* bias = reinterpret_cast<const float4*>(stage0 + c * kCols * 4);
-#pragma unroll
-                    for (int j = 0; j < kCols / 4; ++j) {
-                        const float4 b = bias[j];
-                        v[2 * j] = v[2 * j] + F2(b.x, b.y);
-                        v[2 * j + 1] = v[2 * j + 1] + F2(b.z, b.w);
-                    }
+                        for (int j = c; j < c + 8; ++j) acc[j] = DUAL ? act_f<act>(acc[j]) * acc[(j + 32) % 64] : act_f<act>(acc[j]);
+                    });
                 }
-                with_act(p.act, [&](auto act) {
-#pragma unroll
-                    for (int j = 0; j < kCols / 2; ++j) v[j] = DUAL ? act_f<act>(v[j]) * u[j] : act_f<act>(v[j]);
-                });
             };
-            auto activate = [&]() {   // in place; the bias lies in the staging buffer meanwhile
-                if (!DUAL) {
-                    if (lane == 0) ptx::bulk_wait_read();
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        reinterpret_cast<float*>(stage0)[c * 32 + lane] =
-                            p.bias && c * 32 + lane < left ? __ldg(p.bias + static_cast<int64_t>(expert) * p.h + n0 + c * 32 + lane) : 0.0f;
-                    __syncwarp();
-                }
-#pragma unroll 1
-                for (int c = 0; c < kOut / kCols; ++c) {
-                    F2 v[kCols / 2];
-                    pick(c, v);
-#pragma unroll
-                    for (int k = 0; k < kOut / kCols; ++k)
-                        if (c == k) {
-#pragma unroll
-                            for (int j = 0; j < kCols / 2; ++j) acc[k * (kCols / 2) + j] = v[j];
-                        }
-                }
-                __syncwarp();
-            };
+            if (DUAL || p.act != SPCONV_ACT_NONE) activate();
             if (!EIGHT) {
                 // two staging buffers in turn: rows of 64 bytes in 16-byte pieces whose places are
                 // turned by the row (the copies' 64-byte swizzle)
                 auto place = [](int r, int piece) { return r * 64 + ((piece ^ ((r >> 1) & 3)) << 4); };
                 const int i0 = lane >> 2, c8 = lane & 3;   // of eight rows at a time: row; eight columns
+                // the residual of the next 32 columns is on its way while these are stored
+                uint4 ahead[4];
+                auto whole = [&](int c, int i) { return p.vec_extra && i < rows && c * 32 + c8 * 8 + 8 <= left; };
+                auto read_ahead = [&](int c) {
+#pragma unroll
+                    for (int r = 0; r < 32; r += 8)
+                        if (whole(c, r + i0))
+                            ahead[r / 8] = *reinterpret_cast<const uint4*>(p.extra + (m0 + r + i0) * p.ld_extra + n0 + c * 32 + c8 * 8);
+                };
+                if (!DUAL && p.extra) read_ahead(0);
                 auto store = [&](int c, F2 (&v)[16]) {     // 32 columns
                     const int32_t cols = left - 32 * c;    // (may be negative)
                     uint8_t* stage = stage0 + (c & 1) * 2048;
@@ -522,21 +520,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
 #pragma unroll
                         for (int r = 0; r < 32; r += 8) {
                             const int i = r + i0;
-                            uint4 x4 = make_uint4(0, 0, 0, 0);
-                            if (i < rows && c8 * 8 < cols) {
+                            uint4 x4 = ahead[r / 8];
+                            if (!whole(c, i) && i < rows && c8 * 8 < cols) {
                                 const __nv_bfloat16* x = p.extra + (m0 + i) * p.ld_extra + n0 + c * 32 + c8 * 8;
-                                if (p.vec_extra && c8 * 8 + 8 <= cols) {
-                                    x4 = *reinterpret_cast<const uint4*>(x);
-                                } else {
-                                    uint32_t u[4] = {};
+                                uint32_t u[4] = {};
 #pragma unroll
-                                    for (int j = 0; j < 8; ++j)
-                                        if (c8 * 8 + j < cols) u[j / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x[j])) << (16 * (j & 1));
-                                    x4 = make_uint4(u[0], u[1], u[2], u[3]);
-                                }
+                                for (int j = 0; j < 8; ++j)
+                                    if (c8 * 8 + j < cols) u[j / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x[j])) << (16 * (j & 1));
+                                x4 = make_uint4(u[0], u[1], u[2], u[3]);
                             }
                             *reinterpret_cast<uint4*>(stage + place(i, c8)) = x4;
                         }
+                        if (c < 3) read_ahead(c + 1);
                         __syncwarp();
                     }
 #pragma unroll
@@ -584,20 +579,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                     }
                     if (lane == 0) ptx::bulk_commit();
                 };
-                if constexpr (DUAL) {
-#pragma unroll 1
-                    for (int c = 0; c < kOut / 32; ++c) {
-                        F2 v[kCols / 2];
-                        pick(c, v);
-                        store(c, reinterpret_cast<F2(&)[16]>(v));
-                    }
-                } else {
-                    if (p.act != SPCONV_ACT_NONE || p.bias) activate();
 #pragma unroll
-                    for (int c = 0; c < kOut / 32; ++c) store(c, reinterpret_cast<F2(&)[16]>(acc[c * 16]));
-                }
+                for (int c = 0; c < kOut / 32; ++c) store(c, reinterpret_cast<F2(&)[16]>(acc[c * 16]));
             } else {
-                if (DUAL || p.act != SPCONV_ACT_NONE || p.bias) activate();
                 // the largest of the row's 128 columns: this warp's, or its half and another warp's
                 uint32_t most = 0;
 #pragma unroll
@@ -1032,6 +1016,7 @@ int run(const BlockOp& op, cudaStream_t s) {
     p.map_out = p.vec_out && op.h % (EIGHT ? 16 : 8) == 0;
     if (p.map_out)
         SPCONV_CHECK(make_tensor_map(&p.c, op.out, EIGHT ? 1 : 2, op.h, op.n, op.ld_out, 32, EIGHT && !DUAL ? 128 : 64));
+    if (p.vec_extra) SPCONV_CHECK(make_tensor_map(&p.map_extra, op.extra, 2, op.h, op.n, op.ld_extra, 128));
     return run_tc<DUAL, EIGHT>(op, p, s);
 }
 

@@ -366,7 +366,12 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst_smem, const void* map, 
         : "memory");
 }
 
-// The same into this CTA's shared memory, completing on an mbarrier of either
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_2d(const void* map, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
+// As tma_load_2d, into this CTA's shared memory, completing on an mbarrier of either
 // CTA of a pair.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst_smem, const void* map, int32_t x, int32_t y, uint32_t bar) {
     asm volatile(
