@@ -482,17 +482,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
             // Whole groups of 32 rows leave by tensor-map copies, which nobody waits for; a run's
             // last ones, which a copy would not clip, and unaligned outputs by plain stores.
             const bool mapped = p.map_out && rows == 32;
-            // Activations in place, 16 columns at a time: the empty statement keeps the compiler
-            // from joining them, which would take more registers than there are.
+            // Activations in place, some columns at a time: the empty statements keep the compiler from
+            // working on more of them at once, which would take more registers than there are.  A gated
+            // result's chunks are of one case of the switch, another's a switch each: the other way about
+            // the main loop gets spills, or both take longer (8192 x 512 x 4096: gated to e4m3 without
+            // activation 53 and 61 us; ReLU in 32 columns 39, in 16 44).  No loop over them: moving the
+            // sums to where it finds them takes longer than the unrolled code's wait for instructions (a
+            // plain product 39 us, not 31).
             auto activate = [&]() {
+                constexpr int kChunk = DUAL ? 8 : 16;   // of columns
+                auto apply = [&](int c, auto act) {
 #pragma unroll
-                for (int c = 0; c < kOut / 2; c += 8) {
-                    int32_t a = p.act;
-                    asm volatile("" : "+r"(a));
-                    with_act(a, [&](auto act) {
+                    for (int j = c; j < c + kChunk; ++j) acc[j] = DUAL ? act_f<act>(acc[j]) * acc[(j + 32) % 64] : act_f<act>(acc[j]);
+                };
+                if constexpr (DUAL) {
+                    with_act(p.act, [&](auto act) {
 #pragma unroll
-                        for (int j = c; j < c + 8; ++j) acc[j] = DUAL ? act_f<act>(acc[j]) * acc[(j + 32) % 64] : act_f<act>(acc[j]);
+                        for (int c = 0; c < kOut / 2; c += kChunk) {
+#pragma unroll
+                            for (int j = c; j < c + kChunk; ++j) asm volatile("" : "+l"(acc[j].v));
+                            apply(c, act);
+#pragma unroll
+                            for (int j = c; j < c + kChunk; ++j) asm volatile("" : "+l"(acc[j].v));
+                        }
                     });
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kOut / 2; c += kChunk) {
+                        int32_t a = p.act;
+                        asm volatile("" : "+r"(a));
+                        with_act(a, [&](auto act) { apply(c, act); });
+                    }
                 }
             };
             if (DUAL || p.act != SPCONV_ACT_NONE) activate();
