@@ -976,7 +976,8 @@ int run_few(const BlockOp& op, const BlockArgs& p, int64_t active, cudaStream_t 
     int32_t splits = 1;
     while (splits < kMaxSplits && tiles * active * splits * 2 <= 304 && p.kb >= 4 * splits) splits *= 2;
     a.stage_bytes = (DUAL ? 2 : 1) * kTileW + R * 128;
-    // a smaller ring where all CTAs then run at once and do not otherwise
+    // a smaller ring where all CTAs then run at once and do not otherwise (512 rows of 32
+    // experts, 1408 x 2048: 16.7 us, not 23.3)
     const int64_t ctas = tiles * active * splits;
     const int32_t ring = R == 16 && !DUAL && ctas > 304 && ctas <= 608 ? kFewRing / 2 : kFewRing;
     a.stages = ring / a.stage_bytes < kMaxStages ? ring / a.stage_bytes : kMaxStages;
@@ -1023,10 +1024,15 @@ int run(const BlockOp& op, cudaStream_t s) {
     int64_t ldx = op.ldx;
     rows.add(&x, 1, &ldx, op.n, op.k, 1);
     SPCONV_CHECK(rows.run(s));
-    // few rows a run: an expert has n / experts of them where all are chosen alike
+    // Few rows a run (an expert has n / experts of them where all are chosen alike): the
+    // weight's stream is the bound, which many CTAs share.  One weight of 4096 x 4096, us, and
+    // as 256-row tiles: 32 rows 8.0 and 16.9, 64 rows 9.4 and 17.0; 32 experts of 1408 x 2048:
+    // 16 rows each 16.7 and 23.3, 64 rows 31.9 and 33.0.  A gated product of more than 32 rows
+    // has room for two stages, which is too few where its CTAs do not all run at once: 32
+    // experts of 2048 x 1408 with 40 rows each 56 and 49, 8 experts with 48 rows 16.8 and 22.1.
     const int64_t active = op.experts < op.n ? op.experts : op.n;
     const int64_t each = ceil_div(op.n, active);
-    if (each <= 64) {
+    if (each <= 32 || (each <= 64 && !(DUAL && active * p.hb > 304))) {
         const int32_t r = each <= 16 ? 16 : each <= 32 ? 32 : 64;
         SPCONV_CHECK(make_maps(op, x, ldx, r, &p));
         return r == 16 ? run_few<DUAL, EIGHT, 16>(op, p, active, s) : r == 32 ? run_few<DUAL, EIGHT, 32>(op, p, active, s)

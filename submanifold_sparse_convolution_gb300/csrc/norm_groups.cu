@@ -16,15 +16,20 @@
 // scan's pieces have consecutive ones.  They are added up in that order: no
 // atomics, the same bits every run.
 //
-// Up to kSmallBytes there is one block per SM at most, the second kernel's blocks
-// add up the pieces of their scans themselves, and they load their first rows
-// while the first kernel ends.  Beyond, blocks have kBlockBytes each, a small
-// kernel between the two adds the pieces up, and the second takes the blocks
-// from the last to the first: L2 still has the rows that were read last.
+// There is one block per SM at most, the second kernel's blocks add up the pieces of
+// their scans themselves, and they load their first rows while the first kernel
+// ends.  A forward pass beyond kSmallBytes has blocks of kBlockBytes, a small kernel
+// between the two adds the pieces up, and the second takes the blocks from the last
+// to the first: L2 still has the rows that were read last.
 //
 // Scans of at most kScanBytes on the average are taken whole by a cluster of up
 // to eight CTAs, which keep the rows in registers and exchange their sums through
 // distributed shared memory: one launch, the rows read once.
+//
+// What bounds it: small inputs the launches and the chain offsets - rows - sums -
+// rows (3000 x 64 in bf16: 7 us, 32371 x 128: 14 us for 25 MB), large ones HBM, which
+// has the rows twice and the result (1000000 x 256: 249 us, 6.2 TB/s of 1.54 GB;
+// backward 417 us, 6.1 TB/s of 2.56 GB).
 //
 #include "ptx_sm100.cuh"
 #include "row_vectors.cuh"
@@ -37,7 +42,14 @@ constexpr int kPerLane = 5;              // pieces that a lane adds up where a b
 static_assert(kSms <= 32 * kPerLane, "blocks of a small input");
 constexpr int kThreads = 448;            // blocks of a small input (72 registers a thread, two on an SM); half of it for those of a large one
 constexpr int kApplyThreads = 320;       // (96 registers a thread, and room on an SM beside a block of k_group_stats)
-constexpr int64_t kSmallBytes = 40 << 20, kBlockBytes = 256 << 10;
+// (us, bf16, 256 channels, one scan; the other way: 20 MB 17 and 25, 41 MB 24 and 32, 72 MB 41.5
+// and 39.9, 154 MB 85 and 81, 64 scans of 512 MB 261 and 246.  A backward pass gains nothing
+// from more blocks: 41 MB 44 and 51, 512 MB 417 and 446; only very many scans would, 2000 of 50 rows
+// 106 and 85.)
+constexpr int64_t kSmallBytes = 40 << 20;
+// (154 MB: 81 us, with 64 kB 83; 512 MB: 249, 256, with 1 MB 275.  At least four blocks an SM
+// all the same: 72 MB 40 us, with blocks of 1 MB alone 104)
+constexpr int64_t kBlockBytes = 256 << 10;
 constexpr int64_t kScanBytes = 512 << 10;
 constexpr int kMaxCluster = 8;           // portable cluster size
 
@@ -726,7 +738,6 @@ struct GradPass {
     Shape h;
     Scans scans;
     float2* part;        // of each piece: sums of p and of p u
-    const float2* sums;  // [scans][groups] of all pieces, or null: the second kernel adds them up
     float* cols;         // [blocks][2][c]: sums of dz u, of dz
     int32_t col_blocks;  // the second kernel's first blocks add up cols
     int32_t* status;
@@ -973,8 +984,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_grad_apply(const __grid_c
         return;
     }
     const int ty = h.by_tx(threadIdx.x), tx = threadIdx.x - ty * h.tx, lane = threadIdx.x & 31;
-    const int32_t index = static_cast<int32_t>(blockIdx.x) - p.col_blocks, block = p.sums ? h.blocks - 1 - index : index;
-    const int32_t row0 = block * h.rows;
+    const int32_t index = static_cast<int32_t>(blockIdx.x) - p.col_blocks;
+    const int32_t row0 = index * h.rows;
     const int32_t row1 = row0 + h.rows < p.scans.n ? row0 + h.rows : p.scans.n;
     const T* x0 = static_cast<const T*>(a.x);
     const T* dy0 = static_cast<const T*>(a.dy);
@@ -1005,25 +1016,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_grad_apply(const __grid_c
         const float by_count = 1.0f / (static_cast<float>(s_hi - s_lo) * static_cast<float>(h.width));
         wait();
         __syncthreads();
-        if (p.sums) {
-            for (int32_t g = threadIdx.x; g < h.groups; g += blockDim.x) {
-                const float2 v = __ldcg(p.sums + static_cast<int64_t>(s) * h.groups + g);
-                sh_means[g] = make_float2(v.x * by_count, v.y * by_count);
-            }
-        } else {
-            for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
-                PieceSet set;
-                set.load(h, p.part, g, s, s_lo, s_hi);
-                float z = 0.0f, u = 0.0f;
+        for (int32_t g = threadIdx.x >> 5; g < h.groups; g += blockDim.x >> 5) {
+            PieceSet set;
+            set.load(h, p.part, g, s, s_lo, s_hi);
+            float z = 0.0f, u = 0.0f;
 #pragma unroll
-                for (int k = 0; k < kPerLane; ++k) {
-                    z += set.v[k].x;
-                    u += set.v[k].y;
-                }
-                z = warp_sum(z);
-                u = warp_sum(u);
-                if (lane == 0) sh_means[g] = make_float2(z * by_count, u * by_count);
+            for (int k = 0; k < kPerLane; ++k) {
+                z += set.v[k].x;
+                u += set.v[k].y;
             }
+            z = warp_sum(z);
+            u = warp_sum(u);
+            if (lane == 0) sh_means[g] = make_float2(z * by_count, u * by_count);
         }
         __syncthreads();
         const Deal deal(hi - lo, h);
@@ -1054,28 +1058,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_grad_apply(const __grid_c
         }
 }
 
-template <int THREADS>
-__global__ void __launch_bounds__(256) k_group_grad_join(const __grid_constant__ GradPass p, float2* sums) {
-    __shared__ float2 sh[8];
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * (256 / THREADS) + threadIdx.x / THREADS;
-    pdl_wait();
-    pdl_trigger();
-    if (i >= static_cast<int64_t>(p.scans.scans) * p.h.groups) return;
-    const int32_t s = static_cast<int32_t>(i / p.h.groups), g = static_cast<int32_t>(i - static_cast<int64_t>(s) * p.h.groups);
-    const int32_t lo = p.scans.at(s), hi = p.scans.at(s + 1), t = threadIdx.x % THREADS;
-    if (lo >= hi) return;
-    const float2* part = p.part + g * p.h.slots + s;
-    float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-    for (int32_t b = lo / p.h.rows + t; b <= (hi - 1) / p.h.rows; b += THREADS) {
-        const float2 v = __ldcg(part + b);
-        sum.x += v.x;
-        sum.y += v.y;
-    }
-    sum = sum_of(sum, sh, THREADS);
-    if (t == 0) sums[i] = sum;
-}
-
 // ---- host -----------------------------------------------------------------------
 // Vectors of W elements and the rows of a block; large: enough blocks to be taken
 // in turn, their pieces added up between.
@@ -1090,18 +1072,17 @@ int set_threads(Shape* h, int most) {
     while (h->lanes < 32 && h->lanes < h->ty * wide) h->lanes *= 2;
     return static_cast<int>(round_up(static_cast<size_t>(h->tx) * h->ty, 32));
 }
-Shape make_shape(int64_t n, int32_t c, int32_t groups, int64_t scans, int w, size_t es, int64_t bytes, bool* large, int* threads) {
+Shape make_shape(int64_t n, int32_t c, int32_t groups, int64_t scans, int w, size_t es, bool large, int* threads) {
     Shape h = {};
     h.c = c;
     h.groups = groups;
     h.width = c / groups;
     h.vectors = c / w;
     while ((2 << h.shift) <= w && h.width % (2 << h.shift) == 0) ++h.shift;
-    *large = bytes > kSmallBytes;
-    *threads = set_threads(&h, *large ? kThreads / 2 : kThreads);
+    *threads = set_threads(&h, large ? kThreads / 2 : kThreads);
     int64_t blocks = ceil_div(n, static_cast<int64_t>(4) * h.ty);   // (one step of loads each, at least)
-    int64_t limit = *large ? ceil_div(n * c * static_cast<int64_t>(es), kBlockBytes) : kSms;
-    if (*large && limit < 4 * kSms) limit = 4 * kSms;
+    int64_t limit = large ? ceil_div(n * c * static_cast<int64_t>(es), kBlockBytes) : kSms;
+    if (large && limit < 4 * kSms) limit = 4 * kSms;
     if (blocks > limit) blocks = limit;
     h.rows = static_cast<int32_t>(ceil_div(n, blocks));
     h.blocks = static_cast<int32_t>(ceil_div(n, h.rows));
@@ -1123,14 +1104,14 @@ int launch_wide(int blocks, int threads, size_t smem, cudaStream_t s, const A& a
 }
 
 // The kernel between the two: a warp a scan and group, or a block where a scan
-// has many pieces.
-template <typename A>
-int launch_join(void (*warp)(A, float2*), void (*block)(A, float2*), const A& p, float2* to, cudaStream_t s) {
+// has many pieces (one scan of 512 MB: 249 us with blocks and 279 with warps in
+// all; 64 scans of as much 247 either way).
+int launch_join(const NormPass& p, float2* to, cudaStream_t s) {
     const int64_t count = static_cast<int64_t>(p.scans.scans) * p.h.groups;
     const bool many = p.h.blocks / p.scans.scans > 64;
     const int64_t blocks = many ? count : ceil_div(count, 8);
     if (blocks > 0x7FFFFFFF) return SPCONV_ERR_UNSUPPORTED;
-    return launch_pdl(many ? block : warp, dim3(static_cast<unsigned>(blocks)), 256, 0, s, p, to);
+    return launch_pdl(many ? k_group_join<256> : k_group_join<32>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, p, to);
 }
 
 template <auto KERNEL, typename A>
@@ -1160,26 +1141,30 @@ int launch_clusters(int64_t blocks, int cluster, int threads, size_t smem, cudaS
 }
 
 // CTAs of a cluster that takes a scan of average size whole, with at most `keep`
-// bytes each; 0: too large.  Scans differ in size, so few large ones are left to
-// the other kernels, which deal rows and not scans.
+// bytes each while there are CTAs; 0: too large, or so many CTAs that they run in
+// turns.  (us, bf16, 128 channels, clusters and pieces: 160 scans of 32 kB 9 and 23,
+// of 128 kB 24 and 31, of 256 kB 45 and 39; 600 of 64 kB 36 and 54, of 128 kB 83 and
+// 75; one of 512 kB 10.4 and 11.3, 40 of them 25 and 26.)
 int scan_cluster(int64_t bytes, int64_t scans, int64_t keep) {
     const int64_t each = ceil_div(bytes, scans);
     if (each > kScanBytes) return 0;
     int size = 1;
     while (size < kMaxCluster && each > size * keep) size *= 2;
-    return scans * size >= kSms || bytes <= (int64_t(4) << 20) ? size : 0;
+    return each <= 2 * keep || scans * size <= 5 * kSms ? size : 0;
 }
 
 template <typename T, int W>
 int forward_w(const GroupNormArgs& a, cudaStream_t s) {
     NormPass p = {};
     p.a = a;
-    bool large = false;
     int threads = 0;
     const int64_t bytes = a.n * a.c * static_cast<int64_t>(sizeof(T));
+    const bool large = bytes > kSmallBytes;
     if (const int size = scan_cluster(bytes, a.scans, 32 << 10)) {
-        p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), bytes, &large, &threads);
-        threads = set_threads(&p.h, ceil_div(bytes, a.scans * size) > (16 << 10) ? kThreads : kThreads / 2);
+        p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), false, &threads);
+        // (half as many where two CTAs then share an SM: 300000 rows in 160 scans 69 us, not 123;
+        // one scan of 3000 x 64 8.0, not 7.2)
+        threads = set_threads(&p.h, a.scans * size <= kSms ? kThreads : kThreads / 2);
         p.h.blocks = size;
         p.h.by_blocks = FastDiv(static_cast<uint32_t>(size));
         p.scans = Scans{a.offsets, static_cast<int32_t>(a.scans), static_cast<int32_t>(a.n)};
@@ -1187,7 +1172,7 @@ int forward_w(const GroupNormArgs& a, cudaStream_t s) {
         const size_t smem = static_cast<size_t>(4) * a.groups * 4 + static_cast<size_t>(2) * p.h.ty * (a.c >> p.h.shift) * 4;
         return launch_clusters<k_group_scan<T, W>>(a.scans * size, size, threads, smem, s, p);
     }
-    p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), a.n * a.c * static_cast<int64_t>(sizeof(T)), &large, &threads);
+    p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), large, &threads);
     p.scans = Scans{a.offsets, static_cast<int32_t>(a.scans), static_cast<int32_t>(a.n)};
     SPCONV_CHECK(rows_status_word(&p.status));
     const size_t part_bytes = round_up(static_cast<size_t>(p.h.slots) * a.groups * sizeof(float2), 256);
@@ -1199,7 +1184,7 @@ int forward_w(const GroupNormArgs& a, cudaStream_t s) {
     SPCONV_CHECK((launch_wide<k_group_stats<T, W>>(p.h.blocks, threads, Rows1::bytes(threads) + static_cast<size_t>(2) * p.h.ty * (a.c >> p.h.shift) * 4, s, p)));
     if (large) {
         float2* stats = a.stats ? a.stats : part.as<float2>(part_bytes);
-        SPCONV_CHECK(launch_join(k_group_join<32>, k_group_join<256>, p, stats, s));
+        SPCONV_CHECK(launch_join(p, stats, s));
         p.stats = stats;
     }
     threads = set_threads(&p.h, large ? kApplyThreads / 2 : kApplyThreads);
@@ -1210,25 +1195,17 @@ template <typename T, int W>
 int backward_w(const GroupNormGradArgs& a, cudaStream_t s) {
     GradPass p = {};
     p.a = a;
-    bool large = false;
     int threads = 0;
-    p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), 2 * a.n * a.c * static_cast<int64_t>(sizeof(T)), &large,
-                     &threads);
+    p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), false, &threads);
     p.scans = Scans{a.offsets, static_cast<int32_t>(a.scans), static_cast<int32_t>(a.n)};
     SPCONV_CHECK(rows_status_word(&p.status));
     const size_t part_bytes = round_up(static_cast<size_t>(p.h.slots) * a.groups * sizeof(float2), 256);
-    const size_t sums_bytes = large ? round_up(static_cast<size_t>(a.scans) * a.groups * sizeof(float2), 256) : 0;
-    Scratch buf(part_bytes + sums_bytes + static_cast<size_t>(p.h.blocks) * 2 * a.c * 4, s);
+    Scratch buf(part_bytes + static_cast<size_t>(p.h.blocks) * 2 * a.c * 4, s);
     if (buf.failed()) return SPCONV_ERR_OOM;
     p.part = buf.as<float2>();
-    p.cols = buf.as<float>(part_bytes + sums_bytes);
+    p.cols = buf.as<float>(part_bytes);
     using Rows2 = Stream<Pack<T, W>, 2, kDeepGrad>;
     SPCONV_CHECK((launch_wide<k_group_grad_sums<T, W>>(p.h.blocks, threads, Rows2::bytes(threads) + static_cast<size_t>(2) * (p.h.ty + 1) * a.c * 4, s, p)));
-    if (large) {
-        float2* sums = buf.as<float2>(part_bytes);
-        SPCONV_CHECK(launch_join(k_group_grad_join<32>, k_group_grad_join<256>, p, sums, s));
-        p.sums = sums;
-    }
     p.col_blocks = static_cast<int32_t>(ceil_div(2 * a.c, kColumns));
     size_t smem = static_cast<size_t>(2) * a.groups * 4;
     if (smem < kThreads * 4) smem = kThreads * 4;
