@@ -33,6 +33,16 @@ Between two convolutions on the same sites, on rows of features alone:
 
 with 8-bit forms (``rms_norm(..., quantize=True)``, ``quantize_weight``) and
 gradients (``rms_norm_backward``, ``linear_backward``, ``gated_ffn_backward``).
+Group norm over each scan of a batch, and a feed-forward of experts, each row
+through the k that it has chosen, in e4m3 with a scale for each 128 values:
+
+    y = group_norm(x, w, b, 32, offsets=scans, activation="silu")
+    p = expert_plan(chosen, n_experts)              # int [N, k]
+    q, s = expert_gather(y, p, quantize=True)       # rows sorted by expert
+    wq, ws = quantize_weight_blocks(w_gate)         # [experts, C_in, C_hidden], once
+    h, hs = gated_ffn_blocks(q, wq, uq, s, ws, us, offsets=p.offsets, quantize=True)
+    z = linear_blocks(h, dq, hs, ds, offsets=p.offsets)
+    x = expert_combine(z, p, weights, residual=x)   # back, weighted
 
 The tensors, maps and packs of a call lie on the current GPU (``ValueError``
 otherwise).  A ``stream`` argument belongs to it too; for a row-wise operator it
@@ -56,8 +66,8 @@ __all__ = ["SpconvError", "Map", "WPack", "build_map", "subm_forward", "wpack_cr
            "rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
            "quantize_weight", "group_norm", "group_norm_backward", "ExpertPlan", "expert_plan", "expert_gather",
            "expert_gather_backward", "expert_combine", "expert_combine_backward", "quantize_blocks",
-           "quantize_weight_blocks", "linear_blocks", "gated_ffn_blocks", "rows_status", "trim_pool", "last_launch_count", "status_string", "ACTIVATIONS", "MAPPERS",
-           "BIT_ORDERS", "PIPELINES", "GEMMS", "library"]
+           "quantize_weight_blocks", "linear_blocks", "gated_ffn_blocks", "rows_status", "trim_pool", "last_launch_count",
+           "status_string", "ACTIVATIONS", "MAPPERS", "BIT_ORDERS", "PIPELINES", "GEMMS", "library"]
 
 MAPPERS = {"auto": 0, "dense": 1, "sorted": 2, "hash": 3}
 PIPELINES = {"auto": 0, "fused": 1, "multi": 2, "wide": 3}

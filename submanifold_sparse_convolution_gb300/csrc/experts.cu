@@ -10,7 +10,11 @@
 //
 // All of them walk the tokens, so that a token's row is read once for all its
 // choices and no sum needs an atomic.  They are bound by HBM: a thread holds one
-// vector of a row, and the warps of an SM have enough of them in flight.
+// vector of a row, and the warps of an SM have enough of them in flight (bf16, four
+// choices: 16381 tokens of 1024 channels, gather 24.5 us, 6.8 TB/s, combine 27.5;
+// 8189 of 2048, the gradient of combine 47 us, 6.4 TB/s; 40000 rows of 2048 to e4m3
+// blocks 85 us, 2.9 TB/s: there instructions are the bound).  The sort is two kernels
+// of 3 and 6 us for 32756 pairs, most of it latency.
 #include "row_vectors.cuh"
 
 namespace spconv {

@@ -1144,7 +1144,7 @@ int launch_clusters(int64_t blocks, int cluster, int threads, size_t smem, cudaS
 // bytes each while there are CTAs; 0: too large, or so many CTAs that they run in
 // turns.  (us, bf16, 128 channels, clusters and pieces: 160 scans of 32 kB 9 and 23,
 // of 128 kB 24 and 31, of 256 kB 45 and 39; 600 of 64 kB 36 and 54, of 128 kB 83 and
-// 75; one of 512 kB 10.4 and 11.3, 40 of them 25 and 26.)
+// 53; one of 512 kB 10.4 and 11.3, 40 of them 25 and 26.)
 int scan_cluster(int64_t bytes, int64_t scans, int64_t keep) {
     const int64_t each = ceil_div(bytes, scans);
     if (each > kScanBytes) return 0;
