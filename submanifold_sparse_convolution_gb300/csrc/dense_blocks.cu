@@ -704,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
 // its blocks up in registers (a thread a channel), and the cluster's partial sums
 // are added through distributed shared memory in the order of the ranks.
 // Accumulators of one block of K take turns in a ring in TMEM.  The weights' stream
-// bounds it: 64 rows of 32 experts, gated 2048 x 1408, 27 us at 6.7 TB/s; one row
+// bounds it: 64 rows of 28 experts, gated 2048 x 1408, 27 us at 6.0 TB/s; one row
 // of 4096 x 4096 7 us, where the start and the cluster's sums are 4.  An expert with
 // more than R rows streams its weight again for each R of them.
 constexpr int kFewThreads = 192;       // warp 0 loads, warp 1 issues MMAs, warps 2-5 add up
