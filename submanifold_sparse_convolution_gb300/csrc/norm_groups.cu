@@ -18,8 +18,8 @@
 //
 // There is one block per SM at most, the second kernel's blocks add up the pieces of
 // their scans themselves, and they load their first rows while the first kernel
-// ends.  A forward pass beyond kSmallBytes has blocks of kBlockBytes, a small kernel
-// between the two adds the pieces up, and the second takes the blocks from the last
+// ends.  A forward pass over several scans, or beyond kSmallBytes, has blocks of
+// kBlockBytes, a small kernel between the two adds the pieces up, and the second takes the blocks from the last
 // to the first: L2 still has the rows that were read last.
 //
 // Scans of at most kScanBytes on the average are taken whole by a cluster of up
@@ -42,10 +42,10 @@ constexpr int kPerLane = 5;              // pieces that a lane adds up where a b
 static_assert(kSms <= 32 * kPerLane, "blocks of a small input");
 constexpr int kThreads = 448;            // blocks of a small input (72 registers a thread, two on an SM); half of it for those of a large one
 constexpr int kApplyThreads = 320;       // (96 registers a thread, and room on an SM beside a block of k_group_stats)
-// (us, bf16, 256 channels, one scan; the other way: 20 MB 17 and 25, 41 MB 24 and 32, 72 MB 41.5
-// and 39.9, 154 MB 85 and 81, 64 scans of 512 MB 261 and 246.  A backward pass gains nothing
-// from more blocks: 41 MB 44 and 51, 512 MB 417 and 446; only very many scans would, 2000 of 50 rows
-// 106 and 85.)
+// (us, bf16, 256 channels, as a small input and otherwise: one scan of 10 MB 13.3 and 14.1, 41 MB 24.2
+// and 24.4, 64 MB 36.2 and 34.9, 82 MB 48.7 and 45.9, seven scans of 10 MB together 19.1 and 16.5, of 64 MB
+// 43 and 37.  A backward pass gains nothing from more blocks: 41 MB 44 and 51, 512 MB 417 and 446; only very
+// many scans would, 2000 of 50 rows 106 and 85.)
 constexpr int64_t kSmallBytes = 40 << 20;
 // (154 MB: 81 us, with 64 kB 83; 512 MB: 249, 256, with 1 MB 275.  At least four blocks an SM
 // all the same: 72 MB 40 us, with blocks of 1 MB alone 104)
@@ -1159,7 +1159,7 @@ int forward_w(const GroupNormArgs& a, cudaStream_t s) {
     p.a = a;
     int threads = 0;
     const int64_t bytes = a.n * a.c * static_cast<int64_t>(sizeof(T));
-    const bool large = bytes > kSmallBytes;
+    const bool large = a.scans > 1 || bytes > kSmallBytes;
     if (const int size = scan_cluster(bytes, a.scans, 32 << 10)) {
         p.h = make_shape(a.n, a.c, a.groups, a.scans, W, sizeof(T), false, &threads);
         // (half as many where two CTAs then share an SM: 300000 rows in 160 scans 69 us, not 123;
