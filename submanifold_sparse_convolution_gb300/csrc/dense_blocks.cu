@@ -125,19 +125,73 @@ __device__ __forceinline__ void zero_rest(const BlockArgs& p, int64_t first, int
         }
 }
 
-// The scale of a block whose largest magnitude is m, and the factor to its e4m3
-// values.  The values come from fp32 sums, so a product with the inverse serves;
-// below 2^-119 that would overflow, and they are brought up first.
-struct ToE4m3 {
-    float scale, pre, factor;
-    __device__ __forceinline__ explicit ToE4m3(float m) {
-        scale = __fdiv_rn(m, 448.0f);
-        pre = m < 0x1p-100f ? 0x1p100f : 1.0f;
-        factor = m == 0.0f ? 0.0f : __fdiv_rn(448.0f, m * pre);
-        if (!(m < __int_as_float(0x7F800000))) factor = __int_as_float(0x7FFFFFFF);   // infinity or NaN: all NaN
+// 1 / s rounded towards zero, from the nearest.
+__device__ __forceinline__ float inverse_towards_zero(float s, float nearest) {
+    return fmaf(-s, nearest, 1.0f) < 0.0f ? __uint_as_float(__float_as_uint(nearest) - 1) : nearest;
+}
+
+// The quotients of a block's values and its scale s (largest magnitude / 448), of which
+// e4m3(v / s) is formed with both divisions rounded to nearest, as spconv_quantize_blocks
+// has them.  1 / s is held in two parts, y rounded towards zero and y2 = (1 - s y) y, whose
+// first factor is exact; neither is negative, so a zero keeps its sign.  v y + v y2, rounded
+// once by the multiply-add, is v / s (1 + e) before that rounding, with e at most 1.5 2^-46
+// (y2) + 2^-47 (v y2) = 2^-45.  What the e4m3 value turns on is on which side of T + 2^-24
+// and of T - 2^-24 v / s lies, T the middle of two e4m3 values, t sixteenths in [1, 2)
+// (powers of two aside; where T is one, T - 2^-25).  With s = B 2^-23 and v = A 2^-23, 24
+// bits each, v differs from s (T +- 2^-24) by N 2^-47, N = A 2^24 - B (t 2^20 +- 1), so N =
+// -+B modulo 2^20, and |N| > 16 is more than e can pass over (s T < 4).
+//
+// That fails for scales whose last 20 bits are near 0 (20 is kept), but not 0, and says nothing
+// of those far from 1: those rows take AnyQuotient.  (Measured: 8192 x 4096 x 4096 gated
+// 208 us, with one product by 448 / max, which gives other values near T, 208; 32 experts'
+// rows, 2048 x 1408, 178 and 175.  A division a value where both a product with a little
+// less and one with a little more than 1 / s do not agree: 214 and 183.)
+struct Quotient {
+    F2 y, y2;
+    bool serves;
+    __device__ __forceinline__ explicit Quotient(float s) {
+        const uint32_t last = __float_as_uint(s) & 0xFFFFFu;
+        serves = s == 0.0f || (s >= 0x1p-60f && s <= 0x1p60f && (last == 0 || ((last + 20) & 0xFFFFFu) > 40));
+        const float inverse = s == 0.0f ? 0.0f : inverse_towards_zero(s, __fdiv_rn(1.0f, s));
+        y = F2(inverse);
+        y2 = F2(fmaf(-s, inverse, 1.0f) * inverse);
     }
-    __device__ __forceinline__ float operator()(float v) const { return v * pre * factor; }
+    __device__ __forceinline__ F2 operator()(F2 v) const { return fma_v(v, y, v * y2); }
 };
+
+// For every scale: the step that makes a quotient q within a unit in the last place the
+// rounded one, q + (v - s q) y, y = 1 / s rounded to nearest (P. Markstein, IBM Journal of
+// Research and Development 34, 1990), with s and v times a power of two that keeps every
+// factor in fp32's range.
+struct AnyQuotient {
+    F2 s, pre, y, y2, nearest;   // (pre and the inverses negated: with v - s q the other way about a zero keeps its sign here too)
+    __device__ __forceinline__ explicit AnyQuotient(float scale) {
+        const bool infinite = scale == __int_as_float(0x7F800000);   // (0 for what is finite, NaN for the infinities)
+        const float by = scale < 0x1p-60f ? 0x1p100f : scale > 0x1p60f ? 0x1p-60f : 1.0f, d = scale * by;
+        const float n = scale == 0.0f ? 0.0f : __fdiv_rn(1.0f, d), z = inverse_towards_zero(d, n);
+        s = F2(infinite ? 0.0f : d);
+        pre = F2(-by);
+        y = F2(-z);
+        y2 = F2(infinite ? -0.0f : -fmaf(-d, z, 1.0f) * z);
+        nearest = F2(-n);
+    }
+    __device__ __forceinline__ F2 operator()(F2 v) const {
+        v = v * pre;
+        const F2 q = fma_v(v, y, v * y2);
+        return fma_v(fma_v(q, s, v), nearest, q);
+    }
+};
+
+// Four values; a block of zeros (scale 0) is +0.
+template <typename Q>
+__device__ __forceinline__ uint32_t to_e4m3(const Q& quotient, float scale, F2 ab, F2 cd) {
+    float a, b, c, d;
+    quotient(ab).get(a, b);
+    quotient(cd).get(c, d);
+    const uint32_t q = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
+                       static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
+    return scale == 0.0f ? 0u : q;
+}
 
 // A tile: its expert, first row, the run's end and its column tile.
 struct Tile {
@@ -634,25 +688,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_block
                     }
                     most = max(most, *reinterpret_cast<volatile uint32_t*>(staging + (e ^ 4) * kStaging + slot));
                 }
-                const ToE4m3 to(__uint_as_float(most));
-                if ((!DUAL || part == 0) && live && left > 0) p.scale[static_cast<int64_t>(n0 / 128) * p.runs.n + row] = to.scale;
+                const float scale = __fdiv_rn(__uint_as_float(most), 448.0f);
+                if ((!DUAL || part == 0) && live && left > 0) p.scale[static_cast<int64_t>(n0 / 128) * p.runs.n + row] = scale;
                 if (lane == 0) ptx::bulk_wait_read();
                 __syncwarp();
                 constexpr int kPieces = kOut / 16, kRows = 32 / kPieces;   // 16-byte pieces of a row
                 auto place = [](int r, int piece) { return r * kOut + ((piece ^ (kPieces == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
+                auto stage_row = [&](const auto& quotient) {
 #pragma unroll
-                for (int c = 0; c < kPieces; ++c) {
-                    uint32_t u[4];
+                    for (int c = 0; c < kPieces; ++c) {
+                        uint32_t u[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float a, b, d, g;
-                        acc[c * 8 + j * 2].get(a, b);
-                        acc[c * 8 + j * 2 + 1].get(d, g);
-                        u[j] = __nv_cvt_float2_to_fp8x2(make_float2(to(a), to(b)), __NV_SATFINITE, __NV_E4M3) |
-                               static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(to(d), to(g)), __NV_SATFINITE, __NV_E4M3)) << 16;
+                        for (int j = 0; j < 4; ++j) u[j] = to_e4m3(quotient, scale, acc[c * 8 + j * 2], acc[c * 8 + j * 2 + 1]);
+                        *reinterpret_cast<uint4*>(stage0 + place(lane, c)) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                    *reinterpret_cast<uint4*>(stage0 + place(lane, c)) = make_uint4(u[0], u[1], u[2], u[3]);
-                }
+                };
+                const Quotient quotient(scale);
+                if (__all_sync(0xFFFFFFFFu, quotient.serves)) stage_row(quotient);
+                else stage_row(AnyQuotient(scale));
                 if (mapped) ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (mapped) {
@@ -910,10 +963,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_blocks_few(const __grid_cons
                     if (j < left) most = max(most, __float_as_uint(fabsf(z[0][j])));
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-                const ToE4m3 to(__uint_as_float(most));
-                if (lane == 0) p.scale[static_cast<int64_t>(tn) * p.runs.n + row] = to.scale;
-                const uint32_t v = __nv_cvt_float2_to_fp8x2(make_float2(to(z[0][0]), to(z[0][1])), __NV_SATFINITE, __NV_E4M3) |
-                                   static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(to(z[0][2]), to(z[0][3])), __NV_SATFINITE, __NV_E4M3)) << 16;
+                const float scale = __fdiv_rn(__uint_as_float(most), 448.0f);
+                if (lane == 0) p.scale[static_cast<int64_t>(tn) * p.runs.n + row] = scale;
+                const uint32_t v = to_e4m3(AnyQuotient(scale), scale, F2(z[0][0], z[0][1]), F2(z[0][2], z[0][3]));
                 uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.ld_out + n0 + 4 * lane;
                 if (p.vec_out && left >= 4) {
                     *reinterpret_cast<uint32_t*>(out) = v;
