@@ -507,6 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_dense
                             const float s = column_sum16(z, lane);
                             const int64_t pr = static_cast<int64_t>(t.tm) * 8 + rank * 4 + quarter;
                             if (lane < CW && nc + lane < p.n) p.part[pr * p.n + nc + lane] = s;
+                            __syncwarp();
                         }
                     }
                 }

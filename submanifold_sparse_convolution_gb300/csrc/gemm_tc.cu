@@ -766,9 +766,9 @@ __global__ void __launch_bounds__(TcConfig<NTMAX>::kThreads, 1) k_tc_gemm(const 
                         d[h] = q;
                     }
                 }
+                __syncwarp();   // (rows without an output went another way; the next loads want the whole warp)
             }
             ptx::tc_fence_before();
-            __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
         }
     }

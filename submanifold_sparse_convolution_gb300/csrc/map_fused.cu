@@ -60,6 +60,7 @@ struct FusedSmem {
 };
 
 __device__ __forceinline__ void cluster_sync_all() {
+    __syncwarp();   // (the whole warp has to come together; loops of single lanes stand before it)
     asm volatile(
         "barrier.cluster.arrive.release.aligned;\n\t"
         "barrier.cluster.wait.acquire.aligned;" ::: "memory");

@@ -159,10 +159,16 @@ __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t count) 
 
 // ---------------------------------------------------------------------------
 // tcgen05: tensor memory and the 5th-generation MMA
+//
+// Instructions that are `aligned` want the whole warp at them together.  The barriers of a
+// cluster and what takes and gives back tensor memory often follow work of single lanes, so
+// those bring the warp together themselves; in front of the loads of tensor memory, which
+// stand in inner loops, the caller has done so.
 // ---------------------------------------------------------------------------
 // Allocate ncols TMEM columns (power of two, >= 32); the TMEM address is
 // written to *dst.  Executed by all 32 threads of one warp.
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(dst)),
                  "r"(ncols)
@@ -170,10 +176,12 @@ __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
 }
 
 __device__ __forceinline__ void tmem_relinquish() {
+    __syncwarp();
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                  : "memory");
 }
@@ -332,12 +340,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 
 // All threads of all CTAs of the cluster.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Its two halves: what comes before the arrival is seen behind the others' wait.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // The shared-memory address in CTA `rank` of the cluster that corresponds to `addr` in this one.
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
@@ -421,13 +436,16 @@ __device__ __forceinline__ void prefetch_map(const void* map) {
 // and half of B's, the accumulator rows stay with A's; issued by CTA 0
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
                  : "memory");
 }
 __device__ __forceinline__ void tmem_relinquish_pair() {
+    __syncwarp();
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
