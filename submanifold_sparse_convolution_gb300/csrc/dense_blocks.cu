@@ -58,6 +58,7 @@ struct Regs {
 constexpr int kTableSize = 256;
 constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStaging + kScaleBytes + 256 + 4 * (kTableSize + 1);
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+static_assert(ptx::tmem_fits(kSmem, 512), "TMEM of an SM");
 
 // Experts' runs of rows, in order and range whatever the offsets hold.
 struct Runs {
@@ -773,14 +774,29 @@ struct FewBlockArgs {
     int32_t stages, stage_bytes;
 };
 
+template <bool DUAL, int R>
+struct FewShape {
+    static constexpr int kAcc = DUAL ? 2 : 1;
+    static constexpr int kCols = kAcc * R;                        // TMEM columns of an accumulator
+    static constexpr int kBufs = 256 / kCols < kMaxAcc ? 256 / kCols : kMaxAcc;
+    static constexpr uint32_t kTmem = kBufs * kCols;
+    static constexpr int kSmallRing = R == 16 && !DUAL ? kFewRing / 2 : kFewRing;   // (four CTAs on an SM)
+    static_assert(kTmem >= 32 && (kTmem & (kTmem - 1)) == 0, "TMEM columns");
+    static_assert(kAcc * R * 128 * 4 <= kSmallRing, "the sums take the ring's place");
+    // two CTAs with the large ring, or one and those with the small one in what it leaves (of
+    // the other kernels that take TMEM k_dense_few's small form has as much shared memory and a
+    // quarter of the columns, and the others leave no room beside them)
+    static_assert(ptx::tmem_fits(kFewRing + 1024, kTmem) && ptx::tmem_fits(kSmallRing + 1024, kTmem), "TMEM of an SM");
+    static_assert(kSmallRing == kFewRing ||
+                      256 + (ptx::kSmShared - ptx::cta_shared(kFewRing + 1024)) / ptx::cta_shared(kSmallRing + 1024) * kTmem <= ptx::kSmTmemColumns,
+                  "TMEM of an SM");
+};
+
 template <bool DUAL, bool EIGHT, int R>
 __global__ void __launch_bounds__(kFewThreads, 2) k_blocks_few(const __grid_constant__ FewBlockArgs a) {
-    constexpr int kAcc = DUAL ? 2 : 1;
-    constexpr int kCols = kAcc * R;                               // TMEM columns of an accumulator
-    constexpr int kBufs = 256 / kCols < kMaxAcc ? 256 / kCols : kMaxAcc;
-    constexpr uint32_t kTmem = kBufs * kCols;
-    static_assert(kTmem >= 32 && (kTmem & (kTmem - 1)) == 0, "TMEM columns");
-    static_assert(kAcc * R * 128 * 4 <= kFewRing, "the sums take the ring's place");
+    using Shape = FewShape<DUAL, R>;
+    constexpr int kAcc = Shape::kAcc, kCols = Shape::kCols, kBufs = Shape::kBufs;
+    constexpr uint32_t kTmem = Shape::kTmem;
     const BlockArgs& p = a.b;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kBufs], acc_empty[kBufs];
@@ -1042,7 +1058,7 @@ int run_few(const BlockOp& op, const BlockArgs& p, int64_t active, cudaStream_t 
     // a smaller ring where all CTAs then run at once and do not otherwise (512 rows of 32
     // experts, 1408 x 2048: 16.7 us, not 23.3)
     const int64_t ctas = tiles * active * splits;
-    const int32_t ring = R == 16 && !DUAL && ctas > 304 && ctas <= 608 ? kFewRing / 2 : kFewRing;
+    const int32_t ring = ctas > 304 && ctas <= 608 ? FewShape<DUAL, R>::kSmallRing : kFewRing;
     a.stages = ring / a.stage_bytes < kMaxStages ? ring / a.stage_bytes : kMaxStages;
     SPCONV_CHECK((allow_smem<k_blocks_few<DUAL, EIGHT, R>>(kFewRing + 1024)));
     cudaLaunchAttribute at[2] = {pdl_attr(), {}};

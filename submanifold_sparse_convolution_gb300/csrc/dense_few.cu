@@ -69,6 +69,7 @@ struct FewConfig {
     static constexpr int kRing = (BIG ? 200 : 100) * 1024;            // stages, of one CTA
     static constexpr int kPerSm = BIG ? 1 : 2;
     static_assert(kCols * kChannels * 4 <= kRing, "the sums take the ring's place");
+    static_assert(ptx::tmem_fits(kRing + 1024, kCols), "TMEM of an SM");
 };
 
 struct FewArgs {

@@ -104,6 +104,7 @@ struct TcLaunch {
 constexpr int kStages = 5;
 constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStaging + 512;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+static_assert(ptx::tmem_fits(kSmem, kTmemCols), "TMEM of an SM");
 
 // Columns of an epilogue warp's block: one staging buffer of 128-byte rows, or
 // two of 64-byte rows where there are two outputs.

@@ -145,6 +145,7 @@ struct TcConfig {
     static constexpr int kBarBytes = 512;
     static constexpr int kSmem = kStages * kStage + 2 * kIdxBytes + 1024 + kBarBytes;
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+    static_assert(ptx::tmem_fits(kSmem, kTmemCols), "TMEM of an SM");
 };
 
 // Item that CTA `cta` of `grid` takes in its round L (snake order).

@@ -165,6 +165,14 @@ __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t count) 
 // those bring the warp together themselves; in front of the loads of tensor memory, which
 // stand in inner loops, the caller has done so.
 // ---------------------------------------------------------------------------
+// An allocation waits, without a limit, until the SM has the columns.  CTAs of clusters
+// that waited for each other that way would never end, so CTAs that share an SM may not
+// want more columns together than it has: whether those of a kernel that takes `columns`
+// and `smem` bytes of shared memory (and the 1 kB that every CTA takes) do not.
+constexpr int kSmShared = 228 * 1024, kSmTmemColumns = 512;
+constexpr int cta_shared(int smem) { return smem + 1024; }
+constexpr bool tmem_fits(int smem, int columns) { return kSmShared / cta_shared(smem) * columns <= kSmTmemColumns; }
+
 // Allocate ncols TMEM columns (power of two, >= 32); the TMEM address is
 // written to *dst.  Executed by all 32 threads of one warp.
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
