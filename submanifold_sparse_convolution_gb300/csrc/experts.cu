@@ -94,7 +94,7 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sh) {
 // was counted before: the block counts for itself.
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads) k_expert_place(const SortArgs a) {
-    extern __shared__ uint16_t in_warp[];   // [kSortWarps][n_experts]
+    extern __shared__ __align__(16) uint16_t in_warp[];   // [kSortWarps][n_experts] (cleared by 32 bits)
     __shared__ int32_t next[kSortThreads], part[2][kSortThreads], sh[32];
     const int32_t tid = static_cast<int32_t>(threadIdx.x), lane = tid & 31, warp = tid >> 5, ne = a.n_experts;
     const int32_t chunks = static_cast<int32_t>(gridDim.x), b = static_cast<int32_t>(blockIdx.x);

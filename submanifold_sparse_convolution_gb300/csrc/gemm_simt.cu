@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kFThreads, 3) k_fp32_tiled(const float* __rest
                                                              const int32_t* __restrict__ tile_order,
                                                              int64_t n, int64_t n_pad, int64_t n_in, int c_in,
                                                              int c_out, Epilogue epi, int32_t* __restrict__ status) {
-    extern __shared__ float fsm[];
+    extern __shared__ __align__(16) float fsm[];
     const int t = threadIdx.x;
     const int cg = t & 7, rg = t >> 3;        // columns 8 cg .. + 7; rows rg + 16 i
     // CTAs start in blockIdx order: taking the tiles by descending union size

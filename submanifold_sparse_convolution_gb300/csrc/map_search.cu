@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kSearchRows * kSearchGroups) k_search_window(c
     constexpr int kSearchThreads = kSearchRows * kSearchGroups;
     constexpr int CPT = 9 / kSearchGroups;    // (dx, dy) columns per thread
     static_assert(kSearchRows % 32 == 0 && CPT * kSearchGroups == 9, "a column group is whole warps");
-    extern __shared__ uint64_t sh_search[];
+    extern __shared__ __align__(16) uint64_t sh_search[];
     uint64_t* samp = sh_search;                  // [kSampleMax]
     uint64_t* win = sh_search + kSampleMax;      // [9][padded_cap(wcap)], padded (pad_idx)
     __shared__ int64_t wlo[9];

@@ -598,7 +598,7 @@ template <typename T, int W>
 __global__ void __launch_bounds__(kThreads, 1) k_group_scan(const __grid_constant__ NormPass p) {
     using P = Pack<T, W>;
     constexpr int KEEP = W == 8 ? 6 : 8, U = 4;   // (registers)
-    extern __shared__ float sh[];
+    extern __shared__ __align__(16) float sh[];
     const Shape& h = p.h;
     const GroupNormArgs& a = p.a;
     const int32_t entries = h.c >> h.shift;
