@@ -284,8 +284,7 @@ __global__ void __launch_bounds__(256) k_rows_to_blocks(const ExpertRows a, cons
             if (tiny || near) f[j] = scale == 0.0f ? 0.0f : __fdiv_rn(f[j], scale);
             else f[j] = q;
         }
-        uint32_t q[2];   // eight e4m3 values
-        store_e4m3<8>(reinterpret_cast<uint8_t*>(q), f);
+        const uint32_t q[2] = {pack_e4m3(f), pack_e4m3(f + 4)};
         float* to_scale = v % 16 == 0 ? a.scale + static_cast<int64_t>(v / 16) * rows : nullptr;
         const int32_t* slots = a.slots + t * a.k;
         for (int32_t j = 0; j < a.k; ++j) {

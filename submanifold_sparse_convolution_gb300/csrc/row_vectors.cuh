@@ -53,17 +53,18 @@ __device__ __forceinline__ void pack(const float (&f)[W], Pack<__nv_bfloat16, W>
     }
 }
 
+// Four values as e4m3.
+__device__ __forceinline__ uint32_t pack_e4m3(const float* v) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+// W values to memory with W bytes' alignment.
 template <int W>
 __device__ __forceinline__ void store_e4m3(uint8_t* dst, const float* v) {
     if (W == 8) {
-        uint32_t q[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j], v[4 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j + 2], v[4 * j + 3]), __NV_SATFINITE, __NV_E4M3);
-            q[j] = lo | (hi << 16);
-        }
-        *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_e4m3(v), pack_e4m3(v + 4));
     } else if (W == 2) {
         *reinterpret_cast<uint16_t*>(dst) = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1 % W]), __NV_SATFINITE, __NV_E4M3);
     } else {

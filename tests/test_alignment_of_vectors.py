@@ -25,3 +25,13 @@ def test_dynamic_shared_memory(path):
         by_hand = any(form in text for form in (f"1024 - (ptx::smem_u32({m.group(2)}) & 1023)", "(1024 - (raw & 1023)) & 1023",
                                                 f"(reinterpret_cast<uintptr_t>({m.group(2)}) + 1023) & ~uintptr_t(1023)"))
         assert int(m.group(1) or 0) >= 16 or by_hand, f"{m.group(0)} in {os.path.basename(path)}"
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_no_vector_store_to_an_array_of_smaller_elements(path):
+    """A local array is aligned for its elements: vector stores go through values, or arrays declared for them."""
+    text = open(path).read()
+    arrays = set(re.findall(r"^\s+(?:u?int(?:8|16|32)_t|float|__nv_bfloat16) (\w+)\[[\w\s/*+]+\];", text, re.M))
+    shared = set(re.findall(r"__shared__.* (\w+)\[", text))
+    bad = [n for n in arrays - shared if re.search(rf"store_e4m3<\d>\(reinterpret_cast<uint8_t\*>\({n}\)|reinterpret_cast<(?:u?int|float)[24]\*>\({n}\) = ", text)]
+    assert not bad, f"{bad} in {os.path.basename(path)}"
