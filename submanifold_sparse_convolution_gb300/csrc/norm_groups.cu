@@ -16,11 +16,14 @@
 // scan's pieces have consecutive ones.  They are added up in that order: no
 // atomics, the same bits every run.
 //
-// There is one block per SM at most, the second kernel's blocks add up the pieces of
-// their scans themselves, and they load their first rows while the first kernel
-// ends.  A forward pass over several scans, or beyond kSmallBytes, has blocks of
-// kBlockBytes, a small kernel between the two adds the pieces up, and the second takes the blocks from the last
-// to the first: L2 still has the rows that were read last.
+// One scan of up to kSmallBytes, and every backward pass, have one block per SM at most;
+// the second kernel's blocks add up the pieces of their scans themselves, and they load
+// their first rows while the first kernel ends.  A forward pass over several scans, or
+// beyond kSmallBytes, has blocks of kBlockBytes, or smaller ones where those would be fewer
+// than four an SM; a small kernel between the two adds the pieces up, and the second takes
+// the blocks from the last to the first, whose rows L2 read last (160000 x 256, 82 MB: 44.7
+// us, from the first on 46.4; beyond L2 at most 1 %: of 307 MB the second kernel reads 306
+// from HBM again).
 //
 // Scans of at most kScanBytes on the average are taken whole by a cluster of up
 // to eight CTAs, which keep the rows in registers and exchange their sums through
@@ -29,8 +32,7 @@
 // What bounds it: small inputs the launches and the chain offsets - rows - sums -
 // rows (3000 x 64 in bf16: 7 us, 32371 x 128: 14 us for 25 MB), large ones HBM, which
 // has the rows twice and the result (1000000 x 256: 249 us, 6.2 TB/s of 1.54 GB;
-// backward 417 us, 6.1 TB/s of 2.56 GB).
-//
+// backward 420 us, 6.1 TB/s of 2.56 GB).
 #include "ptx_sm100.cuh"
 #include "row_vectors.cuh"
 
@@ -44,7 +46,7 @@ constexpr int kThreads = 448;            // blocks of a small input (72 register
 constexpr int kApplyThreads = 320;       // (96 registers a thread, and room on an SM beside a block of k_group_stats)
 // (us, bf16, 256 channels, as a small input and otherwise: one scan of 10 MB 13.3 and 14.1, 41 MB 24.2
 // and 24.4, 64 MB 36.2 and 34.9, 82 MB 48.7 and 45.9, seven scans of 10 MB together 19.1 and 16.5, of 64 MB
-// 43 and 37.  A backward pass gains nothing from more blocks: 41 MB 44 and 51, 512 MB 417 and 446; only very
+// 43 and 37.  A backward pass gains nothing from more blocks: 41 MB 44 and 51, 512 MB 420 and 446; only very
 // many scans would, 2000 of 50 rows 106 and 85.)
 constexpr int64_t kSmallBytes = 40 << 20;
 // (154 MB: 81 us, with 64 kB 83; 512 MB: 249, 256, with 1 MB 275.  At least four blocks an SM
