@@ -658,7 +658,8 @@ int spconv_quantize_weight_blocks(const void* w_dev, int32_t count, int32_t c_in
  *                  of a row, as spconv_quantize_blocks forms them (from the fp32
  *                  values, and without a residual).
  * The sums are fp32 throughout.  c_in is a multiple of 16
- * (SPCONV_ERR_UNSUPPORTED otherwise); n_experts <= 1024.
+ * (SPCONV_ERR_UNSUPPORTED otherwise: the rows of the dense weight are read by
+ * tensor-map copies, which take strides of whole 16 bytes); n_experts <= 1024.
  */
 int spconv_linear_blocks(const void* x_dev, int64_t ld_x, const float* x_scale_dev, const void* w_dev, const float* w_scale_dev,
                          const int32_t* offsets_dev, int32_t n_experts, int64_t n, int32_t c_in, int32_t c_out,

@@ -19,9 +19,10 @@
 //
 // What bounds it: in the main loop the chain of a block's commit, its adding up, the
 // arrival and the issue of the next but one (790 clocks a block, not 512: 8192 x
-// 4096 x 4096 106 us, 2.6 PFLOP/s; 8192^3 405 us, 327 without the adding up); between
+// 4096 x 4096 106 us, 2.6 PFLOP/s; 8192^3 405 to 417 us, 327 without the adding up); between
 // tiles the epilogue, which nothing hides because the sums fill the registers (plain
-// 3000 clocks, GELU 9000: 122 us with it, SiLU 115, residual 127; gated to e4m3 213).
+// 3000 clocks, GELU 9000: 123 us with it, with a bias too 128, SiLU 117, residual 129;
+// gated 207, to e4m3 211).
 // Much of that is waiting for instructions: it is run once a tile.
 //
 // Sorted rows: expert e's rows are offsets[e] .. offsets[e + 1] - 1, and its
